@@ -8,6 +8,7 @@ library exists; any other use fails loudly if the library is missing.
 
 _EXPORTS = ("EpDispatchCombineConfig", "EpDispatchCombineOp", "EpError")
 _RANK_EXPORTS = ("EpRankOp", "exchange_workspaces", "phase_barrier")
+_LAYER_EXPORTS = ("EpRouterConfig", "EpRouterOp", "EpLinearConfig", "EpLinearOp")
 
 
 def __getattr__(name):
@@ -18,4 +19,7 @@ def __getattr__(name):
     if name == "ranks" or name in _RANK_EXPORTS:
         ranks = importlib.import_module(".ranks", __name__)
         return ranks if name == "ranks" else getattr(ranks, name)
+    if name == "layer" or name in _LAYER_EXPORTS:
+        layer = importlib.import_module(".layer", __name__)
+        return layer if name == "layer" else getattr(layer, name)
     raise AttributeError(name)

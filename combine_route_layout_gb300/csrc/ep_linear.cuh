@@ -1,0 +1,107 @@
+// Declarations shared by the experts' products (ep_linear*.cu): parameter
+// blocks, the segments of the row pool, activations.
+//
+//   z = x W_g^T + b_g         for the rows of segment g
+//   y = act(z) + residual
+//   dz = dy act'(z),  dx = dz W_g,  dW_g = dz^T x,  db_g = sum of dz
+#pragma once
+
+#include <cuda_bf16.h>
+
+#include "ep_kernels.cuh"
+
+namespace ep {
+
+constexpr int kErrSegment = 1;         // a segment reaches outside the pool
+constexpr int kErrLinearTimeout = 2;   // a bounded wait gave up
+
+// Rows of each group: begin[g] (+ base[g / per_base]) .. + count[g] - 1 of
+// the pool, or the first `dense_rows` rows when begin is NULL (one group).
+struct LinearSegs {
+  int G;
+  int per_base;
+  int64_t pool;
+  int64_t dense_rows;
+  const int32_t* begin;
+  const int32_t* count;
+  const int32_t* base;
+  int32_t* err;
+};
+
+struct LinearParams {
+  LinearSegs s;
+  int K;                       // in_features
+  int N;                       // out_features
+  int Nw;                      // weight rows: N, or 2 N (gate rows, then up rows)
+  int act;
+  int64_t ldz;                 // elements per row of dz
+  const __nv_bfloat16* x;      // [pool][K]
+  const __nv_bfloat16* w;      // [G][Nw][K]
+  const float* bias;           // [G][Nw] or NULL
+  const void* residual;        // [pool][N] of y's type, or NULL
+  void* y;                     // [pool][N]
+  int y_f32;
+  __nv_bfloat16* z;            // [pool][Nw] or NULL
+  // backward
+  const void* dy;              // [pool][N] of y's type
+  const __nv_bfloat16* dz;     // [pool][ldz]
+  __nv_bfloat16* dx;           // [pool][K]
+  void* dw;                    // [G][Nw][K]
+  int dw_f32;
+};
+
+// The products (ep_linear_mma.cu), over `sms` multiprocessors.
+cudaError_t launch_linear_forward(const LinearParams& p, int sms, cudaStream_t st);
+cudaError_t launch_linear_input_grad(const LinearParams& p, int sms, cudaStream_t st);
+cudaError_t launch_linear_weight_grad(const LinearParams& p, int sms, cudaStream_t st);
+
+#ifdef __CUDACC__
+
+// Segment g, kept inside the pool whatever the arrays say.
+__device__ __forceinline__ void segment_of(const LinearSegs& s, int g, int64_t& begin,
+                                           int64_t& count) {
+  if (!s.begin) {
+    begin = 0;
+    count = s.dense_rows;
+    return;
+  }
+  begin = (int64_t)__ldg(s.begin + g) + (s.base ? __ldg(s.base + g / s.per_base) : 0);
+  count = __ldg(s.count + g);
+  if (begin < 0 || count < 0 || begin + count > s.pool) {
+    if (count != 0) atomicOr(s.err, kErrSegment);
+    if (begin < 0 || begin > s.pool || count < 0) {
+      begin = 0;
+      count = 0;
+    } else {
+      count = min(count, s.pool - begin);
+    }
+  }
+}
+
+__device__ __forceinline__ float silu_of(float v) { return v / (1.0f + __expf(-v)); }
+
+__device__ __forceinline__ float act_of(int act, float v) {
+  switch (act) {
+    case EP_ACT_RELU: return fmaxf(v, 0.0f);
+    case EP_ACT_SILU: return silu_of(v);
+    case EP_ACT_GELU: return 0.5f * v * (1.0f + erff(v * 0.70710678118654752f));
+    default: return v;
+  }
+}
+
+__device__ __forceinline__ float slope_of(int act, float v) {
+  switch (act) {
+    case EP_ACT_RELU: return v > 0.0f ? 1.0f : 0.0f;
+    case EP_ACT_SILU: {
+      const float s = 1.0f / (1.0f + __expf(-v));
+      return s * (1.0f + v * (1.0f - s));
+    }
+    case EP_ACT_GELU:
+      return 0.5f * (1.0f + erff(v * 0.70710678118654752f)) +
+             v * __expf(-0.5f * v * v) * 0.39894228040143268f;
+    default: return 1.0f;
+  }
+}
+
+#endif
+}  // namespace ep

@@ -1,0 +1,904 @@
+// The router of a mixture-of-experts layer and its balance loss: what makes
+// the indices and weights that dispatch takes, and the gradient that trains
+// them.
+//
+// Scores of one token, l its logits, masked ones (not above the type's lowest
+// finite value, +inf or NaN) left out:
+//   softmax   selection by l; p_e = exp(l_e - max l) / sum
+//   sigmoid   s_e = 1 / (1 + exp(-l_e)); selection by c_e = s_e + bias_e,
+//             both rounded to f32; p_e = s_e / sum s
+// With groups of experts, the topk_groups best groups stay (by their largest
+// l, or by the sum of their two best c). The k best experts of those, ties to
+// the lowest index, have the weights
+//   softmax   p_e, or softmax over the selected (normalize_weights)
+//   sigmoid   s_e, or s_e / sum of the selected s
+// times route_scale. The balance loss of a segment of n tokens is
+//   sum_e f_e P_e,  f_e = count_e E / (k n),  P_e = (1 / n) sum_t p_te,
+// and balance_coef times its mean over the segments that hold tokens is the
+// loss. Counts carry no gradient.
+//
+// Every kernel reads each logit once: a warp takes a row, a lane VPL
+// consecutive experts, in registers. Consecutive, so that the lowest lane
+// among equals holds the lowest expert and one ballot settles a tie.
+#include <cuda_bf16.h>
+
+#include <cstring>
+#include <new>
+
+#include "ep_kernels.cuh"
+
+namespace ep {
+namespace {
+
+constexpr int kRouterWarps = 8;
+constexpr int kRouterRows = 64;      // most rows of one CTA, all of one segment
+constexpr int kMaxGroups = EP_MAX_ROUTER_GROUPS;
+constexpr int kErrNotFinite = 1;     // a logit was NaN or +inf
+constexpr int kErrRouterIndex = 2;   // an expert id outside [-1, E)
+
+struct RouterParams {
+  int R, Tmax, E, k;
+  int groups, topk_groups;
+  int normalize;
+  float scale;
+  int stretch;               // tokens of a rank that belong to one segment
+  int stretches;             // per rank
+  int chunks;                // CTAs per stretch
+  int rows;                  // rows per CTA
+  int n_seg;                 // 1, or R * stretches
+  int vec;                   // rows are 16-byte aligned
+  int ntok[EP_MAX_WORLD_SIZE];
+  const void* logits;
+  const float* bias;
+  const int32_t* idx_in;     // backward, and the loss of given indices
+  int32_t* idx;
+  float* w;
+  float* part_p;             // [chunk][E] sums of p over the chunk's rows
+  int32_t* part_n;           // [chunk][E] rows per expert
+  int32_t* err;
+};
+
+struct BalanceParams {
+  int R, Tmax, E, k;
+  int stretch, stretches, chunks, n_seg;
+  int ntok[EP_MAX_WORLD_SIZE];
+  float coef;                // balance_coef / segments that hold tokens
+  const float* part_p;
+  const int32_t* part_n;
+  float* part_loss;          // [n_seg][expert blocks]
+  unsigned int* ticket;
+  int32_t* counts;           // [n_seg][E]
+  float* loss;
+};
+
+struct RouterGradParams {
+  RouterParams r;
+  const float* d_w;          // [R][Tmax][k] or NULL
+  const int32_t* counts;     // [n_seg][E] or NULL
+  const float* d_loss;       // scalar
+  float coef;
+  void* d_logits;
+};
+
+template <typename T>
+__device__ __forceinline__ float lowest();
+template <>
+__device__ __forceinline__ float lowest<float>() { return -3.4028234663852886e38f; }
+template <>
+__device__ __forceinline__ float lowest<__nv_bfloat16>() { return -3.3895313892515355e38f; }
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
+  return v;
+}
+
+__device__ __forceinline__ float warp_max(float v) {
+#pragma unroll
+  for (int o = 16; o; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kFull, v, o));
+  return v;
+}
+
+// A key that orders as the float does (both zeros alike), above 0 for every
+// finite value; 0 is "none".
+__device__ __forceinline__ uint32_t key_of(float v) {
+  const uint32_t u = __float_as_uint(v + 0.0f);
+  return u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
+}
+
+// 1 / (1 + exp(-l)) with every step rounded to f32, as the definition has it:
+// the selection compares these values.
+__device__ __forceinline__ float sigmoid(float l) {
+  return __fdiv_rn(1.0f, __fadd_rn(1.0f, expf(-l)));
+}
+
+// This lane's VPL logits of the row; -inf beyond the row's end.
+template <int VPL, typename T>
+__device__ __forceinline__ void load_row(const T* row, int E, int lane, bool vec, float (&l)[VPL]) {
+  const int e0 = lane * VPL;
+  constexpr int kPer = 16 / (int)sizeof(T);   // elements of a 16-byte load
+  if (VPL >= kPer && vec) {
+#pragma unroll
+    for (int v = 0; v < VPL / kPer; ++v) {
+      uint4 q = make_uint4(0, 0, 0, 0);
+      const bool in = e0 + v * kPer < E;      // E is a multiple of kPer here
+      if (in) q = ld_nc_v4(row + e0 + v * kPer);
+      const uint32_t u[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        float x;
+        if (sizeof(T) == 4) {
+          x = __uint_as_float(u[i]);
+        } else {
+          x = (i & 1) ? bf16_hi(u[i / 2]) : bf16_lo(u[i / 2]);
+        }
+        l[v * kPer + i] = in ? x : -INFINITY;
+      }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) l[i] = e0 + i < E ? (float)row[e0 + i] : -INFINITY;
+  }
+}
+
+// Masked logits become -inf; NaN and +inf too, and raise the error bit.
+template <int VPL, typename T>
+__device__ __forceinline__ void mask_row(float (&l)[VPL], int32_t* err) {
+  bool bad = false;
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) {
+    bad |= !(l[i] < INFINITY);
+    if (!(l[i] > lowest<T>()) || !(l[i] < INFINITY)) l[i] = -INFINITY;
+  }
+  if (bad && err) atomicOr(err, kErrNotFinite);
+}
+
+// p (softmax: exp(l - max), sigmoid: s) of the lane's experts, 0 where masked.
+template <int VPL, bool SIGMOID>
+__device__ __forceinline__ void raw_scores(const float (&l)[VPL], float (&p)[VPL]) {
+  if (SIGMOID) {
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) p[i] = l[i] > -INFINITY ? sigmoid(l[i]) : 0.0f;
+  } else {
+    float m = l[0];
+#pragma unroll
+    for (int i = 1; i < VPL; ++i) m = fmaxf(m, l[i]);
+    m = warp_max(m);
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) p[i] = l[i] > -INFINITY ? expf(l[i] - m) : 0.0f;
+  }
+}
+
+template <int VPL>
+__device__ __forceinline__ float row_sum(const float (&p)[VPL]) {
+  float s = 0.0f;
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) s += p[i];
+  return warp_sum(s);
+}
+
+struct RowPlace {
+  int rank, t0, n;    // rows t0 .. t0 + n - 1 of `rank` (n may be 0 or negative)
+  int pad_end;        // rows up to here (exclusive) exist in the arrays
+  int seg;
+};
+
+// The rows of chunk c: `chunks` CTAs walk each stretch of a rank.
+__device__ __forceinline__ RowPlace place_of(const RouterParams& p, int c) {
+  RowPlace w;
+  const int piece = c % p.chunks, st = c / p.chunks;
+  w.rank = st / p.stretches;
+  const int s0 = (st - w.rank * p.stretches) * p.stretch;
+  const int end = min(s0 + p.stretch, p.Tmax);
+  w.t0 = s0 + piece * p.rows;
+  w.pad_end = min(w.t0 + p.rows, end);
+  w.n = min(w.pad_end, p.ntok[w.rank]) - w.t0;
+  w.seg = p.n_seg == 1 ? 0 : st;
+  return w;
+}
+
+// Keep the keys of the topk_groups best groups. `buf`: E floats of this warp.
+template <int VPL, bool SIGMOID>
+__device__ __forceinline__ void limit_groups(const RouterParams& p, int lane, float* buf,
+                                             const float (&c)[VPL], uint32_t (&key)[VPL]) {
+  const int size = p.E / p.groups;
+#pragma unroll
+  for (int i = 0; i < VPL; ++i)
+    if (lane * VPL + i < p.E) buf[lane * VPL + i] = key[i] ? c[i] : -INFINITY;
+  __syncwarp();
+  float best = -INFINITY;
+  if (lane < p.groups) {
+    float second = -INFINITY;
+    for (int j = 0; j < size; ++j) {
+      const float v = buf[lane * size + j];
+      second = fmaxf(second, fminf(v, best));
+      best = fmaxf(best, v);
+    }
+    if (SIGMOID && second > -INFINITY) best = __fadd_rn(best, second);
+  }
+  __syncwarp();
+  int ahead = 0;
+  for (int j = 0; j < p.groups; ++j) {
+    const float v = __shfl_sync(kFull, best, j);
+    ahead += v > best || (v == best && j < lane);
+  }
+  const uint32_t kept = __ballot_sync(kFull, lane < p.groups && ahead < p.topk_groups &&
+                                                 best > -INFINITY);
+#pragma unroll
+  for (int i = 0; i < VPL; ++i)
+    if (lane * VPL + i < p.E && !((kept >> ((lane * VPL + i) / size)) & 1u)) key[i] = 0;
+}
+
+// SELECT: choose the experts, write indices and weights. BALANCE: sums of p
+// and rows per expert for the loss (of the chosen, or of given indices).
+template <int VPL, typename T, bool SIGMOID, bool SELECT, bool BALANCE>
+__global__ void __launch_bounds__(kRouterWarps * 32) router_rows_kernel(RouterParams p) {
+  extern __shared__ float smem[];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const RowPlace at = place_of(p, blockIdx.x);
+  float* buf = smem + (size_t)warp * p.E;                      // group scores, then sums of p
+  int* cnt = reinterpret_cast<int*>(smem + (size_t)kRouterWarps * p.E);
+  if (BALANCE) {
+    for (int e = threadIdx.x; e < p.E; e += blockDim.x) cnt[e] = 0;
+    __syncthreads();
+  }
+  float sum_p[VPL];
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) sum_p[i] = 0.0f;
+
+  for (int t = at.t0 + warp; t < at.t0 + at.n; t += kRouterWarps) {
+    const int64_t g = (int64_t)at.rank * p.Tmax + t;
+    float l[VPL];
+    load_row<VPL, T>(static_cast<const T*>(p.logits) + g * p.E, p.E, lane, p.vec, l);
+    // beyond the row's end the logits are -inf already, which raises nothing
+    mask_row<VPL, T>(l, p.err);
+    float pr[VPL];
+    float total = 0.0f;
+    if (SIGMOID || BALANCE || !p.normalize) raw_scores<VPL, SIGMOID>(l, pr);
+    if (BALANCE || (!SIGMOID && !p.normalize)) total = row_sum<VPL>(pr);
+    if (BALANCE) {
+      const float inv = total > 0.0f ? 1.0f / total : 0.0f;
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) sum_p[i] += pr[i] * inv;
+    }
+    if (SELECT) {
+      float c[VPL];
+      uint32_t key[VPL];
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) {
+        const int e = lane * VPL + i;
+        c[i] = l[i];
+        if (SIGMOID) c[i] = p.bias && e < p.E ? __fadd_rn(pr[i], __ldg(p.bias + e)) : pr[i];
+        key[i] = l[i] > -INFINITY ? key_of(c[i]) : 0u;
+      }
+      if (p.groups > 1) limit_groups<VPL, SIGMOID>(p, lane, buf, c, key);
+      // k rounds: the warp's largest key, its lowest lane; lane j keeps slot j
+      int my_e = -1;
+      float my_v = 0.0f;
+      uint32_t top = 0;
+      int top_i = 0;
+      float top_v = 0.0f;
+      auto rescan = [&]() {
+        top = 0;
+#pragma unroll
+        for (int i = 0; i < VPL; ++i)
+          if (key[i] > top) {
+            top = key[i];
+            top_i = i;
+            top_v = SIGMOID ? pr[i] : l[i];
+          }
+      };
+      rescan();
+      for (int j = 0; j < p.k; ++j) {
+        const uint32_t m = __reduce_max_sync(kFull, top);
+        if (m == 0) break;
+        const int win = __ffs(__ballot_sync(kFull, top == m)) - 1;
+        const int e = __shfl_sync(kFull, lane * VPL + top_i, win);
+        const float v = __shfl_sync(kFull, top_v, win);
+        if (lane == j) {
+          my_e = e;
+          my_v = v;
+        }
+        if (lane == win) {
+#pragma unroll
+          for (int i = 0; i < VPL; ++i)
+            if (i == top_i) key[i] = 0;
+          rescan();
+        }
+      }
+      float wt = 0.0f;
+      if (SIGMOID) {
+        const float s = my_e >= 0 ? my_v : 0.0f;
+        const float d = p.normalize ? warp_sum(s) : 1.0f;
+        wt = d > 0.0f ? s / d : 0.0f;
+      } else {
+        const float m = warp_max(my_e >= 0 ? my_v : -INFINITY);   // the row's largest, if !normalize
+        if (p.normalize) {
+          const float x = my_e >= 0 ? expf(my_v - m) : 0.0f;
+          const float d = warp_sum(x);
+          wt = d > 0.0f ? x / d : 0.0f;
+        } else {
+          const float all = warp_max([&] {
+            float v = l[0];
+#pragma unroll
+            for (int i = 1; i < VPL; ++i) v = fmaxf(v, l[i]);
+            return v;
+          }());
+          wt = my_e >= 0 ? expf(my_v - all) / total : 0.0f;
+        }
+      }
+      if (lane < p.k) {
+        p.idx[g * p.k + lane] = my_e;
+        p.w[g * p.k + lane] = my_e >= 0 ? wt * p.scale : 0.0f;
+        if (BALANCE && my_e >= 0) atomicAdd(cnt + my_e, 1);
+      }
+    } else if (lane < p.k) {
+      const int e = __ldg(p.idx_in + g * p.k + lane);
+      if (e < -1 || e >= p.E) {
+        atomicOr(p.err, kErrRouterIndex);
+      } else if (e >= 0) {
+        atomicAdd(cnt + e, 1);
+      }
+    }
+  }
+  if (SELECT) {  // rows past the rank's tokens hold no expert
+    const int first = max(at.t0, at.t0 + at.n);
+    const int64_t b = ((int64_t)at.rank * p.Tmax + first) * p.k;
+    const int64_t m = (int64_t)max(0, at.pad_end - first) * p.k;
+    for (int64_t i = threadIdx.x; i < m; i += blockDim.x) {
+      p.idx[b + i] = -1;
+      p.w[b + i] = 0.0f;
+    }
+  }
+  if (BALANCE) {
+#pragma unroll
+    for (int i = 0; i < VPL; ++i)
+      if (lane * VPL + i < p.E) buf[lane * VPL + i] = sum_p[i];
+    __syncthreads();
+    for (int e = threadIdx.x; e < p.E; e += blockDim.x) {
+      float s = 0.0f;
+#pragma unroll
+      for (int w = 0; w < kRouterWarps; ++w) s += smem[w * p.E + e];
+      p.part_p[(int64_t)blockIdx.x * p.E + e] = s;
+      p.part_n[(int64_t)blockIdx.x * p.E + e] = cnt[e];
+    }
+  }
+}
+
+// Counts and loss from the chunks' sums, added in chunk order: CTA (b, s)
+// takes 32 experts of segment s, a warp every 8th chunk, and the last CTA adds
+// the products. Every sum has a fixed order.
+constexpr int kBalanceExperts = 32;
+
+__global__ void __launch_bounds__(256) balance_reduce_kernel(BalanceParams p) {
+  __shared__ float sp[8][kBalanceExperts];
+  __shared__ int sn[8][kBalanceExperts];
+  __shared__ bool last;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int e = blockIdx.x * kBalanceExperts + lane;
+  const int seg = blockIdx.y;
+  const int first = p.n_seg == 1 ? 0 : seg * p.chunks;
+  const int n_chunk = p.n_seg == 1 ? p.R * p.stretches * p.chunks : p.chunks;
+  float s = 0.0f;
+  int n = 0;
+  if (e < p.E)
+    for (int c = warp; c < n_chunk; c += 8) {
+      s += __ldg(p.part_p + (int64_t)(first + c) * p.E + e);
+      n += __ldg(p.part_n + (int64_t)(first + c) * p.E + e);
+    }
+  sp[warp][lane] = s;
+  sn[warp][lane] = n;
+  __syncthreads();
+  if (warp == 0) {
+    s = 0.0f;
+    n = 0;
+#pragma unroll
+    for (int w = 0; w < 8; ++w) {
+      s += sp[w][lane];
+      n += sn[w][lane];
+    }
+    int held = 0;
+    if (p.n_seg == 1) {
+      for (int r = 0; r < p.R; ++r) held += p.ntok[r];
+    } else {
+      const int r = seg / p.stretches, s0 = (seg - r * p.stretches) * p.stretch;
+      held = max(0, min(p.ntok[r] - s0, p.stretch));
+    }
+    float term = 0.0f;
+    if (e < p.E) {
+      p.counts[(int64_t)seg * p.E + e] = n;
+      if (held > 0) term = ((float)n * (float)p.E / ((float)held * (float)p.k)) * (s / (float)held);
+    }
+    term = warp_sum(term);
+    if (lane == 0) {
+      const int slot = seg * gridDim.x + blockIdx.x;
+      p.part_loss[slot] = term;
+      __threadfence();
+      last = atomicAdd(p.ticket, 1u) == gridDim.x * gridDim.y - 1;
+    }
+  }
+  __syncthreads();
+  if (!last) return;
+  __threadfence();
+  const int m = gridDim.x * gridDim.y;
+  float acc = 0.0f;
+  for (int i = threadIdx.x; i < m; i += 256) acc += __ldcg(p.part_loss + i);
+  acc = warp_sum(acc);
+  if (lane == 0) sp[0][warp] = acc;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    float v = 0.0f;
+    for (int w = 0; w < 8; ++w) v += sp[0][w];
+    *p.loss = v * p.coef;
+    *p.ticket = 0u;
+  }
+}
+
+// Gradient of the weights (d_w) and of the balance loss (d_loss) in the
+// logits, one pass: the scores are computed again rather than kept, since a
+// row's logits have to be read in any case (softmax's needs them all).
+template <int VPL, typename T, bool SIGMOID>
+__global__ void __launch_bounds__(kRouterWarps * 32) router_grad_kernel(RouterGradParams q) {
+  const RouterParams& p = q.r;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const RowPlace at = place_of(p, blockIdx.x);
+  float slope[VPL];            // f_e's factor of dL/dp
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) slope[i] = 0.0f;
+  if (q.counts && at.n > 0) {
+    int held = 0;
+    if (p.n_seg == 1) {
+      for (int r = 0; r < p.R; ++r) held += p.ntok[r];
+    } else {
+      const int r = at.seg / p.stretches, s0 = (at.seg - r * p.stretches) * p.stretch;
+      held = min(p.ntok[r] - s0, p.stretch);
+    }
+    const float f = q.coef * __ldg(q.d_loss) / (float)held;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+      const int e = lane * VPL + i;
+      if (e < p.E)
+        slope[i] = f * ((float)__ldg(q.counts + (int64_t)at.seg * p.E + e) * (float)p.E /
+                        ((float)held * (float)p.k));
+    }
+  }
+  for (int t = at.t0 + warp; t < at.pad_end; t += kRouterWarps) {
+    const int64_t g = (int64_t)at.rank * p.Tmax + t;
+    float d[VPL];
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) d[i] = 0.0f;
+    if (t < at.t0 + at.n) {
+      float l[VPL], pr[VPL];
+      load_row<VPL, T>(static_cast<const T*>(p.logits) + g * p.E, p.E, lane, p.vec, l);
+      mask_row<VPL, T>(l, p.err);
+      raw_scores<VPL, SIGMOID>(l, pr);
+      const float total = row_sum<VPL>(pr);
+      const float inv = total > 0.0f ? 1.0f / total : 0.0f;
+      if (q.counts) {
+        float dot = 0.0f;
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) dot += slope[i] * (pr[i] * inv);
+        dot = warp_sum(dot);
+#pragma unroll
+        for (int i = 0; i < VPL; ++i)
+          d[i] = pr[i] * inv * (SIGMOID ? 1.0f - pr[i] : 1.0f) * (slope[i] - dot);
+      }
+      if (q.d_w) {
+        int e = -1;
+        float up = 0.0f;
+        if (lane < p.k) {
+          e = __ldg(p.idx_in + g * p.k + lane);
+          if (e < -1 || e >= p.E) {
+            atomicOr(p.err, kErrRouterIndex);
+            e = -1;
+          }
+          if (e >= 0) up = __ldg(q.d_w + g * p.k + lane) * p.scale;
+        }
+        // raw score of the slot's expert, from the lane that holds it
+        float x = 0.0f, xl = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) {
+          const int src = e >= 0 ? e / VPL : 0;
+          const float v = __shfl_sync(kFull, pr[i], src);
+          const float w = __shfl_sync(kFull, l[i], src);
+          if (e >= 0 && e % VPL == i) {
+            x = v;
+            xl = w;
+          }
+        }
+        if (!(xl > -INFINITY)) e = -1;      // a masked expert has no gradient
+        float each = 0.0f, back = 0.0f;     // slot's own part; softmax over all: the rest's
+        if (SIGMOID) {
+          if (p.normalize) {
+            const float sum = warp_sum(e >= 0 ? x : 0.0f);
+            const float r = sum > 0.0f ? 1.0f / sum : 0.0f;
+            const float mean = warp_sum(e >= 0 ? x * r * up : 0.0f);
+            each = (up - mean) * r * x * (1.0f - x);
+          } else {
+            each = up * x * (1.0f - x);
+          }
+        } else if (p.normalize) {
+          const float m = warp_max(e >= 0 ? xl : -INFINITY);
+          float s = e >= 0 ? expf(xl - m) : 0.0f;
+          const float sum = warp_sum(s);
+          s = sum > 0.0f ? s / sum : 0.0f;
+          const float mean = warp_sum(e >= 0 ? s * up : 0.0f);
+          each = s * (up - mean);
+        } else {
+          each = x * inv * up;
+          back = warp_sum(e >= 0 ? each : 0.0f);
+        }
+        if (e < 0) each = 0.0f;
+        if (!SIGMOID && !p.normalize) {
+#pragma unroll
+          for (int i = 0; i < VPL; ++i) d[i] -= pr[i] * inv * back;
+        }
+        for (int j = 0; j < p.k; ++j) {
+          const int ej = __shfl_sync(kFull, e, j);
+          const float vj = __shfl_sync(kFull, each, j);
+          const int i_of = ej - lane * VPL;
+#pragma unroll
+          for (int i = 0; i < VPL; ++i)
+            if (ej >= 0 && i == i_of) d[i] += vj;
+        }
+      }
+    }
+    T* out = static_cast<T*>(q.d_logits) + g * p.E;
+    constexpr int kPer = 16 / (int)sizeof(T);
+    if (VPL >= kPer && p.vec) {
+#pragma unroll
+      for (int v = 0; v < VPL / kPer; ++v) {
+        if (lane * VPL + v * kPer >= p.E) continue;
+        uint4 u;
+        if (sizeof(T) == 4) {
+          u = make_uint4(__float_as_uint(d[v * kPer]), __float_as_uint(d[v * kPer + 1]),
+                         __float_as_uint(d[v * kPer + 2]), __float_as_uint(d[v * kPer + 3]));
+        } else {
+          u = make_uint4(cvt_bf16x2(d[v * kPer], d[v * kPer + 1]),
+                         cvt_bf16x2(d[v * kPer + 2], d[v * kPer + 3]),
+                         cvt_bf16x2(d[v * kPer + (kPer > 4 ? 4 : 0)], d[v * kPer + (kPer > 4 ? 5 : 0)]),
+                         cvt_bf16x2(d[v * kPer + (kPer > 4 ? 6 : 0)], d[v * kPer + (kPer > 4 ? 7 : 0)]));
+        }
+        st_v4(out + lane * VPL + v * kPer, u);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < VPL; ++i)
+        if (lane * VPL + i < p.E) {
+          if (sizeof(T) == 4) {
+            reinterpret_cast<float*>(out)[lane * VPL + i] = d[i];
+          } else {
+            reinterpret_cast<__nv_bfloat16*>(out)[lane * VPL + i] = __float2bfloat16_rn(d[i]);
+          }
+        }
+    }
+  }
+}
+
+size_t rows_smem(int E, bool balance, bool groups) {
+  if (balance) return (size_t)(kRouterWarps + 1) * E * 4;
+  return groups ? (size_t)kRouterWarps * E * 4 : 0;
+}
+
+template <int VPL, typename T, bool SIGMOID>
+cudaError_t rows_vpl(const RouterParams& p, bool select, bool balance, int grid, cudaStream_t st) {
+  const size_t smem = rows_smem(p.E, balance, p.groups > 1);
+  if (select && balance) {
+    router_rows_kernel<VPL, T, SIGMOID, true, true><<<grid, kRouterWarps * 32, smem, st>>>(p);
+  } else if (select) {
+    router_rows_kernel<VPL, T, SIGMOID, true, false><<<grid, kRouterWarps * 32, smem, st>>>(p);
+  } else {
+    router_rows_kernel<VPL, T, SIGMOID, false, true><<<grid, kRouterWarps * 32, smem, st>>>(p);
+  }
+  return cudaGetLastError();
+}
+
+template <int VPL, typename T, bool SIGMOID>
+cudaError_t grad_vpl(const RouterGradParams& q, int grid, cudaStream_t st) {
+  router_grad_kernel<VPL, T, SIGMOID><<<grid, kRouterWarps * 32, 0, st>>>(q);
+  return cudaGetLastError();
+}
+
+// Calls f<VPL, T, SIGMOID> for the config's sizes and types.
+#define EP_ROUTER_SWITCH(CALL)                                      \
+  do {                                                              \
+    if (E <= 32) return CALL(1);                                    \
+    if (E <= 64) return CALL(2);                                    \
+    if (E <= 128) return CALL(4);                                   \
+    if (E <= 256) return CALL(8);                                   \
+    if (E <= 512) return CALL(16);                                  \
+    return CALL(32);                                                \
+  } while (0)
+
+template <typename T, bool SIGMOID>
+cudaError_t rows_typed(const RouterParams& p, bool select, bool balance, int grid,
+                       cudaStream_t st) {
+  const int E = p.E;
+#define EP_CALL(V) rows_vpl<V, T, SIGMOID>(p, select, balance, grid, st)
+  EP_ROUTER_SWITCH(EP_CALL);
+#undef EP_CALL
+}
+
+template <typename T, bool SIGMOID>
+cudaError_t grad_typed(const RouterGradParams& q, int grid, cudaStream_t st) {
+  const int E = q.r.E;
+#define EP_CALL(V) grad_vpl<V, T, SIGMOID>(q, grid, st)
+  EP_ROUTER_SWITCH(EP_CALL);
+#undef EP_CALL
+}
+
+}  // namespace
+}  // namespace ep
+
+struct ep_router_handle {
+  ep_router_config cfg;
+  uint8_t* ws;
+  bool needs_init;
+  int stretch, stretches, n_seg, rows, chunks;
+  int64_t total_chunks;
+  int expert_blocks;
+  int32_t* err;
+  unsigned int* ticket;
+  float* part_p;
+  int32_t* part_n;
+  float* part_loss;
+  size_t bytes;
+};
+
+namespace {
+
+using namespace ep;
+
+ep_status rfail(ep_status st, const char* msg) { return record_error(st, msg); }
+
+ep_status rcuda(cudaError_t e) { return record_error(EP_ERR_CUDA, cudaGetErrorString(e)); }
+
+size_t up256(size_t v) { return (v + 255) / 256 * 256; }
+
+// Validate the config and lay the workspace out in `h`.
+ep_status plan_router(const ep_router_config* c, ep_router_handle* h) {
+  if (!c) return rfail(EP_ERR_INVALID_ARG, "router config is NULL");
+  if (c->world_size < 1 || c->world_size > EP_MAX_WORLD_SIZE)
+    return rfail(EP_ERR_INVALID_ARG, "router world_size outside [1, 32]");
+  if (c->max_num_inp_token_per_rank < 1 ||
+      (int64_t)c->world_size * c->max_num_inp_token_per_rank > INT32_MAX)
+    return rfail(EP_ERR_INVALID_ARG, "router max_num_inp_token_per_rank must be >= 1 and fit int32 over all ranks");
+  if (c->num_experts < 1 || c->num_experts > EP_MAX_EXPERTS)
+    return rfail(EP_ERR_INVALID_ARG, "router num_experts outside [1, 1024]");
+  if (c->num_experts_per_token < 1 || c->num_experts_per_token > EP_MAX_TOPK ||
+      c->num_experts_per_token > c->num_experts)
+    return rfail(EP_ERR_INVALID_ARG, "router num_experts_per_token outside [1, min(32, num_experts)]");
+  if (c->logits_dtype != EP_DTYPE_FP32 && c->logits_dtype != EP_DTYPE_BF16)
+    return rfail(EP_ERR_INVALID_ARG, "router logits_dtype must be FP32 or BF16");
+  if (c->score_func != EP_SCORE_SOFTMAX && c->score_func != EP_SCORE_SIGMOID)
+    return rfail(EP_ERR_INVALID_ARG, "unknown router score_func");
+  if (c->num_groups < 1 || c->num_groups > kMaxGroups || c->num_experts % c->num_groups != 0)
+    return rfail(EP_ERR_INVALID_ARG, "router num_groups must be in [1, 32] and divide num_experts");
+  if (c->topk_groups < 1 || c->topk_groups > c->num_groups ||
+      (int64_t)c->topk_groups * (c->num_experts / c->num_groups) < c->num_experts_per_token)
+    return rfail(EP_ERR_INVALID_ARG, "router topk_groups must be in [1, num_groups] and hold num_experts_per_token experts");
+  if (!(c->route_scale > 0.0f) || !(c->route_scale < INFINITY))
+    return rfail(EP_ERR_INVALID_ARG, "router route_scale must be positive and finite");
+  if (!(c->balance_coef >= 0.0f) || !(c->balance_coef < INFINITY))
+    return rfail(EP_ERR_INVALID_ARG, "router balance_coef must be finite and >= 0");
+  if (c->seq_len < 0) return rfail(EP_ERR_INVALID_ARG, "router seq_len must be >= 0");
+  const int T = c->max_num_inp_token_per_rank;
+  h->cfg = *c;
+  h->stretch = c->seq_len > 0 && c->seq_len < T ? c->seq_len : T;
+  h->stretches = (T + h->stretch - 1) / h->stretch;
+  h->n_seg = c->seq_len > 0 ? c->world_size * h->stretches : 1;
+  h->rows = kRouterRows;
+  h->chunks = (h->stretch + h->rows - 1) / h->rows;
+  h->total_chunks = (int64_t)c->world_size * h->stretches * h->chunks;
+  h->expert_blocks = (c->num_experts + kBalanceExperts - 1) / kBalanceExperts;
+  if (h->total_chunks > INT32_MAX) return rfail(EP_ERR_INVALID_ARG, "router batch too large");
+  if (h->n_seg > 65535) return rfail(EP_ERR_INVALID_ARG, "router seq_len gives more than 65535 segments");
+  size_t off = 256;  // error bits and ticket
+  const size_t part = up256((size_t)h->total_chunks * c->num_experts * 4);
+  h->err = reinterpret_cast<int32_t*>(h->ws);
+  h->ticket = reinterpret_cast<unsigned int*>(h->ws ? h->ws + 64 : nullptr);
+  h->part_p = reinterpret_cast<float*>(h->ws ? h->ws + off : nullptr);
+  off += part;
+  h->part_n = reinterpret_cast<int32_t*>(h->ws ? h->ws + off : nullptr);
+  off += part;
+  h->part_loss = reinterpret_cast<float*>(h->ws ? h->ws + off : nullptr);
+  off += up256((size_t)h->n_seg * h->expert_blocks * 4);
+  h->bytes = off;
+  return EP_OK;
+}
+
+// Clear the error bits and the ticket before the first launch. A call that is
+// being captured clears them inside its graph and leaves that to the next
+// call too: the graph may run later, or never.
+ep_status router_ready(ep_router_handle* h, cudaStream_t st) {
+  if (!h->needs_init) return EP_OK;
+  cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
+  cudaError_t e = cudaStreamIsCapturing(st, &cap);
+  if (e == cudaSuccess) e = cudaMemsetAsync(h->ws, 0, 256, st);
+  if (e != cudaSuccess) return rcuda(e);
+  if (cap == cudaStreamCaptureStatusNone) h->needs_init = false;
+  return EP_OK;
+}
+
+ep_status fill_params(const ep_router_handle* h, const void* logits, const int32_t* num_tokens,
+                      RouterParams* p) {
+  const ep_router_config& c = h->cfg;
+  memset(p, 0, sizeof(*p));
+  const size_t size = c.logits_dtype == EP_DTYPE_FP32 ? 4 : 2;
+  if (!logits || (uintptr_t)logits % size != 0)
+    return rfail(EP_ERR_INVALID_ARG, "router logits are NULL or misaligned");
+  for (int r = 0; r < c.world_size; ++r) {
+    const int n = num_tokens ? num_tokens[r] : c.max_num_inp_token_per_rank;
+    if (n < 0 || n > c.max_num_inp_token_per_rank)
+      return rfail(EP_ERR_INVALID_ARG, "num_tokens outside [0, max_num_inp_token_per_rank]");
+    p->ntok[r] = n;
+  }
+  p->R = c.world_size; p->Tmax = c.max_num_inp_token_per_rank;
+  p->E = c.num_experts; p->k = c.num_experts_per_token;
+  p->groups = c.num_groups; p->topk_groups = c.topk_groups;
+  p->normalize = c.normalize_weights != 0;
+  p->scale = c.route_scale;
+  p->stretch = h->stretch; p->stretches = h->stretches; p->chunks = h->chunks;
+  p->rows = h->rows; p->n_seg = h->n_seg;
+  p->vec = (c.num_experts * size) % 16 == 0 && (uintptr_t)logits % 16 == 0;
+  p->logits = logits;
+  p->err = h->err;
+  return EP_OK;
+}
+
+// balance_coef over the segments that hold tokens.
+float coef_of(const ep_router_handle* h, const RouterParams& p) {
+  int64_t full = 0;
+  for (int r = 0; r < p.R; ++r)
+    full += h->n_seg == 1 ? p.ntok[r] : (p.ntok[r] + h->stretch - 1) / h->stretch;
+  if (h->n_seg == 1) full = full > 0 ? 1 : 0;
+  return full > 0 ? h->cfg.balance_coef / (float)full : 0.0f;
+}
+
+ep_status launch_rows(ep_router_handle* h, const RouterParams& p, bool select, bool balance,
+                      cudaStream_t st) {
+  const bool f32 = h->cfg.logits_dtype == EP_DTYPE_FP32;
+  const bool sig = h->cfg.score_func == EP_SCORE_SIGMOID;
+  const int grid = (int)h->total_chunks;
+  const cudaError_t e =
+      f32 ? (sig ? rows_typed<float, true>(p, select, balance, grid, st)
+                 : rows_typed<float, false>(p, select, balance, grid, st))
+          : (sig ? rows_typed<__nv_bfloat16, true>(p, select, balance, grid, st)
+                 : rows_typed<__nv_bfloat16, false>(p, select, balance, grid, st));
+  return e == cudaSuccess ? EP_OK : rcuda(e);
+}
+
+ep_status launch_balance(ep_router_handle* h, const RouterParams& p, int32_t* counts, float* loss,
+                         cudaStream_t st) {
+  BalanceParams b;
+  memset(&b, 0, sizeof(b));
+  b.R = p.R; b.Tmax = p.Tmax; b.E = p.E; b.k = p.k;
+  b.stretch = p.stretch; b.stretches = p.stretches; b.chunks = p.chunks; b.n_seg = p.n_seg;
+  memcpy(b.ntok, p.ntok, sizeof(b.ntok));
+  b.coef = coef_of(h, p);
+  b.part_p = h->part_p; b.part_n = h->part_n; b.part_loss = h->part_loss;
+  b.ticket = h->ticket; b.counts = counts; b.loss = loss;
+  balance_reduce_kernel<<<dim3(h->expert_blocks, h->n_seg), 256, 0, st>>>(b);
+  const cudaError_t e = cudaGetLastError();
+  return e == cudaSuccess ? EP_OK : rcuda(e);
+}
+
+}  // namespace
+
+extern "C" size_t ep_router_workspace_size(const ep_router_config* cfg) {
+  ep_router_handle h;
+  memset(&h, 0, sizeof(h));
+  return plan_router(cfg, &h) == EP_OK ? h.bytes : 0;
+}
+
+extern "C" ep_status ep_router_create(const ep_router_config* cfg, void* d_workspace,
+                                      size_t workspace_bytes, ep_router_handle** out_handle) {
+  if (!out_handle) return rfail(EP_ERR_INVALID_ARG, "out_handle is NULL");
+  *out_handle = nullptr;
+  ep_router_handle h;
+  memset(&h, 0, sizeof(h));
+  h.ws = static_cast<uint8_t*>(d_workspace);
+  const ep_status s = plan_router(cfg, &h);
+  if (s != EP_OK) return s;
+  if (!d_workspace || (uintptr_t)d_workspace % 256 != 0)
+    return rfail(EP_ERR_WORKSPACE, "router workspace is NULL or not 256-byte aligned");
+  if (workspace_bytes < h.bytes) return rfail(EP_ERR_WORKSPACE, "router workspace too small");
+  ep_router_handle* p = new (std::nothrow) ep_router_handle(h);
+  if (!p) return rfail(EP_ERR_INVALID_ARG, "out of host memory");
+  p->needs_init = true;
+  *out_handle = p;
+  return EP_OK;
+}
+
+extern "C" void ep_router_destroy(ep_router_handle* h) { delete h; }
+
+extern "C" ep_status ep_router_forward(ep_router_handle* h, const void* logits, const float* bias,
+                                       const int32_t* num_tokens, int32_t* indices,
+                                       float* weights, int32_t* counts, float* loss,
+                                       void* stream) {
+  if (!h) return rfail(EP_ERR_INVALID_ARG, "router handle is NULL");
+  if (!indices || !weights) return rfail(EP_ERR_INVALID_ARG, "indices and weights must be given");
+  if ((counts == nullptr) != (loss == nullptr))
+    return rfail(EP_ERR_INVALID_ARG, "give counts and loss together, or neither");
+  if (bias && h->cfg.score_func != EP_SCORE_SIGMOID)
+    return rfail(EP_ERR_UNSUPPORTED, "a selection bias needs sigmoid scores");
+  RouterParams p;
+  ep_status s = fill_params(h, logits, num_tokens, &p);
+  if (s != EP_OK) return s;
+  p.bias = bias; p.idx = indices; p.w = weights;
+  p.part_p = h->part_p; p.part_n = h->part_n;
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if ((s = router_ready(h, st)) != EP_OK) return s;
+  if ((s = launch_rows(h, p, true, loss != nullptr, st)) != EP_OK) return s;
+  return loss ? launch_balance(h, p, counts, loss, st) : EP_OK;
+}
+
+extern "C" ep_status ep_router_balance_loss(ep_router_handle* h, const void* logits,
+                                            const int32_t* indices, const int32_t* num_tokens,
+                                            int32_t* counts, float* loss, void* stream) {
+  if (!h) return rfail(EP_ERR_INVALID_ARG, "router handle is NULL");
+  if (!indices || !counts || !loss)
+    return rfail(EP_ERR_INVALID_ARG, "indices, counts and loss must be given");
+  RouterParams p;
+  ep_status s = fill_params(h, logits, num_tokens, &p);
+  if (s != EP_OK) return s;
+  p.idx_in = indices;
+  p.part_p = h->part_p; p.part_n = h->part_n;
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if ((s = router_ready(h, st)) != EP_OK) return s;
+  if ((s = launch_rows(h, p, false, true, st)) != EP_OK) return s;
+  return launch_balance(h, p, counts, loss, st);
+}
+
+extern "C" ep_status ep_router_backward(ep_router_handle* h, const void* logits,
+                                        const int32_t* indices, const int32_t* num_tokens,
+                                        const float* d_weights, const int32_t* counts,
+                                        const float* d_loss, void* d_logits, void* stream) {
+  if (!h) return rfail(EP_ERR_INVALID_ARG, "router handle is NULL");
+  if (!d_logits) return rfail(EP_ERR_INVALID_ARG, "d_logits must be given");
+  if (!d_weights && !d_loss)
+    return rfail(EP_ERR_INVALID_ARG, "give d_weights, or counts and d_loss, or all three");
+  if (d_weights && !indices) return rfail(EP_ERR_INVALID_ARG, "d_weights needs indices");
+  if ((counts == nullptr) != (d_loss == nullptr))
+    return rfail(EP_ERR_INVALID_ARG, "give counts and d_loss together, or neither");
+  RouterGradParams q;
+  memset(&q, 0, sizeof(q));
+  ep_status s = fill_params(h, logits, num_tokens, &q.r);
+  if (s != EP_OK) return s;
+  const size_t size = h->cfg.logits_dtype == EP_DTYPE_FP32 ? 4 : 2;
+  if ((uintptr_t)d_logits % size != 0)
+    return rfail(EP_ERR_INVALID_ARG, "d_logits is misaligned");
+  if ((uintptr_t)d_logits % 16 != 0) q.r.vec = 0;
+  q.r.idx_in = indices;
+  q.d_w = d_weights; q.counts = counts; q.d_loss = d_loss;
+  q.coef = coef_of(h, q.r);
+  q.d_logits = d_logits;
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if ((s = router_ready(h, st)) != EP_OK) return s;
+  const bool f32 = h->cfg.logits_dtype == EP_DTYPE_FP32;
+  const bool sig = h->cfg.score_func == EP_SCORE_SIGMOID;
+  const int grid = (int)h->total_chunks;
+  const cudaError_t e = f32 ? (sig ? grad_typed<float, true>(q, grid, st)
+                                   : grad_typed<float, false>(q, grid, st))
+                            : (sig ? grad_typed<__nv_bfloat16, true>(q, grid, st)
+                                   : grad_typed<__nv_bfloat16, false>(q, grid, st));
+  return e == cudaSuccess ? EP_OK : rcuda(e);
+}
+
+extern "C" ep_status ep_router_sync(ep_router_handle* h, void* stream) {
+  if (!h) return rfail(EP_ERR_INVALID_ARG, "router handle is NULL");
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  int32_t bits = 0;
+  cudaError_t e = cudaSuccess;
+  if (!h->needs_init) {
+    e = cudaMemcpyAsync(&bits, h->err, sizeof(bits), cudaMemcpyDeviceToHost, st);
+    if (e == cudaSuccess) e = cudaMemsetAsync(h->err, 0, sizeof(bits), st);
+  }
+  if (e == cudaSuccess) e = cudaStreamSynchronize(st);
+  if (e != cudaSuccess) return rcuda(e);
+  if (bits & kErrRouterIndex)
+    return rfail(EP_ERR_INVALID_INDEX, "expert id outside [-1, num_experts) skipped");
+  if (bits & kErrNotFinite)
+    return rfail(EP_ERR_INVALID_ARG, "a logit was NaN or +inf and was left out");
+  return EP_OK;
+}

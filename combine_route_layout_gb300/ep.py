@@ -42,6 +42,13 @@ EP_COMBINE_BULK = 2
 EP_DISPATCH_AUTO = 0
 EP_DISPATCH_VECTOR = 1
 EP_DISPATCH_BULK = 2
+EP_SCORE_SOFTMAX = 0
+EP_SCORE_SIGMOID = 1
+EP_ACT_NONE = 0
+EP_ACT_RELU = 1
+EP_ACT_SILU = 2
+EP_ACT_GELU = 3
+EP_ACT_SWIGLU = 4
 EP_PHASE_DISPATCH = 0
 EP_PHASE_COMBINE = 1
 IMPL_OF = {"auto": 0, "vector": 1, "bulk": 2}        # same codes for both phases
@@ -72,6 +79,19 @@ class ep_config(ctypes.Structure):
         "combine_impl", "dispatch_impl", "use_external_inp_buf")]
 
 
+class ep_router_config(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in (
+        "world_size", "max_num_inp_token_per_rank", "num_experts", "num_experts_per_token",
+        "logits_dtype", "score_func", "num_groups", "topk_groups", "normalize_weights",
+        "seq_len")] + [("route_scale", ctypes.c_float), ("balance_coef", ctypes.c_float)]
+
+
+class ep_linear_config(ctypes.Structure):
+    _fields_ = [("max_rows", ctypes.c_int64)] + [(n, ctypes.c_int32) for n in (
+        "num_groups", "groups_per_base", "in_features", "out_features", "out_dtype",
+        "weight_grad_dtype", "activation", "backward")]
+
+
 class ep_dispatch_out(ctypes.Structure):
     _fields_ = [("x", ctypes.c_void_p), ("scales", ctypes.c_void_p),
                 ("weights", ctypes.c_void_p), ("indices", ctypes.c_void_p),
@@ -94,7 +114,7 @@ def _load() -> ctypes.CDLL:
                           "(there is no fallback path)")
     lib = ctypes.CDLL(LIB_PATH)
     P, I, Z = ctypes.c_void_p, ctypes.c_int32, ctypes.c_size_t
-    S = ctypes.c_int
+    S, L = ctypes.c_int, ctypes.c_int64
     sig = {
         "ep_workspace_size": (Z, [P]),
         "ep_config_create": (S, [P, P, Z, P]),
@@ -126,6 +146,19 @@ def _load() -> ctypes.CDLL:
         "ep_rank_get_registered_combine_input_buffer": (S, [P, P]),
         "ep_rank_get_dispatch_src_token_pos": (S, [P, P]),
         "ep_rank_sync": (S, [P, P]),
+        "ep_router_workspace_size": (Z, [P]),
+        "ep_router_create": (S, [P, P, Z, P]),
+        "ep_router_destroy": (None, [P]),
+        "ep_router_forward": (S, [P] * 9),
+        "ep_router_balance_loss": (S, [P] * 7),
+        "ep_router_backward": (S, [P] * 9),
+        "ep_router_sync": (S, [P, P]),
+        "ep_linear_workspace_size": (Z, [P]),
+        "ep_linear_create": (S, [P, P, Z, P]),
+        "ep_linear_destroy": (None, [P]),
+        "ep_linear_forward": (S, [P] * 8 + [L] + [P] * 3),
+        "ep_linear_backward": (S, [P] * 8 + [L] + [P] * 4),
+        "ep_linear_sync": (S, [P, P]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -314,6 +347,79 @@ def ep_rank_get_dispatch_src_token_pos(handle) -> int:
 
 def ep_rank_sync(handle, stream) -> None:
     _check(_lib.ep_rank_sync(handle, stream))
+
+
+# ------------------------------------- router, balance loss, experts' products
+
+def ep_router_workspace_size(cfg: ep_router_config) -> int:
+    return int(_lib.ep_router_workspace_size(ctypes.byref(cfg)))
+
+
+def ep_router_create(cfg: ep_router_config, d_workspace: int, workspace_bytes: int) -> int:
+    h = ctypes.c_void_p()
+    _check(_lib.ep_router_create(ctypes.byref(cfg), d_workspace, workspace_bytes,
+                                 ctypes.byref(h)))
+    return h.value
+
+
+def ep_router_destroy(handle: int) -> None:
+    _lib.ep_router_destroy(handle)
+
+
+def _i32_array_or_none(values):
+    return None if values is None else _i32_array(values)
+
+
+def ep_router_forward(handle, logits, bias, num_tokens, indices, weights, counts, loss,
+                      stream) -> None:
+    _check(_lib.ep_router_forward(handle, logits, bias, _i32_array_or_none(num_tokens), indices,
+                                  weights, counts, loss, stream))
+
+
+def ep_router_balance_loss(handle, logits, indices, num_tokens, counts, loss, stream) -> None:
+    _check(_lib.ep_router_balance_loss(handle, logits, indices, _i32_array_or_none(num_tokens),
+                                       counts, loss, stream))
+
+
+def ep_router_backward(handle, logits, indices, num_tokens, d_weights, counts, d_loss, d_logits,
+                       stream) -> None:
+    _check(_lib.ep_router_backward(handle, logits, indices, _i32_array_or_none(num_tokens),
+                                   d_weights, counts, d_loss, d_logits, stream))
+
+
+def ep_router_sync(handle, stream) -> None:
+    _check(_lib.ep_router_sync(handle, stream))
+
+
+def ep_linear_workspace_size(cfg: ep_linear_config) -> int:
+    return int(_lib.ep_linear_workspace_size(ctypes.byref(cfg)))
+
+
+def ep_linear_create(cfg: ep_linear_config, d_workspace: int, workspace_bytes: int) -> int:
+    h = ctypes.c_void_p()
+    _check(_lib.ep_linear_create(ctypes.byref(cfg), d_workspace, workspace_bytes,
+                                 ctypes.byref(h)))
+    return h.value
+
+
+def ep_linear_destroy(handle: int) -> None:
+    _lib.ep_linear_destroy(handle)
+
+
+def ep_linear_forward(handle, x, weight, bias, residual, row_begin, row_count, row_base,
+                      num_rows: int, y, preact, stream) -> None:
+    _check(_lib.ep_linear_forward(handle, x, weight, bias, residual, row_begin, row_count,
+                                  row_base, int(num_rows), y, preact, stream))
+
+
+def ep_linear_backward(handle, dy, x, weight, preact, row_begin, row_count, row_base,
+                       num_rows: int, dx, dweight, dbias, stream) -> None:
+    _check(_lib.ep_linear_backward(handle, dy, x, weight, preact, row_begin, row_count, row_base,
+                                   int(num_rows), dx, dweight, dbias, stream))
+
+
+def ep_linear_sync(handle, stream) -> None:
+    _check(_lib.ep_linear_sync(handle, stream))
 
 
 # ------------------------------------------------------- operator class

@@ -496,6 +496,196 @@ ep_status ep_routing_layout_noalloc(int32_t world_size, int32_t max_num_inp_toke
                                     int32_t* recv_num_token, int32_t* src_token_pos,
                                     int32_t* slot_map, int32_t* error_flags, void* stream);
 
+/*
+ * ---------------------------------------------------------------------------
+ * The router of a mixture-of-experts layer: what makes the indices and
+ * weights that dispatch takes, its balance loss, and their gradients. The
+ * pages take both as inputs (User Guide, section 7); this is the layer's own
+ * side of them.
+ *
+ * Logits l of one token, over E experts. An expert is masked for the token
+ * where l is -inf or the type's lowest finite value; NaN and +inf are left
+ * out too and raise EP_ERR_INVALID_ARG at ep_router_sync.
+ *   softmax   selects by l; p_e = exp(l_e) / sum exp(l)
+ *   sigmoid   s_e = 1 / (1 + exp(-l_e)), selects by s_e + bias_e (in f32);
+ *             p_e = s_e / sum s
+ * With num_groups > 1 only the topk_groups best groups of E / num_groups
+ * consecutive experts stay (groups that are a rank's experts bound the ranks
+ * that a token travels to): by their largest l (softmax) or the sum of their
+ * two best s + bias (sigmoid). The num_experts_per_token best experts left,
+ * ties to the lowest index, best first, have the weights
+ *   softmax   p_e; normalize_weights: softmax over the selected
+ *   sigmoid   s_e; normalize_weights: s_e / sum of the selected s
+ * times route_scale; a slot with no expert left holds index -1, weight 0.
+ *
+ * Balance loss of a segment of n tokens: sum_e f_e P_e with
+ * f_e = count_e E / (k n) and P_e the mean of p_e; the loss is balance_coef
+ * times its mean over the segments that hold tokens. Sums run in a fixed
+ * order: results do not change from run to run.
+ *
+ * Calls of one handle share its workspace: the caller orders them.
+ * ---------------------------------------------------------------------------
+ */
+#define EP_MAX_ROUTER_GROUPS 32
+
+typedef enum {
+    EP_SCORE_SOFTMAX = 0,
+    EP_SCORE_SIGMOID = 1
+} ep_score;
+
+typedef struct ep_router_config {
+    int32_t world_size;                  /* source ranks, 1..EP_MAX_WORLD_SIZE */
+    int32_t max_num_inp_token_per_rank;  /* Tmax */
+    int32_t num_experts;                 /* E, 1..EP_MAX_EXPERTS */
+    int32_t num_experts_per_token;       /* k, 1..min(EP_MAX_TOPK, E) */
+    int32_t logits_dtype;                /* ep_dtype of logits and their gradient: FP32, BF16 */
+    int32_t score_func;                  /* ep_score */
+    int32_t num_groups;                  /* divides E; 1: no group limit */
+    int32_t topk_groups;                 /* groups that stay; they hold >= k experts */
+    int32_t normalize_weights;           /* 1: the selected weights add up to route_scale */
+    int32_t seq_len;                     /* balance loss: tokens per segment within a rank;
+                                            0: all tokens of the call are one segment */
+    float route_scale;
+    float balance_coef;
+} ep_router_config;
+
+typedef struct ep_router_handle ep_router_handle;
+
+/* Workspace bytes (0 if the config is invalid). Host only. */
+size_t ep_router_workspace_size(const ep_router_config* cfg);
+
+/* A handle over `d_workspace` (device, 256-byte aligned, the caller's). Makes no CUDA call. */
+ep_status ep_router_create(const ep_router_config* cfg, void* d_workspace, size_t workspace_bytes,
+                           ep_router_handle** out_handle);
+
+/* Free the host-side handle. NULL is a no-op. */
+void ep_router_destroy(ep_router_handle* h);
+
+/*
+ *   logits      device [R][Tmax][E], logits_dtype
+ *   bias        device [E] f32 or NULL: added to sigmoid scores for the selection
+ *               alone (EP_ERR_UNSUPPORTED with softmax scores)
+ *   num_tokens  host [R] or NULL (all Tmax)
+ *   indices     device [R][Tmax][k] out; -1 in rows past num_tokens
+ *   weights     device [R][Tmax][k] f32 out; 0 there
+ *   counts      device [segments][E] int32 out or NULL: slots that chose each
+ *               expert; segments = 1, or R * ceil(Tmax / seq_len)
+ *   loss        device f32 scalar out or NULL (given with counts, or neither)
+ */
+ep_status ep_router_forward(ep_router_handle* h, const void* logits, const float* bias,
+                            const int32_t* num_tokens, int32_t* indices, float* weights,
+                            int32_t* counts, float* loss, void* stream);
+
+/* Counts and loss of indices decided elsewhere (-1: dropped slot; ids outside
+ * [-1, E) are skipped and raise EP_ERR_INVALID_INDEX at ep_router_sync). */
+ep_status ep_router_balance_loss(ep_router_handle* h, const void* logits, const int32_t* indices,
+                                 const int32_t* num_tokens, int32_t* counts, float* loss,
+                                 void* stream);
+
+/*
+ * Gradient in the logits of the weights, of the balance loss, or of both.
+ *   indices    as forward gave them (needed with d_weights)
+ *   d_weights  device [R][Tmax][k] f32 or NULL
+ *   counts     device [segments][E] as forward or balance_loss gave them, and
+ *   d_loss     device f32 scalar, or both NULL
+ *   d_logits   device [R][Tmax][E] out, logits_dtype; 0 for masked experts
+ *              and in rows past num_tokens
+ * The selection, the counts and the bias carry no gradient.
+ */
+ep_status ep_router_backward(ep_router_handle* h, const void* logits, const int32_t* indices,
+                             const int32_t* num_tokens, const float* d_weights,
+                             const int32_t* counts, const float* d_loss, void* d_logits,
+                             void* stream);
+
+/* Wait for `stream`, then report and clear device-detected errors. */
+ep_status ep_router_sync(ep_router_handle* h, void* stream);
+
+/*
+ * ---------------------------------------------------------------------------
+ * The experts' products: a matrix product with bias, activation and residual
+ * in its epilogue, for each segment of a row pool (the packed standard-MoE
+ * layout: one segment per expert) or for all its rows (one dense product):
+ *     z = x W_g^T + bias_g         y = act(z) + residual
+ * and its backward pass
+ *     dz = dy act'(z)    dx = dz W_g    dW_g = dz^T x    dbias_g = sum of dz
+ * (the residual's gradient is dy). SWIGLU takes 2 N weight rows, gate rows
+ * first: y = silu(z_gate) z_up + residual.
+ *
+ * bf16 operands, f32 accumulation. z and dz are rounded to bf16, z because it
+ * is stored, dz because it is a tensor-core operand; dbias sums dz unrounded.
+ * Rows outside the segments are neither used nor written.
+ *
+ * Calls of one handle share its workspace: the caller orders them.
+ * ---------------------------------------------------------------------------
+ */
+typedef enum {
+    EP_ACT_NONE = 0,
+    EP_ACT_RELU = 1,
+    EP_ACT_SILU = 2,
+    EP_ACT_GELU = 3,       /* 0.5 z (1 + erf(z / sqrt 2)) */
+    EP_ACT_SWIGLU = 4
+} ep_activation;
+
+typedef struct ep_linear_config {
+    int64_t max_rows;          /* rows of the pool */
+    int32_t num_groups;        /* segments (experts), 1..EP_MAX_EXPERTS; 1: may be dense */
+    int32_t groups_per_base;   /* row_base[g / groups_per_base] is added to row_begin[g] */
+    int32_t in_features;       /* K, a multiple of 8 */
+    int32_t out_features;      /* N */
+    int32_t out_dtype;         /* ep_dtype of y, residual and dy: BF16, FP32 */
+    int32_t weight_grad_dtype; /* ep_dtype of dweight: BF16, FP32 */
+    int32_t activation;        /* ep_activation */
+    int32_t backward;          /* 1: reserve the backward pass's scratch */
+} ep_linear_config;
+
+typedef struct ep_linear_handle ep_linear_handle;
+
+/* Workspace bytes (0 if the config is invalid). Host only. */
+size_t ep_linear_workspace_size(const ep_linear_config* cfg);
+
+/* A handle over `d_workspace` (device, 256-byte aligned, the caller's). Makes no CUDA call. */
+ep_status ep_linear_create(const ep_linear_config* cfg, void* d_workspace, size_t workspace_bytes,
+                           ep_linear_handle** out_handle);
+
+/* Free the host-side handle. NULL is a no-op. */
+void ep_linear_destroy(ep_linear_handle* h);
+
+/*
+ *   x          device [max_rows][K] bf16, 16-byte aligned
+ *   weight     device [G][Nw][K] bf16, 16-byte aligned; Nw = N, or 2 N (SWIGLU)
+ *   bias       device [G][Nw] f32 or NULL
+ *   residual   device [max_rows][N] out_dtype or NULL (may be y itself)
+ *   row_begin, row_count  device [G] int32: segment g's rows; row_base (or
+ *              NULL) as groups_per_base says: the packed layout's
+ *              expert_offset, packed_count and rank_base with groups_per_base =
+ *              num_experts_per_rank. Both NULL (one group): rows
+ *              [0, num_rows). A segment that reaches outside the pool is cut
+ *              and raises EP_ERR_INVALID_INDEX at ep_linear_sync.
+ *   y          device [max_rows][N] out_dtype
+ *   preact     device [max_rows][Nw] bf16 out (z) or NULL
+ */
+ep_status ep_linear_forward(ep_linear_handle* h, const void* x, const void* weight,
+                            const float* bias, const void* residual, const int32_t* row_begin,
+                            const int32_t* row_count, const int32_t* row_base, int64_t num_rows,
+                            void* y, void* preact, void* stream);
+
+/*
+ *   dy       device [max_rows][N] out_dtype
+ *   preact   device [max_rows][Nw] bf16 as forward wrote it (may be NULL
+ *            without an activation)
+ *   dx       device [max_rows][K] bf16 out or NULL
+ *   dweight  device [G][Nw][K] weight_grad_dtype out or NULL; 0 for a group
+ *            with no rows
+ *   dbias    device [G][Nw] f32 out or NULL
+ */
+ep_status ep_linear_backward(ep_linear_handle* h, const void* dy, const void* x,
+                             const void* weight, const void* preact, const int32_t* row_begin,
+                             const int32_t* row_count, const int32_t* row_base, int64_t num_rows,
+                             void* dx, void* dweight, float* dbias, void* stream);
+
+/* Wait for `stream`, then report and clear device-detected errors. */
+ep_status ep_linear_sync(ep_linear_handle* h, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
