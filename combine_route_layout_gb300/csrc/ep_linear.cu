@@ -1,6 +1,7 @@
-// The experts' products: y = act(x W^T + b) + residual over the segments of a
-// row pool (the packed layout's, one per expert, or one dense product), and
-// its backward pass. Host library and kernels.
+// Host library of the experts' products, y = act(x W^T + b) + residual over
+// the segments of a row pool (the packed layout's, one per expert, or one
+// dense product), and the elementwise kernels of the backward pass. The
+// products themselves are in ep_linear_mma.cu.
 #include <climits>
 #include <cstring>
 #include <new>
@@ -9,112 +10,6 @@
 
 namespace ep {
 namespace {
-
-constexpr int kTile = 64, kDepth = 16;
-
-// The simple form of the three products: a CTA computes a 64 x 64 tile of one
-// group's output, 16 terms at a time through shared memory, f32 sums in
-// registers. blockIdx.x: column tile; blockIdx.y strides the row tiles of all
-// groups (forward, dx) or the tiles of dW's rows of each group.
-enum { kForward = 0, kInputGrad = 1, kWeightGrad = 2 };
-
-template <int MODE>
-__global__ void __launch_bounds__(256) product_kernel(LinearParams p) {
-  __shared__ float sa[kDepth][kTile + 1], sb[kDepth][kTile + 1], su[kDepth][kTile + 1];
-  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  const bool gated = MODE == kForward && p.act == EP_ACT_SWIGLU;
-  const int64_t col0 = (int64_t)blockIdx.x * kTile;
-  int64_t seen = 0;
-  for (int g = 0; g < p.s.G; ++g) {
-    int64_t begin, count;
-    segment_of(p.s, g, begin, count);
-    const int64_t rows = MODE == kWeightGrad ? p.Nw : count;
-    const int64_t tiles = (rows + kTile - 1) / kTile;
-    for (int64_t t = ((int64_t)blockIdx.y - seen % gridDim.y + gridDim.y) % gridDim.y; t < tiles;
-         t += gridDim.y) {
-      const int64_t row0 = t * kTile;
-      const int64_t depth = MODE == kForward ? p.K : MODE == kInputGrad ? p.Nw : count;
-      const int64_t cols = MODE == kForward ? p.N : p.K;
-      const __nv_bfloat16* w = p.w + (int64_t)g * p.Nw * p.K;
-      float acc[4][4] = {}, up[4][4] = {};
-      for (int64_t d0 = 0; d0 < depth; d0 += kDepth) {
-        for (int i = threadIdx.x; i < kTile * kDepth; i += 256) {
-          // consecutive threads walk the operand's contiguous axis
-          const int d = MODE == kWeightGrad ? i / kTile : i % kDepth;
-          const int r = MODE == kWeightGrad ? i % kTile : i / kDepth;
-          const int db = MODE == kForward ? i % kDepth : i / kTile;
-          const int c = MODE == kForward ? i / kDepth : i % kTile;
-          float a = 0.0f, b = 0.0f, u = 0.0f;
-          if (row0 + r < rows && d0 + d < depth) {
-            if (MODE == kForward) a = __bfloat162float(p.x[(begin + row0 + r) * p.K + d0 + d]);
-            if (MODE == kInputGrad) a = __bfloat162float(p.dz[(begin + row0 + r) * p.ldz + d0 + d]);
-            if (MODE == kWeightGrad) a = __bfloat162float(p.dz[(begin + d0 + d) * p.ldz + row0 + r]);
-          }
-          if (col0 + c < cols && d0 + db < depth) {
-            if (MODE == kForward) {
-              b = __bfloat162float(w[(col0 + c) * p.K + d0 + db]);
-              if (gated) u = __bfloat162float(w[(p.N + col0 + c) * p.K + d0 + db]);
-            }
-            if (MODE == kInputGrad) b = __bfloat162float(w[(d0 + db) * p.K + col0 + c]);
-            if (MODE == kWeightGrad) b = __bfloat162float(p.x[(begin + d0 + db) * p.K + col0 + c]);
-          }
-          sa[d][r] = a;
-          sb[db][c] = b;
-          if (gated) su[db][c] = u;
-        }
-        __syncthreads();
-#pragma unroll
-        for (int d = 0; d < kDepth; ++d)
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              acc[i][j] += sa[d][ty * 4 + i] * sb[d][tx + 16 * j];
-              if (gated) up[i][j] += sa[d][ty * 4 + i] * su[d][tx + 16 * j];
-            }
-        __syncthreads();
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int64_t r = row0 + ty * 4 + i, c = col0 + tx + 16 * j;
-          if (r >= rows || c >= cols) continue;
-          float v = acc[i][j];
-          if (MODE == kForward) {
-            if (p.bias) v += p.bias[(int64_t)g * p.Nw + c];
-            if (p.z) p.z[(begin + r) * p.Nw + c] = __float2bfloat16_rn(v);
-            if (gated) {
-              float u = up[i][j];
-              if (p.bias) u += p.bias[(int64_t)g * p.Nw + p.N + c];
-              if (p.z) p.z[(begin + r) * p.Nw + p.N + c] = __float2bfloat16_rn(u);
-              v = silu_of(v) * u;
-            } else {
-              v = act_of(p.act, v);
-            }
-            const int64_t o = (begin + r) * p.N + c;
-            if (p.y_f32) {
-              if (p.residual) v += static_cast<const float*>(p.residual)[o];
-              static_cast<float*>(p.y)[o] = v;
-            } else {
-              if (p.residual) v += __bfloat162float(static_cast<const __nv_bfloat16*>(p.residual)[o]);
-              static_cast<__nv_bfloat16*>(p.y)[o] = __float2bfloat16_rn(v);
-            }
-          } else if (MODE == kInputGrad) {
-            p.dx[(begin + r) * p.K + c] = __float2bfloat16_rn(v);
-          } else {
-            const int64_t o = ((int64_t)g * p.Nw + r) * p.K + c;
-            if (p.dw_f32) {
-              static_cast<float*>(p.dw)[o] = v;
-            } else {
-              static_cast<__nv_bfloat16*>(p.dw)[o] = __float2bfloat16_rn(v);
-            }
-          }
-        }
-    }
-    seen += tiles;
-  }
-}
 
 // dz = dy act'(z) and the sums of dz's columns over each block of rows. A CTA
 // takes kGradRows rows of one group and 256 weight rows' columns, a thread a
@@ -199,6 +94,7 @@ struct ep_linear_handle {
   ep_linear_config cfg;
   uint8_t* ws;
   bool needs_init;
+  int sm_count;
   int Nw;
   int64_t ldz, row_blocks;
   int32_t* err;
@@ -233,6 +129,12 @@ ep_status plan_linear(const ep_linear_config* c, ep_linear_handle* h) {
     return lfail(EP_ERR_INVALID_ARG, "weight_grad_dtype must be BF16 or FP32");
   if (c->activation < EP_ACT_NONE || c->activation > EP_ACT_SWIGLU)
     return lfail(EP_ERR_INVALID_ARG, "unknown activation");
+  // tiles are numbered in int32: at most one per 32 rows (and group) and 256 features
+  const int64_t wide = (2 * (int64_t)c->out_features > c->in_features ? 2 * (int64_t)c->out_features
+                                                                      : c->in_features) / 256 + 1;
+  if ((c->max_rows / 32 + c->num_groups) * wide > INT32_MAX ||
+      (int64_t)c->num_groups * wide * (c->in_features / 256 + 1) > INT32_MAX)
+    return lfail(EP_ERR_INVALID_ARG, "max_rows, num_groups and features give too many tiles");
   h->cfg = *c;
   h->Nw = c->activation == EP_ACT_SWIGLU ? 2 * c->out_features : c->out_features;
   h->ldz = (h->Nw + 7) / 8 * 8;
@@ -253,6 +155,13 @@ ep_status plan_linear(const ep_linear_config* c, ep_linear_handle* h) {
 
 // As the router's: a captured call leaves the clearing to the next one too.
 ep_status linear_ready(ep_linear_handle* h, cudaStream_t st) {
+  if (h->sm_count == 0) {
+    int dev = 0, n = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
+    if (e != cudaSuccess) return lcuda(e);
+    h->sm_count = n;
+  }
   if (!h->needs_init) return EP_OK;
   cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
   cudaError_t e = cudaStreamIsCapturing(st, &cap);
@@ -299,16 +208,7 @@ ep_status fill_linear(const ep_linear_handle* h, const void* x, const void* w,
   return EP_OK;
 }
 
-template <int MODE>
-ep_status launch_product(const LinearParams& p, cudaStream_t st) {
-  const int64_t cols = MODE == kForward ? p.N : p.K;
-  int64_t rows = MODE == kWeightGrad ? (int64_t)p.s.G * ((p.Nw + kTile - 1) / kTile)
-                                     : p.s.pool / kTile + p.s.G;
-  if (rows > 4096) rows = 4096;
-  product_kernel<MODE><<<dim3((unsigned)((cols + kTile - 1) / kTile), (unsigned)rows), 256, 0, st>>>(p);
-  const cudaError_t e = cudaGetLastError();
-  return e == cudaSuccess ? EP_OK : lcuda(e);
-}
+ep_status status_of(cudaError_t e) { return e == cudaSuccess ? EP_OK : lcuda(e); }
 
 }  // namespace
 
@@ -358,7 +258,7 @@ extern "C" ep_status ep_linear_forward(ep_linear_handle* h, const void* x, const
   p.z = static_cast<__nv_bfloat16*>(preact);
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   if ((s = linear_ready(h, st)) != EP_OK) return s;
-  return launch_product<kForward>(p, st);
+  return status_of(launch_linear_forward(p, h->sm_count, st));
 }
 
 extern "C" ep_status ep_linear_backward(ep_linear_handle* h, const void* dy, const void* x,
@@ -402,9 +302,8 @@ extern "C" ep_status ep_linear_backward(ep_linear_handle* h, const void* dy, con
   }
   if (e != cudaSuccess) return lcuda(e);
   p.dz = h->dz;
-  if (dx && (s = launch_product<kInputGrad>(p, st)) != EP_OK) return s;
-  if (dweight && (s = launch_product<kWeightGrad>(p, st)) != EP_OK) return s;
-  return EP_OK;
+  if (dx && (s = status_of(launch_linear_input_grad(p, h->sm_count, st))) != EP_OK) return s;
+  return dweight ? status_of(launch_linear_weight_grad(p, h->sm_count, st)) : EP_OK;
 }
 
 extern "C" ep_status ep_linear_sync(ep_linear_handle* h, void* stream) {
@@ -418,6 +317,8 @@ extern "C" ep_status ep_linear_sync(ep_linear_handle* h, void* stream) {
   }
   if (e == cudaSuccess) e = cudaStreamSynchronize(st);
   if (e != cudaSuccess) return lcuda(e);
+  if (bits & kErrLinearTimeout)
+    return lfail(EP_ERR_TIMEOUT, "a product's bounded wait gave up; its output is not complete");
   if (bits & kErrSegment)
     return lfail(EP_ERR_INVALID_INDEX, "a segment reached outside the row pool and was cut");
   return EP_OK;

@@ -1,0 +1,581 @@
+// The three products of an expert layer on the tensor cores: z = x W^T,
+// dx = dz W, dW = dz^T x, with the forward's bias, activation and residual in
+// the epilogue.
+//
+// Every output is computed transposed: the tensor core's M side is the
+// output's contiguous axis (features), its N side the rows (tokens, or dW's
+// rows). That way the weights always fill M = 256, a tile takes as many rows
+// as an expert has (N in steps of 32, so ragged experts waste no arithmetic
+// and few-row experts cost weight traffic alone), a lane of the accumulator is
+// one feature (one bias value per thread) and a warp stores 32 consecutive
+// features of a row.
+//
+// A pair of CTAs (two SMs) shares one tile of 256 features x up to 256 rows:
+// each stages its 128 features and its half of the rows, 64 terms at a time,
+// by TMA with 128-byte swizzle into a ring of stages; one thread of the even
+// CTA issues the MMAs, the accumulators (two, so that a tile's epilogue runs
+// under the next one's products) stay in TMEM. Grid: one CTA per SM, each pair
+// walks the tiles of all groups.
+//
+// Roles by warp: 0 TMA, 1 MMA, 4-7 epilogue (TMEM lanes go by warp % 4).
+#include <cuda.h>
+
+#include <cstring>
+
+#include "ep_linear.cuh"
+#include "ep_mma.cuh"
+
+namespace ep {
+namespace {
+
+constexpr int kStages = 6;
+constexpr int kDepth = 64;                       // terms per stage: 128 bytes of bf16
+constexpr int kStageA = 128 * kDepth * 2;        // bytes of a CTA's 128 features
+constexpr int kStageB = 128 * kDepth * 2;        // bytes of a CTA's half of the rows
+constexpr int kStageBytes = kStageA + kStageB;
+constexpr int kMaxRows = 256;                    // rows of a tile
+constexpr int kThreads = 256;
+constexpr int kTmemColumns = 512;                // two accumulators
+
+enum Mode { kForward = 0, kInputGrad = 1, kWeightGrad = 2 };
+
+struct MmaParams {
+  LinearParams p;
+  int features;      // length of the output's contiguous axis (weight rows or K)
+  int f_tiles;       // 256-feature tiles
+  int r_tiles;       // dW: 256-row tiles of each group (else by the group's count)
+};
+
+struct Barriers {
+  uint64_t full[kStages];     // both CTAs' operands have landed (even CTA's)
+  uint64_t empty[kStages];    // this CTA's stage may be written again
+  uint64_t landed;            // dW: this CTA's last block, whose tail is cleared
+  uint64_t acc_full[2];
+  uint64_t acc_empty[2];      // even CTA's: both CTAs' epilogues are done
+  uint32_t tmem;
+};
+
+// A tile of one group.
+struct Tile {
+  int g;
+  int64_t begin;     // first pool row of the group
+  int count;         // its rows
+  int r0, rows;      // rows of the tile within the group (dW: of the weight rows)
+  int f0;            // first feature
+  int n;             // MMA's N
+  int blocks;        // stages
+  int terms;         // length of the contraction
+};
+
+// Rows of a tile and tiles of a group of `count` rows: as few tiles as 256
+// rows allow, of about equal size.
+__device__ __forceinline__ int tile_rows(int count) {
+  const int tiles = (count + kMaxRows - 1) / kMaxRows;
+  return tiles ? ((count + tiles - 1) / tiles + 31) / 32 * 32 : 32;
+}
+
+template <int MODE>
+__device__ __forceinline__ Tile tile_at(const MmaParams& q, const int* first, const int* begins,
+                                        const int* counts, int t) {
+  Tile w;
+  int lo = 0, hi = q.p.s.G - 1;          // the last group that starts at or before t
+  if (MODE == kWeightGrad) {
+    lo = t / (q.f_tiles * q.r_tiles);
+    t -= lo * (q.f_tiles * q.r_tiles);
+  } else {
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (first[mid] <= t) lo = mid; else hi = mid - 1;
+    }
+    t -= first[lo];
+  }
+  w.g = lo;
+  w.begin = begins[lo];
+  w.count = counts[lo];
+  if (MODE == kWeightGrad) {
+    w.r0 = (t / q.f_tiles) * kMaxRows;
+    w.f0 = (t % q.f_tiles) * 256;
+    w.rows = min(kMaxRows, q.p.Nw - w.r0);
+    w.n = w.rows > 128 ? 256 : 128;
+    w.terms = w.count;
+  } else {
+    // 8 row tiles at a time pass over all features, so that tiles that run
+    // together share operands in L2
+    const int size = tile_rows(w.count);
+    const int tiles = (w.count + size - 1) / size;
+    const int per = 8 * q.f_tiles;
+    const int band = t / per;
+    const int in = min(8, tiles - band * 8);
+    t -= band * per;
+    w.r0 = (band * 8 + t % in) * size;
+    w.f0 = (t / in) * 256;
+    w.rows = min(size, w.count - w.r0);
+    w.n = (w.rows + 31) / 32 * 32;
+    w.terms = MODE == kForward ? q.p.K : q.p.Nw;
+  }
+  w.blocks = (w.terms + kDepth - 1) / kDepth;
+  return w;
+}
+
+// The groups' segments and, over them, the first tile of each; returns the
+// number of tiles. All threads of the CTA.
+template <int MODE>
+__device__ int plan_tiles(const MmaParams& q, int* first, int* begins, int* counts) {
+  __shared__ int warp_sum_[kThreads / 32];
+  const int G = q.p.s.G;
+  const int per = (G + kThreads - 1) / kThreads;
+  const int g0 = threadIdx.x * per, g1 = min(G, g0 + per);
+  int mine = 0;
+  for (int g = g0; g < g1; ++g) {
+    int64_t b, c;
+    segment_of(q.p.s, g, b, c);
+    begins[g] = (int)b;
+    counts[g] = (int)c;
+    const int size = tile_rows((int)c);
+    mine += ((int)c + size - 1) / size * q.f_tiles;
+  }
+  if (MODE == kWeightGrad) {
+    __syncthreads();
+    return G * q.f_tiles * q.r_tiles;
+  }
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int incl = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(kFull, incl, o);
+    if (lane >= o) incl += v;
+  }
+  if (lane == 31) warp_sum_[warp] = incl;
+  __syncthreads();
+  int before = incl - mine, total = 0;
+  for (int w = 0; w < kThreads / 32; ++w) {
+    if (w < warp) before += warp_sum_[w];
+    total += warp_sum_[w];
+  }
+  for (int g = g0; g < g1; ++g) {
+    first[g] = before;
+    const int size = tile_rows(counts[g]);
+    before += (counts[g] + size - 1) / size * q.f_tiles;
+  }
+  __syncthreads();
+  return total;
+}
+
+// One value of the forward's epilogue.
+template <int ACT>
+__device__ __forceinline__ float activate(float v) {
+  return act_of(ACT, v);
+}
+
+template <int MODE, int ACT>
+__device__ __forceinline__ void store_columns(const MmaParams& q, const Tile& w, int cta, int lane,
+                                              int quad, int c0, const uint32_t (&r)[32], float b) {
+  const LinearParams& p = q.p;
+  const int f = quad * 32 + lane;          // lane of the accumulator
+  const int left = w.rows - c0;            // columns that exist
+  if (MODE == kForward && ACT == EP_ACT_SWIGLU) {
+    // even lanes hold a feature's gate, odd lanes its up value; a pair of
+    // lanes exchanges two columns so that each finishes one of them
+    const int out = w.f0 / 2 + cta * 64 + f / 2;
+    const bool in = out < p.N;
+    const bool odd = lane & 1;
+#pragma unroll
+    for (int c = 0; c < 32; c += 2) {
+      if (c >= left) break;
+      const float v0 = __uint_as_float(r[c]) + b, v1 = __uint_as_float(r[c + 1]) + b;
+      const int64_t row = w.begin + w.r0 + c0 + c;
+      if (p.z && in) {
+        const int64_t o = row * p.Nw + (odd ? p.N : 0) + out;
+        p.z[o] = __float2bfloat16_rn(v0);
+        if (c + 1 < left) p.z[o + p.Nw] = __float2bfloat16_rn(v1);
+      }
+      const float other = __shfl_xor_sync(kFull, odd ? v0 : v1, 1);
+      float y = odd ? silu_of(other) * v1 : silu_of(v0) * other;
+      if (!in || (odd && c + 1 >= left)) continue;
+      const int64_t o = (row + odd) * p.N + out;
+      if (p.y_f32) {
+        if (p.residual) y += static_cast<const float*>(p.residual)[o];
+        static_cast<float*>(p.y)[o] = y;
+      } else {
+        if (p.residual) y += __bfloat162float(static_cast<const __nv_bfloat16*>(p.residual)[o]);
+        static_cast<__nv_bfloat16*>(p.y)[o] = __float2bfloat16_rn(y);
+      }
+    }
+    return;
+  }
+  const int feature = w.f0 + cta * 128 + f;
+  if (feature >= q.features) return;
+#pragma unroll
+  for (int c = 0; c < 32; ++c) {
+    if (c >= left) break;
+    float v = __uint_as_float(r[c]);
+    if (MODE == kWeightGrad) {
+      const int64_t o = ((int64_t)w.g * p.Nw + w.r0 + c0 + c) * p.K + feature;
+      if (p.dw_f32) {
+        static_cast<float*>(p.dw)[o] = v;
+      } else {
+        static_cast<__nv_bfloat16*>(p.dw)[o] = __float2bfloat16_rn(v);
+      }
+      continue;
+    }
+    const int64_t row = w.begin + w.r0 + c0 + c;
+    if (MODE == kInputGrad) {
+      p.dx[row * p.K + feature] = __float2bfloat16_rn(v);
+      continue;
+    }
+    v += b;
+    const int64_t o = row * p.N + feature;
+    if (p.z) p.z[o] = __float2bfloat16_rn(v);
+    v = activate<ACT>(v);
+    if (p.y_f32) {
+      if (p.residual) v += static_cast<const float*>(p.residual)[o];
+      static_cast<float*>(p.y)[o] = v;
+    } else {
+      if (p.residual) v += __bfloat162float(static_cast<const __nv_bfloat16*>(p.residual)[o]);
+      static_cast<__nv_bfloat16*>(p.y)[o] = __float2bfloat16_rn(v);
+    }
+  }
+}
+
+// map_a: features; map_b: rows (box of 128 rows; dW: of 64 rows x 64 columns);
+// map_b16: the same in boxes of 16 rows, for tiles of fewer rows.
+template <int MODE, int ACT>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    product_kernel(const __grid_constant__ CUtensorMap map_a,
+                   const __grid_constant__ CUtensorMap map_b,
+                   const __grid_constant__ CUtensorMap map_b16, MmaParams q) {
+  constexpr bool kGated = MODE == kForward && ACT == EP_ACT_SWIGLU;
+  extern __shared__ uint8_t raw[];
+  uint8_t* ring = reinterpret_cast<uint8_t*>(((uintptr_t)raw + 1023) & ~(uintptr_t)1023);
+  Barriers* bar = reinterpret_cast<Barriers*>(ring + kStages * kStageBytes);
+  int* first = reinterpret_cast<int*>(bar + 1);
+  int* begins = first + q.p.s.G;
+  int* counts = begins + q.p.s.G;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const uint32_t cta = cluster_rank();
+  int32_t* timeout = q.p.s.err;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(&bar->full[s], 2);       // each CTA's producer
+      mbar_init(&bar->empty[s], 1);
+    }
+    mbar_init(&bar->landed, 1);
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(&bar->acc_full[a], 1);
+      mbar_init(&bar->acc_empty[a], 8);  // four epilogue warps of each CTA
+    }
+    mbar_init_fence();
+    tma_prefetch_map(&map_a);
+    tma_prefetch_map(&map_b);
+    if (MODE != kWeightGrad) tma_prefetch_map(&map_b16);
+  }
+  if (warp == 1) tmem_alloc(&bar->tmem, kTmemColumns);
+  const int tiles = plan_tiles<MODE>(q, first, begins, counts);
+  tc_fence_before();
+  cluster_sync();
+  tc_fence_after();
+  const uint32_t tmem = bar->tmem;
+  const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+
+  if (warp == 0) {
+    // ------------------------------------------------ producer
+    const bool one = lane == 0;
+    int it = 0;
+    uint32_t landed_phase = 0;
+    bool ok = true;
+    for (int t = pair; t < tiles && ok; t += pairs) {
+      const Tile w = tile_at<MODE>(q, first, begins, counts, t);
+      const int half = w.n / 2;
+      const int fc = w.f0 + (int)cta * 128;                     // this CTA's features
+      const int rc = w.r0 + (int)cta * half;                    // this CTA's rows
+      const int boxes = MODE == kWeightGrad ? half / 64 : half / 16;
+      const bool whole = half == 128;
+      const uint32_t bytes = kStageA + (MODE == kWeightGrad ? half / 64 * 8192 : half * 128);
+      for (int kb = 0; kb < w.blocks && ok; ++kb, ++it) {
+        const int s = it % kStages;
+        if (it >= kStages) {
+          ok = mbar_wait_cluster(&bar->empty[s], ((it / kStages) - 1) & 1);
+          if (!ok) break;
+          if (cta == 0 && one) mbar_arrive_at(in_cta(&bar->empty[s], 1));
+        }
+        uint8_t* a = ring + s * kStageBytes;
+        uint8_t* b = a + kStageA;
+        const int d = kb * kDepth;
+        const int valid = w.terms - d;                          // terms of this block
+        const bool tail = MODE == kWeightGrad && valid < kDepth && (valid & 15);
+        const uint32_t full = in_cta(&bar->full[s], 0);
+        const uint32_t on = tail ? smem_addr(&bar->landed) : full;
+        if (one) {
+          if (tail) {
+            mbar_arrive_expect_tx(&bar->landed, bytes);
+          } else {
+            mbar_arrive_expect_tx_at(full, bytes);
+          }
+          if (MODE == kForward) {
+            if (kGated) {
+              tma_load_4d(a, &map_a, d, 0, fc / 2, w.g, on);
+            } else {
+              tma_load_3d(a, &map_a, d, fc, w.g, on);
+            }
+          } else if (MODE == kInputGrad) {
+            tma_load_3d(a, &map_a, fc, d, w.g, on);
+            tma_load_3d(a + 8192, &map_a, fc + 64, d, w.g, on);
+          } else {
+            tma_load_2d(a, &map_a, fc, (int)w.begin + d, on);
+            tma_load_2d(a + 8192, &map_a, fc + 64, (int)w.begin + d, on);
+          }
+          if (MODE == kWeightGrad) {
+            for (int i = 0; i < boxes; ++i)
+              tma_load_2d(b + i * 8192, &map_b, rc + i * 64, (int)w.begin + d, on);
+          } else if (whole) {
+            tma_load_2d(b, &map_b, d, (int)w.begin + rc, on);
+          } else {
+            for (int i = 0; i < boxes; ++i)
+              tma_load_2d(b + i * 2048, &map_b16, d, (int)w.begin + rc + i * 16, on);
+          }
+        }
+        if (tail) {
+          // the rows after the segment's last belong to somebody else: clear
+          // those that the last 16-term step would take in
+          ok = mbar_wait(&bar->landed, landed_phase);
+          landed_phase ^= 1;
+          const int end = (valid + 15) / 16 * 16;
+          const int n16 = (2 + boxes) * (end - valid) * 8;      // 16-byte pieces
+          for (int i = lane; i < n16; i += 32) {
+            const int row = valid + i / 8 % (end - valid);
+            const int box = i / 8 / (end - valid);
+            uint8_t* at = (box < 2 ? a + box * 8192 : b + (box - 2) * 8192) + row * 128;
+            reinterpret_cast<uint4*>(at)[i & 7] = make_uint4(0, 0, 0, 0);
+          }
+          fence_async_shared();
+          __syncwarp();
+          if (one) mbar_arrive_at(full);
+        }
+      }
+    }
+    if (!ok) {
+      if (one) atomicOr(timeout, kErrLinearTimeout);
+      if (cta == 0)   // copies in flight must land before the CTA leaves
+        for (int s = 0; s < kStages && s < it; ++s)
+          (void)mbar_wait_cluster(&bar->full[s], ((it - 1 - s) / kStages) & 1);
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------ MMA (even CTA, one thread)
+    if (cta == 0 && lane == 0) {
+      int it = 0, n_acc = 0;
+      bool ok = true;
+      for (int t = pair; t < tiles && ok; t += pairs) {
+        const Tile w = tile_at<MODE>(q, first, begins, counts, t);
+        if (w.blocks == 0) continue;
+        const int acc = n_acc & 1;
+        if (n_acc >= 2) {
+          ok = mbar_wait_cluster(&bar->acc_empty[acc], ((n_acc >> 1) - 1) & 1);
+          if (!ok) break;
+          tc_fence_after();
+        }
+        const uint32_t d = tmem + acc * 256;
+        const uint32_t form = mma_form(w.n, MODE != kForward, MODE == kWeightGrad);
+        for (int kb = 0; kb < w.blocks; ++kb, ++it) {
+          const int s = it % kStages;
+          ok = mbar_wait_cluster(&bar->full[s], (it / kStages) & 1);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t a = smem_addr(ring + s * kStageBytes), b = a + kStageA;
+          const int steps = (min(kDepth, w.terms - kb * kDepth) + 15) / 16;
+          for (int i = 0; i < steps; ++i) {
+            // 16 terms on: 32 bytes of a row (K-major) or 16 rows (MN-major)
+            const uint64_t da = MODE == kForward ? smem_operand(a + i * 32, 16)
+                                                 : smem_operand(a + i * 2048, 8192);
+            const uint64_t db = MODE == kWeightGrad ? smem_operand(b + i * 2048, 8192)
+                                                    : smem_operand(b + i * 32, 16);
+            mma_pair(d, da, db, form, kb > 0 || i > 0);
+          }
+          mma_commit(&bar->empty[s]);
+        }
+        if (!ok) break;
+        mma_commit(&bar->acc_full[acc]);
+        ++n_acc;
+      }
+      if (!ok) atomicOr(timeout, kErrLinearTimeout);
+    }
+  } else if (warp >= 4) {
+    // ------------------------------------------------ epilogue
+    const int quad = warp - 4;
+    int n_acc = 0;
+    for (int t = pair; t < tiles; t += pairs) {
+      const Tile w = tile_at<MODE>(q, first, begins, counts, t);
+      float b = 0.0f;
+      if (MODE == kForward && q.p.bias) {
+        const int f = (int)cta * 128 + quad * 32 + lane;
+        const float* bias = q.p.bias + (int64_t)w.g * q.p.Nw;
+        if (kGated) {
+          const int out = w.f0 / 2 + f / 2;
+          if (out < q.p.N) b = __ldg(bias + (f & 1 ? q.p.N : 0) + out);
+        } else if (w.f0 + f < q.features) {
+          b = __ldg(bias + w.f0 + f);
+        }
+      }
+      if (w.blocks == 0) {   // a group with no rows: its weight gradient is zero
+        uint32_t zero[32];
+#pragma unroll
+        for (int c = 0; c < 32; ++c) zero[c] = 0;
+        for (int c0 = 0; c0 < w.rows; c0 += 32)
+          store_columns<MODE, ACT>(q, w, (int)cta, lane, quad, c0, zero, 0.0f);
+        continue;
+      }
+      const int acc = n_acc & 1;
+      if (!mbar_wait_cluster(&bar->acc_full[acc], (n_acc >> 1) & 1)) {
+        if (lane == 0) atomicOr(timeout, kErrLinearTimeout);
+        break;
+      }
+      if (cta == 0 && threadIdx.x == 128) mbar_arrive_at(in_cta(&bar->acc_full[acc], 1));
+      tc_fence_after();
+      for (int c0 = 0; c0 < w.rows; c0 += 32) {
+        uint32_t r[32];
+        tmem_load32(tmem + ((uint32_t)(quad * 32) << 16) + acc * 256 + c0, r);
+        store_columns<MODE, ACT>(q, w, (int)cta, lane, quad, c0, r, b);
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_at(in_cta(&bar->acc_empty[acc], 0));
+      ++n_acc;
+    }
+  }
+  __syncwarp();
+  __syncthreads();
+  cluster_sync();   // the other CTA may still arrive on this one's barriers
+  if (warp == 1) tmem_free(tmem, kTmemColumns);
+}
+
+// ---------------------------------------------------------------------- host
+
+using Encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                            const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                            const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                            CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+Encode encoder() {
+  static Encode fn = [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult found;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
+                                         &found) != cudaSuccess ||
+        found != cudaDriverEntryPointSuccess)
+      p = nullptr;
+    return reinterpret_cast<Encode>(p);
+  }();
+  return fn;
+}
+
+// A map of bf16 with 128-byte swizzle; zeros beyond the tensor's edges.
+bool make_map(CUtensorMap* m, const void* base, int rank, const int64_t* dims,
+              const int64_t* strides, const int* box) {
+  Encode fn = encoder();
+  if (!fn) return false;
+  cuuint64_t d[4], s[4];
+  cuuint32_t b[4], one[4] = {1, 1, 1, 1};
+  for (int i = 0; i < rank; ++i) {
+    d[i] = (cuuint64_t)(dims[i] > 0 ? dims[i] : 1);
+    b[i] = (cuuint32_t)box[i];
+    if (i) s[i - 1] = (cuuint64_t)strides[i] * 2;
+  }
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (cuuint32_t)rank, const_cast<void*>(base), d, s, b,
+            one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool map_rows(CUtensorMap* m, const void* base, int64_t cols, int64_t rows, int64_t ld, int box_rows) {
+  const int64_t dims[2] = {cols, rows}, strides[2] = {1, ld};
+  const int box[2] = {kDepth, box_rows};
+  return make_map(m, base, 2, dims, strides, box);
+}
+
+template <int MODE, int ACT>
+cudaError_t launch_tiles(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& b16,
+                         const MmaParams& q, int grid, cudaStream_t st) {
+  const size_t smem = 1024 + kStages * kStageBytes + sizeof(Barriers) + (size_t)q.p.s.G * 12;
+  // raises the kernel's shared-memory limit on its first use
+  (void)ctas_per_sm(product_kernel<MODE, ACT>, kThreads, 1024 + kStages * kStageBytes +
+                                                             sizeof(Barriers) + EP_MAX_EXPERTS * 12);
+  product_kernel<MODE, ACT><<<grid, kThreads, smem, st>>>(a, b, b16, q);
+  return cudaGetLastError();
+}
+
+int grid_of(int sms, int64_t tiles) {
+  const int64_t most = sms / 2, pairs = tiles < most ? tiles : most;
+  return (int)(2 * (pairs < 1 ? 1 : pairs));
+}
+
+// Upper bound of the row tiles of all groups (their counts are on the device).
+int64_t row_tiles(const LinearParams& p) {
+  if (!p.s.begin) return (p.s.dense_rows + kMaxRows - 1) / kMaxRows;
+  return p.s.pool / kMaxRows + p.s.G;
+}
+
+}  // namespace
+
+cudaError_t launch_linear_forward(const LinearParams& p, int sms, cudaStream_t st) {
+  const bool gated = p.act == EP_ACT_SWIGLU;
+  const int64_t rows = p.s.begin ? p.s.pool : p.s.dense_rows;
+  MmaParams q;
+  q.p = p;
+  q.features = p.Nw;
+  q.f_tiles = (p.Nw + 255) / 256;
+  q.r_tiles = 0;
+  CUtensorMap a, b, b16;
+  bool ok;
+  if (gated) {   // gate and up rows of a feature next to each other
+    const int64_t dims[4] = {p.K, 2, p.N, p.s.G};
+    const int64_t strides[4] = {1, (int64_t)p.N * p.K, p.K, (int64_t)p.Nw * p.K};
+    const int box[4] = {kDepth, 2, 64, 1};
+    ok = make_map(&a, p.w, 4, dims, strides, box);
+  } else {
+    const int64_t dims[3] = {p.K, p.Nw, p.s.G}, strides[3] = {1, p.K, (int64_t)p.Nw * p.K};
+    const int box[3] = {kDepth, 128, 1};
+    ok = make_map(&a, p.w, 3, dims, strides, box);
+  }
+  ok = ok && map_rows(&b, p.x, p.K, rows, p.K, 128) && map_rows(&b16, p.x, p.K, rows, p.K, 16);
+  if (!ok) return cudaErrorInvalidValue;
+  const int grid = grid_of(sms, row_tiles(p) * q.f_tiles);
+  switch (p.act) {
+    case EP_ACT_RELU: return launch_tiles<kForward, EP_ACT_RELU>(a, b, b16, q, grid, st);
+    case EP_ACT_SILU: return launch_tiles<kForward, EP_ACT_SILU>(a, b, b16, q, grid, st);
+    case EP_ACT_GELU: return launch_tiles<kForward, EP_ACT_GELU>(a, b, b16, q, grid, st);
+    case EP_ACT_SWIGLU: return launch_tiles<kForward, EP_ACT_SWIGLU>(a, b, b16, q, grid, st);
+    default: return launch_tiles<kForward, EP_ACT_NONE>(a, b, b16, q, grid, st);
+  }
+}
+
+cudaError_t launch_linear_input_grad(const LinearParams& p, int sms, cudaStream_t st) {
+  const int64_t rows = p.s.begin ? p.s.pool : p.s.dense_rows;
+  MmaParams q;
+  q.p = p;
+  q.features = p.K;
+  q.f_tiles = (p.K + 255) / 256;
+  q.r_tiles = 0;
+  CUtensorMap a, b, b16;
+  const int64_t dims[3] = {p.K, p.Nw, p.s.G}, strides[3] = {1, p.K, (int64_t)p.Nw * p.K};
+  const int box[3] = {64, kDepth, 1};
+  if (!make_map(&a, p.w, 3, dims, strides, box) ||
+      !map_rows(&b, p.dz, p.Nw, rows, p.ldz, 128) || !map_rows(&b16, p.dz, p.Nw, rows, p.ldz, 16))
+    return cudaErrorInvalidValue;
+  return launch_tiles<kInputGrad, EP_ACT_NONE>(a, b, b16, q, grid_of(sms, row_tiles(p) * q.f_tiles),
+                                               st);
+}
+
+cudaError_t launch_linear_weight_grad(const LinearParams& p, int sms, cudaStream_t st) {
+  const int64_t rows = p.s.begin ? p.s.pool : p.s.dense_rows;
+  MmaParams q;
+  q.p = p;
+  q.features = p.K;
+  q.f_tiles = (p.K + 255) / 256;
+  q.r_tiles = (p.Nw + kMaxRows - 1) / kMaxRows;
+  CUtensorMap a, b;
+  if (!map_rows(&a, p.x, p.K, rows, p.K, kDepth) || !map_rows(&b, p.dz, p.Nw, rows, p.ldz, kDepth))
+    return cudaErrorInvalidValue;
+  return launch_tiles<kWeightGrad, EP_ACT_NONE>(
+      a, b, b, q, grid_of(sms, (int64_t)p.s.G * q.f_tiles * q.r_tiles), st);
+}
+
+}  // namespace ep
