@@ -295,9 +295,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       for (int kb = 0; kb < w.blocks && ok; ++kb, ++it) {
         const int s = it % kStages;
         if (it >= kStages) {
-          ok = mbar_wait_cluster(&bar->empty[s], ((it / kStages) - 1) & 1);
+          ok = mbar_wait(&bar->empty[s], ((it / kStages) - 1) & 1);
           if (!ok) break;
-          if (cta == 0 && one) mbar_arrive_at(in_cta(&bar->empty[s], 1));
+          if (cta == 0 && one) mbar_signal_at(in_cta(&bar->empty[s], 1));
         }
         uint8_t* a = ring + s * kStageBytes;
         uint8_t* b = a + kStageA;
@@ -310,7 +310,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           if (tail) {
             mbar_arrive_expect_tx(&bar->landed, bytes);
           } else {
-            mbar_arrive_expect_tx_at(full, bytes);
+            mbar_signal_expect_tx_at(full, bytes);
           }
           if (MODE == kForward) {
             if (kGated) {
@@ -378,11 +378,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const uint32_t form = mma_form(w.n, MODE != kForward, MODE == kWeightGrad);
         for (int kb = 0; kb < w.blocks; ++kb, ++it) {
           const int s = it % kStages;
-          ok = mbar_wait_cluster(&bar->full[s], (it / kStages) & 1);
+          const int steps = (min(kDepth, w.terms - kb * kDepth) + 15) / 16;
+          // dW's last block holds rows that the producers cleared
+          ok = MODE == kWeightGrad && kb == w.blocks - 1
+                   ? mbar_wait_cluster(&bar->full[s], (it / kStages) & 1)
+                   : mbar_wait(&bar->full[s], (it / kStages) & 1);
           if (!ok) break;
           tc_fence_after();
           const uint32_t a = smem_addr(ring + s * kStageBytes), b = a + kStageA;
-          const int steps = (min(kDepth, w.terms - kb * kDepth) + 15) / 16;
           for (int i = 0; i < steps; ++i) {
             // 16 terms on: 32 bytes of a row (K-major) or 16 rows (MN-major)
             const uint64_t da = MODE == kForward ? smem_operand(a + i * 32, 16)
