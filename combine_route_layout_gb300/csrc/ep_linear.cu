@@ -11,80 +11,210 @@
 namespace ep {
 namespace {
 
-// dz = dy act'(z) and the sums of dz's columns over each block of rows. A CTA
-// takes kGradRows rows of one group and 256 weight rows' columns, a thread a
-// column; the block sums are added in block order by bias_grad_kernel. dz is
-// rounded to bf16 because the products read it as a tensor-core operand; the
-// sums are of the unrounded values.
+// dz = dy act'(z) and the sums of dz's columns over each block of rows: one
+// pass, bound by HBM. A CTA takes kGradRows rows of one group and 256 * VEC
+// columns, a thread VEC neighbouring columns, so that every row of a warp is
+// one contiguous access; the blocks' sums go to `part` and are added in block
+// order by bias_grad_kernel. dz is rounded to bf16 because the products read
+// it as a tensor-core operand; the sums are of the unrounded values.
 constexpr int kGradRows = 64;
+constexpr int kGradThreads = 128;
 
 struct GradParams {
   LinearParams p;
   __nv_bfloat16* dz;         // NULL: only the sums
   float* part;               // [row blocks][Nw] or NULL
+  int64_t row_blocks;        // rows of `part`
   float* db;                 // [G][Nw]
 };
 
-// Row blocks of the groups before each group.
-__device__ int64_t blocks_of(int64_t count) { return (count + kGradRows - 1) / kGradRows; }
+__device__ __forceinline__ int64_t blocks_of(int64_t count) {
+  return (count + kGradRows - 1) / kGradRows;
+}
 
-__global__ void __launch_bounds__(256) act_grad_kernel(GradParams q) {
-  const LinearParams& p = q.p;
-  const int c = blockIdx.x * 256 + threadIdx.x;
-  const bool gated = p.act == EP_ACT_SWIGLU;
-  int64_t seen = 0;
-  for (int g = 0; g < p.s.G; ++g) {
-    int64_t begin, count;
-    segment_of(p.s, g, begin, count);
-    const int64_t blocks = blocks_of(count);
-    for (int64_t b = ((int64_t)blockIdx.y - seen % gridDim.y + gridDim.y) % gridDim.y; b < blocks;
-         b += gridDim.y) {
-      if (c >= p.N) continue;
-      float s0 = 0.0f, s1 = 0.0f;
-      const int64_t end = min(count, (b + 1) * kGradRows);
-      for (int64_t r = b * kGradRows; r < end; ++r) {
-        const int64_t o = (begin + r) * p.N + c;
-        const float dy = p.y_f32 ? static_cast<const float*>(p.dy)[o]
-                                 : __bfloat162float(static_cast<const __nv_bfloat16*>(p.dy)[o]);
-        float d0 = dy, d1 = 0.0f;
-        if (gated) {
-          const float zg = __bfloat162float(p.z[(begin + r) * p.Nw + c]);
-          const float zu = __bfloat162float(p.z[(begin + r) * p.Nw + p.N + c]);
-          d0 = dy * zu * slope_of(EP_ACT_SILU, zg);
-          d1 = dy * silu_of(zg);
-        } else if (p.act != EP_ACT_NONE) {
-          d0 = dy * slope_of(p.act, __bfloat162float(p.z[(begin + r) * p.Nw + c]));
-        }
-        s0 += d0;
-        s1 += d1;
-        if (q.dz) {
-          q.dz[(begin + r) * p.ldz + c] = __float2bfloat16_rn(d0);
-          if (gated) q.dz[(begin + r) * p.ldz + p.N + c] = __float2bfloat16_rn(d1);
-        }
-      }
-      if (q.part) {
-        q.part[(seen + b) * p.Nw + c] = s0;
-        if (gated) q.part[(seen + b) * p.Nw + p.N + c] = s1;
-      }
+// VEC columns from an aligned place, as f32.
+template <int VEC, typename T>
+__device__ __forceinline__ void load_columns(const T* at, float (&v)[VEC]) {
+  if (VEC == 8 && sizeof(T) == 2) {
+    const uint4 q = ld_nc_v4(at);
+    const uint32_t u[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) v[i] = (i & 1) ? bf16_hi(u[i / 2]) : bf16_lo(u[i / 2]);
+  } else if (VEC == 8) {
+#pragma unroll
+    for (int h = 0; h < VEC / 4; ++h) {
+      const uint4 q = ld_nc_v4(at + h * 4);
+      v[(h * 4) % VEC] = __uint_as_float(q.x);
+      v[(h * 4 + 1) % VEC] = __uint_as_float(q.y);
+      v[(h * 4 + 2) % VEC] = __uint_as_float(q.z);
+      v[(h * 4 + 3) % VEC] = __uint_as_float(q.w);
     }
-    seen += blocks;
+  } else {
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) v[i] = (float)at[i];
   }
 }
 
+template <int VEC>
+__device__ __forceinline__ void store_dz(__nv_bfloat16* at, const float (&v)[VEC]) {
+  if (VEC == 8) {
+    st_v4(at, make_uint4(cvt_bf16x2(v[0], v[1 % VEC]), cvt_bf16x2(v[2 % VEC], v[3 % VEC]),
+                         cvt_bf16x2(v[4 % VEC], v[5 % VEC]), cvt_bf16x2(v[6 % VEC], v[7 % VEC])));
+  } else {
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) at[i] = __float2bfloat16_rn(v[i]);
+  }
+}
+
+// A group's block of rows, number `b` over all groups; false past the last.
+struct BlockPlace {
+  int64_t begin, row0, row1;
+};
+
+template <int VEC, int ACT, typename T>
+__global__ void __launch_bounds__(kGradThreads) act_grad_kernel(GradParams q) {
+  const LinearParams& p = q.p;
+  __shared__ BlockPlace at;
+  const bool gated = ACT == EP_ACT_SWIGLU;
+  const int64_t block = blockIdx.x;
+  // the group of this block: a warp adds up the groups' blocks, 32 at a time
+  if (threadIdx.x < 32) {
+    const int lane = threadIdx.x;
+    int64_t before = 0;
+    if (lane == 0) at.row0 = at.row1 = at.begin = 0;
+    for (int g0 = 0; g0 < p.s.G && before <= block; g0 += 32) {
+      int64_t begin = 0, count = 0;
+      if (g0 + lane < p.s.G) segment_of(p.s, g0 + lane, begin, count);
+      int64_t incl = blocks_of(count);
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t v = __shfl_up_sync(kFull, incl, o);
+        if (lane >= o) incl += v;
+      }
+      const int64_t mine = before + incl - blocks_of(count);
+      if (block >= mine && block < before + incl) {
+        at.begin = begin;
+        at.row0 = (block - mine) * kGradRows;
+        at.row1 = min(count, at.row0 + kGradRows);
+      }
+      before += __shfl_sync(kFull, incl, 31);
+    }
+    // segments that do not overlap leave the last block free
+    if (p.s.begin && lane == 0 && block == q.row_blocks - 1 && before > block)
+      atomicOr(p.s.err, kErrSegment);
+  }
+  __syncthreads();
+  const int c = (blockIdx.y * kGradThreads + threadIdx.x) * VEC;
+  if (at.row0 >= at.row1 || c >= p.N) return;
+  float s0[VEC], s1[VEC];
+#pragma unroll
+  for (int i = 0; i < VEC; ++i) s0[i] = s1[i] = 0.0f;
+  const T* dy = static_cast<const T*>(p.dy) + (at.begin + at.row0) * p.N + c;
+  const __nv_bfloat16* z = p.z + (at.begin + at.row0) * p.Nw + c;
+  __nv_bfloat16* out = q.dz + (at.begin + at.row0) * p.ldz + c;
+#pragma unroll 4
+  for (int64_t r = at.row0; r < at.row1; ++r) {
+    float d0[VEC], d1[VEC];
+    load_columns<VEC, T>(dy, d0);
+    if (gated) {
+      float zg[VEC], zu[VEC];
+      load_columns<VEC, __nv_bfloat16>(z, zg);
+      load_columns<VEC, __nv_bfloat16>(z + p.N, zu);
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) {
+        // silu'(g) = s (1 + g (1 - s)), silu(g) = g s
+        const float s = sigmoid_of(zg[i]);
+        d1[i] = d0[i] * (zg[i] * s);
+        d0[i] *= zu[i] * (s * (1.0f + zg[i] * (1.0f - s)));
+      }
+    } else if (ACT != EP_ACT_NONE) {
+      float zv[VEC];
+      load_columns<VEC, __nv_bfloat16>(z, zv);
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) d0[i] *= slope_of(ACT, zv[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) {
+      s0[i] += d0[i];
+      if (gated) s1[i] += d1[i];
+    }
+    if (q.dz) {
+      store_dz<VEC>(out, d0);
+      if (gated) store_dz<VEC>(out + p.N, d1);
+    }
+    dy += p.N;
+    z += p.Nw;
+    out += p.ldz;
+  }
+  if (q.part) {
+    float* part = q.part + block * p.Nw + c;
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) {
+      part[i] = s0[i];
+      if (gated) part[p.N + i] = s1[i];
+    }
+  }
+}
+
+// db_g: the sums of the group's blocks, in block order. A CTA takes 32
+// columns, a warp every 8th block.
 __global__ void __launch_bounds__(256) bias_grad_kernel(GradParams q) {
   const LinearParams& p = q.p;
-  const int c = blockIdx.x * 256 + threadIdx.x;
+  __shared__ float sum[8][32];
+  __shared__ int64_t range[2];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int c = blockIdx.x * 32 + lane;
   const int g = blockIdx.y;
-  int64_t first = 0, begin, count;
-  for (int i = 0; i < g; ++i) {
-    segment_of(p.s, i, begin, count);
-    first += blocks_of(count);
+  if (warp == 0) {
+    int64_t before = 0, begin, count = 0;
+    for (int i = lane; i < g; i += 32) {
+      segment_of(p.s, i, begin, count);
+      before += blocks_of(count);
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) before += __shfl_xor_sync(kFull, before, o);
+    segment_of(p.s, g, begin, count);
+    if (lane == 0) {
+      range[0] = min(before, q.row_blocks);
+      range[1] = min(before + blocks_of(count), q.row_blocks);
+    }
   }
-  segment_of(p.s, g, begin, count);
-  if (c >= p.Nw) return;
+  __syncthreads();
   float s = 0.0f;
-  for (int64_t b = 0; b < blocks_of(count); ++b) s += q.part[(first + b) * p.Nw + c];
-  q.db[(int64_t)g * p.Nw + c] = s;
+  if (c < p.Nw)
+    for (int64_t b = range[0] + warp; b < range[1]; b += 8) s += __ldg(q.part + b * p.Nw + c);
+  sum[warp][lane] = s;
+  __syncthreads();
+  if (warp == 0 && c < p.Nw) {
+    s = 0.0f;
+#pragma unroll
+    for (int w = 0; w < 8; ++w) s += sum[w][lane];
+    q.db[(int64_t)g * p.Nw + c] = s;
+  }
+}
+
+template <int VEC, typename T>
+cudaError_t grad_typed(const GradParams& q, cudaStream_t st) {
+  const dim3 grid((unsigned)q.row_blocks,
+                  (q.p.N + kGradThreads * VEC - 1) / (kGradThreads * VEC));
+  switch (q.p.act) {
+    case EP_ACT_RELU: act_grad_kernel<VEC, EP_ACT_RELU, T><<<grid, kGradThreads, 0, st>>>(q); break;
+    case EP_ACT_SILU: act_grad_kernel<VEC, EP_ACT_SILU, T><<<grid, kGradThreads, 0, st>>>(q); break;
+    case EP_ACT_GELU: act_grad_kernel<VEC, EP_ACT_GELU, T><<<grid, kGradThreads, 0, st>>>(q); break;
+    case EP_ACT_SWIGLU:
+      act_grad_kernel<VEC, EP_ACT_SWIGLU, T><<<grid, kGradThreads, 0, st>>>(q);
+      break;
+    default: act_grad_kernel<VEC, EP_ACT_NONE, T><<<grid, kGradThreads, 0, st>>>(q);
+  }
+  return cudaGetLastError();
+}
+
+cudaError_t launch_act_grad(const GradParams& q, cudaStream_t st) {
+  const LinearParams& p = q.p;
+  // 16-byte accesses need rows and tensors on 16-byte boundaries
+  const bool vec = p.N % 8 == 0 && (uintptr_t)p.dy % 16 == 0 && (uintptr_t)p.z % 16 == 0;
+  if (p.y_f32) return vec ? grad_typed<8, float>(q, st) : grad_typed<1, float>(q, st);
+  return vec ? grad_typed<8, __nv_bfloat16>(q, st) : grad_typed<1, __nv_bfloat16>(q, st);
 }
 
 }  // namespace
@@ -119,8 +249,8 @@ ep_status plan_linear(const ep_linear_config* c, ep_linear_handle* h) {
     return lfail(EP_ERR_INVALID_ARG, "groups_per_base must be >= 0");
   if (c->in_features < 8 || c->in_features % 8 != 0)
     return lfail(EP_ERR_INVALID_ARG, "in_features must be a positive multiple of 8");
-  if (c->out_features < 1 || c->out_features > (1 << 24) || c->in_features > (1 << 24))
-    return lfail(EP_ERR_INVALID_ARG, "in_features and out_features must be in [1, 2^24]");
+  if (c->out_features < 1 || c->out_features > (1 << 22) || c->in_features > (1 << 22))
+    return lfail(EP_ERR_INVALID_ARG, "in_features and out_features must be in [1, 2^22]");
   if (c->max_rows < 1 || c->max_rows > INT32_MAX - 1024)
     return lfail(EP_ERR_INVALID_ARG, "max_rows must be >= 1 and fit int32");
   if (c->out_dtype != EP_DTYPE_BF16 && c->out_dtype != EP_DTYPE_FP32)
@@ -137,7 +267,7 @@ ep_status plan_linear(const ep_linear_config* c, ep_linear_handle* h) {
     return lfail(EP_ERR_INVALID_ARG, "max_rows, num_groups and features give too many tiles");
   h->cfg = *c;
   h->Nw = c->activation == EP_ACT_SWIGLU ? 2 * c->out_features : c->out_features;
-  h->ldz = (h->Nw + 7) / 8 * 8;
+  h->ldz = (h->Nw + 63) / 64 * 64;   // whole 64-element blocks
   h->row_blocks = (c->max_rows + kGradRows - 1) / kGradRows + c->num_groups;
   size_t off = 256;
   h->err = reinterpret_cast<int32_t*>(h->ws);
@@ -287,21 +417,24 @@ extern "C" ep_status ep_linear_backward(ep_linear_handle* h, const void* dy, con
   p.dw = dweight;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   if ((s = linear_ready(h, st)) != EP_OK) return s;
+  // without an activation dz is dy: the products read it in place where its
+  // rows are whole 16-byte pieces
+  const bool in_place = p.act == EP_ACT_NONE && !p.y_f32 && p.N % 8 == 0 && (uintptr_t)dy % 16 == 0;
   GradParams q;
   memset(&q, 0, sizeof(q));
   q.p = p;
-  q.dz = dx || dweight ? h->dz : nullptr;
+  q.dz = (dx || dweight) && !in_place ? h->dz : nullptr;
   q.part = dbias ? h->part : nullptr;
+  q.row_blocks = p.s.begin ? h->row_blocks : (num_rows + kGradRows - 1) / kGradRows;
   q.db = dbias;
-  int64_t rows = h->row_blocks < 4096 ? h->row_blocks : 4096;
-  act_grad_kernel<<<dim3((p.N + 255) / 256, (unsigned)rows), 256, 0, st>>>(q);
-  cudaError_t e = cudaGetLastError();
-  if (e == cudaSuccess && dbias) {
-    bias_grad_kernel<<<dim3((p.Nw + 255) / 256, p.s.G), 256, 0, st>>>(q);
-    e = cudaGetLastError();
+  if ((q.dz || q.part) && q.row_blocks > 0 && (s = status_of(launch_act_grad(q, st))) != EP_OK)
+    return s;
+  if (dbias) {
+    bias_grad_kernel<<<dim3((p.Nw + 31) / 32, p.s.G), 256, 0, st>>>(q);
+    if ((s = status_of(cudaGetLastError())) != EP_OK) return s;
   }
-  if (e != cudaSuccess) return lcuda(e);
-  p.dz = h->dz;
+  p.dz = in_place ? static_cast<const __nv_bfloat16*>(dy) : h->dz;
+  if (in_place) p.ldz = p.N;
   if (dx && (s = status_of(launch_linear_input_grad(p, h->sm_count, st))) != EP_OK) return s;
   return dweight ? status_of(launch_linear_weight_grad(p, h->sm_count, st)) : EP_OK;
 }
@@ -320,6 +453,7 @@ extern "C" ep_status ep_linear_sync(ep_linear_handle* h, void* stream) {
   if (bits & kErrLinearTimeout)
     return lfail(EP_ERR_TIMEOUT, "a product's bounded wait gave up; its output is not complete");
   if (bits & kErrSegment)
-    return lfail(EP_ERR_INVALID_INDEX, "a segment reached outside the row pool and was cut");
+    return lfail(EP_ERR_INVALID_INDEX,
+                 "a segment reached outside the row pool and was cut, or a backward pass's overlapped");
   return EP_OK;
 }

@@ -78,7 +78,13 @@ __device__ __forceinline__ void segment_of(const LinearSegs& s, int g, int64_t& 
   }
 }
 
-__device__ __forceinline__ float silu_of(float v) { return v / (1.0f + __expf(-v)); }
+// 1 / (1 + exp(-v)) to about 2^-21: results are rounded to bf16 or stand next
+// to sums of f32 products. exp(-v) overflows to inf below -88: the quotient is 0.
+__device__ __forceinline__ float sigmoid_of(float v) {
+  return __fdividef(1.0f, 1.0f + __expf(-v));
+}
+
+__device__ __forceinline__ float silu_of(float v) { return v * sigmoid_of(v); }
 
 __device__ __forceinline__ float act_of(int act, float v) {
   switch (act) {
@@ -93,7 +99,7 @@ __device__ __forceinline__ float slope_of(int act, float v) {
   switch (act) {
     case EP_ACT_RELU: return v > 0.0f ? 1.0f : 0.0f;
     case EP_ACT_SILU: {
-      const float s = 1.0f / (1.0f + __expf(-v));
+      const float s = sigmoid_of(v);
       return s * (1.0f + v * (1.0f - s));
     }
     case EP_ACT_GELU:

@@ -44,6 +44,8 @@ struct MmaParams {
   int features;      // length of the output's contiguous axis (weight rows or K)
   int f_tiles;       // 256-feature tiles
   int r_tiles;       // dW: 256-row tiles of each group (else by the group's count)
+  int a_blocks;      // MN-major operands: the map cuts rows into blocks of 64
+  int b_blocks;      // elements, so that one box takes two of them
 };
 
 struct Barriers {
@@ -237,13 +239,18 @@ __device__ __forceinline__ void store_columns(const MmaParams& q, const Tile& w,
   }
 }
 
-// map_a: features; map_b: rows (box of 128 rows; dW: of 64 rows x 64 columns);
-// map_b16: the same in boxes of 16 rows, for tiles of fewer rows.
+// Maps of the two operands. A K-major operand's rows come in boxes of 128, 64,
+// 32 or 16 rows, the smallest that holds a CTA's half of the tile: one TMA
+// instruction each (with boxes of 16 rows alone, seven for 112 rows, ragged
+// experts' products took 3.82 ms where full tiles take 3.1).
+struct Maps {
+  CUtensorMap a;
+  CUtensorMap b[4];
+};
+
 template <int MODE, int ACT>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
-    product_kernel(const __grid_constant__ CUtensorMap map_a,
-                   const __grid_constant__ CUtensorMap map_b,
-                   const __grid_constant__ CUtensorMap map_b16, MmaParams q) {
+    product_kernel(const __grid_constant__ Maps maps, MmaParams q) {
   constexpr bool kGated = MODE == kForward && ACT == EP_ACT_SWIGLU;
   extern __shared__ uint8_t raw[];
   uint8_t* ring = reinterpret_cast<uint8_t*>(((uintptr_t)raw + 1023) & ~(uintptr_t)1023);
@@ -266,9 +273,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       mbar_init(&bar->acc_empty[a], 8);  // four epilogue warps of each CTA
     }
     mbar_init_fence();
-    tma_prefetch_map(&map_a);
-    tma_prefetch_map(&map_b);
-    if (MODE != kWeightGrad) tma_prefetch_map(&map_b16);
+    tma_prefetch_map(&maps.a);
+    tma_prefetch_map(&maps.b[0]);
   }
   if (warp == 1) tmem_alloc(&bar->tmem, kTmemColumns);
   const int tiles = plan_tiles<MODE>(q, first, begins, counts);
@@ -289,9 +295,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const int half = w.n / 2;
       const int fc = w.f0 + (int)cta * 128;                     // this CTA's features
       const int rc = w.r0 + (int)cta * half;                    // this CTA's rows
-      const int boxes = MODE == kWeightGrad ? half / 64 : half / 16;
-      const bool whole = half == 128;
-      const uint32_t bytes = kStageA + (MODE == kWeightGrad ? half / 64 * 8192 : half * 128);
+      const int box = MODE == kWeightGrad ? 0 : half > 64 ? 0 : half > 32 ? 1 : half > 16 ? 2 : 3;
+      const uint32_t bytes = kStageA + (kStageB >> box);
+      const CUtensorMap* map_b = &maps.b[box];
       for (int kb = 0; kb < w.blocks && ok; ++kb, ++it) {
         const int s = it % kStages;
         if (it >= kStages) {
@@ -312,27 +318,33 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           } else {
             mbar_signal_expect_tx_at(full, bytes);
           }
+          const int row = (int)w.begin + d;                     // dW: contraction row
           if (MODE == kForward) {
             if (kGated) {
-              tma_load_4d(a, &map_a, d, 0, fc / 2, w.g, on);
+              tma_load_4d(a, &maps.a, d, 0, fc / 2, w.g, on);
             } else {
-              tma_load_3d(a, &map_a, d, fc, w.g, on);
+              tma_load_3d(a, &maps.a, d, fc, w.g, on);
             }
           } else if (MODE == kInputGrad) {
-            tma_load_3d(a, &map_a, fc, d, w.g, on);
-            tma_load_3d(a + 8192, &map_a, fc + 64, d, w.g, on);
+            if (q.a_blocks) {
+              tma_load_4d(a, &maps.a, 0, d, fc / 64, w.g, on);
+            } else {
+              tma_load_3d(a, &maps.a, fc, d, w.g, on);
+              tma_load_3d(a + 8192, &maps.a, fc + 64, d, w.g, on);
+            }
+          } else if (q.a_blocks) {
+            tma_load_3d(a, &maps.a, 0, row, fc / 64, on);
           } else {
-            tma_load_2d(a, &map_a, fc, (int)w.begin + d, on);
-            tma_load_2d(a + 8192, &map_a, fc + 64, (int)w.begin + d, on);
+            tma_load_2d(a, &maps.a, fc, row, on);
+            tma_load_2d(a + 8192, &maps.a, fc + 64, row, on);
           }
-          if (MODE == kWeightGrad) {
-            for (int i = 0; i < boxes; ++i)
-              tma_load_2d(b + i * 8192, &map_b, rc + i * 64, (int)w.begin + d, on);
-          } else if (whole) {
-            tma_load_2d(b, &map_b, d, (int)w.begin + rc, on);
+          if (MODE != kWeightGrad) {
+            tma_load_2d(b, map_b, d, (int)w.begin + rc, on);
+          } else if (q.b_blocks) {
+            tma_load_3d(b, map_b, 0, row, rc / 64, on);
           } else {
-            for (int i = 0; i < boxes; ++i)
-              tma_load_2d(b + i * 2048, &map_b16, d, (int)w.begin + rc + i * 16, on);
+            tma_load_2d(b, map_b, rc, row, on);
+            tma_load_2d(b + 8192, map_b, rc + 64, row, on);
           }
         }
         if (tail) {
@@ -341,11 +353,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           ok = mbar_wait(&bar->landed, landed_phase);
           landed_phase ^= 1;
           const int end = (valid + 15) / 16 * 16;
-          const int n16 = (2 + boxes) * (end - valid) * 8;      // 16-byte pieces
+          const int n16 = 4 * (end - valid) * 8;                // 16-byte pieces
           for (int i = lane; i < n16; i += 32) {
             const int row = valid + i / 8 % (end - valid);
-            const int box = i / 8 / (end - valid);
-            uint8_t* at = (box < 2 ? a + box * 8192 : b + (box - 2) * 8192) + row * 128;
+            const int part = i / 8 / (end - valid);             // 64 columns of a or b
+            uint8_t* at = a + part * 8192 + row * 128;
             reinterpret_cast<uint4*>(at)[i & 7] = make_uint4(0, 0, 0, 0);
           }
           fence_async_shared();
@@ -365,9 +377,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     if (cta == 0 && lane == 0) {
       int it = 0, n_acc = 0;
       bool ok = true;
+      Tile next;
+      if (pair < tiles) next = tile_at<MODE>(q, first, begins, counts, pair);
       for (int t = pair; t < tiles && ok; t += pairs) {
-        const Tile w = tile_at<MODE>(q, first, begins, counts, t);
-        if (w.blocks == 0) continue;
+        const Tile w = next;
+        if (w.blocks == 0) {
+          if (t + pairs < tiles) next = tile_at<MODE>(q, first, begins, counts, t + pairs);
+          continue;
+        }
         const int acc = n_acc & 1;
         if (n_acc >= 2) {
           ok = mbar_wait_cluster(&bar->acc_empty[acc], ((n_acc >> 1) - 1) & 1);
@@ -395,6 +412,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             mma_pair(d, da, db, form, kb > 0 || i > 0);
           }
           mma_commit(&bar->empty[s]);
+          // the next tile is worked out under this one's products
+          if (kb == 0 && t + pairs < tiles)
+            next = tile_at<MODE>(q, first, begins, counts, t + pairs);
         }
         if (!ok) break;
         mma_commit(&bar->acc_full[acc]);
@@ -494,14 +514,36 @@ bool map_rows(CUtensorMap* m, const void* base, int64_t cols, int64_t rows, int6
   return make_map(m, base, 2, dims, strides, box);
 }
 
+// Rows of a K-major operand, in boxes of 128, 64, 32 and 16 rows.
+bool map_k_major(CUtensorMap (&m)[4], const void* base, int64_t cols, int64_t rows, int64_t ld) {
+  bool ok = true;
+  for (int i = 0; i < 4; ++i) ok = ok && map_rows(&m[i], base, cols, rows, ld, 128 >> i);
+  return ok;
+}
+
+// An MN-major operand of `groups` matrices [rows][cols]: a stage's 64 rows by
+// 128 columns, as two 64-column parts. Where rows are whole blocks of 64
+// elements (`blocks`), one box takes both parts.
+bool map_mn_major(CUtensorMap* m, const void* base, int64_t cols, int64_t rows, int64_t ld,
+                  int groups, int blocks) {
+  if (blocks) {
+    const int64_t dims[4] = {64, rows, (cols + 63) / 64, groups};
+    const int64_t strides[4] = {1, ld, 64, rows * ld};
+    const int box[4] = {64, kDepth, 2, 1};
+    return make_map(m, base, groups ? 4 : 3, dims, strides, box);
+  }
+  const int64_t dims[3] = {cols, rows, groups}, strides[3] = {1, ld, rows * ld};
+  const int box[3] = {64, kDepth, 1};
+  return make_map(m, base, groups ? 3 : 2, dims, strides, box);
+}
+
 template <int MODE, int ACT>
-cudaError_t launch_tiles(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& b16,
-                         const MmaParams& q, int grid, cudaStream_t st) {
+cudaError_t launch_tiles(const Maps& maps, const MmaParams& q, int grid, cudaStream_t st) {
   const size_t smem = 1024 + kStages * kStageBytes + sizeof(Barriers) + (size_t)q.p.s.G * 12;
   // raises the kernel's shared-memory limit on its first use
   (void)ctas_per_sm(product_kernel<MODE, ACT>, kThreads, 1024 + kStages * kStageBytes +
                                                              sizeof(Barriers) + EP_MAX_EXPERTS * 12);
-  product_kernel<MODE, ACT><<<grid, kThreads, smem, st>>>(a, b, b16, q);
+  product_kernel<MODE, ACT><<<grid, kThreads, smem, st>>>(maps, q);
   return cudaGetLastError();
 }
 
@@ -526,27 +568,27 @@ cudaError_t launch_linear_forward(const LinearParams& p, int sms, cudaStream_t s
   q.features = p.Nw;
   q.f_tiles = (p.Nw + 255) / 256;
   q.r_tiles = 0;
-  CUtensorMap a, b, b16;
+  Maps m;
   bool ok;
   if (gated) {   // gate and up rows of a feature next to each other
     const int64_t dims[4] = {p.K, 2, p.N, p.s.G};
     const int64_t strides[4] = {1, (int64_t)p.N * p.K, p.K, (int64_t)p.Nw * p.K};
     const int box[4] = {kDepth, 2, 64, 1};
-    ok = make_map(&a, p.w, 4, dims, strides, box);
+    ok = make_map(&m.a, p.w, 4, dims, strides, box);
   } else {
     const int64_t dims[3] = {p.K, p.Nw, p.s.G}, strides[3] = {1, p.K, (int64_t)p.Nw * p.K};
     const int box[3] = {kDepth, 128, 1};
-    ok = make_map(&a, p.w, 3, dims, strides, box);
+    ok = make_map(&m.a, p.w, 3, dims, strides, box);
   }
-  ok = ok && map_rows(&b, p.x, p.K, rows, p.K, 128) && map_rows(&b16, p.x, p.K, rows, p.K, 16);
-  if (!ok) return cudaErrorInvalidValue;
+  if (!ok || !map_k_major(m.b, p.x, p.K, rows, p.K)) return cudaErrorInvalidValue;
+  q.a_blocks = q.b_blocks = 0;
   const int grid = grid_of(sms, row_tiles(p) * q.f_tiles);
   switch (p.act) {
-    case EP_ACT_RELU: return launch_tiles<kForward, EP_ACT_RELU>(a, b, b16, q, grid, st);
-    case EP_ACT_SILU: return launch_tiles<kForward, EP_ACT_SILU>(a, b, b16, q, grid, st);
-    case EP_ACT_GELU: return launch_tiles<kForward, EP_ACT_GELU>(a, b, b16, q, grid, st);
-    case EP_ACT_SWIGLU: return launch_tiles<kForward, EP_ACT_SWIGLU>(a, b, b16, q, grid, st);
-    default: return launch_tiles<kForward, EP_ACT_NONE>(a, b, b16, q, grid, st);
+    case EP_ACT_RELU: return launch_tiles<kForward, EP_ACT_RELU>(m, q, grid, st);
+    case EP_ACT_SILU: return launch_tiles<kForward, EP_ACT_SILU>(m, q, grid, st);
+    case EP_ACT_GELU: return launch_tiles<kForward, EP_ACT_GELU>(m, q, grid, st);
+    case EP_ACT_SWIGLU: return launch_tiles<kForward, EP_ACT_SWIGLU>(m, q, grid, st);
+    default: return launch_tiles<kForward, EP_ACT_NONE>(m, q, grid, st);
   }
 }
 
@@ -557,14 +599,13 @@ cudaError_t launch_linear_input_grad(const LinearParams& p, int sms, cudaStream_
   q.features = p.K;
   q.f_tiles = (p.K + 255) / 256;
   q.r_tiles = 0;
-  CUtensorMap a, b, b16;
-  const int64_t dims[3] = {p.K, p.Nw, p.s.G}, strides[3] = {1, p.K, (int64_t)p.Nw * p.K};
-  const int box[3] = {64, kDepth, 1};
-  if (!make_map(&a, p.w, 3, dims, strides, box) ||
-      !map_rows(&b, p.dz, p.Nw, rows, p.ldz, 128) || !map_rows(&b16, p.dz, p.Nw, rows, p.ldz, 16))
+  q.a_blocks = p.K % 64 == 0;
+  q.b_blocks = 0;
+  Maps m;
+  if (!map_mn_major(&m.a, p.w, p.K, p.Nw, p.K, p.s.G, q.a_blocks) ||
+      !map_k_major(m.b, p.dz, p.Nw, rows, p.ldz))
     return cudaErrorInvalidValue;
-  return launch_tiles<kInputGrad, EP_ACT_NONE>(a, b, b16, q, grid_of(sms, row_tiles(p) * q.f_tiles),
-                                               st);
+  return launch_tiles<kInputGrad, EP_ACT_NONE>(m, q, grid_of(sms, row_tiles(p) * q.f_tiles), st);
 }
 
 cudaError_t launch_linear_weight_grad(const LinearParams& p, int sms, cudaStream_t st) {
@@ -574,11 +615,15 @@ cudaError_t launch_linear_weight_grad(const LinearParams& p, int sms, cudaStream
   q.features = p.K;
   q.f_tiles = (p.K + 255) / 256;
   q.r_tiles = (p.Nw + kMaxRows - 1) / kMaxRows;
-  CUtensorMap a, b;
-  if (!map_rows(&a, p.x, p.K, rows, p.K, kDepth) || !map_rows(&b, p.dz, p.Nw, rows, p.ldz, kDepth))
+  q.a_blocks = p.K % 64 == 0;
+  q.b_blocks = p.ldz % 64 == 0;   // columns past Nw give rows of dW that are not stored
+  Maps m;
+  if (!map_mn_major(&m.a, p.x, p.K, rows, p.K, 0, q.a_blocks) ||
+      !map_mn_major(&m.b[0], p.dz, p.Nw, rows, p.ldz, 0, q.b_blocks))
     return cudaErrorInvalidValue;
+  for (int i = 1; i < 4; ++i) m.b[i] = m.b[0];
   return launch_tiles<kWeightGrad, EP_ACT_NONE>(
-      a, b, b, q, grid_of(sms, (int64_t)p.s.G * q.f_tiles * q.r_tiles), st);
+      m, q, grid_of(sms, (int64_t)p.s.G * q.f_tiles * q.r_tiles), st);
 }
 
 }  // namespace ep

@@ -670,6 +670,7 @@ ep_status ep_linear_forward(ep_linear_handle* h, const void* x, const void* weig
                             void* y, void* preact, void* stream);
 
 /*
+ * Segments must not overlap here (forward's may).
  *   dy       device [max_rows][N] out_dtype
  *   preact   device [max_rows][Nw] bf16 as forward wrote it (may be NULL
  *            without an activation)
