@@ -17,7 +17,8 @@
 // under the next one's products) stay in TMEM. Grid: one CTA per SM, each pair
 // walks the tiles of all groups.
 //
-// Roles by warp: 0 TMA, 1 MMA, 4-7 epilogue (TMEM lanes go by warp % 4).
+// Roles by warp: 0 TMA, 1 MMA, 4-11 epilogue (TMEM lanes go by warp % 4; the
+// two warps of a quarter take every other 32 columns).
 #include <cuda.h>
 
 #include <cstring>
@@ -34,13 +35,16 @@ constexpr int kStageA = 128 * kDepth * 2;        // bytes of a CTA's 128 feature
 constexpr int kStageB = 128 * kDepth * 2;        // bytes of a CTA's half of the rows
 constexpr int kStageBytes = kStageA + kStageB;
 constexpr int kMaxRows = 256;                    // rows of a tile
-constexpr int kThreads = 256;
+constexpr int kEpilogueWarps = 8;                // two to each quarter of the TMEM lanes
+constexpr int kThreads = (4 + kEpilogueWarps) * 32;
 constexpr int kTmemColumns = 512;                // two accumulators
 
 enum Mode { kForward = 0, kInputGrad = 1, kWeightGrad = 2 };
 
 struct MmaParams {
   LinearParams p;
+  void* out;         // y, dx or dW
+  int out_f32;
   int features;      // length of the output's contiguous axis (weight rows or K)
   int f_tiles;       // 256-feature tiles
   int r_tiles;       // dW: 256-row tiles of each group (else by the group's count)
@@ -163,79 +167,96 @@ __device__ int plan_tiles(const MmaParams& q, int* first, int* begins, int* coun
   return total;
 }
 
-// One value of the forward's epilogue.
-template <int ACT>
-__device__ __forceinline__ float activate(float v) {
-  return act_of(ACT, v);
-}
+__device__ __forceinline__ void put(float* at, float v) { *at = v; }
+__device__ __forceinline__ void put(__nv_bfloat16* at, float v) { *at = __float2bfloat16_rn(v); }
+__device__ __forceinline__ float get(const float* at) { return *at; }
+__device__ __forceinline__ float get(const __nv_bfloat16* at) { return __bfloat162float(*at); }
 
-template <int MODE, int ACT>
+// The epilogue of 32 columns (rows of the output) of a warp's 32 lanes
+// (features), T the output's type. FULL: all 32 exist, so that the columns are
+// independent of one another and the loads of the residual come first.
+template <int MODE, int ACT, bool FULL, typename T>
 __device__ __forceinline__ void store_columns(const MmaParams& q, const Tile& w, int cta, int lane,
                                               int quad, int c0, const uint32_t (&r)[32], float b) {
   const LinearParams& p = q.p;
   const int f = quad * 32 + lane;          // lane of the accumulator
   const int left = w.rows - c0;            // columns that exist
+  const int64_t row0 = (MODE == kWeightGrad ? (int64_t)w.g * p.Nw : w.begin) + w.r0 + c0;
   if (MODE == kForward && ACT == EP_ACT_SWIGLU) {
     // even lanes hold a feature's gate, odd lanes its up value; a pair of
     // lanes exchanges two columns so that each finishes one of them
     const int out = w.f0 / 2 + cta * 64 + f / 2;
+    const int odd = lane & 1;
     const bool in = out < p.N;
-    const bool odd = lane & 1;
+    const int64_t row = row0 + odd;
+    T* y = static_cast<T*>(p.y) + row * p.N + out;
+    const T* res = static_cast<const T*>(p.residual) + row * p.N + out;
+    __nv_bfloat16* z = p.z + row * p.Nw + out;
+    float add[16];
 #pragma unroll
-    for (int c = 0; c < 32; c += 2) {
-      if (c >= left) break;
-      const float v0 = __uint_as_float(r[c]) + b, v1 = __uint_as_float(r[c + 1]) + b;
-      const int64_t row = w.begin + w.r0 + c0 + c;
-      if (p.z && in) {
-        const int64_t o = row * p.Nw + (odd ? p.N : 0) + out;
-        p.z[o] = __float2bfloat16_rn(v0);
-        if (c + 1 < left) p.z[o + p.Nw] = __float2bfloat16_rn(v1);
-      }
+    for (int i = 0; i < 16; ++i)
+      add[i] = p.residual && in && (FULL || 2 * i + odd < left) ? get(res + (int64_t)(2 * i) * p.N) : 0.0f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const float v0 = __uint_as_float(r[2 * i]) + b, v1 = __uint_as_float(r[2 * i + 1]) + b;
       const float other = __shfl_xor_sync(kFull, odd ? v0 : v1, 1);
-      float y = odd ? silu_of(other) * v1 : silu_of(v0) * other;
-      if (!in || (odd && c + 1 >= left)) continue;
-      const int64_t o = (row + odd) * p.N + out;
-      if (p.y_f32) {
-        if (p.residual) y += static_cast<const float*>(p.residual)[o];
-        static_cast<float*>(p.y)[o] = y;
-      } else {
-        if (p.residual) y += __bfloat162float(static_cast<const __nv_bfloat16*>(p.residual)[o]);
-        static_cast<__nv_bfloat16*>(p.y)[o] = __float2bfloat16_rn(y);
+      const float gate = odd ? other : v0, up = odd ? v1 : other;
+      if (in && (FULL || 2 * i + odd < left)) {
+        put(y, silu_of(gate) * up + add[i]);
+        if (p.z) {
+          put(z, gate);
+          put(z + p.N, up);
+        }
       }
+      y += 2 * (int64_t)p.N;
+      z += 2 * (int64_t)p.Nw;
     }
     return;
   }
   const int feature = w.f0 + cta * 128 + f;
   if (feature >= q.features) return;
+  const int64_t ld = q.features;           // the output's rows are its features
+  T* y = static_cast<T*>(q.out) + row0 * ld + feature;
+  if (MODE != kForward) {
+#pragma unroll
+    for (int c = 0; c < 32; ++c) {
+      if (FULL || c < left) put(y, __uint_as_float(r[c]));
+      y += ld;
+    }
+    return;
+  }
+  const T* res = static_cast<const T*>(p.residual) + row0 * ld + feature;
+  __nv_bfloat16* z = p.z + row0 * ld + feature;
+  float add[32];
+#pragma unroll
+  for (int c = 0; c < 32; ++c)
+    add[c] = p.residual && (FULL || c < left) ? get(res + (int64_t)c * ld) : 0.0f;
 #pragma unroll
   for (int c = 0; c < 32; ++c) {
-    if (c >= left) break;
-    float v = __uint_as_float(r[c]);
-    if (MODE == kWeightGrad) {
-      const int64_t o = ((int64_t)w.g * p.Nw + w.r0 + c0 + c) * p.K + feature;
-      if (p.dw_f32) {
-        static_cast<float*>(p.dw)[o] = v;
-      } else {
-        static_cast<__nv_bfloat16*>(p.dw)[o] = __float2bfloat16_rn(v);
-      }
-      continue;
+    const float v = __uint_as_float(r[c]) + b;
+    if (FULL || c < left) {
+      if (p.z) put(z, v);
+      put(y, act_of(ACT, v) + add[c]);
     }
-    const int64_t row = w.begin + w.r0 + c0 + c;
-    if (MODE == kInputGrad) {
-      p.dx[row * p.K + feature] = __float2bfloat16_rn(v);
-      continue;
-    }
-    v += b;
-    const int64_t o = row * p.N + feature;
-    if (p.z) p.z[o] = __float2bfloat16_rn(v);
-    v = activate<ACT>(v);
-    if (p.y_f32) {
-      if (p.residual) v += static_cast<const float*>(p.residual)[o];
-      static_cast<float*>(p.y)[o] = v;
+    y += ld;
+    z += ld;
+  }
+}
+
+template <int MODE, int ACT>
+__device__ __forceinline__ void epilogue(const MmaParams& q, const Tile& w, int cta, int lane,
+                                         int quad, int c0, const uint32_t (&r)[32], float b) {
+  const bool full = w.rows - c0 >= 32;
+  if (q.out_f32) {
+    if (full) {
+      store_columns<MODE, ACT, true, float>(q, w, cta, lane, quad, c0, r, b);
     } else {
-      if (p.residual) v += __bfloat162float(static_cast<const __nv_bfloat16*>(p.residual)[o]);
-      static_cast<__nv_bfloat16*>(p.y)[o] = __float2bfloat16_rn(v);
+      store_columns<MODE, ACT, false, float>(q, w, cta, lane, quad, c0, r, b);
     }
+  } else if (full) {
+    store_columns<MODE, ACT, true, __nv_bfloat16>(q, w, cta, lane, quad, c0, r, b);
+  } else {
+    store_columns<MODE, ACT, false, __nv_bfloat16>(q, w, cta, lane, quad, c0, r, b);
   }
 }
 
@@ -270,7 +291,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     mbar_init(&bar->landed, 1);
     for (int a = 0; a < 2; ++a) {
       mbar_init(&bar->acc_full[a], 1);
-      mbar_init(&bar->acc_empty[a], 8);  // four epilogue warps of each CTA
+      mbar_init(&bar->acc_empty[a], 2 * kEpilogueWarps);  // of both CTAs
     }
     mbar_init_fence();
     tma_prefetch_map(&maps.a);
@@ -286,9 +307,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
   if (warp == 0) {
     // ------------------------------------------------ producer
-    const bool one = lane == 0;
-    int it = 0;
-    uint32_t landed_phase = 0;
+    int it = 0, s = 0;               // stages written so far, the ring's place
+    uint32_t phase = 1, landed_phase = 0;   // the first pass over the ring waits for nothing
     bool ok = true;
     for (int t = pair; t < tiles && ok; t += pairs) {
       const Tile w = tile_at<MODE>(q, first, begins, counts, t);
@@ -299,11 +319,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const uint32_t bytes = kStageA + (kStageB >> box);
       const CUtensorMap* map_b = &maps.b[box];
       for (int kb = 0; kb < w.blocks && ok; ++kb, ++it) {
-        const int s = it % kStages;
         if (it >= kStages) {
-          ok = mbar_wait(&bar->empty[s], ((it / kStages) - 1) & 1);
+          ok = warp_wait(&bar->empty[s], phase);
           if (!ok) break;
-          if (cta == 0 && one) mbar_signal_at(in_cta(&bar->empty[s], 1));
+          if (cta == 0 && elect_one()) mbar_signal_at(in_cta(&bar->empty[s], 1));
         }
         uint8_t* a = ring + s * kStageBytes;
         uint8_t* b = a + kStageA;
@@ -312,7 +331,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const bool tail = MODE == kWeightGrad && valid < kDepth && (valid & 15);
         const uint32_t full = in_cta(&bar->full[s], 0);
         const uint32_t on = tail ? smem_addr(&bar->landed) : full;
-        if (one) {
+        if (elect_one()) {
           if (tail) {
             mbar_arrive_expect_tx(&bar->landed, bytes);
           } else {
@@ -350,7 +369,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (tail) {
           // the rows after the segment's last belong to somebody else: clear
           // those that the last 16-term step would take in
-          ok = mbar_wait(&bar->landed, landed_phase);
+          ok = warp_wait(&bar->landed, landed_phase);
           landed_phase ^= 1;
           const int end = (valid + 15) / 16 * 16;
           const int n16 = 4 * (end - valid) * 8;                // 16-byte pieces
@@ -362,20 +381,32 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           }
           fence_async_shared();
           __syncwarp();
-          if (one) mbar_arrive_at(full);
+          if (lane == 0) mbar_arrive_at(full);
+        }
+        __syncwarp();
+        if (++s == kStages) {
+          s = 0;
+          phase ^= 1;
         }
       }
     }
     if (!ok) {
-      if (one) atomicOr(timeout, kErrLinearTimeout);
+      if (lane == 0) atomicOr(timeout, kErrLinearTimeout);
       if (cta == 0)   // copies in flight must land before the CTA leaves
         for (int s = 0; s < kStages && s < it; ++s)
           (void)mbar_wait_cluster(&bar->full[s], ((it - 1 - s) / kStages) & 1);
     }
   } else if (warp == 1) {
-    // ------------------------------------------------ MMA (even CTA, one thread)
-    if (cta == 0 && lane == 0) {
-      int it = 0, n_acc = 0;
+    // ------------------------------------------------ MMA (even CTA's warp, one lane issues)
+    if (cta == 0) {
+      // operands of stage 0; a stage is kStageBytes on, 16 terms are 32 bytes
+      // of a row (K-major) or 16 rows (MN-major) on
+      constexpr bool kMnA = MODE != kForward, kMnB = MODE == kWeightGrad;
+      constexpr uint32_t kStepA = (kMnA ? 2048 : 32) >> 4, kStepB = (kMnB ? 2048 : 32) >> 4;
+      const uint64_t a0 = smem_operand(smem_addr(ring), kMnA ? 8192 : 16);
+      const uint64_t b0 = smem_operand(smem_addr(ring) + kStageA, kMnB ? 8192 : 16);
+      int n_acc = 0, s = 0;
+      uint32_t phase = 0;
       bool ok = true;
       Tile next;
       if (pair < tiles) next = tile_at<MODE>(q, first, begins, counts, pair);
@@ -387,44 +418,46 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         const int acc = n_acc & 1;
         if (n_acc >= 2) {
-          ok = mbar_wait_cluster(&bar->acc_empty[acc], ((n_acc >> 1) - 1) & 1);
+          ok = warp_wait_cluster(&bar->acc_empty[acc], ((n_acc >> 1) - 1) & 1);
           if (!ok) break;
           tc_fence_after();
         }
         const uint32_t d = tmem + acc * 256;
-        const uint32_t form = mma_form(w.n, MODE != kForward, MODE == kWeightGrad);
-        for (int kb = 0; kb < w.blocks; ++kb, ++it) {
-          const int s = it % kStages;
-          const int steps = (min(kDepth, w.terms - kb * kDepth) + 15) / 16;
+        const uint32_t form = mma_form(w.n, kMnA, kMnB);
+        for (int kb = 0; kb < w.blocks; ++kb) {
           // dW's last block holds rows that the producers cleared
-          ok = MODE == kWeightGrad && kb == w.blocks - 1
-                   ? mbar_wait_cluster(&bar->full[s], (it / kStages) & 1)
-                   : mbar_wait(&bar->full[s], (it / kStages) & 1);
+          ok = MODE == kWeightGrad && kb == w.blocks - 1 ? warp_wait_cluster(&bar->full[s], phase)
+                                                         : warp_wait(&bar->full[s], phase);
           if (!ok) break;
           tc_fence_after();
-          const uint32_t a = smem_addr(ring + s * kStageBytes), b = a + kStageA;
-          for (int i = 0; i < steps; ++i) {
-            // 16 terms on: 32 bytes of a row (K-major) or 16 rows (MN-major)
-            const uint64_t da = MODE == kForward ? smem_operand(a + i * 32, 16)
-                                                 : smem_operand(a + i * 2048, 8192);
-            const uint64_t db = MODE == kWeightGrad ? smem_operand(b + i * 2048, 8192)
-                                                    : smem_operand(b + i * 32, 16);
-            mma_pair(d, da, db, form, kb > 0 || i > 0);
+          const uint64_t a = a0 + (uint32_t)(s * (kStageBytes >> 4));
+          const uint64_t b = b0 + (uint32_t)(s * (kStageBytes >> 4));
+          const int left = w.terms - kb * kDepth;
+          if (elect_one()) {
+            mma_pair(d, a, b, form, kb > 0);
+            if (left > 16) mma_pair(d, a + kStepA, b + kStepB, form, true);
+            if (left > 32) mma_pair(d, a + 2 * kStepA, b + 2 * kStepB, form, true);
+            if (left > 48) mma_pair(d, a + 3 * kStepA, b + 3 * kStepB, form, true);
+            mma_commit(&bar->empty[s]);
+            if (kb == w.blocks - 1) mma_commit(&bar->acc_full[acc]);
           }
-          mma_commit(&bar->empty[s]);
+          __syncwarp();
+          if (++s == kStages) {
+            s = 0;
+            phase ^= 1;
+          }
           // the next tile is worked out under this one's products
           if (kb == 0 && t + pairs < tiles)
             next = tile_at<MODE>(q, first, begins, counts, t + pairs);
         }
         if (!ok) break;
-        mma_commit(&bar->acc_full[acc]);
         ++n_acc;
       }
-      if (!ok) atomicOr(timeout, kErrLinearTimeout);
+      if (!ok && lane == 0) atomicOr(timeout, kErrLinearTimeout);
     }
   } else if (warp >= 4) {
     // ------------------------------------------------ epilogue
-    const int quad = warp - 4;
+    const int quad = warp & 3, turn = (warp - 4) >> 2;
     int n_acc = 0;
     for (int t = pair; t < tiles; t += pairs) {
       const Tile w = tile_at<MODE>(q, first, begins, counts, t);
@@ -443,21 +476,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         uint32_t zero[32];
 #pragma unroll
         for (int c = 0; c < 32; ++c) zero[c] = 0;
-        for (int c0 = 0; c0 < w.rows; c0 += 32)
-          store_columns<MODE, ACT>(q, w, (int)cta, lane, quad, c0, zero, 0.0f);
+        for (int c0 = turn * 32; c0 < w.rows; c0 += 64)
+          epilogue<MODE, ACT>(q, w, (int)cta, lane, quad, c0, zero, 0.0f);
         continue;
       }
       const int acc = n_acc & 1;
-      if (!mbar_wait_cluster(&bar->acc_full[acc], (n_acc >> 1) & 1)) {
+      if (!warp_wait_cluster(&bar->acc_full[acc], (n_acc >> 1) & 1)) {
         if (lane == 0) atomicOr(timeout, kErrLinearTimeout);
         break;
       }
       if (cta == 0 && threadIdx.x == 128) mbar_arrive_at(in_cta(&bar->acc_full[acc], 1));
       tc_fence_after();
-      for (int c0 = 0; c0 < w.rows; c0 += 32) {
+      for (int c0 = turn * 32; c0 < w.rows; c0 += 64) {
         uint32_t r[32];
         tmem_load32(tmem + ((uint32_t)(quad * 32) << 16) + acc * 256 + c0, r);
-        store_columns<MODE, ACT>(q, w, (int)cta, lane, quad, c0, r, b);
+        epilogue<MODE, ACT>(q, w, (int)cta, lane, quad, c0, r, b);
       }
       tc_fence_before();
       __syncwarp();
@@ -565,6 +598,8 @@ cudaError_t launch_linear_forward(const LinearParams& p, int sms, cudaStream_t s
   const int64_t rows = p.s.begin ? p.s.pool : p.s.dense_rows;
   MmaParams q;
   q.p = p;
+  q.out = p.y;
+  q.out_f32 = p.y_f32;
   q.features = p.Nw;
   q.f_tiles = (p.Nw + 255) / 256;
   q.r_tiles = 0;
@@ -596,6 +631,8 @@ cudaError_t launch_linear_input_grad(const LinearParams& p, int sms, cudaStream_
   const int64_t rows = p.s.begin ? p.s.pool : p.s.dense_rows;
   MmaParams q;
   q.p = p;
+  q.out = p.dx;
+  q.out_f32 = 0;
   q.features = p.K;
   q.f_tiles = (p.K + 255) / 256;
   q.r_tiles = 0;
@@ -612,6 +649,8 @@ cudaError_t launch_linear_weight_grad(const LinearParams& p, int sms, cudaStream
   const int64_t rows = p.s.begin ? p.s.pool : p.s.dense_rows;
   MmaParams q;
   q.p = p;
+  q.out = p.dw;
+  q.out_f32 = p.dw_f32;
   q.features = p.K;
   q.f_tiles = (p.K + 255) / 256;
   q.r_tiles = (p.Nw + kMaxRows - 1) / kMaxRows;

@@ -7,6 +7,18 @@
 
 namespace ep {
 
+// One lane of a converged warp, the same at every call: what it issues, the
+// compiler takes from warp-uniform registers.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n .reg .pred p;\n"
+      " elect.sync _|p, 0xFFFFFFFF;\n"
+      " selp.u32 %0, 1, 0, p;\n}"
+      : "=r"(p));
+  return p != 0;
+}
+
 __device__ __forceinline__ uint32_t cluster_rank() {
   uint32_t r;
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
@@ -66,6 +78,21 @@ __device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity
     if (globaltimer_ns() - t0 > kMbarWaitNs) return false;
   }
   return false;
+}
+
+// The same for a whole warp, which agrees on the answer (a lane alone that gave
+// up would leave the others in their next warp-wide step). No look at the clock
+// on the first polls.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
+  bool ok = false;
+#pragma unroll 1
+  for (int i = 0; i < 64 && !ok; ++i) ok = mbar_try_wait(bar, parity);
+  if (!ok) ok = mbar_wait(bar, parity);
+  return __all_sync(0xFFFFFFFFu, ok);
+}
+
+__device__ __forceinline__ bool warp_wait_cluster(uint64_t* bar, uint32_t parity) {
+  return __all_sync(0xFFFFFFFFu, mbar_wait_cluster(bar, parity));
 }
 
 __device__ __forceinline__ void fence_async_shared() {
