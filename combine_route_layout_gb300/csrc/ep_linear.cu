@@ -228,6 +228,8 @@ struct ep_linear_handle {
   int Nw;
   int64_t ldz, row_blocks;
   int32_t* err;
+  unsigned int* tickets;
+  float* partial;
   __nv_bfloat16* dz;
   float* part;
   size_t bytes;
@@ -240,6 +242,9 @@ using namespace ep;
 ep_status lfail(ep_status st, const char* msg) { return record_error(st, msg); }
 ep_status lcuda(cudaError_t e) { return record_error(EP_ERR_CUDA, cudaGetErrorString(e)); }
 size_t up256(size_t v) { return (v + 255) / 256 * 256; }
+
+constexpr size_t kHeaderBytes = 1024;   // error bits, tickets
+static_assert(256 + kLinearMaxPairs * 2 * sizeof(unsigned int) <= kHeaderBytes, "tickets");
 
 ep_status plan_linear(const ep_linear_config* c, ep_linear_handle* h) {
   if (!c) return lfail(EP_ERR_INVALID_ARG, "linear config is NULL");
@@ -269,8 +274,11 @@ ep_status plan_linear(const ep_linear_config* c, ep_linear_handle* h) {
   h->Nw = c->activation == EP_ACT_SWIGLU ? 2 * c->out_features : c->out_features;
   h->ldz = (h->Nw + 63) / 64 * 64;   // whole 64-element blocks
   h->row_blocks = (c->max_rows + kGradRows - 1) / kGradRows + c->num_groups;
-  size_t off = 256;
+  size_t off = kHeaderBytes;
   h->err = reinterpret_cast<int32_t*>(h->ws);
+  h->tickets = reinterpret_cast<unsigned int*>(h->ws ? h->ws + 256 : nullptr);
+  h->partial = reinterpret_cast<float*>(h->ws ? h->ws + off : nullptr);
+  off += kLinearMaxPairs * (c->backward ? kPartBytesGrad : kPartBytes);
   h->dz = nullptr;
   h->part = nullptr;
   if (c->backward) {
@@ -295,7 +303,7 @@ ep_status linear_ready(ep_linear_handle* h, cudaStream_t st) {
   if (!h->needs_init) return EP_OK;
   cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
   cudaError_t e = cudaStreamIsCapturing(st, &cap);
-  if (e == cudaSuccess) e = cudaMemsetAsync(h->ws, 0, 256, st);
+  if (e == cudaSuccess) e = cudaMemsetAsync(h->ws, 0, kHeaderBytes, st);
   if (e != cudaSuccess) return lcuda(e);
   if (cap == cudaStreamCaptureStatusNone) h->needs_init = false;
   return EP_OK;
@@ -326,6 +334,8 @@ ep_status fill_linear(const ep_linear_handle* h, const void* x, const void* w,
   p->s.count = row_count;
   p->s.base = row_base;
   p->s.err = h->err;
+  p->partial = h->partial;
+  p->tickets = h->tickets;
   p->K = c.in_features;
   p->N = c.out_features;
   p->Nw = h->Nw;
@@ -450,8 +460,10 @@ extern "C" ep_status ep_linear_sync(ep_linear_handle* h, void* stream) {
   }
   if (e == cudaSuccess) e = cudaStreamSynchronize(st);
   if (e != cudaSuccess) return lcuda(e);
-  if (bits & kErrLinearTimeout)
+  if (bits & kErrLinearTimeout) {
+    h->needs_init = true;   // tickets may be left over
     return lfail(EP_ERR_TIMEOUT, "a product's bounded wait gave up; its output is not complete");
+  }
   if (bits & kErrSegment)
     return lfail(EP_ERR_INVALID_INDEX,
                  "a segment reached outside the row pool and was cut, or a backward pass's overlapped");

@@ -15,6 +15,12 @@ namespace ep {
 constexpr int kErrSegment = 1;         // a segment reaches outside the pool
 constexpr int kErrLinearTimeout = 2;   // a bounded wait gave up
 
+// The products run on at most this many pairs of SMs; with fewer tiles than
+// pairs they cut contractions into parts, at most one per pair, of at most 64
+// rows x 256 features (dW: 256 x 256) f32 sums.
+constexpr int kLinearMaxPairs = 80;
+constexpr size_t kPartBytes = 64 * 256 * 4, kPartBytesGrad = 256 * 256 * 4;
+
 // Rows of each group: begin[g] (+ base[g / per_base]) .. + count[g] - 1 of
 // the pool, or the first `dense_rows` rows when begin is NULL (one group).
 struct LinearSegs {
@@ -42,6 +48,8 @@ struct LinearParams {
   void* y;                     // [pool][N]
   int y_f32;
   __nv_bfloat16* z;            // [pool][Nw] or NULL
+  float* partial;              // sums of parts
+  unsigned int* tickets;       // [kLinearMaxPairs][2], zero between calls
   // backward
   const void* dy;              // [pool][N] of y's type
   const __nv_bfloat16* dz;     // [pool][ldz]

@@ -34,7 +34,14 @@ constexpr int kDepth = 64;                       // terms per stage: 128 bytes o
 constexpr int kStageA = 128 * kDepth * 2;        // bytes of a CTA's 128 features
 constexpr int kStageB = 128 * kDepth * 2;        // bytes of a CTA's half of the rows
 constexpr int kStageBytes = kStageA + kStageB;
-constexpr int kMaxRows = 256;                    // rows of a tile
+constexpr int kMaxRows = 256;                    // rows of a tile (f32 outputs: half)
+constexpr int kMinCap = 64;
+constexpr int kMaxSplits = 8;
+// f32 outputs: the tensor core cuts off what its accumulator cannot hold, an
+// error that grows with the number of steps to the power 3/2 (7168 terms: 8e-6 of
+// the result); sums of 512 terms are added up in registers instead, which
+// leaves 6e-7.
+constexpr int kChunk32 = 8;                      // stages of such a sum
 constexpr int kEpilogueWarps = 8;                // two to each quarter of the TMEM lanes
 constexpr int kThreads = (4 + kEpilogueWarps) * 32;
 constexpr int kTmemColumns = 512;                // two accumulators
@@ -44,12 +51,13 @@ enum Mode { kForward = 0, kInputGrad = 1, kWeightGrad = 2 };
 struct MmaParams {
   LinearParams p;
   void* out;         // y, dx or dW
-  int out_f32;
   int features;      // length of the output's contiguous axis (weight rows or K)
   int f_tiles;       // 256-feature tiles
   int r_tiles;       // dW: 256-row tiles of each group (else by the group's count)
   int a_blocks;      // MN-major operands: the map cuts rows into blocks of 64
   int b_blocks;      // elements, so that one box takes two of them
+  float* partial;    // sums of parts: [unit][column][256 features], or NULL
+  unsigned int* tickets;   // parts that are done: [tile][2], zero between calls
 };
 
 struct Barriers {
@@ -59,31 +67,61 @@ struct Barriers {
   uint64_t acc_full[2];
   uint64_t acc_empty[2];      // even CTA's: both CTAs' epilogues are done
   uint32_t tmem;
+  uint32_t last;              // this CTA's part of a tile was the last
 };
 
-// A tile of one group.
+// A barrier of the epilogue's warps; whether all of them are well.
+__device__ __forceinline__ bool epilogue_agree(bool ok) {
+  uint32_t all;
+  asm volatile(
+      "{\n .reg .pred p, q;\n"
+      " setp.ne.u32 p, %1, 0;\n"
+      " bar.red.and.pred q, 1, %2, p;\n"
+      " selp.u32 %0, 1, 0, q;\n}"
+      : "=r"(all)
+      : "r"((uint32_t)ok), "n"(kEpilogueWarps * 32)
+      : "memory");
+  return all != 0;
+}
+
+// What every CTA finds out about the call from the groups' counts.
+struct Plan {
+  int tiles;
+  int cap;           // most rows of a tile
+  int splits;        // parts that a tile's contraction is cut into
+};
+
+// A part of the contraction of one tile.
 struct Tile {
   int g;
   int64_t begin;     // first pool row of the group
-  int count;         // its rows
   int r0, rows;      // rows of the tile within the group (dW: of the weight rows)
   int f0;            // first feature
   int n;             // MMA's N
-  int blocks;        // stages
   int terms;         // length of the contraction
+  int kb0, kb1;      // this part's stages; none: kb0 >= kb1
+  int part, parts;   // its place among the tile's parts that have any
 };
 
-// Rows of a tile and tiles of a group of `count` rows: as few tiles as 256
-// rows allow, of about equal size.
-__device__ __forceinline__ int tile_rows(int count) {
-  const int tiles = (count + kMaxRows - 1) / kMaxRows;
+// Rows of a tile of a group of `count` rows: as few tiles as `cap` rows
+// allow, of about equal size.
+__device__ __forceinline__ int tile_rows(int count, int cap) {
+  const int tiles = (count + cap - 1) / cap;
   return tiles ? ((count + tiles - 1) / tiles + 31) / 32 * 32 : 32;
 }
 
+__device__ __forceinline__ int tiles_in(int count, int cap) {
+  const int size = tile_rows(count, cap);
+  return (count + size - 1) / size;
+}
+
+// Unit u of the plan: part u % splits of tile u / splits.
 template <int MODE>
-__device__ __forceinline__ Tile tile_at(const MmaParams& q, const int* first, const int* begins,
-                                        const int* counts, int t) {
+__device__ __forceinline__ Tile tile_at(const MmaParams& q, const Plan& plan, const int* first,
+                                        const int* begins, const int* counts, int u) {
   Tile w;
+  int t = u / plan.splits;
+  w.part = u - t * plan.splits;
   int lo = 0, hi = q.p.s.G - 1;          // the last group that starts at or before t
   if (MODE == kWeightGrad) {
     lo = t / (q.f_tiles * q.r_tiles);
@@ -97,74 +135,113 @@ __device__ __forceinline__ Tile tile_at(const MmaParams& q, const int* first, co
   }
   w.g = lo;
   w.begin = begins[lo];
-  w.count = counts[lo];
+  const int count = counts[lo];
   if (MODE == kWeightGrad) {
-    w.r0 = (t / q.f_tiles) * kMaxRows;
+    w.r0 = (t / q.f_tiles) * plan.cap;
     w.f0 = (t % q.f_tiles) * 256;
-    w.rows = min(kMaxRows, q.p.Nw - w.r0);
+    w.rows = min(plan.cap, q.p.Nw - w.r0);
     w.n = w.rows > 128 ? 256 : 128;
-    w.terms = w.count;
+    w.terms = count;
   } else {
     // 8 row tiles at a time pass over all features, so that tiles that run
     // together share operands in L2
-    const int size = tile_rows(w.count);
-    const int tiles = (w.count + size - 1) / size;
+    const int size = tile_rows(count, plan.cap);
+    const int tiles = (count + size - 1) / size;
     const int per = 8 * q.f_tiles;
     const int band = t / per;
     const int in = min(8, tiles - band * 8);
     t -= band * per;
     w.r0 = (band * 8 + t % in) * size;
     w.f0 = (t / in) * 256;
-    w.rows = min(size, w.count - w.r0);
+    w.rows = min(size, count - w.r0);
     w.n = (w.rows + 31) / 32 * 32;
     w.terms = MODE == kForward ? q.p.K : q.p.Nw;
   }
-  w.blocks = (w.terms + kDepth - 1) / kDepth;
+  const int blocks = (w.terms + kDepth - 1) / kDepth;
+  const int each = (blocks + plan.splits - 1) / plan.splits;
+  w.parts = blocks ? (blocks + each - 1) / each : 1;
+  w.kb0 = w.part * each;
+  w.kb1 = min(blocks, w.kb0 + each);
   return w;
 }
 
-// The groups' segments and, over them, the first tile of each; returns the
-// number of tiles. All threads of the CTA.
+// The groups' segments, the size of the tiles and the first tile of each
+// group. All threads of the CTA.
+//
+// Where the tiles of 256 rows are fewer than half the pairs, tiles of 128 and
+// then 64 rows use more of the SMs at the cost of reading the weights more
+// often; what is still idle then takes parts of the tiles' contractions, whose
+// f32 sums the last part to finish adds up. 1024 x 7168 x 256: 43.7 us as 4
+// tiles of 256 rows, against 16 tiles of 64 rows in 4 parts each.
 template <int MODE>
-__device__ int plan_tiles(const MmaParams& q, int* first, int* begins, int* counts) {
-  __shared__ int warp_sum_[kThreads / 32];
-  const int G = q.p.s.G;
+__device__ Plan plan_tiles(const MmaParams& q, int base_cap, int* first, int* begins, int* counts) {
+  __shared__ int sums[3][kThreads / 32];
+  const int G = q.p.s.G, pairs = gridDim.x >> 1;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int per = (G + kThreads - 1) / kThreads;
   const int g0 = threadIdx.x * per, g1 = min(G, g0 + per);
-  int mine = 0;
+  Plan plan;
+  plan.cap = base_cap;
+  int mine[3] = {0, 0, 0};               // tiles of cap, cap / 2, cap / 4 rows; dW: largest count
   for (int g = g0; g < g1; ++g) {
     int64_t b, c;
     segment_of(q.p.s, g, b, c);
     begins[g] = (int)b;
     counts[g] = (int)c;
-    const int size = tile_rows((int)c);
-    mine += ((int)c + size - 1) / size * q.f_tiles;
-  }
-  if (MODE == kWeightGrad) {
-    __syncthreads();
-    return G * q.f_tiles * q.r_tiles;
-  }
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int incl = mine;
+    if (MODE == kWeightGrad) {
+      mine[0] = max(mine[0], (int)c);
+    } else {
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int v = __shfl_up_sync(kFull, incl, o);
-    if (lane >= o) incl += v;
+      for (int i = 0; i < 3; ++i) mine[i] += tiles_in((int)c, base_cap >> i) * q.f_tiles;
+    }
   }
-  if (lane == 31) warp_sum_[warp] = incl;
-  __syncthreads();
-  int before = incl - mine, total = 0;
-  for (int w = 0; w < kThreads / 32; ++w) {
-    if (w < warp) before += warp_sum_[w];
-    total += warp_sum_[w];
-  }
-  for (int g = g0; g < g1; ++g) {
-    first[g] = before;
-    const int size = tile_rows(counts[g]);
-    before += (counts[g] + size - 1) / size * q.f_tiles;
+#pragma unroll
+  for (int i = 0; i < 3; ++i) {
+    int v = mine[i];
+#pragma unroll
+    for (int o = 16; o; o >>= 1) {
+      const int x = __shfl_xor_sync(kFull, v, o);
+      v = MODE == kWeightGrad ? max(v, x) : v + x;
+    }
+    if (lane == 0) sums[i][warp] = v;
   }
   __syncthreads();
-  return total;
+  int total[3] = {0, 0, 0};
+  for (int w = 0; w < kThreads / 32; ++w)
+#pragma unroll
+    for (int i = 0; i < 3; ++i)
+      total[i] = MODE == kWeightGrad ? max(total[i], sums[i][w]) : total[i] + sums[i][w];
+  int blocks, least;
+  if (MODE == kWeightGrad) {
+    plan.tiles = G * q.f_tiles * q.r_tiles;
+    blocks = (total[0] + kDepth - 1) / kDepth;
+    least = 16;                          // a part's sums of a whole 256 x 256 tile are 256 KB
+  } else {
+    int i = 0;
+    while (i < 2 && 2 * total[i] <= pairs && (base_cap >> i) > kMinCap) ++i;
+    plan.cap = base_cap >> i;
+    plan.tiles = total[i];
+    blocks = ((MODE == kForward ? q.p.K : q.p.Nw) + kDepth - 1) / kDepth;
+    least = 4;
+    // tiles before this thread's groups: an exclusive scan over the threads
+    int incl = mine[i];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(kFull, incl, o);
+      if (lane >= o) incl += v;
+    }
+    int before = incl - mine[i];
+    for (int w = 0; w < warp; ++w) before += sums[i][w];
+    for (int g = g0; g < g1; ++g) {
+      first[g] = before;
+      before += tiles_in(counts[g], plan.cap) * q.f_tiles;
+    }
+  }
+  plan.splits = 1;
+  if (q.partial && plan.tiles > 0)
+    plan.splits = max(1, min(min(pairs / plan.tiles, kMaxSplits), blocks / least));
+  __syncthreads();
+  return plan;
 }
 
 __device__ __forceinline__ void put(float* at, float v) { *at = v; }
@@ -177,7 +254,7 @@ __device__ __forceinline__ float get(const __nv_bfloat16* at) { return __bfloat1
 // independent of one another and the loads of the residual come first.
 template <int MODE, int ACT, bool FULL, typename T>
 __device__ __forceinline__ void store_columns(const MmaParams& q, const Tile& w, int cta, int lane,
-                                              int quad, int c0, const uint32_t (&r)[32], float b) {
+                                              int quad, int c0, const float (&r)[32], float b) {
   const LinearParams& p = q.p;
   const int f = quad * 32 + lane;          // lane of the accumulator
   const int left = w.rows - c0;            // columns that exist
@@ -198,7 +275,7 @@ __device__ __forceinline__ void store_columns(const MmaParams& q, const Tile& w,
       add[i] = p.residual && in && (FULL || 2 * i + odd < left) ? get(res + (int64_t)(2 * i) * p.N) : 0.0f;
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
-      const float v0 = __uint_as_float(r[2 * i]) + b, v1 = __uint_as_float(r[2 * i + 1]) + b;
+      const float v0 = r[2 * i] + b, v1 = r[2 * i + 1] + b;
       const float other = __shfl_xor_sync(kFull, odd ? v0 : v1, 1);
       const float gate = odd ? other : v0, up = odd ? v1 : other;
       if (in && (FULL || 2 * i + odd < left)) {
@@ -220,7 +297,7 @@ __device__ __forceinline__ void store_columns(const MmaParams& q, const Tile& w,
   if (MODE != kForward) {
 #pragma unroll
     for (int c = 0; c < 32; ++c) {
-      if (FULL || c < left) put(y, __uint_as_float(r[c]));
+      if (FULL || c < left) put(y, r[c]);
       y += ld;
     }
     return;
@@ -233,7 +310,7 @@ __device__ __forceinline__ void store_columns(const MmaParams& q, const Tile& w,
     add[c] = p.residual && (FULL || c < left) ? get(res + (int64_t)c * ld) : 0.0f;
 #pragma unroll
   for (int c = 0; c < 32; ++c) {
-    const float v = __uint_as_float(r[c]) + b;
+    const float v = r[c] + b;
     if (FULL || c < left) {
       if (p.z) put(z, v);
       put(y, act_of(ACT, v) + add[c]);
@@ -243,20 +320,13 @@ __device__ __forceinline__ void store_columns(const MmaParams& q, const Tile& w,
   }
 }
 
-template <int MODE, int ACT>
+template <int MODE, int ACT, typename T>
 __device__ __forceinline__ void epilogue(const MmaParams& q, const Tile& w, int cta, int lane,
-                                         int quad, int c0, const uint32_t (&r)[32], float b) {
-  const bool full = w.rows - c0 >= 32;
-  if (q.out_f32) {
-    if (full) {
-      store_columns<MODE, ACT, true, float>(q, w, cta, lane, quad, c0, r, b);
-    } else {
-      store_columns<MODE, ACT, false, float>(q, w, cta, lane, quad, c0, r, b);
-    }
-  } else if (full) {
-    store_columns<MODE, ACT, true, __nv_bfloat16>(q, w, cta, lane, quad, c0, r, b);
+                                         int quad, int c0, const float (&r)[32], float b) {
+  if (w.rows - c0 >= 32) {
+    store_columns<MODE, ACT, true, T>(q, w, cta, lane, quad, c0, r, b);
   } else {
-    store_columns<MODE, ACT, false, __nv_bfloat16>(q, w, cta, lane, quad, c0, r, b);
+    store_columns<MODE, ACT, false, T>(q, w, cta, lane, quad, c0, r, b);
   }
 }
 
@@ -269,10 +339,11 @@ struct Maps {
   CUtensorMap b[4];
 };
 
-template <int MODE, int ACT>
+template <int MODE, int ACT, typename T>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     product_kernel(const __grid_constant__ Maps maps, MmaParams q) {
   constexpr bool kGated = MODE == kForward && ACT == EP_ACT_SWIGLU;
+  constexpr bool kChunked = sizeof(T) == 4;
   extern __shared__ uint8_t raw[];
   uint8_t* ring = reinterpret_cast<uint8_t*>(((uintptr_t)raw + 1023) & ~(uintptr_t)1023);
   Barriers* bar = reinterpret_cast<Barriers*>(ring + kStages * kStageBytes);
@@ -298,7 +369,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     tma_prefetch_map(&maps.b[0]);
   }
   if (warp == 1) tmem_alloc(&bar->tmem, kTmemColumns);
-  const int tiles = plan_tiles<MODE>(q, first, begins, counts);
+  const Plan plan = plan_tiles<MODE>(q, kChunked ? kMaxRows / 2 : kMaxRows, first, begins, counts);
+  const int units = plan.tiles * plan.splits;
   tc_fence_before();
   cluster_sync();
   tc_fence_after();
@@ -310,15 +382,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     int it = 0, s = 0;               // stages written so far, the ring's place
     uint32_t phase = 1, landed_phase = 0;   // the first pass over the ring waits for nothing
     bool ok = true;
-    for (int t = pair; t < tiles && ok; t += pairs) {
-      const Tile w = tile_at<MODE>(q, first, begins, counts, t);
+    for (int u = pair; u < units && ok; u += pairs) {
+      const Tile w = tile_at<MODE>(q, plan, first, begins, counts, u);
       const int half = w.n / 2;
       const int fc = w.f0 + (int)cta * 128;                     // this CTA's features
       const int rc = w.r0 + (int)cta * half;                    // this CTA's rows
       const int box = MODE == kWeightGrad ? 0 : half > 64 ? 0 : half > 32 ? 1 : half > 16 ? 2 : 3;
-      const uint32_t bytes = kStageA + (kStageB >> box);
+      const uint32_t bytes = kStageA + (MODE != kWeightGrad || q.b_blocks ? kStageB >> box
+                                                                          : half / 64 * 8192);
       const CUtensorMap* map_b = &maps.b[box];
-      for (int kb = 0; kb < w.blocks && ok; ++kb, ++it) {
+      for (int kb = w.kb0; kb < w.kb1 && ok; ++kb, ++it) {
         if (it >= kStages) {
           ok = warp_wait(&bar->empty[s], phase);
           if (!ok) break;
@@ -363,7 +436,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             tma_load_3d(b, map_b, 0, row, rc / 64, on);
           } else {
             tma_load_2d(b, map_b, rc, row, on);
-            tma_load_2d(b + 8192, map_b, rc + 64, row, on);
+            if (half == 128) tma_load_2d(b + 8192, map_b, rc + 64, row, on);
           }
         }
         if (tail) {
@@ -409,58 +482,69 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       uint32_t phase = 0;
       bool ok = true;
       Tile next;
-      if (pair < tiles) next = tile_at<MODE>(q, first, begins, counts, pair);
-      for (int t = pair; t < tiles && ok; t += pairs) {
+      if (pair < units) next = tile_at<MODE>(q, plan, first, begins, counts, pair);
+      for (int u = pair; u < units && ok; u += pairs) {
         const Tile w = next;
-        if (w.blocks == 0) {
-          if (t + pairs < tiles) next = tile_at<MODE>(q, first, begins, counts, t + pairs);
-          continue;
-        }
-        const int acc = n_acc & 1;
-        if (n_acc >= 2) {
-          ok = warp_wait_cluster(&bar->acc_empty[acc], ((n_acc >> 1) - 1) & 1);
-          if (!ok) break;
-          tc_fence_after();
-        }
-        const uint32_t d = tmem + acc * 256;
         const uint32_t form = mma_form(w.n, kMnA, kMnB);
-        for (int kb = 0; kb < w.blocks; ++kb) {
+        int stop = w.kb0;                  // end of the accumulator's sum
+        for (int kb = w.kb0; kb < w.kb1; ++kb) {
+          const int acc = n_acc & 1;
+          const bool fresh = kb == stop;
+          if (fresh) {
+            stop = kChunked ? min(w.kb1, kb + kChunk32) : w.kb1;
+            if (n_acc >= 2) {
+              ok = warp_wait_cluster(&bar->acc_empty[acc], ((n_acc >> 1) - 1) & 1);
+              if (!ok) break;
+              tc_fence_after();
+            }
+          }
+          const int left = w.terms - kb * kDepth;
           // dW's last block holds rows that the producers cleared
-          ok = MODE == kWeightGrad && kb == w.blocks - 1 ? warp_wait_cluster(&bar->full[s], phase)
-                                                         : warp_wait(&bar->full[s], phase);
+          ok = MODE == kWeightGrad && left <= kDepth ? warp_wait_cluster(&bar->full[s], phase)
+                                                     : warp_wait(&bar->full[s], phase);
           if (!ok) break;
           tc_fence_after();
+          const uint32_t d = tmem + acc * 256;
           const uint64_t a = a0 + (uint32_t)(s * (kStageBytes >> 4));
           const uint64_t b = b0 + (uint32_t)(s * (kStageBytes >> 4));
-          const int left = w.terms - kb * kDepth;
           if (elect_one()) {
-            mma_pair(d, a, b, form, kb > 0);
+            mma_pair(d, a, b, form, !fresh);
             if (left > 16) mma_pair(d, a + kStepA, b + kStepB, form, true);
             if (left > 32) mma_pair(d, a + 2 * kStepA, b + 2 * kStepB, form, true);
             if (left > 48) mma_pair(d, a + 3 * kStepA, b + 3 * kStepB, form, true);
             mma_commit(&bar->empty[s]);
-            if (kb == w.blocks - 1) mma_commit(&bar->acc_full[acc]);
+            if (kb + 1 == stop) mma_commit(&bar->acc_full[acc]);
           }
           __syncwarp();
+          if (kb + 1 == stop) ++n_acc;
           if (++s == kStages) {
             s = 0;
             phase ^= 1;
           }
-          // the next tile is worked out under this one's products
-          if (kb == 0 && t + pairs < tiles)
-            next = tile_at<MODE>(q, first, begins, counts, t + pairs);
+          // the next unit is worked out under this one's products
+          if (kb == w.kb0 && u + pairs < units)
+            next = tile_at<MODE>(q, plan, first, begins, counts, u + pairs);
         }
-        if (!ok) break;
-        ++n_acc;
+        if (w.kb0 >= w.kb1 && u + pairs < units)
+          next = tile_at<MODE>(q, plan, first, begins, counts, u + pairs);
       }
       if (!ok && lane == 0) atomicOr(timeout, kErrLinearTimeout);
     }
   } else if (warp >= 4) {
     // ------------------------------------------------ epilogue
+    // 64 columns of the tile belong to the warp pair of a quarter: 32 to this
+    // warp (T f32: at most two such blocks, whose sums it keeps)
     const int quad = warp & 3, turn = (warp - 4) >> 2;
+    const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
     int n_acc = 0;
-    for (int t = pair; t < tiles; t += pairs) {
-      const Tile w = tile_at<MODE>(q, first, begins, counts, t);
+    // A warp whose wait gave up does no more work, but meets the others at the
+    // barriers of parts, where all of them learn of it.
+    bool ok = true;
+    for (int u = pair; u < units; u += pairs) {
+      const Tile w = tile_at<MODE>(q, plan, first, begins, counts, u);
+      const bool whole = w.parts == 1;
+      if (w.kb0 >= w.kb1 && (MODE != kWeightGrad || w.part > 0 || w.terms > 0)) continue;
+      if (!ok && whole) continue;
       float b = 0.0f;
       if (MODE == kForward && q.p.bias) {
         const int f = (int)cta * 128 + quad * 32 + lane;
@@ -472,31 +556,87 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           b = __ldg(bias + w.f0 + f);
         }
       }
-      if (w.blocks == 0) {   // a group with no rows: its weight gradient is zero
-        uint32_t zero[32];
+      float* sums = q.partial + ((int64_t)u * plan.cap * 256 + cta * 128 + quad * 32 + lane);
+      if (w.kb0 >= w.kb1) {     // a group with no rows: its weight gradient is zero
+        float r[32];
 #pragma unroll
-        for (int c = 0; c < 32; ++c) zero[c] = 0;
+        for (int c = 0; c < 32; ++c) r[c] = 0.0f;
         for (int c0 = turn * 32; c0 < w.rows; c0 += 64)
-          epilogue<MODE, ACT>(q, w, (int)cta, lane, quad, c0, zero, 0.0f);
+          epilogue<MODE, ACT, T>(q, w, (int)cta, lane, quad, c0, r, 0.0f);
         continue;
       }
-      const int acc = n_acc & 1;
-      if (!warp_wait_cluster(&bar->acc_full[acc], (n_acc >> 1) & 1)) {
-        if (lane == 0) atomicOr(timeout, kErrLinearTimeout);
-        break;
+      // a value of this part: its sum for the others, or the tile's result
+      auto finish = [&](int c0, const float (&r)[32]) {
+        if (whole) {
+          epilogue<MODE, ACT, T>(q, w, (int)cta, lane, quad, c0, r, b);
+        } else {
+#pragma unroll
+          for (int c = 0; c < 32; ++c)
+            if (c0 + c < w.rows) sums[(int64_t)(c0 + c) * 256] = r[c];
+        }
+      };
+      const int chunks = kChunked ? (w.kb1 - w.kb0 + kChunk32 - 1) / kChunk32 : 1;
+      float keep[kChunked ? 2 : 1][32];
+      for (int i = 0; i < chunks && ok; ++i, ++n_acc) {
+        const int acc = n_acc & 1;
+        ok = warp_wait_cluster(&bar->acc_full[acc], (n_acc >> 1) & 1);
+        if (!ok) break;
+        if (cta == 0 && threadIdx.x == 128) mbar_arrive_at(in_cta(&bar->acc_full[acc], 1));
+        tc_fence_after();
+        if (kChunked) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int c0 = turn * 32 + h * 64;
+            if (c0 >= w.rows) continue;
+            float r[32];
+            tmem_load32(lanes + acc * 256 + c0, r);
+#pragma unroll
+            for (int c = 0; c < 32; ++c) keep[h % (kChunked ? 2 : 1)][c] = i ? keep[h % (kChunked ? 2 : 1)][c] + r[c] : r[c];
+          }
+        } else {
+          for (int c0 = turn * 32; c0 < w.rows; c0 += 64) {
+            float r[32];
+            tmem_load32(lanes + acc * 256 + c0, r);
+            finish(c0, r);
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_at(in_cta(&bar->acc_empty[acc], 0));
       }
-      if (cta == 0 && threadIdx.x == 128) mbar_arrive_at(in_cta(&bar->acc_full[acc], 1));
-      tc_fence_after();
+      if (kChunked && ok) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          if (turn * 32 + h * 64 < w.rows) finish(turn * 32 + h * 64, keep[h % (kChunked ? 2 : 1)]);
+      }
+      if (whole) continue;
+      // the tile's last part to get here adds all of them, in their order
+      if (!epilogue_agree(ok)) break;
+      if (threadIdx.x == 128) {
+        __threadfence();
+        unsigned int* ticket = q.tickets + (u / plan.splits) * 2 + cta;
+        const bool last = atomicAdd(ticket, 1u) == (unsigned)w.parts - 1;
+        if (last) *ticket = 0u;
+        bar->last = last;
+        __threadfence();
+      }
+      (void)epilogue_agree(true);
+      if (!bar->last) continue;
+      const float* from = sums - (int64_t)w.part * plan.cap * 256;
       for (int c0 = turn * 32; c0 < w.rows; c0 += 64) {
-        uint32_t r[32];
-        tmem_load32(tmem + ((uint32_t)(quad * 32) << 16) + acc * 256 + c0, r);
-        epilogue<MODE, ACT>(q, w, (int)cta, lane, quad, c0, r, b);
+        float r[32];
+#pragma unroll
+        for (int c = 0; c < 32; ++c) r[c] = 0.0f;
+        for (int part = 0; part < w.parts; ++part) {
+          const float* at = from + ((int64_t)part * plan.cap + c0) * 256;
+#pragma unroll
+          for (int c = 0; c < 32; ++c)
+            if (c0 + c < w.rows) r[c] += __ldcg(at + c * 256);
+        }
+        epilogue<MODE, ACT, T>(q, w, (int)cta, lane, quad, c0, r, b);
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive_at(in_cta(&bar->acc_empty[acc], 0));
-      ++n_acc;
     }
+    if (!ok && lane == 0) atomicOr(timeout, kErrLinearTimeout);
   }
   __syncwarp();
   __syncthreads();
@@ -570,25 +710,38 @@ bool map_mn_major(CUtensorMap* m, const void* base, int64_t cols, int64_t rows, 
   return make_map(m, base, groups ? 3 : 2, dims, strides, box);
 }
 
-template <int MODE, int ACT>
+template <int MODE, int ACT, typename T>
 cudaError_t launch_tiles(const Maps& maps, const MmaParams& q, int grid, cudaStream_t st) {
   const size_t smem = 1024 + kStages * kStageBytes + sizeof(Barriers) + (size_t)q.p.s.G * 12;
   // raises the kernel's shared-memory limit on its first use
-  (void)ctas_per_sm(product_kernel<MODE, ACT>, kThreads, 1024 + kStages * kStageBytes +
+  (void)ctas_per_sm(product_kernel<MODE, ACT, T>, kThreads, 1024 + kStages * kStageBytes +
                                                              sizeof(Barriers) + EP_MAX_EXPERTS * 12);
-  product_kernel<MODE, ACT><<<grid, kThreads, smem, st>>>(maps, q);
+  product_kernel<MODE, ACT, T><<<grid, kThreads, smem, st>>>(maps, q);
   return cudaGetLastError();
 }
 
 int grid_of(int sms, int64_t tiles) {
-  const int64_t most = sms / 2, pairs = tiles < most ? tiles : most;
+  const int64_t most = sms / 2 < kLinearMaxPairs ? sms / 2 : kLinearMaxPairs;
+  const int64_t pairs = tiles < most ? tiles : most;
   return (int)(2 * (pairs < 1 ? 1 : pairs));
 }
 
-// Upper bound of the row tiles of all groups (their counts are on the device).
-int64_t row_tiles(const LinearParams& p) {
-  if (!p.s.begin) return (p.s.dense_rows + kMaxRows - 1) / kMaxRows;
-  return p.s.pool / kMaxRows + p.s.G;
+// Upper bound of the units of all groups (their counts are on the device).
+int64_t most_units(const LinearParams& p, int f_tiles, int terms) {
+  const int64_t rows = p.s.begin ? p.s.pool : p.s.dense_rows;
+  const int64_t parts = terms / (4 * kDepth);
+  return (rows / kMinCap + p.s.G) * f_tiles * (parts < 1 ? 1 : parts < kMaxSplits ? parts : kMaxSplits);
+}
+
+template <typename T>
+cudaError_t launch_forward(const Maps& m, const MmaParams& q, int grid, cudaStream_t st) {
+  switch (q.p.act) {
+    case EP_ACT_RELU: return launch_tiles<kForward, EP_ACT_RELU, T>(m, q, grid, st);
+    case EP_ACT_SILU: return launch_tiles<kForward, EP_ACT_SILU, T>(m, q, grid, st);
+    case EP_ACT_GELU: return launch_tiles<kForward, EP_ACT_GELU, T>(m, q, grid, st);
+    case EP_ACT_SWIGLU: return launch_tiles<kForward, EP_ACT_SWIGLU, T>(m, q, grid, st);
+    default: return launch_tiles<kForward, EP_ACT_NONE, T>(m, q, grid, st);
+  }
 }
 
 }  // namespace
@@ -598,8 +751,9 @@ cudaError_t launch_linear_forward(const LinearParams& p, int sms, cudaStream_t s
   const int64_t rows = p.s.begin ? p.s.pool : p.s.dense_rows;
   MmaParams q;
   q.p = p;
+  q.partial = p.partial;
+  q.tickets = p.tickets;
   q.out = p.y;
-  q.out_f32 = p.y_f32;
   q.features = p.Nw;
   q.f_tiles = (p.Nw + 255) / 256;
   q.r_tiles = 0;
@@ -617,22 +771,18 @@ cudaError_t launch_linear_forward(const LinearParams& p, int sms, cudaStream_t s
   }
   if (!ok || !map_k_major(m.b, p.x, p.K, rows, p.K)) return cudaErrorInvalidValue;
   q.a_blocks = q.b_blocks = 0;
-  const int grid = grid_of(sms, row_tiles(p) * q.f_tiles);
-  switch (p.act) {
-    case EP_ACT_RELU: return launch_tiles<kForward, EP_ACT_RELU>(m, q, grid, st);
-    case EP_ACT_SILU: return launch_tiles<kForward, EP_ACT_SILU>(m, q, grid, st);
-    case EP_ACT_GELU: return launch_tiles<kForward, EP_ACT_GELU>(m, q, grid, st);
-    case EP_ACT_SWIGLU: return launch_tiles<kForward, EP_ACT_SWIGLU>(m, q, grid, st);
-    default: return launch_tiles<kForward, EP_ACT_NONE>(m, q, grid, st);
-  }
+  const int grid = grid_of(sms, most_units(p, q.f_tiles, p.K));
+  return p.y_f32 ? launch_forward<float>(m, q, grid, st)
+                 : launch_forward<__nv_bfloat16>(m, q, grid, st);
 }
 
 cudaError_t launch_linear_input_grad(const LinearParams& p, int sms, cudaStream_t st) {
   const int64_t rows = p.s.begin ? p.s.pool : p.s.dense_rows;
   MmaParams q;
   q.p = p;
+  q.partial = p.partial;
+  q.tickets = p.tickets;
   q.out = p.dx;
-  q.out_f32 = 0;
   q.features = p.K;
   q.f_tiles = (p.K + 255) / 256;
   q.r_tiles = 0;
@@ -642,27 +792,34 @@ cudaError_t launch_linear_input_grad(const LinearParams& p, int sms, cudaStream_
   if (!map_mn_major(&m.a, p.w, p.K, p.Nw, p.K, p.s.G, q.a_blocks) ||
       !map_k_major(m.b, p.dz, p.Nw, rows, p.ldz))
     return cudaErrorInvalidValue;
-  return launch_tiles<kInputGrad, EP_ACT_NONE>(m, q, grid_of(sms, row_tiles(p) * q.f_tiles), st);
+  return launch_tiles<kInputGrad, EP_ACT_NONE, __nv_bfloat16>(
+      m, q, grid_of(sms, most_units(p, q.f_tiles, p.Nw)), st);
 }
 
 cudaError_t launch_linear_weight_grad(const LinearParams& p, int sms, cudaStream_t st) {
   const int64_t rows = p.s.begin ? p.s.pool : p.s.dense_rows;
   MmaParams q;
   q.p = p;
+  q.partial = p.partial;
+  q.tickets = p.tickets;
   q.out = p.dw;
-  q.out_f32 = p.dw_f32;
   q.features = p.K;
   q.f_tiles = (p.K + 255) / 256;
-  q.r_tiles = (p.Nw + kMaxRows - 1) / kMaxRows;
+  const int cap = p.dw_f32 ? kMaxRows / 2 : kMaxRows;
+  q.r_tiles = (p.Nw + cap - 1) / cap;
   q.a_blocks = p.K % 64 == 0;
-  q.b_blocks = p.ldz % 64 == 0;   // columns past Nw give rows of dW that are not stored
+  // columns past Nw give rows of dW that are not stored; tiles of 128 rows
+  // have one 64-column part to a CTA
+  q.b_blocks = p.ldz % 64 == 0 && !p.dw_f32;
   Maps m;
   if (!map_mn_major(&m.a, p.x, p.K, rows, p.K, 0, q.a_blocks) ||
       !map_mn_major(&m.b[0], p.dz, p.Nw, rows, p.ldz, 0, q.b_blocks))
     return cudaErrorInvalidValue;
   for (int i = 1; i < 4; ++i) m.b[i] = m.b[0];
-  return launch_tiles<kWeightGrad, EP_ACT_NONE>(
-      m, q, grid_of(sms, (int64_t)p.s.G * q.f_tiles * q.r_tiles), st);
+  const int64_t units = (int64_t)p.s.G * q.f_tiles * q.r_tiles * kMaxSplits;
+  const int grid = grid_of(sms, units);
+  return p.dw_f32 ? launch_tiles<kWeightGrad, EP_ACT_NONE, float>(m, q, grid, st)
+                  : launch_tiles<kWeightGrad, EP_ACT_NONE, __nv_bfloat16>(m, q, grid, st);
 }
 
 }  // namespace ep
