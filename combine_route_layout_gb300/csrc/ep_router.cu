@@ -19,7 +19,12 @@
 //
 // Every kernel reads each logit once: a warp takes a row, a lane VPL
 // consecutive experts, in registers. Consecutive, so that the lowest lane
-// among equals holds the lowest expert and one ballot settles a tie.
+// among equals holds the lowest expert and one ballot settles a tie. The
+// kernels are bound by instruction issue: 256 experts cost a row about 500 warp
+// instructions, half of them the sigmoid's or softmax's, against 1 KB of reads.
+// Selection therefore sorts each lane's scores once (values alone, a network),
+// pops the warp's largest k times, and finds the experts' numbers at the end,
+// all k at once.
 #include <cuda_bf16.h>
 
 #include <cstring>
@@ -32,6 +37,7 @@ namespace {
 
 constexpr int kRouterWarps = 8;
 constexpr int kRouterRows = 64;      // most rows of one CTA, all of one segment
+constexpr int kRouterCtas = 4 * 152; // CTAs that a batch is spread over, where it has the rows
 constexpr int kMaxGroups = EP_MAX_ROUTER_GROUPS;
 constexpr int kErrNotFinite = 1;     // a logit was NaN or +inf
 constexpr int kErrRouterIndex = 2;   // an expert id outside [-1, E)
@@ -39,6 +45,7 @@ constexpr int kErrRouterIndex = 2;   // an expert id outside [-1, E)
 struct RouterParams {
   int R, Tmax, E, k;
   int groups, topk_groups;
+  int groups_run;            // lanes of a group, where groups are whole runs of a power of two; else 0
   int normalize;
   float scale;
   int stretch;               // tokens of a rank that belong to one segment
@@ -93,23 +100,35 @@ __device__ __forceinline__ float warp_sum(float v) {
   return v;
 }
 
-__device__ __forceinline__ float warp_max(float v) {
-#pragma unroll
-  for (int o = 16; o; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kFull, v, o));
-  return v;
-}
-
-// A key that orders as the float does (both zeros alike), above 0 for every
-// finite value; 0 is "none".
-__device__ __forceinline__ uint32_t key_of(float v) {
-  const uint32_t u = __float_as_uint(v + 0.0f);
-  return u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
+__device__ __forceinline__ float redux_max(float v) {
+  float r;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+  return r;
 }
 
 // 1 / (1 + exp(-l)) with every step rounded to f32, as the definition has it:
-// the selection compares these values.
+// the selection compares these values. (A reciprocal rounded to nearest is the
+// quotient 1 / x rounded to nearest.) -inf gives 0.
 __device__ __forceinline__ float sigmoid(float l) {
-  return __fdiv_rn(1.0f, __fadd_rn(1.0f, expf(-l)));
+  return __frcp_rn(__fadd_rn(1.0f, expf(-l)));
+}
+
+// Batcher's odd-even merge sort, descending, in registers.
+template <int N>
+__device__ __forceinline__ void sort_down(float (&v)[N]) {
+#pragma unroll
+  for (int p = 1; p < N; p <<= 1)
+#pragma unroll
+    for (int k = p; k >= 1; k >>= 1)
+#pragma unroll
+      for (int j = k % p; j + k < N; j += 2 * k)
+#pragma unroll
+        for (int i = 0; i < k; ++i)
+          if (i + j + k < N && (i + j) / (2 * p) == (i + j + k) / (2 * p)) {
+            const float a = v[i + j], b = v[i + j + k];
+            v[i + j] = fmaxf(a, b);
+            v[i + j + k] = fminf(a, b);
+          }
 }
 
 // This lane's VPL logits of the row; -inf beyond the row's end.
@@ -141,32 +160,37 @@ __device__ __forceinline__ void load_row(const T* row, int E, int lane, bool vec
   }
 }
 
-// Masked logits become -inf; NaN and +inf too, and raise the error bit.
+// A logit that counts, else -inf: masked, and (raising `bad`) NaN and +inf.
+template <typename T>
+__device__ __forceinline__ float open_logit(float l, bool& bad) {
+  const bool finite = l < INFINITY;
+  bad |= !finite;
+  return finite && l > lowest<T>() ? l : -INFINITY;
+}
+
 template <int VPL, typename T>
 __device__ __forceinline__ void mask_row(float (&l)[VPL], int32_t* err) {
   bool bad = false;
 #pragma unroll
-  for (int i = 0; i < VPL; ++i) {
-    bad |= !(l[i] < INFINITY);
-    if (!(l[i] > lowest<T>()) || !(l[i] < INFINITY)) l[i] = -INFINITY;
-  }
-  if (bad && err) atomicOr(err, kErrNotFinite);
+  for (int i = 0; i < VPL; ++i) l[i] = open_logit<T>(l[i], bad);
+  if (bad) atomicOr(err, kErrNotFinite);
 }
 
-// p (softmax: exp(l - max), sigmoid: s) of the lane's experts, 0 where masked.
+// The row's largest logit; 0 for a row with none, so that exp(-inf - 0) is 0.
+template <int VPL>
+__device__ __forceinline__ float row_max(const float (&l)[VPL]) {
+  float m = l[0];
+#pragma unroll
+  for (int i = 1; i < VPL; ++i) m = fmaxf(m, l[i]);
+  m = redux_max(m);
+  return m > -INFINITY ? m : 0.0f;
+}
+
+// p (softmax: exp(l - top), sigmoid: s) of the lane's experts, 0 where masked.
 template <int VPL, bool SIGMOID>
-__device__ __forceinline__ void raw_scores(const float (&l)[VPL], float (&p)[VPL]) {
-  if (SIGMOID) {
+__device__ __forceinline__ void raw_scores(const float (&l)[VPL], float top, float (&p)[VPL]) {
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) p[i] = l[i] > -INFINITY ? sigmoid(l[i]) : 0.0f;
-  } else {
-    float m = l[0];
-#pragma unroll
-    for (int i = 1; i < VPL; ++i) m = fmaxf(m, l[i]);
-    m = warp_max(m);
-#pragma unroll
-    for (int i = 0; i < VPL; ++i) p[i] = l[i] > -INFINITY ? expf(l[i] - m) : 0.0f;
-  }
+  for (int i = 0; i < VPL; ++i) p[i] = SIGMOID ? sigmoid(l[i]) : expf(l[i] - top);
 }
 
 template <int VPL>
@@ -197,64 +221,157 @@ __device__ __forceinline__ RowPlace place_of(const RouterParams& p, int c) {
   return w;
 }
 
-// Keep the keys of the topk_groups best groups. `buf`: E floats of this warp.
+// Which of the groups stay, by their two best scores (`best`, `second` on the
+// lane that asks for group `g`; `src`: the lane that answers for group j is
+// j * src).
+template <bool SIGMOID>
+__device__ __forceinline__ bool group_stays(const RouterParams& p, float best, float second, int g,
+                                            int src) {
+  if (SIGMOID && second > -INFINITY) best = __fadd_rn(best, second);
+  int ahead = 0;
+  for (int j = 0; j < p.groups; ++j) {
+    const float v = __shfl_sync(kFull, best, j * src);
+    ahead += v > best || (v == best && j < g);
+  }
+  return ahead < p.topk_groups && best > -INFINITY;
+}
+
+// Drop the scores of all but the best groups, for groups that are not whole
+// runs of lanes: lane g walks group g in shared memory.
 template <int VPL, bool SIGMOID>
-__device__ __forceinline__ void limit_groups(const RouterParams& p, int lane, float* buf,
-                                             const float (&c)[VPL], uint32_t (&key)[VPL]) {
+__device__ __forceinline__ void drop_groups(const RouterParams& p, int lane, const float* buf,
+                                            float (&c)[VPL]) {
   const int size = p.E / p.groups;
-#pragma unroll
-  for (int i = 0; i < VPL; ++i)
-    if (lane * VPL + i < p.E) buf[lane * VPL + i] = key[i] ? c[i] : -INFINITY;
-  __syncwarp();
-  float best = -INFINITY;
-  if (lane < p.groups) {
-    float second = -INFINITY;
+  float best = -INFINITY, second = -INFINITY;
+  if (lane < p.groups)
     for (int j = 0; j < size; ++j) {
       const float v = buf[lane * size + j];
       second = fmaxf(second, fminf(v, best));
       best = fmaxf(best, v);
     }
-    if (SIGMOID && second > -INFINITY) best = __fadd_rn(best, second);
-  }
   __syncwarp();
-  int ahead = 0;
-  for (int j = 0; j < p.groups; ++j) {
-    const float v = __shfl_sync(kFull, best, j);
-    ahead += v > best || (v == best && j < lane);
-  }
-  const uint32_t kept = __ballot_sync(kFull, lane < p.groups && ahead < p.topk_groups &&
-                                                 best > -INFINITY);
+  const uint32_t kept =
+      __ballot_sync(kFull, group_stays<SIGMOID>(p, best, second, lane, 1) && lane < p.groups);
 #pragma unroll
   for (int i = 0; i < VPL; ++i)
-    if (lane * VPL + i < p.E && !((kept >> ((lane * VPL + i) / size)) & 1u)) key[i] = 0;
+    if (lane * VPL + i < p.E && !((kept >> ((lane * VPL + i) / size)) & 1u)) c[i] = -INFINITY;
+}
+
+template <int VPL>
+__device__ __forceinline__ void put_row(float* buf, int lane, const float (&c)[VPL]) {
+  float* at = buf + lane * VPL;
+  if (VPL % 4 == 0) {
+#pragma unroll
+    for (int i = 0; i < VPL; i += 4)
+      *reinterpret_cast<float4*>(at + i) =
+          make_float4(c[i], c[(i + 1) % VPL], c[(i + 2) % VPL], c[(i + 3) % VPL]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) at[i] = c[i];
+  }
+}
+
+// The k best of the warp's scores c (-inf: none), in order, ties to the lowest
+// expert: lane j gets slot j's expert (-1: none left) and score.
+template <int VPL, bool SIGMOID>
+__device__ __forceinline__ void select_experts(const RouterParams& p, int lane, float* buf,
+                                               float (&c)[VPL], int& expert, float& score) {
+  __syncwarp();
+  put_row<VPL>(buf, lane, c);
+  __syncwarp();
+  // groups that are 1, 2, 4, ... whole lanes need no walk through memory
+  const int run = p.groups_run;
+  if (p.groups > 1 && run == 0) {
+    drop_groups<VPL, SIGMOID>(p, lane, buf, c);
+    put_row<VPL>(buf, lane, c);
+    __syncwarp();
+  }
+  sort_down<VPL>(c);
+  if (p.groups > 1 && run > 0) {
+    float best = c[0], second = VPL > 1 ? c[1 % VPL] : -INFINITY;
+    for (int o = 1; o < run; o <<= 1) {
+      const float a = __shfl_xor_sync(kFull, best, o), b = __shfl_xor_sync(kFull, second, o);
+      second = fmaxf(fminf(best, a), fmaxf(second, b));
+      best = fmaxf(best, a);
+    }
+    if (!group_stays<SIGMOID>(p, best, second, lane / run, run)) {
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) c[i] = -INFINITY;
+    }
+  }
+  int from = -1;
+  float mine = 0.0f;
+  for (int j = 0; j < p.k; ++j) {
+    const float m = redux_max(c[0]);
+    if (!(m > -INFINITY)) break;
+    const int win = __ffs(__ballot_sync(kFull, c[0] == m)) - 1;
+    if (lane == j) {
+      from = win;
+      mine = m;
+    }
+    if (lane == win) {
+#pragma unroll
+      for (int i = 0; i + 1 < VPL; ++i) c[i] = c[i + 1];
+      c[VPL - 1] = -INFINITY;
+    }
+  }
+  // slot j's expert: among the winner's, the one with its score; equal scores
+  // of one lane went to neighbouring slots, in the experts' order
+  int skip = 0;
+  const int from1 = __shfl_up_sync(kFull, from, 1);
+  const float mine1 = __shfl_up_sync(kFull, mine, 1);
+  if (__any_sync(kFull, lane > 0 && from >= 0 && from == from1 && mine == mine1)) {
+    for (int o = 1; o < p.k; ++o) {
+      const int f = __shfl_up_sync(kFull, from, o);
+      const float v = __shfl_up_sync(kFull, mine, o);
+      skip += lane >= o && f == from && v == mine;
+    }
+  }
+  expert = -1;
+  score = mine;
+  if (from >= 0) {
+#pragma unroll
+    for (int i = 0; i < VPL; ++i)
+      if (buf[from * VPL + i] == mine && skip-- == 0) expert = from * VPL + i;
+  }
 }
 
 // SELECT: choose the experts, write indices and weights. BALANCE: sums of p
 // and rows per expert for the loss (of the chosen, or of given indices).
 template <int VPL, typename T, bool SIGMOID, bool SELECT, bool BALANCE>
 __global__ void __launch_bounds__(kRouterWarps * 32) router_rows_kernel(RouterParams p) {
-  extern __shared__ float smem[];
+  if (BALANCE) pdl_launch_dependents();   // the reduction may be set up
+  extern __shared__ __align__(16) float smem[];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const RowPlace at = place_of(p, blockIdx.x);
-  float* buf = smem + (size_t)warp * p.E;                      // group scores, then sums of p
-  int* cnt = reinterpret_cast<int*>(smem + (size_t)kRouterWarps * p.E);
+  float* buf = smem + warp * 32 * VPL;                         // a row's scores, then sums of p
+  int* cnt = reinterpret_cast<int*>(smem + kRouterWarps * 32 * VPL);
   if (BALANCE) {
     for (int e = threadIdx.x; e < p.E; e += blockDim.x) cnt[e] = 0;
     __syncthreads();
   }
-  float sum_p[VPL];
+  float sum_p[VPL], bias[VPL];
 #pragma unroll
-  for (int i = 0; i < VPL; ++i) sum_p[i] = 0.0f;
-
-  for (int t = at.t0 + warp; t < at.t0 + at.n; t += kRouterWarps) {
+  for (int i = 0; i < VPL; ++i) {
+    sum_p[i] = 0.0f;
+    bias[i] = SIGMOID && SELECT && p.bias && lane * VPL + i < p.E ? __ldg(p.bias + lane * VPL + i) : 0.0f;
+  }
+  const T* logits = static_cast<const T*>(p.logits);
+  const int end = at.t0 + at.n;
+  float next[VPL];
+  if (at.t0 + warp < end)
+    load_row<VPL, T>(logits + ((int64_t)at.rank * p.Tmax + at.t0 + warp) * p.E, p.E, lane, p.vec, next);
+  for (int t = at.t0 + warp; t < end; t += kRouterWarps) {
     const int64_t g = (int64_t)at.rank * p.Tmax + t;
-    float l[VPL];
-    load_row<VPL, T>(static_cast<const T*>(p.logits) + g * p.E, p.E, lane, p.vec, l);
-    // beyond the row's end the logits are -inf already, which raises nothing
+    float l[VPL], pr[VPL];
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) l[i] = next[i];
+    if (t + kRouterWarps < end)    // the next row is on its way under this one
+      load_row<VPL, T>(logits + (g + kRouterWarps) * p.E, p.E, lane, p.vec, next);
     mask_row<VPL, T>(l, p.err);
-    float pr[VPL];
-    float total = 0.0f;
-    if (SIGMOID || BALANCE || !p.normalize) raw_scores<VPL, SIGMOID>(l, pr);
+    float total = 0.0f, top = 0.0f;
+    if (!SIGMOID && (BALANCE || !p.normalize)) top = row_max<VPL>(l);
+    if (SIGMOID || BALANCE || !p.normalize) raw_scores<VPL, SIGMOID>(l, top, pr);
     if (BALANCE || (!SIGMOID && !p.normalize)) total = row_sum<VPL>(pr);
     if (BALANCE) {
       const float inv = total > 0.0f ? 1.0f / total : 0.0f;
@@ -263,74 +380,31 @@ __global__ void __launch_bounds__(kRouterWarps * 32) router_rows_kernel(RouterPa
     }
     if (SELECT) {
       float c[VPL];
-      uint32_t key[VPL];
 #pragma unroll
-      for (int i = 0; i < VPL; ++i) {
-        const int e = lane * VPL + i;
-        c[i] = l[i];
-        if (SIGMOID) c[i] = p.bias && e < p.E ? __fadd_rn(pr[i], __ldg(p.bias + e)) : pr[i];
-        key[i] = l[i] > -INFINITY ? key_of(c[i]) : 0u;
-      }
-      if (p.groups > 1) limit_groups<VPL, SIGMOID>(p, lane, buf, c, key);
-      // k rounds: the warp's largest key, its lowest lane; lane j keeps slot j
-      int my_e = -1;
-      float my_v = 0.0f;
-      uint32_t top = 0;
-      int top_i = 0;
-      float top_v = 0.0f;
-      auto rescan = [&]() {
-        top = 0;
-#pragma unroll
-        for (int i = 0; i < VPL; ++i)
-          if (key[i] > top) {
-            top = key[i];
-            top_i = i;
-            top_v = SIGMOID ? pr[i] : l[i];
-          }
-      };
-      rescan();
-      for (int j = 0; j < p.k; ++j) {
-        const uint32_t m = __reduce_max_sync(kFull, top);
-        if (m == 0) break;
-        const int win = __ffs(__ballot_sync(kFull, top == m)) - 1;
-        const int e = __shfl_sync(kFull, lane * VPL + top_i, win);
-        const float v = __shfl_sync(kFull, top_v, win);
-        if (lane == j) {
-          my_e = e;
-          my_v = v;
-        }
-        if (lane == win) {
-#pragma unroll
-          for (int i = 0; i < VPL; ++i)
-            if (i == top_i) key[i] = 0;
-          rescan();
-        }
-      }
+      for (int i = 0; i < VPL; ++i)
+        c[i] = !SIGMOID ? l[i] : l[i] > -INFINITY ? __fadd_rn(pr[i], bias[i]) : -INFINITY;
+      int e;
+      float v;
+      select_experts<VPL, SIGMOID>(p, lane, buf, c, e, v);
       float wt = 0.0f;
       if (SIGMOID) {
-        const float s = my_e >= 0 ? my_v : 0.0f;
+        // with a bias the slot's own score is made again from its logit
+        float s = 0.0f;
+        if (e >= 0) s = p.bias ? sigmoid((float)logits[g * p.E + e]) : v;
         const float d = p.normalize ? warp_sum(s) : 1.0f;
         wt = d > 0.0f ? s / d : 0.0f;
+      } else if (p.normalize) {
+        const float m = redux_max(e >= 0 ? v : -INFINITY);
+        const float x = e >= 0 ? expf(v - m) : 0.0f;
+        const float d = warp_sum(x);
+        wt = d > 0.0f ? x / d : 0.0f;
       } else {
-        const float m = warp_max(my_e >= 0 ? my_v : -INFINITY);   // the row's largest, if !normalize
-        if (p.normalize) {
-          const float x = my_e >= 0 ? expf(my_v - m) : 0.0f;
-          const float d = warp_sum(x);
-          wt = d > 0.0f ? x / d : 0.0f;
-        } else {
-          const float all = warp_max([&] {
-            float v = l[0];
-#pragma unroll
-            for (int i = 1; i < VPL; ++i) v = fmaxf(v, l[i]);
-            return v;
-          }());
-          wt = my_e >= 0 ? expf(my_v - all) / total : 0.0f;
-        }
+        wt = e >= 0 ? expf(v - top) / total : 0.0f;
       }
       if (lane < p.k) {
-        p.idx[g * p.k + lane] = my_e;
-        p.w[g * p.k + lane] = my_e >= 0 ? wt * p.scale : 0.0f;
-        if (BALANCE && my_e >= 0) atomicAdd(cnt + my_e, 1);
+        p.idx[g * p.k + lane] = e;
+        p.w[g * p.k + lane] = e >= 0 ? wt * p.scale : 0.0f;
+        if (BALANCE && e >= 0) atomicAdd(cnt + e, 1);
       }
     } else if (lane < p.k) {
       const int e = __ldg(p.idx_in + g * p.k + lane);
@@ -342,7 +416,7 @@ __global__ void __launch_bounds__(kRouterWarps * 32) router_rows_kernel(RouterPa
     }
   }
   if (SELECT) {  // rows past the rank's tokens hold no expert
-    const int first = max(at.t0, at.t0 + at.n);
+    const int first = max(at.t0, end);
     const int64_t b = ((int64_t)at.rank * p.Tmax + first) * p.k;
     const int64_t m = (int64_t)max(0, at.pad_end - first) * p.k;
     for (int64_t i = threadIdx.x; i < m; i += blockDim.x) {
@@ -351,52 +425,55 @@ __global__ void __launch_bounds__(kRouterWarps * 32) router_rows_kernel(RouterPa
     }
   }
   if (BALANCE) {
-#pragma unroll
-    for (int i = 0; i < VPL; ++i)
-      if (lane * VPL + i < p.E) buf[lane * VPL + i] = sum_p[i];
+    __syncwarp();
+    put_row<VPL>(buf, lane, sum_p);
     __syncthreads();
     for (int e = threadIdx.x; e < p.E; e += blockDim.x) {
       float s = 0.0f;
 #pragma unroll
-      for (int w = 0; w < kRouterWarps; ++w) s += smem[w * p.E + e];
+      for (int w = 0; w < kRouterWarps; ++w) s += smem[w * 32 * VPL + e];
       p.part_p[(int64_t)blockIdx.x * p.E + e] = s;
       p.part_n[(int64_t)blockIdx.x * p.E + e] = cnt[e];
     }
   }
 }
 
-// Counts and loss from the chunks' sums, added in chunk order: CTA (b, s)
-// takes 32 experts of segment s, a warp every 8th chunk, and the last CTA adds
-// the products. Every sum has a fixed order.
+// Counts and loss from the chunks' sums, added in a fixed order: CTA (b, s)
+// takes 32 experts of segment s, a warp every 32nd chunk, and the last CTA
+// adds the products. Latency bound: 32 warps keep the loads in flight.
 constexpr int kBalanceExperts = 32;
+constexpr int kBalanceWarps = 32;
 
-__global__ void __launch_bounds__(256) balance_reduce_kernel(BalanceParams p) {
-  __shared__ float sp[8][kBalanceExperts];
-  __shared__ int sn[8][kBalanceExperts];
+__global__ void __launch_bounds__(kBalanceWarps * 32) balance_reduce_kernel(BalanceParams p) {
+  __shared__ float sp[kBalanceWarps][kBalanceExperts + 1];
+  __shared__ int sn[kBalanceWarps][kBalanceExperts + 1];
   __shared__ bool last;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int e = blockIdx.x * kBalanceExperts + lane;
   const int seg = blockIdx.y;
   const int first = p.n_seg == 1 ? 0 : seg * p.chunks;
   const int n_chunk = p.n_seg == 1 ? p.R * p.stretches * p.chunks : p.chunks;
+  pdl_wait();
   float s = 0.0f;
   int n = 0;
-  if (e < p.E)
-    for (int c = warp; c < n_chunk; c += 8) {
-      s += __ldg(p.part_p + (int64_t)(first + c) * p.E + e);
-      n += __ldg(p.part_n + (int64_t)(first + c) * p.E + e);
+  if (e < p.E) {
+#pragma unroll 4
+    for (int c = warp; c < n_chunk; c += kBalanceWarps) {
+      s += __ldcg(p.part_p + (int64_t)(first + c) * p.E + e);
+      n += __ldcg(p.part_n + (int64_t)(first + c) * p.E + e);
     }
+  }
   sp[warp][lane] = s;
   sn[warp][lane] = n;
   __syncthreads();
-  if (warp == 0) {
-    s = 0.0f;
-    n = 0;
+  // lane w of warp e' adds warp w's sums of expert e', in a fixed tree
+  s = warp_sum(sp[lane][warp]);
+  n = sn[lane][warp];
 #pragma unroll
-    for (int w = 0; w < 8; ++w) {
-      s += sp[w][lane];
-      n += sn[w][lane];
-    }
+  for (int o = 16; o; o >>= 1) n += __shfl_xor_sync(kFull, n, o);
+  __syncthreads();
+  if (lane == 0) {
+    const int mine = blockIdx.x * kBalanceExperts + warp;
     int held = 0;
     if (p.n_seg == 1) {
       for (int r = 0; r < p.R; ++r) held += p.ntok[r];
@@ -405,14 +482,17 @@ __global__ void __launch_bounds__(256) balance_reduce_kernel(BalanceParams p) {
       held = max(0, min(p.ntok[r] - s0, p.stretch));
     }
     float term = 0.0f;
-    if (e < p.E) {
-      p.counts[(int64_t)seg * p.E + e] = n;
+    if (mine < p.E) {
+      p.counts[(int64_t)seg * p.E + mine] = n;
       if (held > 0) term = ((float)n * (float)p.E / ((float)held * (float)p.k)) * (s / (float)held);
     }
-    term = warp_sum(term);
+    sp[0][warp] = term;
+  }
+  __syncthreads();
+  if (warp == 0) {
+    const float term = warp_sum(sp[0][lane]);
     if (lane == 0) {
-      const int slot = seg * gridDim.x + blockIdx.x;
-      p.part_loss[slot] = term;
+      p.part_loss[seg * gridDim.x + blockIdx.x] = term;
       __threadfence();
       last = atomicAdd(p.ticket, 1u) == gridDim.x * gridDim.y - 1;
     }
@@ -422,15 +502,16 @@ __global__ void __launch_bounds__(256) balance_reduce_kernel(BalanceParams p) {
   __threadfence();
   const int m = gridDim.x * gridDim.y;
   float acc = 0.0f;
-  for (int i = threadIdx.x; i < m; i += 256) acc += __ldcg(p.part_loss + i);
+  for (int i = threadIdx.x; i < m; i += kBalanceWarps * 32) acc += __ldcg(p.part_loss + i);
   acc = warp_sum(acc);
   if (lane == 0) sp[0][warp] = acc;
   __syncthreads();
-  if (threadIdx.x == 0) {
-    float v = 0.0f;
-    for (int w = 0; w < 8; ++w) v += sp[0][w];
-    *p.loss = v * p.coef;
-    *p.ticket = 0u;
+  if (warp == 0) {
+    const float v = warp_sum(sp[0][lane]);
+    if (lane == 0) {
+      *p.loss = v * p.coef;
+      *p.ticket = 0u;
+    }
   }
 }
 
@@ -440,11 +521,19 @@ __global__ void __launch_bounds__(256) balance_reduce_kernel(BalanceParams p) {
 template <int VPL, typename T, bool SIGMOID>
 __global__ void __launch_bounds__(kRouterWarps * 32) router_grad_kernel(RouterGradParams q) {
   const RouterParams& p = q.r;
+  extern __shared__ __align__(16) float smem[];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const RowPlace at = place_of(p, blockIdx.x);
+  float* buf = smem + warp * 32 * VPL;   // the slots' gradients by expert; zero between rows
+  const T* logits = static_cast<const T*>(p.logits);
+  const int end = at.t0 + at.n;
   float slope[VPL];            // f_e's factor of dL/dp
 #pragma unroll
   for (int i = 0; i < VPL; ++i) slope[i] = 0.0f;
+  if (q.d_w) {
+    put_row<VPL>(buf, lane, slope);
+    __syncwarp();
+  }
   if (q.counts && at.n > 0) {
     int held = 0;
     if (p.n_seg == 1) {
@@ -462,18 +551,43 @@ __global__ void __launch_bounds__(kRouterWarps * 32) router_grad_kernel(RouterGr
                         ((float)held * (float)p.k));
     }
   }
+  float next[VPL];
+  if (at.t0 + warp < end)
+    load_row<VPL, T>(logits + ((int64_t)at.rank * p.Tmax + at.t0 + warp) * p.E, p.E, lane, p.vec, next);
   for (int t = at.t0 + warp; t < at.pad_end; t += kRouterWarps) {
     const int64_t g = (int64_t)at.rank * p.Tmax + t;
     float d[VPL];
 #pragma unroll
     for (int i = 0; i < VPL; ++i) d[i] = 0.0f;
-    if (t < at.t0 + at.n) {
+    if (t < end) {
       float l[VPL], pr[VPL];
-      load_row<VPL, T>(static_cast<const T*>(p.logits) + g * p.E, p.E, lane, p.vec, l);
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) l[i] = next[i];
+      // the slots' own values are asked for before anything is computed
+      int e = -1;
+      float up = 0.0f, xl = -INFINITY;
+      if (q.d_w && lane < p.k) {
+        e = __ldg(p.idx_in + g * p.k + lane);
+        if (e < -1 || e >= p.E) {
+          atomicOr(p.err, kErrRouterIndex);
+          e = -1;
+        }
+        if (e >= 0) {
+          bool ignored = false;
+          xl = open_logit<T>((float)logits[g * p.E + e], ignored);
+          up = __ldg(q.d_w + g * p.k + lane) * p.scale;
+        }
+      }
+      if (t + kRouterWarps < end)
+        load_row<VPL, T>(logits + (g + kRouterWarps) * p.E, p.E, lane, p.vec, next);
       mask_row<VPL, T>(l, p.err);
-      raw_scores<VPL, SIGMOID>(l, pr);
-      const float total = row_sum<VPL>(pr);
-      const float inv = total > 0.0f ? 1.0f / total : 0.0f;
+      const float top = SIGMOID ? 0.0f : row_max<VPL>(l);
+      raw_scores<VPL, SIGMOID>(l, top, pr);
+      float inv = 0.0f;
+      if (q.counts || (!SIGMOID && !p.normalize)) {
+        const float total = row_sum<VPL>(pr);
+        inv = total > 0.0f ? 1.0f / total : 0.0f;
+      }
       if (q.counts) {
         float dot = 0.0f;
 #pragma unroll
@@ -484,63 +598,48 @@ __global__ void __launch_bounds__(kRouterWarps * 32) router_grad_kernel(RouterGr
           d[i] = pr[i] * inv * (SIGMOID ? 1.0f - pr[i] : 1.0f) * (slope[i] - dot);
       }
       if (q.d_w) {
-        int e = -1;
-        float up = 0.0f;
-        if (lane < p.k) {
-          e = __ldg(p.idx_in + g * p.k + lane);
-          if (e < -1 || e >= p.E) {
-            atomicOr(p.err, kErrRouterIndex);
-            e = -1;
-          }
-          if (e >= 0) up = __ldg(q.d_w + g * p.k + lane) * p.scale;
-        }
-        // raw score of the slot's expert, from the lane that holds it
-        float x = 0.0f, xl = -INFINITY;
-#pragma unroll
-        for (int i = 0; i < VPL; ++i) {
-          const int src = e >= 0 ? e / VPL : 0;
-          const float v = __shfl_sync(kFull, pr[i], src);
-          const float w = __shfl_sync(kFull, l[i], src);
-          if (e >= 0 && e % VPL == i) {
-            x = v;
-            xl = w;
-          }
-        }
         if (!(xl > -INFINITY)) e = -1;      // a masked expert has no gradient
-        float each = 0.0f, back = 0.0f;     // slot's own part; softmax over all: the rest's
+        float each = 0.0f;
         if (SIGMOID) {
+          const float x = e >= 0 ? sigmoid(xl) : 0.0f;
           if (p.normalize) {
-            const float sum = warp_sum(e >= 0 ? x : 0.0f);
+            const float sum = warp_sum(x);
             const float r = sum > 0.0f ? 1.0f / sum : 0.0f;
-            const float mean = warp_sum(e >= 0 ? x * r * up : 0.0f);
+            const float mean = warp_sum(x * r * up);
             each = (up - mean) * r * x * (1.0f - x);
           } else {
             each = up * x * (1.0f - x);
           }
         } else if (p.normalize) {
-          const float m = warp_max(e >= 0 ? xl : -INFINITY);
-          float s = e >= 0 ? expf(xl - m) : 0.0f;
-          const float sum = warp_sum(s);
-          s = sum > 0.0f ? s / sum : 0.0f;
-          const float mean = warp_sum(e >= 0 ? s * up : 0.0f);
-          each = s * (up - mean);
+          const float m = redux_max(xl);
+          float x = e >= 0 ? expf(xl - m) : 0.0f;
+          const float sum = warp_sum(x);
+          x = sum > 0.0f ? x / sum : 0.0f;
+          const float mean = warp_sum(x * up);
+          each = x * (up - mean);
         } else {
-          each = x * inv * up;
-          back = warp_sum(e >= 0 ? each : 0.0f);
-        }
-        if (e < 0) each = 0.0f;
-        if (!SIGMOID && !p.normalize) {
+          each = e >= 0 ? expf(xl - top) * inv * up : 0.0f;
+          const float back = warp_sum(each);
 #pragma unroll
           for (int i = 0; i < VPL; ++i) d[i] -= pr[i] * inv * back;
         }
-        for (int j = 0; j < p.k; ++j) {
-          const int ej = __shfl_sync(kFull, e, j);
-          const float vj = __shfl_sync(kFull, each, j);
-          const int i_of = ej - lane * VPL;
-#pragma unroll
-          for (int i = 0; i < VPL; ++i)
-            if (ej >= 0 && i == i_of) d[i] += vj;
+        // to the lanes that hold the experts; slots that name one expert twice
+        // take turns
+        const uint32_t same = __match_any_sync(kFull, e >= 0 ? e : -1 - lane);
+        if (__any_sync(kFull, same & (same - 1))) {
+          for (int j = 0; j < p.k; ++j) {
+            if (lane == j && e >= 0) buf[e] += each;
+            __syncwarp();
+          }
+        } else if (e >= 0) {
+          buf[e] = each;
         }
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) d[i] += buf[lane * VPL + i];
+        __syncwarp();
+        if (e >= 0) buf[e] = 0.0f;
+        __syncwarp();
       }
     }
     T* out = static_cast<T*>(q.d_logits) + g * p.E;
@@ -575,14 +674,10 @@ __global__ void __launch_bounds__(kRouterWarps * 32) router_grad_kernel(RouterGr
   }
 }
 
-size_t rows_smem(int E, bool balance, bool groups) {
-  if (balance) return (size_t)(kRouterWarps + 1) * E * 4;
-  return groups ? (size_t)kRouterWarps * E * 4 : 0;
-}
-
 template <int VPL, typename T, bool SIGMOID>
 cudaError_t rows_vpl(const RouterParams& p, bool select, bool balance, int grid, cudaStream_t st) {
-  const size_t smem = rows_smem(p.E, balance, p.groups > 1);
+  const size_t row = (size_t)kRouterWarps * 32 * VPL * 4;
+  const size_t smem = row + (balance ? (size_t)p.E * 4 : 0);
   if (select && balance) {
     router_rows_kernel<VPL, T, SIGMOID, true, true><<<grid, kRouterWarps * 32, smem, st>>>(p);
   } else if (select) {
@@ -595,7 +690,8 @@ cudaError_t rows_vpl(const RouterParams& p, bool select, bool balance, int grid,
 
 template <int VPL, typename T, bool SIGMOID>
 cudaError_t grad_vpl(const RouterGradParams& q, int grid, cudaStream_t st) {
-  router_grad_kernel<VPL, T, SIGMOID><<<grid, kRouterWarps * 32, 0, st>>>(q);
+  const size_t smem = q.d_w ? (size_t)kRouterWarps * 32 * VPL * 4 : 0;
+  router_grad_kernel<VPL, T, SIGMOID><<<grid, kRouterWarps * 32, smem, st>>>(q);
   return cudaGetLastError();
 }
 
@@ -687,7 +783,10 @@ ep_status plan_router(const ep_router_config* c, ep_router_handle* h) {
   h->stretch = c->seq_len > 0 && c->seq_len < T ? c->seq_len : T;
   h->stretches = (T + h->stretch - 1) / h->stretch;
   h->n_seg = c->seq_len > 0 ? c->world_size * h->stretches : 1;
-  h->rows = kRouterRows;
+  // rows of a CTA: enough CTAs to fill the GPU, few enough sums to add up
+  const int64_t all = (int64_t)c->world_size * T;
+  int64_t rows = ((all + kRouterCtas - 1) / kRouterCtas + kRouterWarps - 1) / kRouterWarps * kRouterWarps;
+  h->rows = (int)(rows < kRouterWarps ? kRouterWarps : rows > kRouterRows ? kRouterRows : rows);
   h->chunks = (h->stretch + h->rows - 1) / h->rows;
   h->total_chunks = (int64_t)c->world_size * h->stretches * h->chunks;
   h->expert_blocks = (c->num_experts + kBalanceExperts - 1) / kBalanceExperts;
@@ -736,6 +835,10 @@ ep_status fill_params(const ep_router_handle* h, const void* logits, const int32
   p->R = c.world_size; p->Tmax = c.max_num_inp_token_per_rank;
   p->E = c.num_experts; p->k = c.num_experts_per_token;
   p->groups = c.num_groups; p->topk_groups = c.topk_groups;
+  int vpl = 1;
+  while (32 * vpl < c.num_experts) vpl *= 2;
+  const int held = c.num_experts / c.num_groups, run = held / vpl;
+  p->groups_run = held % vpl == 0 && (run & (run - 1)) == 0 ? run : 0;
   p->normalize = c.normalize_weights != 0;
   p->scale = c.route_scale;
   p->stretch = h->stretch; p->stretches = h->stretches; p->chunks = h->chunks;
@@ -778,8 +881,16 @@ ep_status launch_balance(ep_router_handle* h, const RouterParams& p, int32_t* co
   b.coef = coef_of(h, p);
   b.part_p = h->part_p; b.part_n = h->part_n; b.part_loss = h->part_loss;
   b.ticket = h->ticket; b.counts = counts; b.loss = loss;
-  balance_reduce_kernel<<<dim3(h->expert_blocks, h->n_seg), 256, 0, st>>>(b);
-  const cudaError_t e = cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(h->expert_blocks, h->n_seg);
+  cfg.blockDim = dim3(kBalanceWarps * 32);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];   // set up while the rows are still being read
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, balance_reduce_kernel, b);
   return e == cudaSuccess ? EP_OK : rcuda(e);
 }
 
