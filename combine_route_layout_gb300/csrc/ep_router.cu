@@ -106,9 +106,19 @@ __device__ __forceinline__ float redux_max(float v) {
   return r;
 }
 
+// 1 / x rounded to nearest for x in [1, 2^125]: an approximation r, its exact
+// residual 1 - x r and one corrected step (Markstein's method). Equal to the
+// quotient for every such x (a test runs through all of them).
+__device__ __forceinline__ float reciprocal(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return __fmaf_rn(r, __fmaf_rn(-x, r, 1.0f), r);
+}
+
+constexpr float kSigmoidLow = -86.0f;   // 1 + exp(-l) is below 2^125 from here on
+
 // 1 / (1 + exp(-l)) with every step rounded to f32, as the definition has it:
-// the selection compares these values. (A reciprocal rounded to nearest is the
-// quotient 1 / x rounded to nearest.) -inf gives 0.
+// the selection compares these values. `reciprocal` serves l >= kSigmoidLow.
 __device__ __forceinline__ float sigmoid(float l) {
   return __frcp_rn(__fadd_rn(1.0f, expf(-l)));
 }
@@ -170,10 +180,17 @@ __device__ __forceinline__ float open_logit(float l, bool& bad) {
 
 template <int VPL, typename T>
 __device__ __forceinline__ void mask_row(float (&l)[VPL], int32_t* err) {
-  bool bad = false;
+  bool fine = true;
 #pragma unroll
-  for (int i = 0; i < VPL; ++i) l[i] = open_logit<T>(l[i], bad);
-  if (bad) atomicOr(err, kErrNotFinite);
+  for (int i = 0; i < VPL; ++i) {
+    fine = fine && l[i] < INFINITY;
+    l[i] = l[i] > lowest<T>() ? l[i] : -INFINITY;   // NaN too
+  }
+  if (!__all_sync(kFull, fine)) {
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) l[i] = l[i] < INFINITY ? l[i] : -INFINITY;
+    if (!fine) atomicOr(err, kErrNotFinite);
+  }
 }
 
 // The row's largest logit; 0 for a row with none, so that exp(-inf - 0) is 0.
@@ -189,8 +206,24 @@ __device__ __forceinline__ float row_max(const float (&l)[VPL]) {
 // p (softmax: exp(l - top), sigmoid: s) of the lane's experts, 0 where masked.
 template <int VPL, bool SIGMOID>
 __device__ __forceinline__ void raw_scores(const float (&l)[VPL], float top, float (&p)[VPL]) {
+  if (!SIGMOID) {
 #pragma unroll
-  for (int i = 0; i < VPL; ++i) p[i] = SIGMOID ? sigmoid(l[i]) : expf(l[i] - top);
+    for (int i = 0; i < VPL; ++i) p[i] = expf(l[i] - top);
+    return;
+  }
+  float least = INFINITY;    // of the logits that count
+#pragma unroll
+  for (int i = 0; i < VPL; ++i) {
+    const bool open = l[i] > -INFINITY;
+    const float v = open ? l[i] : 0.0f;
+    least = fminf(least, v);
+    const float r = reciprocal(__fadd_rn(1.0f, expf(-v)));
+    p[i] = open ? r : 0.0f;
+  }
+  if (__any_sync(kFull, least < kSigmoidLow)) {
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) p[i] = sigmoid(l[i]);
+  }
 }
 
 template <int VPL>
@@ -221,19 +254,23 @@ __device__ __forceinline__ RowPlace place_of(const RouterParams& p, int c) {
   return w;
 }
 
-// Which of the groups stay, by their two best scores (`best`, `second` on the
-// lane that asks for group `g`; `src`: the lane that answers for group j is
-// j * src).
+// Whether this lane's group is one of the topk_groups best, ties to the lowest
+// group, by its two best scores. Groups are runs of `run` lanes (a power of
+// two), whose lanes all bring the same values.
 template <bool SIGMOID>
-__device__ __forceinline__ bool group_stays(const RouterParams& p, float best, float second, int g,
-                                            int src) {
+__device__ __forceinline__ bool group_stays(const RouterParams& p, float best, float second,
+                                            int lane, int run) {
   if (SIGMOID && second > -INFINITY) best = __fadd_rn(best, second);
-  int ahead = 0;
-  for (int j = 0; j < p.groups; ++j) {
-    const float v = __shfl_sync(kFull, best, j * src);
-    ahead += v > best || (v == best && j < g);
+  bool stays = false;
+  for (int j = 0; j < p.topk_groups; ++j) {
+    const float m = redux_max(best);
+    const int win = __ffs(__ballot_sync(kFull, best == m)) - 1;
+    if ((lane ^ win) < run) {
+      stays = m > -INFINITY;
+      best = -INFINITY;
+    }
   }
-  return ahead < p.topk_groups && best > -INFINITY;
+  return stays;
 }
 
 // Drop the scores of all but the best groups, for groups that are not whole
@@ -251,7 +288,7 @@ __device__ __forceinline__ void drop_groups(const RouterParams& p, int lane, con
     }
   __syncwarp();
   const uint32_t kept =
-      __ballot_sync(kFull, group_stays<SIGMOID>(p, best, second, lane, 1) && lane < p.groups);
+      __ballot_sync(kFull, group_stays<SIGMOID>(p, best, second, lane, 1));
 #pragma unroll
   for (int i = 0; i < VPL; ++i)
     if (lane * VPL + i < p.E && !((kept >> ((lane * VPL + i) / size)) & 1u)) c[i] = -INFINITY;
@@ -294,46 +331,71 @@ __device__ __forceinline__ void select_experts(const RouterParams& p, int lane, 
       second = fmaxf(fminf(best, a), fmaxf(second, b));
       best = fmaxf(best, a);
     }
-    if (!group_stays<SIGMOID>(p, best, second, lane / run, run)) {
+    if (!group_stays<SIGMOID>(p, best, second, lane, run)) {
 #pragma unroll
       for (int i = 0; i < VPL; ++i) c[i] = -INFINITY;
     }
   }
-  int from = -1;
-  float mine = 0.0f;
+  // a lane's sorted scores wait in shared memory, the next one in `head`: a
+  // pop is one load for the lane that won
+  float* sorted = buf + 32 * VPL;
+  if (VPL > 1) {
+    put_row<VPL>(sorted, lane, c);
+    __syncwarp();
+  }
+  float head = c[0], mine = -INFINITY;
+  int from = 0, taken = 1;
+#pragma unroll 4
   for (int j = 0; j < p.k; ++j) {
-    const float m = redux_max(c[0]);
-    if (!(m > -INFINITY)) break;
-    const int win = __ffs(__ballot_sync(kFull, c[0] == m)) - 1;
+    const float m = redux_max(head);
+    const int win = __ffs(__ballot_sync(kFull, head == m)) - 1;
     if (lane == j) {
       from = win;
       mine = m;
     }
     if (lane == win) {
-#pragma unroll
-      for (int i = 0; i + 1 < VPL; ++i) c[i] = c[i + 1];
-      c[VPL - 1] = -INFINITY;
+      head = -INFINITY;
+      if (taken < VPL) head = sorted[lane * VPL + taken];
+      ++taken;
     }
   }
-  // slot j's expert: among the winner's, the one with its score; equal scores
-  // of one lane went to neighbouring slots, in the experts' order
-  int skip = 0;
+  // slot j's expert: among the winner's, the one with its score
+  const float* row = buf + from * VPL;
+  float v[VPL];
+  if (VPL % 4 == 0) {
+#pragma unroll
+    for (int i = 0; i < VPL; i += 4) {
+      const float4 f = *reinterpret_cast<const float4*>(row + i);
+      v[i] = f.x;
+      v[(i + 1) % VPL] = f.y;
+      v[(i + 2) % VPL] = f.z;
+      v[(i + 3) % VPL] = f.w;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) v[i] = row[i];
+  }
+  int at = 0;
+#pragma unroll
+  for (int i = VPL - 1; i > 0; --i)
+    if (v[i] == mine) at = i;
+  if (v[0] == mine) at = 0;
+  // equal scores of one lane went to neighbouring slots, in the experts' order
   const int from1 = __shfl_up_sync(kFull, from, 1);
   const float mine1 = __shfl_up_sync(kFull, mine, 1);
-  if (__any_sync(kFull, lane > 0 && from >= 0 && from == from1 && mine == mine1)) {
+  if (__any_sync(kFull, lane > 0 && from == from1 && mine == mine1 && mine > -INFINITY)) {
+    int skip = 0;
     for (int o = 1; o < p.k; ++o) {
       const int f = __shfl_up_sync(kFull, from, o);
-      const float v = __shfl_up_sync(kFull, mine, o);
-      skip += lane >= o && f == from && v == mine;
+      const float x = __shfl_up_sync(kFull, mine, o);
+      skip += lane >= o && f == from && x == mine;
     }
-  }
-  expert = -1;
-  score = mine;
-  if (from >= 0) {
 #pragma unroll
     for (int i = 0; i < VPL; ++i)
-      if (buf[from * VPL + i] == mine && skip-- == 0) expert = from * VPL + i;
+      if (v[i] == mine && skip-- == 0) at = i;
   }
+  expert = lane < p.k && mine > -INFINITY ? from * VPL + at : -1;
+  score = mine;
 }
 
 // SELECT: choose the experts, write indices and weights. BALANCE: sums of p
@@ -344,8 +406,9 @@ __global__ void __launch_bounds__(kRouterWarps * 32) router_rows_kernel(RouterPa
   extern __shared__ __align__(16) float smem[];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const RowPlace at = place_of(p, blockIdx.x);
-  float* buf = smem + warp * 32 * VPL;                         // a row's scores, then sums of p
-  int* cnt = reinterpret_cast<int*>(smem + kRouterWarps * 32 * VPL);
+  constexpr int kRow = (SELECT ? 2 : 1) * 32 * VPL;            // scores, sorted scores; sums of p
+  float* buf = smem + warp * kRow;
+  int* cnt = reinterpret_cast<int*>(smem + kRouterWarps * kRow);
   if (BALANCE) {
     for (int e = threadIdx.x; e < p.E; e += blockDim.x) cnt[e] = 0;
     __syncthreads();
@@ -431,7 +494,7 @@ __global__ void __launch_bounds__(kRouterWarps * 32) router_rows_kernel(RouterPa
     for (int e = threadIdx.x; e < p.E; e += blockDim.x) {
       float s = 0.0f;
 #pragma unroll
-      for (int w = 0; w < kRouterWarps; ++w) s += smem[w * 32 * VPL + e];
+      for (int w = 0; w < kRouterWarps; ++w) s += smem[w * kRow + e];
       p.part_p[(int64_t)blockIdx.x * p.E + e] = s;
       p.part_n[(int64_t)blockIdx.x * p.E + e] = cnt[e];
     }
@@ -677,14 +740,12 @@ __global__ void __launch_bounds__(kRouterWarps * 32) router_grad_kernel(RouterGr
 template <int VPL, typename T, bool SIGMOID>
 cudaError_t rows_vpl(const RouterParams& p, bool select, bool balance, int grid, cudaStream_t st) {
   const size_t row = (size_t)kRouterWarps * 32 * VPL * 4;
-  const size_t smem = row + (balance ? (size_t)p.E * 4 : 0);
-  if (select && balance) {
-    router_rows_kernel<VPL, T, SIGMOID, true, true><<<grid, kRouterWarps * 32, smem, st>>>(p);
-  } else if (select) {
-    router_rows_kernel<VPL, T, SIGMOID, true, false><<<grid, kRouterWarps * 32, smem, st>>>(p);
-  } else {
-    router_rows_kernel<VPL, T, SIGMOID, false, true><<<grid, kRouterWarps * 32, smem, st>>>(p);
-  }
+  const size_t smem = (select ? 2 * row : row) + (balance ? (size_t)p.E * 4 : 0);
+  auto kernel = select && balance ? router_rows_kernel<VPL, T, SIGMOID, true, true>
+                : select          ? router_rows_kernel<VPL, T, SIGMOID, true, false>
+                                  : router_rows_kernel<VPL, T, SIGMOID, false, true>;
+  if (smem > 48 * 1024) (void)ctas_per_sm(kernel, kRouterWarps * 32, smem);   // raises its limit
+  kernel<<<grid, kRouterWarps * 32, smem, st>>>(p);
   return cudaGetLastError();
 }
 
