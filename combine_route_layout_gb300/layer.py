@@ -12,7 +12,7 @@ from dataclasses import dataclass
 import torch
 
 from . import ep
-from .ep import EP_ERR_INVALID_ARG, EpError, _ptr
+from .ep import EP_ERR_INVALID_ARG, EpError, _check, _lib
 
 _SCORE_OF = {"softmax": ep.EP_SCORE_SOFTMAX, "sigmoid": ep.EP_SCORE_SIGMOID}
 _ACT_OF = {"none": ep.EP_ACT_NONE, "relu": ep.EP_ACT_RELU, "silu": ep.EP_ACT_SILU,
@@ -40,6 +40,7 @@ class _Op:
         skip = -raw.data_ptr() % 256
         self.workspace = raw[skip:skip + nbytes]
         self.device = self.workspace.device
+        self._device_index = self.device.index or 0
         self._destroy = destroy
         self._handle = create(self.workspace.data_ptr(), nbytes)
 
@@ -50,18 +51,32 @@ class _Op:
             self._handle = None
 
     def _stream(self):
-        return torch.cuda.current_stream(self.device).cuda_stream
+        """torch's current stream of the workspace's device, as a pointer."""
+        return _raw_stream(self._device_index)
 
-    def _need(self, t, what: str, shape, dtype, optional: bool = False) -> None:
+    def _need(self, t, what: str, shape, dtype) -> int:
+        """The address of a contiguous tensor of this shape and type on this device."""
         if t is None:
-            if not optional:
-                _refuse(f"{what} must be given")
-            return
-        if t.dtype != dtype or t.device != self.device or not t.is_contiguous() or \
-                tuple(t.shape) != tuple(shape):
+            _refuse(f"{what} must be given")
+        if t.dtype is not dtype or t.shape != shape or t.device != self.device or \
+                not t.is_contiguous():
             _refuse(f"{what} must be a contiguous {dtype} {tuple(shape)} tensor on {self.device}, "
                     f"got {t.dtype} {tuple(t.shape)} on {t.device}"
                     f"{'' if t.is_contiguous() else ' (strided)'}")
+        return t.data_ptr()
+
+    def _form(self, shape, dtype):
+        """What _new takes: a tensor of that shape that holds one element. Making a new one
+        like it costs a third of making it from a shape."""
+        return torch.empty((), dtype=dtype, device=self.device).expand(shape)
+
+
+def _new(form):
+    return torch.empty_like(form, memory_format=torch.contiguous_format)
+
+
+def _raw_stream(device_index: int) -> int:
+    return torch._C._cuda_getCurrentRawStream(device_index)
 
 
 # --------------------------------------------------------------------- router
@@ -105,60 +120,79 @@ class EpRouterOp(_Op):
         super().__init__(ep.ep_router_workspace_size(c),
                          lambda ws, n: ep.ep_router_create(c, ws, n), ep.ep_router_destroy,
                          device)
-        R, T = config.world_size, config.max_num_inp_token_per_rank
+        R, T, E = config.world_size, config.max_num_inp_token_per_rank, config.num_experts
         self.num_segments = R * -(-T // config.seq_len) if config.seq_len > 0 else 1
-        self._slots = (R, T, config.num_experts_per_token)
-        self._rows = (R, T, config.num_experts)
-        self._counts = (self.num_segments, config.num_experts)
+        self._slots = torch.Size((R, T, config.num_experts_per_token))
+        self._rows = torch.Size((R, T, E))
+        self._counts = torch.Size((self.num_segments, E))
+        self._scalar, self._bias = torch.Size(()), torch.Size((E,))
+        self._indices_form = self._form(self._slots, torch.int32)
+        self._weights_form = self._form(self._slots, torch.float32)
+        self._counts_form = self._form(self._counts, torch.int32)
+        self._loss_form = self._form((), torch.float32)
+        self._last_tokens = self._last_array = None
 
     def _tokens(self, num_tokens):
-        if num_tokens is not None and len(num_tokens) != self.config.world_size:
-            _refuse("num_tokens must give one count per source rank")
-        return num_tokens
-
-    def _new(self, shape, dtype):
-        return torch.empty(shape, dtype=dtype, device=self.device)
+        """The counts as a C array; the same counts as last time are not converted again."""
+        if num_tokens is None:
+            return None
+        if num_tokens is not self._last_array:
+            if len(num_tokens) != self.config.world_size:
+                _refuse("num_tokens must give one count per source rank")
+            values = [int(n) for n in num_tokens]
+            if values != self._last_tokens:
+                self._last_array = ep._i32_array(values)
+                self._last_tokens = values
+        return self._last_array
 
     def forward(self, logits, bias=None, num_tokens=None, balance=False):
         """(weights, indices), and with balance (weights, indices, counts, loss):
         weights [R, Tmax, k] f32 and indices [R, Tmax, k] int32 are dispatch's inputs;
         counts [segments, E] int32; loss an f32 scalar."""
-        self._need(logits, "logits", self._rows, self.config.logits_dtype)
-        self._need(bias, "bias", (self.config.num_experts,), torch.float32, optional=True)
-        indices = self._new(self._slots, torch.int32)
-        weights = self._new(self._slots, torch.float32)
-        counts = self._new(self._counts, torch.int32) if balance else None
-        loss = self._new((), torch.float32) if balance else None
-        ep.ep_router_forward(self._handle, _ptr(logits), _ptr(bias), self._tokens(num_tokens),
-                             _ptr(indices), _ptr(weights), _ptr(counts), _ptr(loss),
-                             self._stream())
-        return (weights, indices, counts, loss) if balance else (weights, indices)
+        x = self._need(logits, "logits", self._rows, self.config.logits_dtype)
+        b = None if bias is None else self._need(bias, "bias", self._bias, torch.float32)
+        tokens = self._tokens(num_tokens)
+        indices, weights = _new(self._indices_form), _new(self._weights_form)
+        if not balance:
+            _check(_lib.ep_router_forward(self._handle, x, b, tokens, indices.data_ptr(),
+                                          weights.data_ptr(), None, None, self._stream()))
+            return weights, indices
+        counts, loss = _new(self._counts_form), _new(self._loss_form)
+        _check(_lib.ep_router_forward(self._handle, x, b, tokens, indices.data_ptr(),
+                                      weights.data_ptr(), counts.data_ptr(), loss.data_ptr(),
+                                      self._stream()))
+        return weights, indices, counts, loss
 
     def balance_loss(self, logits, indices, num_tokens=None):
         """(counts, loss) of indices decided elsewhere."""
-        self._need(logits, "logits", self._rows, self.config.logits_dtype)
-        self._need(indices, "indices", self._slots, torch.int32)
-        counts, loss = self._new(self._counts, torch.int32), self._new((), torch.float32)
-        ep.ep_router_balance_loss(self._handle, _ptr(logits), _ptr(indices),
-                                  self._tokens(num_tokens), _ptr(counts), _ptr(loss),
-                                  self._stream())
+        x = self._need(logits, "logits", self._rows, self.config.logits_dtype)
+        i = self._need(indices, "indices", self._slots, torch.int32)
+        counts, loss = _new(self._counts_form), _new(self._loss_form)
+        _check(_lib.ep_router_balance_loss(self._handle, x, i, self._tokens(num_tokens),
+                                           counts.data_ptr(), loss.data_ptr(), self._stream()))
         return counts, loss
 
     def backward(self, logits, indices=None, d_weights=None, counts=None, d_loss=None,
                  num_tokens=None, out=None):
         """d_logits from d_weights (with the forward's indices), from d_loss (with the
         loss's counts), or from both."""
-        self._need(logits, "logits", self._rows, self.config.logits_dtype)
-        self._need(indices, "indices", self._slots, torch.int32, optional=d_weights is None)
-        self._need(d_weights, "d_weights", self._slots, torch.float32, optional=True)
-        self._need(counts, "counts", self._counts, torch.int32, optional=d_loss is None)
-        self._need(d_loss, "d_loss", (), torch.float32, optional=counts is None)
-        self._need(out, "out", self._rows, self.config.logits_dtype, optional=True)
+        dt = self.config.logits_dtype
+        x = self._need(logits, "logits", self._rows, dt)
+        i = w = c = d = None
+        if d_weights is not None:
+            w = self._need(d_weights, "d_weights", self._slots, torch.float32)
+        if indices is not None or w is not None:
+            i = self._need(indices, "indices", self._slots, torch.int32)
+        if counts is not None or d_loss is not None:
+            c = self._need(counts, "counts", self._counts, torch.int32)
+            d = self._need(d_loss, "d_loss", self._scalar, torch.float32)
         if out is None:
-            out = self._new(self._rows, self.config.logits_dtype)
-        ep.ep_router_backward(self._handle, _ptr(logits), _ptr(indices),
-                              self._tokens(num_tokens), _ptr(d_weights), _ptr(counts),
-                              _ptr(d_loss), _ptr(out), self._stream())
+            out = torch.empty_like(logits)
+            o = out.data_ptr()
+        else:
+            o = self._need(out, "out", self._rows, dt)
+        _check(_lib.ep_router_backward(self._handle, x, i, self._tokens(num_tokens), w, c, d, o,
+                                       self._stream()))
         return out
 
     def sync(self):
@@ -211,55 +245,65 @@ class EpLinearOp(_Op):
                          lambda ws, n: ep.ep_linear_create(c, ws, n), ep.ep_linear_destroy,
                          device)
 
-    def _rows(self, x, row_begin, row_count, row_base, num_rows):
-        """Check x and the segments; the rows that pool tensors have."""
+        G, Nw = config.num_groups, config.weight_rows
+        self._weight = torch.Size((G, Nw, config.in_features))
+        self._bias = torch.Size((G, Nw))
+        self._act_none = config.activation == "none"
+
+    def _per_group(self, t, what: str, n: int) -> int:
+        if t.dtype is not torch.int32 or t.numel() != n or t.device != self.device or \
+                not t.is_contiguous():
+            _refuse(f"{what} must hold {n} contiguous int32 on {self.device}")
+        return t.data_ptr()
+
+    def _segments(self, x, row_begin, row_count, row_base, num_rows):
+        """Check x and the segments: (rows of pool tensors, row_begin, row_count, row_base,
+        num_rows) as the C calls take them."""
         cfg = self.config
         if x is None or x.dim() != 2 or x.shape[0] > cfg.max_rows:
             _refuse("x must be [rows, in_features] with at most max_rows rows")
         rows = x.shape[0]
-        if (row_begin is None) != (row_count is None) or \
-                (row_begin is None and (cfg.num_groups != 1 or row_base is not None)):
-            _refuse("give row_begin and row_count together; only one group may go without")
-        if row_begin is not None and rows != cfg.max_rows:
+        if row_begin is None or row_count is None:
+            if row_begin is not row_count or cfg.num_groups != 1 or row_base is not None:
+                _refuse("give row_begin and row_count together; only one group may go without")
+            n = rows if num_rows is None else int(num_rows)
+            if not 0 <= n <= rows:
+                _refuse("num_rows outside [0, rows of x]")
+            return rows, None, None, None, n
+        if rows != cfg.max_rows:
             _refuse("with segments, x must hold all max_rows rows of the pool")
-        self._need(x, "x", (rows, cfg.in_features), torch.bfloat16)
-        for name, t in (("row_begin", row_begin), ("row_count", row_count)):
-            if t is not None:
-                self._need(t.reshape(-1), name, (cfg.num_groups,), torch.int32)
-                if not t.is_contiguous():
-                    _refuse(f"{name} must be contiguous")
+        base = None
         if row_base is not None:
             per = cfg.groups_per_base
             if per < 1:
                 _refuse("row_base needs groups_per_base")
-            self._need(row_base, "row_base", (-(-cfg.num_groups // per),), torch.int32)
-        n = rows if num_rows is None else int(num_rows)
-        if not 0 <= n <= rows:
-            _refuse("num_rows outside [0, rows of x]")
-        return rows, n
-
-    def _weight_shape(self):
-        cfg = self.config
-        return (cfg.num_groups, cfg.weight_rows, cfg.in_features)
+            base = self._per_group(row_base, "row_base", -(-cfg.num_groups // per))
+        return (rows, self._per_group(row_begin, "row_begin", cfg.num_groups),
+                self._per_group(row_count, "row_count", cfg.num_groups), base, 0)
 
     def forward(self, x, weight, bias=None, residual=None, row_begin=None, row_count=None,
                 row_base=None, num_rows=None, out=None, preact=None):
         """y [rows, N] (in `out` if given). `preact`: a [rows, Nw] bf16 tensor that
         receives z for the backward pass. Rows outside the segments stay as they are."""
         cfg = self.config
-        rows, n = self._rows(x, row_begin, row_count, row_base, num_rows)
-        self._need(weight, "weight", self._weight_shape(), torch.bfloat16)
-        self._need(bias, "bias", self._weight_shape()[:2], torch.float32, optional=True)
-        self._need(residual, "residual", (rows, cfg.out_features), cfg.out_dtype, optional=True)
-        self._need(out, "out", (rows, cfg.out_features), cfg.out_dtype, optional=True)
-        self._need(preact, "preact", (rows, cfg.weight_rows), torch.bfloat16, optional=True)
+        rows, begin, count, base, n = self._segments(x, row_begin, row_count, row_base, num_rows)
+        xp = self._need(x, "x", (rows, cfg.in_features), torch.bfloat16)
+        w = self._need(weight, "weight", self._weight, torch.bfloat16)
+        b = r = z = None
+        if bias is not None:
+            b = self._need(bias, "bias", self._bias, torch.float32)
+        if residual is not None:
+            r = self._need(residual, "residual", (rows, cfg.out_features), cfg.out_dtype)
+        if preact is not None:
+            z = self._need(preact, "preact", (rows, cfg.weight_rows), torch.bfloat16)
         if out is None:
             out = torch.empty((rows, cfg.out_features), dtype=cfg.out_dtype, device=self.device)
-        if rows == 0:
-            return out
-        ep.ep_linear_forward(self._handle, _ptr(x), _ptr(weight), _ptr(bias), _ptr(residual),
-                             _ptr(row_begin), _ptr(row_count), _ptr(row_base), n, _ptr(out),
-                             _ptr(preact), self._stream())
+            y = out.data_ptr()
+        else:
+            y = self._need(out, "out", (rows, cfg.out_features), cfg.out_dtype)
+        if rows:
+            _check(_lib.ep_linear_forward(self._handle, xp, w, b, r, begin, count, base, n, y, z,
+                                          self._stream()))
         return out
 
     def backward(self, dy, x, weight, preact=None, row_begin=None, row_count=None, row_base=None,
@@ -267,31 +311,38 @@ class EpLinearOp(_Op):
                  dweight=None):
         """(dx, dweight, dbias), None where not wanted. dx's rows outside the segments
         stay as they are (`dx`, `dweight`: tensors to write to)."""
-        cfg = self.config
-        rows, n = self._rows(x, row_begin, row_count, row_base, num_rows)
-        self._need(dy, "dy", (rows, cfg.out_features), cfg.out_dtype)
-        self._need(weight, "weight", self._weight_shape(), torch.bfloat16)
-        self._need(preact, "preact", (rows, cfg.weight_rows), torch.bfloat16,
-                   optional=cfg.activation == "none")
-        self._need(dx, "dx", (rows, cfg.in_features), torch.bfloat16, optional=True)
-        self._need(dweight, "dweight", self._weight_shape(), cfg.weight_grad_dtype, optional=True)
-        dev = self.device
-        if want_dx and dx is None:
-            dx = torch.empty((rows, cfg.in_features), dtype=torch.bfloat16, device=dev)
-        if want_dweight and dweight is None:
-            dweight = torch.empty(self._weight_shape(), dtype=cfg.weight_grad_dtype, device=dev)
-        dbias = torch.empty(self._weight_shape()[:2], dtype=torch.float32, device=dev) \
-            if want_dbias else None
-        dx, dweight = dx if want_dx else None, dweight if want_dweight else None
+        cfg, bf16 = self.config, torch.bfloat16
+        rows, begin, count, base, n = self._segments(x, row_begin, row_count, row_base, num_rows)
+        xp = self._need(x, "x", (rows, cfg.in_features), bf16)
+        w = self._need(weight, "weight", self._weight, bf16)
+        dyp = self._need(dy, "dy", (rows, cfg.out_features), cfg.out_dtype)
+        z = dxp = dwp = dbp = dbias = None
+        if preact is not None or not self._act_none:
+            z = self._need(preact, "preact", (rows, cfg.weight_rows), bf16)
+        if not want_dx:
+            dx = None
+        elif dx is None:
+            dx = torch.empty_like(x)
+            dxp = dx.data_ptr()
+        else:
+            dxp = self._need(dx, "dx", x.shape, bf16)
+        if not want_dweight:
+            dweight = None
+        elif dweight is None:
+            dweight = torch.empty(self._weight, dtype=cfg.weight_grad_dtype, device=self.device)
+            dwp = dweight.data_ptr()
+        else:
+            dwp = self._need(dweight, "dweight", self._weight, cfg.weight_grad_dtype)
+        if want_dbias:
+            dbias = torch.empty(self._bias, dtype=torch.float32, device=self.device)
+            dbp = dbias.data_ptr()
         if rows == 0:
             for t in (dweight, dbias):
                 if t is not None:
                     t.zero_()
-            return dx, dweight, dbias
-        if dx is not None or dweight is not None or dbias is not None:
-            ep.ep_linear_backward(self._handle, _ptr(dy), _ptr(x), _ptr(weight), _ptr(preact),
-                                  _ptr(row_begin), _ptr(row_count), _ptr(row_base), n, _ptr(dx),
-                                  _ptr(dweight), _ptr(dbias), self._stream())
+        elif dxp or dwp or dbp:
+            _check(_lib.ep_linear_backward(self._handle, dyp, xp, w, z, begin, count, base, n,
+                                           dxp, dwp, dbp, self._stream()))
         return dx, dweight, dbias
 
     def sync(self):
