@@ -37,6 +37,7 @@ constexpr int kStageBytes = kStageA + kStageB;
 constexpr int kMaxRows = 256;                    // rows of a tile (f32 outputs: half)
 constexpr int kMinCap = 64;
 constexpr int kMaxSplits = 8;
+constexpr int kLeast = 4, kLeastGrad = 16;       // stages of a part (dW's parts of a tile are 256 KB)
 // f32 outputs: the tensor core cuts off what its accumulator cannot hold, an
 // error that grows with the number of steps to the power 3/2 (7168 terms: 8e-6 of
 // the result); sums of 512 terms are added up in registers instead, which
@@ -48,6 +49,13 @@ constexpr int kTmemColumns = 512;                // two accumulators
 
 enum Mode { kForward = 0, kInputGrad = 1, kWeightGrad = 2 };
 
+// What every CTA finds out about the call from the groups' counts.
+struct Plan {
+  int tiles;
+  int cap;           // most rows of a tile
+  int splits;        // parts that a tile's contraction is cut into
+};
+
 struct MmaParams {
   LinearParams p;
   void* out;         // y, dx or dW
@@ -56,6 +64,7 @@ struct MmaParams {
   int r_tiles;       // dW: 256-row tiles of each group (else by the group's count)
   int a_blocks;      // MN-major operands: the map cuts rows into blocks of 64
   int b_blocks;      // elements, so that one box takes two of them
+  Plan plan;         // of a dense product
   float* partial;    // sums of parts: [unit][column][256 features], or NULL
   unsigned int* tickets;   // parts that are done: [tile][2], zero between calls
 };
@@ -63,12 +72,20 @@ struct MmaParams {
 struct Barriers {
   uint64_t full[kStages];     // both CTAs' operands have landed (even CTA's)
   uint64_t empty[kStages];    // this CTA's stage may be written again
-  uint64_t landed;            // dW: this CTA's last block, whose tail is cleared
+  uint64_t landed[kStages];   // dW: this CTA's last block has landed; its tail is to be cleared
   uint64_t acc_full[2];
   uint64_t acc_empty[2];      // even CTA's: both CTAs' epilogues are done
   uint32_t tmem;
   uint32_t last;              // this CTA's part of a tile was the last
 };
+
+// Count this part in; what the CTA's threads wrote before the barrier ahead of
+// this call is visible to the one that counts last, and theirs to it.
+__device__ __forceinline__ unsigned int ticket_take(unsigned int* ticket) {
+  unsigned int before;
+  asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], 1;" : "=r"(before) : "l"(ticket) : "memory");
+  return before;
+}
 
 // A barrier of the epilogue's warps; whether all of them are well.
 __device__ __forceinline__ bool epilogue_agree(bool ok) {
@@ -84,12 +101,18 @@ __device__ __forceinline__ bool epilogue_agree(bool ok) {
   return all != 0;
 }
 
-// What every CTA finds out about the call from the groups' counts.
-struct Plan {
-  int tiles;
-  int cap;           // most rows of a tile
-  int splits;        // parts that a tile's contraction is cut into
-};
+// n / d. The compiler's integer division takes about 150 cycles, and a tile's
+// place takes ten of them one after another; a float quotient is off by one at
+// most below 2^22.
+__device__ __forceinline__ int quotient(int n, int d) {
+  if (n < d) return 0;
+  if (n >= 1 << 22) return n / d;
+  int q = (int)__fdividef((float)n, (float)d);
+  const int r = n - q * d;
+  if (r < 0) --q;
+  if (r >= d) ++q;
+  return q;
+}
 
 // A part of the contraction of one tile.
 struct Tile {
@@ -103,16 +126,25 @@ struct Tile {
   int part, parts;   // its place among the tile's parts that have any
 };
 
-// Rows of a tile of a group of `count` rows: as few tiles as `cap` rows
-// allow, of about equal size.
-__device__ __forceinline__ int tile_rows(int count, int cap) {
-  const int tiles = (count + cap - 1) / cap;
-  return tiles ? ((count + tiles - 1) / tiles + 31) / 32 * 32 : 32;
+// Rows of a tile of a group of `count` rows: as few tiles as `cap` rows (a
+// power of two) allow, of about equal size, in whole steps of 32.
+__host__ __device__ __forceinline__ int tile_rows(int count, int cap, int (*div)(int, int)) {
+  const int tiles = div(count + cap - 1, cap);
+  return tiles ? (div(count + tiles - 1, tiles) + 31) / 32 * 32 : 32;
+}
+
+// Parts that contractions of `blocks` stages are cut into where `tiles` tiles
+// leave pairs idle; a part has at least `least` stages.
+__host__ __device__ __forceinline__ int splits_for(int pairs, int tiles, int blocks, int least) {
+  int n = tiles > 0 && tiles < pairs ? pairs / tiles : 1;
+  if (n > kMaxSplits) n = kMaxSplits;
+  if (n > blocks / least) n = blocks / least;
+  return n < 1 ? 1 : n;
 }
 
 __device__ __forceinline__ int tiles_in(int count, int cap) {
-  const int size = tile_rows(count, cap);
-  return (count + size - 1) / size;
+  const int size = tile_rows(count, cap, quotient);
+  return quotient(count + size - 1, size);
 }
 
 // Unit u of the plan: part u % splits of tile u / splits.
@@ -120,12 +152,13 @@ template <int MODE>
 __device__ __forceinline__ Tile tile_at(const MmaParams& q, const Plan& plan, const int* first,
                                         const int* begins, const int* counts, int u) {
   Tile w;
-  int t = u / plan.splits;
+  int t = plan.splits == 1 ? u : quotient(u, plan.splits);
   w.part = u - t * plan.splits;
   int lo = 0, hi = q.p.s.G - 1;          // the last group that starts at or before t
   if (MODE == kWeightGrad) {
-    lo = t / (q.f_tiles * q.r_tiles);
-    t -= lo * (q.f_tiles * q.r_tiles);
+    const int per = q.f_tiles * q.r_tiles;
+    lo = quotient(t, per);
+    t -= lo * per;
   } else {
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
@@ -137,109 +170,145 @@ __device__ __forceinline__ Tile tile_at(const MmaParams& q, const Plan& plan, co
   w.begin = begins[lo];
   const int count = counts[lo];
   if (MODE == kWeightGrad) {
-    w.r0 = (t / q.f_tiles) * plan.cap;
-    w.f0 = (t % q.f_tiles) * 256;
+    const int r = quotient(t, q.f_tiles);
+    w.r0 = r * plan.cap;
+    w.f0 = (t - r * q.f_tiles) * 256;
     w.rows = min(plan.cap, q.p.Nw - w.r0);
     w.n = w.rows > 128 ? 256 : 128;
     w.terms = count;
   } else {
     // 8 row tiles at a time pass over all features, so that tiles that run
     // together share operands in L2
-    const int size = tile_rows(count, plan.cap);
-    const int tiles = (count + size - 1) / size;
-    const int per = 8 * q.f_tiles;
-    const int band = t / per;
+    const int size = tile_rows(count, plan.cap, quotient);
+    const int tiles = quotient(count + size - 1, size);
+    const int band = quotient(t, 8 * q.f_tiles);
     const int in = min(8, tiles - band * 8);
-    t -= band * per;
-    w.r0 = (band * 8 + t % in) * size;
-    w.f0 = (t / in) * 256;
+    t -= band * 8 * q.f_tiles;
+    const int f = quotient(t, in);
+    w.r0 = (band * 8 + t - f * in) * size;
+    w.f0 = f * 256;
     w.rows = min(size, count - w.r0);
     w.n = (w.rows + 31) / 32 * 32;
     w.terms = MODE == kForward ? q.p.K : q.p.Nw;
   }
   const int blocks = (w.terms + kDepth - 1) / kDepth;
-  const int each = (blocks + plan.splits - 1) / plan.splits;
-  w.parts = blocks ? (blocks + each - 1) / each : 1;
-  w.kb0 = w.part * each;
-  w.kb1 = min(blocks, w.kb0 + each);
+  w.parts = 1;
+  w.kb0 = 0;
+  w.kb1 = blocks;
+  if (plan.splits > 1) {
+    const int each = quotient(blocks + plan.splits - 1, plan.splits);
+    w.parts = blocks ? quotient(blocks + each - 1, each) : 1;
+    w.kb0 = w.part * each;
+    w.kb1 = min(blocks, w.kb0 + each);
+  }
   return w;
 }
 
+// Whether stage kb is dW's last and ends inside a 16-term step.
+template <int MODE>
+__device__ __forceinline__ bool has_tail(const Tile& w, int kb) {
+  const int valid = w.terms - kb * kDepth;
+  return MODE == kWeightGrad && valid < kDepth && (valid & 15);
+}
+
 // The groups' segments, the size of the tiles and the first tile of each
-// group. All threads of the CTA.
+// group. All threads of the CTA. (A dense product's plan comes from the host.)
 //
 // Where the tiles of 256 rows are fewer than half the pairs, tiles of 128 and
 // then 64 rows use more of the SMs at the cost of reading the weights more
 // often; what is still idle then takes parts of the tiles' contractions, whose
 // f32 sums the last part to finish adds up. 1024 x 7168 x 256: 43.7 us as 4
-// tiles of 256 rows, against 16 tiles of 64 rows in 4 parts each.
+// tiles of 256 rows, 27.5 us as 16 tiles of 64 rows in 4 parts each.
 template <int MODE>
 __device__ Plan plan_tiles(const MmaParams& q, int base_cap, int* first, int* begins, int* counts) {
   __shared__ int sums[3][kThreads / 32];
+  if (!q.p.s.begin) {
+    if (threadIdx.x == 0) {
+      first[0] = begins[0] = 0;
+      counts[0] = (int)q.p.s.dense_rows;
+    }
+    __syncthreads();
+    return q.plan;
+  }
   const int G = q.p.s.G, pairs = gridDim.x >> 1;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int per = (G + kThreads - 1) / kThreads;
   const int g0 = threadIdx.x * per, g1 = min(G, g0 + per);
   Plan plan;
   plan.cap = base_cap;
-  int mine[3] = {0, 0, 0};               // tiles of cap, cap / 2, cap / 4 rows; dW: largest count
+  int n0 = 0, n1 = 0, n2 = 0;            // tiles of cap, cap / 2, cap / 4 rows; dW: largest count
   for (int g = g0; g < g1; ++g) {
     int64_t b, c;
     segment_of(q.p.s, g, b, c);
     begins[g] = (int)b;
     counts[g] = (int)c;
     if (MODE == kWeightGrad) {
-      mine[0] = max(mine[0], (int)c);
+      n0 = max(n0, (int)c);
     } else {
-#pragma unroll
-      for (int i = 0; i < 3; ++i) mine[i] += tiles_in((int)c, base_cap >> i) * q.f_tiles;
+      n0 += tiles_in((int)c, base_cap) * q.f_tiles;
+      n1 += tiles_in((int)c, base_cap / 2) * q.f_tiles;
+      n2 += tiles_in((int)c, base_cap / 4) * q.f_tiles;
     }
   }
+  int s0 = n0, s1 = n1, s2 = n2;
 #pragma unroll
-  for (int i = 0; i < 3; ++i) {
-    int v = mine[i];
-#pragma unroll
-    for (int o = 16; o; o >>= 1) {
-      const int x = __shfl_xor_sync(kFull, v, o);
-      v = MODE == kWeightGrad ? max(v, x) : v + x;
+  for (int o = 16; o; o >>= 1) {
+    const int x = __shfl_xor_sync(kFull, s0, o);
+    s0 = MODE == kWeightGrad ? max(s0, x) : s0 + x;
+    if (MODE != kWeightGrad) {
+      s1 += __shfl_xor_sync(kFull, s1, o);
+      s2 += __shfl_xor_sync(kFull, s2, o);
     }
-    if (lane == 0) sums[i][warp] = v;
+  }
+  if (lane == 0) {
+    sums[0][warp] = s0;
+    sums[1][warp] = s1;
+    sums[2][warp] = s2;
   }
   __syncthreads();
-  int total[3] = {0, 0, 0};
-  for (int w = 0; w < kThreads / 32; ++w)
-#pragma unroll
-    for (int i = 0; i < 3; ++i)
-      total[i] = MODE == kWeightGrad ? max(total[i], sums[i][w]) : total[i] + sums[i][w];
-  int blocks, least;
   if (MODE == kWeightGrad) {
-    plan.tiles = G * q.f_tiles * q.r_tiles;
-    blocks = (total[0] + kDepth - 1) / kDepth;
-    least = 16;                          // a part's sums of a whole 256 x 256 tile are 256 KB
-  } else {
-    int i = 0;
-    while (i < 2 && 2 * total[i] <= pairs && (base_cap >> i) > kMinCap) ++i;
-    plan.cap = base_cap >> i;
-    plan.tiles = total[i];
-    blocks = ((MODE == kForward ? q.p.K : q.p.Nw) + kDepth - 1) / kDepth;
-    least = 4;
-    // tiles before this thread's groups: an exclusive scan over the threads
-    int incl = mine[i];
+    int most = 0;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int v = __shfl_up_sync(kFull, incl, o);
-      if (lane >= o) incl += v;
-    }
-    int before = incl - mine[i];
-    for (int w = 0; w < warp; ++w) before += sums[i][w];
-    for (int g = g0; g < g1; ++g) {
-      first[g] = before;
-      before += tiles_in(counts[g], plan.cap) * q.f_tiles;
+    for (int w = 0; w < kThreads / 32; ++w) most = max(most, sums[0][w]);
+    plan.tiles = G * q.f_tiles * q.r_tiles;
+    plan.splits = splits_for(pairs, plan.tiles, (most + kDepth - 1) / kDepth, kLeastGrad);
+    return plan;
+  }
+  s0 = s1 = s2 = 0;
+#pragma unroll
+  for (int w = 0; w < kThreads / 32; ++w) {
+    s0 += sums[0][w];
+    s1 += sums[1][w];
+    s2 += sums[2][w];
+  }
+  int level = 0, mine = n0;
+  plan.tiles = s0;
+  if (2 * s0 <= pairs) {
+    level = 1;
+    mine = n1;
+    plan.tiles = s1;
+    if (2 * s1 <= pairs && base_cap / 2 > kMinCap) {
+      level = 2;
+      mine = n2;
+      plan.tiles = s2;
     }
   }
-  plan.splits = 1;
-  if (q.partial && plan.tiles > 0)
-    plan.splits = max(1, min(min(pairs / plan.tiles, kMaxSplits), blocks / least));
+  plan.cap = base_cap >> level;
+  plan.splits = splits_for(pairs, plan.tiles,
+                           ((MODE == kForward ? q.p.K : q.p.Nw) + kDepth - 1) / kDepth, kLeast);
+  // tiles before this thread's groups: an exclusive scan over the threads
+  int incl = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(kFull, incl, o);
+    if (lane >= o) incl += v;
+  }
+  int before = incl - mine;
+  for (int w = 0; w < warp; ++w) before += sums[level][w];
+  for (int g = g0; g < g1; ++g) {
+    first[g] = before;
+    before += tiles_in(counts[g], plan.cap) * q.f_tiles;
+  }
   __syncthreads();
   return plan;
 }
@@ -358,8 +427,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     for (int s = 0; s < kStages; ++s) {
       mbar_init(&bar->full[s], 2);       // each CTA's producer
       mbar_init(&bar->empty[s], 1);
+      mbar_init(&bar->landed[s], 1);
     }
-    mbar_init(&bar->landed, 1);
     for (int a = 0; a < 2; ++a) {
       mbar_init(&bar->acc_full[a], 1);
       mbar_init(&bar->acc_empty[a], 2 * kEpilogueWarps);  // of both CTAs
@@ -368,19 +437,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     tma_prefetch_map(&maps.a);
     tma_prefetch_map(&maps.b[0]);
   }
+  __syncthreads();
+  cluster_arrive();                      // the barriers are ready; the wait is below
   if (warp == 1) tmem_alloc(&bar->tmem, kTmemColumns);
   const Plan plan = plan_tiles<MODE>(q, kChunked ? kMaxRows / 2 : kMaxRows, first, begins, counts);
   const int units = plan.tiles * plan.splits;
   tc_fence_before();
-  cluster_sync();
+  __syncthreads();                       // the TMEM address is there
   tc_fence_after();
+  cluster_wait();
   const uint32_t tmem = bar->tmem;
   const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
 
-  if (warp == 0) {
-    // ------------------------------------------------ producer
-    int it = 0, s = 0;               // stages written so far, the ring's place
-    uint32_t phase = 1, landed_phase = 0;   // the first pass over the ring waits for nothing
+  if (warp == 0 && elect_one()) {
+    // ------------------------------------------------ producer: one thread
+    int it = 0, s = 0;                      // stages written so far, the ring's place
+    uint32_t phase = 1;                     // the first pass over the ring waits for nothing
+    const uint32_t full0 = in_cta(&bar->full[0], 0), empty0 = in_cta(&bar->empty[0], 1);
     bool ok = true;
     for (int u = pair; u < units && ok; u += pairs) {
       const Tile w = tile_at<MODE>(q, plan, first, begins, counts, u);
@@ -391,72 +464,50 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const uint32_t bytes = kStageA + (MODE != kWeightGrad || q.b_blocks ? kStageB >> box
                                                                           : half / 64 * 8192);
       const CUtensorMap* map_b = &maps.b[box];
-      for (int kb = w.kb0; kb < w.kb1 && ok; ++kb, ++it) {
+      for (int kb = w.kb0; kb < w.kb1; ++kb, ++it) {
         if (it >= kStages) {
-          ok = warp_wait(&bar->empty[s], phase);
+          ok = mbar_wait_soon(&bar->empty[s], phase);
           if (!ok) break;
-          if (cta == 0 && elect_one()) mbar_signal_at(in_cta(&bar->empty[s], 1));
+          if (cta == 0) mbar_signal_at(empty0 + s * 8);
         }
         uint8_t* a = ring + s * kStageBytes;
         uint8_t* b = a + kStageA;
         const int d = kb * kDepth;
-        const int valid = w.terms - d;                          // terms of this block
-        const bool tail = MODE == kWeightGrad && valid < kDepth && (valid & 15);
-        const uint32_t full = in_cta(&bar->full[s], 0);
-        const uint32_t on = tail ? smem_addr(&bar->landed) : full;
-        if (elect_one()) {
-          if (tail) {
-            mbar_arrive_expect_tx(&bar->landed, bytes);
-          } else {
-            mbar_signal_expect_tx_at(full, bytes);
-          }
-          const int row = (int)w.begin + d;                     // dW: contraction row
-          if (MODE == kForward) {
-            if (kGated) {
-              tma_load_4d(a, &maps.a, d, 0, fc / 2, w.g, on);
-            } else {
-              tma_load_3d(a, &maps.a, d, fc, w.g, on);
-            }
-          } else if (MODE == kInputGrad) {
-            if (q.a_blocks) {
-              tma_load_4d(a, &maps.a, 0, d, fc / 64, w.g, on);
-            } else {
-              tma_load_3d(a, &maps.a, fc, d, w.g, on);
-              tma_load_3d(a + 8192, &maps.a, fc + 64, d, w.g, on);
-            }
-          } else if (q.a_blocks) {
-            tma_load_3d(a, &maps.a, 0, row, fc / 64, on);
-          } else {
-            tma_load_2d(a, &maps.a, fc, row, on);
-            tma_load_2d(a + 8192, &maps.a, fc + 64, row, on);
-          }
-          if (MODE != kWeightGrad) {
-            tma_load_2d(b, map_b, d, (int)w.begin + rc, on);
-          } else if (q.b_blocks) {
-            tma_load_3d(b, map_b, 0, row, rc / 64, on);
-          } else {
-            tma_load_2d(b, map_b, rc, row, on);
-            if (half == 128) tma_load_2d(b + 8192, map_b, rc + 64, row, on);
-          }
+        const int row = (int)w.begin + d;                       // dW: contraction row
+        uint32_t on = full0 + s * 8;
+        if (has_tail<MODE>(w, kb)) {
+          on = smem_addr(&bar->landed[s]);
+          mbar_arrive_expect_tx(&bar->landed[s], bytes);
+        } else {
+          mbar_signal_expect_tx_at(on, bytes);
         }
-        if (tail) {
-          // the rows after the segment's last belong to somebody else: clear
-          // those that the last 16-term step would take in
-          ok = warp_wait(&bar->landed, landed_phase);
-          landed_phase ^= 1;
-          const int end = (valid + 15) / 16 * 16;
-          const int n16 = 4 * (end - valid) * 8;                // 16-byte pieces
-          for (int i = lane; i < n16; i += 32) {
-            const int row = valid + i / 8 % (end - valid);
-            const int part = i / 8 / (end - valid);             // 64 columns of a or b
-            uint8_t* at = a + part * 8192 + row * 128;
-            reinterpret_cast<uint4*>(at)[i & 7] = make_uint4(0, 0, 0, 0);
+        if (MODE == kForward) {
+          if (kGated) {
+            tma_load_4d(a, &maps.a, d, 0, fc / 2, w.g, on);
+          } else {
+            tma_load_3d(a, &maps.a, d, fc, w.g, on);
           }
-          fence_async_shared();
-          __syncwarp();
-          if (lane == 0) mbar_arrive_at(full);
+        } else if (MODE == kInputGrad) {
+          if (q.a_blocks) {
+            tma_load_4d(a, &maps.a, 0, d, fc / 64, w.g, on);
+          } else {
+            tma_load_3d(a, &maps.a, fc, d, w.g, on);
+            tma_load_3d(a + 8192, &maps.a, fc + 64, d, w.g, on);
+          }
+        } else if (q.a_blocks) {
+          tma_load_3d(a, &maps.a, 0, row, fc / 64, on);
+        } else {
+          tma_load_2d(a, &maps.a, fc, row, on);
+          tma_load_2d(a + 8192, &maps.a, fc + 64, row, on);
         }
-        __syncwarp();
+        if (MODE != kWeightGrad) {
+          tma_load_2d(b, map_b, d, (int)w.begin + rc, on);
+        } else if (q.b_blocks) {
+          tma_load_3d(b, map_b, 0, row, rc / 64, on);
+        } else {
+          tma_load_2d(b, map_b, rc, row, on);
+          if (half == 128) tma_load_2d(b + 8192, map_b, rc + 64, row, on);
+        }
         if (++s == kStages) {
           s = 0;
           phase ^= 1;
@@ -464,72 +515,101 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
     }
     if (!ok) {
-      if (lane == 0) atomicOr(timeout, kErrLinearTimeout);
-      if (cta == 0)   // copies in flight must land before the CTA leaves
-        for (int s = 0; s < kStages && s < it; ++s)
-          (void)mbar_wait_cluster(&bar->full[s], ((it - 1 - s) / kStages) & 1);
+      atomicOr(timeout, kErrLinearTimeout);
+      // copies in flight must land before the CTAs leave
+      for (int i = 0; i < kStages && i < it; ++i) {
+        s = s == 0 ? kStages - 1 : s - 1;
+        (void)mbar_wait(&bar->full[s], ((it - 1 - i) / kStages) & 1);
+      }
     }
-  } else if (warp == 1) {
-    // ------------------------------------------------ MMA (even CTA's warp, one lane issues)
-    if (cta == 0) {
-      // operands of stage 0; a stage is kStageBytes on, 16 terms are 32 bytes
-      // of a row (K-major) or 16 rows (MN-major) on
-      constexpr bool kMnA = MODE != kForward, kMnB = MODE == kWeightGrad;
-      constexpr uint32_t kStepA = (kMnA ? 2048 : 32) >> 4, kStepB = (kMnB ? 2048 : 32) >> 4;
-      const uint64_t a0 = smem_operand(smem_addr(ring), kMnA ? 8192 : 16);
-      const uint64_t b0 = smem_operand(smem_addr(ring) + kStageA, kMnB ? 8192 : 16);
-      int n_acc = 0, s = 0;
-      uint32_t phase = 0;
-      bool ok = true;
-      Tile next;
-      if (pair < units) next = tile_at<MODE>(q, plan, first, begins, counts, pair);
-      for (int u = pair; u < units && ok; u += pairs) {
-        const Tile w = next;
-        const uint32_t form = mma_form(w.n, kMnA, kMnB);
-        int stop = w.kb0;                  // end of the accumulator's sum
-        for (int kb = w.kb0; kb < w.kb1; ++kb) {
-          const int acc = n_acc & 1;
-          const bool fresh = kb == stop;
-          if (fresh) {
-            stop = kChunked ? min(w.kb1, kb + kChunk32) : w.kb1;
-            if (n_acc >= 2) {
-              ok = warp_wait_cluster(&bar->acc_empty[acc], ((n_acc >> 1) - 1) & 1);
-              if (!ok) break;
-              tc_fence_after();
-            }
+  } else if (warp == 1 && cta == 0 && elect_one()) {
+    // ------------------------------------------------ MMA: one thread of the even CTA
+    // operands of stage 0; a stage is kStageBytes on, 16 terms are 32 bytes of
+    // a row (K-major) or 16 rows (MN-major) on
+    constexpr bool kMnA = MODE != kForward, kMnB = MODE == kWeightGrad;
+    constexpr uint32_t kStepA = (kMnA ? 2048 : 32) >> 4, kStepB = (kMnB ? 2048 : 32) >> 4;
+    const uint64_t a0 = smem_operand(smem_addr(ring), kMnA ? 8192 : 16);
+    const uint64_t b0 = smem_operand(smem_addr(ring) + kStageA, kMnB ? 8192 : 16);
+    int n_acc = 0, s = 0;
+    uint32_t phase = 0;
+    bool ok = true, ready = false;         // ready: the stage was seen to be full
+    Tile next;
+    if (pair < units) next = tile_at<MODE>(q, plan, first, begins, counts, pair);
+    for (int u = pair; u < units && ok; u += pairs) {
+      const Tile w = next;
+      const uint32_t form = mma_form(w.n, kMnA, kMnB);
+      int stop = w.kb0;                    // end of the accumulator's sum
+      for (int kb = w.kb0; kb < w.kb1; ++kb) {
+        const bool fresh = kb == stop;
+        if (fresh) {
+          stop = kChunked ? min(w.kb1, kb + kChunk32) : w.kb1;
+          if (n_acc >= 2) {
+            ok = mbar_wait_soon(&bar->acc_empty[n_acc & 1], ((n_acc >> 1) - 1) & 1);
+            if (!ok) break;
+            tc_fence_after();
           }
-          const int left = w.terms - kb * kDepth;
-          // dW's last block holds rows that the producers cleared
-          ok = MODE == kWeightGrad && left <= kDepth ? warp_wait_cluster(&bar->full[s], phase)
-                                                     : warp_wait(&bar->full[s], phase);
-          if (!ok) break;
-          tc_fence_after();
-          const uint32_t d = tmem + acc * 256;
-          const uint64_t a = a0 + (uint32_t)(s * (kStageBytes >> 4));
-          const uint64_t b = b0 + (uint32_t)(s * (kStageBytes >> 4));
-          if (elect_one()) {
-            mma_pair(d, a, b, form, !fresh);
-            if (left > 16) mma_pair(d, a + kStepA, b + kStepB, form, true);
-            if (left > 32) mma_pair(d, a + 2 * kStepA, b + 2 * kStepB, form, true);
-            if (left > 48) mma_pair(d, a + 3 * kStepA, b + 3 * kStepB, form, true);
-            mma_commit(&bar->empty[s]);
-            if (kb + 1 == stop) mma_commit(&bar->acc_full[acc]);
-          }
-          __syncwarp();
-          if (kb + 1 == stop) ++n_acc;
-          if (++s == kStages) {
-            s = 0;
-            phase ^= 1;
-          }
-          // the next unit is worked out under this one's products
-          if (kb == w.kb0 && u + pairs < units)
-            next = tile_at<MODE>(q, plan, first, begins, counts, u + pairs);
         }
-        if (w.kb0 >= w.kb1 && u + pairs < units)
+        const int left = w.terms - kb * kDepth;
+        if (has_tail<MODE>(w, kb)) {       // rows that both CTAs cleared
+          ok = mbar_wait_cluster(&bar->full[s], phase);
+        } else if (!ready) {
+          ok = mbar_wait_soon(&bar->full[s], phase);
+        }
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t d = tmem + (n_acc & 1) * 256;
+        const uint64_t a = a0 + (uint32_t)(s * (kStageBytes >> 4));
+        const uint64_t b = b0 + (uint32_t)(s * (kStageBytes >> 4));
+        uint64_t* emptied = &bar->empty[s];
+        if (++s == kStages) {
+          s = 0;
+          phase ^= 1;
+        }
+        ready = mbar_test(&bar->full[s], phase);   // its answer comes under the MMAs
+        mma_pair(d, a, b, form, !fresh);
+        if (left > 16) mma_pair(d, a + kStepA, b + kStepB, form, true);
+        if (left > 32) mma_pair(d, a + 2 * kStepA, b + 2 * kStepB, form, true);
+        if (left > 48) mma_pair(d, a + 3 * kStepA, b + 3 * kStepB, form, true);
+        mma_commit(emptied);
+        if (kb + 1 == stop) {
+          mma_commit(&bar->acc_full[n_acc & 1]);
+          ++n_acc;
+        }
+        // the next unit is worked out under this one's products
+        if (kb == w.kb0 && u + pairs < units)
           next = tile_at<MODE>(q, plan, first, begins, counts, u + pairs);
       }
-      if (!ok && lane == 0) atomicOr(timeout, kErrLinearTimeout);
+      if (w.kb0 >= w.kb1 && u + pairs < units)
+        next = tile_at<MODE>(q, plan, first, begins, counts, u + pairs);
     }
+    if (!ok) atomicOr(timeout, kErrLinearTimeout);
+  } else if (MODE == kWeightGrad && warp == 2) {
+    // ------------------------------------------------ clears the rows past a segment's last
+    // that the last 16-term step of its last stage would take in: they belong
+    // to somebody else, and may hold anything
+    int it = 0;
+    uint32_t tails = 0;      // parity of the tails that each of the ring's places has had
+    bool ok = true;
+    for (int u = pair; u < units && ok; u += pairs) {
+      const Tile w = tile_at<MODE>(q, plan, first, begins, counts, u);
+      if (w.kb0 >= w.kb1) continue;
+      it += w.kb1 - w.kb0;
+      if (!has_tail<MODE>(w, w.kb1 - 1)) continue;
+      const int s = (it - 1) % kStages;
+      ok = warp_wait(&bar->landed[s], (tails >> s) & 1);
+      if (!ok) break;
+      tails ^= 1u << s;
+      const int valid = w.terms - (w.kb1 - 1) * kDepth, more = (valid + 15) / 16 * 16 - valid;
+      uint8_t* stage = ring + s * kStageBytes;
+      for (int i = lane; i < 4 * more * 8; i += 32) {           // 16-byte pieces
+        const int part = i / (more * 8), row = valid + (i / 8 - part * more);
+        reinterpret_cast<uint4*>(stage + part * 8192 + row * 128)[i & 7] = make_uint4(0, 0, 0, 0);
+      }
+      fence_async_shared();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_at(in_cta(&bar->full[s], 0));
+    }
+    if (!ok && lane == 0) atomicOr(timeout, kErrLinearTimeout);
   } else if (warp >= 4) {
     // ------------------------------------------------ epilogue
     // 64 columns of the tile belong to the warp pair of a quarter: 32 to this
@@ -579,9 +659,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       float keep[kChunked ? 2 : 1][32];
       for (int i = 0; i < chunks && ok; ++i, ++n_acc) {
         const int acc = n_acc & 1;
-        ok = warp_wait_cluster(&bar->acc_full[acc], (n_acc >> 1) & 1);
+        ok = warp_wait(&bar->acc_full[acc], (n_acc >> 1) & 1);
         if (!ok) break;
-        if (cta == 0 && threadIdx.x == 128) mbar_arrive_at(in_cta(&bar->acc_full[acc], 1));
+        if (cta == 0 && threadIdx.x == 128) mbar_signal_at(in_cta(&bar->acc_full[acc], 1));
         tc_fence_after();
         if (kChunked) {
 #pragma unroll
@@ -602,7 +682,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive_at(in_cta(&bar->acc_empty[acc], 0));
+        if (lane == 0) mbar_signal_at(in_cta(&bar->acc_empty[acc], 0));
       }
       if (kChunked && ok) {
 #pragma unroll
@@ -613,12 +693,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       // the tile's last part to get here adds all of them, in their order
       if (!epilogue_agree(ok)) break;
       if (threadIdx.x == 128) {
-        __threadfence();
-        unsigned int* ticket = q.tickets + (u / plan.splits) * 2 + cta;
-        const bool last = atomicAdd(ticket, 1u) == (unsigned)w.parts - 1;
+        unsigned int* ticket = q.tickets + quotient(u, plan.splits) * 2 + cta;
+        const bool last = ticket_take(ticket) == (unsigned)w.parts - 1;
         if (last) *ticket = 0u;
         bar->last = last;
-        __threadfence();
       }
       (void)epilogue_agree(true);
       if (!bar->last) continue;
@@ -627,8 +705,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         float r[32];
 #pragma unroll
         for (int c = 0; c < 32; ++c) r[c] = 0.0f;
-        for (int part = 0; part < w.parts; ++part) {
-          const float* at = from + ((int64_t)part * plan.cap + c0) * 256;
+        const float* at = from + c0 * 256;
+#pragma unroll 4
+        for (int part = 0; part < w.parts; ++part, at += plan.cap * 256) {
 #pragma unroll
           for (int c = 0; c < 32; ++c)
             if (c0 + c < w.rows) r[c] += __ldcg(at + c * 256);
@@ -726,6 +805,27 @@ int grid_of(int sms, int64_t tiles) {
   return (int)(2 * (pairs < 1 ? 1 : pairs));
 }
 
+int host_quotient(int n, int d) { return n / d; }
+
+// plan_tiles for a dense product, whose rows the host knows.
+Plan dense_plan(int64_t rows64, int base_cap, int f_tiles, int blocks, int pairs) {
+  const int rows = (int)rows64;
+  Plan plan;
+  plan.cap = base_cap;
+  for (int level = 0;; ++level) {
+    const int size = tile_rows(rows, base_cap >> level, host_quotient);
+    plan.cap = base_cap >> level;
+    plan.tiles = (rows + size - 1) / size * f_tiles;
+    if (2 * plan.tiles > pairs || plan.cap <= kMinCap) break;
+  }
+  plan.splits = splits_for(pairs, plan.tiles, blocks, kLeast);
+  return plan;
+}
+
+Plan dense_grad_plan(int64_t rows, int cap, int tiles, int pairs) {
+  return Plan{tiles, cap, splits_for(pairs, tiles, (int)((rows + kDepth - 1) / kDepth), kLeastGrad)};
+}
+
 // Upper bound of the units of all groups (their counts are on the device).
 int64_t most_units(const LinearParams& p, int f_tiles, int terms) {
   const int64_t rows = p.s.begin ? p.s.pool : p.s.dense_rows;
@@ -772,6 +872,8 @@ cudaError_t launch_linear_forward(const LinearParams& p, int sms, cudaStream_t s
   if (!ok || !map_k_major(m.b, p.x, p.K, rows, p.K)) return cudaErrorInvalidValue;
   q.a_blocks = q.b_blocks = 0;
   const int grid = grid_of(sms, most_units(p, q.f_tiles, p.K));
+  q.plan = dense_plan(p.s.dense_rows, p.y_f32 ? kMaxRows / 2 : kMaxRows, q.f_tiles,
+                      (p.K + kDepth - 1) / kDepth, grid / 2);
   return p.y_f32 ? launch_forward<float>(m, q, grid, st)
                  : launch_forward<__nv_bfloat16>(m, q, grid, st);
 }
@@ -792,8 +894,9 @@ cudaError_t launch_linear_input_grad(const LinearParams& p, int sms, cudaStream_
   if (!map_mn_major(&m.a, p.w, p.K, p.Nw, p.K, p.s.G, q.a_blocks) ||
       !map_k_major(m.b, p.dz, p.Nw, rows, p.ldz))
     return cudaErrorInvalidValue;
-  return launch_tiles<kInputGrad, EP_ACT_NONE, __nv_bfloat16>(
-      m, q, grid_of(sms, most_units(p, q.f_tiles, p.Nw)), st);
+  const int grid = grid_of(sms, most_units(p, q.f_tiles, p.Nw));
+  q.plan = dense_plan(p.s.dense_rows, kMaxRows, q.f_tiles, (p.Nw + kDepth - 1) / kDepth, grid / 2);
+  return launch_tiles<kInputGrad, EP_ACT_NONE, __nv_bfloat16>(m, q, grid, st);
 }
 
 cudaError_t launch_linear_weight_grad(const LinearParams& p, int sms, cudaStream_t st) {
@@ -818,6 +921,7 @@ cudaError_t launch_linear_weight_grad(const LinearParams& p, int sms, cudaStream
   for (int i = 1; i < 4; ++i) m.b[i] = m.b[0];
   const int64_t units = (int64_t)p.s.G * q.f_tiles * q.r_tiles * kMaxSplits;
   const int grid = grid_of(sms, units);
+  q.plan = dense_grad_plan(p.s.dense_rows, cap, q.f_tiles * q.r_tiles, grid / 2);
   return p.dw_f32 ? launch_tiles<kWeightGrad, EP_ACT_NONE, float>(m, q, grid, st)
                   : launch_tiles<kWeightGrad, EP_ACT_NONE, __nv_bfloat16>(m, q, grid, st);
 }

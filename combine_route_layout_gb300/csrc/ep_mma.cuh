@@ -7,8 +7,7 @@
 
 namespace ep {
 
-// One lane of a converged warp, the same at every call: what it issues, the
-// compiler takes from warp-uniform registers.
+// One lane of a converged warp.
 __device__ __forceinline__ bool elect_one() {
   uint32_t p;
   asm volatile(
@@ -28,6 +27,13 @@ __device__ __forceinline__ uint32_t cluster_rank() {
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::
                    : "memory");
+}
+
+__device__ __forceinline__ void cluster_arrive() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
 // The address of this CTA's `p` in CTA `rank` of the cluster.
@@ -80,19 +86,31 @@ __device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity
   return false;
 }
 
-// The same for a whole warp, which agrees on the answer (a lane alone that gave
-// up would leave the others in their next warp-wide step). No look at the clock
-// on the first polls.
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
-  bool ok = false;
-#pragma unroll 1
-  for (int i = 0; i < 64 && !ok; ++i) ok = mbar_try_wait(bar, parity);
-  if (!ok) ok = mbar_wait(bar, parity);
-  return __all_sync(0xFFFFFFFFu, ok);
+// Whether the phase is complete, without waiting.
+__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n .reg .pred p;\n"
+      " mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+      " selp.u32 %0, 1, 0, p;\n}"
+      : "=r"(done)
+      : "r"(smem_addr(bar)), "r"(parity)
+      : "memory");
+  return done != 0;
 }
 
-__device__ __forceinline__ bool warp_wait_cluster(uint64_t* bar, uint32_t parity) {
-  return __all_sync(0xFFFFFFFFu, mbar_wait_cluster(bar, parity));
+// mbar_wait without a look at the clock on the first polls.
+__device__ __forceinline__ bool mbar_wait_soon(uint64_t* bar, uint32_t parity) {
+#pragma unroll 1
+  for (int i = 0; i < 64; ++i)
+    if (mbar_try_wait(bar, parity)) return true;
+  return mbar_wait(bar, parity);
+}
+
+// The same for a whole warp, which agrees on the answer: a lane alone that gave
+// up would leave the others in their next warp-wide step.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
+  return __all_sync(0xFFFFFFFFu, mbar_wait_soon(bar, parity));
 }
 
 __device__ __forceinline__ void fence_async_shared() {
