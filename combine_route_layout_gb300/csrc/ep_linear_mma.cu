@@ -101,16 +101,17 @@ __device__ __forceinline__ bool epilogue_agree(bool ok) {
   return all != 0;
 }
 
-// n / d. The compiler's integer division takes about 150 cycles, and a tile's
-// place takes ten of them one after another; a float quotient is off by one at
-// most below 2^22.
+// n / d for 0 <= n, 0 < d below 2^31, in two float steps. The compiler's integer
+// division is longer, and a tile's place takes ten of them one after another.
 __device__ __forceinline__ int quotient(int n, int d) {
-  if (n < d) return 0;
-  if (n >= 1 << 22) return n / d;
-  int q = (int)__fdividef((float)n, (float)d);
-  const int r = n - q * d;
-  if (r < 0) --q;
-  if (r >= d) ++q;
+  const float r = __fdividef(1.0f, (float)d);
+  int q = (int)((float)n * r);              // off by 2^-21 of itself at most
+  int left = n - q * d;
+  const int more = (int)floorf((float)left * r);   // off by one at most
+  q += more;
+  left -= more * d;
+  if (left < 0) --q;
+  if (left >= d) ++q;
   return q;
 }
 
@@ -318,9 +319,25 @@ __device__ __forceinline__ void put(__nv_bfloat16* at, float v) { *at = __float2
 __device__ __forceinline__ float get(const float* at) { return *at; }
 __device__ __forceinline__ float get(const __nv_bfloat16* at) { return __bfloat162float(*at); }
 
+// An accumulator's sum is there (the even CTA passes the news on), and has
+// been read.
+__device__ __forceinline__ bool accumulator_ready(Barriers* bar, int acc, int n_acc, int cta) {
+  if (!warp_wait(&bar->acc_full[acc], (n_acc >> 1) & 1)) return false;
+  if (cta == 0 && threadIdx.x == 128) mbar_signal_at(in_cta(&bar->acc_full[acc], 1));
+  tc_fence_after();
+  return true;
+}
+
+__device__ __forceinline__ void accumulator_free(Barriers* bar, int acc, int lane) {
+  tc_fence_before();
+  __syncwarp();
+  if (lane == 0) mbar_signal_at(in_cta(&bar->acc_empty[acc], 0));
+}
+
 // The epilogue of 32 columns (rows of the output) of a warp's 32 lanes
-// (features), T the output's type. FULL: all 32 exist, so that the columns are
-// independent of one another and the loads of the residual come first.
+// (features), T the output's type. FULL: all 32 exist, so that no column waits
+// for another (with a test on each, 8192 x 1024 x 8192 takes 237 us, not 102);
+// the loads of the residual come first.
 template <int MODE, int ACT, bool FULL, typename T>
 __device__ __forceinline__ void store_columns(const MmaParams& q, const Tile& w, int cta, int lane,
                                               int quad, int c0, const float (&r)[32], float b) {
@@ -373,19 +390,22 @@ __device__ __forceinline__ void store_columns(const MmaParams& q, const Tile& w,
   }
   const T* res = static_cast<const T*>(p.residual) + row0 * ld + feature;
   __nv_bfloat16* z = p.z + row0 * ld + feature;
-  float add[32];
 #pragma unroll
-  for (int c = 0; c < 32; ++c)
-    add[c] = p.residual && (FULL || c < left) ? get(res + (int64_t)c * ld) : 0.0f;
+  for (int h = 0; h < 32; h += 16) {
+    float add[16];
 #pragma unroll
-  for (int c = 0; c < 32; ++c) {
-    const float v = r[c] + b;
-    if (FULL || c < left) {
-      if (p.z) put(z, v);
-      put(y, act_of(ACT, v) + add[c]);
+    for (int c = 0; c < 16; ++c)
+      add[c] = p.residual && (FULL || h + c < left) ? get(res + (int64_t)(h + c) * ld) : 0.0f;
+#pragma unroll
+    for (int c = 0; c < 16; ++c) {
+      const float v = r[h + c] + b;
+      if (FULL || h + c < left) {
+        if (p.z) put(z, v);
+        put(y, act_of(ACT, v) + add[c]);
+      }
+      y += ld;
+      z += ld;
     }
-    y += ld;
-    z += ld;
   }
 }
 
@@ -423,17 +443,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const uint32_t cta = cluster_rank();
   int32_t* timeout = q.p.s.err;
 
-  if (threadIdx.x == 0) {
-    for (int s = 0; s < kStages; ++s) {
-      mbar_init(&bar->full[s], 2);       // each CTA's producer
-      mbar_init(&bar->empty[s], 1);
-      mbar_init(&bar->landed[s], 1);
-    }
-    for (int a = 0; a < 2; ++a) {
-      mbar_init(&bar->acc_full[a], 1);
-      mbar_init(&bar->acc_empty[a], 2 * kEpilogueWarps);  // of both CTAs
-    }
-    mbar_init_fence();
+  // one thread a barrier
+  if (threadIdx.x < kStages) {
+    mbar_init(&bar->full[threadIdx.x], 2);       // each CTA's producer
+    mbar_init(&bar->empty[threadIdx.x], 1);
+    mbar_init(&bar->landed[threadIdx.x], 1);
+  } else if (threadIdx.x < kStages + 2) {
+    mbar_init(&bar->acc_full[threadIdx.x - kStages], 1);
+    mbar_init(&bar->acc_empty[threadIdx.x - kStages], 2 * kEpilogueWarps);  // of both CTAs
+  }
+  if (threadIdx.x < 32) mbar_init_fence();
+  if (threadIdx.x == 64) {
     tma_prefetch_map(&maps.a);
     tma_prefetch_map(&maps.b[0]);
   }
@@ -616,6 +636,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // warp (T f32: at most two such blocks, whose sums it keeps)
     const int quad = warp & 3, turn = (warp - 4) >> 2;
     const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
+    constexpr int kBlocks = kChunked ? kMaxRows / 2 / 64 : 1;
+    constexpr int kPartsAtOnce = kChunked ? 2 : 4;
     int n_acc = 0;
     // A warp whose wait gave up does no more work, but meets the others at the
     // barriers of parts, where all of them learn of it.
@@ -637,89 +659,93 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
       }
       float* sums = q.partial + ((int64_t)u * plan.cap * 256 + cta * 128 + quad * 32 + lane);
-      if (w.kb0 >= w.kb1) {     // a group with no rows: its weight gradient is zero
-        float r[32];
+      const bool none = w.kb0 >= w.kb1;    // a group with no rows: its weight gradient is zero
+      float keep[kBlocks][32];
+      if (kChunked && !none) {             // the sums of the part's chunks, in their order
+        const int chunks = (w.kb1 - w.kb0 + kChunk32 - 1) / kChunk32;
+        for (int i = 0; i < chunks && ok; ++i, ++n_acc) {
+          const int acc = n_acc & 1;
+          ok = accumulator_ready(bar, acc, n_acc, (int)cta);
+          if (!ok) break;
 #pragma unroll
-        for (int c = 0; c < 32; ++c) r[c] = 0.0f;
-        for (int c0 = turn * 32; c0 < w.rows; c0 += 64)
-          epilogue<MODE, ACT, T>(q, w, (int)cta, lane, quad, c0, r, 0.0f);
-        continue;
-      }
-      // a value of this part: its sum for the others, or the tile's result
-      auto finish = [&](int c0, const float (&r)[32]) {
-        if (whole) {
-          epilogue<MODE, ACT, T>(q, w, (int)cta, lane, quad, c0, r, b);
-        } else {
-#pragma unroll
-          for (int c = 0; c < 32; ++c)
-            if (c0 + c < w.rows) sums[(int64_t)(c0 + c) * 256] = r[c];
-        }
-      };
-      const int chunks = kChunked ? (w.kb1 - w.kb0 + kChunk32 - 1) / kChunk32 : 1;
-      float keep[kChunked ? 2 : 1][32];
-      for (int i = 0; i < chunks && ok; ++i, ++n_acc) {
-        const int acc = n_acc & 1;
-        ok = warp_wait(&bar->acc_full[acc], (n_acc >> 1) & 1);
-        if (!ok) break;
-        if (cta == 0 && threadIdx.x == 128) mbar_signal_at(in_cta(&bar->acc_full[acc], 1));
-        tc_fence_after();
-        if (kChunked) {
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
+          for (int h = 0; h < kBlocks; ++h) {
             const int c0 = turn * 32 + h * 64;
             if (c0 >= w.rows) continue;
             float r[32];
             tmem_load32(lanes + acc * 256 + c0, r);
 #pragma unroll
-            for (int c = 0; c < 32; ++c) keep[h % (kChunked ? 2 : 1)][c] = i ? keep[h % (kChunked ? 2 : 1)][c] + r[c] : r[c];
+            for (int c = 0; c < 32; ++c) keep[h][c] = i ? keep[h][c] + r[c] : r[c];
           }
-        } else {
-          for (int c0 = turn * 32; c0 < w.rows; c0 += 64) {
+          accumulator_free(bar, acc, lane);
+        }
+      } else if (!none) {
+        ok = ok && accumulator_ready(bar, n_acc & 1, n_acc, (int)cta);
+      }
+      if (!ok && whole) continue;
+      // first the values of this part: the tile's result, or sums for the part
+      // that finishes last, which then adds all of them in their order
+      const float* parts_of = nullptr;
+      while (true) {
+        const bool result = whole || parts_of;
+#pragma unroll
+        for (int h = 0; h < (kChunked ? kBlocks : 1); ++h)
+          for (int c0 = turn * 32 + h * 64; c0 < w.rows && ok; c0 += kChunked ? w.rows : 64) {
             float r[32];
-            tmem_load32(lanes + acc * 256 + c0, r);
-            finish(c0, r);
+            if (parts_of) {
+#pragma unroll
+              for (int c = 0; c < 32; ++c) r[c] = 0.0f;
+              const float* at = parts_of + c0 * 256;
+#pragma unroll kPartsAtOnce
+              for (int part = 0; part < w.parts; ++part, at += plan.cap * 256) {
+#pragma unroll
+                for (int c = 0; c < 32; ++c)
+                  if (c0 + c < w.rows) r[c] += __ldcg(at + c * 256);
+              }
+            } else if (none) {
+#pragma unroll
+              for (int c = 0; c < 32; ++c) r[c] = 0.0f;
+            } else if (kChunked) {
+#pragma unroll
+              for (int c = 0; c < 32; ++c) r[c] = keep[h][c];
+            } else {
+              __syncwarp();
+              tmem_load32(lanes + (n_acc & 1) * 256 + c0, r);
+            }
+            if (result) {
+              epilogue<MODE, ACT, T>(q, w, (int)cta, lane, quad, c0, r, b);
+            } else {
+#pragma unroll
+              for (int c = 0; c < 32; ++c)
+                if (c0 + c < w.rows) sums[(c0 + c) * 256] = r[c];
+            }
           }
+        if (!kChunked && !none && !parts_of && ok) {
+          accumulator_free(bar, n_acc & 1, lane);
+          ++n_acc;
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_signal_at(in_cta(&bar->acc_empty[acc], 0));
-      }
-      if (kChunked && ok) {
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-          if (turn * 32 + h * 64 < w.rows) finish(turn * 32 + h * 64, keep[h % (kChunked ? 2 : 1)]);
-      }
-      if (whole) continue;
-      // the tile's last part to get here adds all of them, in their order
-      if (!epilogue_agree(ok)) break;
-      if (threadIdx.x == 128) {
-        unsigned int* ticket = q.tickets + quotient(u, plan.splits) * 2 + cta;
-        const bool last = ticket_take(ticket) == (unsigned)w.parts - 1;
-        if (last) *ticket = 0u;
-        bar->last = last;
-      }
-      (void)epilogue_agree(true);
-      if (!bar->last) continue;
-      const float* from = sums - (int64_t)w.part * plan.cap * 256;
-      for (int c0 = turn * 32; c0 < w.rows; c0 += 64) {
-        float r[32];
-#pragma unroll
-        for (int c = 0; c < 32; ++c) r[c] = 0.0f;
-        const float* at = from + c0 * 256;
-#pragma unroll 4
-        for (int part = 0; part < w.parts; ++part, at += plan.cap * 256) {
-#pragma unroll
-          for (int c = 0; c < 32; ++c)
-            if (c0 + c < w.rows) r[c] += __ldcg(at + c * 256);
+        if (result) break;
+        if (!epilogue_agree(ok)) {
+          ok = false;
+          break;
         }
-        epilogue<MODE, ACT, T>(q, w, (int)cta, lane, quad, c0, r, b);
+        if (threadIdx.x == 128) {
+          unsigned int* ticket = q.tickets + quotient(u, plan.splits) * 2 + cta;
+          const bool last = ticket_take(ticket) == (unsigned)w.parts - 1;
+          if (last) *ticket = 0u;
+          bar->last = last;
+        }
+        (void)epilogue_agree(true);
+        if (!bar->last) break;
+        parts_of = sums - (int64_t)w.part * plan.cap * 256;
       }
+      if (!ok && !whole) break;
     }
     if (!ok && lane == 0) atomicOr(timeout, kErrLinearTimeout);
   }
   __syncwarp();
   __syncthreads();
-  cluster_sync();   // the other CTA may still arrive on this one's barriers
+  cluster_arrive();   // the other CTA may still arrive on this one's barriers
+  cluster_wait();
   if (warp == 1) tmem_free(tmem, kTmemColumns);
 }
 
