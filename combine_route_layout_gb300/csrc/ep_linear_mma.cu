@@ -45,6 +45,7 @@ constexpr int kLeast = 4, kLeastGrad = 16;       // stages of a part (dW's parts
 constexpr int kChunk32 = 8;                      // stages of such a sum
 constexpr int kEpilogueWarps = 8;                // two to each quarter of the TMEM lanes
 constexpr int kThreads = (4 + kEpilogueWarps) * 32;
+constexpr int kGroupBytes = 16;                  // what the plan keeps of a group
 constexpr int kTmemColumns = 512;                // two accumulators
 
 enum Mode { kForward = 0, kInputGrad = 1, kWeightGrad = 2 };
@@ -54,6 +55,7 @@ struct Plan {
   int tiles;
   int cap;           // most rows of a tile
   int splits;        // parts that a tile's contraction is cut into
+  int size;          // dense: rows of a tile
 };
 
 struct MmaParams {
@@ -151,7 +153,8 @@ __device__ __forceinline__ int tiles_in(int count, int cap) {
 // Unit u of the plan: part u % splits of tile u / splits.
 template <int MODE>
 __device__ __forceinline__ Tile tile_at(const MmaParams& q, const Plan& plan, const int* first,
-                                        const int* begins, const int* counts, int u) {
+                                        const int* begins, const int* counts, const int* sizes,
+                                        int u) {
   Tile w;
   int t = plan.splits == 1 ? u : quotient(u, plan.splits);
   w.part = u - t * plan.splits;
@@ -180,7 +183,7 @@ __device__ __forceinline__ Tile tile_at(const MmaParams& q, const Plan& plan, co
   } else {
     // 8 row tiles at a time pass over all features, so that tiles that run
     // together share operands in L2
-    const int size = tile_rows(count, plan.cap, quotient);
+    const int size = sizes[lo];
     const int tiles = quotient(count + size - 1, size);
     const int band = quotient(t, 8 * q.f_tiles);
     const int in = min(8, tiles - band * 8);
@@ -221,12 +224,14 @@ __device__ __forceinline__ bool has_tail(const Tile& w, int kb) {
 // f32 sums the last part to finish adds up. 1024 x 7168 x 256: 43.7 us as 4
 // tiles of 256 rows, 27.5 us as 16 tiles of 64 rows in 4 parts each.
 template <int MODE>
-__device__ Plan plan_tiles(const MmaParams& q, int base_cap, int* first, int* begins, int* counts) {
+__device__ Plan plan_tiles(const MmaParams& q, int base_cap, int* first, int* begins, int* counts,
+                           int* sizes) {
   __shared__ int sums[3][kThreads / 32];
   if (!q.p.s.begin) {
     if (threadIdx.x == 0) {
       first[0] = begins[0] = 0;
       counts[0] = (int)q.p.s.dense_rows;
+      sizes[0] = q.plan.size;
     }
     __syncthreads();
     return q.plan;
@@ -308,16 +313,51 @@ __device__ Plan plan_tiles(const MmaParams& q, int base_cap, int* first, int* be
   for (int w = 0; w < warp; ++w) before += sums[level][w];
   for (int g = g0; g < g1; ++g) {
     first[g] = before;
-    before += tiles_in(counts[g], plan.cap) * q.f_tiles;
+    sizes[g] = tile_rows(counts[g], plan.cap, quotient);
+    before += quotient(counts[g] + sizes[g] - 1, sizes[g]) * q.f_tiles;
   }
   __syncthreads();
   return plan;
 }
 
-__device__ __forceinline__ void put(float* at, float v) { *at = v; }
-__device__ __forceinline__ void put(__nv_bfloat16* at, float v) { *at = __float2bfloat16_rn(v); }
-__device__ __forceinline__ float get(const float* at) { return *at; }
-__device__ __forceinline__ float get(const __nv_bfloat16* at) { return __bfloat162float(*at); }
+// Accesses that a predicate turns off: no branch keeps one column's from the
+// next one's. (With a test on each column the compiler makes branches, and
+// 8192 x 1024 x 8192 takes 237 us instead of 102.)
+__device__ __forceinline__ void put(float* at, float v, bool on) {
+  asm volatile("{\n .reg .pred p;\n setp.ne.u32 p, %2, 0;\n @p st.global.f32 [%0], %1;\n}" ::"l"(at),
+               "f"(v), "r"((uint32_t)on)
+               : "memory");
+}
+__device__ __forceinline__ void put(__nv_bfloat16* at, float v, bool on) {
+  asm volatile("{\n .reg .pred p;\n setp.ne.u32 p, %2, 0;\n @p st.global.b16 [%0], %1;\n}" ::"l"(at),
+               "h"(__bfloat16_as_ushort(__float2bfloat16_rn(v))), "r"((uint32_t)on)
+               : "memory");
+}
+__device__ __forceinline__ float get(const float* at, bool on) {
+  float v;
+  asm volatile("{\n .reg .pred p;\n setp.ne.u32 p, %2, 0;\n mov.b32 %0, 0;\n @p ld.global.f32 %0, [%1];\n}"
+               : "=f"(v)
+               : "l"(at), "r"((uint32_t)on)
+               : "memory");
+  return v;
+}
+__device__ __forceinline__ float get(const __nv_bfloat16* at, bool on) {
+  unsigned short v;
+  asm volatile("{\n .reg .pred p;\n setp.ne.u32 p, %2, 0;\n mov.b16 %0, 0;\n @p ld.global.b16 %0, [%1];\n}"
+               : "=h"(v)
+               : "l"(at), "r"((uint32_t)on)
+               : "memory");
+  return __bfloat162float(__ushort_as_bfloat16(v));
+}
+// Another CTA's sum, from L2.
+__device__ __forceinline__ float get_part(const float* at, bool on) {
+  float v;
+  asm volatile("{\n .reg .pred p;\n setp.ne.u32 p, %2, 0;\n mov.b32 %0, 0;\n @p ld.global.cg.f32 %0, [%1];\n}"
+               : "=f"(v)
+               : "l"(at), "r"((uint32_t)on)
+               : "memory");
+  return v;
+}
 
 // An accumulator's sum is there (the even CTA passes the news on), and has
 // been read.
@@ -335,12 +375,10 @@ __device__ __forceinline__ void accumulator_free(Barriers* bar, int acc, int lan
 }
 
 // The epilogue of 32 columns (rows of the output) of a warp's 32 lanes
-// (features), T the output's type. FULL: all 32 exist, so that no column waits
-// for another (with a test on each, 8192 x 1024 x 8192 takes 237 us, not 102);
-// the loads of the residual come first.
-template <int MODE, int ACT, bool FULL, typename T>
-__device__ __forceinline__ void store_columns(const MmaParams& q, const Tile& w, int cta, int lane,
-                                              int quad, int c0, const float (&r)[32], float b) {
+// (features), T the output's type. The residual's loads come first.
+template <int MODE, int ACT, typename T>
+__device__ __forceinline__ void epilogue(const MmaParams& q, const Tile& w, int cta, int lane,
+                                         int quad, int c0, const float (&r)[32], float b) {
   const LinearParams& p = q.p;
   const int f = quad * 32 + lane;          // lane of the accumulator
   const int left = w.rows - c0;            // columns that exist
@@ -350,72 +388,64 @@ __device__ __forceinline__ void store_columns(const MmaParams& q, const Tile& w,
     // lanes exchanges two columns so that each finishes one of them
     const int out = w.f0 / 2 + cta * 64 + f / 2;
     const int odd = lane & 1;
-    const bool in = out < p.N;
+    const int mine = out < p.N ? left - odd : 0;   // this lane's columns are 0, 2, ... below it
     const int64_t row = row0 + odd;
     T* y = static_cast<T*>(p.y) + row * p.N + out;
     const T* res = static_cast<const T*>(p.residual) + row * p.N + out;
     __nv_bfloat16* z = p.z + row * p.Nw + out;
     float add[16];
 #pragma unroll
-    for (int i = 0; i < 16; ++i)
-      add[i] = p.residual && in && (FULL || 2 * i + odd < left) ? get(res + (int64_t)(2 * i) * p.N) : 0.0f;
+    for (int i = 0; i < 16; ++i) add[i] = 0.0f;
+    if (p.residual) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) add[i] = get(res + (int64_t)(2 * i) * p.N, 2 * i < mine);
+    }
+    const int kept = p.z ? mine : 0;
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
       const float v0 = r[2 * i] + b, v1 = r[2 * i + 1] + b;
       const float other = __shfl_xor_sync(kFull, odd ? v0 : v1, 1);
       const float gate = odd ? other : v0, up = odd ? v1 : other;
-      if (in && (FULL || 2 * i + odd < left)) {
-        put(y, silu_of(gate) * up + add[i]);
-        if (p.z) {
-          put(z, gate);
-          put(z + p.N, up);
-        }
-      }
+      put(y, silu_of(gate) * up + add[i], 2 * i < mine);
+      put(z, gate, 2 * i < kept);
+      put(z + p.N, up, 2 * i < kept);
       y += 2 * (int64_t)p.N;
       z += 2 * (int64_t)p.Nw;
     }
     return;
   }
   const int feature = w.f0 + cta * 128 + f;
-  if (feature >= q.features) return;
+  const int mine = feature < q.features ? left : 0;
   const int64_t ld = q.features;           // the output's rows are its features
   T* y = static_cast<T*>(q.out) + row0 * ld + feature;
   if (MODE != kForward) {
 #pragma unroll
     for (int c = 0; c < 32; ++c) {
-      if (FULL || c < left) put(y, r[c]);
+      put(y, r[c], c < mine);
       y += ld;
     }
     return;
   }
   const T* res = static_cast<const T*>(p.residual) + row0 * ld + feature;
   __nv_bfloat16* z = p.z + row0 * ld + feature;
+  const int kept = p.z ? mine : 0;
 #pragma unroll
   for (int h = 0; h < 32; h += 16) {
     float add[16];
 #pragma unroll
-    for (int c = 0; c < 16; ++c)
-      add[c] = p.residual && (FULL || h + c < left) ? get(res + (int64_t)(h + c) * ld) : 0.0f;
+    for (int c = 0; c < 16; ++c) add[c] = 0.0f;
+    if (p.residual) {
+#pragma unroll
+      for (int c = 0; c < 16; ++c) add[c] = get(res + (int64_t)(h + c) * ld, h + c < mine);
+    }
 #pragma unroll
     for (int c = 0; c < 16; ++c) {
       const float v = r[h + c] + b;
-      if (FULL || h + c < left) {
-        if (p.z) put(z, v);
-        put(y, act_of(ACT, v) + add[c]);
-      }
+      put(z, v, h + c < kept);
+      put(y, act_of(ACT, v) + add[c], h + c < mine);
       y += ld;
       z += ld;
     }
-  }
-}
-
-template <int MODE, int ACT, typename T>
-__device__ __forceinline__ void epilogue(const MmaParams& q, const Tile& w, int cta, int lane,
-                                         int quad, int c0, const float (&r)[32], float b) {
-  if (w.rows - c0 >= 32) {
-    store_columns<MODE, ACT, true, T>(q, w, cta, lane, quad, c0, r, b);
-  } else {
-    store_columns<MODE, ACT, false, T>(q, w, cta, lane, quad, c0, r, b);
   }
 }
 
@@ -439,6 +469,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   int* first = reinterpret_cast<int*>(bar + 1);
   int* begins = first + q.p.s.G;
   int* counts = begins + q.p.s.G;
+  int* sizes = counts + q.p.s.G;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const uint32_t cta = cluster_rank();
   int32_t* timeout = q.p.s.err;
@@ -460,7 +491,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   __syncthreads();
   cluster_arrive();                      // the barriers are ready; the wait is below
   if (warp == 1) tmem_alloc(&bar->tmem, kTmemColumns);
-  const Plan plan = plan_tiles<MODE>(q, kChunked ? kMaxRows / 2 : kMaxRows, first, begins, counts);
+  const Plan plan = plan_tiles<MODE>(q, kChunked ? kMaxRows / 2 : kMaxRows, first, begins, counts, sizes);
   const int units = plan.tiles * plan.splits;
   tc_fence_before();
   __syncthreads();                       // the TMEM address is there
@@ -476,7 +507,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const uint32_t full0 = in_cta(&bar->full[0], 0), empty0 = in_cta(&bar->empty[0], 1);
     bool ok = true;
     for (int u = pair; u < units && ok; u += pairs) {
-      const Tile w = tile_at<MODE>(q, plan, first, begins, counts, u);
+      const Tile w = tile_at<MODE>(q, plan, first, begins, counts, sizes, u);
       const int half = w.n / 2;
       const int fc = w.f0 + (int)cta * 128;                     // this CTA's features
       const int rc = w.r0 + (int)cta * half;                    // this CTA's rows
@@ -554,7 +585,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     uint32_t phase = 0;
     bool ok = true, ready = false;         // ready: the stage was seen to be full
     Tile next;
-    if (pair < units) next = tile_at<MODE>(q, plan, first, begins, counts, pair);
+    if (pair < units) next = tile_at<MODE>(q, plan, first, begins, counts, sizes, pair);
     for (int u = pair; u < units && ok; u += pairs) {
       const Tile w = next;
       const uint32_t form = mma_form(w.n, kMnA, kMnB);
@@ -597,10 +628,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         // the next unit is worked out under this one's products
         if (kb == w.kb0 && u + pairs < units)
-          next = tile_at<MODE>(q, plan, first, begins, counts, u + pairs);
+          next = tile_at<MODE>(q, plan, first, begins, counts, sizes, u + pairs);
       }
       if (w.kb0 >= w.kb1 && u + pairs < units)
-        next = tile_at<MODE>(q, plan, first, begins, counts, u + pairs);
+        next = tile_at<MODE>(q, plan, first, begins, counts, sizes, u + pairs);
     }
     if (!ok) atomicOr(timeout, kErrLinearTimeout);
   } else if (MODE == kWeightGrad && warp == 2) {
@@ -611,7 +642,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     uint32_t tails = 0;      // parity of the tails that each of the ring's places has had
     bool ok = true;
     for (int u = pair; u < units && ok; u += pairs) {
-      const Tile w = tile_at<MODE>(q, plan, first, begins, counts, u);
+      const Tile w = tile_at<MODE>(q, plan, first, begins, counts, sizes, u);
       if (w.kb0 >= w.kb1) continue;
       it += w.kb1 - w.kb0;
       if (!has_tail<MODE>(w, w.kb1 - 1)) continue;
@@ -643,7 +674,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // barriers of parts, where all of them learn of it.
     bool ok = true;
     for (int u = pair; u < units; u += pairs) {
-      const Tile w = tile_at<MODE>(q, plan, first, begins, counts, u);
+      const Tile w = tile_at<MODE>(q, plan, first, begins, counts, sizes, u);
       const bool whole = w.parts == 1;
       if (w.kb0 >= w.kb1 && (MODE != kWeightGrad || w.part > 0 || w.terms > 0)) continue;
       if (!ok && whole) continue;
@@ -698,8 +729,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll kPartsAtOnce
               for (int part = 0; part < w.parts; ++part, at += plan.cap * 256) {
 #pragma unroll
-                for (int c = 0; c < 32; ++c)
-                  if (c0 + c < w.rows) r[c] += __ldcg(at + c * 256);
+                for (int c = 0; c < 32; ++c) r[c] += get_part(at + c * 256, c0 + c < w.rows);
               }
             } else if (none) {
 #pragma unroll
@@ -715,8 +745,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               epilogue<MODE, ACT, T>(q, w, (int)cta, lane, quad, c0, r, b);
             } else {
 #pragma unroll
-              for (int c = 0; c < 32; ++c)
-                if (c0 + c < w.rows) sums[(c0 + c) * 256] = r[c];
+              for (int c = 0; c < 32; ++c) put(sums + (c0 + c) * 256, r[c], c0 + c < w.rows);
             }
           }
         if (!kChunked && !none && !parts_of && ok) {
@@ -817,10 +846,10 @@ bool map_mn_major(CUtensorMap* m, const void* base, int64_t cols, int64_t rows, 
 
 template <int MODE, int ACT, typename T>
 cudaError_t launch_tiles(const Maps& maps, const MmaParams& q, int grid, cudaStream_t st) {
-  const size_t smem = 1024 + kStages * kStageBytes + sizeof(Barriers) + (size_t)q.p.s.G * 12;
+  const size_t smem = 1024 + kStages * kStageBytes + sizeof(Barriers) + (size_t)q.p.s.G * kGroupBytes;
   // raises the kernel's shared-memory limit on its first use
   (void)ctas_per_sm(product_kernel<MODE, ACT, T>, kThreads, 1024 + kStages * kStageBytes +
-                                                             sizeof(Barriers) + EP_MAX_EXPERTS * 12);
+                                                             sizeof(Barriers) + EP_MAX_EXPERTS * kGroupBytes);
   product_kernel<MODE, ACT, T><<<grid, kThreads, smem, st>>>(maps, q);
   return cudaGetLastError();
 }
@@ -842,6 +871,7 @@ Plan dense_plan(int64_t rows64, int base_cap, int f_tiles, int blocks, int pairs
     const int size = tile_rows(rows, base_cap >> level, host_quotient);
     plan.cap = base_cap >> level;
     plan.tiles = (rows + size - 1) / size * f_tiles;
+    plan.size = size;
     if (2 * plan.tiles > pairs || plan.cap <= kMinCap) break;
   }
   plan.splits = splits_for(pairs, plan.tiles, blocks, kLeast);
@@ -849,7 +879,7 @@ Plan dense_plan(int64_t rows64, int base_cap, int f_tiles, int blocks, int pairs
 }
 
 Plan dense_grad_plan(int64_t rows, int cap, int tiles, int pairs) {
-  return Plan{tiles, cap, splits_for(pairs, tiles, (int)((rows + kDepth - 1) / kDepth), kLeastGrad)};
+  return Plan{tiles, cap, splits_for(pairs, tiles, (int)((rows + kDepth - 1) / kDepth), kLeastGrad), 0};
 }
 
 // Upper bound of the units of all groups (their counts are on the device).
