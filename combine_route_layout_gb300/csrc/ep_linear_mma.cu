@@ -359,6 +359,29 @@ __device__ __forceinline__ float get_part(const float* at, bool on) {
   return v;
 }
 
+// The sums of a tile's parts, `next` floats apart, of a lane's 32 columns (`left`
+// of them exist), added in the parts' order. Eight columns of all parts are
+// asked for at once: the parts one after another would wait for L2 each.
+__device__ __forceinline__ void add_parts(const float* at, int next, int parts, int left,
+                                          float (&r)[32]) {
+#pragma unroll
+  for (int h = 0; h < 32; h += 8) {
+#pragma unroll
+    for (int c = 0; c < 8; ++c) r[h + c] = 0.0f;
+    if (h >= left) continue;
+    float v[kMaxSplits][8];
+#pragma unroll
+    for (int i = 0; i < kMaxSplits; ++i)
+#pragma unroll
+      for (int c = 0; c < 8; ++c)
+        v[i][c] = get_part(at + i * next + (h + c) * 256, i < parts && h + c < left);
+#pragma unroll
+    for (int i = 0; i < kMaxSplits; ++i)
+#pragma unroll
+      for (int c = 0; c < 8; ++c) r[h + c] += v[i][c];
+  }
+}
+
 // An accumulator's sum is there (the even CTA passes the news on), and has
 // been read.
 __device__ __forceinline__ bool accumulator_ready(Barriers* bar, int acc, int n_acc, int cta) {
@@ -668,7 +691,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const int quad = warp & 3, turn = (warp - 4) >> 2;
     const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
     constexpr int kBlocks = kChunked ? kMaxRows / 2 / 64 : 1;
-    constexpr int kPartsAtOnce = kChunked ? 2 : 4;
     int n_acc = 0;
     // A warp whose wait gave up does no more work, but meets the others at the
     // barriers of parts, where all of them learn of it.
@@ -723,14 +745,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           for (int c0 = turn * 32 + h * 64; c0 < w.rows && ok; c0 += kChunked ? w.rows : 64) {
             float r[32];
             if (parts_of) {
-#pragma unroll
-              for (int c = 0; c < 32; ++c) r[c] = 0.0f;
-              const float* at = parts_of + c0 * 256;
-#pragma unroll kPartsAtOnce
-              for (int part = 0; part < w.parts; ++part, at += plan.cap * 256) {
-#pragma unroll
-                for (int c = 0; c < 32; ++c) r[c] += get_part(at + c * 256, c0 + c < w.rows);
-              }
+              add_parts(parts_of + c0 * 256, plan.cap * 256, w.parts, w.rows - c0, r);
             } else if (none) {
 #pragma unroll
               for (int c = 0; c < 32; ++c) r[c] = 0.0f;
