@@ -20,8 +20,8 @@
 // Every kernel reads each logit once: a warp takes a row, a lane VPL
 // consecutive experts, in registers. Consecutive, so that the lowest lane
 // among equals holds the lowest expert and one ballot settles a tie. The
-// kernels are bound by instruction issue: 256 experts cost a row about 500 warp
-// instructions, half of them the sigmoid's or softmax's, against 1 KB of reads.
+// kernels are bound by instruction issue, not by HBM: 256 experts are 1 KB of reads
+// and hundreds of warp instructions a row.
 // Selection therefore sorts each lane's scores once (values alone, a network),
 // pops the warp's largest k times, and finds the experts' numbers at the end,
 // all k at once.
@@ -115,10 +115,10 @@ __device__ __forceinline__ float reciprocal(float x) {
   return __fmaf_rn(r, __fmaf_rn(-x, r, 1.0f), r);
 }
 
-constexpr float kSigmoidLow = -86.0f;   // 1 + exp(-l) is below 2^125 from here on
+constexpr float kSigmoidFar = 86.0f;   // 1 + exp(-l) is below 2^125 for l above minus this
 
 // 1 / (1 + exp(-l)) with every step rounded to f32, as the definition has it:
-// the selection compares these values. `reciprocal` serves l >= kSigmoidLow.
+// the selection compares these values. `reciprocal` serves |l| < kSigmoidFar.
 __device__ __forceinline__ float sigmoid(float l) {
   return __frcp_rn(__fadd_rn(1.0f, expf(-l)));
 }
@@ -178,19 +178,19 @@ __device__ __forceinline__ float open_logit(float l, bool& bad) {
   return finite && l > lowest<T>() ? l : -INFINITY;
 }
 
+// Masks the row's logits. Most rows have nothing to mask: then one test a logit
+// finds that all lie within +-`limit` (warp-wide; true is the answer).
 template <int VPL, typename T>
-__device__ __forceinline__ void mask_row(float (&l)[VPL], int32_t* err) {
-  bool fine = true;
+__device__ __forceinline__ bool mask_row(float (&l)[VPL], float limit, int32_t* err) {
+  bool plain = true;
 #pragma unroll
-  for (int i = 0; i < VPL; ++i) {
-    fine = fine && l[i] < INFINITY;
-    l[i] = l[i] > lowest<T>() ? l[i] : -INFINITY;   // NaN too
-  }
-  if (!__all_sync(kFull, fine)) {
+  for (int i = 0; i < VPL; ++i) plain = plain && fabsf(l[i]) < limit;
+  if (__all_sync(kFull, plain)) return true;
+  bool bad = false;
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) l[i] = l[i] < INFINITY ? l[i] : -INFINITY;
-    if (!fine) atomicOr(err, kErrNotFinite);
-  }
+  for (int i = 0; i < VPL; ++i) l[i] = open_logit<T>(l[i], bad);
+  if (bad) atomicOr(err, kErrNotFinite);
+  return false;
 }
 
 // The row's largest logit; 0 for a row with none, so that exp(-inf - 0) is 0.
@@ -203,27 +203,26 @@ __device__ __forceinline__ float row_max(const float (&l)[VPL]) {
   return m > -INFINITY ? m : 0.0f;
 }
 
-// p (softmax: exp(l - top), sigmoid: s) of the lane's experts, 0 where masked.
+// s as the selection compares it, 0 where masked. `plain`: all logits are within
+// kSigmoidFar of zero.
+template <int VPL>
+__device__ __forceinline__ void exact_scores(const float (&l)[VPL], bool plain, float (&s)[VPL]) {
+  if (plain) {
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) s[i] = reciprocal(__fadd_rn(1.0f, expf(-l[i])));
+  } else {
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) s[i] = sigmoid(l[i]);
+  }
+}
+
+// p (softmax: exp(l - top), sigmoid: s) of the lane's experts, 0 where masked, for
+// sums and gradients: to 2^-21 or so, in four instructions each.
 template <int VPL, bool SIGMOID>
 __device__ __forceinline__ void raw_scores(const float (&l)[VPL], float top, float (&p)[VPL]) {
-  if (!SIGMOID) {
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) p[i] = expf(l[i] - top);
-    return;
-  }
-  float least = INFINITY;    // of the logits that count
-#pragma unroll
-  for (int i = 0; i < VPL; ++i) {
-    const bool open = l[i] > -INFINITY;
-    const float v = open ? l[i] : 0.0f;
-    least = fminf(least, v);
-    const float r = reciprocal(__fadd_rn(1.0f, expf(-v)));
-    p[i] = open ? r : 0.0f;
-  }
-  if (__any_sync(kFull, least < kSigmoidLow)) {
-#pragma unroll
-    for (int i = 0; i < VPL; ++i) p[i] = sigmoid(l[i]);
-  }
+  for (int i = 0; i < VPL; ++i)
+    p[i] = SIGMOID ? __fdividef(1.0f, 1.0f + __expf(-l[i])) : __expf(l[i] - top);
 }
 
 template <int VPL>
@@ -431,10 +430,14 @@ __global__ void __launch_bounds__(kRouterWarps * 32) router_rows_kernel(RouterPa
     for (int i = 0; i < VPL; ++i) l[i] = next[i];
     if (t + kRouterWarps < end)    // the next row is on its way under this one
       load_row<VPL, T>(logits + (g + kRouterWarps) * p.E, p.E, lane, p.vec, next);
-    mask_row<VPL, T>(l, p.err);
+    const bool plain = mask_row<VPL, T>(l, SIGMOID && SELECT ? kSigmoidFar : -lowest<T>(), p.err);
     float total = 0.0f, top = 0.0f;
     if (!SIGMOID && (BALANCE || !p.normalize)) top = row_max<VPL>(l);
-    if (SIGMOID || BALANCE || !p.normalize) raw_scores<VPL, SIGMOID>(l, top, pr);
+    if (SIGMOID && SELECT) {
+      exact_scores<VPL>(l, plain, pr);
+    } else if (BALANCE || !p.normalize) {
+      raw_scores<VPL, SIGMOID>(l, top, pr);
+    }
     if (BALANCE || (!SIGMOID && !p.normalize)) total = row_sum<VPL>(pr);
     if (BALANCE) {
       const float inv = total > 0.0f ? 1.0f / total : 0.0f;
@@ -444,8 +447,11 @@ __global__ void __launch_bounds__(kRouterWarps * 32) router_rows_kernel(RouterPa
     if (SELECT) {
       float c[VPL];
 #pragma unroll
-      for (int i = 0; i < VPL; ++i)
-        c[i] = !SIGMOID ? l[i] : l[i] > -INFINITY ? __fadd_rn(pr[i], bias[i]) : -INFINITY;
+      for (int i = 0; i < VPL; ++i) c[i] = SIGMOID ? __fadd_rn(pr[i], bias[i]) : l[i];
+      if (SIGMOID && !plain) {
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) c[i] = l[i] > -INFINITY ? c[i] : -INFINITY;
+      }
       int e;
       float v;
       select_experts<VPL, SIGMOID>(p, lane, buf, c, e, v);
@@ -643,7 +649,7 @@ __global__ void __launch_bounds__(kRouterWarps * 32) router_grad_kernel(RouterGr
       }
       if (t + kRouterWarps < end)
         load_row<VPL, T>(logits + (g + kRouterWarps) * p.E, p.E, lane, p.vec, next);
-      mask_row<VPL, T>(l, p.err);
+      (void)mask_row<VPL, T>(l, -lowest<T>(), p.err);
       const float top = SIGMOID ? 0.0f : row_max<VPL>(l);
       raw_scores<VPL, SIGMOID>(l, top, pr);
       float inv = 0.0f;
