@@ -66,6 +66,7 @@ struct MmaParams {
   int r_tiles;       // dW: 256-row tiles of each group (else by the group's count)
   int a_blocks;      // MN-major operands: the map cuts rows into blocks of 64
   int b_blocks;      // elements, so that one box takes two of them
+  int pairs_out, pairs_z;   // bf16 outputs whose rows allow two features a store
   Plan plan;         // of a dense product
   float* partial;    // sums of parts: [unit][column][256 features], or NULL
   unsigned int* tickets;   // parts that are done: [tile][2], zero between calls
@@ -333,6 +334,11 @@ __device__ __forceinline__ void put(__nv_bfloat16* at, float v, bool on) {
                "h"(__bfloat16_as_ushort(__float2bfloat16_rn(v))), "r"((uint32_t)on)
                : "memory");
 }
+__device__ __forceinline__ void put2(__nv_bfloat16* at, float lo, float hi, bool on) {
+  asm volatile("{\n .reg .pred p;\n setp.ne.u32 p, %2, 0;\n @p st.global.b32 [%0], %1;\n}" ::"l"(at),
+               "r"(cvt_bf16x2(lo, hi)), "r"((uint32_t)on)
+               : "memory");
+}
 __device__ __forceinline__ float get(const float* at, bool on) {
   float v;
   asm volatile("{\n .reg .pred p;\n setp.ne.u32 p, %2, 0;\n mov.b32 %0, 0;\n @p ld.global.f32 %0, [%1];\n}"
@@ -397,6 +403,39 @@ __device__ __forceinline__ void accumulator_free(Barriers* bar, int acc, int lan
   if (lane == 0) mbar_signal_at(in_cta(&bar->acc_empty[acc], 0));
 }
 
+// A lane's feature of `left` rows, one store each.
+template <typename T>
+__device__ __forceinline__ void store_each(T* at, int64_t ld, int left, const float (&v)[32]) {
+  if (left >= 32) {
+#pragma unroll
+    for (int c = 0; c < 32; ++c, at += ld) put(at, v[c], true);
+  } else {
+#pragma unroll
+    for (int c = 0; c < 32; ++c, at += ld) put(at, v[c], c < left);
+  }
+}
+
+// The same two features at a time: lanes 2 i and 2 i + 1 exchange a value of
+// every two rows, so that each stores both features of one of them. Half the
+// stores, each of four whole sectors. Needs rows and tensor on 4-byte
+// boundaries (an even `ld`).
+__device__ __forceinline__ void store_pairs(__nv_bfloat16* rows, int64_t ld, int feature,
+                                            int features, int left, const float (&v)[32]) {
+  const int odd = feature & 1;
+  __nv_bfloat16* at = rows + (feature - odd) + odd * ld;
+  const int mine = feature - odd < features ? left - odd : 0;   // `features` is even with ld
+  const bool all = left >= 32 && mine > 0;
+#pragma unroll
+  for (int c = 0; c < 32; c += 2, at += 2 * ld) {
+    const float other = __shfl_xor_sync(kFull, odd ? v[c] : v[c + 1], 1);
+    put2(at, odd ? other : v[c], odd ? v[c + 1] : other, all || c < mine);
+  }
+}
+__device__ __forceinline__ void store_pairs(float* rows, int64_t ld, int feature, int features,
+                                            int left, const float (&v)[32]) {
+  store_each(rows + feature, ld, feature < features ? left : 0, v);
+}
+
 // The epilogue of 32 columns (rows of the output) of a warp's 32 lanes
 // (features), T the output's type. The residual's loads come first.
 template <int MODE, int ACT, typename T>
@@ -440,35 +479,34 @@ __device__ __forceinline__ void epilogue(const MmaParams& q, const Tile& w, int 
   const int feature = w.f0 + cta * 128 + f;
   const int mine = feature < q.features ? left : 0;
   const int64_t ld = q.features;           // the output's rows are its features
-  T* y = static_cast<T*>(q.out) + row0 * ld + feature;
-  if (MODE != kForward) {
+  float v[32];
+  if (MODE == kForward) {
+    const T* res = static_cast<const T*>(p.residual) + row0 * ld + feature;
 #pragma unroll
-    for (int c = 0; c < 32; ++c) {
-      put(y, r[c], c < mine);
-      y += ld;
+    for (int c = 0; c < 32; ++c) v[c] = r[c] + b;
+    if (p.z) {
+      __nv_bfloat16* z = p.z + row0 * ld;
+      if (q.pairs_z) {
+        store_pairs(z, ld, feature, q.features, left, v);
+      } else {
+        store_each(z + feature, ld, mine, v);
+      }
     }
-    return;
-  }
-  const T* res = static_cast<const T*>(p.residual) + row0 * ld + feature;
-  __nv_bfloat16* z = p.z + row0 * ld + feature;
-  const int kept = p.z ? mine : 0;
 #pragma unroll
-  for (int h = 0; h < 32; h += 16) {
-    float add[16];
-#pragma unroll
-    for (int c = 0; c < 16; ++c) add[c] = 0.0f;
+    for (int c = 0; c < 32; ++c) v[c] = act_of(ACT, v[c]);
     if (p.residual) {
 #pragma unroll
-      for (int c = 0; c < 16; ++c) add[c] = get(res + (int64_t)(h + c) * ld, h + c < mine);
+      for (int c = 0; c < 32; ++c) v[c] += get(res + (int64_t)c * ld, c < mine);
     }
+  } else {
 #pragma unroll
-    for (int c = 0; c < 16; ++c) {
-      const float v = r[h + c] + b;
-      put(z, v, h + c < kept);
-      put(y, act_of(ACT, v) + add[c], h + c < mine);
-      y += ld;
-      z += ld;
-    }
+    for (int c = 0; c < 32; ++c) v[c] = r[c];
+  }
+  T* y = static_cast<T*>(q.out) + row0 * ld;
+  if (q.pairs_out) {
+    store_pairs(y, ld, feature, q.features, left, v);
+  } else {
+    store_each(y + feature, ld, mine, v);
   }
 }
 
@@ -860,7 +898,9 @@ bool map_mn_major(CUtensorMap* m, const void* base, int64_t cols, int64_t rows, 
 }
 
 template <int MODE, int ACT, typename T>
-cudaError_t launch_tiles(const Maps& maps, const MmaParams& q, int grid, cudaStream_t st) {
+cudaError_t launch_tiles(const Maps& maps, MmaParams& q, int grid, cudaStream_t st) {
+  q.pairs_out = q.features % 2 == 0 && (uintptr_t)q.out % 4 == 0;
+  q.pairs_z = q.features % 2 == 0 && (uintptr_t)q.p.z % 4 == 0;
   const size_t smem = 1024 + kStages * kStageBytes + sizeof(Barriers) + (size_t)q.p.s.G * kGroupBytes;
   // raises the kernel's shared-memory limit on its first use
   (void)ctas_per_sm(product_kernel<MODE, ACT, T>, kThreads, 1024 + kStages * kStageBytes +
@@ -905,7 +945,7 @@ int64_t most_units(const LinearParams& p, int f_tiles, int terms) {
 }
 
 template <typename T>
-cudaError_t launch_forward(const Maps& m, const MmaParams& q, int grid, cudaStream_t st) {
+cudaError_t launch_forward(const Maps& m, MmaParams& q, int grid, cudaStream_t st) {
   switch (q.p.act) {
     case EP_ACT_RELU: return launch_tiles<kForward, EP_ACT_RELU, T>(m, q, grid, st);
     case EP_ACT_SILU: return launch_tiles<kForward, EP_ACT_SILU, T>(m, q, grid, st);
