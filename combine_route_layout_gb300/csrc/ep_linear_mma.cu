@@ -17,7 +17,8 @@
 // under the next one's products) stay in TMEM. Grid: one CTA per SM, each pair
 // walks the tiles of all groups.
 //
-// Roles by warp: 0 TMA, 1 MMA, 4-11 epilogue (TMEM lanes go by warp % 4; the
+// Roles by warp: 0 TMA, 1 MMA, 2 clears the tails of dW's contractions, 3 works
+// out the tiles, 4-11 epilogue (TMEM lanes go by warp % 4; the
 // two warps of a quarter take every other 32 columns).
 #include <cuda.h>
 
@@ -72,36 +73,12 @@ struct MmaParams {
   unsigned int* tickets;   // parts that are done: [tile][2], zero between calls
 };
 
-struct Barriers {
-  uint64_t full[kStages];     // both CTAs' operands have landed (even CTA's)
-  uint64_t empty[kStages];    // this CTA's stage may be written again
-  uint64_t landed[kStages];   // dW: this CTA's last block has landed; its tail is to be cleared
-  uint64_t acc_full[2];
-  uint64_t acc_empty[2];      // even CTA's: both CTAs' epilogues are done
-  uint32_t tmem;
-  uint32_t last;              // this CTA's part of a tile was the last
-};
-
 // Count this part in; what the CTA's threads wrote before the barrier ahead of
 // this call is visible to the one that counts last, and theirs to it.
 __device__ __forceinline__ unsigned int ticket_take(unsigned int* ticket) {
   unsigned int before;
   asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], 1;" : "=r"(before) : "l"(ticket) : "memory");
   return before;
-}
-
-// A barrier of the epilogue's warps; whether all of them are well.
-__device__ __forceinline__ bool epilogue_agree(bool ok) {
-  uint32_t all;
-  asm volatile(
-      "{\n .reg .pred p, q;\n"
-      " setp.ne.u32 p, %1, 0;\n"
-      " bar.red.and.pred q, 1, %2, p;\n"
-      " selp.u32 %0, 1, 0, q;\n}"
-      : "=r"(all)
-      : "r"((uint32_t)ok), "n"(kEpilogueWarps * 32)
-      : "memory");
-  return all != 0;
 }
 
 // n / d for 0 <= n, 0 < d below 2^31, in two float steps. The compiler's integer
@@ -128,6 +105,21 @@ struct Tile {
   int terms;         // length of the contraction
   int kb0, kb1;      // this part's stages; none: kb0 >= kb1
   int part, parts;   // its place among the tile's parts that have any
+};
+
+constexpr int kSlots = 4;     // tiles that are worked out ahead
+
+struct Barriers {
+  uint64_t full[kStages];     // both CTAs' operands have landed (even CTA's)
+  uint64_t empty[kStages];    // this CTA's stage may be written again
+  uint64_t landed[kStages];   // dW: this CTA's last block has landed; its tail is to be cleared
+  uint64_t acc_full[2];
+  uint64_t acc_empty[2];      // even CTA's: both CTAs' epilogues are done
+  uint64_t tile_full[kSlots], tile_empty[kSlots];
+  uint64_t joined;            // the epilogue's warps meet
+  Tile tiles[kSlots];
+  uint32_t tmem;
+  uint32_t last;              // this CTA's part of a tile was the last
 };
 
 // Rows of a tile of a group of `count` rows: as few tiles as `cap` rows (a
@@ -388,6 +380,34 @@ __device__ __forceinline__ void add_parts(const float* at, int next, int parts, 
   }
 }
 
+// Tile number i of this pair, as the scheduling warp left it: for one thread,
+// and for a warp.
+__device__ __forceinline__ bool take_tile(Barriers* bar, int i, Tile& w) {
+  const int slot = i % kSlots;
+  if (!mbar_wait_soon(&bar->tile_full[slot], (i / kSlots) & 1)) return false;
+  w = bar->tiles[slot];
+  mbar_arrive(&bar->tile_empty[slot]);
+  return true;
+}
+
+__device__ __forceinline__ bool warp_take_tile(Barriers* bar, int i, Tile& w, int lane) {
+  const int slot = i % kSlots;
+  if (!warp_wait(&bar->tile_full[slot], (i / kSlots) & 1)) return false;
+  w = bar->tiles[slot];
+  __syncwarp();
+  if (lane == 0) mbar_arrive(&bar->tile_empty[slot]);
+  return true;
+}
+
+// The epilogue's warps meet; false if one of them does not come.
+__device__ __forceinline__ bool epilogue_meet(Barriers* bar, int lane, uint32_t& phase) {
+  __syncwarp();
+  if (lane == 0) mbar_arrive(&bar->joined);
+  const bool ok = warp_wait(&bar->joined, phase);
+  phase ^= 1;
+  return ok;
+}
+
 // An accumulator's sum is there (the even CTA passes the news on), and has
 // been read.
 __device__ __forceinline__ bool accumulator_ready(Barriers* bar, int acc, int n_acc, int cta) {
@@ -544,7 +564,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     mbar_init(&bar->acc_full[threadIdx.x - kStages], 1);
     mbar_init(&bar->acc_empty[threadIdx.x - kStages], 2 * kEpilogueWarps);  // of both CTAs
   }
-  if (threadIdx.x < 32) mbar_init_fence();
+  if (threadIdx.x >= 32 && threadIdx.x < 32 + kSlots) {
+    // producer, the epilogue's warps, MMA (even CTA), tails (dW)
+    mbar_init(&bar->tile_full[threadIdx.x - 32], 1);
+    mbar_init(&bar->tile_empty[threadIdx.x - 32],
+              1 + kEpilogueWarps + (cta == 0 ? 1 : 0) + (MODE == kWeightGrad ? 1 : 0));
+  } else if (threadIdx.x == 32 + kSlots) {
+    mbar_init(&bar->joined, kEpilogueWarps);
+  }
+  if (threadIdx.x < 64) mbar_init_fence();
   if (threadIdx.x == 64) {
     tma_prefetch_map(&maps.a);
     tma_prefetch_map(&maps.b[0]);
@@ -560,6 +588,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   cluster_wait();
   const uint32_t tmem = bar->tmem;
   const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+  const int mine = pair < units ? (units - 1 - pair) / pairs + 1 : 0;   // this pair's units
 
   if (warp == 0 && elect_one()) {
     // ------------------------------------------------ producer: one thread
@@ -567,8 +596,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     uint32_t phase = 1;                     // the first pass over the ring waits for nothing
     const uint32_t full0 = in_cta(&bar->full[0], 0), empty0 = in_cta(&bar->empty[0], 1);
     bool ok = true;
-    for (int u = pair; u < units && ok; u += pairs) {
-      const Tile w = tile_at<MODE>(q, plan, first, begins, counts, sizes, u);
+    for (int i = 0; i < mine && ok; ++i) {
+      Tile w;
+      ok = take_tile(bar, i, w);
+      if (!ok) break;
       const int half = w.n / 2;
       const int fc = w.f0 + (int)cta * 128;                     // this CTA's features
       const int rc = w.r0 + (int)cta * half;                    // this CTA's rows
@@ -645,10 +676,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     int n_acc = 0, s = 0;
     uint32_t phase = 0;
     bool ok = true, ready = false;         // ready: the stage was seen to be full
-    Tile next;
-    if (pair < units) next = tile_at<MODE>(q, plan, first, begins, counts, sizes, pair);
-    for (int u = pair; u < units && ok; u += pairs) {
-      const Tile w = next;
+    for (int i = 0; i < mine && ok; ++i) {
+      Tile w;
+      ok = take_tile(bar, i, w);
+      if (!ok) break;
       const uint32_t form = mma_form(w.n, kMnA, kMnB);
       int stop = w.kb0;                    // end of the accumulator's sum
       for (int kb = w.kb0; kb < w.kb1; ++kb) {
@@ -687,12 +718,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           mma_commit(&bar->acc_full[n_acc & 1]);
           ++n_acc;
         }
-        // the next unit is worked out under this one's products
-        if (kb == w.kb0 && u + pairs < units)
-          next = tile_at<MODE>(q, plan, first, begins, counts, sizes, u + pairs);
       }
-      if (w.kb0 >= w.kb1 && u + pairs < units)
-        next = tile_at<MODE>(q, plan, first, begins, counts, sizes, u + pairs);
     }
     if (!ok) atomicOr(timeout, kErrLinearTimeout);
   } else if (MODE == kWeightGrad && warp == 2) {
@@ -702,8 +728,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     int it = 0;
     uint32_t tails = 0;      // parity of the tails that each of the ring's places has had
     bool ok = true;
-    for (int u = pair; u < units && ok; u += pairs) {
-      const Tile w = tile_at<MODE>(q, plan, first, begins, counts, sizes, u);
+    for (int i = 0; i < mine && ok; ++i) {
+      Tile w;
+      ok = warp_take_tile(bar, i, w, lane);
+      if (!ok) break;
       if (w.kb0 >= w.kb1) continue;
       it += w.kb1 - w.kb0;
       if (!has_tail<MODE>(w, w.kb1 - 1)) continue;
@@ -713,15 +741,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       tails ^= 1u << s;
       const int valid = w.terms - (w.kb1 - 1) * kDepth, more = (valid + 15) / 16 * 16 - valid;
       uint8_t* stage = ring + s * kStageBytes;
-      for (int i = lane; i < 4 * more * 8; i += 32) {           // 16-byte pieces
-        const int part = i / (more * 8), row = valid + (i / 8 - part * more);
-        reinterpret_cast<uint4*>(stage + part * 8192 + row * 128)[i & 7] = make_uint4(0, 0, 0, 0);
-      }
+      for (int row = valid + (lane >> 3); row < valid + more; row += 4)
+#pragma unroll
+        for (int part = 0; part < 4; ++part)                    // 16-byte pieces of a and b
+          reinterpret_cast<uint4*>(stage + part * 8192 + row * 128)[lane & 7] = make_uint4(0, 0, 0, 0);
       fence_async_shared();
       __syncwarp();
       if (lane == 0) mbar_arrive_at(in_cta(&bar->full[s], 0));
     }
     if (!ok && lane == 0) atomicOr(timeout, kErrLinearTimeout);
+  } else if (warp == 3 && elect_one()) {
+    // ------------------------------------------------ works out the tiles, ahead of all roles:
+    // a tile's place takes over a thousand cycles of dependent arithmetic
+    bool ok = true;
+    for (int i = 0; i < mine; ++i) {
+      const int slot = i % kSlots;
+      if (i >= kSlots) {
+        ok = mbar_wait_soon(&bar->tile_empty[slot], (i / kSlots - 1) & 1);
+        if (!ok) break;
+      }
+      bar->tiles[slot] = tile_at<MODE>(q, plan, first, begins, counts, sizes, pair + i * pairs);
+      mbar_arrive(&bar->tile_full[slot]);
+    }
+    if (!ok) atomicOr(timeout, kErrLinearTimeout);
   } else if (warp >= 4) {
     // ------------------------------------------------ epilogue
     // 64 columns of the tile belong to the warp pair of a quarter: 32 to this
@@ -730,14 +772,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
     constexpr int kBlocks = kChunked ? kMaxRows / 2 / 64 : 1;
     int n_acc = 0;
-    // A warp whose wait gave up does no more work, but meets the others at the
-    // barriers of parts, where all of them learn of it.
+    uint32_t meeting = 0;
     bool ok = true;
-    for (int u = pair; u < units; u += pairs) {
-      const Tile w = tile_at<MODE>(q, plan, first, begins, counts, sizes, u);
+    for (int i = 0; i < mine && ok; ++i) {
+      const int u = pair + i * pairs;
+      Tile w;
+      ok = warp_take_tile(bar, i, w, lane);
+      if (!ok) break;
       const bool whole = w.parts == 1;
       if (w.kb0 >= w.kb1 && (MODE != kWeightGrad || w.part > 0 || w.terms > 0)) continue;
-      if (!ok && whole) continue;
       float b = 0.0f;
       if (MODE == kForward && q.p.bias) {
         const int f = (int)cta * 128 + quad * 32 + lane;
@@ -754,7 +797,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       float keep[kBlocks][32];
       if (kChunked && !none) {             // the sums of the part's chunks, in their order
         const int chunks = (w.kb1 - w.kb0 + kChunk32 - 1) / kChunk32;
-        for (int i = 0; i < chunks && ok; ++i, ++n_acc) {
+        for (int chunk = 0; chunk < chunks; ++chunk, ++n_acc) {
           const int acc = n_acc & 1;
           ok = accumulator_ready(bar, acc, n_acc, (int)cta);
           if (!ok) break;
@@ -765,14 +808,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             float r[32];
             tmem_load32(lanes + acc * 256 + c0, r);
 #pragma unroll
-            for (int c = 0; c < 32; ++c) keep[h][c] = i ? keep[h][c] + r[c] : r[c];
+            for (int c = 0; c < 32; ++c) keep[h][c] = chunk ? keep[h][c] + r[c] : r[c];
           }
           accumulator_free(bar, acc, lane);
         }
       } else if (!none) {
-        ok = ok && accumulator_ready(bar, n_acc & 1, n_acc, (int)cta);
+        ok = accumulator_ready(bar, n_acc & 1, n_acc, (int)cta);
       }
-      if (!ok && whole) continue;
+      if (!ok) break;
       // first the values of this part: the tile's result, or sums for the part
       // that finishes last, which then adds all of them in their order
       const float* parts_of = nullptr;
@@ -780,7 +823,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const bool result = whole || parts_of;
 #pragma unroll
         for (int h = 0; h < (kChunked ? kBlocks : 1); ++h)
-          for (int c0 = turn * 32 + h * 64; c0 < w.rows && ok; c0 += kChunked ? w.rows : 64) {
+          for (int c0 = turn * 32 + h * 64; c0 < w.rows; c0 += kChunked ? w.rows : 64) {
             float r[32];
             if (parts_of) {
               add_parts(parts_of + c0 * 256, plan.cap * 256, w.parts, w.rows - c0, r);
@@ -801,26 +844,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               for (int c = 0; c < 32; ++c) put(sums + (c0 + c) * 256, r[c], c0 + c < w.rows);
             }
           }
-        if (!kChunked && !none && !parts_of && ok) {
+        if (!kChunked && !none && !parts_of) {
           accumulator_free(bar, n_acc & 1, lane);
           ++n_acc;
         }
         if (result) break;
-        if (!epilogue_agree(ok)) {
-          ok = false;
-          break;
-        }
+        ok = epilogue_meet(bar, lane, meeting);
+        if (!ok) break;
         if (threadIdx.x == 128) {
           unsigned int* ticket = q.tickets + quotient(u, plan.splits) * 2 + cta;
           const bool last = ticket_take(ticket) == (unsigned)w.parts - 1;
           if (last) *ticket = 0u;
           bar->last = last;
         }
-        (void)epilogue_agree(true);
-        if (!bar->last) break;
+        ok = epilogue_meet(bar, lane, meeting);
+        if (!ok || !bar->last) break;
         parts_of = sums - (int64_t)w.part * plan.cap * 256;
       }
-      if (!ok && !whole) break;
     }
     if (!ok && lane == 0) atomicOr(timeout, kErrLinearTimeout);
   }
