@@ -112,7 +112,7 @@ constexpr int kSlots = 4;     // tiles that are worked out ahead
 struct Barriers {
   uint64_t full[kStages];     // both CTAs' operands have landed (even CTA's)
   uint64_t empty[kStages];    // this CTA's stage may be written again
-  uint64_t landed[kStages];   // dW: this CTA's last block has landed; its tail is to be cleared
+  uint64_t landed;            // dW: this CTA's last block has landed; its tail is to be cleared
   uint64_t acc_full[2];
   uint64_t acc_empty[2];      // even CTA's: both CTAs' epilogues are done
   uint64_t tile_full[kSlots], tile_empty[kSlots];
@@ -544,6 +544,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     product_kernel(const __grid_constant__ Maps maps, MmaParams q) {
   constexpr bool kGated = MODE == kForward && ACT == EP_ACT_SWIGLU;
   constexpr bool kChunked = sizeof(T) == 4;
+  // dW: the last stage of a contraction, whose tail has to be cleared, has a
+  // place beside the ring, so that the time this takes passes under the others
+  constexpr int kTail = kStages - 1, kRing = MODE == kWeightGrad ? kTail : kStages;
   extern __shared__ uint8_t raw[];
   uint8_t* ring = reinterpret_cast<uint8_t*>(((uintptr_t)raw + 1023) & ~(uintptr_t)1023);
   Barriers* bar = reinterpret_cast<Barriers*>(ring + kStages * kStageBytes);
@@ -559,7 +562,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   if (threadIdx.x < kStages) {
     mbar_init(&bar->full[threadIdx.x], 2);       // each CTA's producer
     mbar_init(&bar->empty[threadIdx.x], 1);
-    mbar_init(&bar->landed[threadIdx.x], 1);
   } else if (threadIdx.x < kStages + 2) {
     mbar_init(&bar->acc_full[threadIdx.x - kStages], 1);
     mbar_init(&bar->acc_empty[threadIdx.x - kStages], 2 * kEpilogueWarps);  // of both CTAs
@@ -570,6 +572,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     mbar_init(&bar->tile_empty[threadIdx.x - 32],
               1 + kEpilogueWarps + (cta == 0 ? 1 : 0) + (MODE == kWeightGrad ? 1 : 0));
   } else if (threadIdx.x == 32 + kSlots) {
+    mbar_init(&bar->landed, 1);
     mbar_init(&bar->joined, kEpilogueWarps);
   }
   if (threadIdx.x < 64) mbar_init_fence();
@@ -592,7 +595,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
   if (warp == 0 && elect_one()) {
     // ------------------------------------------------ producer: one thread
-    int it = 0, s = 0;                      // stages written so far, the ring's place
+    int it = 0, s = 0, tails = 0;           // stages written so far, the ring's place
     uint32_t phase = 1;                     // the first pass over the ring waits for nothing
     const uint32_t full0 = in_cta(&bar->full[0], 0), empty0 = in_cta(&bar->empty[0], 1);
     bool ok = true;
@@ -607,23 +610,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const uint32_t bytes = kStageA + (MODE != kWeightGrad || q.b_blocks ? kStageB >> box
                                                                           : half / 64 * 8192);
       const CUtensorMap* map_b = &maps.b[box];
-      for (int kb = w.kb0; kb < w.kb1; ++kb, ++it) {
-        if (it >= kStages) {
-          ok = mbar_wait_soon(&bar->empty[s], phase);
-          if (!ok) break;
-          if (cta == 0) mbar_signal_at(empty0 + s * 8);
-        }
-        uint8_t* a = ring + s * kStageBytes;
+      // stage kb's operands into place `to`, their bytes on barrier `on`
+      auto load = [&](int kb, int to, uint32_t on) {
+        uint8_t* a = ring + to * kStageBytes;
         uint8_t* b = a + kStageA;
         const int d = kb * kDepth;
         const int row = (int)w.begin + d;                       // dW: contraction row
-        uint32_t on = full0 + s * 8;
-        if (has_tail<MODE>(w, kb)) {
-          on = smem_addr(&bar->landed[s]);
-          mbar_arrive_expect_tx(&bar->landed[s], bytes);
-        } else {
-          mbar_signal_expect_tx_at(on, bytes);
-        }
         if (MODE == kForward) {
           if (kGated) {
             tma_load_4d(a, &maps.a, d, 0, fc / 2, w.g, on);
@@ -651,7 +643,33 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           tma_load_2d(b, map_b, rc, row, on);
           if (half == 128) tma_load_2d(b + 8192, map_b, rc + 64, row, on);
         }
-        if (++s == kStages) {
+      };
+      const bool tail = has_tail<MODE>(w, w.kb1 - 1);
+      const int end = w.kb1 - (tail ? 1 : 0);
+      // once the ring is full of this tile's stages, the place of the last
+      // tile's tail is free or soon will be
+      const int tail_at = min(w.kb0 + kRing, end);
+      for (int kb = w.kb0; kb < w.kb1; ++kb) {
+        if (tail && kb == tail_at) {
+          if (tails > 0) {
+            ok = mbar_wait_soon(&bar->empty[kTail], (tails - 1) & 1);
+            if (!ok) break;
+            if (cta == 0) mbar_signal_at(empty0 + kTail * 8);
+          }
+          ++tails;
+          mbar_arrive_expect_tx(&bar->landed, bytes);
+          load(w.kb1 - 1, kTail, smem_addr(&bar->landed));
+        }
+        if (kb == end) break;
+        if (it >= kRing) {
+          ok = mbar_wait_soon(&bar->empty[s], phase);
+          if (!ok) break;
+          if (cta == 0) mbar_signal_at(empty0 + s * 8);
+        }
+        ++it;
+        mbar_signal_expect_tx_at(full0 + s * 8, bytes);
+        load(kb, s, full0 + s * 8);
+        if (++s == kRing) {
           s = 0;
           phase ^= 1;
         }
@@ -660,10 +678,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     if (!ok) {
       atomicOr(timeout, kErrLinearTimeout);
       // copies in flight must land before the CTAs leave
-      for (int i = 0; i < kStages && i < it; ++i) {
-        s = s == 0 ? kStages - 1 : s - 1;
-        (void)mbar_wait(&bar->full[s], ((it - 1 - i) / kStages) & 1);
+      for (int i = 0; i < kRing && i < it; ++i) {
+        s = s == 0 ? kRing - 1 : s - 1;
+        (void)mbar_wait(&bar->full[s], ((it - 1 - i) / kRing) & 1);
       }
+      if (tails > 0) (void)mbar_wait(&bar->landed, (tails - 1) & 1);
     }
   } else if (warp == 1 && cta == 0 && elect_one()) {
     // ------------------------------------------------ MMA: one thread of the even CTA
@@ -673,7 +692,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     constexpr uint32_t kStepA = (kMnA ? 2048 : 32) >> 4, kStepB = (kMnB ? 2048 : 32) >> 4;
     const uint64_t a0 = smem_operand(smem_addr(ring), kMnA ? 8192 : 16);
     const uint64_t b0 = smem_operand(smem_addr(ring) + kStageA, kMnB ? 8192 : 16);
-    int n_acc = 0, s = 0;
+    int n_acc = 0, s = 0, tails = 0;
     uint32_t phase = 0;
     bool ok = true, ready = false;         // ready: the stage was seen to be full
     for (int i = 0; i < mine && ok; ++i) {
@@ -693,18 +712,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           }
         }
         const int left = w.terms - kb * kDepth;
-        if (has_tail<MODE>(w, kb)) {       // rows that both CTAs cleared
-          ok = mbar_wait_cluster(&bar->full[s], phase);
+        int at = s;
+        if (has_tail<MODE>(w, kb)) {       // a place of its own, whose rows both CTAs cleared
+          at = kTail;
+          ok = mbar_wait_cluster(&bar->full[kTail], tails++ & 1);
         } else if (!ready) {
           ok = mbar_wait_soon(&bar->full[s], phase);
         }
         if (!ok) break;
         tc_fence_after();
         const uint32_t d = tmem + (n_acc & 1) * 256;
-        const uint64_t a = a0 + (uint32_t)(s * (kStageBytes >> 4));
-        const uint64_t b = b0 + (uint32_t)(s * (kStageBytes >> 4));
-        uint64_t* emptied = &bar->empty[s];
-        if (++s == kStages) {
+        const uint64_t a = a0 + (uint32_t)(at * (kStageBytes >> 4));
+        const uint64_t b = b0 + (uint32_t)(at * (kStageBytes >> 4));
+        if (at == s && ++s == kRing) {
           s = 0;
           phase ^= 1;
         }
@@ -713,7 +733,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (left > 16) mma_pair(d, a + kStepA, b + kStepB, form, true);
         if (left > 32) mma_pair(d, a + 2 * kStepA, b + 2 * kStepB, form, true);
         if (left > 48) mma_pair(d, a + 3 * kStepA, b + 3 * kStepB, form, true);
-        mma_commit(emptied);
+        mma_commit(&bar->empty[at]);
         if (kb + 1 == stop) {
           mma_commit(&bar->acc_full[n_acc & 1]);
           ++n_acc;
@@ -725,29 +745,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // ------------------------------------------------ clears the rows past a segment's last
     // that the last 16-term step of its last stage would take in: they belong
     // to somebody else, and may hold anything
-    int it = 0;
-    uint32_t tails = 0;      // parity of the tails that each of the ring's places has had
+    uint32_t tails = 0;
     bool ok = true;
     for (int i = 0; i < mine && ok; ++i) {
       Tile w;
       ok = warp_take_tile(bar, i, w, lane);
       if (!ok) break;
-      if (w.kb0 >= w.kb1) continue;
-      it += w.kb1 - w.kb0;
-      if (!has_tail<MODE>(w, w.kb1 - 1)) continue;
-      const int s = (it - 1) % kStages;
-      ok = warp_wait(&bar->landed[s], (tails >> s) & 1);
+      if (w.kb0 >= w.kb1 || !has_tail<MODE>(w, w.kb1 - 1)) continue;
+      ok = warp_wait(&bar->landed, tails++ & 1);
       if (!ok) break;
-      tails ^= 1u << s;
       const int valid = w.terms - (w.kb1 - 1) * kDepth, more = (valid + 15) / 16 * 16 - valid;
-      uint8_t* stage = ring + s * kStageBytes;
+      uint8_t* stage = ring + kTail * kStageBytes;
       for (int row = valid + (lane >> 3); row < valid + more; row += 4)
 #pragma unroll
         for (int part = 0; part < 4; ++part)                    // 16-byte pieces of a and b
           reinterpret_cast<uint4*>(stage + part * 8192 + row * 128)[lane & 7] = make_uint4(0, 0, 0, 0);
       fence_async_shared();
       __syncwarp();
-      if (lane == 0) mbar_arrive_at(in_cta(&bar->full[s], 0));
+      if (lane == 0) mbar_arrive_at(in_cta(&bar->full[kTail], 0));
     }
     if (!ok && lane == 0) atomicOr(timeout, kErrLinearTimeout);
   } else if (warp == 3 && elect_one()) {
