@@ -398,6 +398,8 @@ extern "C" ep_status ep_linear_forward(ep_linear_handle* h, const void* x, const
   p.z = static_cast<__nv_bfloat16*>(preact);
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   if ((s = linear_ready(h, st)) != EP_OK) return s;
+  if (!row_begin && num_rows == 0) return EP_OK;
+  if (few_rows_supported(p)) return status_of(launch_linear_few_rows(p, h->sm_count, st));
   return status_of(launch_linear_forward(p, h->sm_count, st));
 }
 

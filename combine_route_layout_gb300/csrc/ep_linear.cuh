@@ -60,6 +60,10 @@ struct LinearParams {
 
 // The products (ep_linear_mma.cu), over `sms` multiprocessors.
 cudaError_t launch_linear_forward(const LinearParams& p, int sms, cudaStream_t st);
+// The forward for at most kFewRows dense rows (ep_linear_rows.cu).
+constexpr int kFewRows = 2;
+bool few_rows_supported(const LinearParams& p);
+cudaError_t launch_linear_few_rows(const LinearParams& p, int sms, cudaStream_t st);
 cudaError_t launch_linear_input_grad(const LinearParams& p, int sms, cudaStream_t st);
 cudaError_t launch_linear_weight_grad(const LinearParams& p, int sms, cudaStream_t st);
 

@@ -349,6 +349,14 @@ LINEAR = [
     (2, 512, 129, [700, 2500], "none", True, False, torch.float32, torch.float32),
     (40, 128, 64, [i % 7 * 11 for i in range(40)], "gelu", True, False, torch.bfloat16, torch.bfloat16),
     (2, 1000, 520, [1, 2], "silu", True, True, torch.bfloat16, torch.bfloat16),
+    # one and two dense rows; contractions cut into parts, forward and dW, and joined
+    (1, 2056, 40, [1], "swiglu", True, True, torch.bfloat16, torch.bfloat16),
+    (1, 1032, 9, [2], "gelu", True, True, torch.float32, torch.bfloat16),
+    (1, 4104, 96, [5], "none", True, True, torch.float32, torch.float32),
+    (1, 4096, 200, [70], "relu", False, False, torch.bfloat16, torch.bfloat16),
+    (2, 2048, 300, [3, 40], "swiglu", True, False, torch.bfloat16, torch.bfloat16),
+    (1, 64, 72, [5003], "silu", True, False, torch.bfloat16, torch.bfloat16),
+    (3, 72, 40, [0, 2500, 17], "none", True, False, torch.bfloat16, torch.float32),
 ]
 
 
