@@ -38,7 +38,9 @@ constexpr int kStageBytes = kStageA + kStageB;
 constexpr int kMaxRows = 256;                    // rows of a tile (f32 outputs: half)
 constexpr int kMinCap = 64;
 constexpr int kMaxSplits = 8;
-constexpr int kLeast = 4, kLeastGrad = 16;       // stages of a part (dW's parts of a tile are 256 KB)
+// Least stages of a part: joining costs about as much as ten stages (dW, whose
+// parts of a tile are 256 KB: as forty).
+constexpr int kLeast = 12, kLeastGrad = 32;
 // f32 outputs: the tensor core cuts off what its accumulator cannot hold, an
 // error that grows with the number of steps to the power 3/2 (7168 terms: 8e-6 of
 // the result); sums of 512 terms are added up in registers instead, which
@@ -995,7 +997,7 @@ Plan dense_grad_plan(int64_t rows, int cap, int tiles, int pairs) {
 // Upper bound of the units of all groups (their counts are on the device).
 int64_t most_units(const LinearParams& p, int f_tiles, int terms) {
   const int64_t rows = p.s.begin ? p.s.pool : p.s.dense_rows;
-  const int64_t parts = terms / (4 * kDepth);
+  const int64_t parts = terms / (kLeast * kDepth);
   return (rows / kMinCap + p.s.G) * f_tiles * (parts < 1 ? 1 : parts < kMaxSplits ? parts : kMaxSplits);
 }
 

@@ -508,17 +508,20 @@ __global__ void __launch_bounds__(kRouterWarps * 32) router_rows_kernel(RouterPa
 }
 
 // Counts and loss from the chunks' sums, added in a fixed order: CTA (b, s)
-// takes 32 experts of segment s, a warp every 32nd chunk, and the last CTA
-// adds the products. Latency bound: 32 warps keep the loads in flight.
-constexpr int kBalanceExperts = 32;
-constexpr int kBalanceWarps = 32;
+// takes 8 experts of segment s, 32 threads an expert, and the last CTA adds the
+// products. Latency bound: few experts a CTA make many CTAs, whose loads are in
+// flight together (32 experts a CTA: 10 us for 512 chunks).
+constexpr int kBalanceExperts = 8;
+constexpr int kBalanceThreads = 256;
 
-__global__ void __launch_bounds__(kBalanceWarps * 32) balance_reduce_kernel(BalanceParams p) {
-  __shared__ float sp[kBalanceWarps][kBalanceExperts + 1];
-  __shared__ int sn[kBalanceWarps][kBalanceExperts + 1];
+__global__ void __launch_bounds__(kBalanceThreads) balance_reduce_kernel(BalanceParams p) {
+  constexpr int kWarps = kBalanceThreads / 32;
+  __shared__ float sp[kWarps][kBalanceExperts];
+  __shared__ int sn[kWarps][kBalanceExperts];
   __shared__ bool last;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int e = blockIdx.x * kBalanceExperts + lane;
+  const int in = threadIdx.x % kBalanceExperts;
+  const int e = blockIdx.x * kBalanceExperts + in;
   const int seg = blockIdx.y;
   const int first = p.n_seg == 1 ? 0 : seg * p.chunks;
   const int n_chunk = p.n_seg == 1 ? p.R * p.stretches * p.chunks : p.chunks;
@@ -526,40 +529,43 @@ __global__ void __launch_bounds__(kBalanceWarps * 32) balance_reduce_kernel(Bala
   float s = 0.0f;
   int n = 0;
   if (e < p.E) {
-#pragma unroll 4
-    for (int c = warp; c < n_chunk; c += kBalanceWarps) {
+#pragma unroll 8
+    for (int c = threadIdx.x / kBalanceExperts; c < n_chunk; c += kBalanceThreads / kBalanceExperts) {
       s += __ldcg(p.part_p + (int64_t)(first + c) * p.E + e);
       n += __ldcg(p.part_n + (int64_t)(first + c) * p.E + e);
     }
   }
-  sp[warp][lane] = s;
-  sn[warp][lane] = n;
-  __syncthreads();
-  // lane w of warp e' adds warp w's sums of expert e', in a fixed tree
-  s = warp_sum(sp[lane][warp]);
-  n = sn[lane][warp];
 #pragma unroll
-  for (int o = 16; o; o >>= 1) n += __shfl_xor_sync(kFull, n, o);
-  __syncthreads();
-  if (lane == 0) {
-    const int mine = blockIdx.x * kBalanceExperts + warp;
-    int held = 0;
-    if (p.n_seg == 1) {
-      for (int r = 0; r < p.R; ++r) held += p.ntok[r];
-    } else {
-      const int r = seg / p.stretches, s0 = (seg - r * p.stretches) * p.stretch;
-      held = max(0, min(p.ntok[r] - s0, p.stretch));
-    }
-    float term = 0.0f;
-    if (mine < p.E) {
-      p.counts[(int64_t)seg * p.E + mine] = n;
-      if (held > 0) term = ((float)n * (float)p.E / ((float)held * (float)p.k)) * (s / (float)held);
-    }
-    sp[0][warp] = term;
+  for (int o = kBalanceExperts; o < 32; o <<= 1) {
+    s += __shfl_xor_sync(kFull, s, o);
+    n += __shfl_xor_sync(kFull, n, o);
+  }
+  if (lane < kBalanceExperts) {
+    sp[warp][lane] = s;
+    sn[warp][lane] = n;
   }
   __syncthreads();
   if (warp == 0) {
-    const float term = warp_sum(sp[0][lane]);
+    float term = 0.0f;
+    if (lane < kBalanceExperts && e < p.E) {
+      s = 0.0f;
+      n = 0;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        s += sp[w][lane];
+        n += sn[w][lane];
+      }
+      int held = 0;
+      if (p.n_seg == 1) {
+        for (int r = 0; r < p.R; ++r) held += p.ntok[r];
+      } else {
+        const int r = seg / p.stretches, s0 = (seg - r * p.stretches) * p.stretch;
+        held = max(0, min(p.ntok[r] - s0, p.stretch));
+      }
+      p.counts[(int64_t)seg * p.E + e] = n;
+      if (held > 0) term = ((float)n * (float)p.E / ((float)held * (float)p.k)) * (s / (float)held);
+    }
+    term = warp_sum(term);
     if (lane == 0) {
       p.part_loss[seg * gridDim.x + blockIdx.x] = term;
       __threadfence();
@@ -571,16 +577,15 @@ __global__ void __launch_bounds__(kBalanceWarps * 32) balance_reduce_kernel(Bala
   __threadfence();
   const int m = gridDim.x * gridDim.y;
   float acc = 0.0f;
-  for (int i = threadIdx.x; i < m; i += kBalanceWarps * 32) acc += __ldcg(p.part_loss + i);
+  for (int i = threadIdx.x; i < m; i += kBalanceThreads) acc += __ldcg(p.part_loss + i);
   acc = warp_sum(acc);
-  if (lane == 0) sp[0][warp] = acc;
+  if (lane == 0) sp[warp][0] = acc;
   __syncthreads();
-  if (warp == 0) {
-    const float v = warp_sum(sp[0][lane]);
-    if (lane == 0) {
-      *p.loss = v * p.coef;
-      *p.ticket = 0u;
-    }
+  if (threadIdx.x == 0) {
+    float v = 0.0f;
+    for (int w = 0; w < kWarps; ++w) v += sp[w][0];
+    *p.loss = v * p.coef;
+    *p.ticket = 0u;
   }
 }
 
@@ -623,6 +628,15 @@ __global__ void __launch_bounds__(kRouterWarps * 32) router_grad_kernel(RouterGr
   float next[VPL];
   if (at.t0 + warp < end)
     load_row<VPL, T>(logits + ((int64_t)at.rank * p.Tmax + at.t0 + warp) * p.E, p.E, lane, p.vec, next);
+  // a slot's expert and its weight's gradient, a row ahead as the logits are
+  int e_next = -1;
+  float up_next = 0.0f;
+  auto load_slot = [&](int64_t row) {
+    e_next = __ldg(p.idx_in + row * p.k + lane);
+    up_next = __ldg(q.d_w + row * p.k + lane);
+  };
+  const bool slots = q.d_w && lane < p.k;
+  if (slots && at.t0 + warp < end) load_slot((int64_t)at.rank * p.Tmax + at.t0 + warp);
   for (int t = at.t0 + warp; t < at.pad_end; t += kRouterWarps) {
     const int64_t g = (int64_t)at.rank * p.Tmax + t;
     float d[VPL];
@@ -635,8 +649,9 @@ __global__ void __launch_bounds__(kRouterWarps * 32) router_grad_kernel(RouterGr
       // the slots' own values are asked for before anything is computed
       int e = -1;
       float up = 0.0f, xl = -INFINITY;
-      if (q.d_w && lane < p.k) {
-        e = __ldg(p.idx_in + g * p.k + lane);
+      if (slots) {
+        e = e_next;
+        up = up_next * p.scale;
         if (e < -1 || e >= p.E) {
           atomicOr(p.err, kErrRouterIndex);
           e = -1;
@@ -644,8 +659,10 @@ __global__ void __launch_bounds__(kRouterWarps * 32) router_grad_kernel(RouterGr
         if (e >= 0) {
           bool ignored = false;
           xl = open_logit<T>((float)logits[g * p.E + e], ignored);
-          up = __ldg(q.d_w + g * p.k + lane) * p.scale;
+        } else {
+          up = 0.0f;
         }
+        if (t + kRouterWarps < end) load_slot(g + kRouterWarps);
       }
       if (t + kRouterWarps < end)
         load_row<VPL, T>(logits + (g + kRouterWarps) * p.E, p.E, lane, p.vec, next);
@@ -950,7 +967,7 @@ ep_status launch_balance(ep_router_handle* h, const RouterParams& p, int32_t* co
   b.ticket = h->ticket; b.counts = counts; b.loss = loss;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(h->expert_blocks, h->n_seg);
-  cfg.blockDim = dim3(kBalanceWarps * 32);
+  cfg.blockDim = dim3(kBalanceThreads);
   cfg.stream = st;
   cudaLaunchAttribute attr[1];   // set up while the rows are still being read
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -245,6 +245,45 @@ def test_router_gradient_matches_differences(layer):
                 assert abs((v[0] - v[1]) / (2 * h) - float(d[0, t, e])) < 1e-3
 
 
+def test_sigmoid_scores_are_the_formula_s_own_bits(layer):
+    """The scores that selection compares are 1 / (1 + exp(-l)) with each step
+    rounded to f32. A grid of 2^-24 over l in [-1.11, 0] puts 1 + exp(-l) on
+    every float in [2, 4): every significand a reciprocal can have. The rest of
+    the range, and the far side of exp's, is sampled."""
+    cfg = layer.EpRouterConfig(1, 1 << 18, 32, 32, score_func="sigmoid", normalize_weights=False)
+    op = layer.EpRouterOp(cfg)
+    n = 32 << 18
+    fine = [-(torch.arange(n, device=DEV, dtype=torch.float64) + i * n) * 2.0 ** -24 for i in range(3)]
+    gen = torch.Generator(device=DEV).manual_seed(4)
+    wide = (torch.rand(n, generator=gen, device=DEV, dtype=torch.float64) * 2 - 1) * 120
+    tiny = torch.randn(n, generator=gen, device=DEV, dtype=torch.float64) * 1e-4
+    for l in (*fine, wide, tiny):
+        l = l.float().view(1, -1, 32)
+        w, idx = op.forward(l)
+        s = 1.0 / (1.0 + torch.exp(-l))
+        assert torch.equal(w, s.gather(-1, idx.long()))
+        assert (w[..., :-1] >= w[..., 1:]).all()
+        assert torch.equal(idx.sort(-1).values, torch.arange(32, device=DEV, dtype=torch.int32).expand_as(idx))
+
+
+def test_router_over_2_31_logits(layer):
+    """Offsets past 32 bits: 8 x 300,000 rows of 1,024 bf16 logits."""
+    cfg = layer.EpRouterConfig(8, 300000, 1024, 2, logits_dtype=torch.bfloat16, balance_coef=2.0)
+    op = layer.EpRouterOp(cfg)
+    l = torch.zeros((8, 300000, 1024), dtype=torch.bfloat16, device=DEV)
+    l[7, 299990:, 5] = 2.0
+    l[7, 299990:, 1000] = 1.0
+    l[7, 299990:, 1001:1005] = 0.5
+    w, idx, counts, loss = op.forward(l, balance=True)
+    assert idx[7, -1].tolist() == [5, 1000] and idx[0, 0].tolist() == [0, 1] and idx[7, 299989].tolist() == [0, 1]
+    assert counts[0, 5] == 10 and counts[0, 1000] == 10 and counts[0, 0] == 2400000 - 10
+    d = op.backward(l, idx, d_weights=torch.ones_like(w), counts=counts, d_loss=loss)
+    small = layer.EpRouterOp(layer.EpRouterConfig(1, 16, 1024, 2, logits_dtype=torch.bfloat16))
+    tail = l[7:, -16:].contiguous()
+    assert torch.equal(small.forward(tail)[0], w[7:, -16:])
+    assert torch.isfinite(d[7, -16:].float()).all() and (d[7, -1] != 0).any()
+
+
 def test_router_ties_and_signed_zeros(layer):
     cfg = layer.EpRouterConfig(1, 3, 40, 5)
     op = layer.EpRouterOp(cfg)
@@ -504,6 +543,33 @@ def test_linear_cuts_segments_that_leave_the_pool(layer):
     assert (y[10:40] == 0).all()
 
 
+def test_linear_over_2_31_values(layer):
+    """Offsets past 32 bits in y, z, dy and dz: 270,000 rows of 8,192."""
+    rows, K, N = 270000, 64, 8192
+    cfg = layer.EpLinearConfig(2, K, N, rows, activation="relu")
+    op = layer.EpLinearOp(cfg, backward=True)
+    gen = torch.Generator(device=DEV).manual_seed(1)
+    x = torch.randn((rows, K), generator=gen, device=DEV).bfloat16()
+    w = torch.randn((2, N, K), generator=gen, device=DEV).bfloat16()
+    at = {"row_begin": torch.tensor([0, rows - 300], dtype=torch.int32, device=DEV),
+          "row_count": torch.tensor([rows - 300, 300], dtype=torch.int32, device=DEV)}
+    z = torch.empty((rows, N), dtype=torch.bfloat16, device=DEV)
+    y = op.forward(x, w, preact=z, **at)
+    dy = torch.ones((rows, N), dtype=torch.bfloat16, device=DEV)
+    dx, dw, db = op.backward(dy, x, w, z, want_dbias=True, **at)
+    op.sync()
+    s = slice(rows - 300, rows)
+    ref = x[s].double() @ w[1].double().t()
+    ulp_close(z[s], ref, torch.bfloat16, scale=x[s].double().abs() @ w[1].double().abs().t())
+    assert torch.equal(y[s], z[s].clamp(min=0))
+    g = (z[s] > 0).double()
+    ulp_close(dx[s], g @ w[1].double(), torch.bfloat16, scale=g @ w[1].double().abs(), terms=N)
+    ulp_close(dw[1], g.t() @ x[s].double(), torch.bfloat16, scale=g.t() @ x[s].double().abs(), terms=300)
+    ulp_close(db[1], g.sum(0), torch.float32)
+    g0 = (z[:rows - 300] > 0).sum(0)
+    assert (db[0].long() - g0).abs().max() <= rows * 2.0 ** -23 * rows
+
+
 def test_linear_in_a_graph_with_changing_counts(layer):
     """Counts are read on the device: a captured product follows them."""
     t = Product(layer, (3, 64, 48, [100, 1, 128], "swiglu", True, False, torch.bfloat16, torch.bfloat16))
@@ -552,3 +618,63 @@ def test_linear_over_dispatch_standard_moe(layer):
                 ulp_close(y[b:b + n], a @ ww.t(), torch.bfloat16, scale=a.abs() @ ww.abs().t())
             seen += n
     assert seen > 100
+
+
+# ----------------------------------------------------------- the whole layer
+
+def load_example():
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "moe_layer.py")
+    spec = importlib.util.spec_from_file_location("moe_layer", path)
+    mod = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(mod)
+    return mod
+
+
+def test_moe_layer_example_gradients(layer):
+    """The example's outputs and gradients against autograd in 64 bits over the
+    same routing, on ragged ranks. Every product rounds its result to bf16, and
+    the chain has four of them on the way to w_gate, so 2^-8 times a few of the
+    largest gradient bounds the difference: 3 % of it is taken."""
+    ex = load_example()
+    R, T, H, inner, E_r, k = 2, 24, 64, 48, 3, 2
+    m = ex.MoeLayer(R, T, H, inner, E_r, k, 1)
+    gen = torch.Generator(device=DEV).manual_seed(5)
+    x = torch.randn((R, T, H), generator=gen, device=DEV).bfloat16()
+    dy = torch.randn((R, T, H), generator=gen, device=DEV).bfloat16().float()
+    ntok = [T, T - 7]
+    y, loss = m.forward(x, num_tokens=ntok, balance=True)
+    one = torch.ones((), device=DEV)
+    dy[1, T - 7:] = 0
+    got = m.backward(dy, one)
+    m.sync()
+    idx = m.saved[4].long()
+    xd = x.double().requires_grad_(True)
+    ws = [w.double().requires_grad_(True) for w in (m.w_gate, m.w_up, m.w_down)]
+    s = torch.sigmoid(xd @ ws[0][0].t())
+    valid = torch.arange(T, device=DEV)[None] < torch.tensor(ntok, device=DEV)[:, None]
+    held = (idx >= 0) & valid[..., None]
+    q = s.gather(-1, idx.clamp(min=0)) * held
+    wt = q / q.sum(-1, keepdim=True).clamp(min=1e-30)
+    z = torch.einsum("rth,eoh->rteo", xd, ws[1])
+    h = torch.nn.functional.silu(z[..., :inner]) * z[..., inner:]
+    full = torch.einsum("rtei,ehi->rteh", h, ws[2])
+    out = (wt[..., None] * full.gather(2, idx.clamp(min=0)[..., None].expand(-1, -1, -1, H))).sum(2)
+    p = s / s.sum(-1, keepdim=True) * valid[..., None]
+    n = sum(ntok)
+    counts = torch.zeros(R * E_r, device=DEV, dtype=torch.float64).index_add_(0, idx[held], torch.ones(int(held.sum()), device=DEV, dtype=torch.float64))
+    bal = 0.01 * (counts * R * E_r / (k * n) * p.sum((0, 1)) / n).sum()
+    assert (y.double() - out).abs()[valid].max() < 0.03 * out.abs().max()
+    assert abs(float(loss) - float(bal)) < 1e-3 * float(bal)
+    refs = torch.autograd.grad((out * dy.double()).sum() + bal, [*ws, xd])
+    for g, ref in zip(got, refs):
+        ref = ref.detach()
+        assert torch.isfinite(g.float()).all()
+        sel = valid if g.shape == x.shape else slice(None)
+        assert (g.double() - ref)[sel].abs().max() < 0.03 * ref.abs().max()
+
+
+def test_moe_layer_example_trains(layer):
+    losses = load_example().train(steps=6)
+    assert all(b < a for a, b in zip(losses, losses[1:]))
