@@ -1,0 +1,59 @@
+// The first bytes of a router's or a product's workspace: error bits, and what
+// its kernels expect to be zero when they start (tickets). The first call on a
+// handle clears them on its stream. A call that is being captured clears them
+// inside its graph and leaves that to the next call too, since the graph may run
+// later, or never; the mark says whether the bits were ever cleared for this
+// handle, so that a report read from them is never left-over memory.
+#pragma once
+
+#include <atomic>
+
+#include "ep_kernels.cuh"
+
+namespace ep {
+
+constexpr size_t kHeaderBytes = 1024;
+constexpr size_t kTicketOffset = 256;
+
+struct Header {
+  uint32_t* words = nullptr;   // [0] error bits, [1] mark
+  uint32_t mark = 0;
+  bool ready = false;          // cleared by a call that ran
+};
+
+static __global__ void clear_header_kernel(uint32_t* words, uint32_t mark) {
+  words[threadIdx.x] = threadIdx.x == 1 ? mark : 0u;
+}
+
+inline void open_header(Header* h, void* workspace) {
+  static std::atomic<uint32_t> next{1};
+  h->words = static_cast<uint32_t*>(workspace);
+  h->mark = 0x45500000u + next.fetch_add(1);
+  h->ready = false;
+}
+
+inline cudaError_t header_ready(Header* h, cudaStream_t st) {
+  if (h->ready) return cudaSuccess;
+  cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
+  cudaError_t e = cudaStreamIsCapturing(st, &cap);
+  if (e != cudaSuccess) return e;
+  clear_header_kernel<<<1, kHeaderBytes / 4, 0, st>>>(h->words, h->mark);
+  e = cudaGetLastError();
+  if (e == cudaSuccess && cap == cudaStreamCaptureStatusNone) h->ready = true;
+  return e;
+}
+
+// Wait for `st`, then read and clear the error bits.
+inline cudaError_t header_report(Header* h, cudaStream_t st, uint32_t* bits) {
+  uint32_t got[2] = {0, 0};
+  *bits = 0;
+  cudaError_t e = cudaMemcpyAsync(got, h->words, sizeof(got), cudaMemcpyDeviceToHost, st);
+  if (e == cudaSuccess) e = cudaStreamSynchronize(st);
+  if (e != cudaSuccess || got[1] != h->mark || got[0] == 0) return e;
+  *bits = got[0];
+  e = cudaMemsetAsync(h->words, 0, sizeof(uint32_t), st);
+  if (e == cudaSuccess) e = cudaStreamSynchronize(st);
+  return e;
+}
+
+}  // namespace ep

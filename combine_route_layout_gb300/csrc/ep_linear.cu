@@ -6,6 +6,7 @@
 #include <cstring>
 #include <new>
 
+#include "ep_header.cuh"
 #include "ep_linear.cuh"
 
 namespace ep {
@@ -248,7 +249,7 @@ cudaError_t launch_act_grad(const GradParams& q, cudaStream_t st) {
 struct ep_linear_handle {
   ep_linear_config cfg;
   uint8_t* ws;
-  bool needs_init;
+  ep::Header header;
   int sm_count;
   int Nw;
   int64_t ldz, row_blocks;
@@ -268,8 +269,7 @@ ep_status lfail(ep_status st, const char* msg) { return record_error(st, msg); }
 ep_status lcuda(cudaError_t e) { return record_error(EP_ERR_CUDA, cudaGetErrorString(e)); }
 size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 
-constexpr size_t kHeaderBytes = 1024;   // error bits, tickets
-static_assert(256 + kLinearMaxPairs * 2 * sizeof(unsigned int) <= kHeaderBytes, "tickets");
+static_assert(kTicketOffset + kLinearMaxPairs * 2 * sizeof(unsigned int) <= kHeaderBytes, "tickets");
 
 ep_status plan_linear(const ep_linear_config* c, ep_linear_handle* h) {
   if (!c) return lfail(EP_ERR_INVALID_ARG, "linear config is NULL");
@@ -301,7 +301,7 @@ ep_status plan_linear(const ep_linear_config* c, ep_linear_handle* h) {
   h->row_blocks = (c->max_rows + kGradRows - 1) / kGradRows + c->num_groups;
   size_t off = kHeaderBytes;
   h->err = reinterpret_cast<int32_t*>(h->ws);
-  h->tickets = reinterpret_cast<unsigned int*>(h->ws ? h->ws + 256 : nullptr);
+  h->tickets = reinterpret_cast<unsigned int*>(h->ws ? h->ws + kTicketOffset : nullptr);
   h->partial = reinterpret_cast<float*>(h->ws ? h->ws + off : nullptr);
   off += kLinearMaxPairs * (c->backward ? kPartBytesGrad : kPartBytes);
   h->dz = nullptr;
@@ -316,7 +316,6 @@ ep_status plan_linear(const ep_linear_config* c, ep_linear_handle* h) {
   return EP_OK;
 }
 
-// As the router's: a captured call leaves the clearing to the next one too.
 ep_status linear_ready(ep_linear_handle* h, cudaStream_t st) {
   if (h->sm_count == 0) {
     int dev = 0, n = 0;
@@ -325,13 +324,8 @@ ep_status linear_ready(ep_linear_handle* h, cudaStream_t st) {
     if (e != cudaSuccess) return lcuda(e);
     h->sm_count = n;
   }
-  if (!h->needs_init) return EP_OK;
-  cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
-  cudaError_t e = cudaStreamIsCapturing(st, &cap);
-  if (e == cudaSuccess) e = cudaMemsetAsync(h->ws, 0, kHeaderBytes, st);
-  if (e != cudaSuccess) return lcuda(e);
-  if (cap == cudaStreamCaptureStatusNone) h->needs_init = false;
-  return EP_OK;
+  const cudaError_t e = header_ready(&h->header, st);
+  return e == cudaSuccess ? EP_OK : lcuda(e);
 }
 
 ep_status fill_linear(const ep_linear_handle* h, const void* x, const void* w,
@@ -378,8 +372,7 @@ ep_status status_of(cudaError_t e) { return e == cudaSuccess ? EP_OK : lcuda(e);
 }  // namespace
 
 extern "C" size_t ep_linear_workspace_size(const ep_linear_config* cfg) {
-  ep_linear_handle h;
-  memset(&h, 0, sizeof(h));
+  ep_linear_handle h{};
   return plan_linear(cfg, &h) == EP_OK ? h.bytes : 0;
 }
 
@@ -387,8 +380,7 @@ extern "C" ep_status ep_linear_create(const ep_linear_config* cfg, void* d_works
                                       size_t workspace_bytes, ep_linear_handle** out_handle) {
   if (!out_handle) return lfail(EP_ERR_INVALID_ARG, "out_handle is NULL");
   *out_handle = nullptr;
-  ep_linear_handle h;
-  memset(&h, 0, sizeof(h));
+  ep_linear_handle h{};
   h.ws = static_cast<uint8_t*>(d_workspace);
   const ep_status s = plan_linear(cfg, &h);
   if (s != EP_OK) return s;
@@ -397,7 +389,7 @@ extern "C" ep_status ep_linear_create(const ep_linear_config* cfg, void* d_works
   if (workspace_bytes < h.bytes) return lfail(EP_ERR_WORKSPACE, "linear workspace too small");
   ep_linear_handle* p = new (std::nothrow) ep_linear_handle(h);
   if (!p) return lfail(EP_ERR_INVALID_ARG, "out of host memory");
-  p->needs_init = true;
+  open_header(&p->header, d_workspace);
   *out_handle = p;
   return EP_OK;
 }
@@ -478,17 +470,11 @@ extern "C" ep_status ep_linear_backward(ep_linear_handle* h, const void* dy, con
 
 extern "C" ep_status ep_linear_sync(ep_linear_handle* h, void* stream) {
   if (!h) return lfail(EP_ERR_INVALID_ARG, "linear handle is NULL");
-  const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  int32_t bits = 0;
-  cudaError_t e = cudaSuccess;
-  if (!h->needs_init) {
-    e = cudaMemcpyAsync(&bits, h->err, sizeof(bits), cudaMemcpyDeviceToHost, st);
-    if (e == cudaSuccess) e = cudaMemsetAsync(h->err, 0, sizeof(bits), st);
-  }
-  if (e == cudaSuccess) e = cudaStreamSynchronize(st);
+  uint32_t bits = 0;
+  const cudaError_t e = header_report(&h->header, static_cast<cudaStream_t>(stream), &bits);
   if (e != cudaSuccess) return lcuda(e);
   if (bits & kErrLinearTimeout) {
-    h->needs_init = true;   // tickets may be left over
+    h->header.ready = false;   // tickets may be left over
     return lfail(EP_ERR_TIMEOUT, "a product's bounded wait gave up; its output is not complete");
   }
   if (bits & kErrSegment)

@@ -30,6 +30,7 @@
 #include <cstring>
 #include <new>
 
+#include "ep_header.cuh"
 #include "ep_kernels.cuh"
 
 namespace ep {
@@ -767,7 +768,11 @@ cudaError_t rows_vpl(const RouterParams& p, bool select, bool balance, int grid,
   auto kernel = select && balance ? router_rows_kernel<VPL, T, SIGMOID, true, true>
                 : select          ? router_rows_kernel<VPL, T, SIGMOID, true, false>
                                   : router_rows_kernel<VPL, T, SIGMOID, false, true>;
-  if (smem > 48 * 1024) (void)ctas_per_sm(kernel, kRouterWarps * 32, smem);   // raises its limit
+  if (smem > 48 * 1024) {
+    const cudaError_t e =
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+  }
   kernel<<<grid, kRouterWarps * 32, smem, st>>>(p);
   return cudaGetLastError();
 }
@@ -813,7 +818,7 @@ cudaError_t grad_typed(const RouterGradParams& q, int grid, cudaStream_t st) {
 struct ep_router_handle {
   ep_router_config cfg;
   uint8_t* ws;
-  bool needs_init;
+  ep::Header header;
   int stretch, stretches, n_seg, rows, chunks;
   int64_t total_chunks;
   int expert_blocks;
@@ -876,10 +881,10 @@ ep_status plan_router(const ep_router_config* c, ep_router_handle* h) {
   h->expert_blocks = (c->num_experts + kBalanceExperts - 1) / kBalanceExperts;
   if (h->total_chunks > INT32_MAX) return rfail(EP_ERR_INVALID_ARG, "router batch too large");
   if (h->n_seg > 65535) return rfail(EP_ERR_INVALID_ARG, "router seq_len gives more than 65535 segments");
-  size_t off = 256;  // error bits and ticket
+  size_t off = kHeaderBytes;  // error bits and ticket
   const size_t part = up256((size_t)h->total_chunks * c->num_experts * 4);
   h->err = reinterpret_cast<int32_t*>(h->ws);
-  h->ticket = reinterpret_cast<unsigned int*>(h->ws ? h->ws + 64 : nullptr);
+  h->ticket = reinterpret_cast<unsigned int*>(h->ws ? h->ws + kTicketOffset : nullptr);
   h->part_p = reinterpret_cast<float*>(h->ws ? h->ws + off : nullptr);
   off += part;
   h->part_n = reinterpret_cast<int32_t*>(h->ws ? h->ws + off : nullptr);
@@ -890,17 +895,9 @@ ep_status plan_router(const ep_router_config* c, ep_router_handle* h) {
   return EP_OK;
 }
 
-// Clear the error bits and the ticket before the first launch. A call that is
-// being captured clears them inside its graph and leaves that to the next
-// call too: the graph may run later, or never.
 ep_status router_ready(ep_router_handle* h, cudaStream_t st) {
-  if (!h->needs_init) return EP_OK;
-  cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
-  cudaError_t e = cudaStreamIsCapturing(st, &cap);
-  if (e == cudaSuccess) e = cudaMemsetAsync(h->ws, 0, 256, st);
-  if (e != cudaSuccess) return rcuda(e);
-  if (cap == cudaStreamCaptureStatusNone) h->needs_init = false;
-  return EP_OK;
+  const cudaError_t e = header_ready(&h->header, st);
+  return e == cudaSuccess ? EP_OK : rcuda(e);
 }
 
 ep_status fill_params(const ep_router_handle* h, const void* logits, const int32_t* num_tokens,
@@ -981,8 +978,7 @@ ep_status launch_balance(ep_router_handle* h, const RouterParams& p, int32_t* co
 }  // namespace
 
 extern "C" size_t ep_router_workspace_size(const ep_router_config* cfg) {
-  ep_router_handle h;
-  memset(&h, 0, sizeof(h));
+  ep_router_handle h{};
   return plan_router(cfg, &h) == EP_OK ? h.bytes : 0;
 }
 
@@ -990,8 +986,7 @@ extern "C" ep_status ep_router_create(const ep_router_config* cfg, void* d_works
                                       size_t workspace_bytes, ep_router_handle** out_handle) {
   if (!out_handle) return rfail(EP_ERR_INVALID_ARG, "out_handle is NULL");
   *out_handle = nullptr;
-  ep_router_handle h;
-  memset(&h, 0, sizeof(h));
+  ep_router_handle h{};
   h.ws = static_cast<uint8_t*>(d_workspace);
   const ep_status s = plan_router(cfg, &h);
   if (s != EP_OK) return s;
@@ -1000,7 +995,7 @@ extern "C" ep_status ep_router_create(const ep_router_config* cfg, void* d_works
   if (workspace_bytes < h.bytes) return rfail(EP_ERR_WORKSPACE, "router workspace too small");
   ep_router_handle* p = new (std::nothrow) ep_router_handle(h);
   if (!p) return rfail(EP_ERR_INVALID_ARG, "out of host memory");
-  p->needs_init = true;
+  open_header(&p->header, d_workspace);
   *out_handle = p;
   return EP_OK;
 }
@@ -1082,14 +1077,8 @@ extern "C" ep_status ep_router_backward(ep_router_handle* h, const void* logits,
 
 extern "C" ep_status ep_router_sync(ep_router_handle* h, void* stream) {
   if (!h) return rfail(EP_ERR_INVALID_ARG, "router handle is NULL");
-  const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  int32_t bits = 0;
-  cudaError_t e = cudaSuccess;
-  if (!h->needs_init) {
-    e = cudaMemcpyAsync(&bits, h->err, sizeof(bits), cudaMemcpyDeviceToHost, st);
-    if (e == cudaSuccess) e = cudaMemsetAsync(h->err, 0, sizeof(bits), st);
-  }
-  if (e == cudaSuccess) e = cudaStreamSynchronize(st);
+  uint32_t bits = 0;
+  const cudaError_t e = header_report(&h->header, static_cast<cudaStream_t>(stream), &bits);
   if (e != cudaSuccess) return rcuda(e);
   if (bits & kErrRouterIndex)
     return rfail(EP_ERR_INVALID_INDEX, "expert id outside [-1, num_experts) skipped");

@@ -36,11 +36,13 @@ class _Op:
     def __init__(self, nbytes: int, create, destroy, device):
         if nbytes == 0:
             raise EpError(EP_ERR_INVALID_ARG, ep.ep_last_error())
-        raw = torch.empty(nbytes + 255, dtype=torch.uint8, device=device)
-        skip = -raw.data_ptr() % 256
-        self.workspace = raw[skip:skip + nbytes]
+        self._raw = torch.empty(nbytes + 255, dtype=torch.uint8, device=device)
+        skip = -self._raw.data_ptr() % 256
+        self.workspace = self._raw[skip:skip + nbytes]
         self.device = self.workspace.device
         self._device_index = self.device.index or 0
+        # the stream that the allocator knows the workspace by, and others it was told of
+        self._streams = {_raw_stream(self._device_index)} if self.device.type == "cuda" else {0}
         self._destroy = destroy
         self._handle = create(self.workspace.data_ptr(), nbytes)
 
@@ -51,8 +53,14 @@ class _Op:
             self._handle = None
 
     def _stream(self):
-        """torch's current stream of the workspace's device, as a pointer."""
-        return _raw_stream(self._device_index)
+        """torch's current stream of the workspace's device, as a pointer. The allocator is
+        told of a stream other than the workspace's own, so that freeing the operator waits
+        for the work on it."""
+        s = _raw_stream(self._device_index)
+        if s not in self._streams:
+            self._raw.record_stream(torch.cuda.current_stream(self.device))
+            self._streams.add(s)
+        return s
 
     def _need(self, t, what: str, shape, dtype) -> int:
         """The address of a contiguous tensor of this shape and type on this device."""

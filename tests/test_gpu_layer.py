@@ -620,6 +620,36 @@ def test_linear_over_dispatch_standard_moe(layer):
     assert seen > 100
 
 
+def test_errors_are_reported_when_every_call_was_captured(layer):
+    from combine_route_layout_gb300 import ep
+    router = layer.EpRouterOp(layer.EpRouterConfig(1, 4, 8, 2))
+    l = torch.zeros((1, 4, 8), device=DEV)
+    linear = layer.EpLinearOp(layer.EpLinearConfig(2, 16, 8, 10))
+    x = torch.zeros((10, 16), dtype=torch.bfloat16, device=DEV)
+    w = torch.zeros((2, 8, 16), dtype=torch.bfloat16, device=DEV)
+    count = torch.tensor([4, 4], dtype=torch.int32, device=DEV)
+    begin = torch.tensor([0, 5], dtype=torch.int32, device=DEV)
+    router.sync()                                   # nothing ran: nothing to report
+    linear.sync()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        router.forward(l)
+        linear.forward(x, w, row_begin=begin, row_count=count)
+    router.sync()
+    linear.sync()
+    g.replay()
+    router.sync()
+    linear.sync()
+    l[0, 2, 3] = math.nan
+    count[1] = 6
+    g.replay()
+    for op, status in ((router, ep.EP_ERR_INVALID_ARG), (linear, ep.EP_ERR_INVALID_INDEX)):
+        with pytest.raises(ep.EpError) as ei:
+            op.sync()
+        assert ei.value.status == status
+        op.sync()
+
+
 # ----------------------------------------------------------- the whole layer
 
 def load_example():
@@ -666,7 +696,7 @@ def test_moe_layer_example_gradients(layer):
     counts = torch.zeros(R * E_r, device=DEV, dtype=torch.float64).index_add_(0, idx[held], torch.ones(int(held.sum()), device=DEV, dtype=torch.float64))
     bal = 0.01 * (counts * R * E_r / (k * n) * p.sum((0, 1)) / n).sum()
     assert (y.double() - out).abs()[valid].max() < 0.03 * out.abs().max()
-    assert abs(float(loss) - float(bal)) < 1e-3 * float(bal)
+    assert abs(float(loss) - float(bal.detach())) < 1e-3 * float(bal.detach())
     refs = torch.autograd.grad((out * dy.double()).sum() + bal, [*ws, xd])
     for g, ref in zip(got, refs):
         ref = ref.detach()
