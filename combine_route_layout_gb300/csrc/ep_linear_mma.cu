@@ -601,7 +601,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     int it = 0, s = 0, tails = 0;           // stages written so far, the ring's place
     uint32_t phase = 1;                     // the first pass over the ring waits for nothing
     const uint32_t full0 = in_cta(&bar->full[0], 0), empty0 = in_cta(&bar->empty[0], 1);
-    bool ok = true;
+    const uint32_t ring0 = smem_addr(ring), own0 = smem_addr(&bar->empty[0]);
+    bool ok = true, ready = false;          // ready: the place was seen to be free
     for (int i = 0; i < mine && ok; ++i) {
       Tile w;
       ok = take_tile(bar, i, w);
@@ -615,8 +616,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const CUtensorMap* map_b = &maps.b[box];
       // stage kb's operands into place `to`, their bytes on barrier `on`
       auto load = [&](int kb, int to, uint32_t on) {
-        uint8_t* a = ring + to * kStageBytes;
-        uint8_t* b = a + kStageA;
+        const uint32_t a = ring0 + to * kStageBytes, b = a + kStageA;
         const int d = kb * kDepth;
         const int row = (int)w.begin + d;                       // dW: contraction row
         if (MODE == kForward) {
@@ -665,17 +665,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         if (kb == end) break;
         if (it >= kRing) {
-          ok = mbar_wait_soon(&bar->empty[s], phase);
+          if (!ready) ok = mbar_wait_soon(&bar->empty[s], phase);
           if (!ok) break;
           if (cta == 0) mbar_signal_at(empty0 + s * 8);
         }
+        const int to = s;
         ++it;
-        mbar_signal_expect_tx_at(full0 + s * 8, bytes);
-        load(kb, s, full0 + s * 8);
         if (++s == kRing) {
           s = 0;
           phase ^= 1;
         }
+        ready = it >= kRing && mbar_test(own0 + s * 8, phase);   // its answer comes under the loads
+        mbar_signal_expect_tx_at(full0 + to * 8, bytes);
+        load(kb, to, full0 + to * 8);
       }
     }
     if (!ok) {
@@ -693,54 +695,68 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // a row (K-major) or 16 rows (MN-major) on
     constexpr bool kMnA = MODE != kForward, kMnB = MODE == kWeightGrad;
     constexpr uint32_t kStepA = (kMnA ? 2048 : 32) >> 4, kStepB = (kMnB ? 2048 : 32) >> 4;
-    const uint64_t a0 = smem_operand(smem_addr(ring), kMnA ? 8192 : 16);
-    const uint64_t b0 = smem_operand(smem_addr(ring) + kStageA, kMnB ? 8192 : 16);
-    int n_acc = 0, s = 0, tails = 0;
-    uint32_t phase = 0;
-    bool ok = true, ready = false;         // ready: the stage was seen to be full
+    constexpr uint32_t kStageUnits = kStageBytes >> 4;
+    const uint64_t op_a = smem_operand(smem_addr(ring), kMnA ? 8192 : 16);
+    const uint64_t op_b = smem_operand(smem_addr(ring) + kStageA, kMnB ? 8192 : 16);
+    const uint32_t a0 = (uint32_t)op_a, a_high = (uint32_t)(op_a >> 32);
+    const uint32_t b0 = (uint32_t)op_b, b_high = (uint32_t)(op_b >> 32);
+    const uint32_t full0 = smem_addr(&bar->full[0]), empty0 = smem_addr(&bar->empty[0]);
+    int n_acc = 0, tails = 0;
+    uint32_t s = 0, phase = 0;             // the ring's place
+    bool ok = true, ready = false;         // ready: that place was seen to be full
     for (int i = 0; i < mine && ok; ++i) {
       Tile w;
       ok = take_tile(bar, i, w);
       if (!ok) break;
       const uint32_t form = mma_form(w.n, kMnA, kMnB);
-      int stop = w.kb0;                    // end of the accumulator's sum
-      for (int kb = w.kb0; kb < w.kb1; ++kb) {
-        const bool fresh = kb == stop;
-        if (fresh) {
-          stop = kChunked ? min(w.kb1, kb + kChunk32) : w.kb1;
-          if (n_acc >= 2) {
-            ok = mbar_wait_soon(&bar->acc_empty[n_acc & 1], ((n_acc >> 1) - 1) & 1);
-            if (!ok) break;
-            tc_fence_after();
-          }
+      const int full_end = min(w.kb1, w.terms / kDepth);   // stages of 64 terms end here
+      for (int kb = w.kb0; kb < w.kb1 && ok; ++n_acc) {    // an accumulator's sum
+        const int stop = kChunked ? min(w.kb1, kb + kChunk32) : w.kb1;
+        if (n_acc >= 2) {
+          ok = mbar_wait_soon(&bar->acc_empty[n_acc & 1], ((n_acc >> 1) - 1) & 1);
+          if (!ok) break;
         }
-        const int left = w.terms - kb * kDepth;
-        int at = s;
-        if (has_tail<MODE>(w, kb)) {       // a place of its own, whose rows both CTAs cleared
-          at = kTail;
-          ok = mbar_wait_cluster(&bar->full[kTail], tails++ & 1);
-        } else if (!ready) {
-          ok = mbar_wait_soon(&bar->full[s], phase);
-        }
-        if (!ok) break;
-        tc_fence_after();
         const uint32_t d = tmem + (n_acc & 1) * 256;
-        const uint64_t a = a0 + (uint32_t)(at * (kStageBytes >> 4));
-        const uint64_t b = b0 + (uint32_t)(at * (kStageBytes >> 4));
-        if (at == s && ++s == kRing) {
-          s = 0;
-          phase ^= 1;
+        bool accumulate = false;
+        for (const int run = min(stop, full_end); kb < run; ++kb) {
+          if (!ready) ok = mbar_wait_soon(&bar->full[s], phase);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t at = s;
+          if (++s == kRing) {
+            s = 0;
+            phase ^= 1;
+          }
+          ready = mbar_test(full0 + s * 8, phase);         // its answer comes under the MMAs
+          mma_stage<kStepA, kStepB>(d, a0 + at * kStageUnits, a_high, b0 + at * kStageUnits, b_high,
+                                    form, accumulate);
+          mma_commit(empty0 + at * 8);
+          accumulate = true;
         }
-        ready = mbar_test(&bar->full[s], phase);   // its answer comes under the MMAs
-        mma_pair(d, a, b, form, !fresh);
-        if (left > 16) mma_pair(d, a + kStepA, b + kStepB, form, true);
-        if (left > 32) mma_pair(d, a + 2 * kStepA, b + 2 * kStepB, form, true);
-        if (left > 48) mma_pair(d, a + 3 * kStepA, b + 3 * kStepB, form, true);
-        mma_commit(&bar->empty[at]);
-        if (kb + 1 == stop) {
-          mma_commit(&bar->acc_full[n_acc & 1]);
-          ++n_acc;
+        if (ok && kb < stop) {             // the last stage, of fewer terms
+          uint32_t at = s;
+          if (has_tail<MODE>(w, kb)) {     // in a place of its own, whose rows both CTAs cleared
+            at = kTail;
+            ok = mbar_wait_cluster(&bar->full[kTail], tails++ & 1);
+          } else {
+            if (!ready) ok = mbar_wait_soon(&bar->full[s], phase);
+            if (++s == kRing) {
+              s = 0;
+              phase ^= 1;
+            }
+            ready = false;
+          }
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t a = a0 + at * kStageUnits, b = b0 + at * kStageUnits;
+          const int steps = (w.terms - kb * kDepth + 15) / 16;
+          for (int step = 0; step < steps; ++step)
+            mma_step(d, a + step * kStepA, a_high, b + step * kStepB, b_high, form,
+                     accumulate || step > 0);
+          mma_commit(empty0 + at * 8);
+          ++kb;
         }
+        if (ok) mma_commit(smem_addr(&bar->acc_full[n_acc & 1]));
       }
     }
     if (!ok) atomicOr(timeout, kErrLinearTimeout);

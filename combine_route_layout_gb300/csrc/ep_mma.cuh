@@ -82,15 +82,15 @@ __device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity
   return false;
 }
 
-// Whether the phase is complete, without waiting.
-__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
+// Whether the phase is complete, without waiting. `bar`: shared-memory address.
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
   uint32_t done;
   asm volatile(
       "{\n .reg .pred p;\n"
       " mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n"
       " selp.u32 %0, 1, 0, p;\n}"
       : "=r"(done)
-      : "r"(smem_addr(bar)), "r"(parity)
+      : "r"(bar), "r"(parity)
       : "memory");
   return done != 0;
 }
@@ -116,29 +116,29 @@ __device__ __forceinline__ void fence_async_shared() {
 // Tiled TMA loads into this CTA's shared memory; the bytes complete on the
 // barrier at `bar`, which may be the other CTA's of the pair. The innermost
 // coordinate is a multiple of 16 bytes.
-__device__ __forceinline__ void tma_load_2d(void* dst, const void* map, int c0, int c1,
+__device__ __forceinline__ void tma_load_2d(uint32_t dst, const void* map, int c0, int c1,
                                             uint32_t bar) {
   asm volatile(
       "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%2, %3}], [%4];" ::"r"(smem_addr(dst)),
+      " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
       "l"(map), "r"(c0), "r"(c1), "r"(bar)
       : "memory");
 }
 
-__device__ __forceinline__ void tma_load_3d(void* dst, const void* map, int c0, int c1, int c2,
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const void* map, int c0, int c1, int c2,
                                             uint32_t bar) {
   asm volatile(
       "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_addr(dst)),
+      " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
       "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(bar)
       : "memory");
 }
 
-__device__ __forceinline__ void tma_load_4d(void* dst, const void* map, int c0, int c1, int c2,
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const void* map, int c0, int c1, int c2,
                                             int c3, uint32_t bar) {
   asm volatile(
       "cp.async.bulk.tensor.4d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(smem_addr(dst)),
+      " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
       "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(bar)
       : "memory");
 }
@@ -183,20 +183,43 @@ __device__ __forceinline__ uint32_t mma_form(uint32_t n, bool a_mn_major, bool b
          ((uint32_t)b_mn_major << 16) | ((n >> 3) << 17) | ((256u >> 4) << 24);
 }
 
-__device__ __forceinline__ void mma_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t form,
-                                         bool accumulate) {
+// Four products of 16 terms each, a stage: d += a b, or d = a b + ... unless
+// `accumulate`. The operands' steps, A_STEP and B_STEP (in 16-byte units), change
+// their descriptors' low words alone. One statement: the thread that issues has
+// to stay ahead of the tensor core.
+template <uint32_t A_STEP, uint32_t B_STEP>
+__device__ __forceinline__ void mma_stage(uint32_t d, uint32_t a, uint32_t a_high, uint32_t b,
+                                          uint32_t b_high, uint32_t form, bool accumulate) {
   asm volatile(
-      "{\n .reg .pred p;\n"
-      " setp.ne.u32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d),
-      "l"(a), "l"(b), "r"(form), "r"((uint32_t)accumulate)
+      "{\n .reg .pred p, t;\n .reg .b32 x, y;\n .reg .b64 a, b;\n"
+      " setp.ne.u32 p, %6, 0;\n setp.eq.u32 t, 0, 0;\n"
+      " mov.b64 a, {%1, %2};\n mov.b64 b, {%3, %4};\n"
+      " tcgen05.mma.cta_group::2.kind::f16 [%0], a, b, %5, p;\n"
+      " add.u32 x, %1, %7;\n add.u32 y, %3, %8;\n mov.b64 a, {x, %2};\n mov.b64 b, {y, %4};\n"
+      " tcgen05.mma.cta_group::2.kind::f16 [%0], a, b, %5, t;\n"
+      " add.u32 x, %1, %9;\n add.u32 y, %3, %10;\n mov.b64 a, {x, %2};\n mov.b64 b, {y, %4};\n"
+      " tcgen05.mma.cta_group::2.kind::f16 [%0], a, b, %5, t;\n"
+      " add.u32 x, %1, %11;\n add.u32 y, %3, %12;\n mov.b64 a, {x, %2};\n mov.b64 b, {y, %4};\n"
+      " tcgen05.mma.cta_group::2.kind::f16 [%0], a, b, %5, t;\n}" ::"r"(d),
+      "r"(a), "r"(a_high), "r"(b), "r"(b_high), "r"(form), "r"((uint32_t)accumulate), "n"(A_STEP),
+      "n"(B_STEP), "n"(2 * A_STEP), "n"(2 * B_STEP), "n"(3 * A_STEP), "n"(3 * B_STEP)
+      : "memory");
+}
+
+// One product of 16 terms.
+__device__ __forceinline__ void mma_step(uint32_t d, uint32_t a, uint32_t a_high, uint32_t b,
+                                         uint32_t b_high, uint32_t form, bool accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n .reg .b64 a, b;\n"
+      " setp.ne.u32 p, %6, 0;\n mov.b64 a, {%1, %2};\n mov.b64 b, {%3, %4};\n"
+      " tcgen05.mma.cta_group::2.kind::f16 [%0], a, b, %5, p;\n}" ::"r"(d),
+      "r"(a), "r"(a_high), "r"(b), "r"(b_high), "r"(form), "r"((uint32_t)accumulate)
       : "memory");
 }
 
 // Arrive on this CTA's barrier once the MMAs issued so far are complete.
-__device__ __forceinline__ void mma_commit(uint64_t* bar) {
-  asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
-                   smem_addr(bar))
+__device__ __forceinline__ void mma_commit(uint32_t bar) {
+  asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
                : "memory");
 }
 
