@@ -15,11 +15,22 @@
 // by TMA with 128-byte swizzle into a ring of stages; one thread of the even
 // CTA issues the MMAs, the accumulators (two, so that a tile's epilogue runs
 // under the next one's products) stay in TMEM. Grid: one CTA per SM, each pair
-// walks the tiles of all groups.
+// walks the tiles of all groups. A pair reads 64 KB a stage for 8.4 MFLOP; tiles
+// of one CTA alone would read half as much again.
 //
 // Roles by warp: 0 TMA, 1 MMA, 2 clears the tails of dW's contractions, 3 works
-// out the tiles, 4-11 epilogue (TMEM lanes go by warp % 4; the
-// two warps of a quarter take every other 32 columns).
+// out the tiles, 4-11 epilogue (TMEM lanes go by warp % 4; the two warps of a
+// quarter take every other 32 columns). TMA, MMA and tiles are one thread each,
+// whose loop must take less than a stage's products, 512 cycles: it takes about
+// 280, and an epilogue's warps beside it slow it down.
+//
+// What bounds it. Long products run at the tensor core's rate in cycles (512 a
+// stage) and at the power limit in time: 32768 x 4096 x 4096 dense 1.70 PFLOP/s at
+// 1.6 GHz (the library's product 1.77); 128 experts of 973 rows, 4096 x 4096,
+// SwiGLU with pre-activation, 1.42-1.47 at 1.3 GHz, where the experts' weights
+// come from HBM as well. From idle clocks: 8192^3 1.9 PFLOP/s. Few rows an expert:
+// HBM (256 experts x 32 rows, 7168 x 1024: 6.5 TB/s). Small products: launch, set-up
+// and pipeline latency (about 8 us) and the stages of a tile one after another.
 #include <cuda.h>
 
 #include <atomic>
@@ -218,7 +229,8 @@ __device__ __forceinline__ bool has_tail(const Tile& w, int kb) {
 // then 64 rows use more of the SMs at the cost of reading the weights more
 // often; what is still idle then takes parts of the tiles' contractions, whose
 // f32 sums the last part to finish adds up. 1024 x 7168 x 256: 43.7 us as 4
-// tiles of 256 rows, 27.5 us as 16 tiles of 64 rows in 4 parts each.
+// tiles of 256 rows, 27.5 us as 16 tiles of 64 rows in 4 parts each (as measured
+// when it was built; 19.4 us now).
 template <int MODE>
 __device__ Plan plan_tiles(const MmaParams& q, int base_cap, int* first, int* begins, int* counts,
                            int* sizes) {
