@@ -1,0 +1,36 @@
+// Launches whose start overlaps the end of the kernel before them (programmatic
+// dependent launch). The kernel calls begin_overlapped() before its first access
+// to global memory: what comes ahead of it (barriers, TMEM, constant operands) is
+// set up while the kernel before still runs, everything after it sees that
+// kernel's writes. A kernel that is followed by one of these lets it start as
+// soon as all of its own CTAs have.
+#pragma once
+
+#include "ep_kernels.cuh"
+
+namespace ep {
+
+#ifdef __CUDACC__
+__device__ __forceinline__ void begin_overlapped() {
+  pdl_launch_dependents();
+  pdl_wait();
+}
+#endif
+
+template <typename... Params, typename... Args>
+inline cudaError_t launch_overlapped(void (*kernel)(Params...), dim3 grid, int block, size_t smem,
+                                     cudaStream_t st, const Args&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3((unsigned)block);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+}  // namespace ep

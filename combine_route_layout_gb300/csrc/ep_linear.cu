@@ -7,6 +7,7 @@
 #include <new>
 
 #include "ep_header.cuh"
+#include "ep_launch.cuh"
 #include "ep_linear.cuh"
 
 namespace ep {
@@ -75,6 +76,7 @@ struct BlockPlace {
 
 template <int VEC, int ACT, typename T>
 __global__ void __launch_bounds__(kGradThreads) act_grad_kernel(GradParams q) {
+  begin_overlapped();
   const LinearParams& p = q.p;
   __shared__ BlockPlace at;
   const bool gated = ACT == EP_ACT_SWIGLU;
@@ -182,6 +184,7 @@ __global__ void __launch_bounds__(kGradThreads) act_grad_kernel(GradParams q) {
 // db_g: the sums of the group's blocks, in block order. A CTA takes 32
 // columns, a warp every 8th block.
 __global__ void __launch_bounds__(256) bias_grad_kernel(GradParams q) {
+  begin_overlapped();
   const LinearParams& p = q.p;
   __shared__ float sum[8][32];
   __shared__ int64_t range[2];
@@ -223,16 +226,14 @@ cudaError_t grad_typed(GradParams q, cudaStream_t st) {
   while (q.lanes < 8 && q.p.N * q.lanes * 2 <= kGradThreads * VEC) q.lanes *= 2;
   const int wide = kGradThreads / q.lanes;
   const dim3 grid((unsigned)q.row_blocks, (q.p.N + wide * VEC - 1) / (wide * VEC));
+  auto kernel = act_grad_kernel<VEC, EP_ACT_NONE, T>;
   switch (q.p.act) {
-    case EP_ACT_RELU: act_grad_kernel<VEC, EP_ACT_RELU, T><<<grid, kGradThreads, 0, st>>>(q); break;
-    case EP_ACT_SILU: act_grad_kernel<VEC, EP_ACT_SILU, T><<<grid, kGradThreads, 0, st>>>(q); break;
-    case EP_ACT_GELU: act_grad_kernel<VEC, EP_ACT_GELU, T><<<grid, kGradThreads, 0, st>>>(q); break;
-    case EP_ACT_SWIGLU:
-      act_grad_kernel<VEC, EP_ACT_SWIGLU, T><<<grid, kGradThreads, 0, st>>>(q);
-      break;
-    default: act_grad_kernel<VEC, EP_ACT_NONE, T><<<grid, kGradThreads, 0, st>>>(q);
+    case EP_ACT_RELU: kernel = act_grad_kernel<VEC, EP_ACT_RELU, T>; break;
+    case EP_ACT_SILU: kernel = act_grad_kernel<VEC, EP_ACT_SILU, T>; break;
+    case EP_ACT_GELU: kernel = act_grad_kernel<VEC, EP_ACT_GELU, T>; break;
+    case EP_ACT_SWIGLU: kernel = act_grad_kernel<VEC, EP_ACT_SWIGLU, T>; break;
   }
-  return cudaGetLastError();
+  return launch_overlapped(kernel, grid, kGradThreads, 0, st, q);
 }
 
 cudaError_t launch_act_grad(const GradParams& q, cudaStream_t st) {
@@ -459,8 +460,8 @@ extern "C" ep_status ep_linear_backward(ep_linear_handle* h, const void* dy, con
   if ((q.dz || q.part) && q.row_blocks > 0 && (s = status_of(launch_act_grad(q, st))) != EP_OK)
     return s;
   if (dbias) {
-    bias_grad_kernel<<<dim3((p.Nw + 31) / 32, p.s.G), 256, 0, st>>>(q);
-    if ((s = status_of(cudaGetLastError())) != EP_OK) return s;
+    s = status_of(launch_overlapped(bias_grad_kernel, dim3((p.Nw + 31) / 32, p.s.G), 256, 0, st, q));
+    if (s != EP_OK) return s;
   }
   p.dz = in_place ? static_cast<const __nv_bfloat16*>(dy) : h->dz;
   if (in_place) p.ldz = p.N;

@@ -36,6 +36,7 @@
 #include <atomic>
 #include <cstring>
 
+#include "ep_launch.cuh"
 #include "ep_linear.cuh"
 #include "ep_mma.cuh"
 
@@ -598,6 +599,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   __syncthreads();
   cluster_arrive();                      // the barriers are ready; the wait is below
   if (warp == 1) tmem_alloc(&bar->tmem, kTmemColumns);
+  begin_overlapped();
   const Plan plan = plan_tiles<MODE>(q, kChunked ? kMaxRows / 2 : kMaxRows, first, begins, counts, sizes);
   const int units = plan.tiles * plan.splits;
   tc_fence_before();
@@ -1001,8 +1003,7 @@ cudaError_t launch_tiles(const Maps& maps, MmaParams& q, int grid, cudaStream_t 
     if (e != cudaSuccess) return e;
     raised.fetch_or(bit, std::memory_order_relaxed);
   }
-  product_kernel<MODE, ACT, T><<<grid, kThreads, smem, st>>>(maps, q);
-  return cudaGetLastError();
+  return launch_overlapped(product_kernel<MODE, ACT, T>, dim3((unsigned)grid), kThreads, smem, st, maps, q);
 }
 
 int grid_of(int sms, int64_t tiles) {

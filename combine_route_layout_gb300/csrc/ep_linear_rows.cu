@@ -11,6 +11,7 @@
 // 4096, in us, against that kernel: one row 8.2 (12.3), two 10.3 (12.3), three
 // 16.4 (12.3): every row more has its loads of x and its conversions, so more
 // than two rows go to the tensor cores. N 256: 4.9, 5.1, 8.2 (10.3).
+#include "ep_launch.cuh"
 #include "ep_linear.cuh"
 
 namespace ep {
@@ -29,6 +30,7 @@ __device__ __forceinline__ void unpack8(uint4 q, float (&v)[8]) {
 
 template <int R, int FEATURES, bool GATED>
 __global__ void __launch_bounds__(kWarps * 32) few_rows_kernel(LinearParams p, int split) {
+  begin_overlapped();
   constexpr int kUnroll = 4;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   __shared__ float joined[kWarps][FEATURES * R];
@@ -140,8 +142,8 @@ cudaError_t launch(const LinearParams& p, int sms, cudaStream_t st) {
   int split = 1;
   while (split < kWarps && shares * split < (int64_t)sms * 24 && split * 256 < p.K) split *= 2;
   const int64_t ctas = (shares * split + kWarps - 1) / kWarps;
-  few_rows_kernel<R, FEATURES, GATED><<<(unsigned)ctas, kWarps * 32, 0, st>>>(p, split);
-  return cudaGetLastError();
+  return launch_overlapped(few_rows_kernel<R, FEATURES, GATED>, dim3((unsigned)ctas), kWarps * 32, 0,
+                           st, p, split);
 }
 
 }  // namespace

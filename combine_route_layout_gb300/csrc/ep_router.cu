@@ -34,6 +34,7 @@
 
 #include "ep_header.cuh"
 #include "ep_kernels.cuh"
+#include "ep_launch.cuh"
 
 namespace ep {
 namespace {
@@ -404,7 +405,7 @@ __device__ __forceinline__ void select_experts(const RouterParams& p, int lane, 
 // and rows per expert for the loss (of the chosen, or of given indices).
 template <int VPL, typename T, bool SIGMOID, bool SELECT, bool BALANCE>
 __global__ void __launch_bounds__(kRouterWarps * 32) router_rows_kernel(RouterParams p) {
-  if (BALANCE) pdl_launch_dependents();   // the reduction may be set up
+  begin_overlapped();
   extern __shared__ __align__(16) float smem[];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const RowPlace at = place_of(p, blockIdx.x);
@@ -528,7 +529,7 @@ __global__ void __launch_bounds__(kBalanceThreads) balance_reduce_kernel(Balance
   const int seg = blockIdx.y;
   const int first = p.n_seg == 1 ? 0 : seg * p.chunks;
   const int n_chunk = p.n_seg == 1 ? p.R * p.stretches * p.chunks : p.chunks;
-  pdl_wait();
+  begin_overlapped();
   float s = 0.0f;
   int n = 0;
   if (e < p.E) {
@@ -597,6 +598,7 @@ __global__ void __launch_bounds__(kBalanceThreads) balance_reduce_kernel(Balance
 // row's logits have to be read in any case (softmax's needs them all).
 template <int VPL, typename T, bool SIGMOID>
 __global__ void __launch_bounds__(kRouterWarps * 32) router_grad_kernel(RouterGradParams q) {
+  begin_overlapped();
   const RouterParams& p = q.r;
   extern __shared__ __align__(16) float smem[];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -775,15 +777,14 @@ cudaError_t rows_vpl(const RouterParams& p, bool select, bool balance, int grid,
         cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
   }
-  kernel<<<grid, kRouterWarps * 32, smem, st>>>(p);
-  return cudaGetLastError();
+  return launch_overlapped(kernel, dim3((unsigned)grid), kRouterWarps * 32, smem, st, p);
 }
 
 template <int VPL, typename T, bool SIGMOID>
 cudaError_t grad_vpl(const RouterGradParams& q, int grid, cudaStream_t st) {
   const size_t smem = q.d_w ? (size_t)kRouterWarps * 32 * VPL * 4 : 0;
-  router_grad_kernel<VPL, T, SIGMOID><<<grid, kRouterWarps * 32, smem, st>>>(q);
-  return cudaGetLastError();
+  return launch_overlapped(router_grad_kernel<VPL, T, SIGMOID>, dim3((unsigned)grid),
+                           kRouterWarps * 32, smem, st, q);
 }
 
 // Calls f<VPL, T, SIGMOID> for the config's sizes and types.
@@ -964,16 +965,8 @@ ep_status launch_balance(ep_router_handle* h, const RouterParams& p, int32_t* co
   b.coef = coef_of(h, p);
   b.part_p = h->part_p; b.part_n = h->part_n; b.part_loss = h->part_loss;
   b.ticket = h->ticket; b.counts = counts; b.loss = loss;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(h->expert_blocks, h->n_seg);
-  cfg.blockDim = dim3(kBalanceThreads);
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];   // set up while the rows are still being read
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, balance_reduce_kernel, b);
+  const cudaError_t e = launch_overlapped(balance_reduce_kernel, dim3(h->expert_blocks, h->n_seg),
+                                          kBalanceThreads, 0, st, b);
   return e == cudaSuccess ? EP_OK : rcuda(e);
 }
 

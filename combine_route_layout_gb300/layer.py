@@ -142,13 +142,12 @@ class EpRouterOp(_Op):
         """The counts as a C array; the same counts as last time are not converted again."""
         if num_tokens is None:
             return None
-        if num_tokens is not self._last_array:
-            if len(num_tokens) != self.config.world_size:
-                _refuse("num_tokens must give one count per source rank")
-            values = [int(n) for n in num_tokens]
-            if values != self._last_tokens:
-                self._last_array = ep._i32_array(values)
-                self._last_tokens = values
+        if type(num_tokens) is list and num_tokens == self._last_tokens:
+            return self._last_array
+        if len(num_tokens) != self.config.world_size:
+            _refuse("num_tokens must give one count per source rank")
+        self._last_tokens = [int(n) for n in num_tokens]
+        self._last_array = ep._i32_array(self._last_tokens)
         return self._last_array
 
     def forward(self, logits, bias=None, num_tokens=None, balance=False):
