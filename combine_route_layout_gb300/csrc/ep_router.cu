@@ -43,7 +43,7 @@ constexpr int kRouterWarps = 8;
 constexpr int kRouterRows = 64;      // most rows of one CTA, all of one segment
 constexpr int kRouterCtas = 4 * 152; // CTAs that a batch is spread over, where it has the rows
 constexpr int kMaxGroups = EP_MAX_ROUTER_GROUPS;
-constexpr int kErrNotFinite = 1;     // a logit was NaN or +inf
+constexpr int kErrNotFinite = 1;     // a logit was NaN or +inf, or a bias NaN
 constexpr int kErrRouterIndex = 2;   // an expert id outside [-1, E)
 
 struct RouterParams {
@@ -417,11 +417,15 @@ __global__ void __launch_bounds__(kRouterWarps * 32) router_rows_kernel(RouterPa
     __syncthreads();
   }
   float sum_p[VPL], bias[VPL];
+  bool bad_bias = false;       // NaN: -inf instead, which leaves the expert out
 #pragma unroll
   for (int i = 0; i < VPL; ++i) {
     sum_p[i] = 0.0f;
     bias[i] = SIGMOID && SELECT && p.bias && lane * VPL + i < p.E ? __ldg(p.bias + lane * VPL + i) : 0.0f;
+    bad_bias |= isnan(bias[i]);
+    if (isnan(bias[i])) bias[i] = -INFINITY;
   }
+  if (bad_bias) atomicOr(p.err, kErrNotFinite);
   const T* logits = static_cast<const T*>(p.logits);
   const int end = at.t0 + at.n;
   float next[VPL];
@@ -1078,6 +1082,6 @@ extern "C" ep_status ep_router_sync(ep_router_handle* h, void* stream) {
   if (bits & kErrRouterIndex)
     return rfail(EP_ERR_INVALID_INDEX, "expert id outside [-1, num_experts) skipped");
   if (bits & kErrNotFinite)
-    return rfail(EP_ERR_INVALID_ARG, "a logit was NaN or +inf and was left out");
+    return rfail(EP_ERR_INVALID_ARG, "a logit was NaN or +inf, or a bias NaN: its expert was left out");
   return EP_OK;
 }

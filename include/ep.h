@@ -564,7 +564,9 @@ void ep_router_destroy(ep_router_handle* h);
 /*
  *   logits      device [R][Tmax][E], logits_dtype
  *   bias        device [E] f32 or NULL: added to sigmoid scores for the selection
- *               alone (EP_ERR_UNSUPPORTED with softmax scores)
+ *               alone (EP_ERR_UNSUPPORTED with softmax scores). -inf leaves an
+ *               expert out of it; so does NaN, which raises EP_ERR_INVALID_ARG
+ *               at ep_router_sync
  *   num_tokens  host [R] or NULL (all Tmax)
  *   indices     device [R][Tmax][k] out; -1 in rows past num_tokens
  *   weights     device [R][Tmax][k] f32 out; 0 there

@@ -343,6 +343,38 @@ def test_router_reports_bad_values(layer):
     assert int(counts.sum()) == 6
 
 
+@pytest.mark.parametrize("E,groups,stay", [(256, 1, 1), (256, 8, 4), (256, 32, 2), (96, 4, 2), (30, 3, 2), (7, 1, 1)])
+def test_router_bias_that_is_not_finite(layer, E, groups, stay):
+    """A bias of -inf or NaN leaves its expert out of the selection, NaN is reported; rows
+    with no expert left hold index -1 and weight 0."""
+    from combine_route_layout_gb300 import ep
+    g = torch.Generator(device="cpu").manual_seed(E + groups)
+    k = 4
+    op = layer.EpRouterOp(layer.EpRouterConfig(1, 37, E, k, score_func="sigmoid", num_groups=groups,
+                                               topk_groups=stay))
+    l = torch.randn((1, 37, E), generator=g).to(DEV)
+    w, idx = op.forward(l, bias=torch.full((E,), -math.inf, device=DEV))
+    op.sync()
+    assert (idx == -1).all() and (w == 0).all()
+    w, idx = op.forward(l, bias=torch.full((E,), math.nan, device=DEV))
+    with pytest.raises(ep.EpError) as ei:
+        op.sync()
+    assert ei.value.status == ep.EP_ERR_INVALID_ARG
+    assert (idx == -1).all() and (w == 0).all()
+    bias = torch.zeros(E)
+    bias[0], bias[E // 2], bias[E - 1] = math.nan, -math.inf, math.nan
+    w, idx = op.forward(l, bias=bias.to(DEV))
+    with pytest.raises(ep.EpError):
+        op.sync()
+    out = bias.clone()
+    out[[0, E // 2, E - 1]] = -math.inf
+    w2, idx2 = op.forward(l, bias=out.to(DEV))
+    op.sync()
+    assert torch.equal(idx, idx2) and torch.equal(w, w2)
+    assert not torch.isin(idx, torch.tensor([0, E // 2, E - 1], device=DEV)).any()
+    assert (idx >= 0).all() and torch.allclose(w.sum(-1), torch.ones((), device=DEV), rtol=0, atol=7 * 2.0 ** -24)
+
+
 def test_router_on_another_stream_and_in_a_graph(layer):
     cfg = layer.EpRouterConfig(4, 64, 64, 6, score_func="sigmoid")
     op = layer.EpRouterOp(cfg)
