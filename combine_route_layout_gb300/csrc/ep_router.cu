@@ -41,7 +41,12 @@ namespace {
 
 constexpr int kRouterWarps = 8;
 constexpr int kRouterRows = 64;      // most rows of one CTA, all of one segment
-constexpr int kRouterCtas = 4 * 152; // CTAs that a batch is spread over, where it has the rows
+// CTAs that are resident on an SM with the registers that `vpl` experts a lane
+// take (the selection's: a batch is spread over as many, where it has the rows).
+constexpr int router_ctas(int vpl, bool select = true) {
+  if (!select) return vpl <= 8 ? 5 : vpl == 16 ? 3 : 2;
+  return vpl <= 4 ? 5 : vpl == 8 ? 4 : vpl == 16 ? 2 : 1;
+}
 constexpr int kMaxGroups = EP_MAX_ROUTER_GROUPS;
 constexpr int kErrNotFinite = 1;     // a logit was NaN or +inf, or a bias NaN
 constexpr int kErrRouterIndex = 2;   // an expert id outside [-1, E)
@@ -259,11 +264,24 @@ __device__ __forceinline__ RowPlace place_of(const RouterParams& p, int c) {
 
 // Whether this lane's group is one of the topk_groups best, ties to the lowest
 // group, by its two best scores. Groups are runs of `run` lanes (a power of
-// two), whose lanes all bring the same values.
+// two), whose lanes all bring the same values. Up to eight groups count the
+// better ones of the others, in shuffles that wait for nothing; more would take
+// more of them than rounds of the largest do.
 template <bool SIGMOID>
 __device__ __forceinline__ bool group_stays(const RouterParams& p, float best, float second,
                                             int lane, int run) {
   if (SIGMOID && second > -INFINITY) best = __fadd_rn(best, second);
+  if (run >= 4) {
+    int better = 0;
+#pragma unroll
+    for (int i = 1; i < 8; ++i) {
+      if (i * run >= 32) break;
+      const float other = __shfl_xor_sync(kFull, best, i * run);
+      const bool lower = (lane ^ (i * run)) < lane;
+      better += lower ? other >= best : other > best;
+    }
+    return better < p.topk_groups && best > -INFINITY;
+  }
   bool stays = false;
   for (int j = 0; j < p.topk_groups; ++j) {
     const float m = redux_max(best);
@@ -297,9 +315,9 @@ __device__ __forceinline__ void drop_groups(const RouterParams& p, int lane, con
     if (lane * VPL + i < p.E && !((kept >> ((lane * VPL + i) / size)) & 1u)) c[i] = -INFINITY;
 }
 
-template <int VPL>
+template <int VPL, int STRIDE = VPL>
 __device__ __forceinline__ void put_row(float* buf, int lane, const float (&c)[VPL]) {
-  float* at = buf + lane * VPL;
+  float* at = buf + lane * STRIDE;
   if (VPL % 4 == 0) {
 #pragma unroll
     for (int i = 0; i < VPL; i += 4)
@@ -311,8 +329,22 @@ __device__ __forceinline__ void put_row(float* buf, int lane, const float (&c)[V
   }
 }
 
+// A warp's shared memory for the selection, in words: its scores by expert; each
+// lane's sorted scores and a -inf that ends them, whole 16-byte pieces apart
+// whose distance keeps the lanes' accesses off each other's banks; the slots;
+// sigmoid: s by expert.
+template <int VPL>
+constexpr int kSortedStride = VPL + (VPL % 4 == 0 ? 4 : 1);
+template <int VPL>
+constexpr int kSlotsAt = 32 * VPL + 32 * kSortedStride<VPL>;
+template <int VPL>
+constexpr int kScoresAt = kSlotsAt<VPL> + 64;
+template <int VPL, bool SIGMOID>
+constexpr int kSelectWords = kScoresAt<VPL> + (SIGMOID ? 32 * VPL : 0);
+
 // The k best of the warp's scores c (-inf: none), in order, ties to the lowest
-// expert: lane j gets slot j's expert (-1: none left) and score.
+// expert: lane j gets slot j's expert (-1: none left) and score. No score is
+// NaN, so that every round has a winner.
 template <int VPL, bool SIGMOID>
 __device__ __forceinline__ void select_experts(const RouterParams& p, int lane, float* buf,
                                                float (&c)[VPL], int& expert, float& score) {
@@ -340,27 +372,32 @@ __device__ __forceinline__ void select_experts(const RouterParams& p, int lane, 
     }
   }
   // a lane's sorted scores wait in shared memory, the next one in `head`: a
-  // pop is one load for the lane that won
+  // round is one store and one load for the lane that won, the lowest of those
+  // with the largest head
   float* sorted = buf + 32 * VPL;
-  if (VPL > 1) {
-    put_row<VPL>(sorted, lane, c);
-    __syncwarp();
-  }
-  float head = c[0], mine = -INFINITY;
-  int from = 0, taken = 1;
+  float2* slots = reinterpret_cast<float2*>(buf + kSlotsAt<VPL>);
+  put_row<VPL, kSortedStride<VPL>>(sorted, lane, c);
+  const uint32_t below = (1u << lane) - 1;
+  const int stop = lane * kSortedStride<VPL> + VPL;   // holds -inf
+  int next = stop - VPL;
+  float head = c[0];
 #pragma unroll 4
   for (int j = 0; j < p.k; ++j) {
     const float m = redux_max(head);
-    const int win = __ffs(__ballot_sync(kFull, head == m)) - 1;
-    if (lane == j) {
-      from = win;
-      mine = m;
+    const uint32_t equal = __ballot_sync(kFull, head == m);
+    if (head == m && !(equal & below)) {
+      slots[j] = make_float2(m, __int_as_float(lane));
+      next = min(next + 1, stop);
+      head = sorted[next];
     }
-    if (lane == win) {
-      head = -INFINITY;
-      if (taken < VPL) head = sorted[lane * VPL + taken];
-      ++taken;
-    }
+  }
+  __syncwarp();
+  int from = 0;
+  float mine = -INFINITY;
+  if (lane < p.k) {
+    const float2 slot = slots[lane];
+    mine = slot.x;
+    from = __float_as_int(slot.y);
   }
   // slot j's expert: among the winner's, the one with its score
   const float* row = buf + from * VPL;
@@ -404,13 +441,15 @@ __device__ __forceinline__ void select_experts(const RouterParams& p, int lane, 
 // SELECT: choose the experts, write indices and weights. BALANCE: sums of p
 // and rows per expert for the loss (of the chosen, or of given indices).
 template <int VPL, typename T, bool SIGMOID, bool SELECT, bool BALANCE>
-__global__ void __launch_bounds__(kRouterWarps * 32) router_rows_kernel(RouterParams p) {
+__global__ void __launch_bounds__(kRouterWarps * 32, router_ctas(VPL, SELECT))
+    router_rows_kernel(RouterParams p) {
   begin_overlapped();
   extern __shared__ __align__(16) float smem[];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const RowPlace at = place_of(p, blockIdx.x);
-  constexpr int kRow = (SELECT ? 2 : 1) * 32 * VPL;            // scores, sorted scores; sums of p
+  constexpr int kRow = SELECT ? kSelectWords<VPL, SIGMOID> : 32 * VPL;   // and for the sums of p
   float* buf = smem + warp * kRow;
+  if (SELECT) buf[32 * VPL + lane * kSortedStride<VPL> + VPL] = -INFINITY;
   int* cnt = reinterpret_cast<int*>(smem + kRouterWarps * kRow);
   if (BALANCE) {
     for (int e = threadIdx.x; e < p.E; e += blockDim.x) cnt[e] = 0;
@@ -462,12 +501,15 @@ __global__ void __launch_bounds__(kRouterWarps * 32) router_rows_kernel(RouterPa
       }
       int e;
       float v;
+      if (SIGMOID && p.bias) {
+        __syncwarp();
+        put_row<VPL>(buf + kScoresAt<VPL>, lane, pr);
+      }
       select_experts<VPL, SIGMOID>(p, lane, buf, c, e, v);
       float wt = 0.0f;
       if (SIGMOID) {
-        // with a bias the slot's own score is made again from its logit
         float s = 0.0f;
-        if (e >= 0) s = p.bias ? sigmoid((float)logits[g * p.E + e]) : v;
+        if (e >= 0) s = p.bias ? buf[kScoresAt<VPL> + e] : v;
         const float d = p.normalize ? warp_sum(s) : 1.0f;
         wt = d > 0.0f ? s / d : 0.0f;
       } else if (p.normalize) {
@@ -516,16 +558,23 @@ __global__ void __launch_bounds__(kRouterWarps * 32) router_rows_kernel(RouterPa
 }
 
 // Counts and loss from the chunks' sums, added in a fixed order: CTA (b, s)
-// takes 8 experts of segment s, 32 threads an expert, and the last CTA adds the
-// products. Latency bound: few experts a CTA make many CTAs, whose loads are in
-// flight together (32 experts a CTA: 10 us for 512 chunks).
+// takes 8 experts of segment s, 32 threads an expert or more, and the last CTA
+// adds the products. Latency bound: few experts a CTA make many CTAs, and threads
+// enough for the chunks have all loads in flight together (32 experts a CTA of
+// 256 threads: 10 us for 512 chunks).
 constexpr int kBalanceExperts = 8;
-constexpr int kBalanceThreads = 256;
+constexpr int kBalanceThreads = 1024;      // at most
+
+int balance_threads(int n_chunk) {
+  int threads = 256;
+  while (threads < kBalanceThreads && threads < n_chunk) threads *= 2;
+  return threads;
+}
 
 __global__ void __launch_bounds__(kBalanceThreads) balance_reduce_kernel(BalanceParams p) {
-  constexpr int kWarps = kBalanceThreads / 32;
-  __shared__ float sp[kWarps][kBalanceExperts];
-  __shared__ int sn[kWarps][kBalanceExperts];
+  __shared__ float sp[kBalanceThreads / 32][kBalanceExperts];
+  __shared__ int sn[kBalanceThreads / 32][kBalanceExperts];
+  const int threads = blockDim.x, warps = threads / 32;
   __shared__ bool last;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int in = threadIdx.x % kBalanceExperts;
@@ -538,7 +587,7 @@ __global__ void __launch_bounds__(kBalanceThreads) balance_reduce_kernel(Balance
   int n = 0;
   if (e < p.E) {
 #pragma unroll 8
-    for (int c = threadIdx.x / kBalanceExperts; c < n_chunk; c += kBalanceThreads / kBalanceExperts) {
+    for (int c = threadIdx.x / kBalanceExperts; c < n_chunk; c += threads / kBalanceExperts) {
       s += __ldcg(p.part_p + (int64_t)(first + c) * p.E + e);
       n += __ldcg(p.part_n + (int64_t)(first + c) * p.E + e);
     }
@@ -558,8 +607,8 @@ __global__ void __launch_bounds__(kBalanceThreads) balance_reduce_kernel(Balance
     if (lane < kBalanceExperts && e < p.E) {
       s = 0.0f;
       n = 0;
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
+#pragma unroll 8
+      for (int w = 0; w < warps; ++w) {
         s += sp[w][lane];
         n += sn[w][lane];
       }
@@ -585,13 +634,13 @@ __global__ void __launch_bounds__(kBalanceThreads) balance_reduce_kernel(Balance
   __threadfence();
   const int m = gridDim.x * gridDim.y;
   float acc = 0.0f;
-  for (int i = threadIdx.x; i < m; i += kBalanceThreads) acc += __ldcg(p.part_loss + i);
+  for (int i = threadIdx.x; i < m; i += threads) acc += __ldcg(p.part_loss + i);
   acc = warp_sum(acc);
   if (lane == 0) sp[warp][0] = acc;
   __syncthreads();
   if (threadIdx.x == 0) {
     float v = 0.0f;
-    for (int w = 0; w < kWarps; ++w) v += sp[w][0];
+    for (int w = 0; w < warps; ++w) v += sp[w][0];
     *p.loss = v * p.coef;
     *p.ticket = 0u;
   }
@@ -601,7 +650,8 @@ __global__ void __launch_bounds__(kBalanceThreads) balance_reduce_kernel(Balance
 // logits, one pass: the scores are computed again rather than kept, since a
 // row's logits have to be read in any case (softmax's needs them all).
 template <int VPL, typename T, bool SIGMOID>
-__global__ void __launch_bounds__(kRouterWarps * 32) router_grad_kernel(RouterGradParams q) {
+__global__ void __launch_bounds__(kRouterWarps * 32, router_ctas(VPL))
+    router_grad_kernel(RouterGradParams q) {
   begin_overlapped();
   const RouterParams& p = q.r;
   extern __shared__ __align__(16) float smem[];
@@ -771,8 +821,8 @@ __global__ void __launch_bounds__(kRouterWarps * 32) router_grad_kernel(RouterGr
 
 template <int VPL, typename T, bool SIGMOID>
 cudaError_t rows_vpl(const RouterParams& p, bool select, bool balance, int grid, cudaStream_t st) {
-  const size_t row = (size_t)kRouterWarps * 32 * VPL * 4;
-  const size_t smem = (select ? 2 * row : row) + (balance ? (size_t)p.E * 4 : 0);
+  const size_t row = select ? kSelectWords<VPL, SIGMOID> : 32 * VPL;
+  const size_t smem = kRouterWarps * row * 4 + (balance ? (size_t)p.E * 4 : 0);
   auto kernel = select && balance ? router_rows_kernel<VPL, T, SIGMOID, true, true>
                 : select          ? router_rows_kernel<VPL, T, SIGMOID, true, false>
                                   : router_rows_kernel<VPL, T, SIGMOID, false, true>;
@@ -845,6 +895,13 @@ ep_status rfail(ep_status st, const char* msg) { return record_error(st, msg); }
 
 ep_status rcuda(cudaError_t e) { return record_error(EP_ERR_CUDA, cudaGetErrorString(e)); }
 
+// Experts that a lane holds.
+int vpl_of(int experts) {
+  int vpl = 1;
+  while (32 * vpl < experts) vpl *= 2;
+  return vpl;
+}
+
 size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 
 // Validate the config and lay the workspace out in `h`.
@@ -881,7 +938,8 @@ ep_status plan_router(const ep_router_config* c, ep_router_handle* h) {
   h->n_seg = c->seq_len > 0 ? c->world_size * h->stretches : 1;
   // rows of a CTA: enough CTAs to fill the GPU, few enough sums to add up
   const int64_t all = (int64_t)c->world_size * T;
-  int64_t rows = ((all + kRouterCtas - 1) / kRouterCtas + kRouterWarps - 1) / kRouterWarps * kRouterWarps;
+  const int64_t ctas = router_ctas(vpl_of(c->num_experts)) * 152;
+  int64_t rows = ((all + ctas - 1) / ctas + kRouterWarps - 1) / kRouterWarps * kRouterWarps;
   h->rows = (int)(rows < kRouterWarps ? kRouterWarps : rows > kRouterRows ? kRouterRows : rows);
   h->chunks = (h->stretch + h->rows - 1) / h->rows;
   h->total_chunks = (int64_t)c->world_size * h->stretches * h->chunks;
@@ -923,8 +981,7 @@ ep_status fill_params(const ep_router_handle* h, const void* logits, const int32
   p->R = c.world_size; p->Tmax = c.max_num_inp_token_per_rank;
   p->E = c.num_experts; p->k = c.num_experts_per_token;
   p->groups = c.num_groups; p->topk_groups = c.topk_groups;
-  int vpl = 1;
-  while (32 * vpl < c.num_experts) vpl *= 2;
+  const int vpl = vpl_of(c.num_experts);
   const int held = c.num_experts / c.num_groups, run = held / vpl;
   p->groups_run = held % vpl == 0 && (run & (run - 1)) == 0 ? run : 0;
   p->normalize = c.normalize_weights != 0;
@@ -970,7 +1027,8 @@ ep_status launch_balance(ep_router_handle* h, const RouterParams& p, int32_t* co
   b.part_p = h->part_p; b.part_n = h->part_n; b.part_loss = h->part_loss;
   b.ticket = h->ticket; b.counts = counts; b.loss = loss;
   const cudaError_t e = launch_overlapped(balance_reduce_kernel, dim3(h->expert_blocks, h->n_seg),
-                                          kBalanceThreads, 0, st, b);
+                                          balance_threads((int)(h->total_chunks / (h->n_seg == 1 ? 1 : h->n_seg))),
+                                          0, st, b);
   return e == cudaSuccess ? EP_OK : rcuda(e);
 }
 
