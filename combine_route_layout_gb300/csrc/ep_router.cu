@@ -150,18 +150,33 @@ __device__ __forceinline__ void sort_down(float (&v)[N]) {
           }
 }
 
+// Elements that a lane reads and writes at a time: 16 bytes, or the 8 or 4 that
+// its experts fill.
+template <int VPL, typename T>
+constexpr int kPiece = VPL * (int)sizeof(T) < 16 ? VPL : 16 / (int)sizeof(T);
+
 // This lane's VPL logits of the row; -inf beyond the row's end.
 template <int VPL, typename T>
 __device__ __forceinline__ void load_row(const T* row, int E, int lane, bool vec, float (&l)[VPL]) {
   const int e0 = lane * VPL;
-  constexpr int kPer = 16 / (int)sizeof(T);   // elements of a 16-byte load
-  if (VPL >= kPer && vec) {
+  constexpr int kPer = kPiece<VPL, T>, kBytes = kPer * (int)sizeof(T);
+  if (kBytes >= 4 && vec) {
 #pragma unroll
     for (int v = 0; v < VPL / kPer; ++v) {
-      uint4 q = make_uint4(0, 0, 0, 0);
+      uint32_t u[4] = {0, 0, 0, 0};
       const bool in = e0 + v * kPer < E;      // E is a multiple of kPer here
-      if (in) q = ld_nc_v4(row + e0 + v * kPer);
-      const uint32_t u[4] = {q.x, q.y, q.z, q.w};
+      if (in) {
+        const T* at = row + e0 + v * kPer;
+        if (kBytes == 16) {
+          const uint4 q = ld_nc_v4(at);
+          u[0] = q.x, u[1] = q.y, u[2] = q.z, u[3] = q.w;
+        } else if (kBytes == 8) {
+          const uint2 q = __ldg(reinterpret_cast<const uint2*>(at));
+          u[0] = q.x, u[1] = q.y;
+        } else {
+          u[0] = __ldg(reinterpret_cast<const uint32_t*>(at));
+        }
+      }
 #pragma unroll
       for (int i = 0; i < kPer; ++i) {
         float x;
@@ -468,15 +483,23 @@ __global__ void __launch_bounds__(kRouterWarps * 32, router_ctas(VPL, SELECT))
   const T* logits = static_cast<const T*>(p.logits);
   const int end = at.t0 + at.n;
   float next[VPL];
-  if (at.t0 + warp < end)
-    load_row<VPL, T>(logits + ((int64_t)at.rank * p.Tmax + at.t0 + warp) * p.E, p.E, lane, p.vec, next);
+  int e_next = -1;             // given indices come a row ahead as the logits do
+  const bool slots = !SELECT && lane < p.k;
+  if (at.t0 + warp < end) {
+    const int64_t g = (int64_t)at.rank * p.Tmax + at.t0 + warp;
+    load_row<VPL, T>(logits + g * p.E, p.E, lane, p.vec, next);
+    if (slots) e_next = __ldg(p.idx_in + g * p.k + lane);
+  }
   for (int t = at.t0 + warp; t < end; t += kRouterWarps) {
     const int64_t g = (int64_t)at.rank * p.Tmax + t;
     float l[VPL], pr[VPL];
 #pragma unroll
     for (int i = 0; i < VPL; ++i) l[i] = next[i];
-    if (t + kRouterWarps < end)    // the next row is on its way under this one
+    const int e_given = e_next;
+    if (t + kRouterWarps < end) {  // the next row is on its way under this one
       load_row<VPL, T>(logits + (g + kRouterWarps) * p.E, p.E, lane, p.vec, next);
+      if (slots) e_next = __ldg(p.idx_in + (g + kRouterWarps) * p.k + lane);
+    }
     const bool plain = mask_row<VPL, T>(l, SIGMOID && SELECT ? kSigmoidFar : -lowest<T>(), p.err);
     float total = 0.0f, top = 0.0f;
     if (!SIGMOID && (BALANCE || !p.normalize)) top = row_max<VPL>(l);
@@ -525,8 +548,8 @@ __global__ void __launch_bounds__(kRouterWarps * 32, router_ctas(VPL, SELECT))
         p.w[g * p.k + lane] = e >= 0 ? wt * p.scale : 0.0f;
         if (BALANCE && e >= 0) atomicAdd(cnt + e, 1);
       }
-    } else if (lane < p.k) {
-      const int e = __ldg(p.idx_in + g * p.k + lane);
+    } else if (slots) {
+      const int e = e_given;
       if (e < -1 || e >= p.E) {
         atomicOr(p.err, kErrRouterIndex);
       } else if (e >= 0) {
@@ -788,22 +811,24 @@ __global__ void __launch_bounds__(kRouterWarps * 32, router_ctas(VPL))
       }
     }
     T* out = static_cast<T*>(q.d_logits) + g * p.E;
-    constexpr int kPer = 16 / (int)sizeof(T);
-    if (VPL >= kPer && p.vec) {
+    constexpr int kPer = kPiece<VPL, T>, kBytes = kPer * (int)sizeof(T);
+    if (kBytes >= 4 && p.vec) {
 #pragma unroll
       for (int v = 0; v < VPL / kPer; ++v) {
         if (lane * VPL + v * kPer >= p.E) continue;
-        uint4 u;
-        if (sizeof(T) == 4) {
-          u = make_uint4(__float_as_uint(d[v * kPer]), __float_as_uint(d[v * kPer + 1]),
-                         __float_as_uint(d[v * kPer + 2]), __float_as_uint(d[v * kPer + 3]));
+        T* to = out + lane * VPL + v * kPer;
+        uint32_t u[4];
+#pragma unroll
+        for (int i = 0; i < kBytes / 4; ++i)
+          u[i] = sizeof(T) == 4 ? __float_as_uint(d[v * kPer + i])
+                                : cvt_bf16x2(d[(v * kPer + 2 * i) % VPL], d[(v * kPer + 2 * i + 1) % VPL]);
+        if (kBytes == 16) {
+          st_v4(to, make_uint4(u[0], u[1], u[2], u[3]));
+        } else if (kBytes == 8) {
+          *reinterpret_cast<uint2*>(to) = make_uint2(u[0], u[1]);
         } else {
-          u = make_uint4(cvt_bf16x2(d[v * kPer], d[v * kPer + 1]),
-                         cvt_bf16x2(d[v * kPer + 2], d[v * kPer + 3]),
-                         cvt_bf16x2(d[v * kPer + (kPer > 4 ? 4 : 0)], d[v * kPer + (kPer > 4 ? 5 : 0)]),
-                         cvt_bf16x2(d[v * kPer + (kPer > 4 ? 6 : 0)], d[v * kPer + (kPer > 4 ? 7 : 0)]));
+          *reinterpret_cast<uint32_t*>(to) = u[0];
         }
-        st_v4(out + lane * VPL + v * kPer, u);
       }
     } else {
 #pragma unroll
