@@ -109,6 +109,14 @@ __device__ __forceinline__ float warp_sum(float v) {
   return v;
 }
 
+// The sum over a row's k slots, in their lanes; the lanes past them bring zeros.
+__device__ __forceinline__ float slot_sum(float v, int k) {
+#pragma unroll
+  for (int o = 16; o; o >>= 1)
+    if (k > o) v += __shfl_xor_sync(kFull, v, o);
+  return v;
+}
+
 __device__ __forceinline__ float redux_max(float v) {
   float r;
   asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
@@ -344,6 +352,23 @@ __device__ __forceinline__ void put_row(float* buf, int lane, const float (&c)[V
   }
 }
 
+template <int VPL>
+__device__ __forceinline__ void get_row(const float* at, float (&v)[VPL]) {
+  if (VPL % 4 == 0) {
+#pragma unroll
+    for (int i = 0; i < VPL; i += 4) {
+      const float4 f = *reinterpret_cast<const float4*>(at + i);
+      v[i] = f.x;
+      v[(i + 1) % VPL] = f.y;
+      v[(i + 2) % VPL] = f.z;
+      v[(i + 3) % VPL] = f.w;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) v[i] = at[i];
+  }
+}
+
 // A warp's shared memory for the selection, in words: its scores by expert; each
 // lane's sorted scores and a -inf that ends them, whole 16-byte pieces apart
 // whose distance keeps the lanes' accesses off each other's banks; the slots;
@@ -415,21 +440,8 @@ __device__ __forceinline__ void select_experts(const RouterParams& p, int lane, 
     from = __float_as_int(slot.y);
   }
   // slot j's expert: among the winner's, the one with its score
-  const float* row = buf + from * VPL;
   float v[VPL];
-  if (VPL % 4 == 0) {
-#pragma unroll
-    for (int i = 0; i < VPL; i += 4) {
-      const float4 f = *reinterpret_cast<const float4*>(row + i);
-      v[i] = f.x;
-      v[(i + 1) % VPL] = f.y;
-      v[(i + 2) % VPL] = f.z;
-      v[(i + 3) % VPL] = f.w;
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < VPL; ++i) v[i] = row[i];
-  }
+  get_row<VPL>(buf + from * VPL, v);
   int at = 0;
 #pragma unroll
   for (int i = VPL - 1; i > 0; --i)
@@ -533,12 +545,12 @@ __global__ void __launch_bounds__(kRouterWarps * 32, router_ctas(VPL, SELECT))
       if (SIGMOID) {
         float s = 0.0f;
         if (e >= 0) s = p.bias ? buf[kScoresAt<VPL> + e] : v;
-        const float d = p.normalize ? warp_sum(s) : 1.0f;
+        const float d = p.normalize ? slot_sum(s, p.k) : 1.0f;
         wt = d > 0.0f ? s / d : 0.0f;
       } else if (p.normalize) {
         const float m = redux_max(e >= 0 ? v : -INFINITY);
         const float x = e >= 0 ? expf(v - m) : 0.0f;
-        const float d = warp_sum(x);
+        const float d = slot_sum(x, p.k);
         wt = d > 0.0f ? x / d : 0.0f;
       } else {
         wt = e >= 0 ? expf(v - top) / total : 0.0f;
@@ -771,9 +783,9 @@ __global__ void __launch_bounds__(kRouterWarps * 32, router_ctas(VPL))
         if (SIGMOID) {
           const float x = e >= 0 ? sigmoid(xl) : 0.0f;
           if (p.normalize) {
-            const float sum = warp_sum(x);
+            const float sum = slot_sum(x, p.k);
             const float r = sum > 0.0f ? 1.0f / sum : 0.0f;
-            const float mean = warp_sum(x * r * up);
+            const float mean = slot_sum(x * r * up, p.k);
             each = (up - mean) * r * x * (1.0f - x);
           } else {
             each = up * x * (1.0f - x);
@@ -781,9 +793,9 @@ __global__ void __launch_bounds__(kRouterWarps * 32, router_ctas(VPL))
         } else if (p.normalize) {
           const float m = redux_max(xl);
           float x = e >= 0 ? expf(xl - m) : 0.0f;
-          const float sum = warp_sum(x);
+          const float sum = slot_sum(x, p.k);
           x = sum > 0.0f ? x / sum : 0.0f;
-          const float mean = warp_sum(x * up);
+          const float mean = slot_sum(x * up, p.k);
           each = x * (up - mean);
         } else {
           each = e >= 0 ? expf(xl - top) * inv * up : 0.0f;
@@ -792,9 +804,12 @@ __global__ void __launch_bounds__(kRouterWarps * 32, router_ctas(VPL))
           for (int i = 0; i < VPL; ++i) d[i] -= pr[i] * inv * back;
         }
         // to the lanes that hold the experts; slots that name one expert twice
-        // take turns
-        const uint32_t same = __match_any_sync(kFull, e >= 0 ? e : -1 - lane);
-        if (__any_sync(kFull, same & (same - 1))) {
+        // (one of them finds another's number there) take turns
+        if (e >= 0) buf[e] = __int_as_float(lane);
+        __syncwarp();
+        if (__any_sync(kFull, e >= 0 && __float_as_int(buf[e]) != lane)) {
+          if (e >= 0) buf[e] = 0.0f;
+          __syncwarp();
           for (int j = 0; j < p.k; ++j) {
             if (lane == j && e >= 0) buf[e] += each;
             __syncwarp();
@@ -803,8 +818,10 @@ __global__ void __launch_bounds__(kRouterWarps * 32, router_ctas(VPL))
           buf[e] = each;
         }
         __syncwarp();
+        float mine[VPL];
+        get_row<VPL>(buf + lane * VPL, mine);
 #pragma unroll
-        for (int i = 0; i < VPL; ++i) d[i] += buf[lane * VPL + i];
+        for (int i = 0; i < VPL; ++i) d[i] += mine[i];
         __syncwarp();
         if (e >= 0) buf[e] = 0.0f;
         __syncwarp();
