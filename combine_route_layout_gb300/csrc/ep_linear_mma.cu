@@ -25,12 +25,13 @@
 // 280, and an epilogue's warps beside it slow it down.
 //
 // What bounds it. Long products run at the tensor core's rate in cycles (512 a
-// stage) and at the power limit in time: 32768 x 4096 x 4096 dense 1.70 PFLOP/s at
+// stage) and at the power limit in time: 32768 x 4096 x 4096 dense 1.73 PFLOP/s at
 // 1.6 GHz (the library's product 1.77); 128 experts of 973 rows, 4096 x 4096,
 // SwiGLU with pre-activation, 1.42-1.47 at 1.3 GHz, where the experts' weights
 // come from HBM as well. From idle clocks: 8192^3 1.9 PFLOP/s. Few rows an expert:
-// HBM (256 experts x 32 rows, 7168 x 1024: 6.5 TB/s). Small products: launch, set-up
-// and pipeline latency (about 8 us) and the stages of a tile one after another.
+// HBM (256 experts x 32 rows, 7168 x 1024: 6.5 TB/s). Small products: set-up and
+// pipeline latency (about 6 us, part of it under the kernel before) and the stages
+// of a tile one after another.
 #include <cuda.h>
 
 #include <atomic>
@@ -231,7 +232,7 @@ __device__ __forceinline__ bool has_tail(const Tile& w, int kb) {
 // often; what is still idle then takes parts of the tiles' contractions, whose
 // f32 sums the last part to finish adds up. 1024 x 7168 x 256: 43.7 us as 4
 // tiles of 256 rows, 27.5 us as 16 tiles of 64 rows in 4 parts each (as measured
-// when it was built; 19.4 us now).
+// when it was built; 17.6 us now).
 template <int MODE>
 __device__ Plan plan_tiles(const MmaParams& q, int base_cap, int* first, int* begins, int* counts,
                            int* sizes) {
