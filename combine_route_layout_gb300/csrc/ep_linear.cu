@@ -338,6 +338,8 @@ ep_status fill_linear(const ep_linear_handle* h, const void* x, const void* w,
     return lfail(EP_ERR_INVALID_ARG, "x and weight must be given, 16-byte aligned");
   if ((row_begin == nullptr) != (row_count == nullptr))
     return lfail(EP_ERR_INVALID_ARG, "give row_begin and row_count together, or neither");
+  if (((uintptr_t)row_begin | (uintptr_t)row_count | (uintptr_t)row_base) % 4 != 0)
+    return lfail(EP_ERR_INVALID_ARG, "row_begin, row_count or row_base is misaligned");
   if (!row_begin) {
     if (c.num_groups != 1)
       return lfail(EP_ERR_INVALID_ARG, "several groups need row_begin and row_count");

@@ -945,6 +945,12 @@ int vpl_of(int experts) {
   return vpl;
 }
 
+// Whether one of the addresses is not a multiple of 4.
+template <typename... P>
+bool misaligned4(const P*... at) {
+  return ((... | (uintptr_t)at) & 3) != 0;
+}
+
 size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 
 // Validate the config and lay the workspace out in `h`.
@@ -1110,6 +1116,8 @@ extern "C" ep_status ep_router_forward(ep_router_handle* h, const void* logits, 
   if (!indices || !weights) return rfail(EP_ERR_INVALID_ARG, "indices and weights must be given");
   if ((counts == nullptr) != (loss == nullptr))
     return rfail(EP_ERR_INVALID_ARG, "give counts and loss together, or neither");
+  if (misaligned4(bias, indices, weights, counts, loss))
+    return rfail(EP_ERR_INVALID_ARG, "a router argument is misaligned");
   if (bias && h->cfg.score_func != EP_SCORE_SIGMOID)
     return rfail(EP_ERR_UNSUPPORTED, "a selection bias needs sigmoid scores");
   RouterParams p;
@@ -1129,6 +1137,8 @@ extern "C" ep_status ep_router_balance_loss(ep_router_handle* h, const void* log
   if (!h) return rfail(EP_ERR_INVALID_ARG, "router handle is NULL");
   if (!indices || !counts || !loss)
     return rfail(EP_ERR_INVALID_ARG, "indices, counts and loss must be given");
+  if (misaligned4(indices, counts, loss))
+    return rfail(EP_ERR_INVALID_ARG, "a router argument is misaligned");
   RouterParams p;
   ep_status s = fill_params(h, logits, num_tokens, &p);
   if (s != EP_OK) return s;
@@ -1148,6 +1158,8 @@ extern "C" ep_status ep_router_backward(ep_router_handle* h, const void* logits,
   if (!d_logits) return rfail(EP_ERR_INVALID_ARG, "d_logits must be given");
   if (!d_weights && !d_loss)
     return rfail(EP_ERR_INVALID_ARG, "give d_weights, or counts and d_loss, or all three");
+  if (misaligned4(indices, d_weights, counts, d_loss))
+    return rfail(EP_ERR_INVALID_ARG, "a router argument is misaligned");
   if (d_weights && !indices) return rfail(EP_ERR_INVALID_ARG, "d_weights needs indices");
   if ((counts == nullptr) != (d_loss == nullptr))
     return rfail(EP_ERR_INVALID_ARG, "give counts and d_loss together, or neither");

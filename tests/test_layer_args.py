@@ -139,6 +139,36 @@ def test_linear_workspace_and_arguments(ep):
         ep.ep_linear_destroy(None)
 
 
+def test_misaligned_addresses_refused(ep):
+    c = router(ep)
+    h = ep.ep_router_create(c, FAKE, ep.ep_router_workspace_size(c))
+    bad = ep.EP_ERR_INVALID_ARG
+    try:
+        for at in (2, 4, 5, 6, 7):               # bias, indices, weights, counts, loss
+            args = [h, FAKE, FAKE, None, FAKE, FAKE, FAKE, FAKE, None]
+            args[at] = FAKE + 2
+            refused(ep, bad, lambda: ep.ep_router_forward(*args))
+        for at in (2, 4, 5):                     # indices, counts, loss
+            args = [h, FAKE, FAKE, None, FAKE, FAKE, None]
+            args[at] = FAKE + 1
+            refused(ep, bad, lambda: ep.ep_router_balance_loss(*args))
+        for at in (2, 4, 5, 6, 7):               # indices, d_weights, counts, d_loss, d_logits
+            args = [h, FAKE, FAKE, None, FAKE, FAKE, FAKE, FAKE, None]
+            args[at] = FAKE + 2
+            refused(ep, bad, lambda: ep.ep_router_backward(*args))
+    finally:
+        ep.ep_router_destroy(h)
+    c = linear(ep)
+    h = ep.ep_linear_create(c, FAKE, ep.ep_linear_workspace_size(c))
+    try:
+        for at in (5, 6, 7):                     # row_begin, row_count, row_base
+            args = [h, FAKE, FAKE, None, None, FAKE, FAKE, FAKE, 0, FAKE, None, None]
+            args[at] = FAKE + 2
+            refused(ep, bad, lambda: ep.ep_linear_forward(*args))
+    finally:
+        ep.ep_linear_destroy(h)
+
+
 def test_layer_refuses_tensors_that_do_not_fit(ep):
     from combine_route_layout_gb300 import EpError, EpLinearConfig, EpLinearOp, EpRouterConfig, EpRouterOp
     op = EpRouterOp(EpRouterConfig(2, 4, 16, 2), device="cpu")       # nothing is launched
