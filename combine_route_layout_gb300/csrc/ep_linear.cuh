@@ -100,7 +100,7 @@ __device__ __forceinline__ float silu_of(float v) { return v * sigmoid_of(v); }
 
 __device__ __forceinline__ float act_of(int act, float v) {
   switch (act) {
-    case EP_ACT_RELU: return fmaxf(v, 0.0f);
+    case EP_ACT_RELU: return v < 0.0f ? 0.0f : v;   // NaN stays
     case EP_ACT_SILU: return silu_of(v);
     case EP_ACT_GELU: return 0.5f * v * (1.0f + erff(v * 0.70710678118654752f));
     default: return v;
@@ -109,7 +109,7 @@ __device__ __forceinline__ float act_of(int act, float v) {
 
 __device__ __forceinline__ float slope_of(int act, float v) {
   switch (act) {
-    case EP_ACT_RELU: return v > 0.0f ? 1.0f : 0.0f;
+    case EP_ACT_RELU: return v <= 0.0f ? 0.0f : 1.0f;
     case EP_ACT_SILU: {
       const float s = sigmoid_of(v);
       return s * (1.0f + v * (1.0f - s));

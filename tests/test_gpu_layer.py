@@ -547,6 +547,39 @@ def test_linear_gradient_matches_differences(layer):
             assert abs(slope - float(grad[place])) < 0.02 * (1.0 + float(grad.float().abs().max()))
 
 
+@pytest.mark.parametrize("rows", [1, 5])
+@pytest.mark.parametrize("act", ["none", "relu", "silu", "gelu", "swiglu"])
+def test_linear_keeps_nan_and_infinity_in_their_rows(layer, act, rows):
+    """A NaN or an infinity in a row of x reaches that row's results as it does in the formula,
+    and no other row's."""
+    bf = torch.bfloat16
+    K, N = 64, 40
+    Nw = N * (2 if act == "swiglu" else 1)
+    g = torch.Generator().manual_seed(5)
+    x = torch.randn((rows, K), generator=g).to(bf).to(DEV)
+    w = torch.randn((1, Nw, K), generator=g).to(bf).to(DEV)
+    dy = torch.randn((rows, N), generator=g).to(bf).to(DEV)
+    op = layer.EpLinearOp(layer.EpLinearConfig(1, K, N, rows, activation=act), backward=True)
+    z = torch.empty((rows, Nw), dtype=bf, device=DEV)
+    y = op.forward(x, w, preact=z)
+    dx, _, _ = op.backward(dy, x, w, z)
+    for value in (math.nan, math.inf):
+        x2 = x.clone()
+        x2[0, 3] = value
+        z2 = torch.empty_like(z)
+        y2 = op.forward(x2, w, preact=z2)
+        dx2, _, _ = op.backward(dy, x2, w, z2)
+        assert torch.equal(y2[1:], y[1:]) and torch.equal(dx2[1:], dx[1:])
+        want = x2.double() @ w[0].double().t()
+        assert torch.equal(z2[0].isnan(), want[0].isnan()) and torch.equal(z2[0].isinf(), want[0].isinf())
+        assert torch.equal(z2[0][z2[0].isinf()].double(), want[0][want[0].isinf()])
+        if math.isnan(value):
+            assert y2[0].isnan().all() and (act in ("none", "relu") or dx2[0].isnan().all())
+        elif act in ("none", "relu"):
+            assert torch.equal(y2[0].double(), act64(act, want)[0])
+    op.sync()
+
+
 def test_linear_residual_may_be_the_output(layer):
     t = Product(layer, (1, 128, 200, [77], "gelu", True, True, torch.bfloat16, torch.bfloat16), packed=False)
     op = layer.EpLinearOp(t.cfg)
