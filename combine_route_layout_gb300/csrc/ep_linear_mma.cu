@@ -52,9 +52,11 @@ constexpr int kStageBytes = kStageA + kStageB;
 constexpr int kMaxRows = 256;                    // rows of a tile (f32 outputs: half)
 constexpr int kMinCap = 64;
 constexpr int kMaxSplits = 8;
-// Least stages of a part: joining costs about as much as ten stages (dW, whose
-// parts of a tile are 256 KB: as forty).
-constexpr int kLeast = 12, kLeastGrad = 32;
+// Stages of a contraction that is cut, and of a part of it, at least. Joining
+// costs as much as sixteen stages, few parts or many (16 stages in two parts:
+// 9.3 us for 7.3; 32 stages in four parts 10.5 and 8.8, in two 11.3 and 10.4: 1024
+// x 1024 or 2048 x 256 f32, 16 x 2048 x 2048). dW's parts of a tile are 256 KB.
+constexpr int kWorth = 24, kLeast = 7, kWorthGrad = 64, kLeastGrad = 32;
 // f32 outputs: the tensor core cuts off what its accumulator cannot hold, an
 // error that grows with the number of steps to the power 3/2 (7168 terms: 8e-6 of
 // the result); sums of 512 terms are added up in registers instead, which
@@ -146,8 +148,10 @@ __host__ __device__ __forceinline__ int tile_rows(int count, int cap, int (*div)
 }
 
 // Parts that contractions of `blocks` stages are cut into where `tiles` tiles
-// leave pairs idle; a part has at least `least` stages.
-__host__ __device__ __forceinline__ int splits_for(int pairs, int tiles, int blocks, int least) {
+// leave pairs idle, from `worth` stages on; a part has at least `least` of them.
+__host__ __device__ __forceinline__ int splits_for(int pairs, int tiles, int blocks, int worth,
+                                                   int least) {
+  if (blocks < worth) return 1;
   int n = tiles > 0 && tiles < pairs ? pairs / tiles : 1;
   if (n > kMaxSplits) n = kMaxSplits;
   if (n > blocks / least) n = blocks / least;
@@ -287,7 +291,8 @@ __device__ Plan plan_tiles(const MmaParams& q, int base_cap, int* first, int* be
 #pragma unroll
     for (int w = 0; w < kThreads / 32; ++w) most = max(most, sums[0][w]);
     plan.tiles = G * q.f_tiles * q.r_tiles;
-    plan.splits = splits_for(pairs, plan.tiles, (most + kDepth - 1) / kDepth, kLeastGrad);
+    plan.splits = splits_for(pairs, plan.tiles, (most + kDepth - 1) / kDepth, kWorthGrad,
+                             kLeastGrad);
     return plan;
   }
   s0 = s1 = s2 = 0;
@@ -311,7 +316,7 @@ __device__ Plan plan_tiles(const MmaParams& q, int base_cap, int* first, int* be
   }
   plan.cap = base_cap >> level;
   plan.splits = splits_for(pairs, plan.tiles,
-                           ((MODE == kForward ? q.p.K : q.p.Nw) + kDepth - 1) / kDepth, kLeast);
+                           ((MODE == kForward ? q.p.K : q.p.Nw) + kDepth - 1) / kDepth, kWorth, kLeast);
   // tiles before this thread's groups: an exclusive scan over the threads
   int incl = mine;
 #pragma unroll
@@ -1041,12 +1046,12 @@ Plan dense_plan(int64_t rows64, int base_cap, int f_tiles, int blocks, int pairs
     plan.size = size;
     if (2 * plan.tiles > pairs || plan.cap <= kMinCap) break;
   }
-  plan.splits = splits_for(pairs, plan.tiles, blocks, kLeast);
+  plan.splits = splits_for(pairs, plan.tiles, blocks, kWorth, kLeast);
   return plan;
 }
 
 Plan dense_grad_plan(int64_t rows, int cap, int tiles, int pairs) {
-  return Plan{tiles, cap, splits_for(pairs, tiles, (int)((rows + kDepth - 1) / kDepth), kLeastGrad), 0};
+  return Plan{tiles, cap, splits_for(pairs, tiles, (int)((rows + kDepth - 1) / kDepth), kWorthGrad, kLeastGrad), 0};
 }
 
 // Upper bound of the units of all groups (their counts are on the device).
