@@ -17,9 +17,9 @@ constexpr int kErrLinearTimeout = 2;   // a bounded wait gave up
 
 // The products run on at most this many pairs of SMs; with fewer tiles than
 // pairs they cut contractions into parts, at most one per pair, of at most 64
-// rows x 256 features (dW: 256 x 256) f32 sums.
+// rows x 256 features (dW: 128 x 256) f32 sums.
 constexpr int kLinearMaxPairs = 80;
-constexpr size_t kPartBytes = 64 * 256 * 4, kPartBytesGrad = 256 * 256 * 4;
+constexpr size_t kPartBytes = 64 * 256 * 4, kPartBytesGrad = 128 * 256 * 4;
 
 // Rows of each group: begin[g] (+ base[g / per_base]) .. + count[g] - 1 of
 // the pool, or the first `dense_rows` rows when begin is NULL (one group).

@@ -35,6 +35,7 @@
 #include <cuda.h>
 
 #include <atomic>
+#include <climits>
 #include <cstring>
 
 #include "ep_launch.cuh"
@@ -55,8 +56,9 @@ constexpr int kMaxSplits = 8;
 // Stages of a contraction that is cut, and of a part of it, at least. Joining
 // costs as much as sixteen stages, few parts or many (16 stages in two parts:
 // 9.3 us for 7.3; 32 stages in four parts 10.5 and 8.8, in two 11.3 and 10.4: 1024
-// x 1024 or 2048 x 256 f32, 16 x 2048 x 2048). dW's parts of a tile are 256 KB.
-constexpr int kWorth = 24, kLeast = 7, kWorthGrad = 64, kLeastGrad = 32;
+// x 1024 or 2048 x 256 f32, 16 x 2048 x 2048). dW's parts of a tile are 128 KB (32
+// stages of 8 tiles in two parts 19.2 us for 15.7, with tiles of 256 rows).
+constexpr int kWorth = 24, kLeast = 7, kWorthGrad = 48, kLeastGrad = 16;
 // f32 outputs: the tensor core cuts off what its accumulator cannot hold, an
 // error that grows with the number of steps to the power 3/2 (7168 terms: 8e-6 of
 // the result); sums of 512 terms are added up in registers instead, which
@@ -82,7 +84,8 @@ struct MmaParams {
   void* out;         // y, dx or dW
   int features;      // length of the output's contiguous axis (weight rows or K)
   int f_tiles;       // 256-feature tiles
-  int r_tiles;       // dW: 256-row tiles of each group (else by the group's count)
+  int r_tiles;       // dW: tiles of `cap` rows of each group (else by the group's count)
+  int cap;           // most rows of a tile
   int a_blocks;      // MN-major operands: the map cuts rows into blocks of 64
   int b_blocks;      // elements, so that one box takes two of them
   int pairs_out, pairs_z;   // bf16 outputs whose rows allow two features a store
@@ -238,8 +241,8 @@ __device__ __forceinline__ bool has_tail(const Tile& w, int kb) {
 // tiles of 256 rows, 27.5 us as 16 tiles of 64 rows in 4 parts each (as measured
 // when it was built; 15.0 us now).
 template <int MODE>
-__device__ Plan plan_tiles(const MmaParams& q, int base_cap, int* first, int* begins, int* counts,
-                           int* sizes) {
+__device__ Plan plan_tiles(const MmaParams& q, int* first, int* begins, int* counts, int* sizes) {
+  const int base_cap = q.cap;
   __shared__ int sums[3][kThreads / 32];
   if (!q.p.s.begin) {
     if (threadIdx.x == 0) {
@@ -620,7 +623,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   cluster_arrive();                      // the barriers are ready; the wait is below
   if (warp == 1) tmem_alloc(&bar->tmem, kTmemColumns);
   begin_overlapped();
-  const Plan plan = plan_tiles<MODE>(q, kChunked ? kMaxRows / 2 : kMaxRows, first, begins, counts, sizes);
+  const Plan plan = plan_tiles<MODE>(q, first, begins, counts, sizes);
   const int units = plan.tiles * plan.splits;
   tc_fence_before();
   __syncthreads();                       // the TMEM address is there
@@ -1085,6 +1088,7 @@ cudaError_t launch_linear_forward(const LinearParams& p, int sms, cudaStream_t s
   q.features = p.Nw;
   q.f_tiles = (p.Nw + 255) / 256;
   q.r_tiles = 0;
+  q.cap = p.y_f32 ? kMaxRows / 2 : kMaxRows;
   Maps m;
   bool ok;
   if (gated) {   // gate and up rows of a feature next to each other
@@ -1100,7 +1104,7 @@ cudaError_t launch_linear_forward(const LinearParams& p, int sms, cudaStream_t s
   if (!ok || !map_k_major(m.b, p.x, p.K, rows, p.K)) return cudaErrorInvalidValue;
   q.a_blocks = q.b_blocks = 0;
   const int grid = grid_of(sms, most_units(p, q.f_tiles, p.K));
-  q.plan = dense_plan(p.s.dense_rows, p.y_f32 ? kMaxRows / 2 : kMaxRows, q.f_tiles,
+  q.plan = dense_plan(p.s.dense_rows, q.cap, q.f_tiles,
                       (p.K + kDepth - 1) / kDepth, grid / 2);
   return p.y_f32 ? launch_forward<float>(m, q, grid, st)
                  : launch_forward<__nv_bfloat16>(m, q, grid, st);
@@ -1116,6 +1120,7 @@ cudaError_t launch_linear_input_grad(const LinearParams& p, int sms, cudaStream_
   q.features = p.K;
   q.f_tiles = (p.K + 255) / 256;
   q.r_tiles = 0;
+  q.cap = kMaxRows;
   q.a_blocks = p.K % 64 == 0;
   q.b_blocks = 0;
   Maps m;
@@ -1123,7 +1128,7 @@ cudaError_t launch_linear_input_grad(const LinearParams& p, int sms, cudaStream_
       !map_k_major(m.b, p.dz, p.Nw, rows, p.ldz))
     return cudaErrorInvalidValue;
   const int grid = grid_of(sms, most_units(p, q.f_tiles, p.Nw));
-  q.plan = dense_plan(p.s.dense_rows, kMaxRows, q.f_tiles, (p.Nw + kDepth - 1) / kDepth, grid / 2);
+  q.plan = dense_plan(p.s.dense_rows, q.cap, q.f_tiles, (p.Nw + kDepth - 1) / kDepth, grid / 2);
   return launch_tiles<kInputGrad, EP_ACT_NONE, __nv_bfloat16>(m, q, grid, st);
 }
 
@@ -1136,12 +1141,17 @@ cudaError_t launch_linear_weight_grad(const LinearParams& p, int sms, cudaStream
   q.out = p.dw;
   q.features = p.K;
   q.f_tiles = (p.K + 255) / 256;
-  const int cap = p.dw_f32 ? kMaxRows / 2 : kMaxRows;
+  // tiles of 128 rows where those of 256 leave half of the pairs idle, so that a
+  // part of a tile never has more (4096 rows, 1024 x 512: 15.7 us for 24.2; 16384
+  // rows, 512 x 256: 24.2 for 35.2)
+  const int64_t wide = (int64_t)p.s.G * q.f_tiles * ((p.Nw + kMaxRows - 1) / kMaxRows);
+  const int cap = p.dw_f32 || 2 * wide <= grid_of(sms, INT_MAX) / 2 ? kMaxRows / 2 : kMaxRows;
+  q.cap = cap;
   q.r_tiles = (p.Nw + cap - 1) / cap;
   q.a_blocks = p.K % 64 == 0;
   // columns past Nw give rows of dW that are not stored; tiles of 128 rows
   // have one 64-column part to a CTA
-  q.b_blocks = p.ldz % 64 == 0 && !p.dw_f32;
+  q.b_blocks = p.ldz % 64 == 0 && cap == kMaxRows;
   Maps m;
   if (!map_mn_major(&m.a, p.x, p.K, rows, p.K, 0, q.a_blocks) ||
       !map_mn_major(&m.b[0], p.dz, p.Nw, rows, p.ldz, 0, q.b_blocks))
