@@ -45,11 +45,14 @@
 namespace ep {
 namespace {
 
-constexpr int kStages = 6;
 constexpr int kDepth = 64;                       // terms per stage: 128 bytes of bf16
 constexpr int kStageA = 128 * kDepth * 2;        // bytes of a CTA's 128 features
 constexpr int kStageB = 128 * kDepth * 2;        // bytes of a CTA's half of the rows
-constexpr int kStageBytes = kStageA + kStageB;
+// The ring holds 6 stages of 256 rows, 8 of 128 or 9 of 64: products of few rows
+// wait for their loads' latency, and more of them are on their way (1024 x 7168 x
+// 256: 14.1 us, 15.1 with 6; dW of 4096 rows, 2048 x 1024: 19.8 and 22.2).
+constexpr int kRingBytes = 6 * (kStageA + kStageB);
+constexpr int kMaxStages = 9;
 constexpr int kMaxRows = 256;                    // rows of a tile (f32 outputs: half)
 constexpr int kMinCap = 64;
 constexpr int kMaxSplits = 8;
@@ -131,8 +134,8 @@ struct Tile {
 constexpr int kSlots = 4;     // tiles that are worked out ahead
 
 struct Barriers {
-  uint64_t full[kStages];     // both CTAs' operands have landed (even CTA's)
-  uint64_t empty[kStages];    // this CTA's stage may be written again
+  uint64_t full[kMaxStages];  // both CTAs' operands have landed (even CTA's)
+  uint64_t empty[kMaxStages]; // this CTA's stage may be written again
   uint64_t landed;            // dW: this CTA's last block has landed; its tail is to be cleared
   uint64_t acc_full[2];
   uint64_t acc_empty[2];      // even CTA's: both CTAs' epilogues are done
@@ -239,7 +242,7 @@ __device__ __forceinline__ bool has_tail(const Tile& w, int kb) {
 // often; what is still idle then takes parts of the tiles' contractions, whose
 // f32 sums the last part to finish adds up. 1024 x 7168 x 256: 43.7 us as 4
 // tiles of 256 rows, 27.5 us as 16 tiles of 64 rows in 4 parts each (as measured
-// when it was built; 15.0 us now).
+// when it was built; 14.1 us now).
 template <int MODE>
 __device__ Plan plan_tiles(const MmaParams& q, int* first, int* begins, int* counts, int* sizes) {
   const int base_cap = q.cap;
@@ -583,12 +586,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     product_kernel(const __grid_constant__ Maps maps, MmaParams q) {
   constexpr bool kGated = MODE == kForward && ACT == EP_ACT_SWIGLU;
   constexpr bool kChunked = sizeof(T) == 4;
-  // dW: the last stage of a contraction, whose tail has to be cleared, has a
-  // place beside the ring, so that the time this takes passes under the others
-  constexpr int kTail = kStages - 1, kRing = MODE == kWeightGrad ? kTail : kStages;
   extern __shared__ uint8_t raw[];
   uint8_t* ring = reinterpret_cast<uint8_t*>(((uintptr_t)raw + 1023) & ~(uintptr_t)1023);
-  Barriers* bar = reinterpret_cast<Barriers*>(ring + kStages * kStageBytes);
+  Barriers* bar = reinterpret_cast<Barriers*>(ring + kRingBytes);
   int* first = reinterpret_cast<int*>(bar + 1);
   int* begins = first + q.p.s.G;
   int* counts = begins + q.p.s.G;
@@ -598,12 +598,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   int32_t* timeout = q.p.s.err;
 
   // one thread a barrier
-  if (threadIdx.x < kStages) {
+  if (threadIdx.x < kMaxStages) {
     mbar_init(&bar->full[threadIdx.x], 2);       // each CTA's producer
     mbar_init(&bar->empty[threadIdx.x], 1);
-  } else if (threadIdx.x < kStages + 2) {
-    mbar_init(&bar->acc_full[threadIdx.x - kStages], 1);
-    mbar_init(&bar->acc_empty[threadIdx.x - kStages], 2 * kEpilogueWarps);  // of both CTAs
+  } else if (threadIdx.x < kMaxStages + 2) {
+    mbar_init(&bar->acc_full[threadIdx.x - kMaxStages], 1);
+    mbar_init(&bar->acc_empty[threadIdx.x - kMaxStages], 2 * kEpilogueWarps);  // of both CTAs
   }
   if (threadIdx.x >= 32 && threadIdx.x < 32 + kSlots) {
     // producer, the epilogue's warps, MMA (even CTA), tails (dW)
@@ -625,6 +625,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   begin_overlapped();
   const Plan plan = plan_tiles<MODE>(q, first, begins, counts, sizes);
   const int units = plan.tiles * plan.splits;
+  const int stage_bytes = kStageA + plan.cap / 2 * kDepth * 2;
+  const int stages = min(kMaxStages, kRingBytes / stage_bytes);
+  // dW: the last stage of a contraction, whose tail has to be cleared, has a
+  // place beside the ring, so that the time this takes passes under the others
+  const int tail_place = stages - 1, ring_stages = MODE == kWeightGrad ? tail_place : stages;
   tc_fence_before();
   __syncthreads();                       // the TMEM address is there
   tc_fence_after();
@@ -653,7 +658,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const CUtensorMap* map_b = &maps.b[box];
       // stage kb's operands into place `to`, their bytes on barrier `on`
       auto load = [&](int kb, int to, uint32_t on) {
-        const uint32_t a = ring0 + to * kStageBytes, b = a + kStageA;
+        const uint32_t a = ring0 + to * stage_bytes, b = a + kStageA;
         const int d = kb * kDepth;
         const int row = (int)w.begin + d;                       // dW: contraction row
         if (MODE == kForward) {
@@ -688,31 +693,31 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const int end = w.kb1 - (tail ? 1 : 0);
       // once the ring is full of this tile's stages, the place of the last
       // tile's tail is free or soon will be
-      const int tail_at = min(w.kb0 + kRing, end);
+      const int tail_at = min(w.kb0 + ring_stages, end);
       for (int kb = w.kb0; kb < w.kb1; ++kb) {
         if (tail && kb == tail_at) {
           if (tails > 0) {
-            ok = mbar_wait_soon(&bar->empty[kTail], (tails - 1) & 1);
+            ok = mbar_wait_soon(&bar->empty[tail_place], (tails - 1) & 1);
             if (!ok) break;
-            if (cta == 0) mbar_signal_at(empty0 + kTail * 8);
+            if (cta == 0) mbar_signal_at(empty0 + tail_place * 8);
           }
           ++tails;
           mbar_arrive_expect_tx(&bar->landed, bytes);
-          load(w.kb1 - 1, kTail, smem_addr(&bar->landed));
+          load(w.kb1 - 1, tail_place, smem_addr(&bar->landed));
         }
         if (kb == end) break;
-        if (it >= kRing) {
+        if (it >= ring_stages) {
           if (!ready) ok = mbar_wait_soon(&bar->empty[s], phase);
           if (!ok) break;
           if (cta == 0) mbar_signal_at(empty0 + s * 8);
         }
         const int to = s;
         ++it;
-        if (++s == kRing) {
+        if (++s == ring_stages) {
           s = 0;
           phase ^= 1;
         }
-        ready = it >= kRing && mbar_test(own0 + s * 8, phase);   // its answer comes under the loads
+        ready = it >= ring_stages && mbar_test(own0 + s * 8, phase);   // its answer comes under the loads
         mbar_signal_expect_tx_at(full0 + to * 8, bytes);
         load(kb, to, full0 + to * 8);
       }
@@ -720,19 +725,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     if (!ok) {
       atomicOr(timeout, kErrLinearTimeout);
       // copies in flight must land before the CTAs leave
-      for (int i = 0; i < kRing && i < it; ++i) {
-        s = s == 0 ? kRing - 1 : s - 1;
-        (void)mbar_wait(&bar->full[s], ((it - 1 - i) / kRing) & 1);
+      for (int i = 0; i < ring_stages && i < it; ++i) {
+        s = s == 0 ? ring_stages - 1 : s - 1;
+        (void)mbar_wait(&bar->full[s], ((it - 1 - i) / ring_stages) & 1);
       }
       if (tails > 0) (void)mbar_wait(&bar->landed, (tails - 1) & 1);
     }
   } else if (warp == 1 && cta == 0 && elect_one()) {
     // ------------------------------------------------ MMA: one thread of the even CTA
-    // operands of stage 0; a stage is kStageBytes on, 16 terms are 32 bytes of
+    // operands of stage 0; a stage is stage_bytes on, 16 terms are 32 bytes of
     // a row (K-major) or 16 rows (MN-major) on
     constexpr bool kMnA = MODE != kForward, kMnB = MODE == kWeightGrad;
     constexpr uint32_t kStepA = (kMnA ? 2048 : 32) >> 4, kStepB = (kMnB ? 2048 : 32) >> 4;
-    constexpr uint32_t kStageUnits = kStageBytes >> 4;
+    const uint32_t stage_units = (uint32_t)stage_bytes >> 4;
     const uint64_t op_a = smem_operand(smem_addr(ring), kMnA ? 8192 : 16);
     const uint64_t op_b = smem_operand(smem_addr(ring) + kStageA, kMnB ? 8192 : 16);
     const uint32_t a0 = (uint32_t)op_a, a_high = (uint32_t)(op_a >> 32);
@@ -760,12 +765,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           if (!ok) break;
           tc_fence_after();
           const uint32_t at = s;
-          if (++s == kRing) {
+          if (++s == ring_stages) {
             s = 0;
             phase ^= 1;
           }
           ready = mbar_test(full0 + s * 8, phase);         // its answer comes under the MMAs
-          mma_stage<kStepA, kStepB>(d, a0 + at * kStageUnits, a_high, b0 + at * kStageUnits, b_high,
+          mma_stage<kStepA, kStepB>(d, a0 + at * stage_units, a_high, b0 + at * stage_units, b_high,
                                     form, accumulate);
           mma_commit(empty0 + at * 8);
           accumulate = true;
@@ -773,11 +778,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (ok && kb < stop) {             // the last stage, of fewer terms
           uint32_t at = s;
           if (has_tail<MODE>(w, kb)) {     // in a place of its own, whose rows both CTAs cleared
-            at = kTail;
-            ok = mbar_wait_cluster(&bar->full[kTail], tails++ & 1);
+            at = tail_place;
+            ok = mbar_wait_cluster(&bar->full[tail_place], tails++ & 1);
           } else {
             if (!ready) ok = mbar_wait_soon(&bar->full[s], phase);
-            if (++s == kRing) {
+            if (++s == ring_stages) {
               s = 0;
               phase ^= 1;
             }
@@ -785,7 +790,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           }
           if (!ok) break;
           tc_fence_after();
-          const uint32_t a = a0 + at * kStageUnits, b = b0 + at * kStageUnits;
+          const uint32_t a = a0 + at * stage_units, b = b0 + at * stage_units;
           const int steps = (w.terms - kb * kDepth + 15) / 16;
           for (int step = 0; step < steps; ++step)
             mma_step(d, a + step * kStepA, a_high, b + step * kStepB, b_high, form,
@@ -811,14 +816,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       ok = warp_wait(&bar->landed, tails++ & 1);
       if (!ok) break;
       const int valid = w.terms - (w.kb1 - 1) * kDepth, more = (valid + 15) / 16 * 16 - valid;
-      uint8_t* stage = ring + kTail * kStageBytes;
+      uint8_t* stage = ring + tail_place * stage_bytes;
       for (int row = valid + (lane >> 3); row < valid + more; row += 4)
 #pragma unroll
         for (int part = 0; part < 4; ++part)                    // 16-byte pieces of a and b
-          reinterpret_cast<uint4*>(stage + part * 8192 + row * 128)[lane & 7] = make_uint4(0, 0, 0, 0);
+          if (part * 8192 < stage_bytes)
+            reinterpret_cast<uint4*>(stage + part * 8192 + row * 128)[lane & 7] = make_uint4(0, 0, 0, 0);
       fence_async_shared();
       __syncwarp();
-      if (lane == 0) mbar_arrive_at(in_cta(&bar->full[kTail], 0));
+      if (lane == 0) mbar_arrive_at(in_cta(&bar->full[tail_place], 0));
     }
     if (!ok && lane == 0) atomicOr(timeout, kErrLinearTimeout);
   } else if (warp == 3 && elect_one()) {
@@ -1012,7 +1018,7 @@ template <int MODE, int ACT, typename T>
 cudaError_t launch_tiles(const Maps& maps, MmaParams& q, int grid, cudaStream_t st) {
   q.pairs_out = q.features % 2 == 0 && (uintptr_t)q.out % 4 == 0;
   q.pairs_z = q.features % 2 == 0 && (uintptr_t)q.p.z % 4 == 0;
-  const size_t smem = 1024 + kStages * kStageBytes + sizeof(Barriers) + (size_t)q.p.s.G * kGroupBytes;
+  const size_t smem = 1024 + kRingBytes + sizeof(Barriers) + (size_t)q.p.s.G * kGroupBytes;
   // the kernel's shared-memory limit, once on each device
   static std::atomic<uint64_t> raised{0};
   int dev = 0;
@@ -1021,7 +1027,7 @@ cudaError_t launch_tiles(const Maps& maps, MmaParams& q, int grid, cudaStream_t 
   const uint64_t bit = 1ull << (dev & 63);
   if (!(raised.load(std::memory_order_relaxed) & bit)) {
     e = cudaFuncSetAttribute(product_kernel<MODE, ACT, T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             (int)(1024 + kStages * kStageBytes + sizeof(Barriers) +
+                             (int)(1024 + kRingBytes + sizeof(Barriers) +
                                    EP_MAX_EXPERTS * kGroupBytes));
     if (e != cudaSuccess) return e;
     raised.fetch_or(bit, std::memory_order_relaxed);
