@@ -137,7 +137,7 @@ struct Barriers {
   uint64_t full[kMaxStages];  // both CTAs' operands have landed (even CTA's)
   uint64_t empty[kMaxStages]; // this CTA's stage may be written again
   uint64_t landed;            // dW: this CTA's last block has landed; its tail is to be cleared
-  uint64_t acc_full[2];
+  uint64_t acc_full[2];       // the MMAs of a sum are complete (both CTAs')
   uint64_t acc_empty[2];      // even CTA's: both CTAs' epilogues are done
   uint64_t tile_full[kSlots], tile_empty[kSlots];
   uint64_t joined;            // the epilogue's warps meet
@@ -450,11 +450,11 @@ __device__ __forceinline__ bool epilogue_meet(Barriers* bar, int lane, uint32_t&
   return ok;
 }
 
-// An accumulator's sum is there (the even CTA passes the news on), and has
-// been read.
-__device__ __forceinline__ bool accumulator_ready(Barriers* bar, int acc, int n_acc, int cta) {
-  if (!warp_wait(&bar->acc_full[acc], (n_acc >> 1) & 1)) return false;
-  if (cta == 0 && threadIdx.x == 128) mbar_signal_at(in_cta(&bar->acc_full[acc], 1));
+// An accumulator's sum is there (the tensor core tells both CTAs), and has
+// been read: arrivals and waits at cluster scope, since the MMAs that write the odd
+// CTA's accumulator are issued and waited for by a thread of the even one.
+__device__ __forceinline__ bool accumulator_ready(Barriers* bar, int acc, int n_acc) {
+  if (!warp_wait_cluster(&bar->acc_full[acc], (n_acc >> 1) & 1)) return false;
   tc_fence_after();
   return true;
 }
@@ -462,7 +462,7 @@ __device__ __forceinline__ bool accumulator_ready(Barriers* bar, int acc, int n_
 __device__ __forceinline__ void accumulator_free(Barriers* bar, int acc, int lane) {
   tc_fence_before();
   __syncwarp();
-  if (lane == 0) mbar_signal_at(in_cta(&bar->acc_empty[acc], 0));
+  if (lane == 0) mbar_arrive_at(in_cta(&bar->acc_empty[acc], 0));
 }
 
 // A lane's feature of `left` rows, one store each.
@@ -755,8 +755,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       for (int kb = w.kb0; kb < w.kb1 && ok; ++n_acc) {    // an accumulator's sum
         const int stop = kChunked ? min(w.kb1, kb + kChunk32) : w.kb1;
         if (n_acc >= 2) {
-          ok = mbar_wait_soon(&bar->acc_empty[n_acc & 1], ((n_acc >> 1) - 1) & 1);
+          ok = mbar_wait_soon_cluster(&bar->acc_empty[n_acc & 1], ((n_acc >> 1) - 1) & 1);
           if (!ok) break;
+          tc_fence_after();
         }
         const uint32_t d = tmem + (n_acc & 1) * 256;
         bool accumulate = false;
@@ -798,7 +799,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           mma_commit(empty0 + at * 8);
           ++kb;
         }
-        if (ok) mma_commit(smem_addr(&bar->acc_full[n_acc & 1]));
+        if (ok) mma_commit_pair(smem_addr(&bar->acc_full[n_acc & 1]));
       }
     }
     if (!ok) atomicOr(timeout, kErrLinearTimeout);
@@ -876,7 +877,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const int chunks = (w.kb1 - w.kb0 + kChunk32 - 1) / kChunk32;
         for (int chunk = 0; chunk < chunks; ++chunk, ++n_acc) {
           const int acc = n_acc & 1;
-          ok = accumulator_ready(bar, acc, n_acc, (int)cta);
+          ok = accumulator_ready(bar, acc, n_acc);
           if (!ok) break;
 #pragma unroll
           for (int h = 0; h < kBlocks; ++h) {
@@ -890,7 +891,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           accumulator_free(bar, acc, lane);
         }
       } else if (!none) {
-        ok = accumulator_ready(bar, n_acc & 1, n_acc, (int)cta);
+        ok = accumulator_ready(bar, n_acc & 1, n_acc);
       }
       if (!ok) break;
       // first the values of this part: the tile's result, or sums for the part
