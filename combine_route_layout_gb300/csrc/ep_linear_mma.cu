@@ -137,7 +137,7 @@ struct Barriers {
   uint64_t full[kMaxStages];  // both CTAs' operands have landed (even CTA's)
   uint64_t empty[kMaxStages]; // this CTA's stage may be written again
   uint64_t landed;            // dW: this CTA's last block has landed; its tail is to be cleared
-  uint64_t acc_full[2];       // the MMAs of a sum are complete (both CTAs')
+  uint64_t acc_full[2];       // the MMAs of a sum are complete
   uint64_t acc_empty[2];      // even CTA's: both CTAs' epilogues are done
   uint64_t tile_full[kSlots], tile_empty[kSlots];
   uint64_t joined;            // the epilogue's warps meet
@@ -450,12 +450,18 @@ __device__ __forceinline__ bool epilogue_meet(Barriers* bar, int lane, uint32_t&
   return ok;
 }
 
-// An accumulator's sum is there (the tensor core tells both CTAs), and has
-// been read: arrivals and waits at cluster scope, since the MMAs that write the odd
-// CTA's accumulator are issued and waited for by a thread of the even one.
-__device__ __forceinline__ bool accumulator_ready(Barriers* bar, int acc, int n_acc) {
+// An accumulator's sum is there (a thread of the even CTA passes the news on), and
+// has been read: arrivals and waits at cluster scope between the tensor core's
+// fences, since the MMAs that write the odd CTA's accumulator are issued and waited
+// for by threads of the even one.
+__device__ __forceinline__ bool accumulator_ready(Barriers* bar, int acc, int n_acc, int cta) {
   if (!warp_wait_cluster(&bar->acc_full[acc], (n_acc >> 1) & 1)) return false;
   tc_fence_after();
+  if (cta == 0 && threadIdx.x == 128) {
+    tc_fence_before();
+    mbar_arrive_at(in_cta(&bar->acc_full[acc], 1));
+  }
+  __syncwarp();
   return true;
 }
 
@@ -799,7 +805,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           mma_commit(empty0 + at * 8);
           ++kb;
         }
-        if (ok) mma_commit_pair(smem_addr(&bar->acc_full[n_acc & 1]));
+        if (ok) mma_commit(smem_addr(&bar->acc_full[n_acc & 1]));
       }
     }
     if (!ok) atomicOr(timeout, kErrLinearTimeout);
@@ -877,7 +883,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const int chunks = (w.kb1 - w.kb0 + kChunk32 - 1) / kChunk32;
         for (int chunk = 0; chunk < chunks; ++chunk, ++n_acc) {
           const int acc = n_acc & 1;
-          ok = accumulator_ready(bar, acc, n_acc);
+          ok = accumulator_ready(bar, acc, n_acc, (int)cta);
           if (!ok) break;
 #pragma unroll
           for (int h = 0; h < kBlocks; ++h) {
@@ -891,7 +897,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           accumulator_free(bar, acc, lane);
         }
       } else if (!none) {
-        ok = accumulator_ready(bar, n_acc & 1, n_acc);
+        ok = accumulator_ready(bar, n_acc & 1, n_acc, (int)cta);
       }
       if (!ok) break;
       // first the values of this part: the tile's result, or sums for the part

@@ -47,8 +47,8 @@ __device__ __forceinline__ void mbar_arrive_at(uint32_t cluster_addr) {
 // The relaxed forms order no other access of this thread: enough where what
 // the barrier guards is moved by TMA and read by the tensor core alone. A
 // release at cluster scope costs about half a microsecond, on every stage.
-// Accumulators, which threads read, go from CTA to CTA by mma_commit_pair,
-// mbar_arrive_at and waits at cluster scope.
+// Accumulators, which threads read, go from CTA to CTA by mbar_arrive_at and
+// waits at cluster scope.
 __device__ __forceinline__ void mbar_signal_at(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr)
                : "memory");
@@ -234,15 +234,6 @@ __device__ __forceinline__ void mma_step(uint32_t d, uint32_t a, uint32_t a_high
 __device__ __forceinline__ void mma_commit(uint32_t bar) {
   asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
                : "memory");
-}
-
-// The same on the barrier at this address in both CTAs of the pair.
-__device__ __forceinline__ void mma_commit_pair(uint32_t bar) {
-  asm volatile(
-      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
-          bar),
-      "h"((uint16_t)3)
-      : "memory");
 }
 
 // 32 columns of this warp's 32 lanes: register c holds column c of the lane.
