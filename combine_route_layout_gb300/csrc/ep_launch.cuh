@@ -15,6 +15,16 @@ __device__ __forceinline__ void begin_overlapped() {
   pdl_launch_dependents();
   pdl_wait();
 }
+
+// 16 bytes that this SM reads once.
+__device__ __forceinline__ uint4 ld_once_v4(const void* p) {
+  uint4 v;
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p)
+               : "memory");
+  return v;
+}
 #endif
 
 template <typename... Params, typename... Args>

@@ -39,14 +39,14 @@ __device__ __forceinline__ int64_t blocks_of(int64_t count) {
 template <int VEC, typename T>
 __device__ __forceinline__ void load_columns(const T* at, float (&v)[VEC]) {
   if (VEC == 8 && sizeof(T) == 2) {
-    const uint4 q = ld_nc_v4(at);
+    const uint4 q = ld_once_v4(at);
     const uint32_t u[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
     for (int i = 0; i < VEC; ++i) v[i] = (i & 1) ? bf16_hi(u[i / 2]) : bf16_lo(u[i / 2]);
   } else if (VEC == 8) {
 #pragma unroll
     for (int h = 0; h < VEC / 4; ++h) {
-      const uint4 q = ld_nc_v4(at + h * 4);
+      const uint4 q = ld_once_v4(at + h * 4);
       v[(h * 4) % VEC] = __uint_as_float(q.x);
       v[(h * 4 + 1) % VEC] = __uint_as_float(q.y);
       v[(h * 4 + 2) % VEC] = __uint_as_float(q.z);
@@ -208,7 +208,7 @@ __global__ void __launch_bounds__(256) bias_grad_kernel(GradParams q) {
   __syncthreads();
   float s = 0.0f;
   if (c < p.Nw)
-    for (int64_t b = range[0] + warp; b < range[1]; b += 8) s += __ldg(q.part + b * p.Nw + c);
+    for (int64_t b = range[0] + warp; b < range[1]; b += 8) s += q.part[b * p.Nw + c];
   sum[warp][lane] = s;
   __syncthreads();
   if (warp == 0 && c < p.Nw) {

@@ -77,8 +77,8 @@ __device__ __forceinline__ void segment_of(const LinearSegs& s, int g, int64_t& 
     count = s.dense_rows;
     return;
   }
-  begin = (int64_t)__ldg(s.begin + g) + (s.base ? __ldg(s.base + g / s.per_base) : 0);
-  count = __ldg(s.count + g);
+  begin = (int64_t)s.begin[g] + (s.base ? s.base[g / s.per_base] : 0);
+  count = s.count[g];
   if (begin < 0 || count < 0 || begin + count > s.pool) {
     if (count != 0) atomicOr(s.err, kErrSegment);
     if (begin < 0 || begin > s.pool || count < 0) {

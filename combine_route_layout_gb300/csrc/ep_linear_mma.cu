@@ -871,9 +871,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const float* bias = q.p.bias + (int64_t)w.g * q.p.Nw;
         if (kGated) {
           const int out = w.f0 / 2 + f / 2;
-          if (out < q.p.N) b = __ldg(bias + (f & 1 ? q.p.N : 0) + out);
+          if (out < q.p.N) b = bias[(f & 1 ? q.p.N : 0) + out];
         } else if (w.f0 + f < q.features) {
-          b = __ldg(bias + w.f0 + f);
+          b = bias[w.f0 + f];
         }
       }
       float* sums = q.partial + ((int64_t)u * plan.cap * 256 + cta * 128 + quad * 32 + lane);

@@ -58,7 +58,7 @@ __global__ void __launch_bounds__(kWarps * 32) few_rows_kernel(LinearParams p, i
     for (int r = 0; r < R; ++r) {
       if (r >= rows) break;
       float x[8];
-      unpack8(__ldg(reinterpret_cast<const uint4*>(p.x + (int64_t)r * p.K + k)), x);
+      unpack8(*reinterpret_cast<const uint4*>(p.x + (int64_t)r * p.K + k), x);
 #pragma unroll
       for (int f = 0; f < FEATURES; ++f)
 #pragma unroll
@@ -73,14 +73,14 @@ __global__ void __launch_bounds__(kWarps * 32) few_rows_kernel(LinearParams p, i
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u)
 #pragma unroll
-      for (int f = 0; f < FEATURES; ++f) q[u][f] = ld_nc_v4(w[f] + k + u * step);
+      for (int f = 0; f < FEATURES; ++f) q[u][f] = ld_once_v4(w[f] + k + u * step);
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) add(k + u * step, q[u]);
   }
   for (; k < p.K; k += step) {
     uint4 q[FEATURES];
 #pragma unroll
-    for (int f = 0; f < FEATURES; ++f) q[f] = ld_nc_v4(w[f] + k);
+    for (int f = 0; f < FEATURES; ++f) q[f] = ld_once_v4(w[f] + k);
     add(k, q);
   }
 #pragma unroll
@@ -113,10 +113,10 @@ __global__ void __launch_bounds__(kWarps * 32) few_rows_kernel(LinearParams p, i
       const int64_t n = first + f;
       if (lane != r * kOut + f || r >= rows || n >= p.N) continue;
       float z = acc[GATED ? 2 * f : f][r], y;
-      if (p.bias) z += __ldg(p.bias + n);
+      if (p.bias) z += p.bias[n];
       if (GATED) {
         float up = acc[(2 * f + 1) % FEATURES][r];
-        if (p.bias) up += __ldg(p.bias + p.N + n);
+        if (p.bias) up += p.bias[p.N + n];
         if (p.z) p.z[(int64_t)r * p.Nw + p.N + n] = __float2bfloat16_rn(up);
         y = silu_of(z) * up;
       } else {

@@ -177,13 +177,13 @@ __device__ __forceinline__ void load_row(const T* row, int E, int lane, bool vec
       if (in) {
         const T* at = row + e0 + v * kPer;
         if (kBytes == 16) {
-          const uint4 q = ld_nc_v4(at);
+          const uint4 q = ld_once_v4(at);
           u[0] = q.x, u[1] = q.y, u[2] = q.z, u[3] = q.w;
         } else if (kBytes == 8) {
-          const uint2 q = __ldg(reinterpret_cast<const uint2*>(at));
+          const uint2 q = *reinterpret_cast<const uint2*>(at);
           u[0] = q.x, u[1] = q.y;
         } else {
-          u[0] = __ldg(reinterpret_cast<const uint32_t*>(at));
+          u[0] = *reinterpret_cast<const uint32_t*>(at);
         }
       }
 #pragma unroll
@@ -488,7 +488,7 @@ __global__ void __launch_bounds__(kRouterWarps * 32, router_ctas(VPL, SELECT))
 #pragma unroll
   for (int i = 0; i < VPL; ++i) {
     sum_p[i] = 0.0f;
-    bias[i] = SIGMOID && SELECT && p.bias && lane * VPL + i < p.E ? __ldg(p.bias + lane * VPL + i) : 0.0f;
+    bias[i] = SIGMOID && SELECT && p.bias && lane * VPL + i < p.E ? p.bias[lane * VPL + i] : 0.0f;
     bad_bias |= isnan(bias[i]);
     if (isnan(bias[i])) bias[i] = -INFINITY;
   }
@@ -501,7 +501,7 @@ __global__ void __launch_bounds__(kRouterWarps * 32, router_ctas(VPL, SELECT))
   if (at.t0 + warp < end) {
     const int64_t g = (int64_t)at.rank * p.Tmax + at.t0 + warp;
     load_row<VPL, T>(logits + g * p.E, p.E, lane, p.vec, next);
-    if (slots) e_next = __ldg(p.idx_in + g * p.k + lane);
+    if (slots) e_next = p.idx_in[g * p.k + lane];
   }
   for (int t = at.t0 + warp; t < end; t += kRouterWarps) {
     const int64_t g = (int64_t)at.rank * p.Tmax + t;
@@ -511,7 +511,7 @@ __global__ void __launch_bounds__(kRouterWarps * 32, router_ctas(VPL, SELECT))
     const int e_given = e_next;
     if (t + kRouterWarps < end) {  // the next row is on its way under this one
       load_row<VPL, T>(logits + (g + kRouterWarps) * p.E, p.E, lane, p.vec, next);
-      if (slots) e_next = __ldg(p.idx_in + (g + kRouterWarps) * p.k + lane);
+      if (slots) e_next = p.idx_in[(g + kRouterWarps) * p.k + lane];
     }
     const bool plain = mask_row<VPL, T>(l, SIGMOID && SELECT ? kSigmoidFar : -lowest<T>(), p.err);
     float total = 0.0f, top = 0.0f;
@@ -711,12 +711,12 @@ __global__ void __launch_bounds__(kRouterWarps * 32, router_ctas(VPL))
       const int r = at.seg / p.stretches, s0 = (at.seg - r * p.stretches) * p.stretch;
       held = min(p.ntok[r] - s0, p.stretch);
     }
-    const float f = q.coef * __ldg(q.d_loss) / (float)held;
+    const float f = q.coef * *q.d_loss / (float)held;
 #pragma unroll
     for (int i = 0; i < VPL; ++i) {
       const int e = lane * VPL + i;
       if (e < p.E)
-        slope[i] = f * ((float)__ldg(q.counts + (int64_t)at.seg * p.E + e) * (float)p.E /
+        slope[i] = f * ((float)q.counts[(int64_t)at.seg * p.E + e] * (float)p.E /
                         ((float)held * (float)p.k));
     }
   }
@@ -727,8 +727,8 @@ __global__ void __launch_bounds__(kRouterWarps * 32, router_ctas(VPL))
   int e_next = -1;
   float up_next = 0.0f;
   auto load_slot = [&](int64_t row) {
-    e_next = __ldg(p.idx_in + row * p.k + lane);
-    up_next = __ldg(q.d_w + row * p.k + lane);
+    e_next = p.idx_in[row * p.k + lane];
+    up_next = q.d_w[row * p.k + lane];
   };
   const bool slots = q.d_w && lane < p.k;
   if (slots && at.t0 + warp < end) load_slot((int64_t)at.rank * p.Tmax + at.t0 + warp);

@@ -21,3 +21,14 @@ def test_accumulators_change_hands_at_cluster_scope():
     assert len(uses) >= 5                      # three arrivals, two waits
     for line in uses:
         assert any(g in line for g in good), line
+
+
+def test_overlapped_kernels_read_by_plain_loads():
+    """A kernel that starts under the end of the one before it is alive while that one writes:
+    the read-only path, for data that nobody writes meanwhile, is not for it."""
+    for name in sorted(os.listdir(CSRC)):
+        lines = code(name)
+        if not any("begin_overlapped()" in line for line in lines) and name != "ep_linear.cuh":
+            continue
+        for line in lines:
+            assert not re.search(r"__ldg\(|ld_nc|\.nc\.", line), f"{name}: {line.strip()}"
