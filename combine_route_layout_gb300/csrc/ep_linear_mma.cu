@@ -451,15 +451,16 @@ __device__ __forceinline__ bool epilogue_meet(Barriers* bar, int lane, uint32_t&
 }
 
 // An accumulator's sum is there (a thread of the even CTA passes the news on), and
-// has been read: arrivals and waits at cluster scope between the tensor core's
-// fences, since the MMAs that write the odd CTA's accumulator are issued and waited
-// for by threads of the even one.
+// has been read. What these barriers guard lies in tensor memory alone, and the
+// tensor core's own fences order it with the arrivals and waits between them, which
+// need cluster scope, since they meet threads of both CTAs, and no release: one
+// costs 0.4 to 0.5 us each time (1024 x 7168 x 256: 15.7 us for 13.8).
 __device__ __forceinline__ bool accumulator_ready(Barriers* bar, int acc, int n_acc, int cta) {
   if (!warp_wait_cluster(&bar->acc_full[acc], (n_acc >> 1) & 1)) return false;
   tc_fence_after();
   if (cta == 0 && threadIdx.x == 128) {
     tc_fence_before();
-    mbar_arrive_at(in_cta(&bar->acc_full[acc], 1));
+    mbar_signal_at(in_cta(&bar->acc_full[acc], 1));
   }
   __syncwarp();
   return true;
@@ -468,7 +469,7 @@ __device__ __forceinline__ bool accumulator_ready(Barriers* bar, int acc, int n_
 __device__ __forceinline__ void accumulator_free(Barriers* bar, int acc, int lane) {
   tc_fence_before();
   __syncwarp();
-  if (lane == 0) mbar_arrive_at(in_cta(&bar->acc_empty[acc], 0));
+  if (lane == 0) mbar_signal_at(in_cta(&bar->acc_empty[acc], 0));
 }
 
 // A lane's feature of `left` rows, one store each.

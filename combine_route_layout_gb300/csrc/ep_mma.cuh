@@ -47,8 +47,8 @@ __device__ __forceinline__ void mbar_arrive_at(uint32_t cluster_addr) {
 // The relaxed forms order no other access of this thread: enough where what
 // the barrier guards is moved by TMA and read by the tensor core alone. A
 // release at cluster scope costs about half a microsecond, on every stage.
-// Accumulators, which threads read, go from CTA to CTA by mbar_arrive_at and
-// waits at cluster scope.
+// Enough too where it guards tensor memory: tc_fence_before() ahead of the arrival
+// and tc_fence_after() behind the wait, at cluster scope both, order that.
 __device__ __forceinline__ void mbar_signal_at(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr)
                : "memory");

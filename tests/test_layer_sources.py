@@ -13,14 +13,23 @@ def code(name):
 
 
 def test_accumulators_change_hands_at_cluster_scope():
-    """Threads read the accumulators that the other CTA's thread filled: no relaxed arrival
-    and no wait at the scope of one CTA stands on their barriers."""
-    good = ("warp_wait_cluster(", "mbar_wait_soon_cluster(", "mbar_wait_cluster(", "mbar_arrive_at(", "mma_commit(")
-    uses = [line.strip() for line in code("ep_linear_mma.cu")
-            if re.search(r"bar->acc_(full|empty)", line) and "mbar_init(" not in line]
-    assert len(uses) >= 5                      # three arrivals, two waits
-    for line in uses:
-        assert any(g in line for g in good), line
+    """Threads of both CTAs read and free the accumulators that a thread of one has filled:
+    every wait on their barriers is at cluster scope with the tensor core's fence behind
+    it, every thread's arrival at cluster scope with the fence ahead of it."""
+    lines = [line.strip() for line in code("ep_linear_mma.cu")]
+    waits = arrivals = 0
+    for i, line in enumerate(lines):
+        if not re.search(r"bar->acc_(full|empty)", line) or "mbar_init(" in line:
+            continue
+        if "wait" in line:
+            waits += 1
+            assert re.search(r"\b(warp_wait_cluster|mbar_wait_soon_cluster|mbar_wait_cluster)\(", line), line
+            assert any("tc_fence_after();" in after for after in lines[i + 1:i + 3]), line
+        elif "mma_commit(" not in line:        # the tensor core's own arrival
+            arrivals += 1
+            assert "mbar_signal_at(in_cta(" in line or "mbar_arrive_at(in_cta(" in line, line
+            assert "tc_fence_before();" in lines[i - 2:i], line
+    assert (waits, arrivals) == (2, 2)
 
 
 def test_overlapped_kernels_read_by_plain_loads():
