@@ -309,9 +309,10 @@ __device__ __forceinline__ bool group_stays(const RouterParams& p, float best, f
   bool stays = false;
   for (int j = 0; j < p.topk_groups; ++j) {
     const float m = redux_max(best);
+    if (!(m > -INFINITY)) break;   // no open group is left; those that won stand at -inf too
     const int win = __ffs(__ballot_sync(kFull, best == m)) - 1;
     if ((lane ^ win) < run) {
-      stays = m > -INFINITY;
+      stays = true;
       best = -INFINITY;
     }
   }
