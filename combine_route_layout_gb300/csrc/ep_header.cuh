@@ -56,4 +56,12 @@ inline cudaError_t header_report(Header* h, cudaStream_t st, uint32_t* bits) {
   return e;
 }
 
+// Zero everything behind the mark, on `st`, and wait: what a kernel that gave up left
+// behind. A graph captured on a handle that had run clears nothing itself.
+inline cudaError_t header_renew(Header* h, cudaStream_t st) {
+  cudaError_t e = cudaMemsetAsync(h->words + 2, 0, kHeaderBytes - 2 * sizeof(uint32_t), st);
+  if (e == cudaSuccess) e = cudaStreamSynchronize(st);
+  return e;
+}
+
 }  // namespace ep

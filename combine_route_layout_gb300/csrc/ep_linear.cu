@@ -474,10 +474,11 @@ extern "C" ep_status ep_linear_backward(ep_linear_handle* h, const void* dy, con
 extern "C" ep_status ep_linear_sync(ep_linear_handle* h, void* stream) {
   if (!h) return lfail(EP_ERR_INVALID_ARG, "linear handle is NULL");
   uint32_t bits = 0;
-  const cudaError_t e = header_report(&h->header, static_cast<cudaStream_t>(stream), &bits);
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  cudaError_t e = header_report(&h->header, st, &bits);
   if (e != cudaSuccess) return lcuda(e);
   if (bits & kErrLinearTimeout) {
-    h->header.ready = false;   // tickets may be left over
+    if ((e = header_renew(&h->header, st)) != cudaSuccess) return lcuda(e);   // tickets may be left over
     return lfail(EP_ERR_TIMEOUT, "a product's bounded wait gave up; its output is not complete");
   }
   if (bits & kErrSegment)
