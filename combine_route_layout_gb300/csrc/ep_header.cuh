@@ -1,9 +1,10 @@
 // The first bytes of a router's or a product's workspace: error bits, and what
-// its kernels expect to be zero when they start (tickets). The first call on a
-// handle clears them on its stream. A call that is being captured clears them
-// inside its graph and leaves that to the next call too, since the graph may run
-// later, or never; the mark says whether the bits were ever cleared for this
-// handle, so that a report read from them is never left-over memory.
+// its kernels expect to be zero when they start (tickets). A handle's first call
+// puts a kernel ahead of its own that clears them and leaves the handle's mark
+// there. Where it finds the mark it does nothing, so that error bits wait for their
+// report whatever runs after them: a call that is being captured puts the kernel
+// into its graph, once a capture, since a graph may run later, or never, or often.
+// The mark also says that a report reads no left-over memory.
 #pragma once
 
 #include <atomic>
@@ -18,11 +19,14 @@ constexpr size_t kTicketOffset = 256;
 struct Header {
   uint32_t* words = nullptr;   // [0] error bits, [1] mark
   uint32_t mark = 0;
-  bool ready = false;          // cleared by a call that ran
+  bool ready = false;          // a call that was not captured has cleared it
+  unsigned long long capture = 0;   // the capture whose graph clears it
 };
 
 static __global__ void clear_header_kernel(uint32_t* words, uint32_t mark) {
-  words[threadIdx.x] = threadIdx.x == 1 ? mark : 0u;
+  const bool cleared = words[1] == mark;
+  __syncthreads();
+  if (!cleared) words[threadIdx.x] = threadIdx.x == 1 ? mark : 0u;
 }
 
 inline void open_header(Header* h, void* workspace) {
@@ -35,12 +39,20 @@ inline void open_header(Header* h, void* workspace) {
 inline cudaError_t header_ready(Header* h, cudaStream_t st) {
   if (h->ready) return cudaSuccess;
   cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
-  cudaError_t e = cudaStreamIsCapturing(st, &cap);
+  unsigned long long id = 0;
+  cudaError_t e = cudaStreamGetCaptureInfo(st, &cap, &id);
   if (e != cudaSuccess) return e;
+  const bool capturing = cap != cudaStreamCaptureStatusNone;
+  if (capturing && id == h->capture) return cudaSuccess;
   clear_header_kernel<<<1, kHeaderBytes / 4, 0, st>>>(h->words, h->mark);
   e = cudaGetLastError();
-  if (e == cudaSuccess && cap == cudaStreamCaptureStatusNone) h->ready = true;
-  return e;
+  if (e != cudaSuccess) return e;
+  if (capturing) {
+    h->capture = id;
+  } else {
+    h->ready = true;
+  }
+  return cudaSuccess;
 }
 
 // Wait for `st`, then read and clear the error bits.
