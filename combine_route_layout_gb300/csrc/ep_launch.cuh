@@ -6,6 +6,8 @@
 // soon as all of its own CTAs have.
 #pragma once
 
+#include <atomic>
+
 #include "ep_kernels.cuh"
 
 namespace ep {
@@ -41,6 +43,21 @@ inline cudaError_t launch_overlapped(void (*kernel)(Params...), dim3 grid, int b
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+// Raise the kernel's shared-memory limit to `most`, all that any launch of it takes, once
+// on each device (`raised`: the kernel's own). A limit of each launch's own size could
+// be lowered by one host thread between another's and its launch.
+template <typename Kernel>
+inline cudaError_t raise_shared_limit(Kernel* kernel, size_t most, std::atomic<uint64_t>* raised) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = 1ull << (dev & 63);
+  if (raised->load(std::memory_order_relaxed) & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
+  if (e == cudaSuccess) raised->fetch_or(bit, std::memory_order_relaxed);
+  return e;
 }
 
 }  // namespace ep

@@ -1027,19 +1027,10 @@ cudaError_t launch_tiles(const Maps& maps, MmaParams& q, int grid, cudaStream_t 
   q.pairs_out = q.features % 2 == 0 && (uintptr_t)q.out % 4 == 0;
   q.pairs_z = q.features % 2 == 0 && (uintptr_t)q.p.z % 4 == 0;
   const size_t smem = 1024 + kRingBytes + sizeof(Barriers) + (size_t)q.p.s.G * kGroupBytes;
-  // the kernel's shared-memory limit, once on each device
   static std::atomic<uint64_t> raised{0};
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
+  const cudaError_t e = raise_shared_limit(
+      product_kernel<MODE, ACT, T>, 1024 + kRingBytes + sizeof(Barriers) + EP_MAX_EXPERTS * kGroupBytes, &raised);
   if (e != cudaSuccess) return e;
-  const uint64_t bit = 1ull << (dev & 63);
-  if (!(raised.load(std::memory_order_relaxed) & bit)) {
-    e = cudaFuncSetAttribute(product_kernel<MODE, ACT, T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             (int)(1024 + kRingBytes + sizeof(Barriers) +
-                                   EP_MAX_EXPERTS * kGroupBytes));
-    if (e != cudaSuccess) return e;
-    raised.fetch_or(bit, std::memory_order_relaxed);
-  }
   return launch_overlapped(product_kernel<MODE, ACT, T>, dim3((unsigned)grid), kThreads, smem, st, maps, q);
 }
 

@@ -870,9 +870,10 @@ cudaError_t rows_vpl(const RouterParams& p, bool select, bool balance, int grid,
   auto kernel = select && balance ? router_rows_kernel<VPL, T, SIGMOID, true, true>
                 : select          ? router_rows_kernel<VPL, T, SIGMOID, true, false>
                                   : router_rows_kernel<VPL, T, SIGMOID, false, true>;
-  if (smem > 48 * 1024) {
-    const cudaError_t e =
-        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  const size_t most = kRouterWarps * row * 4 + (balance ? (size_t)32 * VPL * 4 : 0);
+  if (most > 48 * 1024) {
+    static std::atomic<uint64_t> raised[3];
+    const cudaError_t e = raise_shared_limit(kernel, most, &raised[!select ? 2 : balance ? 1 : 0]);
     if (e != cudaSuccess) return e;
   }
   return launch_overlapped(kernel, dim3((unsigned)grid), kRouterWarps * 32, smem, st, p);
