@@ -304,7 +304,10 @@ ep_status plan_linear(const ep_linear_config* c, ep_linear_handle* h) {
   h->err = reinterpret_cast<int32_t*>(h->ws);
   h->tickets = reinterpret_cast<unsigned int*>(h->ws ? h->ws + kTicketOffset : nullptr);
   h->partial = reinterpret_cast<float*>(h->ws ? h->ws + off : nullptr);
-  off += kLinearMaxPairs * (c->backward ? kPartBytesGrad : kPartBytes);
+  int64_t terms = c->in_features;
+  if (c->backward && h->Nw > terms) terms = h->Nw;
+  if (c->backward && c->max_rows > terms) terms = c->max_rows;
+  off += kLinearMaxPairs * (terms > kLongTerms ? kPartBytesLong : c->backward ? kPartBytesGrad : kPartBytes);
   h->dz = nullptr;
   h->part = nullptr;
   if (c->backward) {

@@ -20,6 +20,13 @@ constexpr int kErrLinearTimeout = 2;   // a bounded wait gave up
 // rows x 256 features (dW: 128 x 256) f32 sums.
 constexpr int kLinearMaxPairs = 80;
 constexpr size_t kPartBytes = 64 * 256 * 4, kPartBytesGrad = 128 * 256 * 4;
+// The tensor core cuts off what its accumulator cannot hold, an error that grows
+// with the contraction: 16,777,216 equal terms in eight parts came out 1.6 % low.
+// Contractions of more terms than this are summed up so many at a time, in f32 in
+// the pair's place of `partial`, which is then this large (2.5e-4 of the sum at most
+// for terms of one sign, where bf16 rounds by 2e-3; f32 results have shorter sums).
+constexpr int kLongTerms = 1 << 15;
+constexpr size_t kPartBytesLong = 256 * 256 * 4;
 
 // Rows of each group: begin[g] (+ base[g / per_base]) .. + count[g] - 1 of
 // the pool, or the first `dense_rows` rows when begin is NULL (one group).
@@ -48,7 +55,7 @@ struct LinearParams {
   void* y;                     // [pool][N]
   int y_f32;
   __nv_bfloat16* z;            // [pool][Nw] or NULL
-  float* partial;              // sums of parts
+  float* partial;              // sums of parts, and of long contractions
   unsigned int* tickets;       // [kLinearMaxPairs][2], zero between calls
   // backward
   const void* dy;              // [pool][N] of y's type

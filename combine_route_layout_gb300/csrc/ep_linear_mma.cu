@@ -67,6 +67,7 @@ constexpr int kWorth = 24, kLeast = 7, kWorthGrad = 48, kLeastGrad = 16;
 // the result); sums of 512 terms are added up in registers instead, which
 // leaves 6e-7.
 constexpr int kChunk32 = 8;                      // stages of such a sum
+constexpr int kLongStages = kLongTerms / kDepth; // bf16 outputs: stages of a sum
 constexpr int kEpilogueWarps = 8;                // two to each quarter of the TMEM lanes
 constexpr int kThreads = (4 + kEpilogueWarps) * 32;
 constexpr int kGroupBytes = 16;                  // what the plan keeps of a group
@@ -93,7 +94,7 @@ struct MmaParams {
   int b_blocks;      // elements, so that one box takes two of them
   int pairs_out, pairs_z;   // bf16 outputs whose rows allow two features a store
   Plan plan;         // of a dense product
-  float* partial;    // sums of parts: [unit][column][256 features], or NULL
+  float* partial;    // sums of parts and of long contractions: [pair][column][256 features]
   unsigned int* tickets;   // parts that are done: [tile][2], zero between calls
 };
 
@@ -760,7 +761,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const uint32_t form = mma_form(w.n, kMnA, kMnB);
       const int full_end = min(w.kb1, w.terms / kDepth);   // stages of 64 terms end here
       for (int kb = w.kb0; kb < w.kb1 && ok; ++n_acc) {    // an accumulator's sum
-        const int stop = kChunked ? min(w.kb1, kb + kChunk32) : w.kb1;
+        const int stop = min(w.kb1, kb + (kChunked ? kChunk32 : kLongStages));
         if (n_acc >= 2) {
           ok = mbar_wait_soon_cluster(&bar->acc_empty[n_acc & 1], ((n_acc >> 1) - 1) & 1);
           if (!ok) break;
@@ -877,7 +878,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           b = bias[w.f0 + f];
         }
       }
-      float* sums = q.partial + ((int64_t)u * plan.cap * 256 + cta * 128 + quad * 32 + lane);
+      // this lane's column in the pair's place (a pair has one unit where there are parts)
+      float* sums = q.partial + ((int64_t)pair * plan.cap * 256 + cta * 128 + quad * 32 + lane);
       const bool none = w.kb0 >= w.kb1;    // a group with no rows: its weight gradient is zero
       float keep[kBlocks][32];
       if (kChunked && !none) {             // the sums of the part's chunks, in their order
@@ -897,8 +899,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           }
           accumulator_free(bar, acc, lane);
         }
-      } else if (!none) {
-        ok = accumulator_ready(bar, n_acc & 1, n_acc, (int)cta);
+      }
+      bool kept = false;                   // sums of a long contraction wait in the pair's place
+      if (!kChunked && !none) {
+        for (int kb = w.kb0 + kLongStages; kb < w.kb1; kb += kLongStages, ++n_acc, kept = true) {
+          ok = accumulator_ready(bar, n_acc & 1, n_acc, (int)cta);
+          if (!ok) break;
+          for (int c0 = turn * 32; c0 < w.rows; c0 += 64) {
+            float r[32];
+            __syncwarp();
+            tmem_load32(lanes + (n_acc & 1) * 256 + c0, r);
+#pragma unroll
+            for (int c = 0; c < 32; ++c) {
+              r[c] += get(sums + (c0 + c) * 256, kept && c0 + c < w.rows);
+              put(sums + (c0 + c) * 256, r[c], c0 + c < w.rows);
+            }
+          }
+          accumulator_free(bar, n_acc & 1, lane);
+        }
+        if (ok) ok = accumulator_ready(bar, n_acc & 1, n_acc, (int)cta);
       }
       if (!ok) break;
       // first the values of this part: the tile's result, or sums for the part
@@ -921,6 +940,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             } else {
               __syncwarp();
               tmem_load32(lanes + (n_acc & 1) * 256 + c0, r);
+              if (kept) {
+#pragma unroll
+                for (int c = 0; c < 32; ++c) r[c] += get(sums + (c0 + c) * 256, c0 + c < w.rows);
+              }
             }
             if (result) {
               epilogue<MODE, ACT, T>(q, w, (int)cta, lane, quad, c0, r, b);

@@ -85,3 +85,67 @@ def test_kernels_see_what_the_one_before_them_wrote(layer):
     for i, db in enumerate(out):
         assert torch.equal(db[0], refs[i % 2])
     op.sync()
+
+
+# 129/128 and 252/128: their product is 1.98413, a little less than 254 times bf16's spacing in [1, 2)
+ONE, TWO = 129 / 128, 252 / 128
+
+
+def test_bias_gradient_of_many_rows_is_exact(layer):
+    """Counts of 16,777,216 rows: whole sums below 2^24 in every step."""
+    rows = 1 << 24
+    op = layer.EpLinearOp(layer.EpLinearConfig(1, 8, 8, rows), backward=True)
+    x = torch.zeros((rows, 8), dtype=torch.bfloat16, device=DEV)
+    dy = torch.zeros((rows, 8), dtype=torch.bfloat16, device=DEV)
+    dy[::3] = 1.0
+    w = torch.zeros((1, 8, 8), dtype=torch.bfloat16, device=DEV)
+    db = op.backward(dy, x, w, want_dx=False, want_dweight=False, want_dbias=True)[2]
+    op.sync()
+    assert (db == -(-rows // 3)).all()
+
+
+@pytest.mark.parametrize("what", ["dweight", "dweight of a segment", "forward", "dx"])
+def test_long_contractions_round_once(layer, what):
+    """Contractions of 2^21 to 2^24 equal terms of one sign. The sum's f32 error is bounded by
+    the sums that it is made of: 2^15 terms at a time in the tensor core, 2^11 steps that each
+    cut off less than 2^-22 of the sum so far, and up to 2^9 f32 additions: a little over 2^-11
+    altogether. The true sum lies 0.03 of a spacing from a bf16 value and rounding turns to the
+    next one 2^-9.1 of it away: the result has to be that value."""
+    bf = torch.bfloat16
+    one, two = (torch.tensor(v, dtype=bf, device=DEV) for v in (ONE, TWO))
+
+    def check(got, terms):
+        want = torch.tensor(terms * ONE * TWO, dtype=torch.float64).to(bf)
+        assert terms < 1 << 21 or abs(float(want) / (terms * ONE * TWO) - 1) < 2.0 ** -12
+        assert (got.float() == float(want)).all(), (float(got.float().min()), float(got.float().max()), float(want))
+
+    if what == "dweight":                      # cut into parts, each of many sums
+        rows = 1 << 24
+        op = layer.EpLinearOp(layer.EpLinearConfig(1, 8, 8, rows), backward=True)
+        x, dy = one.expand(rows, 8).contiguous(), two.expand(rows, 8).contiguous()
+        dw = op.backward(dy, x, torch.zeros((1, 8, 8), dtype=bf, device=DEV), want_dx=False)[1]
+        check(dw, rows)
+    elif what == "dweight of a segment":       # too many tiles for parts; short and empty ones beside it
+        counts = [5 * i % 97 for i in range(40)]
+        counts[7] = 1 << 21
+        begins = [sum(counts[:i]) for i in range(40)]
+        rows = sum(counts)
+        op = layer.EpLinearOp(layer.EpLinearConfig(40, 8, 8, rows), backward=True)
+        x, dy = one.expand(rows, 8).contiguous(), two.expand(rows, 8).contiguous()
+        at = {"row_begin": torch.tensor(begins, dtype=torch.int32, device=DEV),
+              "row_count": torch.tensor(counts, dtype=torch.int32, device=DEV)}
+        dw = op.backward(dy, x, torch.zeros((40, 8, 8), dtype=bf, device=DEV), want_dx=False, **at)[1]
+        for g in (7, 6, 39):
+            check(dw[g], counts[g])
+        assert (dw[0] == 0).all()
+    elif what == "forward":
+        K = 1 << 22
+        op = layer.EpLinearOp(layer.EpLinearConfig(1, K, 8, 5))
+        check(op.forward(one.expand(5, K).contiguous(), two.expand(1, 8, K).contiguous()), K)
+    else:
+        N = 1 << 22
+        op = layer.EpLinearOp(layer.EpLinearConfig(1, 8, N, 5), backward=True)
+        dx = op.backward(one.expand(5, N).contiguous(), torch.zeros((5, 8), dtype=bf, device=DEV),
+                         two.expand(1, N, 8).contiguous(), want_dweight=False)[0]
+        check(dx, N)
+    op.sync()
