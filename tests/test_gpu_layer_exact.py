@@ -149,3 +149,59 @@ def test_long_contractions_round_once(layer, what):
                          two.expand(1, N, 8).contiguous(), want_dweight=False)[0]
         check(dx, N)
     op.sync()
+
+
+# groups, K, N, counts, dweight dtype: contractions long enough to be cut, beside others that are not
+@pytest.mark.parametrize("c", [(3, 72, 40, [0, 3200, 17], torch.float32), (2, 512, 129, [700, 4000], torch.float32),
+                               (4, 64, 96, [5003, 1, 64, 3073], torch.bfloat16), (3, 136, 200, [3136, 0, 6271], torch.bfloat16)])
+def test_weight_gradient_cut_into_parts_over_uneven_segments(layer, c):
+    """Whole numbers: every sum is exact below 2^24. Rows outside the segments hold NaN."""
+    G, K, N, counts, dt = c
+    gen = torch.Generator(device=DEV).manual_seed(G)
+    begins = [sum(-(-n // 128) * 128 for n in counts[:i]) for i in range(G)]
+    rows = begins[-1] + counts[-1] + 70
+    x, dy = whole(gen, rows, K), whole(gen, rows, N)
+    held = torch.zeros(rows, dtype=torch.bool, device=DEV)
+    for b, n in zip(begins, counts):
+        held[b:b + n] = True
+    x[~held] = float("nan")
+    dy[~held] = float("nan")
+    w = torch.zeros((G, N, K), dtype=torch.bfloat16, device=DEV)
+    at = {"row_begin": torch.tensor(begins, dtype=torch.int32, device=DEV),
+          "row_count": torch.tensor(counts, dtype=torch.int32, device=DEV)}
+    op = layer.EpLinearOp(layer.EpLinearConfig(G, K, N, rows, weight_grad_dtype=dt), backward=True)
+    for _ in range(3):
+        _, dw, db = op.backward(dy, x, w, want_dx=False, want_dbias=True, **at)
+        for g, (b, n) in enumerate(zip(begins, counts)):
+            assert torch.equal(dw[g], (dy[b:b + n].double().t() @ x[b:b + n].double()).to(dt))
+            assert torch.equal(db[g], dy[b:b + n].double().sum(0).float())
+    op.sync()
+
+
+def test_all_of_a_large_segment(layer):
+    """270,000 rows of 8,192, nearly all of them in one segment: its weight and bias gradients
+    whole, its first and last rows and some between them of everything else."""
+    rows, K, N = 270000, 64, 8192
+    gen = torch.Generator(device=DEV).manual_seed(1)
+    x = torch.randint(0, 3, (rows, K), generator=gen, device=DEV).to(torch.bfloat16)
+    w = whole(gen, 2, N, K)
+    counts = [rows - 300, 300]
+    at = {"row_begin": torch.tensor([0, counts[0]], dtype=torch.int32, device=DEV),
+          "row_count": torch.tensor(counts, dtype=torch.int32, device=DEV)}
+    op = layer.EpLinearOp(layer.EpLinearConfig(2, K, N, rows, activation="relu"), backward=True)
+    z = torch.empty((rows, N), dtype=torch.bfloat16, device=DEV)
+    y = op.forward(x, w, preact=z, **at)
+    dx, dw, db = op.backward(torch.ones_like(z), x, w, z, want_dbias=True, **at)
+    op.sync()
+    some = torch.cat([torch.arange(0, 300), torch.arange(150000, 150300), torch.arange(counts[0] - 300, counts[0])]).to(DEV)
+    ref = x[some].double() @ w[0].double().t()
+    assert torch.equal(z[some].double(), ref) and torch.equal(y[some].double(), ref.clamp(min=0))
+    assert torch.equal(dx[some], ((ref > 0).double() @ w[0].double()).bfloat16())
+    want_w = torch.zeros((N, K), dtype=torch.float64, device=DEV)
+    want_b = torch.zeros(N, dtype=torch.float64, device=DEV)
+    for a in range(0, counts[0], 10000):
+        b = min(a + 10000, counts[0])
+        on = (x[a:b].float() @ w[0].float().t() > 0).double()    # whole numbers: exact
+        want_w += on.t() @ x[a:b].double()
+        want_b += on.sum(0)
+    assert torch.equal(dw[0], want_w.bfloat16()) and torch.equal(db[0], want_b.float())
