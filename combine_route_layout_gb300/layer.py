@@ -3,7 +3,9 @@ tensors: the router with its balance loss (EpRouterOp) and the experts'
 products (EpLinearOp). Argument checks and marshalling only; the work is the
 CUDA kernels behind ep_router_* and ep_linear_* of include/ep.h, on torch's
 current stream. An operator owns its workspace; calls on one operator are
-ordered by the caller (same stream, or events).
+ordered by the caller (same stream, or events), with the operator's device the
+current one. Results carry no autograd graph, as dispatch's and combine's do not:
+gradients come from the operators' own backward().
 """
 from __future__ import annotations
 
@@ -53,9 +55,13 @@ class _Op:
             self._handle = None
 
     def _stream(self):
-        """torch's current stream of the workspace's device, as a pointer. The allocator is
-        told of a stream other than the workspace's own, so that freeing the operator waits
-        for the work on it."""
+        """torch's current stream of the workspace's device, as a pointer. That device has to
+        be the current one, which is where the library launches. The allocator is told of a
+        stream other than the workspace's own, so that freeing the operator waits for the
+        work on it."""
+        if torch.cuda.current_device() != self._device_index:
+            _refuse(f"the operator is on {self.device}, which is not the current device "
+                    f"({torch.cuda.current_device()})")
         s = _raw_stream(self._device_index)
         if s not in self._streams:
             self._raw.record_stream(torch.cuda.current_stream(self.device))

@@ -523,7 +523,8 @@ ep_status ep_routing_layout_noalloc(int32_t world_size, int32_t max_num_inp_toke
  * times its mean over the segments that hold tokens. Sums run in a fixed
  * order: results do not change from run to run.
  *
- * Calls of one handle share its workspace: the caller orders them.
+ * Calls of one handle share its workspace: the caller orders them, and makes
+ * them with the workspace's device current.
  * ---------------------------------------------------------------------------
  */
 #define EP_MAX_ROUTER_GROUPS 32
@@ -617,7 +618,8 @@ ep_status ep_router_sync(ep_router_handle* h, void* stream);
  * is stored, dz because it is a tensor-core operand; dbias sums dz unrounded.
  * Rows outside the segments are neither used nor written.
  *
- * Calls of one handle share its workspace: the caller orders them.
+ * Calls of one handle share its workspace: the caller orders them, and makes
+ * them with the workspace's device current.
  * ---------------------------------------------------------------------------
  */
 typedef enum {
