@@ -142,19 +142,21 @@ class EpRouterOp(_Op):
         self._weights_form = self._form(self._slots, torch.float32)
         self._counts_form = self._form(self._counts, torch.int32)
         self._loss_form = self._form((), torch.float32)
-        self._last_tokens = self._last_array = None
+        self._last = (None, None)       # token counts and the C array that they became
 
     def _tokens(self, num_tokens):
         """The counts as a C array; the same counts as last time are not converted again."""
         if num_tokens is None:
             return None
-        if type(num_tokens) is list and num_tokens == self._last_tokens:
-            return self._last_array
+        last, array = self._last
+        if type(num_tokens) is list and num_tokens == last:
+            return array
         if len(num_tokens) != self.config.world_size:
             _refuse("num_tokens must give one count per source rank")
-        self._last_tokens = [int(n) for n in num_tokens]
-        self._last_array = ep._i32_array(self._last_tokens)
-        return self._last_array
+        counts = [int(n) for n in num_tokens]
+        array = ep._i32_array(counts)
+        self._last = (counts, array)    # in one step: host threads may ask meanwhile
+        return array
 
     def forward(self, logits, bias=None, num_tokens=None, balance=False):
         """(weights, indices), and with balance (weights, indices, counts, loss):

@@ -1,5 +1,5 @@
 """What the layer module does around a call, without a GPU: which device the call
-goes to. Nothing is launched."""
+goes to, what it keeps of its arguments. Nothing is launched."""
 import pytest
 import torch
 
@@ -37,3 +37,22 @@ def test_calls_are_refused_while_another_device_is_current(layer, monkeypatch):
         with pytest.raises(EpError) as ei:
             call()
         assert ei.value.status == EP_ERR_INVALID_ARG and "current" in str(ei.value)
+
+
+def test_token_counts_are_kept_whole(layer, monkeypatch):
+    """Counts and the C array that they became are replaced together: whoever asks for the same
+    counts between the two steps gets an array of these counts."""
+    op = layer.EpRouterOp(layer.EpRouterConfig(2, 4, 16, 2), device="cpu")
+    op._tokens([1, 2])
+    convert, seen = layer.ep._i32_array, []
+
+    def interrupted(values):
+        if len(seen) < 1:
+            seen.append(None)
+            seen.append(list(op._tokens([3, 4])))    # another thread, just now
+        return convert(values)
+
+    monkeypatch.setattr(layer.ep, "_i32_array", interrupted)
+    assert list(op._tokens([3, 4])) == [3, 4]
+    assert seen[1] == [3, 4]
+    assert list(op._tokens([1, 2])) == [1, 2]
