@@ -47,7 +47,7 @@ __global__ void __launch_bounds__(256, 4) dispatch_copy_kernel(DispatchParams p)
     }
 
     if (!STD) {
-      const uint32_t m = __ldg(p.mask + g);
+      const uint32_t m = p.mask[g];
       const int my_slot = slot_on_lane_rank(p, g, s, t, m, lane);
       if (seg == 0) write_meta_2d(p, g, s, t, m, my_slot, lane);
       for (uint32_t mm = m; mm; mm &= mm - 1) {
@@ -157,7 +157,7 @@ __global__ void __launch_bounds__(256, 4) dispatch_quant_kernel(DispatchParams p
       }
     };
     if (!STD) {
-      const uint32_t m = __ldg(p.mask + g);
+      const uint32_t m = p.mask[g];
       const int my_slot = slot_on_lane_rank(p, g, s, t, m, lane);
       if (seg == 0) write_meta_2d(p, g, s, t, m, my_slot, lane);
       for (uint32_t mm = m; mm; mm &= mm - 1) {

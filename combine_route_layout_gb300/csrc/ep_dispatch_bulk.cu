@@ -69,11 +69,11 @@ __global__ void __launch_bounds__(32) dispatch_bulk_copy_kernel(DispatchParams p
     int64_t dst_row = -1;
     uint32_t m;
     if (!STD) {
-      const uint32_t mask = __ldg(p.mask + g);
+      const uint32_t mask = p.mask[g];
       int sl = -1;
       if (lane < p.R && ((mask >> lane) & 1u)) {
         const int c = s * p.cpr + t / kChunk;
-        sl = __ldg(p.chunk_off + (int64_t)c * p.R + lane) + (int)__ldg(p.local8 + g * p.R + lane);
+        sl = p.chunk_off[(int64_t)c * p.R + lane] + (int)p.local8[g * p.R + lane];
         dst_row = (int64_t)lane * p.cap + sl;
         p.src_pos[dst_row] = s * (p.R * p.Tmax) + t;
       }
@@ -91,12 +91,12 @@ __global__ void __launch_bounds__(32) dispatch_bulk_copy_kernel(DispatchParams p
     } else {
       if (lane < p.k) {
         const int e = __ldg(p.idx + g * p.k + lane);
-        const int l = __ldg(p.local16 + g * p.k + lane);
+        const int l = p.local16[g * p.k + lane];
         if (e >= 0 && e < p.E && l != 0xFFFF) {
           const int c = s * p.cpr + t / kChunk;
-          const int64_t row = (int64_t)__ldg(p.rank_base + e / p.E_r) +
-                              __ldg(p.expert_offset + e) +
-                              __ldg(p.chunk_off + (int64_t)c * p.E + e) + l;
+          const int64_t row = (int64_t)p.rank_base[e / p.E_r] +
+                              p.expert_offset[e] +
+                              p.chunk_off[(int64_t)c * p.E + e] + l;
           if (row < p.cap) dst_row = row;
         }
         p.row_map[g * p.k + lane] = (int32_t)dst_row;

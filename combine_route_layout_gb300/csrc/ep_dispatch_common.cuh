@@ -15,11 +15,11 @@ __device__ __forceinline__ int slot_on_lane_rank(const DispatchParams& p, int64_
                                                  uint32_t m, int lane) {
   if (lane < p.R && ((m >> lane) & 1u)) {
     const int c = s * p.cpr + t / kChunk;
-    const int local = __ldg(p.local8 + g * p.R + lane);
-    if (!p.chunk_cnt) return __ldg(p.chunk_off + (int64_t)c * p.R + lane) + local;
+    const int local = p.local8[g * p.R + lane];
+    if (!p.chunk_cnt) return p.chunk_off[(int64_t)c * p.R + lane] + local;
     int off = 0;  // small batch: at most kSmallScanChunks - 1 earlier chunks
 #pragma unroll 4
-    for (int cc = 0; cc < c; ++cc) off += __ldg(p.chunk_cnt + (int64_t)cc * p.R + lane);
+    for (int cc = 0; cc < c; ++cc) off += p.chunk_cnt[(int64_t)cc * p.R + lane];
     return off + local;
   }
   return -1;
@@ -29,7 +29,7 @@ __device__ __forceinline__ int slot_on_lane_rank(const DispatchParams& p, int64_
 __device__ __forceinline__ void recv_from_counts(const DispatchParams& p) {
   if (!p.chunk_cnt || blockIdx.x != 0 || (int)threadIdx.x >= p.R) return;
   int n = 0;
-  for (int cc = 0; cc < p.R * p.cpr; ++cc) n += __ldg(p.chunk_cnt + (int64_t)cc * p.R + threadIdx.x);
+  for (int cc = 0; cc < p.R * p.cpr; ++cc) n += p.chunk_cnt[(int64_t)cc * p.R + threadIdx.x];
   p.recv_num_token[threadIdx.x] = n;
 }
 
@@ -40,11 +40,11 @@ __device__ __forceinline__ int64_t row_on_lane_slot(const DispatchParams& p, int
   if (lane >= p.k) return -1;
   const int e = __ldg(p.idx + g * p.k + lane);
   if (e < 0 || e >= p.E) return -1;
-  const int l = __ldg(p.local16 + g * p.k + lane);
+  const int l = p.local16[g * p.k + lane];
   if (l == 0xFFFF) return -1;
   const int c = s * p.cpr + t / kChunk;
-  const int64_t row = (int64_t)__ldg(p.rank_base + e / p.E_r) + __ldg(p.expert_offset + e) +
-                      __ldg(p.chunk_off + (int64_t)c * p.E + e) + l;
+  const int64_t row = (int64_t)p.rank_base[e / p.E_r] + p.expert_offset[e] +
+                      p.chunk_off[(int64_t)c * p.E + e] + l;
   if (row >= p.cap) return -1;  // capacity overflow is flagged by the layout kernel
   return row;
 }

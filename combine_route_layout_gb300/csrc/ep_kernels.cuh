@@ -286,7 +286,8 @@ constexpr int kCombineUnroll = EP_COMBINE_UNROLL;  // 256-element steps per comb
 
 // Launch `kernel` with programmatic stream serialization, so it may begin
 // while the previous kernel in the stream is still running (it waits with
-// griddepcontrol.wait before reading that kernel's outputs).
+// griddepcontrol.wait before reading that kernel's outputs, and reads them by plain
+// loads: the read-only path is for data that nobody writes while the kernel is alive).
 template <typename... Args>
 inline cudaError_t launch_pdl(void (*kernel)(Args...), int grid, int block, size_t smem,
                               cudaStream_t st, Args... args) {

@@ -103,11 +103,11 @@ __global__ void __launch_bounds__(256, 4) split_stage_kernel(SplitParams p) {
       pdl_wait();
       waited = true;
     }
-    const uint32_t m = __ldg(p.mask + t);
+    const uint32_t m = p.mask[t];
     int pos = -1;
     if (lane < p.R && ((m >> lane) & 1u))
-      pos = __ldg(p.chunk_off + (int64_t)(t / kChunk) * p.R + lane) +
-            __ldg(p.local8 + (int64_t)t * p.R + lane);
+      pos = p.chunk_off[(int64_t)(t / kChunk) * p.R + lane] +
+            p.local8[(int64_t)t * p.R + lane];
     if (lane < p.R) p.slot_own[(int64_t)t * p.R + lane] = pos;
     if (pos >= 0) p.send_list[(int64_t)lane * p.Tmax + pos] = t;
   }

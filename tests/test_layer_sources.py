@@ -1,4 +1,4 @@
-"""What the layer operators' kernels have to keep to and no run can show: the
+"""What the kernels have to keep to and no run can show: the
 memory order of what they share, read from their sources."""
 import os
 import re
@@ -41,3 +41,12 @@ def test_overlapped_kernels_read_by_plain_loads():
             continue
         for line in lines:
             assert not re.search(r"__ldg\(|ld_nc|\.nc\.", line), f"{name}: {line.strip()}"
+
+
+def test_dispatch_reads_the_routing_layout_by_plain_loads():
+    """Dispatch kernels start while the routing layout is still being written."""
+    written = "mask|local8|local16|chunk_off|chunk_cnt|rank_base|expert_offset"
+    for name in ("ep_dispatch.cu", "ep_dispatch_bulk.cu", "ep_dispatch_common.cuh", "ep_split.cu"):
+        text = "".join(code(name))
+        assert not re.search(rf"(__ldg|ld_nc_v4)\(\s*p\.({written})\b", text), name
+        assert re.search(rf"p\.({written})\[", text), name
