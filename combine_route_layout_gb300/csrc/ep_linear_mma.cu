@@ -65,7 +65,7 @@ constexpr int kWorth = 24, kLeast = 7, kWorthGrad = 48, kLeastGrad = 16;
 // f32 outputs: the tensor core cuts off what its accumulator cannot hold, an
 // error that grows with the number of steps to the power 3/2 (7168 terms: 8e-6 of
 // the result); sums of 512 terms are added up in registers instead, which
-// leaves 6e-7.
+// leaves 4.5e-7.
 constexpr int kChunk32 = 8;                      // stages of such a sum
 constexpr int kLongStages = kLongTerms / kDepth; // bf16 outputs: stages of a sum
 constexpr int kEpilogueWarps = 8;                // two to each quarter of the TMEM lanes

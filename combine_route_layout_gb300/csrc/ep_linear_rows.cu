@@ -8,9 +8,10 @@
 // few to fill the GPU with warps, `split` warps of a CTA share them, each with
 // its part of the terms. There is nothing to set up, where the tensor-core kernel
 // waits for its pipeline to fill and then joins the parts of its tiles. K 4096, N
-// 4096, in us, against that kernel: one row 8.2 (12.3), two 10.3 (12.3), three
-// 16.4 (12.3): every row more has its loads of x and its conversions, so more
-// than two rows go to the tensor cores. N 256: 4.9, 5.1, 8.2 (10.3).
+// 4096, in us from a graph, against that kernel: one row 9.9 (11.7), two 8.9 (11.7);
+// N 256: 3.1, 3.2 (8.0); K 1024, N 1024: 3.1, 3.0 (5.8); only two rows x 4096 x 32768
+// take longer, 51.2 (45.4). Every row more has its loads of x and its conversions:
+// three took 16.4 (11.8 there), so more than two go to the tensor cores.
 #include "ep_launch.cuh"
 #include "ep_linear.cuh"
 

@@ -1,7 +1,9 @@
-"""One training step of a mixture-of-experts layer, and one decode step, with
-everything on the path from this package: the router's projection, the router
-with its balance loss, dispatch into the packed per-expert layout, the gated
-experts, the weighted combine, and all gradients.
+"""One training step of a mixture-of-experts layer, and one decode step, over this
+package's operators: the router's projection, the router with its balance loss,
+dispatch into the packed per-expert layout, the gated experts, the weighted
+combine, and their gradients. Between them, the backward pass takes torch's
+elementwise operations for the gradient of combine's weights and for the rows
+that it scales by them.
 
     python examples/moe_layer.py            # prints the loss falling over a few steps
 

@@ -516,11 +516,14 @@ ep_status ep_routing_layout_noalloc(int32_t world_size, int32_t max_num_inp_toke
  * ties to the lowest index, best first, have the weights
  *   softmax   p_e; normalize_weights: softmax over the selected
  *   sigmoid   s_e; normalize_weights: s_e / sum of the selected s
- * times route_scale; a slot with no expert left holds index -1, weight 0.
+ * times route_scale; a slot with no expert left holds index -1, weight 0. Where
+ * all selected scores are 0 in f32 (sigmoid of logits below about -88), so are
+ * the weights.
  *
  * Balance loss of a segment of n tokens: sum_e f_e P_e with
  * f_e = count_e E / (k n) and P_e the mean of p_e; the loss is balance_coef
- * times its mean over the segments that hold tokens. Sums run in a fixed
+ * times its mean over the segments that hold tokens. The loss' p_e and all
+ * gradients are exact to about 2^-21 of a term. Sums run in a fixed
  * order: results do not change from run to run.
  *
  * Calls of one handle share its workspace: the caller orders them, and makes
@@ -615,7 +618,8 @@ ep_status ep_router_sync(ep_router_handle* h, void* stream);
  * first: y = silu(z_gate) z_up + residual.
  *
  * bf16 operands, f32 accumulation. z and dz are rounded to bf16, z because it
- * is stored, dz because it is a tensor-core operand; dbias sums dz unrounded.
+ * is stored, dz because it is a tensor-core operand, whatever the results'
+ * types; dbias sums dz unrounded. silu and its slope are exact to about 2^-21.
  * Rows outside the segments are neither used nor written.
  *
  * Calls of one handle share its workspace: the caller orders them, and makes
