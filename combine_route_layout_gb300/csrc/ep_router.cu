@@ -266,6 +266,19 @@ __device__ __forceinline__ float row_sum(const float (&p)[VPL]) {
   return warp_sum(s);
 }
 
+// raw_scores and their sum. The fast quotient is 0 where 1 + exp(-l) is above 2^126: a
+// row whose every sigmoid is that small (l below -87) takes the exact ones.
+template <int VPL, bool SIGMOID>
+__device__ __forceinline__ float raw_total(const float (&l)[VPL], float top, float (&p)[VPL]) {
+  raw_scores<VPL, SIGMOID>(l, top, p);
+  float total = row_sum<VPL>(p);
+  if (SIGMOID && !(total > 1e-30f)) {
+    exact_scores<VPL>(l, false, p);
+    total = row_sum<VPL>(p);
+  }
+  return total;
+}
+
 struct RowPlace {
   int rank, t0, n;    // rows t0 .. t0 + n - 1 of `rank` (n may be 0 or negative)
   int pad_end;        // rows up to here (exclusive) exist in the arrays
@@ -519,10 +532,10 @@ __global__ void __launch_bounds__(kRouterWarps * 32, router_ctas(VPL, SELECT))
     if (!SIGMOID && (BALANCE || !p.normalize)) top = row_max<VPL>(l);
     if (SIGMOID && SELECT) {
       exact_scores<VPL>(l, plain, pr);
+      if (BALANCE) total = row_sum<VPL>(pr);
     } else if (BALANCE || !p.normalize) {
-      raw_scores<VPL, SIGMOID>(l, top, pr);
+      total = raw_total<VPL, SIGMOID>(l, top, pr);
     }
-    if (BALANCE || (!SIGMOID && !p.normalize)) total = row_sum<VPL>(pr);
     if (BALANCE) {
       const float inv = total > 0.0f ? 1.0f / total : 0.0f;
 #pragma unroll
@@ -764,10 +777,9 @@ __global__ void __launch_bounds__(kRouterWarps * 32, router_ctas(VPL))
         load_row<VPL, T>(logits + (g + kRouterWarps) * p.E, p.E, lane, p.vec, next);
       (void)mask_row<VPL, T>(l, -lowest<T>(), p.err);
       const float top = SIGMOID ? 0.0f : row_max<VPL>(l);
-      raw_scores<VPL, SIGMOID>(l, top, pr);
       float inv = 0.0f;
       if (q.counts || (!SIGMOID && !p.normalize)) {
-        const float total = row_sum<VPL>(pr);
+        const float total = raw_total<VPL, SIGMOID>(l, top, pr);
         inv = total > 0.0f ? 1.0f / total : 0.0f;
       }
       if (q.counts) {

@@ -48,3 +48,28 @@ def test_router_with_fewer_open_groups_than_it_may_take(layer, E, groups, score)
     assert torch.equal(counts.cpu().long(), ct)
     # a mean of at most 15 rows' quotients, each over up to 1024 terms that decay quickly
     assert abs(float(loss) - float(ls)) <= 84 * 2.0 ** -23 * max(1.0, float(ls))
+
+
+def test_sigmoid_rows_at_the_end_of_their_range(layer):
+    """Rows whose scores are the last ones above f32's underflow: the loss of the call that
+    selects, the loss of given indices and the gradient agree with the formula. A score of
+    2^-128 has 21 bits, so a probability is off by a few 2^-21, the others' steps by less."""
+    E, k = 32, 4
+    gen = torch.Generator().manual_seed(7)
+    l = -87.4 - 1.3 * torch.rand((1, 9, E), generator=gen)
+    l[0, 3, 5:] = -math.inf
+    l[0, 4] = torch.randn(E, generator=gen)
+    l = l.to(DEV)
+    op = layer.EpRouterOp(layer.EpRouterConfig(1, 9, E, k, score_func="sigmoid"))
+    w, idx, counts, loss = op.forward(l, balance=True)
+    counts2, loss2 = op.balance_loss(l, idx)
+    d = op.backward(l, counts=counts, d_loss=torch.ones((), device=DEV))
+    op.sync()
+    x = l.double().requires_grad_(True)
+    p = torch.sigmoid(x) / torch.sigmoid(x).sum(-1, keepdim=True)
+    want = (counts[0].double() * E / (k * 9) * p.sum((0, 1)) / 9).sum()
+    (grad,) = torch.autograd.grad(want, x)
+    assert torch.equal(counts, counts2)
+    for got in (loss, loss2):
+        assert abs(float(got) - float(want.detach())) <= 2.0 ** -18 * float(want.detach())
+    assert (d.double() - torch.nan_to_num(grad)).abs().max() <= 2.0 ** -18 * grad.nan_to_num().abs().max()
