@@ -15,7 +15,7 @@ def test_host_threads_with_handles_of_their_own():
     from combine_route_layout_gb300.build import build
     build()
     from combine_route_layout_gb300 import ep, layer
-    T, k, failed, start = 8, 4, [], threading.Barrier(4)
+    T, k, failed, start = 8, 4, [], threading.Barrier(4, timeout=60)
 
     def work(E):
         try:
