@@ -8,7 +8,8 @@ library exists; any other use fails loudly if the library is missing.
 
 _EXPORTS = ("EpDispatchCombineConfig", "EpDispatchCombineOp", "EpError")
 _RANK_EXPORTS = ("EpRankOp", "exchange_workspaces", "phase_barrier")
-_LAYER_EXPORTS = ("EpRouterConfig", "EpRouterOp", "EpLinearConfig", "EpLinearOp")
+_LAYER_EXPORTS = ("EpRouterConfig", "EpRouterOp", "EpLinearConfig", "EpLinearOp", "EpQuantConfig",
+                  "EpQuantOp", "EpQuantLinearOp", "EpNormConfig", "EpNormOp")
 
 
 def __getattr__(name):

@@ -4,7 +4,7 @@
 // the FP8 / FP4 block quantisers.
 #pragma once
 
-#include "ep_kernels.cuh"
+#include "ep_quant.cuh"
 
 namespace ep {
 namespace {
@@ -101,40 +101,6 @@ __device__ void write_meta_std(const DispatchParams& p, int64_t g, int s, int t,
 // bf16 in. Lane covers 16 consecutive elements (two 16-byte loads) per
 // 512-element step, so 8 lanes cover one 128-element block; the block's amax
 // is reduced with three xor-shuffles inside that 8-lane group.
-
-__device__ __forceinline__ void unpack16(const uint4& a, const uint4& b, float f[16]) {
-  const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    f[2 * i] = bf16_lo(w[i]);
-    f[2 * i + 1] = bf16_hi(w[i]);
-  }
-}
-
-// x / scale rounded to nearest even, for |x| <= amax = scale * 448 (or * 6),
-// from rcp = 1/scale correctly rounded: the product q0 = x * rcp is within
-// two ulps of the quotient, the residual x - q0 * scale is exact in one
-// fused multiply-add, and one more fused multiply-add with rcp rounds the
-// corrected quotient (Markstein's correction step). The residual is exact
-// while it does not underflow, which holds for every |x| >= 2^-103; with
-// amax >= kRcpMinAmax any smaller x quotes below 2^-14, far under half the
-// smallest nonzero code (2^-10 for E4M3, 0.25 for E2M1), so its code (a
-// signed zero) does not depend on the last bits. Blocks with a smaller amax are scaled by 2^100 first (x and
-// the scale, both exactly, so the quotient is unchanged). An all-zero block
-// (scale 0) gets rcp = 0, which turns every quotient into a zero of x's
-// sign, the code of x / 0 as the block quantiser defines it. The sign bit of
-// x is put back for x = -0 (the residual step would make it +0). Four
-// floating-point operations instead of a full division per element, with no
-// branch; every (x, amax) pair of bf16 values is checked against the IEEE
-// quotient's code on the GPU.
-constexpr float kRcpMinAmax = 0x1p-80f;
-
-__device__ __forceinline__ float quotient(float x, float scale, float rcp) {
-  const float q0 = __fmul_rn(x, rcp);
-  const float r = __fmaf_rn(-q0, scale, x);
-  const float q = __fmaf_rn(r, rcp, q0);
-  return __int_as_float(__float_as_int(q) | (__float_as_int(x) & 0x80000000));
-}
 
 // RCP: quotients from the reciprocal and residual (above); otherwise by IEEE
 // division. Both give the same codes.

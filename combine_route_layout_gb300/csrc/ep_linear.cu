@@ -8,7 +8,7 @@
 
 #include "ep_header.cuh"
 #include "ep_launch.cuh"
-#include "ep_linear.cuh"
+#include "ep_linear_grad.cuh"
 
 namespace ep {
 namespace {
@@ -19,61 +19,6 @@ namespace {
 // columns of every `lanes`th row, so that a warp's access is contiguous; the
 // blocks' sums go to `part` and are added in block order by bias_grad_kernel. dz is rounded to bf16 because the products read
 // it as a tensor-core operand; the sums are of the unrounded values.
-constexpr int kGradRows = 64;
-constexpr int kGradThreads = 256;
-
-struct GradParams {
-  LinearParams p;
-  __nv_bfloat16* dz;         // NULL: only the sums
-  float* part;               // [row blocks][Nw] or NULL
-  int64_t row_blocks;        // rows of `part`
-  int lanes;                 // threads that share a column: 1, 2, 4 or 8
-  float* db;                 // [G][Nw]
-};
-
-__device__ __forceinline__ int64_t blocks_of(int64_t count) {
-  return (count + kGradRows - 1) / kGradRows;
-}
-
-// VEC columns from an aligned place, as f32.
-template <int VEC, typename T>
-__device__ __forceinline__ void load_columns(const T* at, float (&v)[VEC]) {
-  if (VEC == 8 && sizeof(T) == 2) {
-    const uint4 q = ld_once_v4(at);
-    const uint32_t u[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-    for (int i = 0; i < VEC; ++i) v[i] = (i & 1) ? bf16_hi(u[i / 2]) : bf16_lo(u[i / 2]);
-  } else if (VEC == 8) {
-#pragma unroll
-    for (int h = 0; h < VEC / 4; ++h) {
-      const uint4 q = ld_once_v4(at + h * 4);
-      v[(h * 4) % VEC] = __uint_as_float(q.x);
-      v[(h * 4 + 1) % VEC] = __uint_as_float(q.y);
-      v[(h * 4 + 2) % VEC] = __uint_as_float(q.z);
-      v[(h * 4 + 3) % VEC] = __uint_as_float(q.w);
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < VEC; ++i) v[i] = (float)at[i];
-  }
-}
-
-template <int VEC>
-__device__ __forceinline__ void store_dz(__nv_bfloat16* at, const float (&v)[VEC]) {
-  if (VEC == 8) {
-    st_v4(at, make_uint4(cvt_bf16x2(v[0], v[1 % VEC]), cvt_bf16x2(v[2 % VEC], v[3 % VEC]),
-                         cvt_bf16x2(v[4 % VEC], v[5 % VEC]), cvt_bf16x2(v[6 % VEC], v[7 % VEC])));
-  } else {
-#pragma unroll
-    for (int i = 0; i < VEC; ++i) at[i] = __float2bfloat16_rn(v[i]);
-  }
-}
-
-// A group's block of rows, number `b` over all groups; false past the last.
-struct BlockPlace {
-  int64_t begin, row0, row1;
-};
-
 template <int VEC, int ACT, typename T>
 __global__ void __launch_bounds__(kGradThreads) act_grad_kernel(GradParams q) {
   begin_overlapped();
@@ -81,33 +26,7 @@ __global__ void __launch_bounds__(kGradThreads) act_grad_kernel(GradParams q) {
   __shared__ BlockPlace at;
   const bool gated = ACT == EP_ACT_SWIGLU;
   const int64_t block = blockIdx.x;
-  // the group of this block: a warp adds up the groups' blocks, 32 at a time
-  if (threadIdx.x < 32) {
-    const int lane = threadIdx.x;
-    int64_t before = 0;
-    if (lane == 0) at.row0 = at.row1 = at.begin = 0;
-    __syncwarp();
-    for (int g0 = 0; g0 < p.s.G && before <= block; g0 += 32) {
-      int64_t begin = 0, count = 0;
-      if (g0 + lane < p.s.G) segment_of(p.s, g0 + lane, begin, count);
-      int64_t incl = blocks_of(count);
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int64_t v = __shfl_up_sync(kFull, incl, o);
-        if (lane >= o) incl += v;
-      }
-      const int64_t mine = before + incl - blocks_of(count);
-      if (block >= mine && block < before + incl) {
-        at.begin = begin;
-        at.row0 = (block - mine) * kGradRows;
-        at.row1 = min(count, at.row0 + kGradRows);
-      }
-      before += __shfl_sync(kFull, incl, 31);
-    }
-    // segments that do not overlap leave the last block free
-    if (p.s.begin && lane == 0 && block == q.row_blocks - 1 && before > block)
-      atomicOr(p.s.err, kErrSegment);
-  }
+  find_block(p.s, block, q.row_blocks, at);
   __syncthreads();
   const int wide = kGradThreads / q.lanes;      // threads beside each other in a row
   const int lane_row = threadIdx.x / wide, tx = threadIdx.x - lane_row * wide;
@@ -181,44 +100,6 @@ __global__ void __launch_bounds__(kGradThreads) act_grad_kernel(GradParams q) {
   }
 }
 
-// db_g: the sums of the group's blocks, in block order. A CTA takes 32
-// columns, a warp every 8th block.
-__global__ void __launch_bounds__(256) bias_grad_kernel(GradParams q) {
-  begin_overlapped();
-  const LinearParams& p = q.p;
-  __shared__ float sum[8][32];
-  __shared__ int64_t range[2];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int c = blockIdx.x * 32 + lane;
-  const int g = blockIdx.y;
-  if (warp == 0) {
-    int64_t before = 0, begin, count = 0;
-    for (int i = lane; i < g; i += 32) {
-      segment_of(p.s, i, begin, count);
-      before += blocks_of(count);
-    }
-#pragma unroll
-    for (int o = 16; o; o >>= 1) before += __shfl_xor_sync(kFull, before, o);
-    segment_of(p.s, g, begin, count);
-    if (lane == 0) {
-      range[0] = min(before, q.row_blocks);
-      range[1] = min(before + blocks_of(count), q.row_blocks);
-    }
-  }
-  __syncthreads();
-  float s = 0.0f;
-  if (c < p.Nw)
-    for (int64_t b = range[0] + warp; b < range[1]; b += 8) s += q.part[b * p.Nw + c];
-  sum[warp][lane] = s;
-  __syncthreads();
-  if (warp == 0 && c < p.Nw) {
-    s = 0.0f;
-#pragma unroll
-    for (int w = 0; w < 8; ++w) s += sum[w][lane];
-    q.db[(int64_t)g * p.Nw + c] = s;
-  }
-}
-
 template <int VEC, typename T>
 cudaError_t grad_typed(GradParams q, cudaStream_t st) {
   // rows too short for a CTA's threads: several of them share a column
@@ -273,29 +154,8 @@ size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 static_assert(kTicketOffset + kLinearMaxPairs * 2 * sizeof(unsigned int) <= kHeaderBytes, "tickets");
 
 ep_status plan_linear(const ep_linear_config* c, ep_linear_handle* h) {
-  if (!c) return lfail(EP_ERR_INVALID_ARG, "linear config is NULL");
-  if (c->num_groups < 1 || c->num_groups > EP_MAX_EXPERTS)
-    return lfail(EP_ERR_INVALID_ARG, "num_groups outside [1, 1024]");
-  if (c->groups_per_base < 0)
-    return lfail(EP_ERR_INVALID_ARG, "groups_per_base must be >= 0");
-  if (c->in_features < 8 || c->in_features % 8 != 0)
-    return lfail(EP_ERR_INVALID_ARG, "in_features must be a positive multiple of 8");
-  if (c->out_features < 1 || c->out_features > (1 << 22) || c->in_features > (1 << 22))
-    return lfail(EP_ERR_INVALID_ARG, "in_features and out_features must be in [1, 2^22]");
-  if (c->max_rows < 1 || c->max_rows > INT32_MAX - 1024)
-    return lfail(EP_ERR_INVALID_ARG, "max_rows must be >= 1 and fit int32");
-  if (c->out_dtype != EP_DTYPE_BF16 && c->out_dtype != EP_DTYPE_FP32)
-    return lfail(EP_ERR_INVALID_ARG, "out_dtype must be BF16 or FP32");
-  if (c->weight_grad_dtype != EP_DTYPE_BF16 && c->weight_grad_dtype != EP_DTYPE_FP32)
-    return lfail(EP_ERR_INVALID_ARG, "weight_grad_dtype must be BF16 or FP32");
-  if (c->activation < EP_ACT_NONE || c->activation > EP_ACT_SWIGLU)
-    return lfail(EP_ERR_INVALID_ARG, "unknown activation");
-  // tiles are numbered in int32: at most one per 32 rows (and group) and 256 features
-  const int64_t wide = (2 * (int64_t)c->out_features > c->in_features ? 2 * (int64_t)c->out_features
-                                                                      : c->in_features) / 256 + 1;
-  if ((c->max_rows / 32 + c->num_groups) * wide > INT32_MAX ||
-      (int64_t)c->num_groups * wide * (c->in_features / 256 + 1) > INT32_MAX)
-    return lfail(EP_ERR_INVALID_ARG, "max_rows, num_groups and features give too many tiles");
+  const ep_status s = check_linear(c);
+  if (s != EP_OK) return s;
   h->cfg = *c;
   h->Nw = c->activation == EP_ACT_SWIGLU ? 2 * c->out_features : c->out_features;
   h->ldz = (h->Nw + 63) / 64 * 64;   // whole 64-element blocks
@@ -376,6 +236,37 @@ ep_status fill_linear(const ep_linear_handle* h, const void* x, const void* w,
 ep_status status_of(cudaError_t e) { return e == cudaSuccess ? EP_OK : lcuda(e); }
 
 }  // namespace
+
+namespace ep {
+
+ep_status check_linear(const ep_linear_config* c) {
+  if (!c) return lfail(EP_ERR_INVALID_ARG, "linear config is NULL");
+  if (c->num_groups < 1 || c->num_groups > EP_MAX_EXPERTS)
+    return lfail(EP_ERR_INVALID_ARG, "num_groups outside [1, 1024]");
+  if (c->groups_per_base < 0)
+    return lfail(EP_ERR_INVALID_ARG, "groups_per_base must be >= 0");
+  if (c->in_features < 8 || c->in_features % 8 != 0)
+    return lfail(EP_ERR_INVALID_ARG, "in_features must be a positive multiple of 8");
+  if (c->out_features < 1 || c->out_features > (1 << 22) || c->in_features > (1 << 22))
+    return lfail(EP_ERR_INVALID_ARG, "in_features and out_features must be in [1, 2^22]");
+  if (c->max_rows < 1 || c->max_rows > INT32_MAX - 1024)
+    return lfail(EP_ERR_INVALID_ARG, "max_rows must be >= 1 and fit int32");
+  if (c->out_dtype != EP_DTYPE_BF16 && c->out_dtype != EP_DTYPE_FP32)
+    return lfail(EP_ERR_INVALID_ARG, "out_dtype must be BF16 or FP32");
+  if (c->weight_grad_dtype != EP_DTYPE_BF16 && c->weight_grad_dtype != EP_DTYPE_FP32)
+    return lfail(EP_ERR_INVALID_ARG, "weight_grad_dtype must be BF16 or FP32");
+  if (c->activation < EP_ACT_NONE || c->activation > EP_ACT_SWIGLU)
+    return lfail(EP_ERR_INVALID_ARG, "unknown activation");
+  // tiles are numbered in int32: at most one per 32 rows (and group) and 256 features
+  const int64_t wide = (2 * (int64_t)c->out_features > c->in_features ? 2 * (int64_t)c->out_features
+                                                                      : c->in_features) / 256 + 1;
+  if ((c->max_rows / 32 + c->num_groups) * wide > INT32_MAX ||
+      (int64_t)c->num_groups * wide * (c->in_features / 256 + 1) > INT32_MAX)
+    return lfail(EP_ERR_INVALID_ARG, "max_rows, num_groups and features give too many tiles");
+  return EP_OK;
+}
+
+}  // namespace ep
 
 extern "C" size_t ep_linear_workspace_size(const ep_linear_config* cfg) {
   ep_linear_handle h{};

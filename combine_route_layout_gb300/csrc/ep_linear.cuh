@@ -65,6 +65,9 @@ struct LinearParams {
   int dw_f32;
 };
 
+// EP_OK, or what is wrong with a config of the products.
+ep_status check_linear(const ep_linear_config* c);
+
 // The products (ep_linear_mma.cu), over `sms` multiprocessors.
 cudaError_t launch_linear_forward(const LinearParams& p, int sms, cudaStream_t st);
 // The forward for at most kFewRows dense rows (ep_linear_rows.cu).

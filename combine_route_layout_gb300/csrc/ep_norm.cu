@@ -1,0 +1,516 @@
+// The norms around a block: u = norm(block) w_post, stream = residual + alpha gate
+// u, out = norm(stream) w, and the backward pass. Definitions: ep.h.
+//
+// Forward: a CTA takes a row, which stays in registers, VECS pieces of 8 elements a
+// thread, between the one or two sums over it and its results: every tensor is read
+// and written once. Bound by HBM; with few rows by latency, so that a row then takes
+// as many threads as it has pieces (up to 1024).
+//
+// Backward: a CTA walks rows, thread t always at the same columns, whose sums over
+// rows stay in registers; the CTAs' sums are added in their order by
+// norm_sums_kernel.
+#include <climits>
+#include <cstring>
+#include <new>
+
+#include <cuda_bf16.h>
+
+#include "ep_header.cuh"
+#include "ep_launch.cuh"
+#include "ep_pieces.cuh"
+#include "ep_quant.cuh"
+
+namespace ep {
+namespace {
+
+struct NormParams {
+  int64_t rows;
+  int H, Hb, pieces;            // features, blocks of 128, pieces of 8
+  float eps, alpha, inv;        // inv: 1 / H
+  int post, gate, quant;
+  const void* residual;
+  const void* block;            // NULL: stream is the residual
+  const float* gates;
+  const float* w_post;
+  const float* w;
+  void* stream;
+  void* out;
+  float* scales;
+  float* stats;                 // [rows][2] or NULL
+  // backward
+  const void* dout;
+  const void* d_stream;         // NULL: zero
+  void* d_residual;
+  void* d_block;
+  float* d_gate;                // of tokens
+  float* part;                  // [CTAs][sums][H]
+  int n_sums;                   // of w, w_post, gate of features
+  float* sums[3];
+  int ctas;
+};
+
+// The sum over the CTA, the same in every thread: warps by shuffles, then their sums
+// in their order. `room` is written anew by every call: two calls in a row take two.
+__device__ __forceinline__ float cta_sum(float v, float* room) {
+#pragma unroll
+  for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
+  if ((threadIdx.x & 31) == 0) room[threadIdx.x >> 5] = v;
+  __syncthreads();
+  const int warps = blockDim.x >> 5;
+  v = 0.0f;
+  for (int w = 0; w < warps; ++w) v += room[w];
+  return v;
+}
+
+// 1 / sqrt(v), rounded within a step of f32; 0 for an infinite v.
+__device__ __forceinline__ float inv_sqrt(float v) { return __frsqrt_rn(v); }
+
+template <typename S, typename B, int VECS>
+__global__ void __launch_bounds__(VECS == 1 ? 1024 : 512) norm_kernel(NormParams p) {
+  begin_overlapped();
+  __shared__ float room[2][32];
+  const int64_t row = blockIdx.x;
+  const int64_t base = row * p.H;
+  const int T = blockDim.x;
+  Raw8<S> rs[VECS];
+  Raw8<B> rb[VECS];
+  bool in[VECS];
+#pragma unroll
+  for (int i = 0; i < VECS; ++i) {
+    const int piece = threadIdx.x + i * T;
+    in[i] = piece < p.pieces;
+    zero8(rs[i]);
+    zero8(rb[i]);
+    if (in[i]) {
+      load8<S>(p.residual, base + piece * 8, rs[i]);
+      if (p.block) load8<B>(p.block, base + piece * 8, rb[i]);
+    }
+  }
+  float by_block = 1.0f;
+  if (p.post && p.block) {
+    float sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < VECS; ++i) {
+      float y[8];
+      floats8(rb[i], y);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) sum = fmaf(y[j], y[j], sum);
+    }
+    by_block = inv_sqrt(cta_sum(sum, room[0]) * p.inv + p.eps);
+  }
+  float s[VECS][8];
+  float times = p.alpha;
+  if (p.block && p.gate == EP_GATE_TOKEN) times *= p.gates[row];
+  float sum = 0.0f;
+#pragma unroll
+  for (int i = 0; i < VECS; ++i) {
+    floats8(rs[i], s[i]);
+    if (p.block && in[i]) {
+      const int at = (threadIdx.x + i * T) * 8;
+      float y[8];
+      floats8(rb[i], y);
+      if (p.post) {
+        float w[8];
+        weights8(p.w_post, at, w);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) y[j] = y[j] * by_block * w[j];
+      }
+      if (p.gate == EP_GATE_FEATURE) {
+        float g[8];
+        weights8(p.gates, at, g);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) y[j] *= g[j];
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) s[i][j] = fmaf(times, y[j], s[i][j]);
+      store8<S>(p.stream, base + at, s[i]);
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) sum = fmaf(s[i][j], s[i][j], sum);
+  }
+  const float by = inv_sqrt(cta_sum(sum, room[1]) * p.inv + p.eps);
+  if (p.stats && threadIdx.x == 0) {
+    p.stats[2 * row] = by;
+    p.stats[2 * row + 1] = by_block;
+  }
+#pragma unroll
+  for (int i = 0; i < VECS; ++i) {
+    const int at = (threadIdx.x + i * T) * 8;
+    float w[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+    if (in[i]) weights8(p.w, at, w);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) w[j] *= s[i][j] * by;
+    if (!p.quant) {
+      if (in[i]) store8<__nv_bfloat16>(p.out, base + at, w);
+    } else {   // 16 neighbouring lanes hold a block of 128
+      const float amax = max16(amax8(w));
+      const float scale = __fdiv_rn(amax, 448.0f);
+      const uint2 q = e4m3x8(w, block_scale(amax, scale));
+      if (in[i]) {
+        *reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.out) + base + at) = q;
+        if ((threadIdx.x & 15) == 0) p.scales[row * p.Hb + at / 128] = scale;
+      }
+    }
+  }
+}
+
+template <typename S, typename B, int VECS>
+__global__ void __launch_bounds__(512) norm_grad_kernel(NormParams p) {
+  begin_overlapped();
+  __shared__ float room[4][32];
+  const int T = blockDim.x;
+  const bool has_block = p.block != nullptr;
+  float dw[VECS][8], dp[VECS][8], dg[VECS][8];
+#pragma unroll
+  for (int i = 0; i < VECS; ++i)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) dw[i][j] = dp[i][j] = dg[i][j] = 0.0f;
+  for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
+    const int64_t base = row * p.H;
+    Raw8<__nv_bfloat16> rd[VECS];
+    Raw8<S> rt[VECS], rs[VECS];
+    Raw8<B> rb[VECS];
+    const float by = p.stats[2 * row], by_block = p.stats[2 * row + 1];
+#pragma unroll
+    for (int i = 0; i < VECS; ++i) {
+      const int piece = threadIdx.x + i * T;
+      zero8(rd[i]);
+      zero8(rt[i]);
+      zero8(rs[i]);
+      zero8(rb[i]);
+      if (piece < p.pieces) {
+        load8<__nv_bfloat16>(p.dout, base + piece * 8, rd[i]);
+        load8<S>(p.stream, base + piece * 8, rs[i]);
+        if (p.d_stream) load8<S>(p.d_stream, base + piece * 8, rt[i]);
+        if (has_block) load8<B>(p.block, base + piece * 8, rb[i]);
+      }
+    }
+    float sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < VECS; ++i) {
+      const int at = (threadIdx.x + i * T) * 8;
+      if (at >= p.H) continue;
+      float d[8], s[8], w[8];
+      floats8(rd[i], d);
+      floats8(rs[i], s);
+      weights8(p.w, at, w);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float n = s[j] * by;
+        dw[i][j] = fmaf(d[j], n, dw[i][j]);
+        sum = fmaf(d[j] * w[j], n, sum);
+      }
+    }
+    const float mean = cta_sum(sum, room[0]) * p.inv;
+    float times = p.alpha;
+    if (has_block && p.gate == EP_GATE_TOKEN) times *= p.gates[row];
+    float dot_gate = 0.0f, dot_post = 0.0f;
+    float t[VECS][8];
+#pragma unroll
+    for (int i = 0; i < VECS; ++i) {
+      const int at = (threadIdx.x + i * T) * 8;
+      if (at >= p.H) continue;
+      float d[8], s[8], w[8];
+      floats8(rd[i], d);
+      floats8(rs[i], s);
+      floats8(rt[i], t[i]);
+      weights8(p.w, at, w);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) t[i][j] = fmaf(by, d[j] * w[j] - s[j] * by * mean, t[i][j]);
+      store8<S>(p.d_residual, base + at, t[i]);
+      if (!has_block) continue;
+      float y[8], wp[8], g[8];
+      floats8(rb[i], y);
+      if (p.post) weights8(p.w_post, at, wp);
+      if (p.gate == EP_GATE_FEATURE) weights8(p.gates, at, g);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float n = y[j] * by_block;                 // y without post_norm
+        const float u = p.post ? n * wp[j] : n;
+        if (p.gate == EP_GATE_TOKEN) dot_gate = fmaf(u, t[i][j], dot_gate);
+        if (p.gate == EP_GATE_FEATURE) dg[i][j] = fmaf(u, t[i][j], dg[i][j]);
+        const float du = times * (p.gate == EP_GATE_FEATURE ? g[j] : 1.0f) * t[i][j];
+        if (p.post) {
+          dp[i][j] = fmaf(du, n, dp[i][j]);
+          dot_post = fmaf(du * wp[j], n, dot_post);
+        }
+        t[i][j] = p.post ? du * wp[j] : du;
+      }
+      if (!p.post) store8<B>(p.d_block, base + at, t[i]);
+    }
+    if (has_block && p.gate == EP_GATE_TOKEN) {
+      const float v = cta_sum(dot_gate, room[1]);
+      if (threadIdx.x == 0) p.d_gate[row] = p.alpha * v;
+    }
+    if (has_block && p.post) {
+      const float mean_post = cta_sum(dot_post, room[2]) * p.inv;
+#pragma unroll
+      for (int i = 0; i < VECS; ++i) {
+        const int at = (threadIdx.x + i * T) * 8;
+        if (at >= p.H) continue;
+        float y[8];
+        floats8(rb[i], y);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) t[i][j] = by_block * (t[i][j] - y[j] * by_block * mean_post);
+        store8<B>(p.d_block, base + at, t[i]);
+      }
+    }
+    __syncthreads();   // `room` is written anew
+  }
+  float* part = p.part + (int64_t)blockIdx.x * p.n_sums * p.H;
+#pragma unroll
+  for (int i = 0; i < VECS; ++i) {
+    const int at = (threadIdx.x + i * T) * 8;
+    if (at >= p.H) continue;
+    float* to = part + at;
+    store8<float>(to, 0, dw[i]);
+    to += p.H;
+    if (has_block && p.post) {
+      store8<float>(to, 0, dp[i]);
+      to += p.H;
+    }
+    if (has_block && p.gate == EP_GATE_FEATURE) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) dg[i][j] *= p.alpha;
+      store8<float>(to, 0, dg[i]);
+    }
+  }
+}
+
+// The sums over the CTAs, in their order: a CTA takes 32 columns, warp w the CTAs
+// w, w + 8, ... of them.
+__global__ void __launch_bounds__(256) norm_sums_kernel(NormParams p) {
+  begin_overlapped();
+  __shared__ float room[8][32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t column = (int64_t)blockIdx.x * 32 + lane, width = (int64_t)p.n_sums * p.H;
+  float v = 0.0f;
+  if (column < width)
+    for (int c = warp; c < p.ctas; c += 8) v += p.part[c * width + column];
+  room[warp][lane] = v;
+  __syncthreads();
+  if (warp == 0 && column < width) {
+    v = 0.0f;
+#pragma unroll
+    for (int w = 0; w < 8; ++w) v += room[w][lane];
+    const int which = (int)(column / p.H);
+    p.sums[which][column - (int64_t)which * p.H] = v;
+  }
+}
+
+template <typename S, typename B>
+cudaError_t launch_norm(const NormParams& p, int sms, cudaStream_t st) {
+  // few rows: as many threads as pieces; else four pieces a thread
+  const int vecs = p.pieces > 1024 || (p.rows > 2 * sms && p.pieces > 128) ? 4 : 1;
+  const int threads = ((p.pieces + vecs - 1) / vecs + 31) / 32 * 32;
+  const auto kernel = vecs == 1 ? norm_kernel<S, B, 1> : norm_kernel<S, B, 4>;
+  return launch_overlapped(kernel, dim3((unsigned)p.rows), threads, 0, st, p);
+}
+
+template <typename S, typename B>
+cudaError_t launch_norm_grad(NormParams& p, cudaStream_t st) {
+  const int vecs = p.pieces <= 128 ? 1 : p.pieces <= 1024 ? 2 : 4;
+  const int threads = ((p.pieces + vecs - 1) / vecs + 31) / 32 * 32;
+  const auto kernel = vecs == 1   ? norm_grad_kernel<S, B, 1>
+                      : vecs == 2 ? norm_grad_kernel<S, B, 2>
+                                  : norm_grad_kernel<S, B, 4>;
+  if (p.ctas > 0) {   // without rows the sums are zero
+    const cudaError_t e = launch_overlapped(kernel, dim3((unsigned)p.ctas), threads, 0, st, p);
+    if (e != cudaSuccess) return e;
+  }
+  const int64_t width = (int64_t)p.n_sums * p.H;
+  return launch_overlapped(norm_sums_kernel, dim3((unsigned)((width + 31) / 32)), 256, 0, st, p);
+}
+
+}  // namespace
+}  // namespace ep
+
+struct ep_norm_handle {
+  ep_norm_config cfg;
+  float* part;
+  int sm_count;
+};
+
+namespace {
+
+using namespace ep;
+
+constexpr int kMaxGradCtas = 320;
+
+ep_status nfail(ep_status st, const char* msg) { return record_error(st, msg); }
+ep_status ncuda(cudaError_t e) { return record_error(EP_ERR_CUDA, cudaGetErrorString(e)); }
+
+int norm_sums(const ep_norm_config& c) { return 1 + (c.post_norm ? 1 : 0) + (c.gate == EP_GATE_FEATURE); }
+
+ep_status plan_norm(const ep_norm_config* c, size_t* bytes) {
+  if (!c) return nfail(EP_ERR_INVALID_ARG, "norm config is NULL");
+  if (c->max_rows < 1 || c->max_rows > INT32_MAX)
+    return nfail(EP_ERR_INVALID_ARG, "max_rows must be >= 1 and fit int32");
+  if (c->hidden_dim < 8 || c->hidden_dim % 8 != 0 || c->hidden_dim > EP_MAX_NORM_HIDDEN)
+    return nfail(EP_ERR_INVALID_ARG, "hidden_dim must be a positive multiple of 8 up to EP_MAX_NORM_HIDDEN");
+  for (const int t : {c->stream_dtype, c->block_dtype})
+    if (t != EP_DTYPE_BF16 && t != EP_DTYPE_FP32)
+      return nfail(EP_ERR_INVALID_ARG, "stream_dtype and block_dtype must be BF16 or FP32");
+  if (c->quant_type != EP_QUANT_NONE && c->quant_type != EP_QUANT_FP8_E4M3_BLOCK128)
+    return nfail(EP_ERR_INVALID_ARG, "quant_type must be NONE or FP8_E4M3_BLOCK128");
+  if (c->gate < EP_GATE_NONE || c->gate > EP_GATE_FEATURE)
+    return nfail(EP_ERR_INVALID_ARG, "unknown gate");
+  if (!(c->eps > 0.0f) || !(c->eps < 1e30f))
+    return nfail(EP_ERR_INVALID_ARG, "eps must be positive and finite");
+  if (!(c->residual_scale > -1e30f && c->residual_scale < 1e30f))
+    return nfail(EP_ERR_INVALID_ARG, "residual_scale must be finite");
+  *bytes = 256 + (c->backward ? (size_t)kMaxGradCtas * norm_sums(*c) * c->hidden_dim * 4 : 0);
+  return EP_OK;
+}
+
+bool off(const void* p, size_t to) { return (uintptr_t)p % to != 0; }
+
+// What both passes check; fills what they share.
+ep_status fill_norm(ep_norm_handle* h, const void* block, const float* gate, const float* w_post,
+                    const float* w, int64_t num_rows, NormParams* p) {
+  if (!h) return nfail(EP_ERR_INVALID_ARG, "norm handle is NULL");
+  const ep_norm_config& c = h->cfg;
+  if (num_rows < 0 || num_rows > c.max_rows)
+    return nfail(EP_ERR_INVALID_ARG, "num_rows outside [0, max_rows]");
+  if (!w || off(w, 16) || off(block, 16) || off(w_post, 16))
+    return nfail(EP_ERR_INVALID_ARG, "weight must be given; tensors are 16-byte aligned");
+  if ((w_post != nullptr) != (block && c.post_norm))
+    return nfail(EP_ERR_INVALID_ARG, "weight_post goes with post_norm and a block");
+  if ((gate != nullptr) != (block && c.gate != EP_GATE_NONE))
+    return nfail(EP_ERR_INVALID_ARG, "gate goes with the config's gate and a block");
+  if (off(gate, c.gate == EP_GATE_FEATURE ? 16 : 4))
+    return nfail(EP_ERR_INVALID_ARG, "gate is misaligned");
+  memset(p, 0, sizeof(*p));
+  p->rows = num_rows;
+  p->H = c.hidden_dim;
+  p->Hb = (c.hidden_dim + 127) / 128;
+  p->pieces = c.hidden_dim / 8;
+  p->eps = c.eps;
+  p->alpha = c.residual_scale;
+  p->inv = 1.0f / (float)c.hidden_dim;
+  p->post = c.post_norm != 0;
+  p->gate = c.gate;
+  p->quant = c.quant_type != EP_QUANT_NONE;
+  p->block = block;
+  p->gates = gate;
+  p->w_post = w_post;
+  p->w = w;
+  return EP_OK;
+}
+
+ep_status norm_ready(ep_norm_handle* h) {
+  if (h->sm_count) return EP_OK;
+  int dev = 0, n = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return ncuda(e);
+  h->sm_count = n;
+  return EP_OK;
+}
+
+}  // namespace
+
+extern "C" size_t ep_norm_workspace_size(const ep_norm_config* cfg) {
+  size_t bytes = 0;
+  return plan_norm(cfg, &bytes) == EP_OK ? bytes : 0;
+}
+
+extern "C" ep_status ep_norm_create(const ep_norm_config* cfg, void* d_workspace,
+                                    size_t workspace_bytes, ep_norm_handle** out_handle) {
+  if (!out_handle) return nfail(EP_ERR_INVALID_ARG, "out_handle is NULL");
+  *out_handle = nullptr;
+  size_t bytes = 0;
+  const ep_status s = plan_norm(cfg, &bytes);
+  if (s != EP_OK) return s;
+  if (!d_workspace || off(d_workspace, 256))
+    return nfail(EP_ERR_WORKSPACE, "norm workspace is NULL or not 256-byte aligned");
+  if (workspace_bytes < bytes) return nfail(EP_ERR_WORKSPACE, "norm workspace too small");
+  ep_norm_handle* p = new (std::nothrow) ep_norm_handle{};
+  if (!p) return nfail(EP_ERR_INVALID_ARG, "out of host memory");
+  p->cfg = *cfg;
+  p->part = reinterpret_cast<float*>(static_cast<uint8_t*>(d_workspace) + 256);
+  *out_handle = p;
+  return EP_OK;
+}
+
+extern "C" void ep_norm_destroy(ep_norm_handle* h) { delete h; }
+
+extern "C" ep_status ep_norm_forward(ep_norm_handle* h, const void* residual, const void* block,
+                                     const float* gate, const float* weight_post,
+                                     const float* weight, int64_t num_rows, void* stream_out,
+                                     void* out, float* scales, float* stats, void* stream) {
+  NormParams p;
+  ep_status s = fill_norm(h, block, gate, weight_post, weight, num_rows, &p);
+  if (s != EP_OK) return s;
+  if (!residual || !out || off(residual, 16) || off(out, 16) || off(stream_out, 16) ||
+      off(scales, 4) || off(stats, 4))
+    return nfail(EP_ERR_INVALID_ARG, "residual and out must be given; an argument may be misaligned");
+  if ((stream_out != nullptr) != (block != nullptr))
+    return nfail(EP_ERR_INVALID_ARG, "stream_out goes with a block");
+  if ((scales != nullptr) != (p.quant != 0))
+    return nfail(EP_ERR_INVALID_ARG, "scales go with quantisation");
+  p.residual = residual;
+  p.stream = stream_out;
+  p.out = out;
+  p.scales = scales;
+  p.stats = stats;
+  if ((s = norm_ready(h)) != EP_OK || num_rows == 0) return s;
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const bool s32 = h->cfg.stream_dtype == EP_DTYPE_FP32, b32 = h->cfg.block_dtype == EP_DTYPE_FP32;
+  using bf16 = __nv_bfloat16;
+  const cudaError_t e = s32 ? b32 ? launch_norm<float, float>(p, h->sm_count, st)
+                                  : launch_norm<float, bf16>(p, h->sm_count, st)
+                        : b32 ? launch_norm<bf16, float>(p, h->sm_count, st)
+                              : launch_norm<bf16, bf16>(p, h->sm_count, st);
+  return e == cudaSuccess ? EP_OK : ncuda(e);
+}
+
+extern "C" ep_status ep_norm_backward(ep_norm_handle* h, const void* dout, const void* d_stream,
+                                      const void* stream_in, const void* block, const float* gate,
+                                      const float* weight_post, const float* weight,
+                                      const float* stats, int64_t num_rows, void* d_residual,
+                                      void* d_block, float* d_weight, float* d_weight_post,
+                                      float* d_gate, void* stream) {
+  NormParams p;
+  ep_status s = fill_norm(h, block, gate, weight_post, weight, num_rows, &p);
+  if (s != EP_OK) return s;
+  if (!h->cfg.backward)
+    return nfail(EP_ERR_STATE, "the config did not reserve the backward pass's scratch");
+  if (!dout || !stream_in || !stats || !d_residual || !d_weight || off(dout, 16) ||
+      off(d_stream, 16) || off(stream_in, 16) || off(stats, 4) || off(d_residual, 16) ||
+      off(d_block, 16) || off(d_weight, 4) || off(d_weight_post, 4) || off(d_gate, 4))
+    return nfail(EP_ERR_INVALID_ARG,
+                 "dout, stream_in, stats, d_residual and d_weight must be given; an argument may be misaligned");
+  if ((d_block != nullptr) != (block != nullptr) ||
+      (d_weight_post != nullptr) != (weight_post != nullptr) ||
+      (d_gate != nullptr) != (gate != nullptr))
+    return nfail(EP_ERR_INVALID_ARG, "d_block, d_weight_post and d_gate go with block, weight_post and gate");
+  if ((s = norm_ready(h)) != EP_OK) return s;
+  p.dout = dout;
+  p.d_stream = d_stream;
+  p.stream = const_cast<void*>(stream_in);
+  p.stats = const_cast<float*>(stats);
+  p.d_residual = d_residual;
+  p.d_block = d_block;
+  p.d_gate = p.gate == EP_GATE_TOKEN ? d_gate : nullptr;
+  p.part = h->part;
+  p.sums[p.n_sums++] = d_weight;
+  if (weight_post) p.sums[p.n_sums++] = d_weight_post;
+  if (gate && p.gate == EP_GATE_FEATURE) p.sums[p.n_sums++] = d_gate;
+  int64_t ctas = 2 * (int64_t)h->sm_count;
+  if (ctas > kMaxGradCtas) ctas = kMaxGradCtas;
+  if (ctas > num_rows) ctas = num_rows;
+  p.ctas = (int)ctas;
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const bool s32 = h->cfg.stream_dtype == EP_DTYPE_FP32, b32 = h->cfg.block_dtype == EP_DTYPE_FP32;
+  using bf16 = __nv_bfloat16;
+  const cudaError_t e = s32 ? b32 ? launch_norm_grad<float, float>(p, st) : launch_norm_grad<float, bf16>(p, st)
+                        : b32 ? launch_norm_grad<bf16, float>(p, st) : launch_norm_grad<bf16, bf16>(p, st);
+  return e == cudaSuccess ? EP_OK : ncuda(e);
+}
+
+extern "C" ep_status ep_norm_sync(ep_norm_handle* h, void* stream) {
+  if (!h) return nfail(EP_ERR_INVALID_ARG, "norm handle is NULL");
+  const cudaError_t e = cudaStreamSynchronize(static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? EP_OK : ncuda(e);
+}

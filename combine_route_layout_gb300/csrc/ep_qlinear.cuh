@@ -1,0 +1,45 @@
+// Declarations shared by the products of block-quantised operands (ep_qlinear*.cu).
+//
+//   z = sum over blocks b of sx[r][b] sw[n / 128][b] (qx[r][k in b] . qw[n][k in b]) + bias
+//   y = act(z) + residual
+//   dx = sum over blocks b of sd[r][b] sw[b][k / 128] (qd[r][n in b] . qw[n in b][k])
+//
+// with qd, sd: dz = dy act'(z) quantised by 128 of a row, each half (gate, up) apart.
+#pragma once
+
+#include "ep_linear.cuh"
+
+namespace ep {
+
+struct QLinearParams {
+  LinearSegs s;
+  int K, N, Nw;                // as LinearParams
+  int act;
+  int Kb, Nb;                  // blocks of K and of N
+  int Sw;                      // rows of a group's weight scales: Nb, or 2 Nb
+  const uint8_t* x;            // [pool][K]
+  const float* xs;             // [pool][Kb]
+  const uint8_t* w;            // [G][Nw][K]
+  const float* ws;             // [G][Sw][Kb]
+  const float* bias;           // [G][Nw] or NULL
+  const void* residual;        // [pool][N] of y's type, or NULL
+  void* y;                     // [pool][N]
+  int y_f32;
+  __nv_bfloat16* z;            // [pool][Nw] or NULL
+  float* partial;              // sums of parts
+  unsigned int* tickets;
+  // backward
+  const uint8_t* dz8;          // [pool][Sw * 128], zeros behind each half's N columns
+  const float* dzs;            // [pool][Sw]
+  __nv_bfloat16* dx;           // [pool][K]
+};
+
+// The products (ep_qlinear_mma.cu), over `sms` multiprocessors.
+cudaError_t launch_qlinear_forward(const QLinearParams& p, int sms, cudaStream_t st);
+cudaError_t launch_qlinear_input_grad(const QLinearParams& p, int sms, cudaStream_t st);
+
+// Rows of codes with scales to bf16 (ep_quant.cu).
+cudaError_t launch_dequantize(const LinearSegs& s, const uint8_t* codes, const float* scales, int K,
+                              __nv_bfloat16* out, int sms, cudaStream_t st);
+
+}  // namespace ep

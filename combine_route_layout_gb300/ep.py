@@ -36,6 +36,7 @@ EP_DTYPE_FP4_E2M1X2 = 3
 EP_QUANT_NONE = 0
 EP_QUANT_FP8_E4M3_BLOCK128 = 1
 EP_QUANT_FP4_E2M1_BLOCK32 = 2
+EP_QUANT_BLOCK = 128
 EP_COMBINE_AUTO = 0
 EP_COMBINE_VECTOR = 1
 EP_COMBINE_BULK = 2
@@ -49,6 +50,9 @@ EP_ACT_RELU = 1
 EP_ACT_SILU = 2
 EP_ACT_GELU = 3
 EP_ACT_SWIGLU = 4
+EP_GATE_NONE = 0
+EP_GATE_TOKEN = 1
+EP_GATE_FEATURE = 2
 EP_PHASE_DISPATCH = 0
 EP_PHASE_COMBINE = 1
 IMPL_OF = {"auto": 0, "vector": 1, "bulk": 2}        # same codes for both phases
@@ -90,6 +94,17 @@ class ep_linear_config(ctypes.Structure):
     _fields_ = [("max_rows", ctypes.c_int64)] + [(n, ctypes.c_int32) for n in (
         "num_groups", "groups_per_base", "in_features", "out_features", "out_dtype",
         "weight_grad_dtype", "activation", "backward")]
+
+
+class ep_quant_config(ctypes.Structure):
+    _fields_ = [("max_rows", ctypes.c_int64)] + [(n, ctypes.c_int32) for n in (
+        "num_groups", "groups_per_base", "features", "block_rows", "dtype")]
+
+
+class ep_norm_config(ctypes.Structure):
+    _fields_ = [("max_rows", ctypes.c_int64)] + [(n, ctypes.c_int32) for n in (
+        "hidden_dim", "stream_dtype", "block_dtype", "quant_type", "post_norm", "gate",
+        "backward")] + [("eps", ctypes.c_float), ("residual_scale", ctypes.c_float)]
 
 
 class ep_dispatch_out(ctypes.Structure):
@@ -159,6 +174,24 @@ def _load() -> ctypes.CDLL:
         "ep_linear_forward": (S, [P] * 8 + [L] + [P] * 3),
         "ep_linear_backward": (S, [P] * 8 + [L] + [P] * 4),
         "ep_linear_sync": (S, [P, P]),
+        "ep_quant_workspace_size": (Z, [P]),
+        "ep_quant_create": (S, [P, P, Z, P]),
+        "ep_quant_destroy": (None, [P]),
+        "ep_quantize": (S, [P] * 5 + [L] + [P] * 3),
+        "ep_dequantize": (S, [P] * 6 + [L] + [P] * 2),
+        "ep_quant_sync": (S, [P, P]),
+        "ep_qlinear_workspace_size": (Z, [P]),
+        "ep_qlinear_create": (S, [P, P, Z, P]),
+        "ep_qlinear_destroy": (None, [P]),
+        "ep_qlinear_forward": (S, [P] * 10 + [L] + [P] * 3),
+        "ep_qlinear_backward": (S, [P] * 10 + [L] + [P] * 4),
+        "ep_qlinear_sync": (S, [P, P]),
+        "ep_norm_workspace_size": (Z, [P]),
+        "ep_norm_create": (S, [P, P, Z, P]),
+        "ep_norm_destroy": (None, [P]),
+        "ep_norm_forward": (S, [P] * 6 + [L] + [P] * 5),
+        "ep_norm_backward": (S, [P] * 9 + [L] + [P] * 6),
+        "ep_norm_sync": (S, [P, P]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -420,6 +453,105 @@ def ep_linear_backward(handle, dy, x, weight, preact, row_begin, row_count, row_
 
 def ep_linear_sync(handle, stream) -> None:
     _check(_lib.ep_linear_sync(handle, stream))
+
+
+# ------------------------ block quantisation, products of such operands, norms
+
+def _sized(size, cfg) -> int:
+    return int(size(ctypes.byref(cfg)))
+
+
+def _created(create, cfg, d_workspace: int, workspace_bytes: int) -> int:
+    h = ctypes.c_void_p()
+    _check(create(ctypes.byref(cfg), d_workspace, workspace_bytes, ctypes.byref(h)))
+    return h.value
+
+
+def ep_quant_workspace_size(cfg: ep_quant_config) -> int:
+    return _sized(_lib.ep_quant_workspace_size, cfg)
+
+
+def ep_quant_create(cfg: ep_quant_config, d_workspace: int, workspace_bytes: int) -> int:
+    return _created(_lib.ep_quant_create, cfg, d_workspace, workspace_bytes)
+
+
+def ep_quant_destroy(handle: int) -> None:
+    _lib.ep_quant_destroy(handle)
+
+
+def ep_quantize(handle, x, row_begin, row_count, row_base, num_rows: int, codes, scales,
+                stream) -> None:
+    _check(_lib.ep_quantize(handle, x, row_begin, row_count, row_base, int(num_rows), codes,
+                            scales, stream))
+
+
+def ep_dequantize(handle, codes, scales, row_begin, row_count, row_base, num_rows: int, x,
+                  stream) -> None:
+    _check(_lib.ep_dequantize(handle, codes, scales, row_begin, row_count, row_base,
+                              int(num_rows), x, stream))
+
+
+def ep_quant_sync(handle, stream) -> None:
+    _check(_lib.ep_quant_sync(handle, stream))
+
+
+def ep_qlinear_workspace_size(cfg: ep_linear_config) -> int:
+    return _sized(_lib.ep_qlinear_workspace_size, cfg)
+
+
+def ep_qlinear_create(cfg: ep_linear_config, d_workspace: int, workspace_bytes: int) -> int:
+    return _created(_lib.ep_qlinear_create, cfg, d_workspace, workspace_bytes)
+
+
+def ep_qlinear_destroy(handle: int) -> None:
+    _lib.ep_qlinear_destroy(handle)
+
+
+def ep_qlinear_forward(handle, x, x_scale, weight, w_scale, bias, residual, row_begin, row_count,
+                       row_base, num_rows: int, y, preact, stream) -> None:
+    _check(_lib.ep_qlinear_forward(handle, x, x_scale, weight, w_scale, bias, residual, row_begin,
+                                   row_count, row_base, int(num_rows), y, preact, stream))
+
+
+def ep_qlinear_backward(handle, dy, x, x_scale, weight, w_scale, preact, row_begin, row_count,
+                        row_base, num_rows: int, dx, dweight, dbias, stream) -> None:
+    _check(_lib.ep_qlinear_backward(handle, dy, x, x_scale, weight, w_scale, preact, row_begin,
+                                    row_count, row_base, int(num_rows), dx, dweight, dbias,
+                                    stream))
+
+
+def ep_qlinear_sync(handle, stream) -> None:
+    _check(_lib.ep_qlinear_sync(handle, stream))
+
+
+def ep_norm_workspace_size(cfg: ep_norm_config) -> int:
+    return _sized(_lib.ep_norm_workspace_size, cfg)
+
+
+def ep_norm_create(cfg: ep_norm_config, d_workspace: int, workspace_bytes: int) -> int:
+    return _created(_lib.ep_norm_create, cfg, d_workspace, workspace_bytes)
+
+
+def ep_norm_destroy(handle: int) -> None:
+    _lib.ep_norm_destroy(handle)
+
+
+def ep_norm_forward(handle, residual, block, gate, weight_post, weight, num_rows: int, stream_out,
+                    out, scales, stats, stream) -> None:
+    _check(_lib.ep_norm_forward(handle, residual, block, gate, weight_post, weight, int(num_rows),
+                                stream_out, out, scales, stats, stream))
+
+
+def ep_norm_backward(handle, dout, d_stream, stream_in, block, gate, weight_post, weight, stats,
+                     num_rows: int, d_residual, d_block, d_weight, d_weight_post, d_gate,
+                     stream) -> None:
+    _check(_lib.ep_norm_backward(handle, dout, d_stream, stream_in, block, gate, weight_post,
+                                 weight, stats, int(num_rows), d_residual, d_block, d_weight,
+                                 d_weight_post, d_gate, stream))
+
+
+def ep_norm_sync(handle, stream) -> None:
+    _check(_lib.ep_norm_sync(handle, stream))
 
 
 # ------------------------------------------------------- operator class

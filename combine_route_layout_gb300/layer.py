@@ -1,7 +1,9 @@
 """What a mixture-of-experts layer has around dispatch and combine, on torch
-tensors: the router with its balance loss (EpRouterOp) and the experts'
-products (EpLinearOp). Argument checks and marshalling only; the work is the
-CUDA kernels behind ep_router_* and ep_linear_* of include/ep.h, on torch's
+tensors: the router with its balance loss (EpRouterOp), the experts' products
+(EpLinearOp) and their form for the E4M3 rows of FP8 dispatch (EpQuantLinearOp),
+the quantiser (EpQuantOp), and the norms around the layer (EpNormOp). Argument
+checks and marshalling only; the work is the CUDA kernels behind ep_router_*,
+ep_linear_*, ep_qlinear_*, ep_quant* and ep_norm_* of include/ep.h, on torch's
 current stream. An operator owns its workspace; calls on one operator are
 ordered by the caller (same stream, or events), with the operator's device the
 current one. Results carry no autograd graph, as dispatch's and combine's do not:
@@ -20,6 +22,9 @@ _SCORE_OF = {"softmax": ep.EP_SCORE_SOFTMAX, "sigmoid": ep.EP_SCORE_SIGMOID}
 _ACT_OF = {"none": ep.EP_ACT_NONE, "relu": ep.EP_ACT_RELU, "silu": ep.EP_ACT_SILU,
            "gelu": ep.EP_ACT_GELU, "swiglu": ep.EP_ACT_SWIGLU}
 _FLOAT_OF = {torch.float32: ep.EP_DTYPE_FP32, torch.bfloat16: ep.EP_DTYPE_BF16}
+_GATE_OF = {"none": ep.EP_GATE_NONE, "token": ep.EP_GATE_TOKEN, "feature": ep.EP_GATE_FEATURE}
+_QUANT_OF = {"none": ep.EP_QUANT_NONE, "fp8_e4m3_block128": ep.EP_QUANT_FP8_E4M3_BLOCK128}
+_E4M3 = torch.float8_e4m3fn
 
 
 def _refuse(msg: str):
@@ -82,6 +87,41 @@ class _Op:
     def _form(self, shape, dtype):
         """A tensor that results are made like: a third of the cost of making them from a shape."""
         return torch.empty(shape, dtype=dtype, device=self.device)
+
+
+class _PoolOp(_Op):
+    """An operator over the segments of a pool of max_rows rows, as its config has them."""
+
+    def _per_group(self, t, what: str, n: int) -> int:
+        if t.dtype is not torch.int32 or t.numel() != n or t.device != self.device or \
+                not t.is_contiguous():
+            _refuse(f"{what} must hold {n} contiguous int32 on {self.device}")
+        return t.data_ptr()
+
+    def _segments(self, x, row_begin, row_count, row_base, num_rows):
+        """Check x and the segments: (rows of pool tensors, row_begin, row_count, row_base,
+        num_rows) as the C calls take them."""
+        cfg = self.config
+        if x is None or x.dim() != 2 or x.shape[0] > cfg.max_rows:
+            _refuse("x must be [rows, features] with at most max_rows rows")
+        rows = x.shape[0]
+        if row_begin is None or row_count is None:
+            if row_begin is not row_count or cfg.num_groups != 1 or row_base is not None:
+                _refuse("give row_begin and row_count together; only one group may go without")
+            n = rows if num_rows is None else int(num_rows)
+            if not 0 <= n <= rows:
+                _refuse("num_rows outside [0, rows of x]")
+            return rows, None, None, None, n
+        if rows != cfg.max_rows:
+            _refuse("with segments, x must hold all max_rows rows of the pool")
+        base = None
+        if row_base is not None:
+            per = cfg.groups_per_base
+            if per < 1:
+                _refuse("row_base needs groups_per_base")
+            base = self._per_group(row_base, "row_base", -(-cfg.num_groups // per))
+        return (rows, self._per_group(row_begin, "row_begin", cfg.num_groups),
+                self._per_group(row_count, "row_count", cfg.num_groups), base, 0)
 
 
 _new = torch.empty_like
@@ -242,7 +282,7 @@ class EpLinearConfig:
         return c
 
 
-class EpLinearOp(_Op):
+class EpLinearOp(_PoolOp):
     """The product over one workspace (backward: reserve its scratch too).
 
     Segments: row_begin and row_count [G] int32, plus row_base (one entry per
@@ -262,37 +302,6 @@ class EpLinearOp(_Op):
         self._weight = torch.Size((G, Nw, config.in_features))
         self._bias = torch.Size((G, Nw))
         self._act_none = config.activation == "none"
-
-    def _per_group(self, t, what: str, n: int) -> int:
-        if t.dtype is not torch.int32 or t.numel() != n or t.device != self.device or \
-                not t.is_contiguous():
-            _refuse(f"{what} must hold {n} contiguous int32 on {self.device}")
-        return t.data_ptr()
-
-    def _segments(self, x, row_begin, row_count, row_base, num_rows):
-        """Check x and the segments: (rows of pool tensors, row_begin, row_count, row_base,
-        num_rows) as the C calls take them."""
-        cfg = self.config
-        if x is None or x.dim() != 2 or x.shape[0] > cfg.max_rows:
-            _refuse("x must be [rows, in_features] with at most max_rows rows")
-        rows = x.shape[0]
-        if row_begin is None or row_count is None:
-            if row_begin is not row_count or cfg.num_groups != 1 or row_base is not None:
-                _refuse("give row_begin and row_count together; only one group may go without")
-            n = rows if num_rows is None else int(num_rows)
-            if not 0 <= n <= rows:
-                _refuse("num_rows outside [0, rows of x]")
-            return rows, None, None, None, n
-        if rows != cfg.max_rows:
-            _refuse("with segments, x must hold all max_rows rows of the pool")
-        base = None
-        if row_base is not None:
-            per = cfg.groups_per_base
-            if per < 1:
-                _refuse("row_base needs groups_per_base")
-            base = self._per_group(row_base, "row_base", -(-cfg.num_groups // per))
-        return (rows, self._per_group(row_begin, "row_begin", cfg.num_groups),
-                self._per_group(row_count, "row_count", cfg.num_groups), base, 0)
 
     def forward(self, x, weight, bias=None, residual=None, row_begin=None, row_count=None,
                 row_base=None, num_rows=None, out=None, preact=None):
@@ -360,3 +369,335 @@ class EpLinearOp(_Op):
 
     def sync(self):
         ep.ep_linear_sync(self._handle, self._stream())
+
+
+# -------------------------------------------------------- block quantisation
+
+def _blocks(n: int) -> int:
+    return -(-n // ep.EP_QUANT_BLOCK)
+
+
+@dataclass
+class EpQuantConfig:
+    """ep_quant_config: E4M3 codes with an f32 scale for each 128 elements of a row
+    (block_rows 1) or for each 128 x 128 of num_groups matrices of max_rows rows
+    (block_rows 128)."""
+    num_groups: int
+    features: int
+    max_rows: int
+    block_rows: int = 1
+    dtype: torch.dtype = torch.bfloat16   # of what is quantised: bfloat16 or float32
+    groups_per_base: int = 0    # with row_base: segments that share an entry of it
+
+    def to_c(self) -> ep.ep_quant_config:
+        c = ep.ep_quant_config()
+        for n in ("num_groups", "groups_per_base", "features", "block_rows", "max_rows"):
+            setattr(c, n, int(getattr(self, n)))
+        c.dtype = _code(_FLOAT_OF, self.dtype, "dtype")
+        return c
+
+
+class EpQuantOp(_PoolOp):
+    """The quantiser over one workspace. Rows: [rows, K] tensors and EpLinearOp's
+    segments. Matrices: [G, max_rows, K] tensors, scales [G, ceil(max_rows / 128),
+    ceil(K / 128)]; SWIGLU's [G, 2 N, K] weights are 2 G matrices of N rows."""
+
+    def __init__(self, config: EpQuantConfig, device: torch.device | str = "cuda"):
+        self.config = config
+        c = config.to_c()
+        super().__init__(ep.ep_quant_workspace_size(c), lambda ws, n: ep.ep_quant_create(c, ws, n),
+                         ep.ep_quant_destroy, device)
+        self._kb = _blocks(config.features)
+        G, M = config.num_groups, config.max_rows
+        self._matrices = torch.Size((G, M, config.features))
+        self._matrix_scales = torch.Size((G, _blocks(M), self._kb))
+
+    def _places(self, t, row_begin, row_count, row_base, num_rows):
+        """(shape of t, shape of its scales, segments as the C calls take them)."""
+        cfg = self.config
+        if cfg.block_rows == 1:
+            rows, *at = self._segments(t, row_begin, row_count, row_base, num_rows)
+            return (rows, cfg.features), (rows, self._kb), at
+        if any(v is not None for v in (row_begin, row_count, row_base, num_rows)):
+            _refuse("blocks of 128 rows take whole matrices: no segments")
+        return self._matrices, self._matrix_scales, (None, None, None, cfg.max_rows)
+
+    def quantize(self, x, row_begin=None, row_count=None, row_base=None, num_rows=None, codes=None,
+                 scales=None):
+        """(codes, scales) of x (in `codes` and `scales` if given). Rows outside the
+        segments stay as they are."""
+        shape, scale_shape, at = self._places(x, row_begin, row_count, row_base, num_rows)
+        xp = self._need(x, "x", shape, self.config.dtype)
+        if codes is None:
+            codes = torch.empty(shape, dtype=_E4M3, device=self.device)
+            cp = codes.data_ptr()
+        else:
+            cp = self._need(codes, "codes", shape, _E4M3)
+        if scales is None:
+            scales = torch.empty(scale_shape, dtype=torch.float32, device=self.device)
+            sp = scales.data_ptr()
+        else:
+            sp = self._need(scales, "scales", scale_shape, torch.float32)
+        if shape[0]:
+            _check(_lib.ep_quantize(self._handle, xp, *at, cp, sp, self._stream()))
+        return codes, scales
+
+    def dequantize(self, codes, scales, row_begin=None, row_count=None, row_base=None, num_rows=None,
+                   out=None):
+        """What codes and scales stand for, rounded to the config's dtype."""
+        shape, scale_shape, at = self._places(codes, row_begin, row_count, row_base, num_rows)
+        cp = self._need(codes, "codes", shape, _E4M3)
+        sp = self._need(scales, "scales", scale_shape, torch.float32)
+        if out is None:
+            out = torch.empty(shape, dtype=self.config.dtype, device=self.device)
+            xp = out.data_ptr()
+        else:
+            xp = self._need(out, "out", shape, self.config.dtype)
+        if shape[0]:
+            _check(_lib.ep_dequantize(self._handle, cp, sp, *at, xp, self._stream()))
+        return out
+
+    def sync(self):
+        ep.ep_quant_sync(self._handle, self._stream())
+
+
+# ----------------------------------- experts' products of quantised operands
+
+class EpQuantLinearOp(_PoolOp):
+    """EpLinearOp's product of E4M3 operands: x [rows, K] with x_scale [rows, ceil(K / 128)],
+    as FP8 dispatch or EpQuantOp gives them, and weight [G, Nw, K] with weight_scale
+    [G, Nw / N ceil(N / 128), ceil(K / 128)]. The rest is EpLinearOp's, except that
+    in_features is a multiple of 16."""
+
+    def __init__(self, config: EpLinearConfig, device: torch.device | str = "cuda",
+                 backward: bool = False):
+        self.config = config
+        c = config.to_c(backward)
+        super().__init__(ep.ep_qlinear_workspace_size(c),
+                         lambda ws, n: ep.ep_qlinear_create(c, ws, n), ep.ep_qlinear_destroy,
+                         device)
+        G, N, Nw = config.num_groups, config.out_features, config.weight_rows
+        self._kb = _blocks(config.in_features)
+        self._weight = torch.Size((G, Nw, config.in_features))
+        self._weight_scale = torch.Size((G, Nw // N * _blocks(N), self._kb))
+        self._bias = torch.Size((G, Nw))
+        self._act_none = config.activation == "none"
+
+    def _operands(self, rows, x, x_scale, weight, weight_scale):
+        return (self._need(x, "x", (rows, self.config.in_features), _E4M3),
+                self._need(x_scale, "x_scale", (rows, self._kb), torch.float32),
+                self._need(weight, "weight", self._weight, _E4M3),
+                self._need(weight_scale, "weight_scale", self._weight_scale, torch.float32))
+
+    def forward(self, x, x_scale, weight, weight_scale, bias=None, residual=None, row_begin=None,
+                row_count=None, row_base=None, num_rows=None, out=None, preact=None):
+        """y [rows, N] (in `out` if given). `preact`: a [rows, Nw] bf16 tensor that
+        receives z for the backward pass. Rows outside the segments stay as they are."""
+        cfg = self.config
+        rows, *at = self._segments(x, row_begin, row_count, row_base, num_rows)
+        operands = self._operands(rows, x, x_scale, weight, weight_scale)
+        b = r = z = None
+        if bias is not None:
+            b = self._need(bias, "bias", self._bias, torch.float32)
+        if residual is not None:
+            r = self._need(residual, "residual", (rows, cfg.out_features), cfg.out_dtype)
+        if preact is not None:
+            z = self._need(preact, "preact", (rows, cfg.weight_rows), torch.bfloat16)
+        if out is None:
+            out = torch.empty((rows, cfg.out_features), dtype=cfg.out_dtype, device=self.device)
+            y = out.data_ptr()
+        else:
+            y = self._need(out, "out", (rows, cfg.out_features), cfg.out_dtype)
+        if rows:
+            _check(_lib.ep_qlinear_forward(self._handle, *operands, b, r, *at, y, z,
+                                           self._stream()))
+        return out
+
+    def backward(self, dy, x, x_scale, weight, weight_scale, preact=None, row_begin=None,
+                 row_count=None, row_base=None, num_rows=None, want_dx=True, want_dweight=True,
+                 want_dbias=False, dx=None, dweight=None):
+        """(dx, dweight, dbias), None where not wanted: dx bf16, dweight [G, Nw, K] of
+        weight_grad_dtype. dx's rows outside the segments stay as they are (`dx`,
+        `dweight`: tensors to write to)."""
+        cfg, bf16 = self.config, torch.bfloat16
+        rows, *at = self._segments(x, row_begin, row_count, row_base, num_rows)
+        operands = self._operands(rows, x, x_scale, weight, weight_scale)
+        dyp = self._need(dy, "dy", (rows, cfg.out_features), cfg.out_dtype)
+        z = dxp = dwp = dbp = dbias = None
+        if preact is not None or not self._act_none:
+            z = self._need(preact, "preact", (rows, cfg.weight_rows), bf16)
+        if not want_dx:
+            dx = None
+        elif dx is None:
+            dx = torch.empty((rows, cfg.in_features), dtype=bf16, device=self.device)
+            dxp = dx.data_ptr()
+        else:
+            dxp = self._need(dx, "dx", (rows, cfg.in_features), bf16)
+        if not want_dweight:
+            dweight = None
+        elif dweight is None:
+            dweight = torch.empty(self._weight, dtype=cfg.weight_grad_dtype, device=self.device)
+            dwp = dweight.data_ptr()
+        else:
+            dwp = self._need(dweight, "dweight", self._weight, cfg.weight_grad_dtype)
+        if want_dbias:
+            dbias = torch.empty(self._bias, dtype=torch.float32, device=self.device)
+            dbp = dbias.data_ptr()
+        if rows == 0:
+            for t in (dweight, dbias):
+                if t is not None:
+                    t.zero_()
+        elif dxp or dwp or dbp:
+            _check(_lib.ep_qlinear_backward(self._handle, dyp, *operands, z, *at, dxp, dwp, dbp,
+                                            self._stream()))
+        return dx, dweight, dbias
+
+    def sync(self):
+        ep.ep_qlinear_sync(self._handle, self._stream())
+
+
+# ---------------------------------------------------------------------- norms
+
+@dataclass
+class EpNormConfig:
+    """ep_norm_config: stream = residual + residual_scale gate u, with u the block's
+    output or (post_norm) its norm, and out = norm(stream)."""
+    hidden_dim: int
+    max_rows: int
+    eps: float = 1e-6
+    post_norm: bool = False
+    gate: str = "none"          # "none" | "token" | "feature"
+    residual_scale: float = 1.0
+    stream_dtype: torch.dtype = torch.bfloat16   # of residual and stream: bfloat16 or float32
+    block_dtype: torch.dtype = torch.bfloat16    # of the block's output: combine's type
+    quant_type: str = "none"    # "none": out is bf16 | "fp8_e4m3_block128": codes with scales
+
+    def to_c(self, backward: bool) -> ep.ep_norm_config:
+        c = ep.ep_norm_config()
+        c.hidden_dim, c.max_rows = int(self.hidden_dim), int(self.max_rows)
+        c.eps, c.residual_scale = float(self.eps), float(self.residual_scale)
+        c.post_norm = int(bool(self.post_norm))
+        c.gate = _code(_GATE_OF, self.gate, "gate")
+        c.quant_type = _code(_QUANT_OF, self.quant_type, "quant_type")
+        c.stream_dtype = _code(_FLOAT_OF, self.stream_dtype, "stream_dtype")
+        c.block_dtype = _code(_FLOAT_OF, self.block_dtype, "block_dtype")
+        c.backward = int(bool(backward))
+        return c
+
+
+class EpNormOp(_Op):
+    """The norms around a block over one workspace (backward: reserve its scratch too).
+    Tensors are [rows, hidden_dim] with at most max_rows rows; weight, weight_post and a
+    gate of features are f32 [hidden_dim], a gate of tokens is f32 [rows]."""
+
+    def __init__(self, config: EpNormConfig, device: torch.device | str = "cuda",
+                 backward: bool = False):
+        self.config = config
+        c = config.to_c(backward)
+        super().__init__(ep.ep_norm_workspace_size(c), lambda ws, n: ep.ep_norm_create(c, ws, n),
+                         ep.ep_norm_destroy, device)
+        self._features = torch.Size((config.hidden_dim,))
+        self._hb = _blocks(config.hidden_dim)
+        self._quant = config.quant_type != "none"
+
+    def _shared(self, t, weight, block, weight_post, gate):
+        """(shape, block, gate, weight_post, weight) of a call, the last four as addresses."""
+        cfg = self.config
+        if t is None or t.dim() != 2 or t.shape[0] > cfg.max_rows:
+            _refuse("tensors must be [rows, hidden_dim] with at most max_rows rows")
+        shape = t.shape
+        f32, b, p, g = torch.float32, None, None, None
+        if block is not None:
+            b = self._need(block, "block", shape, cfg.block_dtype)
+            if cfg.post_norm:
+                p = self._need(weight_post, "weight_post", self._features, f32)
+            if cfg.gate != "none":
+                g = self._need(gate, "gate", self._features if cfg.gate == "feature" else shape[:1], f32)
+        if (weight_post is not None) != (p is not None) or (gate is not None) != (g is not None):
+            _refuse("weight_post and gate go with a block and the config's post_norm and gate")
+        return shape, b, g, p, self._need(weight, "weight", self._features, f32)
+
+    def forward(self, residual, weight, block=None, weight_post=None, gate=None, stream=None,
+                out=None, scales=None, stats=None):
+        """(stream, out, scales, stats): stream is `residual` itself without a block; out is
+        bf16, scales None, or E4M3 codes with f32 scales [rows, ceil(hidden_dim / 128)];
+        stats [rows, 2] f32 are for the backward pass. `stream` (which may be
+        `residual`), `out`, `scales`, `stats`: tensors to write to."""
+        cfg, dev, f32 = self.config, self.device, torch.float32
+        shape, b, g, p, w = self._shared(residual, weight, block, weight_post, gate)
+        rows = shape[0]
+        r = self._need(residual, "residual", (rows, cfg.hidden_dim), cfg.stream_dtype)
+        s = sc = None
+        if b is None:
+            if stream is not None and stream is not residual:
+                _refuse("without a block, stream is the residual")
+            stream = residual
+        elif stream is None:
+            stream = _new(residual)
+            s = stream.data_ptr()
+        else:
+            s = self._need(stream, "stream", shape, cfg.stream_dtype)
+        dt = _E4M3 if self._quant else torch.bfloat16
+        if out is None:
+            out = torch.empty(shape, dtype=dt, device=dev)
+            o = out.data_ptr()
+        else:
+            o = self._need(out, "out", shape, dt)
+        if not self._quant:
+            if scales is not None:
+                _refuse("scales go with quantisation")
+        elif scales is None:
+            scales = torch.empty((rows, self._hb), dtype=f32, device=dev)
+            sc = scales.data_ptr()
+        else:
+            sc = self._need(scales, "scales", (rows, self._hb), f32)
+        if stats is None:
+            stats = torch.empty((rows, 2), dtype=f32, device=dev)
+            st = stats.data_ptr()
+        else:
+            st = self._need(stats, "stats", (rows, 2), f32)
+        if rows:
+            _check(_lib.ep_norm_forward(self._handle, r, b, g, p, w, rows, s, o, sc, st,
+                                        self._stream()))
+        return stream, out, scales, stats
+
+    def backward(self, d_out, stream, weight, stats, d_stream=None, block=None, weight_post=None,
+                 gate=None, d_residual=None):
+        """(d_residual, d_block, d_weight, d_weight_post, d_gate), None for what the forward
+        pass did not take, from d_out [rows, hidden_dim] bf16, the stream's own gradient and
+        what forward took and gave. `d_residual` (a tensor to write to) may be `d_stream`."""
+        cfg, dev, f32 = self.config, self.device, torch.float32
+        shape, b, g, p, w = self._shared(stream, weight, block, weight_post, gate)
+        rows = shape[0]
+        s = self._need(stream, "stream", (rows, cfg.hidden_dim), cfg.stream_dtype)
+        do = self._need(d_out, "d_out", shape, torch.bfloat16)
+        ds = None if d_stream is None else self._need(d_stream, "d_stream", shape, cfg.stream_dtype)
+        st = self._need(stats, "stats", (rows, 2), f32)
+        if d_residual is None:
+            d_residual = _new(stream)
+            dr = d_residual.data_ptr()
+        else:
+            dr = self._need(d_residual, "d_residual", shape, cfg.stream_dtype)
+        d_weight = _new(weight)
+        d_block = d_post = d_gate = None
+        db = dp = dg = None
+        if b is not None:
+            d_block = _new(block)
+            db = d_block.data_ptr()
+            if p is not None:
+                d_post = _new(weight_post)
+                dp = d_post.data_ptr()
+            if g is not None:
+                d_gate = _new(gate)
+                dg = d_gate.data_ptr()
+        if rows:
+            _check(_lib.ep_norm_backward(self._handle, do, ds, s, b, g, p, w, st, rows, dr, db,
+                                         d_weight.data_ptr(), dp, dg, self._stream()))
+        else:
+            for t in (d_weight, d_post, d_gate):
+                if t is not None:
+                    t.zero_()
+        return d_residual, d_block, d_weight, d_post, d_gate
+
+    def sync(self):
+        ep.ep_norm_sync(self._handle, self._stream())

@@ -695,6 +695,218 @@ ep_status ep_linear_backward(ep_linear_handle* h, const void* dy, const void* x,
 /* Wait for `stream`, then report and clear device-detected errors. */
 ep_status ep_linear_sync(ep_linear_handle* h, void* stream);
 
+/*
+ * ---------------------------------------------------------------------------
+ * Block quantisation of what the products take: E4M3 codes with one f32 scale
+ * for each 128 elements of a row (block_rows 1, what dispatch's FP8 quantisation
+ * gives) or for each 128 x 128 of a matrix (block_rows 128, weights):
+ *     scale = amax / 448     code = E4M3(x / scale)     value = code scale
+ * in f32, every step rounded to nearest even, codes clamped to +-448. Blocks end
+ * with the row or the matrix. A block whose scale is 0 has codes of 0. A NaN
+ * keeps a NaN code and leaves its block's scale alone; a block that holds an
+ * infinity has the scale inf, and no value but NaN.
+ *
+ * Calls of one handle share its workspace: the caller orders them, and makes
+ * them with the workspace's device current.
+ * ---------------------------------------------------------------------------
+ */
+typedef struct ep_quant_config {
+    int64_t max_rows;          /* rows of the pool, or (block_rows 128) of each matrix */
+    int32_t num_groups;        /* segments, 1..EP_MAX_EXPERTS (1: may be dense); block_rows
+                                  128: matrices, 1..2 EP_MAX_EXPERTS */
+    int32_t groups_per_base;   /* row_base[g / groups_per_base] is added to row_begin[g] */
+    int32_t features;          /* K, elements of a row, a multiple of 16 */
+    int32_t block_rows;        /* 1 or 128 */
+    int32_t dtype;             /* ep_dtype of x: BF16, FP32 */
+} ep_quant_config;
+
+typedef struct ep_quant_handle ep_quant_handle;
+
+/* Workspace bytes (0 if the config is invalid). Host only. */
+size_t ep_quant_workspace_size(const ep_quant_config* cfg);
+
+/* A handle over `d_workspace` (device, 256-byte aligned, the caller's). Makes no CUDA call. */
+ep_status ep_quant_create(const ep_quant_config* cfg, void* d_workspace, size_t workspace_bytes,
+                          ep_quant_handle** out_handle);
+
+/* Free the host-side handle. NULL is a no-op. */
+void ep_quant_destroy(ep_quant_handle* h);
+
+/*
+ *   x       device [max_rows][K], or [G][max_rows][K] (block_rows 128), 16-byte aligned
+ *   row_begin, row_count, row_base, num_rows  as for ep_linear_forward; with
+ *           block_rows 128 the first three are NULL and num_rows is max_rows
+ *   codes   device out, shaped as x, 16-byte aligned
+ *   scales  device f32 out [max_rows][ceil(K/128)], or (block_rows 128)
+ *           [G][ceil(max_rows/128)][ceil(K/128)]
+ * Rows outside the segments are neither read nor written.
+ */
+ep_status ep_quantize(ep_quant_handle* h, const void* x, const int32_t* row_begin,
+                      const int32_t* row_count, const int32_t* row_base, int64_t num_rows,
+                      void* codes, float* scales, void* stream);
+
+/* x of codes and scales: code scale, rounded once to dtype. */
+ep_status ep_dequantize(ep_quant_handle* h, const void* codes, const float* scales,
+                        const int32_t* row_begin, const int32_t* row_count,
+                        const int32_t* row_base, int64_t num_rows, void* x, void* stream);
+
+/* Wait for `stream`, then report and clear device-detected errors. */
+ep_status ep_quant_sync(ep_quant_handle* h, void* stream);
+
+/*
+ * ---------------------------------------------------------------------------
+ * The experts' products of block-quantised operands: ep_linear's, with x in E4M3
+ * and an f32 scale for each 128 of a row (FP8 dispatch's rows and scales as they
+ * are, or ep_quantize's), W in E4M3 and a scale for each 128 x 128:
+ *     z[r,n] = sum over blocks b of sx[r,b] sw[n/128,b] (sum over k in b of qx[r,k] qw[n,k]) + bias[n]
+ *     y = act(z) + residual
+ * SWIGLU's gate and up rows are two matrices of N rows, each with its own scale
+ * blocks. Backward:
+ *     dz = dy act'(z)    dx = dz' W    dW = dz^T x    dbias = sum of dz
+ * where dz' is dz (of f32) quantised by 128 of a row, gate and up apart, as
+ * ep_quantize does it: the products' operands are 8 bits wide. dW takes dz and
+ * x's values rounded to bf16, which is what its tensor-core operands hold.
+ *
+ * The tensor core adds up a block's 128 terms; scales and the sum over blocks are
+ * f32. in_features is a multiple of 16. A handle is made from an ep_linear_config.
+ * ---------------------------------------------------------------------------
+ */
+typedef struct ep_qlinear_handle ep_qlinear_handle;
+
+/* Workspace bytes (0 if the config is invalid). Host only. */
+size_t ep_qlinear_workspace_size(const ep_linear_config* cfg);
+
+/* A handle over `d_workspace` (device, 256-byte aligned, the caller's). Makes no CUDA call. */
+ep_status ep_qlinear_create(const ep_linear_config* cfg, void* d_workspace,
+                            size_t workspace_bytes, ep_qlinear_handle** out_handle);
+
+/* Free the host-side handle. NULL is a no-op. */
+void ep_qlinear_destroy(ep_qlinear_handle* h);
+
+/*
+ *   x         device [max_rows][K] E4M3, 16-byte aligned
+ *   x_scale   device [max_rows][ceil(K/128)] f32
+ *   weight    device [G][Nw][K] E4M3, 16-byte aligned; Nw = N, or 2 N (SWIGLU)
+ *   w_scale   device [G][Nw/N ceil(N/128)][ceil(K/128)] f32
+ * and the rest as for ep_linear_forward.
+ */
+ep_status ep_qlinear_forward(ep_qlinear_handle* h, const void* x, const float* x_scale,
+                             const void* weight, const float* w_scale, const float* bias,
+                             const void* residual, const int32_t* row_begin,
+                             const int32_t* row_count, const int32_t* row_base, int64_t num_rows,
+                             void* y, void* preact, void* stream);
+
+/* As ep_linear_backward; segments must not overlap. */
+ep_status ep_qlinear_backward(ep_qlinear_handle* h, const void* dy, const void* x,
+                              const float* x_scale, const void* weight, const float* w_scale,
+                              const void* preact, const int32_t* row_begin,
+                              const int32_t* row_count, const int32_t* row_base,
+                              int64_t num_rows, void* dx, void* dweight, float* dbias,
+                              void* stream);
+
+/* Wait for `stream`, then report and clear device-detected errors. */
+ep_status ep_qlinear_sync(ep_qlinear_handle* h, void* stream);
+
+/*
+ * ---------------------------------------------------------------------------
+ * The norms around a block (the experts' layer between router and combine, or any
+ * other): its end and the next block's beginning in one pass,
+ *     u      = post_norm ? block rms(block) w_post : block
+ *     stream = residual + residual_scale gate u
+ *     out    = stream rms(stream) w
+ * with rms(v) = 1 / sqrt(mean of v^2 + eps) of a row. Without a block, stream is the
+ * residual: the norm before a first block. The gate is absent, one f32 for each
+ * row (a token's), or one for each feature. out is bf16, or E4M3 codes with f32
+ * scales by 128 of a row (what FP8 dispatch's pass-through and ep_qlinear take).
+ * All arithmetic is f32; out is made from the unrounded stream. A mean of squares
+ * beyond f32's range (values above 1e19) gives rms 0.
+ *
+ * Backward, from the stored stream and the forward's stats, with
+ * n = stream rms, v = dout w:
+ *     t       = d_stream + rms (v - n mean(v n))      the gradient of residual
+ *     du      = residual_scale gate t
+ *     d_block = post_norm ? rms' (du w_post - n' mean(du w_post n')) : du
+ *     d_weight = sum of dout n    d_weight_post = sum of du n'    over rows
+ *     d_gate  = residual_scale sum of u t    over features, or over rows
+ * Sums over rows run in a fixed order: results do not change from run to run.
+ *
+ * Calls of one handle share its workspace: the caller orders them, and makes
+ * them with the workspace's device current.
+ * ---------------------------------------------------------------------------
+ */
+#define EP_MAX_NORM_HIDDEN 16384
+
+typedef enum {
+    EP_GATE_NONE = 0,
+    EP_GATE_TOKEN = 1,
+    EP_GATE_FEATURE = 2
+} ep_gate;
+
+typedef struct ep_norm_config {
+    int64_t max_rows;
+    int32_t hidden_dim;        /* H, a multiple of 8, at most EP_MAX_NORM_HIDDEN */
+    int32_t stream_dtype;      /* ep_dtype of residual and stream: BF16, FP32 */
+    int32_t block_dtype;       /* ep_dtype of block: BF16, FP32 */
+    int32_t quant_type;        /* ep_quant of out: NONE (bf16) or FP8_E4M3_BLOCK128 */
+    int32_t post_norm;         /* 1: the block's output is normed too */
+    int32_t gate;              /* ep_gate */
+    int32_t backward;          /* 1: reserve the backward pass's scratch */
+    float eps;                 /* positive */
+    float residual_scale;
+} ep_norm_config;
+
+typedef struct ep_norm_handle ep_norm_handle;
+
+/* Workspace bytes (0 if the config is invalid). Host only. */
+size_t ep_norm_workspace_size(const ep_norm_config* cfg);
+
+/* A handle over `d_workspace` (device, 256-byte aligned, the caller's). Makes no CUDA call. */
+ep_status ep_norm_create(const ep_norm_config* cfg, void* d_workspace, size_t workspace_bytes,
+                         ep_norm_handle** out_handle);
+
+/* Free the host-side handle. NULL is a no-op. */
+void ep_norm_destroy(ep_norm_handle* h);
+
+/*
+ *   residual     device [num_rows][H] stream_dtype
+ *   block        device [num_rows][H] block_dtype or NULL
+ *   gate         device f32 [num_rows] or [H], as the config says; NULL without one,
+ *                or without a block
+ *   weight_post  device [H] f32; NULL without post_norm, or without a block
+ *   weight       device [H] f32
+ *   stream_out   device [num_rows][H] stream_dtype (may be residual itself); NULL
+ *                without a block
+ *   out          device [num_rows][H] bf16 or E4M3
+ *   scales       device [num_rows][ceil(H/128)] f32 with quantisation, else NULL
+ *   stats        device [num_rows][2] f32 out or NULL: rms of stream and of block (1
+ *                without post_norm or block), for the backward pass
+ * Tensors are 16-byte aligned; scales, stats and a token's gate 4-byte.
+ */
+ep_status ep_norm_forward(ep_norm_handle* h, const void* residual, const void* block,
+                          const float* gate, const float* weight_post, const float* weight,
+                          int64_t num_rows, void* stream_out, void* out, float* scales,
+                          float* stats, void* stream);
+
+/*
+ *   dout        device [num_rows][H] bf16
+ *   d_stream    device [num_rows][H] stream_dtype or NULL (zero)
+ *   stream_in   device [num_rows][H] stream_dtype: forward's stream_out, or the
+ *               residual where there was no block
+ *   block, gate, weight_post, weight, stats  as forward took and gave them
+ *   d_residual  device [num_rows][H] stream_dtype out (may be d_stream itself)
+ *   d_block     device [num_rows][H] block_dtype out; NULL without a block
+ *   d_weight, d_weight_post  device [H] f32 out; the second as weight_post
+ *   d_gate      device f32 out, shaped as gate; NULL as it is
+ */
+ep_status ep_norm_backward(ep_norm_handle* h, const void* dout, const void* d_stream,
+                           const void* stream_in, const void* block, const float* gate,
+                           const float* weight_post, const float* weight, const float* stats,
+                           int64_t num_rows, void* d_residual, void* d_block, float* d_weight,
+                           float* d_weight_post, float* d_gate, void* stream);
+
+/* Wait for `stream`, then report errors of its launches. */
+ep_status ep_norm_sync(ep_norm_handle* h, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
