@@ -230,10 +230,57 @@ __device__ __forceinline__ void mma_step(uint32_t d, uint32_t a, uint32_t a_high
       : "memory");
 }
 
+// Both operands E4M3, f32 accumulator, M = 256 over the CTA pair.
+__device__ __forceinline__ uint32_t mma8_form(uint32_t n, bool a_mn_major) {
+  return (1u << 4) | ((uint32_t)a_mn_major << 15) | ((n >> 3) << 17) | ((256u >> 4) << 24);
+}
+
+// Four products of 32 terms each, a stage: d = a b. K-major operands' steps are 32
+// bytes of a row on, MN-major ones' 32 rows; see mma_stage.
+template <uint32_t A_STEP, uint32_t B_STEP>
+__device__ __forceinline__ void mma8_stage(uint32_t d, uint32_t a, uint32_t a_high, uint32_t b,
+                                           uint32_t b_high, uint32_t form) {
+  asm volatile(
+      "{\n .reg .pred p, t;\n .reg .b32 x, y;\n .reg .b64 a, b;\n"
+      " setp.ne.u32 p, 0, 0;\n setp.eq.u32 t, 0, 0;\n"
+      " mov.b64 a, {%1, %2};\n mov.b64 b, {%3, %4};\n"
+      " tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], a, b, %5, p;\n"
+      " add.u32 x, %1, %6;\n add.u32 y, %3, %7;\n mov.b64 a, {x, %2};\n mov.b64 b, {y, %4};\n"
+      " tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], a, b, %5, t;\n"
+      " add.u32 x, %1, %8;\n add.u32 y, %3, %9;\n mov.b64 a, {x, %2};\n mov.b64 b, {y, %4};\n"
+      " tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], a, b, %5, t;\n"
+      " add.u32 x, %1, %10;\n add.u32 y, %3, %11;\n mov.b64 a, {x, %2};\n mov.b64 b, {y, %4};\n"
+      " tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], a, b, %5, t;\n}" ::"r"(d),
+      "r"(a), "r"(a_high), "r"(b), "r"(b_high), "r"(form), "n"(A_STEP), "n"(B_STEP), "n"(2 * A_STEP),
+      "n"(2 * B_STEP), "n"(3 * A_STEP), "n"(3 * B_STEP)
+      : "memory");
+}
+
+// Arrive on this barrier of both CTAs of the pair once the MMAs issued so far are
+// complete.
+__device__ __forceinline__ void mma_commit_both(uint32_t bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+          bar),
+      "h"((uint16_t)3)
+      : "memory");
+}
+
 // Arrive on this CTA's barrier once the MMAs issued so far are complete.
 __device__ __forceinline__ void mma_commit(uint32_t bar) {
   asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
                : "memory");
+}
+
+// A warpgroup gives registers of its own back, or takes more from what the block was
+// launched with: all its warps call these.
+template <int N>
+__device__ __forceinline__ void registers_less() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void registers_more() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
 }
 
 // 32 columns of this warp's 32 lanes: register c holds column c of the lane.
