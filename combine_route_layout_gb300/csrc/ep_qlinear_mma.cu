@@ -374,44 +374,48 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive(&bar->scale_empty[slot]);
       }
       if (!ok) break;
-      // this lane's column in the pair's place (a pair has one unit where there are parts)
-      float* sums = q.p.partial + ((int64_t)pair * plan.cap * 256 + cta * 128 + quad * 32 + lane);
-      // first the values of this part: the tile's result, or sums for the part that
-      // finishes last, which then adds all of them in their order
-      const float* parts_of = nullptr;
-      while (true) {
-        const bool result = whole || parts_of;
+      // the values of this part: the tile's result, or sums for the part that finishes
+      // last, which then adds all of them in their order
+      if (whole) {
 #pragma unroll
         for (int h = 0; h < kBlocks; ++h) {
           const int c0 = turn * 32 + h * 64;
           if (c0 >= w.rows) continue;
           float r[32];
-          if (parts_of) {
-            add_parts(parts_of + c0 * 256, plan.cap * 256, w.parts, w.rows - c0, r);
-          } else {
 #pragma unroll
-            for (int c = 0; c < 16; ++c) floats_of(sum[h][c], r[2 * c], r[2 * c + 1]);
-          }
-          if (result) {
-            epilogue<MODE, ACT, T>(q, w, (int)cta, lane, quad, c0, r, b);
-          } else {
-#pragma unroll
-            for (int c = 0; c < 32; ++c) put(sums + (c0 + c) * 256, r[c], c0 + c < w.rows);
-          }
+          for (int c = 0; c < 16; ++c) floats_of(sum[h][c], r[2 * c], r[2 * c + 1]);
+          epilogue<MODE, ACT, T>(q, w, (int)cta, lane, quad, c0, r, b);
         }
-        if (result) break;
-        ok = epilogue_meet(bar, lane, meeting);
-        if (!ok) break;
-        if (threadIdx.x == 128) {
-          unsigned int* ticket = q.p.tickets + quotient(u, plan.splits) * 2 + cta;
-          const bool last = ticket_take(ticket) == (unsigned)w.parts - 1;
-          if (last) *ticket = 0u;
-          bar->last = last;
-        }
-        ok = epilogue_meet(bar, lane, meeting);
-        if (!ok || !bar->last) break;
-        parts_of = sums - (int64_t)w.part * plan.cap * 256;
+        continue;
       }
+      // this lane's column in the pair's place (a pair has one unit where there are parts)
+      float* sums = q.p.partial + ((int64_t)pair * plan.cap * 256 + cta * 128 + quad * 32 + lane);
+#pragma unroll
+      for (int h = 0; h < kMinCap / 64; ++h) {          // parts are of tiles of few rows
+        const int c0 = turn * 32 + h * 64;
+#pragma unroll
+        for (int c = 0; c < 16; ++c) {
+          float lo, hi;
+          floats_of(sum[h][c], lo, hi);
+          put(sums + (c0 + 2 * c) * 256, lo, c0 + 2 * c < w.rows);
+          put(sums + (c0 + 2 * c + 1) * 256, hi, c0 + 2 * c + 1 < w.rows);
+        }
+      }
+      ok = epilogue_meet(bar, lane, meeting);
+      if (!ok) break;
+      if (threadIdx.x == 128) {
+        unsigned int* ticket = q.p.tickets + quotient(u, plan.splits) * 2 + cta;
+        const bool last = ticket_take(ticket) == (unsigned)w.parts - 1;
+        if (last) *ticket = 0u;
+        bar->last = last;
+      }
+      ok = epilogue_meet(bar, lane, meeting);
+      if (!ok) break;
+      const int c0 = turn * 32;
+      if (!bar->last || c0 >= w.rows) continue;
+      float r[32];
+      add_parts(sums - (int64_t)w.part * plan.cap * 256 + c0 * 256, plan.cap * 256, w.parts, w.rows - c0, r);
+      epilogue<MODE, ACT, T>(q, w, (int)cta, lane, quad, c0, r, b);
     }
     if (!ok && lane == 0) atomicOr(timeout, kErrLinearTimeout);
   }
