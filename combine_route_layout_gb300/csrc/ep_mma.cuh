@@ -302,4 +302,33 @@ __device__ __forceinline__ void tmem_load32(uint32_t addr, float (&v)[32]) {
   for (int c = 0; c < 32; ++c) v[c] = __uint_as_float(r[c]);
 }
 
+// 32 columns of this warp's 32 lanes, two neighbouring columns of a lane to a
+// register pair: thread t holds lanes t / 4 + 8 j and columns 8 i + 2 (t % 4), + 1 in
+// v[j][2 i], v[j][2 i + 1].
+__device__ __forceinline__ void tmem_load_pairs(uint32_t addr, float (&v)[4][8]) {
+  uint32_t r[32];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%32];\n"
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+      "{%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%33];\n"
+      "tcgen05.wait::ld.sync.aligned;"  // one statement: no register is read before the wait
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]),
+        "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]),
+        "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(addr), "r"(addr + (16u << 16))
+      : "memory");
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      v[0][2 * i + e] = __uint_as_float(r[4 * i + e]);
+      v[1][2 * i + e] = __uint_as_float(r[4 * i + 2 + e]);
+      v[2][2 * i + e] = __uint_as_float(r[16 + 4 * i + e]);
+      v[3][2 * i + e] = __uint_as_float(r[16 + 4 * i + 2 + e]);
+    }
+}
+
 }  // namespace ep

@@ -30,11 +30,12 @@ namespace {
 constexpr int kDepth = 128;                      // terms per stage: 128 bytes
 constexpr int kStageA = 128 * kDepth;            // bytes of a CTA's 128 features
 constexpr int kStageB = 128 * kDepth;            // bytes of a CTA's half of the rows
-constexpr int kRingBytes = 6 * (kStageA + kStageB);
-constexpr int kMaxStages = 9;
-constexpr int kScaleSlots = 8;                   // stages whose scales are there ahead
-constexpr int kScaleAhead = 4;                   // stages whose scales are fetched at once
-constexpr int kScaleBytes = kScaleSlots * 2 * kMaxRows * 4;
+constexpr int kRingBytes = 5 * (kStageA + kStageB);
+constexpr int kMaxStages = 8;
+constexpr int kScaleBytes = 8 * kMaxRows * 4;    // 8 stages' scales are there ahead (gated: 4)
+constexpr int kMaxScaleSlots = 8;
+constexpr int kPitch = 36;                       // words of a row of 32 that warps turn round
+constexpr int kTurnBytes = kEpilogueWarps * 32 * kPitch * 4;
 constexpr int kTmemColumns = 512;                // two accumulators
 // Registers of a thread at the start, of the first four warps and of the epilogue's.
 constexpr int kRegisters = 168, kRegistersLess = 88, kRegistersMore = 208;
@@ -63,7 +64,7 @@ struct Barriers {
   uint64_t empty[kMaxStages]; // the MMAs have read this stage
   uint64_t acc_full[2];       // a stage's sum is complete
   uint64_t acc_empty[2];      // even CTA's: both CTAs' epilogues have read it
-  uint64_t scale_full[kScaleSlots], scale_empty[kScaleSlots];
+  uint64_t scale_full[kMaxScaleSlots], scale_empty[kMaxScaleSlots];
   uint64_t tile_full[kSlots], tile_empty[kSlots];
   uint64_t joined;            // the epilogue's warps meet
   Tile tiles[kSlots];
@@ -97,6 +98,26 @@ __device__ __forceinline__ void sum_free(Barriers* bar, int n_acc, int lane) {
   if (lane == 0) mbar_signal_at(in_cta(&bar->acc_empty[n_acc & 1], 0));
 }
 
+// A block of 32 features by 32 rows, from the order in which the tensor memory gives
+// pairs of rows to a feature of a lane and all its rows, by way of shared memory: the
+// pitch keeps both ways free of conflicts.
+__device__ __forceinline__ void turn_round(float* at, int lane, const uint64_t (&sum)[4][4], float (&r)[32]) {
+  float* to = at + (lane & 3) * 2 * kPitch + (lane >> 2);
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float lo, hi;
+      floats_of(sum[j][i], lo, hi);
+      to[8 * i * kPitch + 8 * j] = lo;
+      to[(8 * i + 1) * kPitch + 8 * j] = hi;
+    }
+  __syncwarp();
+#pragma unroll
+  for (int c = 0; c < 32; ++c) r[c] = at[c * kPitch + lane];
+  __syncwarp();
+}
+
 struct Maps {
   CUtensorMap a;
   CUtensorMap b[4];        // boxes of 128, 64, 32 and 16 rows
@@ -107,10 +128,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     product8_kernel(const __grid_constant__ Maps maps, MmaParams q) {
   constexpr bool kGated = MODE == kForward && ACT == EP_ACT_SWIGLU;
   constexpr int kBlocks = kMaxRows / 64;         // of 32 columns, of a warp
+  constexpr int kScaleSlots = kGated ? 4 : 8, kScaleRow = kGated ? 2 * kMaxRows : kMaxRows;
+  constexpr int kScaleAhead = kGated ? 2 : 4;    // stages whose scales are fetched at once
   extern __shared__ uint8_t raw[];
   uint8_t* ring = reinterpret_cast<uint8_t*>(((uintptr_t)raw + 1023) & ~(uintptr_t)1023);
   float* scales = reinterpret_cast<float*>(ring + kRingBytes);   // [slot][gate, up][row]
-  Barriers* bar = reinterpret_cast<Barriers*>(ring + kRingBytes + kScaleBytes);
+  float* turned = scales + kScaleBytes / 4;                      // [epilogue warp][row][feature]
+  Barriers* bar = reinterpret_cast<Barriers*>(ring + kRingBytes + kScaleBytes + kTurnBytes);
   int* first = reinterpret_cast<int*>(bar + 1);
   int* begins = first + q.p.s.G;
   int* counts = begins + q.p.s.G;
@@ -131,7 +155,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // producer, scales, the epilogue's warps, MMA (even CTA)
     mbar_init(&bar->tile_full[threadIdx.x - 32], 1);
     mbar_init(&bar->tile_empty[threadIdx.x - 32], 2 + kEpilogueWarps + (cta == 0 ? 1 : 0));
-  } else if (threadIdx.x >= 40 && threadIdx.x < 40 + kScaleSlots) {
+  } else if (threadIdx.x >= 40 && threadIdx.x < 40 + kMaxScaleSlots) {
     mbar_init(&bar->scale_full[threadIdx.x - 40], 1);
     mbar_init(&bar->scale_empty[threadIdx.x - 40], kEpilogueWarps);
   } else if (threadIdx.x == 32 + kSlots) {
@@ -289,7 +313,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             const int slot = n_scale % kScaleSlots;
             if (n_scale >= kScaleSlots) ok = warp_wait(&bar->scale_empty[slot], (n_scale / kScaleSlots - 1) & 1);
             if (!ok) continue;
-            float* to = scales + slot * 2 * kMaxRows + lane;
+            // the order in which the epilogue's threads take a block of 32 rows
+            float* to = scales + slot * kScaleRow + (lane & 7) / 2 * 8 + lane / 8 * 2 + (lane & 1);
 #pragma unroll
             for (int j = 0; j < kMaxRows / 32; ++j) {
               if (32 * j >= w.n) continue;
@@ -323,7 +348,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // 64 columns of the tile belong to the warp pair of a quarter: 32 to this warp
     const int quad = warp & 3, turn = (warp - 4) >> 2;
     const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
-    const float* my_scales = scales + (kGated && (lane & 1) ? kMaxRows : 0) + turn * 32;
+    // a thread's sums are of the features lane / 4 + 8 j: gates, or up's
+    const float* my_scales = scales + (kGated && (lane & 4) ? kMaxRows : 0) + turn * 32 + (lane & 3) * 8;
+    float* turn_at = turned + (warp - 4) * 32 * kPitch;
     int n_acc = 0;                         // sums, and their scales
     uint32_t meeting = 0;
     bool ok = true;
@@ -346,28 +373,31 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
       }
       const int blocks = (w.n - turn * 32 + 63) / 64;   // of this warp (none below 1)
-      uint64_t sum[kBlocks][16];
+      uint64_t sum[kBlocks][4][4];                      // [..][lane / 4 + 8 j][8 i + 2 (lane % 4), + 1]
 #pragma unroll
       for (int h = 0; h < kBlocks; ++h)
 #pragma unroll
-        for (int c = 0; c < 16; ++c) sum[h][c] = 0;     // two f32 zeros
+        for (int c = 0; c < 16; ++c) sum[h][c / 4][c % 4] = 0;   // two f32 zeros
       for (int kb = w.kb0; kb < w.kb1; ++kb, ++n_acc) {
         const int slot = n_acc % kScaleSlots;
-        ok = sum_ready(bar, n_acc) && warp_wait(&bar->scale_full[slot], (n_acc / kScaleSlots) & 1);
+        ok = warp_wait(&bar->scale_full[slot], (n_acc / kScaleSlots) & 1) && sum_ready(bar, n_acc);
         if (!ok) break;
-        const float* scale = my_scales + slot * 2 * kMaxRows;
+        const float* scale = my_scales + slot * kScaleRow;
         if (blocks < 1) sum_free(bar, n_acc, lane);
 #pragma unroll
         for (int h = 0; h < kBlocks; ++h) {
           if (h >= blocks) continue;
-          float r[32];
-          tmem_load32(lanes + (n_acc & 1) * 256 + turn * 32 + h * 64, r);
+          const ulonglong2 by0 = *reinterpret_cast<const ulonglong2*>(scale + h * 64);
+          const ulonglong2 by1 = *reinterpret_cast<const ulonglong2*>(scale + h * 64 + 4);
+          float r[4][8];
+          tmem_load_pairs(lanes + (n_acc & 1) * 256 + turn * 32 + h * 64, r);
           if (h == blocks - 1) sum_free(bar, n_acc, lane);
 #pragma unroll
-          for (int c = 0; c < 32; c += 4) {
-            const ulonglong2 by = *reinterpret_cast<const ulonglong2*>(scale + h * 64 + c);
-            fma2(sum[h][c / 2], pair_of(r[c], r[c + 1]), by.x);
-            fma2(sum[h][c / 2 + 1], pair_of(r[c + 2], r[c + 3]), by.y);
+          for (int j = 0; j < 4; ++j) {
+            fma2(sum[h][j][0], pair_of(r[j][0], r[j][1]), by0.x);
+            fma2(sum[h][j][1], pair_of(r[j][2], r[j][3]), by0.y);
+            fma2(sum[h][j][2], pair_of(r[j][4], r[j][5]), by1.x);
+            fma2(sum[h][j][3], pair_of(r[j][6], r[j][7]), by1.y);
           }
         }
         __syncwarp();
@@ -382,25 +412,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           const int c0 = turn * 32 + h * 64;
           if (c0 >= w.rows) continue;
           float r[32];
-#pragma unroll
-          for (int c = 0; c < 16; ++c) floats_of(sum[h][c], r[2 * c], r[2 * c + 1]);
+          turn_round(turn_at, lane, sum[h], r);
           epilogue<MODE, ACT, T>(q, w, (int)cta, lane, quad, c0, r, b);
         }
         continue;
       }
       // this lane's column in the pair's place (a pair has one unit where there are parts)
       float* sums = q.p.partial + ((int64_t)pair * plan.cap * 256 + cta * 128 + quad * 32 + lane);
+      const int c0 = turn * 32;                         // parts are of tiles of at most 64 rows
+      float r[32];
+      turn_round(turn_at, lane, sum[0], r);
 #pragma unroll
-      for (int h = 0; h < kMinCap / 64; ++h) {          // parts are of tiles of few rows
-        const int c0 = turn * 32 + h * 64;
-#pragma unroll
-        for (int c = 0; c < 16; ++c) {
-          float lo, hi;
-          floats_of(sum[h][c], lo, hi);
-          put(sums + (c0 + 2 * c) * 256, lo, c0 + 2 * c < w.rows);
-          put(sums + (c0 + 2 * c + 1) * 256, hi, c0 + 2 * c + 1 < w.rows);
-        }
-      }
+      for (int c = 0; c < 32; ++c) put(sums + (c0 + c) * 256, r[c], c0 + c < w.rows);
       ok = epilogue_meet(bar, lane, meeting);
       if (!ok) break;
       if (threadIdx.x == 128) {
@@ -411,9 +434,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
       ok = epilogue_meet(bar, lane, meeting);
       if (!ok) break;
-      const int c0 = turn * 32;
       if (!bar->last || c0 >= w.rows) continue;
-      float r[32];
       add_parts(sums - (int64_t)w.part * plan.cap * 256 + c0 * 256, plan.cap * 256, w.parts, w.rows - c0, r);
       epilogue<MODE, ACT, T>(q, w, (int)cta, lane, quad, c0, r, b);
     }
@@ -443,7 +464,7 @@ template <int MODE, int ACT, typename T>
 cudaError_t launch_tiles(const Maps& maps, MmaParams& q, int grid, cudaStream_t st) {
   q.pairs_out = q.features % 2 == 0 && (uintptr_t)q.out % 4 == 0;
   q.pairs_z = q.features % 2 == 0 && (uintptr_t)q.p.z % 4 == 0;
-  constexpr size_t kFixed = 1024 + kRingBytes + kScaleBytes + sizeof(Barriers);
+  constexpr size_t kFixed = 1024 + kRingBytes + kScaleBytes + kTurnBytes + sizeof(Barriers);
   static_assert(kFixed + EP_MAX_EXPERTS * kGroupBytes <= 227 * 1024, "shared memory");
   static std::atomic<uint64_t> raised{0};
   const auto kernel = product8_kernel<MODE, ACT, T>;
