@@ -230,9 +230,9 @@ __device__ __forceinline__ void mma_step(uint32_t d, uint32_t a, uint32_t a_high
       : "memory");
 }
 
-// Both operands E4M3, f32 accumulator, M = 256 over the CTA pair.
-__device__ __forceinline__ uint32_t mma8_form(uint32_t n, bool a_mn_major) {
-  return (1u << 4) | ((uint32_t)a_mn_major << 15) | ((n >> 3) << 17) | ((256u >> 4) << 24);
+// One CTA's own products: both operands E4M3, f32 accumulator, M = 128.
+__device__ __forceinline__ uint32_t mma8_form(uint32_t n, bool b_mn_major) {
+  return (1u << 4) | ((uint32_t)b_mn_major << 16) | ((n >> 3) << 17) | ((128u >> 4) << 24);
 }
 
 // Four products of 32 terms each, a stage: d = a b. K-major operands' steps are 32
@@ -244,26 +244,70 @@ __device__ __forceinline__ void mma8_stage(uint32_t d, uint32_t a, uint32_t a_hi
       "{\n .reg .pred p, t;\n .reg .b32 x, y;\n .reg .b64 a, b;\n"
       " setp.ne.u32 p, 0, 0;\n setp.eq.u32 t, 0, 0;\n"
       " mov.b64 a, {%1, %2};\n mov.b64 b, {%3, %4};\n"
-      " tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], a, b, %5, p;\n"
+      " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %5, p;\n"
       " add.u32 x, %1, %6;\n add.u32 y, %3, %7;\n mov.b64 a, {x, %2};\n mov.b64 b, {y, %4};\n"
-      " tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], a, b, %5, t;\n"
+      " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %5, t;\n"
       " add.u32 x, %1, %8;\n add.u32 y, %3, %9;\n mov.b64 a, {x, %2};\n mov.b64 b, {y, %4};\n"
-      " tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], a, b, %5, t;\n"
+      " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %5, t;\n"
       " add.u32 x, %1, %10;\n add.u32 y, %3, %11;\n mov.b64 a, {x, %2};\n mov.b64 b, {y, %4};\n"
-      " tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], a, b, %5, t;\n}" ::"r"(d),
+      " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %5, t;\n}" ::"r"(d),
       "r"(a), "r"(a_high), "r"(b), "r"(b_high), "r"(form), "n"(A_STEP), "n"(B_STEP), "n"(2 * A_STEP),
       "n"(2 * B_STEP), "n"(3 * A_STEP), "n"(3 * B_STEP)
       : "memory");
 }
 
-// Arrive on this barrier of both CTAs of the pair once the MMAs issued so far are
-// complete.
-__device__ __forceinline__ void mma_commit_both(uint32_t bar) {
+// Arrive once this CTA's own products issued so far are complete: on this CTA's
+// barrier, and on this barrier of both CTAs of the cluster.
+__device__ __forceinline__ void mma8_commit(uint32_t bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
+               : "memory");
+}
+__device__ __forceinline__ void mma8_commit_both(uint32_t bar) {
   asm volatile(
-      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
           bar),
       "h"((uint16_t)3)
       : "memory");
+}
+
+__device__ __forceinline__ void tmem_alloc_own(uint32_t* dst, uint32_t columns) {
+  asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                   smem_addr(dst)),
+               "r"(columns)
+               : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+}
+
+__device__ __forceinline__ void tmem_free_own(uint32_t addr, uint32_t columns) {
+  asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(columns));
+}
+
+// Tiled TMA loads: into this CTA's shared memory, and to the same place of both CTAs of
+// the cluster, where the bytes complete on each one's own barrier at `bar`.
+__device__ __forceinline__ void tma_own_2d(uint32_t dst, const void* map, int c0, int c1, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+      "l"(map), "r"(c0), "r"(c1), "r"(bar)
+      : "memory");
+}
+
+__device__ __forceinline__ void tma_both_4d(uint32_t dst, const void* map, int c0, int c1, int c2,
+                                            int c3, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      ".multicast::cluster [%0], [%1, {%2, %3, %4, %5}], [%6], %7;" ::"r"(dst),
+      "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(bar), "h"((uint16_t)3)
+      : "memory");
+}
+
+// A hardware barrier of so many threads, number `id`: a warp that arrives goes on, one
+// that syncs waits for all of them.
+__device__ __forceinline__ void named_arrive(int id, int threads) {
+  asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+__device__ __forceinline__ void named_sync(int id, int threads) {
+  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
 
 // Arrive on this CTA's barrier once the MMAs issued so far are complete.
@@ -300,35 +344,6 @@ __device__ __forceinline__ void tmem_load32(uint32_t addr, float (&v)[32]) {
       : "memory");
 #pragma unroll
   for (int c = 0; c < 32; ++c) v[c] = __uint_as_float(r[c]);
-}
-
-// 32 columns of this warp's 32 lanes, two neighbouring columns of a lane to a
-// register pair: thread t holds lanes t / 4 + 8 j and columns 8 i + 2 (t % 4), + 1 in
-// v[j][2 i], v[j][2 i + 1].
-__device__ __forceinline__ void tmem_load_pairs(uint32_t addr, float (&v)[4][8]) {
-  uint32_t r[32];
-  asm volatile(
-      "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
-      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%32];\n"
-      "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
-      "{%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%33];\n"
-      "tcgen05.wait::ld.sync.aligned;"  // one statement: no register is read before the wait
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]),
-        "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]),
-        "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-      : "r"(addr), "r"(addr + (16u << 16))
-      : "memory");
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      v[0][2 * i + e] = __uint_as_float(r[4 * i + e]);
-      v[1][2 * i + e] = __uint_as_float(r[4 * i + 2 + e]);
-      v[2][2 * i + e] = __uint_as_float(r[16 + 4 * i + e]);
-      v[3][2 * i + e] = __uint_as_float(r[16 + 4 * i + 2 + e]);
-    }
 }
 
 }  // namespace ep

@@ -217,7 +217,7 @@ ep_status plan_qlinear(const ep_linear_config* c, ep_qlinear_handle* h) {
   h->tickets = reinterpret_cast<unsigned int*>(h->ws ? h->ws + kTicketOffset : nullptr);
   h->bytes = kHeaderBytes;
   carve(h, &h->partial,
-        kLinearMaxPairs * (!c->backward ? kPartBytes : c->max_rows > kLongTerms ? kPartBytesLong : kPartBytesGrad));
+        kLinearMaxPairs * (c->backward && c->max_rows > kLongTerms ? kPartBytesLong : kPartBytesGrad));
   h->dz = h->x = nullptr;
   h->dz8 = nullptr;
   h->dzs = h->part = nullptr;

@@ -1,22 +1,30 @@
 // The products of block-quantised operands on the tensor cores: z = x W^T and
 // dx = dz' W, with the forward's bias, activation and residual in the epilogue.
 //
-// Tiles, pairs of CTAs, the ring of stages and the parts of contractions are those of
-// the bf16 products (ep_linear_mma.cu): outputs are computed transposed, features on
-// the tensor core's M side, rows on its N side. A stage is 128 bytes of each operand
-// row, which of E4M3 are 128 terms: exactly one scale block. So the tensor core adds
-// up one stage at a time, into the two accumulators in turn, and the epilogue's warps
-// take each such sum out of TMEM and add it, times its scales, to f32 sums of the tile
-// in their registers, while the next stage's is made:
-//     sum[feature][row] += stage[feature][row] (sx[row][block] sw[feature block][block])
-// The transposed form has one weight scale for all of a CTA's features (two with
-// SwiGLU: gate on even lanes, up on odd ones); a warp of its own fetches the scales of
-// the rows, as the quantiser lays them out, and leaves the products of both in shared
-// memory, kSlots stages ahead, from where the epilogue reads four rows' at once for
-// all lanes. W is read as it is for dx too: MN-major, a box of 128 terms x 128
+// A stage is 128 bytes of each operand row, which of E4M3 are 128 terms: exactly one
+// scale block. The tensor core adds up one stage at a time, into two accumulators in
+// turn, and the epilogue's warps take each such sum out of tensor memory and add it,
+// times its scales, to f32 sums of the tile in their registers, while the next one is
+// made:
+//     sum[row][feature] += stage[row][feature] (sx[row][block] sw[feature block][block])
+// Rows are on the M side, 128 of them to a CTA, features on the N side, 256 (or 128
+// where those leave half of the pairs idle): a lane is a row, whose scale is one
+// register, and the weights' scale is one for all of a warp's columns (two with SwiGLU),
+// so that the epilogue reads no shared memory. (Features on the M side, as in the bf16
+// products, take the rows' scales from there, eight 16-byte loads a warp and stage:
+// under the tensor core's own reads each takes 100 cycles, and 8192^3 961 us.)
+//
+// A sum changes hands twice a stage (512 cycles of the tensor core), and every look at a
+// shared-memory barrier takes 200 to 250 cycles then. So each CTA makes its own
+// products, and its epilogue hands an accumulator back by a hardware barrier. A pair of
+// CTAs still shares a tile of 256 rows: each loads half of its weights for both.
+// SwiGLU: half of the tile's columns are gates, half the same features' up values; a
+// thread has both. W is read as it is for dx too: MN-major, a box of 128 terms x 128
 // features.
 //
-// Registers: 128 sums a thread of the epilogue; the other warps give theirs up.
+// Roles by warp: 0 TMA, 1 MMA, 3 works out the tiles (one thread each, but for MMA,
+// whose warp waits as one), 4-11 epilogue: TMEM lanes go by warp % 4, columns by halves.
+// 128 sums a thread: the other warps give registers up for them.
 #include <atomic>
 #include <climits>
 #include <cstring>
@@ -28,28 +36,35 @@ namespace ep {
 namespace {
 
 constexpr int kDepth = 128;                      // terms per stage: 128 bytes
-constexpr int kStageA = 128 * kDepth;            // bytes of a CTA's 128 features
-constexpr int kStageB = 128 * kDepth;            // bytes of a CTA's half of the rows
-constexpr int kRingBytes = 5 * (kStageA + kStageB);
-constexpr int kMaxStages = 8;
-constexpr int kScaleBytes = 8 * kMaxRows * 4;    // 8 stages' scales are there ahead (gated: 4)
-constexpr int kMaxScaleSlots = 8;
-constexpr int kPitch = 36;                       // words of a row of 32 that warps turn round
-constexpr int kTurnBytes = kEpilogueWarps * 32 * kPitch * 4;
+constexpr int kTileRows = 256;                   // of the pair
+constexpr int kStageA = 128 * kDepth;            // bytes of a CTA's rows
+constexpr int kRingBytes = 4 * (kStageA + 256 * kDepth);
+constexpr int kMaxStages = 6;                    // of 128 features
 constexpr int kTmemColumns = 512;                // two accumulators
+constexpr int kTurnRows = 8, kTurnPitch = 33;    // words: rows that are stored by column
+constexpr int kTurnWords = 2 * kTurnRows * kTurnPitch;   // of a warp: gates and up
+constexpr int kTurnBytes = kEpilogueWarps * kTurnWords * 4;
+constexpr int kHandover = 32 * (1 + kEpilogueWarps);     // threads of the hardware barriers
 // Registers of a thread at the start, of the first four warps and of the epilogue's.
-constexpr int kRegisters = 168, kRegistersLess = 88, kRegistersMore = 208;
+constexpr int kRegisters = 168, kRegistersLess = 72, kRegistersMore = 216;
 static_assert(kThreads * kRegisters >= 128 * kRegistersLess + kEpilogueWarps * 32 * kRegistersMore,
               "registers for the epilogue");
+constexpr int kScaleGroup = 4;                   // stages whose scales are fetched at once
+
+struct QPlan {
+  int tiles, splits;
+  int width;         // columns of a tile: 256 or 128
+  int f_tiles;       // tiles beside each other
+  int size;          // dense: rows of a tile
+};
 
 struct MmaParams {
-  static constexpr int kDepth = ep::kDepth;
   QLinearParams p;
   void* out;               // y or dx
-  int features;            // length of the output's contiguous axis (weight rows or K)
-  int f_tiles, cap, terms;
-  int pairs_out, pairs_z;  // bf16 outputs whose rows allow two features a store
-  Plan plan;               // of a dense product
+  int outs;                // length of its rows
+  int stages;              // of a contraction
+  int vec;                 // rows and tensors allow 32-byte accesses
+  QPlan plan;              // of a dense product
   // scale of (pool row, block) and of (group, feature block, block)
   const float* row_scale;
   int row_ld;
@@ -60,11 +75,9 @@ struct MmaParams {
 };
 
 struct Barriers {
-  uint64_t full[kMaxStages];  // both CTAs' operands have landed (even CTA's)
-  uint64_t empty[kMaxStages]; // the MMAs have read this stage
+  uint64_t full[kMaxStages];  // a stage's operands have landed
+  uint64_t empty[kMaxStages]; // both CTAs' products have read this stage
   uint64_t acc_full[2];       // a stage's sum is complete
-  uint64_t acc_empty[2];      // even CTA's: both CTAs' epilogues have read it
-  uint64_t scale_full[kMaxScaleSlots], scale_empty[kMaxScaleSlots];
   uint64_t tile_full[kSlots], tile_empty[kSlots];
   uint64_t joined;            // the epilogue's warps meet
   Tile tiles[kSlots];
@@ -85,94 +98,291 @@ __device__ __forceinline__ void floats_of(uint64_t v, float& lo, float& hi) {
   asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
 }
 
-// A stage's sum is there, on both CTAs by the tensor core's own arrival, and has been
-// read. What these barriers guard lies in tensor memory alone: see ep_linear_mma.cu.
-__device__ __forceinline__ bool sum_ready(Barriers* bar, int n_acc) {
-  if (!warp_wait_cluster(&bar->acc_full[n_acc & 1], (n_acc >> 1) & 1)) return false;
-  tc_fence_after();
-  return true;
-}
-__device__ __forceinline__ void sum_free(Barriers* bar, int n_acc, int lane) {
-  tc_fence_before();
-  __syncwarp();
-  if (lane == 0) mbar_signal_at(in_cta(&bar->acc_empty[n_acc & 1], 0));
+// Tiles beside each other for `outs` results of a row.
+__host__ __device__ __forceinline__ int tiles_beside(int outs, int width, bool gated) {
+  const int each = gated ? width / 2 : width;
+  return (outs + each - 1) / each;
 }
 
-// A block of 32 features by 32 rows, from the order in which the tensor memory gives
-// pairs of rows to a feature of a lane and all its rows, by way of shared memory: the
-// pitch keeps both ways free of conflicts.
-__device__ __forceinline__ void turn_round(float* at, int lane, const uint64_t (&sum)[4][4], float (&r)[32]) {
-  float* to = at + (lane & 3) * 2 * kPitch + (lane >> 2);
-#pragma unroll
-  for (int j = 0; j < 4; ++j)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      float lo, hi;
-      floats_of(sum[j][i], lo, hi);
-      to[8 * i * kPitch + 8 * j] = lo;
-      to[(8 * i + 1) * kPitch + 8 * j] = hi;
+// The groups' segments, the rows of the tiles and the first tile of each group. All
+// threads of the CTA. (A dense product's plan comes from the host.)
+template <bool GATED>
+__device__ QPlan plan_qtiles(const MmaParams& q, int* first, int* begins, int* counts, int* sizes) {
+  __shared__ int sums[kThreads / 32];
+  if (!q.p.s.begin) {
+    if (threadIdx.x == 0) {
+      first[0] = begins[0] = 0;
+      counts[0] = (int)q.p.s.dense_rows;
+      sizes[0] = q.plan.size;
     }
-  __syncwarp();
+    __syncthreads();
+    return q.plan;
+  }
+  const int G = q.p.s.G, pairs = gridDim.x >> 1;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int per = (G + kThreads - 1) / kThreads;
+  const int g0 = threadIdx.x * per, g1 = min(G, g0 + per);
+  int mine = 0;                          // tiles above each other
+  for (int g = g0; g < g1; ++g) {
+    int64_t b, c;
+    segment_of(q.p.s, g, b, c);
+    begins[g] = (int)b;
+    counts[g] = (int)c;
+    mine += tiles_in((int)c, kTileRows);
+  }
+  int incl = mine;
 #pragma unroll
-  for (int c = 0; c < 32; ++c) r[c] = at[c * kPitch + lane];
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(kFull, incl, o);
+    if (lane >= o) incl += v;
+  }
+  if (lane == 31) sums[warp] = incl;
+  __syncthreads();
+  int all = 0, before = incl - mine;
+#pragma unroll
+  for (int w = 0; w < kThreads / 32; ++w) {
+    if (w < warp) before += sums[w];
+    all += sums[w];
+  }
+  QPlan plan;
+  plan.width = 256;
+  plan.f_tiles = tiles_beside(q.outs, 256, GATED);
+  if (2 * all * plan.f_tiles <= pairs) {
+    plan.width = 128;
+    plan.f_tiles = tiles_beside(q.outs, 128, GATED);
+  }
+  plan.tiles = all * plan.f_tiles;
+  plan.splits = plan.width == 128 ? splits_for(pairs, plan.tiles, q.stages, kWorth, kLeast) : 1;
+  plan.size = 0;
+  for (int g = g0; g < g1; ++g) {
+    first[g] = before * plan.f_tiles;
+    sizes[g] = tile_rows(counts[g], kTileRows, quotient);
+    before += quotient(counts[g] + sizes[g] - 1, sizes[g]);
+  }
+  __syncthreads();
+  return plan;
+}
+
+// Unit u of the plan: part u % splits of tile u / splits. f0 counts results of a row.
+template <bool GATED>
+__device__ __forceinline__ Tile qtile_at(const MmaParams& q, const QPlan& plan, const int* first,
+                                         const int* begins, const int* counts, const int* sizes, int u) {
+  Tile w;
+  int t = plan.splits == 1 ? u : quotient(u, plan.splits);
+  w.part = u - t * plan.splits;
+  int lo = 0, hi = q.p.s.G - 1;          // the last group that starts at or before t
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (first[mid] <= t) lo = mid; else hi = mid - 1;
+  }
+  t -= first[lo];
+  w.g = lo;
+  w.begin = begins[lo];
+  const int count = counts[lo];
+  // 8 row tiles at a time pass over all features, so that tiles that run together
+  // share operands in L2
+  const int size = sizes[lo];
+  const int tiles = quotient(count + size - 1, size);
+  const int band = quotient(t, 8 * plan.f_tiles);
+  const int in = min(8, tiles - band * 8);
+  t -= band * 8 * plan.f_tiles;
+  const int f = quotient(t, in);
+  w.r0 = (band * 8 + t - f * in) * size;
+  w.f0 = f * (GATED ? plan.width / 2 : plan.width);
+  w.rows = min(size, count - w.r0);
+  w.n = (w.rows + 63) / 64 * 32;         // rows of the even CTA, the others are the odd one's
+  w.terms = 0;
+  w.parts = 1;
+  w.kb0 = 0;
+  w.kb1 = q.stages;
+  if (plan.splits > 1) {
+    const int each = quotient(q.stages + plan.splits - 1, plan.splits);
+    w.parts = quotient(q.stages + each - 1, each);
+    w.kb0 = w.part * each;
+    w.kb1 = min(q.stages, w.kb0 + each);
+  }
+  return w;
+}
+
+// Rows of a tile that are this CTA's.
+__device__ __forceinline__ int rows_of(const Tile& w, int cta) {
+  return cta ? w.rows - w.n : min(w.rows, w.n);
+}
+
+__device__ __forceinline__ void store_v8(void* p, const uint32_t (&v)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]),
+               "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
+}
+__device__ __forceinline__ void load_v8(const void* p, uint32_t (&v)[8]) {
+  asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
+               : "l"(p)
+               : "memory");
+}
+
+// 32 neighbouring values of a row, 32 bytes at a time: whole sectors of a lane's own.
+__device__ __forceinline__ void store_row(__nv_bfloat16* at, const float (&v)[32]) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    uint32_t u[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) u[i] = cvt_bf16x2(v[16 * h + 2 * i], v[16 * h + 2 * i + 1]);
+    store_v8(at + 16 * h, u);
+  }
+}
+__device__ __forceinline__ void store_row(float* at, const float (&v)[32]) {
+#pragma unroll
+  for (int h = 0; h < 4; ++h) {
+    uint32_t u[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) u[i] = __float_as_uint(v[8 * h + i]);
+    store_v8(at + 8 * h, u);
+  }
+}
+__device__ __forceinline__ void add_row(const __nv_bfloat16* at, float (&v)[32]) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    uint32_t u[8];
+    load_v8(at + 16 * h, u);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      v[16 * h + 2 * i] += bf16_lo(u[i]);
+      v[16 * h + 2 * i + 1] += bf16_hi(u[i]);
+    }
+  }
+}
+__device__ __forceinline__ void add_row(const float* at, float (&v)[32]) {
+#pragma unroll
+  for (int h = 0; h < 4; ++h) {
+    uint32_t u[8];
+    load_v8(at + 8 * h, u);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[8 * h + i] += __uint_as_float(u[i]);
+  }
+}
+
+// The epilogue of 32 columns of a warp's rows: `z` (and `up`, with SwiGLU) is a lane's
+// row, T the output's type. Whole aligned pieces go out as they are; others are turned
+// round, kTurnRows rows at a time, so that a warp stores 32 neighbours of a row.
+template <int MODE, int ACT, typename T>
+__device__ __forceinline__ void finish(const MmaParams& q, float* room, int g, int64_t row0, int rows,
+                                       int col, int lane, float (&z)[32], float (&up)[32]) {
+  constexpr bool kGated = MODE == kForward && ACT == EP_ACT_SWIGLU;
+  const QLinearParams& p = q.p;
+  const float* bias = MODE == kForward && p.bias ? p.bias + (int64_t)g * p.Nw + col : nullptr;
+  T* y = static_cast<T*>(q.out) + row0 * q.outs + col;
+  const T* res = MODE == kForward && p.residual ? static_cast<const T*>(p.residual) + row0 * q.outs + col : nullptr;
+  __nv_bfloat16* zp = MODE == kForward && p.z ? p.z + row0 * p.Nw + col : nullptr;
+  if (q.vec && col + 32 <= q.outs) {
+    if (lane >= rows) return;
+    if (bias) {
+#pragma unroll
+      for (int c = 0; c < 32; ++c) {
+        z[c] += bias[c];
+        if (kGated) up[c] += bias[p.N + c];
+      }
+    }
+    if (zp) {
+      store_row(zp + (int64_t)lane * p.Nw, z);
+      if (kGated) store_row(zp + (int64_t)lane * p.Nw + p.N, up);
+    }
+    if (MODE == kForward) {
+#pragma unroll
+      for (int c = 0; c < 32; ++c) z[c] = kGated ? silu_of(z[c]) * up[c] : act_of(ACT, z[c]);
+    }
+    if (res) add_row(res + (int64_t)lane * q.outs, z);
+    store_row(y + (int64_t)lane * q.outs, z);
+    return;
+  }
+  const bool in = col + lane < q.outs;
+  const float b = bias && in ? bias[lane] : 0.0f, b_up = kGated && bias && in ? bias[p.N + lane] : 0.0f;
+  for (int r0 = 0; r0 < 32; r0 += kTurnRows) {
+    if (r0 >= rows) break;
+    __syncwarp();
+    if (lane / kTurnRows == r0 / kTurnRows) {
+      float* to = room + (lane % kTurnRows) * kTurnPitch;
+#pragma unroll
+      for (int c = 0; c < 32; ++c) {
+        to[c] = z[c];
+        if (kGated) to[kTurnRows * kTurnPitch + c] = up[c];
+      }
+    }
+    __syncwarp();
+#pragma unroll
+    for (int r = 0; r < kTurnRows; ++r) {
+      const int64_t row = r0 + r;
+      const bool on = in && row < rows;
+      float v = room[r * kTurnPitch + lane] + b;
+      if (zp) put(zp + row * p.Nw + lane, v, on);
+      if (kGated) {
+        const float u = room[(kTurnRows + r) * kTurnPitch + lane] + b_up;
+        if (zp) put(zp + row * p.Nw + p.N + lane, u, on);
+        v = silu_of(v) * u;
+      } else if (MODE == kForward) {
+        v = act_of(ACT, v);
+      }
+      if (res) v += get(res + row * q.outs + lane, on);
+      put(y + row * q.outs + lane, v, on);
+    }
+  }
   __syncwarp();
+}
+
+// 32 sums of a lane, as pairs.
+__device__ __forceinline__ void unpack_sums(const uint64_t (&sum)[16], float (&v)[32]) {
+#pragma unroll
+  for (int c = 0; c < 16; ++c) floats_of(sum[c], v[2 * c], v[2 * c + 1]);
 }
 
 struct Maps {
-  CUtensorMap a;
-  CUtensorMap b[4];        // boxes of 128, 64, 32 and 16 rows
+  CUtensorMap rows[3];     // boxes of 128, 64 and 32 rows
+  CUtensorMap w[2];        // boxes of 128 and 64 features (dx: 128 features of 128 and 64 terms)
 };
 
 template <int MODE, int ACT, typename T>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     product8_kernel(const __grid_constant__ Maps maps, MmaParams q) {
   constexpr bool kGated = MODE == kForward && ACT == EP_ACT_SWIGLU;
-  constexpr int kBlocks = kMaxRows / 64;         // of 32 columns, of a warp
-  constexpr int kScaleSlots = kGated ? 4 : 8, kScaleRow = kGated ? 2 * kMaxRows : kMaxRows;
-  constexpr int kScaleAhead = kGated ? 2 : 4;    // stages whose scales are fetched at once
   extern __shared__ uint8_t raw[];
   uint8_t* ring = reinterpret_cast<uint8_t*>(((uintptr_t)raw + 1023) & ~(uintptr_t)1023);
-  float* scales = reinterpret_cast<float*>(ring + kRingBytes);   // [slot][gate, up][row]
-  float* turned = scales + kScaleBytes / 4;                      // [epilogue warp][row][feature]
-  Barriers* bar = reinterpret_cast<Barriers*>(ring + kRingBytes + kScaleBytes + kTurnBytes);
+  float* rooms = reinterpret_cast<float*>(ring + kRingBytes);    // [epilogue warp][kTurnWords]
+  Barriers* bar = reinterpret_cast<Barriers*>(ring + kRingBytes + kTurnBytes);
   int* first = reinterpret_cast<int*>(bar + 1);
   int* begins = first + q.p.s.G;
   int* counts = begins + q.p.s.G;
   int* sizes = counts + q.p.s.G;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const uint32_t cta = cluster_rank();
+  const int cta = (int)cluster_rank();
   int32_t* timeout = q.p.s.err;
 
   // one thread a barrier
   if (threadIdx.x < kMaxStages) {
-    mbar_init(&bar->full[threadIdx.x], 2);       // each CTA's producer
-    mbar_init(&bar->empty[threadIdx.x], 1);
+    mbar_init(&bar->full[threadIdx.x], 1);
+    mbar_init(&bar->empty[threadIdx.x], 2);      // each CTA's products
   } else if (threadIdx.x < kMaxStages + 2) {
     mbar_init(&bar->acc_full[threadIdx.x - kMaxStages], 1);
-    mbar_init(&bar->acc_empty[threadIdx.x - kMaxStages], 2 * kEpilogueWarps);  // of both CTAs
   }
   if (threadIdx.x >= 32 && threadIdx.x < 32 + kSlots) {
-    // producer, scales, the epilogue's warps, MMA (even CTA)
+    // producer, MMA, the epilogue's warps
     mbar_init(&bar->tile_full[threadIdx.x - 32], 1);
-    mbar_init(&bar->tile_empty[threadIdx.x - 32], 2 + kEpilogueWarps + (cta == 0 ? 1 : 0));
-  } else if (threadIdx.x >= 40 && threadIdx.x < 40 + kMaxScaleSlots) {
-    mbar_init(&bar->scale_full[threadIdx.x - 40], 1);
-    mbar_init(&bar->scale_empty[threadIdx.x - 40], kEpilogueWarps);
+    mbar_init(&bar->tile_empty[threadIdx.x - 32], 2 + kEpilogueWarps);
   } else if (threadIdx.x == 32 + kSlots) {
     mbar_init(&bar->joined, kEpilogueWarps);
   }
   if (threadIdx.x < 64) mbar_init_fence();
   if (threadIdx.x == 64) {
-    tma_prefetch_map(&maps.a);
-    tma_prefetch_map(&maps.b[0]);
+    tma_prefetch_map(&maps.rows[0]);
+    tma_prefetch_map(&maps.w[0]);
   }
   __syncthreads();
   cluster_arrive();                      // the barriers are ready; the wait is below
-  if (warp == 1) tmem_alloc(&bar->tmem, kTmemColumns);
+  if (warp == 1) tmem_alloc_own(&bar->tmem, kTmemColumns);
   begin_overlapped();
-  const Plan plan = plan_tiles<MODE>(q, first, begins, counts, sizes);
+  const QPlan plan = plan_qtiles<kGated>(q, first, begins, counts, sizes);
   const int units = plan.tiles * plan.splits;
-  const int stage_bytes = kStageA + plan.cap / 2 * kDepth;
+  const int half_bytes = plan.width / 2 * kDepth;         // of the weights, of each CTA
+  const int stage_bytes = kStageA + 2 * half_bytes;
   const int stages = min(kMaxStages, kRingBytes / stage_bytes);
   tc_fence_before();
   __syncthreads();                       // the TMEM address is there
@@ -188,36 +398,37 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       // ---------------------------------------------- producer: one thread
       int it = 0, s = 0;                      // stages written so far, the ring's place
       uint32_t phase = 1;                     // the first pass over the ring waits for nothing
-      const uint32_t full0 = in_cta(&bar->full[0], 0);
-      const uint32_t ring0 = smem_addr(ring);
+      const uint32_t full0 = smem_addr(&bar->full[0]), ring0 = smem_addr(ring);
       bool ok = true;
       for (int i = 0; i < mine && ok; ++i) {
         Tile w;
         ok = take_tile(bar, i, w);
         if (!ok) break;
-        const int half = w.n / 2;
-        const int fc = w.f0 + (int)cta * 128;                     // this CTA's features
-        const int row = (int)w.begin + w.r0 + (int)cta * half;    // this CTA's rows
-        const int box = half > 64 ? 0 : half > 32 ? 1 : half > 16 ? 2 : 3;
-        const uint32_t bytes = kStageA + (kStageB >> box);
-        const CUtensorMap* map_b = &maps.b[box];
+        const bool some = rows_of(w, cta) > 0;
+        const int row = (int)w.begin + w.r0 + cta * w.n;
+        const int box = w.n > 64 ? 0 : w.n > 32 ? 1 : 2;
+        const uint32_t bytes = (some ? kStageA >> box : 0) + 2 * half_bytes;
+        const CUtensorMap* map_w = &maps.w[plan.width == 256 ? 0 : 1];
         for (int kb = w.kb0; kb < w.kb1; ++kb) {
           if (it >= stages) {
             ok = mbar_wait_soon(&bar->empty[s], phase);
             if (!ok) break;
           }
           const uint32_t on = full0 + s * 8, a = ring0 + s * stage_bytes;
-          mbar_signal_expect_tx_at(on, bytes);
+          const uint32_t b = a + kStageA + cta * half_bytes;
+          mbar_arrive_expect_tx(&bar->full[s], bytes);
           const int d = kb * kDepth;
           if (MODE == kInputGrad) {
             const int second = kb >= q.p.Nb;                      // up's half of the terms
-            tma_load_4d(a, &maps.a, fc, d - second * q.p.Nb * kDepth, second, w.g, on);
+            const int term = d - second * q.p.Nb * kDepth;
+            const bool wide = plan.width == 256;
+            tma_both_4d(b, map_w, w.f0 + (wide ? cta * 128 : 0), term + (wide ? 0 : cta * 64), second, w.g, on);
           } else if (kGated) {
-            tma_load_4d(a, &maps.a, d, 0, fc / 2, w.g, on);
+            tma_both_4d(b, map_w, d, w.f0, cta, w.g, on);
           } else {
-            tma_load_3d(a, &maps.a, d, fc, w.g, on);
+            tma_both_4d(b, map_w, d, w.f0 + cta * (plan.width / 2), 0, w.g, on);
           }
-          tma_load_2d(a + kStageA, map_b, d, row, on);
+          if (some) tma_own_2d(a, &maps.rows[box], d, row, on);
           ++it;
           if (++s == stages) {
             s = 0;
@@ -225,7 +436,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           }
         }
       }
-      // the MMAs' arrivals are this CTA's to wait for, the other's too
+      // both CTAs' arrivals here, before this one may leave
       for (int i = 0; i < stages && i < it && ok; ++i) {
         s = s == 0 ? stages - 1 : s - 1;
         ok = mbar_wait_soon(&bar->empty[s], ((it - 1 - i) / stages) & 1);
@@ -236,97 +447,52 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         for (int i = 0; i < stages && i < it; ++i)
           (void)mbar_wait(&bar->full[(it - 1 - i) % stages], ((it - 1 - i) / stages) & 1);
       }
-    } else if (warp == 1 && cta == 0 && elect_one()) {
-      // ---------------------------------------------- MMA: one thread of the even CTA
-      // operands of stage 0; a stage is stage_bytes on
-      constexpr bool kMnA = MODE == kInputGrad;
-      constexpr uint32_t kStepA = (kMnA ? 4096 : 32) >> 4, kStepB = 32 >> 4;
+    } else if (warp == 1) {
+      // ---------------------------------------------- MMA: one lane issues, the warp waits.
+      // After a wait that gave up it issues nothing, but meets the epilogue as often
+      // as ever, and so do the epilogue's warps: the hardware barriers have no limit.
+      constexpr bool kMnB = MODE == kInputGrad;
+      constexpr uint32_t kStepA = 32 >> 4, kStepB = (kMnB ? 4096 : 32) >> 4;
       const uint32_t stage_units = (uint32_t)stage_bytes >> 4;
       const uint64_t op_a = smem_operand(smem_addr(ring), 16);
-      const uint64_t op_b = smem_operand(smem_addr(ring) + kStageA, 16);
+      const uint64_t op_b = smem_operand(smem_addr(ring) + kStageA, kMnB ? 128 * kDepth : 16);
       const uint32_t a0 = (uint32_t)op_a, a_high = (uint32_t)(op_a >> 32);
       const uint32_t b0 = (uint32_t)op_b, b_high = (uint32_t)(op_b >> 32);
       const uint32_t empty0 = smem_addr(&bar->empty[0]), sum0 = smem_addr(&bar->acc_full[0]);
+      const uint32_t full0 = smem_addr(&bar->full[0]);
+      const uint32_t form = mma8_form(plan.width, kMnB);
       int n_acc = 0;
       uint32_t s = 0, phase = 0;             // the ring's place
-      bool ok = true;
-      for (int i = 0; i < mine && ok; ++i) {
+      bool ok = true, ready = false;         // ready: that place was seen to be full
+      for (int i = 0; i < mine; ++i) {
         Tile w;
-        ok = take_tile(bar, i, w);
-        if (!ok) break;
-        const uint32_t form = mma8_form(w.n, kMnA);
-        for (int kb = w.kb0; kb < w.kb1; ++kb, ++n_acc) {
-          if (n_acc >= 2) {
-            ok = mbar_wait_soon_cluster(&bar->acc_empty[n_acc & 1], ((n_acc >> 1) - 1) & 1);
-            if (!ok) break;
+        if (ok) ok = warp_take_tile(bar, i, w, lane);
+        if (!ok) w = qtile_at<kGated>(q, plan, first, begins, counts, sizes, pair + i * pairs);
+        const bool some = rows_of(w, cta) > 0;
+        for (int kb = w.kb0; kb < w.kb1; ++kb) {
+          if (ok && !__all_sync(kFull, ready)) ok = warp_wait(&bar->full[s], phase);
+          if (some && n_acc >= 2) named_sync(1 + (n_acc & 1), kHandover);
+          if (ok) {
             tc_fence_after();
-          }
-          ok = mbar_wait_soon(&bar->full[s], phase);
-          if (!ok) break;
-          tc_fence_after();
-          mma8_stage<kStepA, kStepB>(tmem + (n_acc & 1) * 256, a0 + s * stage_units, a_high,
-                                     b0 + s * stage_units, b_high, form);
-          mma_commit_both(empty0 + s * 8);
-          mma_commit_both(sum0 + (n_acc & 1) * 8);
-          if (++s == (uint32_t)stages) {
-            s = 0;
-            phase ^= 1;
-          }
-        }
-      }
-      // the other CTA's last arrivals here
-      for (int last = n_acc - 2; last < n_acc && ok; ++last)
-        if (last >= 0) ok = mbar_wait_soon_cluster(&bar->acc_empty[last & 1], (last >> 1) & 1);
-      if (!ok) atomicOr(timeout, kErrLinearTimeout);
-      tc_fence_after();
-    } else if (warp == 2) {
-      // ---------------------------------------------- scales
-      int n_scale = 0;
-      bool ok = true;
-      for (int i = 0; i < mine && ok; ++i) {
-        Tile w;
-        ok = warp_take_tile(bar, i, w, lane);
-        if (!ok) break;
-        const float* rows = q.row_scale + (w.begin + w.r0 + lane) * q.row_ld;
-        const int fc = kGated ? w.f0 / 2 + (int)cta * 64 : w.f0 + (int)cta * 128;
-        const float* features = q.p.ws + w.g * q.group_ld + (int64_t)min(fc / 128, q.feature_blocks - 1) * q.feature_ld;
-        for (int kb0 = w.kb0; kb0 < w.kb1 && ok; kb0 += kScaleAhead) {
-          float v[kScaleAhead][kMaxRows / 32], gate[kScaleAhead], up[kScaleAhead];
-#pragma unroll
-          for (int u = 0; u < kScaleAhead; ++u) {
-            const int kb = kb0 + u;
-            const bool there = kb < w.kb1;
-#pragma unroll
-            for (int j = 0; j < kMaxRows / 32; ++j) {
-              v[u][j] = 0.0f;
-              if (there && lane + 32 * j < w.rows) v[u][j] = rows[(int64_t)(32 * j) * q.row_ld + kb];
-            }
-            gate[u] = up[u] = 0.0f;
-            if (there) {
-              gate[u] = features[(int64_t)kb * q.block_ld];
-              if (kGated) up[u] = features[q.up + (int64_t)kb * q.block_ld];
-            }
-          }
-#pragma unroll
-          for (int u = 0; u < kScaleAhead; ++u) {
-            if (kb0 + u >= w.kb1 || !ok) continue;
-            const int slot = n_scale % kScaleSlots;
-            if (n_scale >= kScaleSlots) ok = warp_wait(&bar->scale_empty[slot], (n_scale / kScaleSlots - 1) & 1);
-            if (!ok) continue;
-            // the order in which the epilogue's threads take a block of 32 rows
-            float* to = scales + slot * kScaleRow + (lane & 7) / 2 * 8 + lane / 8 * 2 + (lane & 1);
-#pragma unroll
-            for (int j = 0; j < kMaxRows / 32; ++j) {
-              if (32 * j >= w.n) continue;
-              to[32 * j] = v[u][j] * gate[u];
-              if (kGated) to[kMaxRows + 32 * j] = v[u][j] * up[u];
+            if (lane == 0) {
+              if (some) {
+                mma8_stage<kStepA, kStepB>(tmem + (n_acc & 1) * 256, a0 + s * stage_units, a_high,
+                                           b0 + s * stage_units, b_high, form);
+                mma8_commit(sum0 + (n_acc & 1) * 8);
+              }
+              mma8_commit_both(empty0 + s * 8);
             }
             __syncwarp();
-            if (lane == 0) mbar_arrive(&bar->scale_full[slot]);
-            ++n_scale;
+            if (++s == (uint32_t)stages) {
+              s = 0;
+              phase ^= 1;
+            }
+            ready = mbar_test(full0 + s * 8, phase);       // its answer comes under the MMAs
           }
+          n_acc += some;
         }
       }
+      for (int last = n_acc < 2 ? 0 : n_acc - 2; last < n_acc; ++last) named_sync(1 + (last & 1), kHandover);
       if (!ok && lane == 0) atomicOr(timeout, kErrLinearTimeout);
     } else if (warp == 3 && elect_one()) {
       // ---------------------------------------------- works out the tiles, ahead of all roles
@@ -337,7 +503,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           ok = mbar_wait_soon(&bar->tile_empty[slot], (i / kSlots - 1) & 1);
           if (!ok) break;
         }
-        bar->tiles[slot] = tile_at<MODE>(q, plan, first, begins, counts, sizes, pair + i * pairs);
+        bar->tiles[slot] = qtile_at<kGated>(q, plan, first, begins, counts, sizes, pair + i * pairs);
         mbar_arrive(&bar->tile_full[slot]);
       }
       if (!ok) atomicOr(timeout, kErrLinearTimeout);
@@ -345,87 +511,116 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   } else {
     registers_more<kRegistersMore>();
     // ------------------------------------------------ epilogue
-    // 64 columns of the tile belong to the warp pair of a quarter: 32 to this warp
+    // Blocks of 32 columns: of four (256 columns) or two of this warp's half; with
+    // SwiGLU blocks 0 and 1 are gates, 2 and 3 the same features' up values (128
+    // columns: 0 and 2).
     const int quad = warp & 3, turn = (warp - 4) >> 2;
     const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
-    // a thread's sums are of the features lane / 4 + 8 j: gates, or up's
-    const float* my_scales = scales + (kGated && (lane & 4) ? kMaxRows : 0) + turn * 32 + (lane & 3) * 8;
-    float* turn_at = turned + (warp - 4) * 32 * kPitch;
-    int n_acc = 0;                         // sums, and their scales
+    const int sub = plan.width / 128;                     // blocks 0 .. 2 sub - 1, or 0 .. sub - 1 and 2 ..
+    const uint32_t sum0 = smem_addr(&bar->acc_full[0]);
+    float* room = rooms + (warp - 4) * kTurnWords;
+    int n_acc = 0;
     uint32_t meeting = 0;
-    bool ok = true;
-    for (int i = 0; i < mine && ok; ++i) {
+    bool ok = true, seen = false;                         // seen: the next sum was there already
+    for (int i = 0; i < mine; ++i) {
       const int u = pair + i * pairs;
       Tile w;
-      ok = warp_take_tile(bar, i, w, lane);
-      if (!ok) break;
-      if (w.kb0 >= w.kb1) continue;
-      const bool whole = w.parts == 1;
-      float b = 0.0f;
-      if (MODE == kForward && q.p.bias) {
-        const int f = (int)cta * 128 + quad * 32 + lane;
-        const float* bias = q.p.bias + (int64_t)w.g * q.p.Nw;
-        if (kGated) {
-          const int out = w.f0 / 2 + f / 2;
-          if (out < q.p.N) b = bias[(f & 1 ? q.p.N : 0) + out];
-        } else if (w.f0 + f < q.features) {
-          b = bias[w.f0 + f];
-        }
-      }
-      const int blocks = (w.n - turn * 32 + 63) / 64;   // of this warp (none below 1)
-      uint64_t sum[kBlocks][4][4];                      // [..][lane / 4 + 8 j][8 i + 2 (lane % 4), + 1]
+      if (ok) ok = warp_take_tile(bar, i, w, lane);
+      if (!ok) w = qtile_at<kGated>(q, plan, first, begins, counts, sizes, u);
+      const int rows = rows_of(w, cta);
+      if (rows <= 0 || w.kb0 >= w.kb1) continue;
+      const int mine_rows = rows - quad * 32;             // from this warp's on
+      const int64_t row0 = w.begin + w.r0 + cta * w.n + quad * 32;
+      const int col0 = w.f0 + turn * (kGated ? plan.width / 4 : plan.width / 2);
+      // this lane's scales and its features', kScaleGroup stages ahead
+      const float* row_scales = q.row_scale + (row0 + min(lane, max(mine_rows, 1) - 1)) * q.row_ld;
+      const float* w_scales = q.p.ws + w.g * q.group_ld +
+                              (int64_t)min(col0 / 128, q.feature_blocks - 1) * q.feature_ld;
+      float by[kScaleGroup], by_up[kScaleGroup], next[kScaleGroup], next_w[kScaleGroup], next_up[kScaleGroup];
+      auto fetch = [&](int kb) {
 #pragma unroll
-      for (int h = 0; h < kBlocks; ++h)
-#pragma unroll
-        for (int c = 0; c < 16; ++c) sum[h][c / 4][c % 4] = 0;   // two f32 zeros
-      for (int kb = w.kb0; kb < w.kb1; ++kb, ++n_acc) {
-        const int slot = n_acc % kScaleSlots;
-        ok = warp_wait(&bar->scale_full[slot], (n_acc / kScaleSlots) & 1) && sum_ready(bar, n_acc);
-        if (!ok) break;
-        const float* scale = my_scales + slot * kScaleRow;
-        if (blocks < 1) sum_free(bar, n_acc, lane);
-#pragma unroll
-        for (int h = 0; h < kBlocks; ++h) {
-          if (h >= blocks) continue;
-          const ulonglong2 by0 = *reinterpret_cast<const ulonglong2*>(scale + h * 64);
-          const ulonglong2 by1 = *reinterpret_cast<const ulonglong2*>(scale + h * 64 + 4);
-          float r[4][8];
-          tmem_load_pairs(lanes + (n_acc & 1) * 256 + turn * 32 + h * 64, r);
-          if (h == blocks - 1) sum_free(bar, n_acc, lane);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            fma2(sum[h][j][0], pair_of(r[j][0], r[j][1]), by0.x);
-            fma2(sum[h][j][1], pair_of(r[j][2], r[j][3]), by0.y);
-            fma2(sum[h][j][2], pair_of(r[j][4], r[j][5]), by1.x);
-            fma2(sum[h][j][3], pair_of(r[j][6], r[j][7]), by1.y);
+        for (int j = 0; j < kScaleGroup; ++j) {
+          next[j] = next_w[j] = next_up[j] = 0.0f;
+          if (mine_rows > 0 && kb + j < w.kb1) {
+            next[j] = row_scales[kb + j];
+            next_w[j] = w_scales[(int64_t)(kb + j) * q.block_ld];
+            if (kGated) next_up[j] = w_scales[q.up + (int64_t)(kb + j) * q.block_ld];
           }
         }
+      };
+      fetch(w.kb0);
+      uint64_t sum[4][16];
+#pragma unroll
+      for (int h = 0; h < 4; ++h)
+#pragma unroll
+        for (int c = 0; c < 16; ++c) sum[h][c] = 0;       // two f32 zeros
+      int left = 0;                                       // scales that are there
+      for (int kb = w.kb0; kb < w.kb1; ++kb, ++n_acc, --left) {
+        if (left == 0) {
+#pragma unroll
+          for (int j = 0; j < kScaleGroup; ++j) {
+            by[j] = next[j] * next_w[j];
+            by_up[j] = next[j] * next_up[j];
+          }
+          left = kScaleGroup;
+          fetch(kb + kScaleGroup);
+        }
+        if (ok && !__all_sync(kFull, seen)) ok = warp_wait(&bar->acc_full[n_acc & 1], (n_acc >> 1) & 1);
+        tc_fence_after();
+        const uint64_t scale = pair_of(by[0], by[0]), scale_up = pair_of(by_up[0], by_up[0]);
+#pragma unroll
+        for (int j = 0; j + 1 < kScaleGroup; ++j) {
+          by[j] = by[j + 1];
+          by_up[j] = by_up[j + 1];
+        }
+        const uint32_t at = lanes + (n_acc & 1) * 256 + turn * (kGated ? plan.width / 4 : plan.width / 2);
         __syncwarp();
-        if (lane == 0) mbar_arrive(&bar->scale_empty[slot]);
+        if (mine_rows > 0 && ok) {
+#pragma unroll
+          for (int h = 0; h < 4; ++h) {
+            if ((kGated ? h & 1 : h >> 1) >= sub) continue;
+            float r[32];
+            tmem_load32(at + (kGated && h >= 2 ? plan.width / 2 + (h - 2) * 32 : h * 32), r);
+#pragma unroll
+            for (int c = 0; c < 16; ++c)
+              fma2(sum[h][c], pair_of(r[2 * c], r[2 * c + 1]), kGated && h >= 2 ? scale_up : scale);
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        named_arrive(1 + (n_acc & 1), kHandover);
+        seen = mbar_test(sum0 + ((n_acc + 1) & 1) * 8, ((n_acc + 1) >> 1) & 1);
       }
-      if (!ok) break;
+      if (!ok) continue;
       // the values of this part: the tile's result, or sums for the part that finishes
       // last, which then adds all of them in their order
-      if (whole) {
+      if (w.parts == 1) {
+        if (mine_rows <= 0) continue;
 #pragma unroll
-        for (int h = 0; h < kBlocks; ++h) {
-          const int c0 = turn * 32 + h * 64;
-          if (c0 >= w.rows) continue;
-          float r[32];
-          turn_round(turn_at, lane, sum[h], r);
-          epilogue<MODE, ACT, T>(q, w, (int)cta, lane, quad, c0, r, b);
+        for (int h = 0; h < (kGated ? 2 : 4); ++h) {
+          const int col = col0 + h * 32;
+          if ((kGated ? h & 1 : h >> 1) >= sub || col >= q.outs) continue;
+          float z[32], up[32];
+          unpack_sums(sum[h], z);
+          if (kGated) unpack_sums(sum[(h + 2) & 3], up);
+          finish<MODE, ACT, T>(q, room, w.g, row0, mine_rows, col, lane, z, up);
         }
         continue;
       }
-      // this lane's column in the pair's place (a pair has one unit where there are parts)
-      float* sums = q.p.partial + ((int64_t)pair * plan.cap * 256 + cta * 128 + quad * 32 + lane);
-      const int c0 = turn * 32;                         // parts are of tiles of at most 64 rows
-      float r[32];
-      turn_round(turn_at, lane, sum[0], r);
+      // this lane's place in the pair's (a pair has one unit where there are parts, of
+      // tiles of 128 columns)
+      float* sums = q.p.partial + ((int64_t)pair * 128 * 256 + cta * 128 + quad * 32 + lane);
 #pragma unroll
-      for (int c = 0; c < 32; ++c) put(sums + (c0 + c) * 256, r[c], c0 + c < w.rows);
+      for (int h = 0; h < 4; ++h) {
+        if ((kGated ? h & 1 : h >> 1) >= 1) continue;
+        const int column = (kGated && h >= 2 ? 64 : h * 32) + turn * (kGated ? 32 : 64);
+        float v[32];
+        unpack_sums(sum[h], v);
+#pragma unroll
+        for (int c = 0; c < 32; ++c) put(sums + (column + c) * 256, v[c], lane < mine_rows);
+      }
       ok = epilogue_meet(bar, lane, meeting);
-      if (!ok) break;
+      if (!ok) continue;
       if (threadIdx.x == 128) {
         unsigned int* ticket = q.p.tickets + quotient(u, plan.splits) * 2 + cta;
         const bool last = ticket_take(ticket) == (unsigned)w.parts - 1;
@@ -433,10 +628,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         bar->last = last;
       }
       ok = epilogue_meet(bar, lane, meeting);
-      if (!ok) break;
-      if (!bar->last || c0 >= w.rows) continue;
-      add_parts(sums - (int64_t)w.part * plan.cap * 256 + c0 * 256, plan.cap * 256, w.parts, w.rows - c0, r);
-      epilogue<MODE, ACT, T>(q, w, (int)cta, lane, quad, c0, r, b);
+      if (!ok || !bar->last || mine_rows <= 0) continue;
+      const float* parts = sums - (int64_t)w.part * 128 * 256;
+      const int there = lane < mine_rows ? 32 : 0;        // a lane without a row reads nothing
+#pragma unroll 1
+      for (int h = 0; h < (kGated ? 1 : 2); ++h) {
+        const int col = col0 + h * 32;
+        if (col >= q.outs) continue;
+        const int column = h * 32 + turn * (kGated ? 32 : 64);
+        float z[32], up[32];
+        add_parts(parts + column * 256, 128 * 256, w.parts, there, z);
+        if (kGated) add_parts(parts + (column + 64) * 256, 128 * 256, w.parts, there, up);
+        finish<MODE, ACT, T>(q, room, w.g, row0, mine_rows, col, lane, z, up);
+      }
     }
     if (!ok && lane == 0) atomicOr(timeout, kErrLinearTimeout);
   }
@@ -444,28 +648,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   __syncthreads();
   cluster_arrive();   // the other CTA may still arrive on this one's barriers
   cluster_wait();
-  if (warp == 1) tmem_free(tmem, kTmemColumns);
+  if (warp == 1) tmem_free_own(tmem, kTmemColumns);
 }
 
 // ---------------------------------------------------------------------- host
 
-// Rows of a K-major operand, in boxes of 128, 64, 32 and 16 rows.
-bool map_rows8(CUtensorMap (&m)[4], const void* base, int64_t cols, int64_t rows) {
-  const int64_t dims[2] = {cols, rows}, strides[2] = {1, cols};
-  bool ok = true;
-  for (int i = 0; i < 4; ++i) {
-    const int box[2] = {kDepth, 128 >> i};
-    ok = ok && make_map(&m[i], base, 2, dims, strides, box, 1);
-  }
-  return ok;
-}
-
 template <int MODE, int ACT, typename T>
 cudaError_t launch_tiles(const Maps& maps, MmaParams& q, int grid, cudaStream_t st) {
-  q.pairs_out = q.features % 2 == 0 && (uintptr_t)q.out % 4 == 0;
-  q.pairs_z = q.features % 2 == 0 && (uintptr_t)q.p.z % 4 == 0;
-  constexpr size_t kFixed = 1024 + kRingBytes + kScaleBytes + kTurnBytes + sizeof(Barriers);
-  static_assert(kFixed + EP_MAX_EXPERTS * kGroupBytes <= 227 * 1024, "shared memory");
+  const auto whole = [](const void* p) { return (uintptr_t)p % 32 == 0; };
+  q.vec = q.outs % 16 == 0 && whole(q.out) && whole(q.p.residual) && whole(q.p.z);
+  constexpr size_t kOther = 1024 + kRingBytes + kTurnBytes + sizeof(Barriers);
+  constexpr size_t kMost = kOther + EP_MAX_EXPERTS * kGroupBytes;
+  static_assert(kMost <= 227 * 1024 - 512, "shared memory");
   static std::atomic<uint64_t> raised{0};
   const auto kernel = product8_kernel<MODE, ACT, T>;
   // the epilogue's warps ask for registers that the block has to have been launched
@@ -478,10 +672,10 @@ cudaError_t launch_tiles(const Maps& maps, MmaParams& q, int grid, cudaStream_t 
     if (a.numRegs < kRegisters) return cudaErrorInvalidKernelImage;
     checked.store(1, std::memory_order_relaxed);
   }
-  const cudaError_t e = raise_shared_limit(kernel, kFixed + EP_MAX_EXPERTS * kGroupBytes, &raised);
+  const cudaError_t e = raise_shared_limit(kernel, kMost, &raised);
   if (e != cudaSuccess) return e;
-  return launch_overlapped(kernel, dim3((unsigned)grid), kThreads, kFixed + (size_t)q.p.s.G * kGroupBytes,
-                           st, maps, q);
+  return launch_overlapped(kernel, dim3((unsigned)grid), kThreads, kOther + (size_t)q.p.s.G * kGroupBytes, st,
+                           maps, q);
 }
 
 template <typename T>
@@ -496,24 +690,53 @@ cudaError_t launch_forward(const Maps& m, MmaParams& q, int grid, cudaStream_t s
 }
 
 // What both products set: the grid, and a dense product's plan.
-int plan_grid(MmaParams& q, int sms) {
-  q.f_tiles = (q.features + 255) / 256;
-  q.cap = kMaxRows;
-  const int stages = (q.terms + kDepth - 1) / kDepth;
-  const int grid = grid_of(sms, most_units(q.p.s, q.f_tiles, stages));
-  q.plan = dense_plan(q.p.s.dense_rows, q.cap, q.f_tiles, stages, grid / 2);
+int plan_grid(MmaParams& q, bool gated, int sms) {
+  const LinearSegs& s = q.p.s;
+  const int64_t rows = s.begin ? s.pool : s.dense_rows;
+  const int narrow = tiles_beside(q.outs, 128, gated), parts = q.stages / kLeast;
+  const int64_t most = (rows / kTileRows + s.G) * narrow * (parts < 1 ? 1 : parts < kMaxSplits ? parts : kMaxSplits);
+  const int grid = grid_of(sms, most), pairs = grid / 2;
+  QPlan& plan = q.plan;
+  plan.size = tile_rows((int)s.dense_rows, kTileRows, host_quotient);
+  const int above = (int)((s.dense_rows + plan.size - 1) / plan.size);
+  plan.width = 256;
+  plan.f_tiles = tiles_beside(q.outs, 256, gated);
+  if (2 * (int64_t)above * plan.f_tiles <= pairs) {
+    plan.width = 128;
+    plan.f_tiles = narrow;
+  }
+  plan.tiles = above * plan.f_tiles;
+  plan.splits = plan.width == 128 ? splits_for(pairs, plan.tiles, q.stages, kWorth, kLeast) : 1;
   return grid;
+}
+
+// Maps of both operands: rows of codes in boxes of 128, 64 and 32 rows; W [G][parts][N][K]
+// in boxes of 128 bytes by 128 or 64 rows.
+bool make_maps(Maps* m, const QLinearParams& p, const uint8_t* rows, int64_t cols) {
+  const int64_t count = p.s.begin ? p.s.pool : p.s.dense_rows;
+  const int64_t row_dims[2] = {cols, count}, row_strides[2] = {1, cols};
+  const int64_t dims[4] = {p.K, p.N, p.Nw / p.N, p.s.G};
+  const int64_t strides[4] = {1, p.K, (int64_t)p.N * p.K, (int64_t)p.Nw * p.K};
+  bool ok = true;
+  for (int i = 0; i < 3; ++i) {
+    const int box[2] = {kDepth, 128 >> i};
+    ok = ok && make_map(&m->rows[i], rows, 2, row_dims, row_strides, box, 1);
+  }
+  for (int i = 0; i < 2; ++i) {
+    const int box[4] = {kDepth, 128 >> i, 1, 1};
+    ok = ok && make_map(&m->w[i], p.w, 4, dims, strides, box, 1);
+  }
+  return ok;
 }
 
 }  // namespace
 
 cudaError_t launch_qlinear_forward(const QLinearParams& p, int sms, cudaStream_t st) {
-  const int64_t rows = p.s.begin ? p.s.pool : p.s.dense_rows;
   MmaParams q;
   q.p = p;
   q.out = p.y;
-  q.features = p.Nw;
-  q.terms = p.K;
+  q.outs = p.N;
+  q.stages = p.Kb;
   q.row_scale = p.xs;
   q.row_ld = p.Kb;
   q.group_ld = (int64_t)p.Sw * p.Kb;
@@ -522,30 +745,17 @@ cudaError_t launch_qlinear_forward(const QLinearParams& p, int sms, cudaStream_t
   q.feature_blocks = p.Nb;
   q.up = p.Nb * p.Kb;
   Maps m;
-  bool ok;
-  if (p.act == EP_ACT_SWIGLU) {   // gate and up rows of a feature next to each other
-    const int64_t dims[4] = {p.K, 2, p.N, p.s.G};
-    const int64_t strides[4] = {1, (int64_t)p.N * p.K, p.K, (int64_t)p.Nw * p.K};
-    const int box[4] = {kDepth, 2, 64, 1};
-    ok = make_map(&m.a, p.w, 4, dims, strides, box, 1);
-  } else {
-    const int64_t dims[3] = {p.K, p.Nw, p.s.G}, strides[3] = {1, p.K, (int64_t)p.Nw * p.K};
-    const int box[3] = {kDepth, 128, 1};
-    ok = make_map(&m.a, p.w, 3, dims, strides, box, 1);
-  }
-  if (!ok || !map_rows8(m.b, p.x, p.K, rows)) return cudaErrorInvalidValue;
-  const int grid = plan_grid(q, sms);
+  if (!make_maps(&m, p, p.x, p.K)) return cudaErrorInvalidValue;
+  const int grid = plan_grid(q, p.act == EP_ACT_SWIGLU, sms);
   return p.y_f32 ? launch_forward<float>(m, q, grid, st) : launch_forward<__nv_bfloat16>(m, q, grid, st);
 }
 
 cudaError_t launch_qlinear_input_grad(const QLinearParams& p, int sms, cudaStream_t st) {
-  const int64_t rows = p.s.begin ? p.s.pool : p.s.dense_rows;
-  const int parts = p.Sw / p.Nb;
   MmaParams q;
   q.p = p;
   q.out = p.dx;
-  q.features = p.K;
-  q.terms = p.Sw * kDepth;
+  q.outs = p.K;
+  q.stages = p.Sw;
   q.row_scale = p.dzs;
   q.row_ld = p.Sw;
   q.group_ld = (int64_t)p.Sw * p.Kb;
@@ -554,12 +764,8 @@ cudaError_t launch_qlinear_input_grad(const QLinearParams& p, int sms, cudaStrea
   q.feature_blocks = p.Kb;
   q.up = 0;
   Maps m;
-  const int64_t dims[4] = {p.K, p.N, parts, p.s.G};
-  const int64_t strides[4] = {1, p.K, (int64_t)p.N * p.K, (int64_t)p.Nw * p.K};
-  const int box[4] = {128, kDepth, 1, 1};
-  if (!make_map(&m.a, p.w, 4, dims, strides, box, 1) || !map_rows8(m.b, p.dz8, q.terms, rows))
-    return cudaErrorInvalidValue;
-  const int grid = plan_grid(q, sms);
+  if (!make_maps(&m, p, p.dz8, (int64_t)p.Sw * kDepth)) return cudaErrorInvalidValue;
+  const int grid = plan_grid(q, false, sms);
   return launch_tiles<kInputGrad, EP_ACT_NONE, __nv_bfloat16>(m, q, grid, st);
 }
 
