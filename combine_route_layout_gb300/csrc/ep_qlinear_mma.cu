@@ -85,19 +85,6 @@ struct Barriers {
   uint32_t last;              // this CTA's part of a tile was the last
 };
 
-// Two sums of f32 at once: acc += a b.
-__device__ __forceinline__ void fma2(uint64_t& acc, uint64_t a, uint64_t b) {
-  asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(acc) : "l"(a), "l"(b));
-}
-__device__ __forceinline__ uint64_t pair_of(float lo, float hi) {
-  uint64_t v;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(lo), "f"(hi));
-  return v;
-}
-__device__ __forceinline__ void floats_of(uint64_t v, float& lo, float& hi) {
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
-}
-
 // Tiles beside each other for `outs` results of a row.
 __host__ __device__ __forceinline__ int tiles_beside(int outs, int width, bool gated) {
   const int each = gated ? width / 2 : width;
@@ -329,12 +316,6 @@ __device__ __forceinline__ void finish(const MmaParams& q, float* room, int g, i
   __syncwarp();
 }
 
-// 32 sums of a lane, as pairs.
-__device__ __forceinline__ void unpack_sums(const uint64_t (&sum)[16], float (&v)[32]) {
-#pragma unroll
-  for (int c = 0; c < 16; ++c) floats_of(sum[c], v[2 * c], v[2 * c + 1]);
-}
-
 struct Maps {
   CUtensorMap rows[3];     // boxes of 128, 64 and 32 rows
   CUtensorMap w[2];        // boxes of 128 and 64 features (dx: 128 features of 128 and 64 terms)
@@ -549,11 +530,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
       };
       fetch(w.kb0);
-      uint64_t sum[4][16];
+      float sum[4][32];
 #pragma unroll
       for (int h = 0; h < 4; ++h)
 #pragma unroll
-        for (int c = 0; c < 16; ++c) sum[h][c] = 0;       // two f32 zeros
+        for (int c = 0; c < 32; ++c) sum[h][c] = 0.0f;
       int left = 0;                                       // scales that are there
       for (int kb = w.kb0; kb < w.kb1; ++kb, ++n_acc, --left) {
         if (left == 0) {
@@ -567,7 +548,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         if (ok && !__all_sync(kFull, seen)) ok = warp_wait(&bar->acc_full[n_acc & 1], (n_acc >> 1) & 1);
         tc_fence_after();
-        const uint64_t scale = pair_of(by[0], by[0]), scale_up = pair_of(by_up[0], by_up[0]);
+        const float scale = by[0], scale_up = by_up[0];
 #pragma unroll
         for (int j = 0; j + 1 < kScaleGroup; ++j) {
           by[j] = by[j + 1];
@@ -582,8 +563,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             float r[32];
             tmem_load32(at + (kGated && h >= 2 ? plan.width / 2 + (h - 2) * 32 : h * 32), r);
 #pragma unroll
-            for (int c = 0; c < 16; ++c)
-              fma2(sum[h][c], pair_of(r[2 * c], r[2 * c + 1]), kGated && h >= 2 ? scale_up : scale);
+            for (int c = 0; c < 32; ++c) sum[h][c] = fmaf(r[c], kGated && h >= 2 ? scale_up : scale, sum[h][c]);
           }
         }
         tc_fence_before();
@@ -600,10 +580,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         for (int h = 0; h < (kGated ? 2 : 4); ++h) {
           const int col = col0 + h * 32;
           if ((kGated ? h & 1 : h >> 1) >= sub || col >= q.outs) continue;
-          float z[32], up[32];
-          unpack_sums(sum[h], z);
-          if (kGated) unpack_sums(sum[(h + 2) & 3], up);
-          finish<MODE, ACT, T>(q, room, w.g, row0, mine_rows, col, lane, z, up);
+          finish<MODE, ACT, T>(q, room, w.g, row0, mine_rows, col, lane, sum[h], sum[(h + 2) & 3]);
         }
         continue;
       }
@@ -614,10 +591,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       for (int h = 0; h < 4; ++h) {
         if ((kGated ? h & 1 : h >> 1) >= 1) continue;
         const int column = (kGated && h >= 2 ? 64 : h * 32) + turn * (kGated ? 32 : 64);
-        float v[32];
-        unpack_sums(sum[h], v);
 #pragma unroll
-        for (int c = 0; c < 32; ++c) put(sums + (column + c) * 256, v[c], lane < mine_rows);
+        for (int c = 0; c < 32; ++c) put(sums + (column + c) * 256, sum[h][c], lane < mine_rows);
       }
       ok = epilogue_meet(bar, lane, meeting);
       if (!ok) continue;
