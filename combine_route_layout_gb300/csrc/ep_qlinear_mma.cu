@@ -17,7 +17,9 @@
 // A sum changes hands twice a stage (512 cycles of the tensor core), and every look at a
 // shared-memory barrier takes 200 to 250 cycles then. So each CTA makes its own
 // products, and its epilogue hands an accumulator back by a hardware barrier. A pair of
-// CTAs still shares a tile of 256 rows: each loads half of its weights for both.
+// CTAs still shares a tile of 256 rows: each loads half of its weights for both. Groups
+// of at most 128 rows have tiles of twice the features instead, half of them each
+// CTA's, so that experts with a handful of rows keep all SMs reading weights.
 // SwiGLU: half of the tile's columns are gates, half the same features' up values; a
 // thread has both. W is read as it is for dx too: MN-major, a box of 128 terms x 128
 // features.
@@ -53,8 +55,7 @@ constexpr int kScaleGroup = 4;                   // stages whose scales are fetc
 
 struct QPlan {
   int tiles, splits;
-  int width;         // columns of a tile: 256 or 128
-  int f_tiles;       // tiles beside each other
+  int width;         // columns of a CTA's tile: 256 or 128
   int size;          // dense: rows of a tile
 };
 
@@ -85,17 +86,24 @@ struct Barriers {
   uint32_t last;              // this CTA's part of a tile was the last
 };
 
-// Tiles beside each other for `outs` results of a row.
-__host__ __device__ __forceinline__ int tiles_beside(int outs, int width, bool gated) {
-  const int each = gated ? width / 2 : width;
-  return (outs + each - 1) / each;
+// Results of a row that a CTA's tile has.
+__host__ __device__ __forceinline__ int results_in(int width, bool gated) { return gated ? width / 2 : width; }
+
+// Whether a group's tiles are all rows by twice the features.
+__host__ __device__ __forceinline__ bool few_rows(int count) { return count <= kTileRows / 2; }
+
+// Tiles beside each other for `outs` results of a row of a group.
+__host__ __device__ __forceinline__ int tiles_beside(int outs, int width, bool gated, int count,
+                                                     int (*div)(int, int)) {
+  const int each = results_in(width, gated) * (few_rows(count) ? 2 : 1);
+  return div(outs + each - 1, each);
 }
 
 // The groups' segments, the rows of the tiles and the first tile of each group. All
 // threads of the CTA. (A dense product's plan comes from the host.)
 template <bool GATED>
 __device__ QPlan plan_qtiles(const MmaParams& q, int* first, int* begins, int* counts, int* sizes) {
-  __shared__ int sums[kThreads / 32];
+  __shared__ int sums[2][kThreads / 32];
   if (!q.p.s.begin) {
     if (threadIdx.x == 0) {
       first[0] = begins[0] = 0;
@@ -109,42 +117,48 @@ __device__ QPlan plan_qtiles(const MmaParams& q, int* first, int* begins, int* c
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int per = (G + kThreads - 1) / kThreads;
   const int g0 = threadIdx.x * per, g1 = min(G, g0 + per);
-  int mine = 0;                          // tiles above each other
+  int n0 = 0, n1 = 0;                    // tiles of 256 and 128 columns
   for (int g = g0; g < g1; ++g) {
     int64_t b, c;
     segment_of(q.p.s, g, b, c);
     begins[g] = (int)b;
     counts[g] = (int)c;
-    mine += tiles_in((int)c, kTileRows);
+    const int above = tiles_in((int)c, kTileRows);
+    n0 += above * tiles_beside(q.outs, 256, GATED, (int)c, quotient);
+    n1 += above * tiles_beside(q.outs, 128, GATED, (int)c, quotient);
   }
-  int incl = mine;
+  int i0 = n0, i1 = n1;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int v = __shfl_up_sync(kFull, incl, o);
-    if (lane >= o) incl += v;
+    const int v0 = __shfl_up_sync(kFull, i0, o), v1 = __shfl_up_sync(kFull, i1, o);
+    if (lane >= o) {
+      i0 += v0;
+      i1 += v1;
+    }
   }
-  if (lane == 31) sums[warp] = incl;
+  if (lane == 31) {
+    sums[0][warp] = i0;
+    sums[1][warp] = i1;
+  }
   __syncthreads();
-  int all = 0, before = incl - mine;
+  int all0 = 0, all1 = 0;
 #pragma unroll
   for (int w = 0; w < kThreads / 32; ++w) {
-    if (w < warp) before += sums[w];
-    all += sums[w];
+    all0 += sums[0][w];
+    all1 += sums[1][w];
   }
   QPlan plan;
-  plan.width = 256;
-  plan.f_tiles = tiles_beside(q.outs, 256, GATED);
-  if (2 * all * plan.f_tiles <= pairs) {
-    plan.width = 128;
-    plan.f_tiles = tiles_beside(q.outs, 128, GATED);
-  }
-  plan.tiles = all * plan.f_tiles;
+  const int narrow = 2 * all0 <= pairs;
+  plan.width = narrow ? 128 : 256;
+  plan.tiles = narrow ? all1 : all0;
+  int before = narrow ? i1 - n1 : i0 - n0;
+  for (int w = 0; w < warp; ++w) before += sums[narrow][w];
   plan.splits = plan.width == 128 ? splits_for(pairs, plan.tiles, q.stages, kWorth, kLeast) : 1;
   plan.size = 0;
   for (int g = g0; g < g1; ++g) {
-    first[g] = before * plan.f_tiles;
+    first[g] = before;
     sizes[g] = tile_rows(counts[g], kTileRows, quotient);
-    before += quotient(counts[g] + sizes[g] - 1, sizes[g]);
+    before += quotient(counts[g] + sizes[g] - 1, sizes[g]) * tiles_beside(q.outs, plan.width, GATED, counts[g], quotient);
   }
   __syncthreads();
   return plan;
@@ -170,15 +184,17 @@ __device__ __forceinline__ Tile qtile_at(const MmaParams& q, const QPlan& plan, 
   // share operands in L2
   const int size = sizes[lo];
   const int tiles = quotient(count + size - 1, size);
-  const int band = quotient(t, 8 * plan.f_tiles);
+  const int f_tiles = tiles_beside(q.outs, plan.width, GATED, count, quotient);
+  const int band = quotient(t, 8 * f_tiles);
   const int in = min(8, tiles - band * 8);
-  t -= band * 8 * plan.f_tiles;
+  t -= band * 8 * f_tiles;
   const int f = quotient(t, in);
   w.r0 = (band * 8 + t - f * in) * size;
-  w.f0 = f * (GATED ? plan.width / 2 : plan.width);
   w.rows = min(size, count - w.r0);
-  w.n = (w.rows + 63) / 64 * 32;         // rows of the even CTA, the others are the odd one's
-  w.terms = 0;
+  // rows of the even CTA, the others are the odd one's; or all are both's
+  w.n = few_rows(count) ? w.rows : (w.rows + 63) / 64 * 32;
+  w.terms = few_rows(count) ? results_in(plan.width, GATED) : 0;   // to the odd CTA's features
+  w.f0 = f * results_in(plan.width, GATED) * (few_rows(count) ? 2 : 1);
   w.parts = 1;
   w.kb0 = 0;
   w.kb1 = q.stages;
@@ -191,9 +207,19 @@ __device__ __forceinline__ Tile qtile_at(const MmaParams& q, const QPlan& plan, 
   return w;
 }
 
-// Rows of a tile that are this CTA's.
-__device__ __forceinline__ int rows_of(const Tile& w, int cta) {
-  return cta ? w.rows - w.n : min(w.rows, w.n);
+// A CTA's part of a tile: how many rows, the first of them, the first feature.
+struct Share {
+  int rows;
+  int64_t row0;
+  int f0;
+};
+__device__ __forceinline__ Share share_of(const MmaParams& q, const Tile& w, int cta) {
+  Share s;
+  const bool few = w.terms > 0;
+  s.f0 = w.f0 + cta * w.terms;
+  s.rows = s.f0 >= q.outs ? 0 : few || !cta ? min(w.rows, w.n) : w.rows - w.n;
+  s.row0 = w.begin + w.r0 + (few ? 0 : cta * w.n);
+  return s;
 }
 
 __device__ __forceinline__ void store_v8(void* p, const uint32_t (&v)[8]) {
@@ -385,29 +411,43 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         Tile w;
         ok = take_tile(bar, i, w);
         if (!ok) break;
-        const bool some = rows_of(w, cta) > 0;
-        const int row = (int)w.begin + w.r0 + cta * w.n;
+        const Share mine_of = share_of(q, w, cta);
+        const bool some = mine_of.rows > 0, few = w.terms > 0;
+        const int row = (int)mine_of.row0, f = mine_of.f0;
         const int box = w.n > 64 ? 0 : w.n > 32 ? 1 : 2;
-        const uint32_t bytes = (some ? kStageA >> box : 0) + 2 * half_bytes;
-        const CUtensorMap* map_w = &maps.w[plan.width == 256 ? 0 : 1];
+        const uint32_t bytes = (some ? kStageA >> box : 0) + (some || !few ? 2 * half_bytes : 0);
+        const bool wide = plan.width == 256;
+        const CUtensorMap* map_w = &maps.w[wide ? 0 : 1];
         for (int kb = w.kb0; kb < w.kb1; ++kb) {
           if (it >= stages) {
             ok = mbar_wait_soon(&bar->empty[s], phase);
             if (!ok) break;
           }
-          const uint32_t on = full0 + s * 8, a = ring0 + s * stage_bytes;
-          const uint32_t b = a + kStageA + cta * half_bytes;
+          const uint32_t on = full0 + s * 8, a = ring0 + s * stage_bytes, b = a + kStageA;
           mbar_arrive_expect_tx(&bar->full[s], bytes);
           const int d = kb * kDepth;
-          if (MODE == kInputGrad) {
-            const int second = kb >= q.p.Nb;                      // up's half of the terms
-            const int term = d - second * q.p.Nb * kDepth;
-            const bool wide = plan.width == 256;
-            tma_both_4d(b, map_w, w.f0 + (wide ? cta * 128 : 0), term + (wide ? 0 : cta * 64), second, w.g, on);
-          } else if (kGated) {
-            tma_both_4d(b, map_w, d, w.f0, cta, w.g, on);
-          } else {
-            tma_both_4d(b, map_w, d, w.f0 + cta * (plan.width / 2), 0, w.g, on);
+          const int second = MODE == kInputGrad && kb >= q.p.Nb;  // up's half of the terms
+          // half h of the weights: 128 bytes by width / 2
+          const auto half_at = [&](int h, int (&c)[3]) {
+            if (MODE == kInputGrad) {
+              c[0] = f + (wide ? h * 128 : 0);
+              c[1] = d - second * q.p.Nb * kDepth + (wide ? 0 : h * 64);
+              c[2] = second;
+            } else {
+              c[0] = d;
+              c[1] = kGated ? f : f + h * (plan.width / 2);
+              c[2] = kGated ? h : 0;
+            }
+          };
+          int c[3];
+          if (!few) {
+            half_at(cta, c);
+            tma_both_4d(b + cta * half_bytes, map_w, c[0], c[1], c[2], w.g, on);
+          } else if (some) {
+            half_at(0, c);
+            tma_own_4d(b, map_w, c[0], c[1], c[2], w.g, on);
+            half_at(1, c);
+            tma_own_4d(b + half_bytes, map_w, c[0], c[1], c[2], w.g, on);
           }
           if (some) tma_own_2d(a, &maps.rows[box], d, row, on);
           ++it;
@@ -449,7 +489,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         Tile w;
         if (ok) ok = warp_take_tile(bar, i, w, lane);
         if (!ok) w = qtile_at<kGated>(q, plan, first, begins, counts, sizes, pair + i * pairs);
-        const bool some = rows_of(w, cta) > 0;
+        const bool some = share_of(q, w, cta).rows > 0;
         for (int kb = w.kb0; kb < w.kb1; ++kb) {
           if (ok && !__all_sync(kFull, ready)) ok = warp_wait(&bar->full[s], phase);
           if (some && n_acc >= 2) named_sync(1 + (n_acc & 1), kHandover);
@@ -508,11 +548,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       Tile w;
       if (ok) ok = warp_take_tile(bar, i, w, lane);
       if (!ok) w = qtile_at<kGated>(q, plan, first, begins, counts, sizes, u);
-      const int rows = rows_of(w, cta);
-      if (rows <= 0 || w.kb0 >= w.kb1) continue;
-      const int mine_rows = rows - quad * 32;             // from this warp's on
-      const int64_t row0 = w.begin + w.r0 + cta * w.n + quad * 32;
-      const int col0 = w.f0 + turn * (kGated ? plan.width / 4 : plan.width / 2);
+      const Share share = share_of(q, w, cta);
+      if (share.rows <= 0 || w.kb0 >= w.kb1) continue;
+      const int mine_rows = share.rows - quad * 32;       // from this warp's on
+      const int64_t row0 = share.row0 + quad * 32;
+      const int col0 = share.f0 + turn * (kGated ? plan.width / 4 : plan.width / 2);
       // this lane's scales and its features', kScaleGroup stages ahead
       const float* row_scales = q.row_scale + (row0 + min(lane, max(mine_rows, 1) - 1)) * q.row_ld;
       const float* w_scales = q.p.ws + w.g * q.group_ld +
@@ -668,19 +708,20 @@ cudaError_t launch_forward(const Maps& m, MmaParams& q, int grid, cudaStream_t s
 int plan_grid(MmaParams& q, bool gated, int sms) {
   const LinearSegs& s = q.p.s;
   const int64_t rows = s.begin ? s.pool : s.dense_rows;
-  const int narrow = tiles_beside(q.outs, 128, gated), parts = q.stages / kLeast;
-  const int64_t most = (rows / kTileRows + s.G) * narrow * (parts < 1 ? 1 : parts < kMaxSplits ? parts : kMaxSplits);
+  const int each = results_in(128, gated), parts = q.stages / kLeast;
+  const int64_t most = (rows / kTileRows + s.G) * ((q.outs + each - 1) / each) *
+                       (parts < 1 ? 1 : parts < kMaxSplits ? parts : kMaxSplits);
   const int grid = grid_of(sms, most), pairs = grid / 2;
   QPlan& plan = q.plan;
-  plan.size = tile_rows((int)s.dense_rows, kTileRows, host_quotient);
-  const int above = (int)((s.dense_rows + plan.size - 1) / plan.size);
+  const int dense = (int)s.dense_rows;
+  plan.size = tile_rows(dense, kTileRows, host_quotient);
+  const int above = (dense + plan.size - 1) / plan.size;
   plan.width = 256;
-  plan.f_tiles = tiles_beside(q.outs, 256, gated);
-  if (2 * (int64_t)above * plan.f_tiles <= pairs) {
+  plan.tiles = above * tiles_beside(q.outs, 256, gated, dense, host_quotient);
+  if (2 * plan.tiles <= pairs) {
     plan.width = 128;
-    plan.f_tiles = narrow;
+    plan.tiles = above * tiles_beside(q.outs, 128, gated, dense, host_quotient);
   }
-  plan.tiles = above * plan.f_tiles;
   plan.splits = plan.width == 128 ? splits_for(pairs, plan.tiles, q.stages, kWorth, kLeast) : 1;
   return grid;
 }
