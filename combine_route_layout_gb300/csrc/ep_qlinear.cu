@@ -338,6 +338,7 @@ extern "C" ep_status ep_qlinear_forward(ep_qlinear_handle* h, const void* x, con
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   if ((s = qlinear_ready(h, st)) != EP_OK) return s;
   if (!row_begin && num_rows == 0) return EP_OK;
+  if (few_qrows_supported(p)) return qlstatus(launch_qlinear_few_rows(p, h->sm_count, st));
   return qlstatus(launch_qlinear_forward(p, h->sm_count, st));
 }
 

@@ -37,6 +37,9 @@ struct QLinearParams {
 // The products (ep_qlinear_mma.cu), over `sms` multiprocessors.
 cudaError_t launch_qlinear_forward(const QLinearParams& p, int sms, cudaStream_t st);
 cudaError_t launch_qlinear_input_grad(const QLinearParams& p, int sms, cudaStream_t st);
+// The forward for at most kFewRows dense rows (ep_qlinear_rows.cu).
+bool few_qrows_supported(const QLinearParams& p);
+cudaError_t launch_qlinear_few_rows(const QLinearParams& p, int sms, cudaStream_t st);
 
 // Rows of codes with scales to bf16 (ep_quant.cu).
 cudaError_t launch_dequantize(const LinearSegs& s, const uint8_t* codes, const float* scales, int K,

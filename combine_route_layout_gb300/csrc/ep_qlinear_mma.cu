@@ -312,6 +312,9 @@ __device__ __forceinline__ void finish(const MmaParams& q, float* room, int g, i
   const float b = bias && in ? bias[lane] : 0.0f, b_up = kGated && bias && in ? bias[p.N + lane] : 0.0f;
   for (int r0 = 0; r0 < 32; r0 += kTurnRows) {
     if (r0 >= rows) break;
+    float add[kTurnRows];                // all of the residual's loads ahead of the stores
+#pragma unroll
+    for (int r = 0; r < kTurnRows; ++r) add[r] = res ? get(res + (int64_t)(r0 + r) * q.outs + lane, in && r0 + r < rows) : 0.0f;
     __syncwarp();
     if (lane / kTurnRows == r0 / kTurnRows) {
       float* to = room + (lane % kTurnRows) * kTurnPitch;
@@ -335,8 +338,7 @@ __device__ __forceinline__ void finish(const MmaParams& q, float* room, int g, i
       } else if (MODE == kForward) {
         v = act_of(ACT, v);
       }
-      if (res) v += get(res + row * q.outs + lane, on);
-      put(y + row * q.outs + lane, v, on);
+      put(y + row * q.outs + lane, v + add[r], on);
     }
   }
   __syncwarp();
