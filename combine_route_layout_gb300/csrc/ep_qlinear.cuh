@@ -37,7 +37,8 @@ struct QLinearParams {
 // The products (ep_qlinear_mma.cu), over `sms` multiprocessors.
 cudaError_t launch_qlinear_forward(const QLinearParams& p, int sms, cudaStream_t st);
 cudaError_t launch_qlinear_input_grad(const QLinearParams& p, int sms, cudaStream_t st);
-// The forward for at most kFewRows dense rows (ep_qlinear_rows.cu).
+// The forward for at most kFewQRows dense rows (ep_qlinear_rows.cu).
+constexpr int kFewQRows = 8;
 bool few_qrows_supported(const QLinearParams& p);
 cudaError_t launch_qlinear_few_rows(const QLinearParams& p, int sms, cudaStream_t st);
 

@@ -65,6 +65,7 @@ struct MmaParams {
   int outs;                // length of its rows
   int stages;              // of a contraction
   int vec;                 // rows and tensors allow 32-byte accesses
+  int pairs;               // of multiprocessors: the grid has fewer where units are
   QPlan plan;              // of a dense product
   // scale of (pool row, block) and of (group, feature block, block)
   const float* row_scale;
@@ -113,7 +114,7 @@ __device__ QPlan plan_qtiles(const MmaParams& q, int* first, int* begins, int* c
     __syncthreads();
     return q.plan;
   }
-  const int G = q.p.s.G, pairs = gridDim.x >> 1;
+  const int G = q.p.s.G, pairs = q.pairs;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int per = (G + kThreads - 1) / kThreads;
   const int g0 = threadIdx.x * per, g1 = min(G, g0 + per);
@@ -153,7 +154,8 @@ __device__ QPlan plan_qtiles(const MmaParams& q, int* first, int* begins, int* c
   plan.tiles = narrow ? all1 : all0;
   int before = narrow ? i1 - n1 : i0 - n0;
   for (int w = 0; w < warp; ++w) before += sums[narrow][w];
-  plan.splits = plan.width == 128 ? splits_for(pairs, plan.tiles, q.stages, kWorth, kLeast) : 1;
+  // no more units than the grid has pairs: each has one place for sums of parts
+  plan.splits = plan.width == 128 ? splits_for(gridDim.x >> 1, plan.tiles, q.stages, kWorth, kLeast) : 1;
   plan.size = 0;
   for (int g = g0; g < g1; ++g) {
     first[g] = before;
@@ -325,20 +327,23 @@ __device__ __forceinline__ void finish(const MmaParams& q, float* room, int g, i
       }
     }
     __syncwarp();
+    float v[kTurnRows], u[kTurnRows];
 #pragma unroll
     for (int r = 0; r < kTurnRows; ++r) {
-      const int64_t row = r0 + r;
-      const bool on = in && row < rows;
-      float v = room[r * kTurnPitch + lane] + b;
-      if (zp) put(zp + row * p.Nw + lane, v, on);
-      if (kGated) {
-        const float u = room[(kTurnRows + r) * kTurnPitch + lane] + b_up;
-        if (zp) put(zp + row * p.Nw + p.N + lane, u, on);
-        v = silu_of(v) * u;
-      } else if (MODE == kForward) {
-        v = act_of(ACT, v);
+      v[r] = room[r * kTurnPitch + lane] + b;
+      u[r] = kGated ? room[(kTurnRows + r) * kTurnPitch + lane] + b_up : 0.0f;
+    }
+    if (zp) {
+#pragma unroll
+      for (int r = 0; r < kTurnRows; ++r) {
+        put(zp + (int64_t)(r0 + r) * p.Nw + lane, v[r], in && r0 + r < rows);
+        if (kGated) put(zp + (int64_t)(r0 + r) * p.Nw + p.N + lane, u[r], in && r0 + r < rows);
       }
-      put(y + row * q.outs + lane, v + add[r], on);
+    }
+#pragma unroll
+    for (int r = 0; r < kTurnRows; ++r) {
+      if (MODE == kForward) v[r] = kGated ? silu_of(v[r]) * u[r] : act_of(ACT, v[r]);
+      put(y + (int64_t)(r0 + r) * q.outs + lane, v[r] + add[r], in && r0 + r < rows);
     }
   }
   __syncwarp();
@@ -713,7 +718,8 @@ int plan_grid(MmaParams& q, bool gated, int sms) {
   const int each = results_in(128, gated), parts = q.stages / kLeast;
   const int64_t most = (rows / kTileRows + s.G) * ((q.outs + each - 1) / each) *
                        (parts < 1 ? 1 : parts < kMaxSplits ? parts : kMaxSplits);
-  const int grid = grid_of(sms, most), pairs = grid / 2;
+  const int grid = grid_of(sms, most), pairs = grid_of(sms, INT_MAX) / 2;
+  q.pairs = pairs;
   QPlan& plan = q.plan;
   const int dense = (int)s.dense_rows;
   plan.size = tile_rows(dense, kTileRows, host_quotient);
@@ -724,7 +730,7 @@ int plan_grid(MmaParams& q, bool gated, int sms) {
     plan.width = 128;
     plan.tiles = above * tiles_beside(q.outs, 128, gated, dense, host_quotient);
   }
-  plan.splits = plan.width == 128 ? splits_for(pairs, plan.tiles, q.stages, kWorth, kLeast) : 1;
+  plan.splits = plan.width == 128 ? splits_for(grid / 2, plan.tiles, q.stages, kWorth, kLeast) : 1;
   return grid;
 }
 

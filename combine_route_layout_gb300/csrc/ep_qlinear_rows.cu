@@ -1,172 +1,149 @@
-// The forward product of block-quantised operands for a handful of dense rows (single
-// tokens), bound by reading W once.
+// The forward product of block-quantised operands for up to eight dense rows (single
+// tokens, a few of them), bound by reading W once.
 //
-// As ep_linear_rows.cu for bf16: a warp takes FEATURES weight rows (gated: gate rows and
-// their up rows) and all R rows of x, a lane 16 neighbouring codes of every 512, 16 bytes
-// a load, kUnroll loads of each weight row ahead of the arithmetic. A lane's 16 codes are
-// of one scale block, so their products are summed up first, in f32, and take both
-// scales at once. Where the features are too few to fill the GPU with warps, `split`
-// warps of a CTA share them, each with its part of the terms.
+// A warp takes 16 weight rows (gated: 8 gate rows and their up rows) and all rows of x,
+// and lets the warp-wide 16 x 8 x 32 product of E4M3 do the arithmetic: with a
+// conversion and a multiply-add for each code a single row of 4096 x 32768 takes 39 us.
+// Which term a place of a fragment stands for is free, as long as both operands agree: a
+// lane loads 16 neighbouring codes of weight rows t / 4 and t / 4 + 8 and of row t / 4 of
+// x, and these are the two steps' fragments of 64 terms as they come. The four products of
+// a scale block are added up by the tensor core, blocks in f32 with both scales. Where the
+// features are too few to fill the GPU with warps, `split` warps of a CTA share them, each
+// with its part of the blocks, and their sums are added in their order.
 #include "ep_launch.cuh"
 #include "ep_qlinear.cuh"
-#include "ep_quant.cuh"
 
 namespace ep {
 namespace {
 
 constexpr int kWarps = 8;
-constexpr int kStep = 512;     // terms that a warp takes at once
+constexpr int kTile = 16;      // weight rows of a warp
+constexpr int kAhead = 2;      // blocks of 128 terms that a warp has on their way
 
-__device__ __forceinline__ void values16(const uint4& q, float (&v)[16]) {
-  float a[8], b[8];
-  e4m3x8_values(make_uint2(q.x, q.y), a);
-  e4m3x8_values(make_uint2(q.z, q.w), b);
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    v[i] = a[i];
-    v[8 + i] = b[i];
-  }
+__device__ __forceinline__ void mma_16x8x32(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                            uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-template <int R, int FEATURES, bool GATED>
+template <bool GATED>
 __global__ void __launch_bounds__(kWarps * 32) few_rows8_kernel(QLinearParams p, int split) {
   begin_overlapped();
-  constexpr int kUnroll = R * FEATURES > 2 ? 2 : 4;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  __shared__ float joined[kWarps][FEATURES * R];
+  const int quad = lane >> 2, sub = lane & 3;
+  __shared__ float joined[kWarps][32][4];
   const int part = warp % split;
-  const int64_t first = ((int64_t)blockIdx.x * kWarps + warp) / split * (GATED ? FEATURES / 2 : FEATURES);
-  // weight rows of this warp; those past the last one repeat it and are not stored
-  const uint8_t* w[FEATURES];
-  const float* ws[FEATURES];
-#pragma unroll
-  for (int f = 0; f < FEATURES; ++f) {
-    const int64_t n = min(first + (GATED ? f / 2 : f), (int64_t)p.N - 1);
-    const int up = GATED ? f & 1 : 0;
-    w[f] = p.w + (n + up * (int64_t)p.N) * p.K;
-    ws[f] = p.ws + (up * p.Nb + n / 128) * p.Kb;
-  }
+  const int64_t first = ((int64_t)blockIdx.x * kWarps + warp) / split * (GATED ? kTile / 2 : kTile);
+  // weight rows of this lane; those past the last one repeat it and are not stored
+  const int64_t n0 = min(first + quad, (int64_t)p.N - 1);
+  const int64_t n1 = GATED ? n0 + p.N : min(first + quad + 8, (int64_t)p.N - 1);
+  const uint8_t* w0 = p.w + n0 * p.K + sub * 16;
+  const uint8_t* w1 = p.w + n1 * p.K + sub * 16;
+  const float* s0 = p.ws + n0 / 128 * p.Kb;
+  const float* s1 = p.ws + (GATED ? p.Nb + n0 / 128 : n1 / 128) * p.Kb;
   const int rows = (int)p.s.dense_rows;
-  float acc[FEATURES][R];
-#pragma unroll
-  for (int f = 0; f < FEATURES; ++f)
-#pragma unroll
-    for (int r = 0; r < R; ++r) acc[f][r] = 0.0f;
-  auto add = [&](int k, const uint4 (&q)[FEATURES], const float (&sw)[FEATURES]) {
-    float a[FEATURES][16];
-#pragma unroll
-    for (int f = 0; f < FEATURES; ++f) values16(q[f], a[f]);
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-      if (r >= rows) break;
-      float x[16];
-      values16(*reinterpret_cast<const uint4*>(p.x + (int64_t)r * p.K + k), x);
-      const float sx = p.xs[(int64_t)r * p.Kb + k / 128];
-#pragma unroll
-      for (int f = 0; f < FEATURES; ++f) {
-        float sum = 0.0f;
-#pragma unroll
-        for (int i = 0; i < 16; ++i) sum = fmaf(a[f][i], x[i], sum);
-        acc[f][r] = fmaf(sum, sx * sw[f], acc[f][r]);
-      }
-    }
+  const bool has_row = quad < rows;
+  const uint8_t* x = p.x + (int64_t)(has_row ? quad : 0) * p.K + sub * 16;
+  // the results' rows of x: 2 sub and 2 sub + 1
+  const float* sx0 = p.xs + (int64_t)min(2 * sub, rows - 1) * p.Kb;
+  const float* sx1 = p.xs + (int64_t)min(2 * sub + 1, rows - 1) * p.Kb;
+  float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  struct Block {
+    uint4 a0[2], a1[2], b[2];
+    float w0, w1, x0, x1;
   };
-  // this warp's blocks of kStep terms: part, part + split, ...
-  const int step = split * kStep;
-  int k = part * kStep + lane * 16;
-  for (; k + (kUnroll - 1) * step < p.K; k += kUnroll * step) {
-    uint4 q[kUnroll][FEATURES];
-    float sw[kUnroll][FEATURES];
+  Block q[kAhead];
+  const uint4 none = make_uint4(0, 0, 0, 0);
+  auto fetch = [&](int kb, Block& t) {
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u)
+    for (int h = 0; h < 2; ++h) {
+      const int k = kb * 128 + h * 64;
+      const bool in = kb < p.Kb && k + sub * 16 < p.K;
+      t.a0[h] = in ? ld_once_v4(w0 + k) : none;
+      t.a1[h] = in ? ld_once_v4(w1 + k) : none;
+      t.b[h] = in && has_row ? *reinterpret_cast<const uint4*>(x + k) : none;
+    }
+    const bool in = kb < p.Kb;
+    t.w0 = in ? s0[kb] : 0.0f;
+    t.w1 = in ? s1[kb] : 0.0f;
+    t.x0 = in ? sx0[kb] : 0.0f;
+    t.x1 = in ? sx1[kb] : 0.0f;
+  };
+  // this warp's blocks: part, part + split, ...
 #pragma unroll
-      for (int f = 0; f < FEATURES; ++f) {
-        q[u][f] = ld_once_v4(w[f] + k + u * step);
-        sw[u][f] = ws[f][(k + u * step) / 128];
+  for (int i = 0; i < kAhead; ++i) fetch(part + i * split, q[i]);
+  for (int kb = part; kb < p.Kb; kb += kAhead * split) {
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const Block t = q[i];
+      fetch(kb + (kAhead + i) * split, q[i]);
+      float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        mma_16x8x32(d, t.a0[h].x, t.a1[h].x, t.a0[h].y, t.a1[h].y, t.b[h].x, t.b[h].y);
+        mma_16x8x32(d, t.a0[h].z, t.a1[h].z, t.a0[h].w, t.a1[h].w, t.b[h].z, t.b[h].w);
       }
-#pragma unroll
-    for (int u = 0; u < kUnroll; ++u) add(k + u * step, q[u], sw[u]);
-  }
-  for (; k < p.K; k += step) {
-    uint4 q[FEATURES];
-    float sw[FEATURES];
-#pragma unroll
-    for (int f = 0; f < FEATURES; ++f) {
-      q[f] = ld_once_v4(w[f] + k);
-      sw[f] = ws[f][k / 128];
+      if (kb + i * split < p.Kb) {
+        acc[0] = fmaf(d[0], t.w0 * t.x0, acc[0]);
+        acc[1] = fmaf(d[1], t.w0 * t.x1, acc[1]);
+        acc[2] = fmaf(d[2], t.w1 * t.x0, acc[2]);
+        acc[3] = fmaf(d[3], t.w1 * t.x1, acc[3]);
+      }
     }
-    add(k, q, sw);
   }
-#pragma unroll
-  for (int f = 0; f < FEATURES; ++f)
-#pragma unroll
-    for (int r = 0; r < R; ++r)
-#pragma unroll
-      for (int o = 16; o; o >>= 1) acc[f][r] += __shfl_xor_sync(kFull, acc[f][r], o);
   if (split > 1) {   // the first warp of each share adds the others' sums, in their order
-    if (lane == 0) {
 #pragma unroll
-      for (int f = 0; f < FEATURES; ++f)
-#pragma unroll
-        for (int r = 0; r < R; ++r) joined[warp][f * R + r] = acc[f][r];
-    }
+    for (int i = 0; i < 4; ++i) joined[warp][lane][i] = acc[i];
     __syncthreads();
     if (part != 0) return;
-    for (int i = 1; i < split; ++i)
+    for (int o = 1; o < split; ++o)
 #pragma unroll
-      for (int f = 0; f < FEATURES; ++f)
-#pragma unroll
-        for (int r = 0; r < R; ++r) acc[f][r] += joined[warp + i][f * R + r];
+      for (int i = 0; i < 4; ++i) acc[i] += joined[warp + o][lane][i];
   }
-  // lane r x outputs + f finishes output f of row r
-  constexpr int kOut = GATED ? FEATURES / 2 : FEATURES;
+  // acc: features n0 of rows 2 sub, 2 sub + 1, then n1 of the same
 #pragma unroll
-  for (int f = 0; f < kOut; ++f)
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-      const int64_t n = first + f;
-      if (lane != r * kOut + f || r >= rows || n >= p.N) continue;
-      float z = acc[GATED ? 2 * f : f][r], y;
-      if (p.bias) z += p.bias[n];
-      if (GATED) {
-        float up = acc[(2 * f + 1) % FEATURES][r];
-        if (p.bias) up += p.bias[p.N + n];
-        if (p.z) p.z[(int64_t)r * p.Nw + p.N + n] = __float2bfloat16_rn(up);
-        y = silu_of(z) * up;
-      } else {
-        y = act_of(p.act, z);
-      }
-      if (p.z) p.z[(int64_t)r * p.Nw + n] = __float2bfloat16_rn(z);
-      const int64_t o = (int64_t)r * p.N + n;
-      if (p.y_f32) {
-        if (p.residual) y += static_cast<const float*>(p.residual)[o];
-        static_cast<float*>(p.y)[o] = y;
-      } else {
-        if (p.residual) y += __bfloat162float(static_cast<const __nv_bfloat16*>(p.residual)[o]);
-        static_cast<__nv_bfloat16*>(p.y)[o] = __float2bfloat16_rn(y);
-      }
+  for (int i = 0; i < (GATED ? 2 : 4); ++i) {
+    const int r = 2 * sub + (i & 1);
+    const int64_t n = first + quad + (i >> 1) * 8;
+    if (r >= rows || n >= p.N) continue;
+    float z = acc[i], y;
+    if (p.bias) z += p.bias[n];
+    if (GATED) {
+      float up = acc[(i + 2) & 3];
+      if (p.bias) up += p.bias[p.N + n];
+      if (p.z) p.z[(int64_t)r * p.Nw + p.N + n] = __float2bfloat16_rn(up);
+      y = silu_of(z) * up;
+    } else {
+      y = act_of(p.act, z);
     }
-}
-
-template <int R, int FEATURES, bool GATED>
-cudaError_t launch(const QLinearParams& p, int sms, cudaStream_t st) {
-  const int64_t outs = GATED ? FEATURES / 2 : FEATURES;
-  const int64_t shares = (p.N + outs - 1) / outs;
-  // 24 warps an SM keep HBM busy; a warp should have a block of terms at least
-  int split = 1;
-  while (split < kWarps && shares * split < (int64_t)sms * 24 && split * kStep < p.K) split *= 2;
-  const int64_t ctas = (shares * split + kWarps - 1) / kWarps;
-  return launch_overlapped(few_rows8_kernel<R, FEATURES, GATED>, dim3((unsigned)ctas), kWarps * 32, 0, st, p, split);
+    if (p.z) p.z[(int64_t)r * p.Nw + n] = __float2bfloat16_rn(z);
+    const int64_t o = (int64_t)r * p.N + n;
+    if (p.y_f32) {
+      if (p.residual) y += static_cast<const float*>(p.residual)[o];
+      static_cast<float*>(p.y)[o] = y;
+    } else {
+      if (p.residual) y += __bfloat162float(static_cast<const __nv_bfloat16*>(p.residual)[o]);
+      static_cast<__nv_bfloat16*>(p.y)[o] = __float2bfloat16_rn(y);
+    }
+  }
 }
 
 }  // namespace
 
-bool few_qrows_supported(const QLinearParams& p) { return !p.s.begin && p.s.dense_rows <= kFewRows; }
+bool few_qrows_supported(const QLinearParams& p) { return !p.s.begin && p.s.dense_rows <= kFewQRows; }
 
 cudaError_t launch_qlinear_few_rows(const QLinearParams& p, int sms, cudaStream_t st) {
   const bool gated = p.act == EP_ACT_SWIGLU;
-  if (p.s.dense_rows == 1) return gated ? launch<1, 2, true>(p, sms, st) : launch<1, 1, false>(p, sms, st);
-  return gated ? launch<2, 2, true>(p, sms, st) : launch<2, 2, false>(p, sms, st);
+  const int64_t outs = gated ? kTile / 2 : kTile, shares = (p.N + outs - 1) / outs;
+  // 24 warps an SM keep HBM busy; a warp should have a block of terms at least
+  int split = 1;
+  while (split < kWarps && shares * split < (int64_t)sms * 24 && split < p.Kb) split *= 2;
+  const int64_t ctas = (shares * split + kWarps - 1) / kWarps;
+  return launch_overlapped(gated ? few_rows8_kernel<true> : few_rows8_kernel<false>, dim3((unsigned)ctas),
+                           kWarps * 32, 0, st, p, split);
 }
 
 }  // namespace ep

@@ -288,6 +288,10 @@ SHAPES = [
     dict(counts=[40] * 20, k=512, n=384, pad=0),
     dict(counts=[0, 0, 0], k=128, n=64),
     dict(counts=[700, 1, 0, 31], k=640, n=128, base=2),
+    dict(counts=[8], k=2000, n=333, dense=True),
+    dict(counts=[5], k=128 * 40, n=17, dense=True),
+    dict(counts=[9], k=400, n=272, dense=True),
+    dict(counts=[128, 129, 64, 0, 97, 33], k=384, n=520),
 ]
 
 
