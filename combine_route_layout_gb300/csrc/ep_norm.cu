@@ -8,13 +8,15 @@
 //
 // Backward: a CTA walks rows, thread t always at the same columns, whose sums over
 // rows stay in registers; the CTAs' sums are added in their order by
-// norm_sums_kernel.
+// norm_sums_kernel. Rows come by bulk copies into a ring of shared memory, the next
+// ones under the arithmetic of this one, which has two meetings of the CTA a row.
 #include <climits>
 #include <cstring>
 #include <new>
 
 #include <cuda_bf16.h>
 
+#include "ep_bulk.cuh"
 #include "ep_header.cuh"
 #include "ep_launch.cuh"
 #include "ep_pieces.cuh"
@@ -22,6 +24,10 @@
 
 namespace ep {
 namespace {
+
+constexpr int kRingRows = 4;              // rows of the backward pass on their way, at most
+constexpr int kMaxGradCtas = 320;
+constexpr int kErrNormTimeout = 1;
 
 struct NormParams {
   int64_t rows;
@@ -46,7 +52,8 @@ struct NormParams {
   float* part;                  // [CTAs][sums][H]
   int n_sums;                   // of w, w_post, gate of features
   float* sums[3];
-  int ctas;
+  int ctas, ring_rows;
+  int32_t* err;
 };
 
 // The sum over the CTA, the same in every thread: warps by shuffles, then their sums
@@ -60,6 +67,26 @@ __device__ __forceinline__ float cta_sum(float v, float* room) {
   v = 0.0f;
   for (int w = 0; w < warps; ++w) v += room[w];
   return v;
+}
+
+// Two sums at once, in place.
+__device__ __forceinline__ void cta_sums(float& a, float& b, float* room_a, float* room_b) {
+#pragma unroll
+  for (int o = 16; o; o >>= 1) {
+    a += __shfl_xor_sync(kFull, a, o);
+    b += __shfl_xor_sync(kFull, b, o);
+  }
+  if ((threadIdx.x & 31) == 0) {
+    room_a[threadIdx.x >> 5] = a;
+    room_b[threadIdx.x >> 5] = b;
+  }
+  __syncthreads();
+  const int warps = blockDim.x >> 5;
+  a = b = 0.0f;
+  for (int w = 0; w < warps; ++w) {
+    a += room_a[w];
+    b += room_b[w];
+  }
 }
 
 // 1 / sqrt(v), rounded within a step of f32; 0 for an infinite v.
@@ -144,7 +171,7 @@ __global__ void __launch_bounds__(VECS == 1 ? 1024 : 512) norm_kernel(NormParams
       if (in[i]) store8<__nv_bfloat16>(p.out, base + at, w);
     } else {   // 16 neighbouring lanes hold a block of 128
       const float amax = max16(amax8(w));
-      const float scale = __fdiv_rn(amax, 448.0f);
+      const float scale = scale_of(amax);
       const uint2 q = e4m3x8(w, block_scale(amax, scale));
       if (in[i]) {
         *reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.out) + base + at) = q;
@@ -154,45 +181,76 @@ __global__ void __launch_bounds__(VECS == 1 ? 1024 : 512) norm_kernel(NormParams
   }
 }
 
+// Where a row's tensors lie in a place of the ring.
+struct RowPlace {
+  int stream, d_stream, block, bytes;     // the gradient of out comes first
+};
+template <typename S, typename B>
+__host__ __device__ __forceinline__ RowPlace row_place(int H, bool has_d_stream, bool has_block) {
+  RowPlace p;
+  p.stream = H * 2;
+  p.d_stream = p.stream + H * (int)sizeof(S);
+  p.block = p.d_stream + (has_d_stream ? H * (int)sizeof(S) : 0);
+  p.bytes = p.block + (has_block ? H * (int)sizeof(B) : 0);
+  return p;
+}
+
+template <typename T>
+__device__ __forceinline__ void floats_at(const uint8_t* row, int at, float (&f)[8]) {
+  const uint4* p = reinterpret_cast<const uint4*>(row + (size_t)at * sizeof(T));
+  Raw8<T> r;
+#pragma unroll
+  for (int i = 0; i < (int)(sizeof(T) / 2); ++i) r.v[i] = p[i];
+  floats8(r, f);
+}
+
 template <typename S, typename B, int VECS>
 __global__ void __launch_bounds__(512) norm_grad_kernel(NormParams p) {
-  begin_overlapped();
+  extern __shared__ __align__(16) uint8_t ring[];
   __shared__ float room[4][32];
+  __shared__ uint64_t landed[kRingRows];
   const int T = blockDim.x;
   const bool has_block = p.block != nullptr;
+  const RowPlace place = row_place<S, B>(p.H, p.d_stream != nullptr, has_block);
+  if (threadIdx.x < kRingRows) mbar_init(&landed[threadIdx.x], 1);
+  if (threadIdx.x == 0) mbar_init_fence();
+  __syncthreads();
+  begin_overlapped();
+  const auto fetch = [&](int64_t row, int slot) {      // one thread
+    uint8_t* to = ring + (size_t)slot * place.bytes;
+    mbar_arrive_expect_tx(&landed[slot], (uint32_t)place.bytes);
+    bulk_g2s(to, static_cast<const __nv_bfloat16*>(p.dout) + row * p.H, p.H * 2, &landed[slot]);
+    bulk_g2s(to + place.stream, static_cast<const S*>(p.stream) + row * p.H, p.H * (uint32_t)sizeof(S), &landed[slot]);
+    if (p.d_stream)
+      bulk_g2s(to + place.d_stream, static_cast<const S*>(p.d_stream) + row * p.H, p.H * (uint32_t)sizeof(S), &landed[slot]);
+    if (has_block)
+      bulk_g2s(to + place.block, static_cast<const B*>(p.block) + row * p.H, p.H * (uint32_t)sizeof(B), &landed[slot]);
+  };
+  if (threadIdx.x == 0)
+    for (int i = 0; i < p.ring_rows && blockIdx.x + (int64_t)i * gridDim.x < p.rows; ++i)
+      fetch(blockIdx.x + (int64_t)i * gridDim.x, i);
   float dw[VECS][8], dp[VECS][8], dg[VECS][8];
 #pragma unroll
   for (int i = 0; i < VECS; ++i)
 #pragma unroll
     for (int j = 0; j < 8; ++j) dw[i][j] = dp[i][j] = dg[i][j] = 0.0f;
+  int slot = 0;
+  uint32_t phase = 0;
   for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
     const int64_t base = row * p.H;
-    Raw8<__nv_bfloat16> rd[VECS];
-    Raw8<S> rt[VECS], rs[VECS];
-    Raw8<B> rb[VECS];
+    const uint8_t* here = ring + (size_t)slot * place.bytes;
     const float by = p.stats[2 * row], by_block = p.stats[2 * row + 1];
-#pragma unroll
-    for (int i = 0; i < VECS; ++i) {
-      const int piece = threadIdx.x + i * T;
-      zero8(rd[i]);
-      zero8(rt[i]);
-      zero8(rs[i]);
-      zero8(rb[i]);
-      if (piece < p.pieces) {
-        load8<__nv_bfloat16>(p.dout, base + piece * 8, rd[i]);
-        load8<S>(p.stream, base + piece * 8, rs[i]);
-        if (p.d_stream) load8<S>(p.d_stream, base + piece * 8, rt[i]);
-        if (has_block) load8<B>(p.block, base + piece * 8, rb[i]);
-      }
-    }
+    float times = p.alpha;
+    if (has_block && p.gate == EP_GATE_TOKEN) times *= p.gates[row];
+    if (!mbar_wait(&landed[slot], phase) && threadIdx.x == 0) atomicOr(p.err, kErrNormTimeout);
     float sum = 0.0f;
 #pragma unroll
     for (int i = 0; i < VECS; ++i) {
       const int at = (threadIdx.x + i * T) * 8;
       if (at >= p.H) continue;
       float d[8], s[8], w[8];
-      floats8(rd[i], d);
-      floats8(rs[i], s);
+      floats_at<__nv_bfloat16>(here, at, d);
+      floats_at<S>(here + place.stream, at, s);
       weights8(p.w, at, w);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
@@ -202,8 +260,6 @@ __global__ void __launch_bounds__(512) norm_grad_kernel(NormParams p) {
       }
     }
     const float mean = cta_sum(sum, room[0]) * p.inv;
-    float times = p.alpha;
-    if (has_block && p.gate == EP_GATE_TOKEN) times *= p.gates[row];
     float dot_gate = 0.0f, dot_post = 0.0f;
     float t[VECS][8];
 #pragma unroll
@@ -211,16 +267,21 @@ __global__ void __launch_bounds__(512) norm_grad_kernel(NormParams p) {
       const int at = (threadIdx.x + i * T) * 8;
       if (at >= p.H) continue;
       float d[8], s[8], w[8];
-      floats8(rd[i], d);
-      floats8(rs[i], s);
-      floats8(rt[i], t[i]);
+      floats_at<__nv_bfloat16>(here, at, d);
+      floats_at<S>(here + place.stream, at, s);
+      if (p.d_stream) {
+        floats_at<S>(here + place.d_stream, at, t[i]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) t[i][j] = 0.0f;
+      }
       weights8(p.w, at, w);
 #pragma unroll
       for (int j = 0; j < 8; ++j) t[i][j] = fmaf(by, d[j] * w[j] - s[j] * by * mean, t[i][j]);
       store8<S>(p.d_residual, base + at, t[i]);
       if (!has_block) continue;
       float y[8], wp[8], g[8];
-      floats8(rb[i], y);
+      floats_at<B>(here + place.block, at, y);
       if (p.post) weights8(p.w_post, at, wp);
       if (p.gate == EP_GATE_FEATURE) weights8(p.gates, at, g);
 #pragma unroll
@@ -238,24 +299,31 @@ __global__ void __launch_bounds__(512) norm_grad_kernel(NormParams p) {
       }
       if (!p.post) store8<B>(p.d_block, base + at, t[i]);
     }
-    if (has_block && p.gate == EP_GATE_TOKEN) {
-      const float v = cta_sum(dot_gate, room[1]);
-      if (threadIdx.x == 0) p.d_gate[row] = p.alpha * v;
+    // both sums in one meeting
+    if (has_block && (p.post || p.gate == EP_GATE_TOKEN)) {
+      cta_sums(dot_gate, dot_post, room[1], room[2]);
+      if (p.gate == EP_GATE_TOKEN && threadIdx.x == 0) p.d_gate[row] = p.alpha * dot_gate;
     }
     if (has_block && p.post) {
-      const float mean_post = cta_sum(dot_post, room[2]) * p.inv;
+      const float mean_post = dot_post * p.inv;
 #pragma unroll
       for (int i = 0; i < VECS; ++i) {
         const int at = (threadIdx.x + i * T) * 8;
         if (at >= p.H) continue;
         float y[8];
-        floats8(rb[i], y);
+        floats_at<B>(here + place.block, at, y);
 #pragma unroll
         for (int j = 0; j < 8; ++j) t[i][j] = by_block * (t[i][j] - y[j] * by_block * mean_post);
         store8<B>(p.d_block, base + at, t[i]);
       }
     }
-    __syncthreads();   // `room` is written anew
+    __syncthreads();   // the row has been read, and `room` is written anew
+    const int64_t next = row + (int64_t)p.ring_rows * gridDim.x;
+    if (threadIdx.x == 0 && next < p.rows) fetch(next, slot);
+    if (++slot == p.ring_rows) {
+      slot = 0;
+      phase ^= 1;
+    }
   }
   float* part = p.part + (int64_t)blockIdx.x * p.n_sums * p.H;
 #pragma unroll
@@ -307,17 +375,34 @@ cudaError_t launch_norm(const NormParams& p, int sms, cudaStream_t st) {
   return launch_overlapped(kernel, dim3((unsigned)p.rows), threads, 0, st, p);
 }
 
+template <typename S, typename B, int VECS>
+cudaError_t launch_grad_rows(NormParams& p, int sms, cudaStream_t st) {
+  // two CTAs an SM where two rows each fit beside each other, else one
+  constexpr size_t kMost = 227 * 1024 - 1024;
+  const size_t row = (size_t)row_place<S, B>(p.H, p.d_stream != nullptr, p.block != nullptr).bytes;
+  const int threads = ((p.pieces + VECS - 1) / VECS + 31) / 32 * 32;
+  const int beside = kMost / 2 / row >= 2 ? 2 : 1;
+  size_t rows = (kMost / beside - (beside - 1) * 1024) / row;
+  if (rows > kRingRows) rows = kRingRows;
+  p.ring_rows = (int)rows;
+  int64_t ctas = (int64_t)beside * sms;
+  if (ctas > kMaxGradCtas) ctas = kMaxGradCtas;
+  if (ctas > p.rows) ctas = p.rows;
+  p.ctas = (int)ctas;
+  if (ctas == 0) return cudaSuccess;       // without rows the sums are zero
+  static std::atomic<uint64_t> raised{0};
+  const auto kernel = norm_grad_kernel<S, B, VECS>;
+  const cudaError_t e = raise_shared_limit(kernel, kMost, &raised);
+  if (e != cudaSuccess) return e;
+  return launch_overlapped(kernel, dim3((unsigned)ctas), threads, rows * row, st, p);
+}
+
 template <typename S, typename B>
-cudaError_t launch_norm_grad(NormParams& p, cudaStream_t st) {
-  const int vecs = p.pieces <= 128 ? 1 : p.pieces <= 1024 ? 2 : 4;
-  const int threads = ((p.pieces + vecs - 1) / vecs + 31) / 32 * 32;
-  const auto kernel = vecs == 1   ? norm_grad_kernel<S, B, 1>
-                      : vecs == 2 ? norm_grad_kernel<S, B, 2>
-                                  : norm_grad_kernel<S, B, 4>;
-  if (p.ctas > 0) {   // without rows the sums are zero
-    const cudaError_t e = launch_overlapped(kernel, dim3((unsigned)p.ctas), threads, 0, st, p);
-    if (e != cudaSuccess) return e;
-  }
+cudaError_t launch_norm_grad(NormParams& p, int sms, cudaStream_t st) {
+  const cudaError_t e = p.pieces <= 128    ? launch_grad_rows<S, B, 1>(p, sms, st)
+                        : p.pieces <= 1024 ? launch_grad_rows<S, B, 2>(p, sms, st)
+                                           : launch_grad_rows<S, B, 4>(p, sms, st);
+  if (e != cudaSuccess) return e;
   const int64_t width = (int64_t)p.n_sums * p.H;
   return launch_overlapped(norm_sums_kernel, dim3((unsigned)((width + 31) / 32)), 256, 0, st, p);
 }
@@ -327,6 +412,8 @@ cudaError_t launch_norm_grad(NormParams& p, cudaStream_t st) {
 
 struct ep_norm_handle {
   ep_norm_config cfg;
+  ep::Header header;
+  int32_t* err;
   float* part;
   int sm_count;
 };
@@ -334,8 +421,6 @@ struct ep_norm_handle {
 namespace {
 
 using namespace ep;
-
-constexpr int kMaxGradCtas = 320;
 
 ep_status nfail(ep_status st, const char* msg) { return record_error(st, msg); }
 ep_status ncuda(cudaError_t e) { return record_error(EP_ERR_CUDA, cudaGetErrorString(e)); }
@@ -359,7 +444,7 @@ ep_status plan_norm(const ep_norm_config* c, size_t* bytes) {
     return nfail(EP_ERR_INVALID_ARG, "eps must be positive and finite");
   if (!(c->residual_scale > -1e30f && c->residual_scale < 1e30f))
     return nfail(EP_ERR_INVALID_ARG, "residual_scale must be finite");
-  *bytes = 256 + (c->backward ? (size_t)kMaxGradCtas * norm_sums(*c) * c->hidden_dim * 4 : 0);
+  *bytes = kHeaderBytes + (c->backward ? (size_t)kMaxGradCtas * norm_sums(*c) * c->hidden_dim * 4 : 0);
   return EP_OK;
 }
 
@@ -428,7 +513,9 @@ extern "C" ep_status ep_norm_create(const ep_norm_config* cfg, void* d_workspace
   ep_norm_handle* p = new (std::nothrow) ep_norm_handle{};
   if (!p) return nfail(EP_ERR_INVALID_ARG, "out of host memory");
   p->cfg = *cfg;
-  p->part = reinterpret_cast<float*>(static_cast<uint8_t*>(d_workspace) + 256);
+  p->err = static_cast<int32_t*>(d_workspace);
+  p->part = reinterpret_cast<float*>(static_cast<uint8_t*>(d_workspace) + kHeaderBytes);
+  open_header(&p->header, d_workspace);
   *out_handle = p;
   return EP_OK;
 }
@@ -497,20 +584,24 @@ extern "C" ep_status ep_norm_backward(ep_norm_handle* h, const void* dout, const
   p.sums[p.n_sums++] = d_weight;
   if (weight_post) p.sums[p.n_sums++] = d_weight_post;
   if (gate && p.gate == EP_GATE_FEATURE) p.sums[p.n_sums++] = d_gate;
-  int64_t ctas = 2 * (int64_t)h->sm_count;
-  if (ctas > kMaxGradCtas) ctas = kMaxGradCtas;
-  if (ctas > num_rows) ctas = num_rows;
-  p.ctas = (int)ctas;
+  p.err = h->err;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   const bool s32 = h->cfg.stream_dtype == EP_DTYPE_FP32, b32 = h->cfg.block_dtype == EP_DTYPE_FP32;
   using bf16 = __nv_bfloat16;
-  const cudaError_t e = s32 ? b32 ? launch_norm_grad<float, float>(p, st) : launch_norm_grad<float, bf16>(p, st)
-                        : b32 ? launch_norm_grad<bf16, float>(p, st) : launch_norm_grad<bf16, bf16>(p, st);
+  cudaError_t e = header_ready(&h->header, st);
+  if (e != cudaSuccess) return ncuda(e);
+  const int sms = h->sm_count;
+  e = s32 ? b32 ? launch_norm_grad<float, float>(p, sms, st) : launch_norm_grad<float, bf16>(p, sms, st)
+          : b32 ? launch_norm_grad<bf16, float>(p, sms, st) : launch_norm_grad<bf16, bf16>(p, sms, st);
   return e == cudaSuccess ? EP_OK : ncuda(e);
 }
 
 extern "C" ep_status ep_norm_sync(ep_norm_handle* h, void* stream) {
   if (!h) return nfail(EP_ERR_INVALID_ARG, "norm handle is NULL");
-  const cudaError_t e = cudaStreamSynchronize(static_cast<cudaStream_t>(stream));
-  return e == cudaSuccess ? EP_OK : ncuda(e);
+  uint32_t bits = 0;
+  const cudaError_t e = header_report(&h->header, static_cast<cudaStream_t>(stream), &bits);
+  if (e != cudaSuccess) return ncuda(e);
+  if (bits & kErrNormTimeout)
+    return nfail(EP_ERR_TIMEOUT, "a norm's bounded wait gave up; its gradients are not complete");
+  return EP_OK;
 }

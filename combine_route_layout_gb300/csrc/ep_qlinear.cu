@@ -111,7 +111,7 @@ __global__ void __launch_bounds__(kGradThreads) quant_grad_kernel(QGradParams a)
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] = i < here ? (h ? d1[i] : d0[i]) : 0.0f;
         const float amax = max16(amax8(v));
-        const float scale = __fdiv_rn(amax, 448.0f);
+        const float scale = scale_of(amax);
         const uint2 code = e4m3x8(v, block_scale(amax, scale));
         if (row_in && block_in) {
           *reinterpret_cast<uint2*>(a.codes + row * a.ld + (int64_t)h * a.Nb * 128 + c) = code;

@@ -18,7 +18,7 @@ namespace {
 
 constexpr int kWarps = 8;
 constexpr int kTile = 16;      // weight rows of a warp
-constexpr int kAhead = 2;      // blocks of 128 terms that a warp has on their way
+constexpr int kGroup = 4;      // neighbouring blocks of 128 terms that a warp asks for at once
 
 __device__ __forceinline__ void mma_16x8x32(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                             uint32_t b0, uint32_t b1) {
@@ -51,47 +51,40 @@ __global__ void __launch_bounds__(kWarps * 32) few_rows8_kernel(QLinearParams p,
   const float* sx0 = p.xs + (int64_t)min(2 * sub, rows - 1) * p.Kb;
   const float* sx1 = p.xs + (int64_t)min(2 * sub + 1, rows - 1) * p.Kb;
   float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-  struct Block {
-    uint4 a0[2], a1[2], b[2];
-    float w0, w1, x0, x1;
-  };
-  Block q[kAhead];
   const uint4 none = make_uint4(0, 0, 0, 0);
-  auto fetch = [&](int kb, Block& t) {
+  // this warp's groups of blocks: part, part + split, ...
+  for (int kb0 = part * kGroup; kb0 < p.Kb; kb0 += kGroup * split) {
+    uint4 a0[kGroup][2], a1[kGroup][2];
+    float v0[kGroup], v1[kGroup];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int k = kb * 128 + h * 64;
-      const bool in = kb < p.Kb && k + sub * 16 < p.K;
-      t.a0[h] = in ? ld_once_v4(w0 + k) : none;
-      t.a1[h] = in ? ld_once_v4(w1 + k) : none;
-      t.b[h] = in && has_row ? *reinterpret_cast<const uint4*>(x + k) : none;
+    for (int i = 0; i < kGroup; ++i) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int k = (kb0 + i) * 128 + h * 64;
+        const bool in = k + sub * 16 < p.K;
+        a0[i][h] = in ? ld_once_v4(w0 + k) : none;
+        a1[i][h] = in ? ld_once_v4(w1 + k) : none;
+      }
+      const bool in = kb0 + i < p.Kb;
+      v0[i] = in ? s0[kb0 + i] : 0.0f;
+      v1[i] = in ? s1[kb0 + i] : 0.0f;
     }
-    const bool in = kb < p.Kb;
-    t.w0 = in ? s0[kb] : 0.0f;
-    t.w1 = in ? s1[kb] : 0.0f;
-    t.x0 = in ? sx0[kb] : 0.0f;
-    t.x1 = in ? sx1[kb] : 0.0f;
-  };
-  // this warp's blocks: part, part + split, ...
 #pragma unroll
-  for (int i = 0; i < kAhead; ++i) fetch(part + i * split, q[i]);
-  for (int kb = part; kb < p.Kb; kb += kAhead * split) {
-#pragma unroll
-    for (int i = 0; i < kAhead; ++i) {
-      const Block t = q[i];
-      fetch(kb + (kAhead + i) * split, q[i]);
+    for (int i = 0; i < kGroup; ++i) {
+      if (kb0 + i >= p.Kb) break;
+      const float x0 = sx0[kb0 + i], x1 = sx1[kb0 + i];
       float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        mma_16x8x32(d, t.a0[h].x, t.a1[h].x, t.a0[h].y, t.a1[h].y, t.b[h].x, t.b[h].y);
-        mma_16x8x32(d, t.a0[h].z, t.a1[h].z, t.a0[h].w, t.a1[h].w, t.b[h].z, t.b[h].w);
+        const int k = (kb0 + i) * 128 + h * 64;
+        const uint4 b = has_row && k + sub * 16 < p.K ? *reinterpret_cast<const uint4*>(x + k) : none;
+        mma_16x8x32(d, a0[i][h].x, a1[i][h].x, a0[i][h].y, a1[i][h].y, b.x, b.y);
+        mma_16x8x32(d, a0[i][h].z, a1[i][h].z, a0[i][h].w, a1[i][h].w, b.z, b.w);
       }
-      if (kb + i * split < p.Kb) {
-        acc[0] = fmaf(d[0], t.w0 * t.x0, acc[0]);
-        acc[1] = fmaf(d[1], t.w0 * t.x1, acc[1]);
-        acc[2] = fmaf(d[2], t.w1 * t.x0, acc[2]);
-        acc[3] = fmaf(d[3], t.w1 * t.x1, acc[3]);
-      }
+      acc[0] = fmaf(d[0], v0[i] * x0, acc[0]);
+      acc[1] = fmaf(d[1], v0[i] * x1, acc[1]);
+      acc[2] = fmaf(d[2], v1[i] * x0, acc[2]);
+      acc[3] = fmaf(d[3], v1[i] * x1, acc[3]);
     }
   }
   if (split > 1) {   // the first warp of each share adds the others' sums, in their order
@@ -138,9 +131,9 @@ bool few_qrows_supported(const QLinearParams& p) { return !p.s.begin && p.s.dens
 cudaError_t launch_qlinear_few_rows(const QLinearParams& p, int sms, cudaStream_t st) {
   const bool gated = p.act == EP_ACT_SWIGLU;
   const int64_t outs = gated ? kTile / 2 : kTile, shares = (p.N + outs - 1) / outs;
-  // 24 warps an SM keep HBM busy; a warp should have a block of terms at least
+  // 24 warps an SM keep HBM busy; a warp should have a group of blocks at least
   int split = 1;
-  while (split < kWarps && shares * split < (int64_t)sms * 24 && split < p.Kb) split *= 2;
+  while (split < kWarps && shares * split < (int64_t)sms * 24 && split * kGroup < p.Kb) split *= 2;
   const int64_t ctas = (shares * split + kWarps - 1) / kWarps;
   return launch_overlapped(gated ? few_rows8_kernel<true> : few_rows8_kernel<false>, dim3((unsigned)ctas),
                            kWarps * 32, 0, st, p, split);

@@ -90,7 +90,7 @@ __global__ void __launch_bounds__(kThreads) quant_rows_kernel(QuantParams p) {
         float f[8];
         floats8(raw[u], f);
         const float amax = max16(amax8(f));
-        const float scale = __fdiv_rn(amax, 448.0f);
+        const float scale = scale_of(amax);
         const uint2 q = e4m3x8(f, block_scale(amax, scale));
         if (in[u]) *reinterpret_cast<uint2*>(p.codes + to[u]) = q;
         if (sub == 0 && scale_at[u] >= 0) p.scales[scale_at[u]] = scale;
@@ -147,7 +147,7 @@ __global__ void __launch_bounds__(kThreads) dequant_rows_kernel(QuantParams p) {
 
 // A CTA's 128 x 128: half-warp h has rows h, h + 16, ...
 template <typename T>
-__global__ void __launch_bounds__(kThreads) quant_tiles_kernel(QuantParams p) {
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 3 : 2) quant_tiles_kernel(QuantParams p) {
   begin_overlapped();
   __shared__ float most[kThreads / 32];
   constexpr int kRows = 128 / kHalves;
@@ -180,7 +180,7 @@ __global__ void __launch_bounds__(kThreads) quant_tiles_kernel(QuantParams p) {
   __syncthreads();
 #pragma unroll
   for (int w = 0; w < kThreads / 32; ++w) amax = fmaxf(amax, most[w]);
-  const float scale = __fdiv_rn(amax, 448.0f);
+  const float scale = scale_of(amax);
   const BlockScale by = block_scale(amax, scale);
   uint8_t* codes = p.codes + base;
 #pragma unroll

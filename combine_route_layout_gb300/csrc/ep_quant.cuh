@@ -41,6 +41,15 @@ __device__ __forceinline__ float quotient(float x, float scale, float rcp) {
   return __int_as_float(__float_as_int(q) | (__float_as_int(x) & 0x80000000));
 }
 
+// amax / 448 rounded to nearest, by the same correction: 1 / 448 is rounded correctly,
+// and the residual is exact unless it underflows.
+__device__ __forceinline__ float scale_of(float amax) {
+  if (!(amax >= 0x1p-90f && amax < 0x1p127f)) return __fdiv_rn(amax, 448.0f);
+  constexpr float r = 1.0f / 448.0f;
+  const float q = __fmul_rn(amax, r);
+  return __fmaf_rn(__fmaf_rn(-q, 448.0f, amax), r, q);
+}
+
 // What the quotients of a block with this amax and scale need. Blocks below
 // kRcpMinAmax: x and scale times 2^100, exact, same quotient; a scale of 0 (an
 // all-zero block, or f32 values whose scale underflows): rcp = 0, every quotient a
@@ -57,13 +66,38 @@ __device__ __forceinline__ BlockScale block_scale(float amax, float scale) {
   return b;
 }
 
+// Two of `quotient`'s at once.
+__device__ __forceinline__ uint32_t quotient_codes(float x0, float x1, uint64_t scale2, uint64_t rcp2) {
+  uint32_t c;
+  asm("{\n .reg .b64 x, q, n, r;\n .reg .b32 lo, hi;\n .reg .b16 o;\n"
+      " mov.b64 x, {%1, %2};\n"
+      " mul.rn.f32x2 q, x, %4;\n"
+      " xor.b64 n, q, 0x8000000080000000;\n"
+      " fma.rn.f32x2 r, n, %3, x;\n"
+      " fma.rn.f32x2 q, r, %4, q;\n"
+      " and.b64 x, x, 0x8000000080000000;\n"
+      " or.b64 q, q, x;\n"
+      " mov.b64 {lo, hi}, q;\n"
+      " cvt.rn.satfinite.e4m3x2.f32 o, hi, lo;\n"
+      " cvt.u32.u16 %0, o;\n}"
+      : "=r"(c)
+      : "f"(x0), "f"(x1), "l"(scale2), "l"(rcp2));
+  return c;
+}
+
 // Eight E4M3 codes, the first in the lowest byte.
 __device__ __forceinline__ uint2 e4m3x8(const float (&f)[8], const BlockScale& b) {
   uint32_t c[4];
+  uint64_t scale2, rcp2;
+  asm("mov.b64 %0, {%1, %1};" : "=l"(scale2) : "f"(b.scaled));
+  asm("mov.b64 %0, {%1, %1};" : "=l"(rcp2) : "f"(b.rcp));
+  if (b.times == 1.0f) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    c[i] = cvt_e4m3x2(quotient(f[2 * i] * b.times, b.scaled, b.rcp),
-                      quotient(f[2 * i + 1] * b.times, b.scaled, b.rcp));
+    for (int i = 0; i < 4; ++i) c[i] = quotient_codes(f[2 * i], f[2 * i + 1], scale2, rcp2);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) c[i] = quotient_codes(f[2 * i] * b.times, f[2 * i + 1] * b.times, scale2, rcp2);
+  }
   return make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
 }
 

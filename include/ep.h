@@ -904,7 +904,7 @@ ep_status ep_norm_backward(ep_norm_handle* h, const void* dout, const void* d_st
                            int64_t num_rows, void* d_residual, void* d_block, float* d_weight,
                            float* d_weight_post, float* d_gate, void* stream);
 
-/* Wait for `stream`, then report errors of its launches. */
+/* Wait for `stream`, then report and clear device-detected errors. */
 ep_status ep_norm_sync(ep_norm_handle* h, void* stream);
 
 #ifdef __cplusplus

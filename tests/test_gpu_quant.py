@@ -377,3 +377,24 @@ def check_backward(c, bias, seed=50):
 def test_backward(layer, shape, act, out, weight_grad):
     c = Case(layer, act=act, out=out, seed=shape + 100, backward=True, weight_grad=weight_grad, **SHAPES[shape])
     check_backward(c, bias=shape % 2 == 0)
+
+
+def test_scales_of_every_bf16(layer):
+    """Every positive finite bf16 as a block's largest value, and f32 significands at their ends: a
+    scale is the quotient by 448, rounded once."""
+    every = torch.arange(1, 0x7F80, dtype=torch.int32).to(torch.int16).view(torch.bfloat16)
+    x = torch.zeros((every.numel(), 16), dtype=torch.bfloat16, device=DEV)
+    x[:, 5] = -every.to(DEV)
+    op = layer.EpQuantOp(layer.EpQuantConfig(1, 16, x.shape[0]))
+    codes, scales = op.quantize(x)
+    want = every.float().numpy() / np.float32(448)
+    assert torch.equal(scales.cpu()[:, 0], torch.from_numpy(want))
+    assert (bits(codes)[:, 5][torch.from_numpy(want) > 0] >= 0x80 + 0x7E).all()      # -448, or -448 of a rounded-up scale
+    bit = torch.cat([torch.randint(0, 1 << 23, (200000,), generator=torch.Generator().manual_seed(3)), torch.arange(0, 1 << 23, 257)])
+    for exponent in (1, 40, 127, 200, 254):
+        v = ((exponent << 23) | bit).to(torch.int32).view(torch.float32)
+        x = torch.zeros((v.numel(), 16), device=DEV)
+        x[:, 0] = v.to(DEV)
+        op = layer.EpQuantOp(layer.EpQuantConfig(1, 16, x.shape[0], dtype=torch.float32))
+        scales = op.quantize(x)[1].cpu()[:, 0]
+        assert torch.equal(scales, torch.from_numpy(v.numpy() / np.float32(448)))
