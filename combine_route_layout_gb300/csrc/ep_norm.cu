@@ -234,14 +234,22 @@ __global__ void __launch_bounds__(512) norm_grad_kernel(NormParams p) {
   for (int i = 0; i < VECS; ++i)
 #pragma unroll
     for (int j = 0; j < 8; ++j) dw[i][j] = dp[i][j] = dg[i][j] = 0.0f;
+  // a row's own numbers, a row ahead of their use
+  float2 next;
+  float next_times = p.alpha;
+  const auto numbers = [&](int64_t row) {
+    if (row >= p.rows) return;
+    next = *reinterpret_cast<const float2*>(p.stats + 2 * row);
+    if (has_block && p.gate == EP_GATE_TOKEN) next_times = p.alpha * p.gates[row];
+  };
+  numbers(blockIdx.x);
   int slot = 0;
   uint32_t phase = 0;
   for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x) {
     const int64_t base = row * p.H;
     const uint8_t* here = ring + (size_t)slot * place.bytes;
-    const float by = p.stats[2 * row], by_block = p.stats[2 * row + 1];
-    float times = p.alpha;
-    if (has_block && p.gate == EP_GATE_TOKEN) times *= p.gates[row];
+    const float by = next.x, by_block = next.y, times = next_times;
+    numbers(row + gridDim.x);
     if (!mbar_wait(&landed[slot], phase) && threadIdx.x == 0) atomicOr(p.err, kErrNormTimeout);
     float sum = 0.0f;
 #pragma unroll
@@ -318,8 +326,8 @@ __global__ void __launch_bounds__(512) norm_grad_kernel(NormParams p) {
       }
     }
     __syncthreads();   // the row has been read, and `room` is written anew
-    const int64_t next = row + (int64_t)p.ring_rows * gridDim.x;
-    if (threadIdx.x == 0 && next < p.rows) fetch(next, slot);
+    const int64_t ahead = row + (int64_t)p.ring_rows * gridDim.x;
+    if (threadIdx.x == 0 && ahead < p.rows) fetch(ahead, slot);
     if (++slot == p.ring_rows) {
       slot = 0;
       phase ^= 1;
@@ -530,7 +538,7 @@ extern "C" ep_status ep_norm_forward(ep_norm_handle* h, const void* residual, co
   ep_status s = fill_norm(h, block, gate, weight_post, weight, num_rows, &p);
   if (s != EP_OK) return s;
   if (!residual || !out || off(residual, 16) || off(out, 16) || off(stream_out, 16) ||
-      off(scales, 4) || off(stats, 4))
+      off(scales, 4) || off(stats, 8))
     return nfail(EP_ERR_INVALID_ARG, "residual and out must be given; an argument may be misaligned");
   if ((stream_out != nullptr) != (block != nullptr))
     return nfail(EP_ERR_INVALID_ARG, "stream_out goes with a block");
@@ -564,7 +572,7 @@ extern "C" ep_status ep_norm_backward(ep_norm_handle* h, const void* dout, const
   if (!h->cfg.backward)
     return nfail(EP_ERR_STATE, "the config did not reserve the backward pass's scratch");
   if (!dout || !stream_in || !stats || !d_residual || !d_weight || off(dout, 16) ||
-      off(d_stream, 16) || off(stream_in, 16) || off(stats, 4) || off(d_residual, 16) ||
+      off(d_stream, 16) || off(stream_in, 16) || off(stats, 8) || off(d_residual, 16) ||
       off(d_block, 16) || off(d_weight, 4) || off(d_weight_post, 4) || off(d_gate, 4))
     return nfail(EP_ERR_INVALID_ARG,
                  "dout, stream_in, stats, d_residual and d_weight must be given; an argument may be misaligned");

@@ -39,16 +39,21 @@ struct QuantParams {
   void* out;             // dequantised
 };
 
-// The blocks of a piece that a half-warp takes, kHalves apart, without divisions.
+// The blocks of a piece that a half-warp takes, kHalves apart, without divisions: where
+// rows are whole blocks (FLAT) they are one after another in memory.
+template <bool FLAT>
 struct Walk {
-  int row, block, drow, dblock, Kb;
-  __device__ __forceinline__ Walk(int half, int blocks) : Kb(blocks) {
+  int row, block, drow, dblock, Kb, n;
+  __device__ __forceinline__ Walk(int half, int blocks) : Kb(blocks), n(half) {
+    if (FLAT) return;
     row = half / Kb;
     block = half - row * Kb;
     drow = kHalves / Kb;
     dblock = kHalves - drow * Kb;
   }
   __device__ __forceinline__ void next() {
+    n += kHalves;
+    if (FLAT) return;
     row += drow;
     block += dblock;
     if (block >= Kb) {
@@ -56,34 +61,46 @@ struct Walk {
       ++row;
     }
   }
+  // whether there is such a block of a piece of `all` blocks, whether this lane's part of
+  // it is in, and where, counted from the piece
+  __device__ __forceinline__ bool place(int all, int K, int sub, bool& in, int64_t& at) const {
+    const bool there = n < all;
+    if (FLAT) {
+      in = there;
+      at = (int64_t)n * 128 + sub * 8;
+    } else {
+      in = there && block * 128 + sub * 8 < K;
+      at = (int64_t)row * K + block * 128 + sub * 8;
+    }
+    return there;
+  }
 };
 
 // Every half-warp goes through the same number of steps, with blocks past the end of
 // the piece left out: the shuffles are the whole warp's.
-template <typename T>
+template <typename T, bool FLAT>
 __global__ void __launch_bounds__(kThreads) quant_rows_kernel(QuantParams p) {
   extern __shared__ int table[];
   begin_overlapped();
   const int pieces = segment_table(p.s, p.per, table);
   const int half = threadIdx.x >> 4, sub = threadIdx.x & 15;
-  const T* x = static_cast<const T*>(p.x);
   for (int i = blockIdx.x; i < pieces; i += gridDim.x) {
-    const Piece at = piece_at(p.s, p.per, table, i);
-    const int steps = (at.rows * p.Kb + kHalves - 1) / kHalves;
-    Walk w(half, p.Kb);
-    for (int step = 0; step < steps; step += kUnroll) {
+    const Piece piece = piece_at(p.s, p.per, table, i);
+    const int all = piece.rows * p.Kb;
+    const T* x = static_cast<const T*>(p.x) + piece.row * p.K;
+    uint8_t* codes = p.codes + piece.row * p.K;
+    float* scales = p.scales + piece.row * p.Kb;
+    Walk<FLAT> w(half, p.Kb);
+    for (int step = 0; step < all; step += kUnroll * kHalves) {
       Raw8<T> raw[kUnroll];
-      int64_t to[kUnroll], scale_at[kUnroll];
-      bool in[kUnroll];
+      int64_t at[kUnroll];
+      bool in[kUnroll], there[kUnroll];
+      const int first = w.n;
 #pragma unroll
       for (int u = 0; u < kUnroll; ++u, w.next()) {
-        const int col = w.block * 128 + sub * 8;
-        const bool row_in = w.row < at.rows;
-        in[u] = row_in && col < p.K;
-        to[u] = (at.row + w.row) * p.K + col;
-        scale_at[u] = row_in ? (at.row + w.row) * p.Kb + w.block : -1;
+        there[u] = w.place(all, p.K, sub, in[u], at[u]);
         zero8(raw[u]);
-        if (in[u]) load8<T>(x, to[u], raw[u]);
+        if (in[u]) load8<T>(x, at[u], raw[u]);
       }
 #pragma unroll
       for (int u = 0; u < kUnroll; ++u) {
@@ -92,8 +109,8 @@ __global__ void __launch_bounds__(kThreads) quant_rows_kernel(QuantParams p) {
         const float amax = max16(amax8(f));
         const float scale = scale_of(amax);
         const uint2 q = e4m3x8(f, block_scale(amax, scale));
-        if (in[u]) *reinterpret_cast<uint2*>(p.codes + to[u]) = q;
-        if (sub == 0 && scale_at[u] >= 0) p.scales[scale_at[u]] = scale;
+        if (in[u]) *reinterpret_cast<uint2*>(codes + at[u]) = q;
+        if (sub == 0 && there[u]) scales[first + u * kHalves] = scale;
       }
     }
   }
@@ -109,7 +126,7 @@ __global__ void __launch_bounds__(kThreads) dequant_rows_kernel(QuantParams p) {
   for (int i = blockIdx.x; i < pieces; i += gridDim.x) {
     const Piece at = piece_at(p.s, p.per, table, i);
     const int steps = (at.rows * p.Kb + kHalves - 1) / kHalves;
-    Walk w(half, p.Kb);
+    Walk<false> w(half, p.Kb);
     for (int step = 0; step < steps; step += kUnroll) {
       uint2 q[kUnroll];
       float scale[kUnroll];
@@ -203,7 +220,7 @@ cudaError_t launch_rows(QuantParams& p, bool back, int64_t rows, int sms, cudaSt
   p.per = per < 1 ? 1 : (int)per;
   int64_t grid = rows / p.per + p.s.G;
   if (grid > (int64_t)sms * 8) grid = (int64_t)sms * 8;
-  const auto kernel = back ? dequant_rows_kernel<T> : quant_rows_kernel<T>;
+  const auto kernel = back ? dequant_rows_kernel<T> : p.K % 128 == 0 ? quant_rows_kernel<T, true> : quant_rows_kernel<T, false>;
   return launch_overlapped(kernel, dim3((unsigned)grid), kThreads, segment_bytes(p.s.G), st, p);
 }
 

@@ -66,39 +66,43 @@ __device__ __forceinline__ BlockScale block_scale(float amax, float scale) {
   return b;
 }
 
-// Two of `quotient`'s at once.
-__device__ __forceinline__ uint32_t quotient_codes(float x0, float x1, uint64_t scale2, uint64_t rcp2) {
+// Two of `quotient`'s at once, without the sign of a zero.
+__device__ __forceinline__ uint32_t quotient_codes(float x0, float x1, uint64_t minus_scale2, uint64_t rcp2) {
   uint32_t c;
-  asm("{\n .reg .b64 x, q, n, r;\n .reg .b32 lo, hi;\n .reg .b16 o;\n"
+  asm("{\n .reg .b64 x, q, r;\n .reg .b32 lo, hi;\n .reg .b16 o;\n"
       " mov.b64 x, {%1, %2};\n"
       " mul.rn.f32x2 q, x, %4;\n"
-      " xor.b64 n, q, 0x8000000080000000;\n"
-      " fma.rn.f32x2 r, n, %3, x;\n"
+      " fma.rn.f32x2 r, q, %3, x;\n"
       " fma.rn.f32x2 q, r, %4, q;\n"
-      " and.b64 x, x, 0x8000000080000000;\n"
-      " or.b64 q, q, x;\n"
       " mov.b64 {lo, hi}, q;\n"
       " cvt.rn.satfinite.e4m3x2.f32 o, hi, lo;\n"
       " cvt.u32.u16 %0, o;\n}"
       : "=r"(c)
-      : "f"(x0), "f"(x1), "l"(scale2), "l"(rcp2));
+      : "f"(x0), "f"(x1), "l"(minus_scale2), "l"(rcp2));
   return c;
+}
+
+// The four signs, in the codes' places.
+__device__ __forceinline__ uint32_t with_signs(uint32_t codes, const float* f) {
+  const uint32_t lo = __byte_perm(__float_as_uint(f[0]), __float_as_uint(f[1]), 0x0073);
+  const uint32_t hi = __byte_perm(__float_as_uint(f[2]), __float_as_uint(f[3]), 0x0073);
+  return codes | (__byte_perm(lo, hi, 0x5410) & 0x80808080u);
 }
 
 // Eight E4M3 codes, the first in the lowest byte.
 __device__ __forceinline__ uint2 e4m3x8(const float (&f)[8], const BlockScale& b) {
   uint32_t c[4];
-  uint64_t scale2, rcp2;
-  asm("mov.b64 %0, {%1, %1};" : "=l"(scale2) : "f"(b.scaled));
+  uint64_t minus2, rcp2;
+  asm("mov.b64 %0, {%1, %1};" : "=l"(minus2) : "f"(-b.scaled));
   asm("mov.b64 %0, {%1, %1};" : "=l"(rcp2) : "f"(b.rcp));
   if (b.times == 1.0f) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) c[i] = quotient_codes(f[2 * i], f[2 * i + 1], scale2, rcp2);
+    for (int i = 0; i < 4; ++i) c[i] = quotient_codes(f[2 * i], f[2 * i + 1], minus2, rcp2);
   } else {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) c[i] = quotient_codes(f[2 * i] * b.times, f[2 * i + 1] * b.times, scale2, rcp2);
+    for (int i = 0; i < 4; ++i) c[i] = quotient_codes(f[2 * i] * b.times, f[2 * i + 1] * b.times, minus2, rcp2);
   }
-  return make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
+  return make_uint2(with_signs(__byte_perm(c[0], c[1], 0x5410), f), with_signs(__byte_perm(c[2], c[3], 0x5410), f + 4));
 }
 
 __device__ __forceinline__ float amax8(const float (&f)[8]) {

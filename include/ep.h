@@ -880,7 +880,7 @@ void ep_norm_destroy(ep_norm_handle* h);
  *   scales       device [num_rows][ceil(H/128)] f32 with quantisation, else NULL
  *   stats        device [num_rows][2] f32 out or NULL: rms of stream and of block (1
  *                without post_norm or block), for the backward pass
- * Tensors are 16-byte aligned; scales, stats and a token's gate 4-byte.
+ * Tensors are 16-byte aligned; scales and a token's gate 4-byte, stats 8-byte.
  */
 ep_status ep_norm_forward(ep_norm_handle* h, const void* residual, const void* block,
                           const float* gate, const float* weight_post, const float* weight,
