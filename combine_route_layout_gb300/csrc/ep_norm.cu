@@ -27,6 +27,7 @@ namespace {
 
 constexpr int kRingRows = 4;              // rows of the backward pass on their way, at most
 constexpr int kMaxGradCtas = 320;
+constexpr int kGradThreadsMost = 512, kGradOnePiece = 128;
 constexpr int kErrNormTimeout = 1;
 
 struct NormParams {
@@ -204,8 +205,8 @@ __device__ __forceinline__ void floats_at(const uint8_t* row, int at, float (&f)
   floats8(r, f);
 }
 
-template <typename S, typename B, int VECS>
-__global__ void __launch_bounds__(512) norm_grad_kernel(NormParams p) {
+template <typename S, typename B, int VECS, bool POST, bool FEATURE>
+__global__ void __launch_bounds__(VECS == 1 ? kGradThreadsMost : 512) norm_grad_kernel(NormParams p) {
   extern __shared__ __align__(16) uint8_t ring[];
   __shared__ float room[4][32];
   __shared__ uint64_t landed[kRingRows];
@@ -267,7 +268,7 @@ __global__ void __launch_bounds__(512) norm_grad_kernel(NormParams p) {
         sum = fmaf(d[j] * w[j], n, sum);
       }
     }
-    const float mean = cta_sum(sum, room[0]) * p.inv;
+    const float by_mean = -by * by * (cta_sum(sum, room[0]) * p.inv);
     float dot_gate = 0.0f, dot_post = 0.0f;
     float t[VECS][8];
 #pragma unroll
@@ -285,35 +286,35 @@ __global__ void __launch_bounds__(512) norm_grad_kernel(NormParams p) {
       }
       weights8(p.w, at, w);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) t[i][j] = fmaf(by, d[j] * w[j] - s[j] * by * mean, t[i][j]);
+      for (int j = 0; j < 8; ++j) t[i][j] = fmaf(by, d[j] * w[j], fmaf(s[j], by_mean, t[i][j]));
       store8<S>(p.d_residual, base + at, t[i]);
       if (!has_block) continue;
       float y[8], wp[8], g[8];
       floats_at<B>(here + place.block, at, y);
-      if (p.post) weights8(p.w_post, at, wp);
-      if (p.gate == EP_GATE_FEATURE) weights8(p.gates, at, g);
+      if (POST) weights8(p.w_post, at, wp);
+      if (FEATURE) weights8(p.gates, at, g);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const float n = y[j] * by_block;                 // y without post_norm
-        const float u = p.post ? n * wp[j] : n;
+        const float u = POST ? n * wp[j] : n;
         if (p.gate == EP_GATE_TOKEN) dot_gate = fmaf(u, t[i][j], dot_gate);
-        if (p.gate == EP_GATE_FEATURE) dg[i][j] = fmaf(u, t[i][j], dg[i][j]);
-        const float du = times * (p.gate == EP_GATE_FEATURE ? g[j] : 1.0f) * t[i][j];
-        if (p.post) {
+        if (FEATURE) dg[i][j] = fmaf(u, t[i][j], dg[i][j]);
+        const float du = times * (FEATURE ? g[j] : 1.0f) * t[i][j];
+        if (POST) {
           dp[i][j] = fmaf(du, n, dp[i][j]);
           dot_post = fmaf(du * wp[j], n, dot_post);
         }
-        t[i][j] = p.post ? du * wp[j] : du;
+        t[i][j] = POST ? du * wp[j] : du;
       }
-      if (!p.post) store8<B>(p.d_block, base + at, t[i]);
+      if (!POST) store8<B>(p.d_block, base + at, t[i]);
     }
     // both sums in one meeting
-    if (has_block && (p.post || p.gate == EP_GATE_TOKEN)) {
+    if (has_block && (POST || p.gate == EP_GATE_TOKEN)) {
       cta_sums(dot_gate, dot_post, room[1], room[2]);
       if (p.gate == EP_GATE_TOKEN && threadIdx.x == 0) p.d_gate[row] = p.alpha * dot_gate;
     }
-    if (has_block && p.post) {
-      const float mean_post = dot_post * p.inv;
+    if (has_block && POST) {
+      const float by_post = -by_block * by_block * (dot_post * p.inv);
 #pragma unroll
       for (int i = 0; i < VECS; ++i) {
         const int at = (threadIdx.x + i * T) * 8;
@@ -321,7 +322,7 @@ __global__ void __launch_bounds__(512) norm_grad_kernel(NormParams p) {
         float y[8];
         floats_at<B>(here + place.block, at, y);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) t[i][j] = by_block * (t[i][j] - y[j] * by_block * mean_post);
+        for (int j = 0; j < 8; ++j) t[i][j] = fmaf(by_block, t[i][j], y[j] * by_post);
         store8<B>(p.d_block, base + at, t[i]);
       }
     }
@@ -341,11 +342,11 @@ __global__ void __launch_bounds__(512) norm_grad_kernel(NormParams p) {
     float* to = part + at;
     store8<float>(to, 0, dw[i]);
     to += p.H;
-    if (has_block && p.post) {
+    if (has_block && POST) {
       store8<float>(to, 0, dp[i]);
       to += p.H;
     }
-    if (has_block && p.gate == EP_GATE_FEATURE) {
+    if (has_block && FEATURE) {
 #pragma unroll
       for (int j = 0; j < 8; ++j) dg[i][j] *= p.alpha;
       store8<float>(to, 0, dg[i]);
@@ -383,7 +384,7 @@ cudaError_t launch_norm(const NormParams& p, int sms, cudaStream_t st) {
   return launch_overlapped(kernel, dim3((unsigned)p.rows), threads, 0, st, p);
 }
 
-template <typename S, typename B, int VECS>
+template <typename S, typename B, int VECS, bool POST, bool FEATURE>
 cudaError_t launch_grad_rows(NormParams& p, int sms, cudaStream_t st) {
   // two CTAs an SM where two rows each fit beside each other, else one
   constexpr size_t kMost = 227 * 1024 - 1024;
@@ -399,17 +400,26 @@ cudaError_t launch_grad_rows(NormParams& p, int sms, cudaStream_t st) {
   p.ctas = (int)ctas;
   if (ctas == 0) return cudaSuccess;       // without rows the sums are zero
   static std::atomic<uint64_t> raised{0};
-  const auto kernel = norm_grad_kernel<S, B, VECS>;
+  const auto kernel = norm_grad_kernel<S, B, VECS, POST, FEATURE>;
   const cudaError_t e = raise_shared_limit(kernel, kMost, &raised);
   if (e != cudaSuccess) return e;
   return launch_overlapped(kernel, dim3((unsigned)ctas), threads, rows * row, st, p);
 }
 
+template <typename S, typename B, bool POST, bool FEATURE>
+cudaError_t launch_grad_vecs(NormParams& p, int sms, cudaStream_t st) {
+  if (p.pieces <= kGradOnePiece) return launch_grad_rows<S, B, 1, POST, FEATURE>(p, sms, st);
+  if (p.pieces <= 1024) return launch_grad_rows<S, B, 2, POST, FEATURE>(p, sms, st);
+  return launch_grad_rows<S, B, 4, POST, FEATURE>(p, sms, st);
+}
+
 template <typename S, typename B>
 cudaError_t launch_norm_grad(NormParams& p, int sms, cudaStream_t st) {
-  const cudaError_t e = p.pieces <= 128    ? launch_grad_rows<S, B, 1>(p, sms, st)
-                        : p.pieces <= 1024 ? launch_grad_rows<S, B, 2>(p, sms, st)
-                                           : launch_grad_rows<S, B, 4>(p, sms, st);
+  const bool post = p.post && p.block, feature = p.gate == EP_GATE_FEATURE && p.block;
+  const cudaError_t e = post ? feature ? launch_grad_vecs<S, B, true, true>(p, sms, st)
+                                       : launch_grad_vecs<S, B, true, false>(p, sms, st)
+                        : feature ? launch_grad_vecs<S, B, false, true>(p, sms, st)
+                                  : launch_grad_vecs<S, B, false, false>(p, sms, st);
   if (e != cudaSuccess) return e;
   const int64_t width = (int64_t)p.n_sums * p.H;
   return launch_overlapped(norm_sums_kernel, dim3((unsigned)((width + 31) / 32)), 256, 0, st, p);
