@@ -48,10 +48,9 @@ constexpr int kTurnWords = 2 * kTurnRows * kTurnPitch;   // of a warp: gates and
 constexpr int kTurnBytes = kEpilogueWarps * kTurnWords * 4;
 constexpr int kHandover = 32 * (1 + kEpilogueWarps);     // threads of the hardware barriers
 // Registers of a thread at the start, of the first four warps and of the epilogue's.
-constexpr int kRegisters = 168, kRegistersLess = 72, kRegistersMore = 216;
+constexpr int kRegisters = 168, kRegistersLess = 56, kRegistersMore = 224;
 static_assert(kThreads * kRegisters >= 128 * kRegistersLess + kEpilogueWarps * 32 * kRegistersMore,
               "registers for the epilogue");
-constexpr int kScaleGroup = 4;                   // stages whose scales are fetched at once
 
 struct QPlan {
   int tiles, splits;
@@ -358,6 +357,7 @@ template <int MODE, int ACT, typename T>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     product8_kernel(const __grid_constant__ Maps maps, MmaParams q) {
   constexpr bool kGated = MODE == kForward && ACT == EP_ACT_SWIGLU;
+  constexpr int kScaleGroup = kGated ? 4 : 2;   // stages whose scales are fetched at once
   extern __shared__ uint8_t raw[];
   uint8_t* ring = reinterpret_cast<uint8_t*>(((uintptr_t)raw + 1023) & ~(uintptr_t)1023);
   float* rooms = reinterpret_cast<float*>(ring + kRingBytes);    // [epilogue warp][kTurnWords]
@@ -539,12 +539,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   } else {
     registers_more<kRegistersMore>();
     // ------------------------------------------------ epilogue
-    // Blocks of 32 columns: of four (256 columns) or two of this warp's half; with
-    // SwiGLU blocks 0 and 1 are gates, 2 and 3 the same features' up values (128
-    // columns: 0 and 2).
+    // Blocks of 32 columns: four (256 columns) or two of this warp's half; with SwiGLU
+    // blocks 0 and 2 are gates, 1 and 3 the same features' up values.
     const int quad = warp & 3, turn = (warp - 4) >> 2;
     const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
-    const int sub = plan.width / 128;                     // blocks 0 .. 2 sub - 1, or 0 .. sub - 1 and 2 ..
+    const int sub = plan.width / 128;                     // half as many blocks
     const uint32_t sum0 = smem_addr(&bar->acc_full[0]);
     float* room = rooms + (warp - 4) * kTurnWords;
     int n_acc = 0;
@@ -604,13 +603,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const uint32_t at = lanes + (n_acc & 1) * 256 + turn * (kGated ? plan.width / 4 : plan.width / 2);
         __syncwarp();
         if (mine_rows > 0 && ok) {
+          // 16 columns' loads are on their way under the arithmetic of the 16 before:
+          // tensor memory gives 64 bytes a cycle to each quarter of the SM
+          float r[2][16];
+          const auto column_of = [&](int c) {             // of piece c of 16 columns
+            return kGated ? (c >> 1 & 1) * (plan.width / 2) + (c >> 2) * 32 + (c & 1) * 16 : c * 16;
+          };
+          tmem_begin16(at, r[0]);
+          tmem_wait16(r[0]);
 #pragma unroll
-          for (int h = 0; h < 4; ++h) {
-            if ((kGated ? h & 1 : h >> 1) >= sub) continue;
-            float r[32];
-            tmem_load32(at + (kGated && h >= 2 ? plan.width / 2 + (h - 2) * 32 : h * 32), r);
+          for (int c = 0; c < 8; ++c) {
+            if (c >= 4 && sub == 1) continue;
+            const bool more = c != 7 && (c != 3 || sub == 2);
+            if (more) tmem_begin16(at + column_of(c + 1), r[(c + 1) & 1]);
+            const float by_c = kGated && (c >> 1 & 1) ? scale_up : scale;
 #pragma unroll
-            for (int c = 0; c < 32; ++c) sum[h][c] = fmaf(r[c], kGated && h >= 2 ? scale_up : scale, sum[h][c]);
+            for (int k = 0; k < 16; ++k)
+              sum[c / 2][(c & 1) * 16 + k] = fmaf(r[c & 1][k], by_c, sum[c / 2][(c & 1) * 16 + k]);
+            if (more) tmem_wait16(r[(c + 1) & 1]);
           }
         }
         tc_fence_before();
@@ -624,10 +634,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       if (w.parts == 1) {
         if (mine_rows <= 0) continue;
 #pragma unroll
-        for (int h = 0; h < (kGated ? 2 : 4); ++h) {
-          const int col = col0 + h * 32;
-          if ((kGated ? h & 1 : h >> 1) >= sub || col >= q.outs) continue;
-          finish<MODE, ACT, T>(q, room, w.g, row0, mine_rows, col, lane, sum[h], sum[(h + 2) & 3]);
+        for (int h = 0; h < 4; h += kGated ? 2 : 1) {
+          const int col = col0 + (kGated ? h / 2 : h) * 32;
+          if (h >= 2 * sub || col >= q.outs) continue;
+          finish<MODE, ACT, T>(q, room, w.g, row0, mine_rows, col, lane, sum[h], sum[(h + 1) & 3]);
         }
         continue;
       }
@@ -635,9 +645,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       // tiles of 128 columns)
       float* sums = q.p.partial + ((int64_t)pair * 128 * 256 + cta * 128 + quad * 32 + lane);
 #pragma unroll
-      for (int h = 0; h < 4; ++h) {
-        if ((kGated ? h & 1 : h >> 1) >= 1) continue;
-        const int column = (kGated && h >= 2 ? 64 : h * 32) + turn * (kGated ? 32 : 64);
+      for (int h = 0; h < 2; ++h) {
+        const int column = (kGated ? h * 64 : h * 32) + turn * (kGated ? 32 : 64);
 #pragma unroll
         for (int c = 0; c < 32; ++c) put(sums + (column + c) * 256, sum[h][c], lane < mine_rows);
       }
