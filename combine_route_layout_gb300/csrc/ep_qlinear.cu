@@ -3,10 +3,12 @@
 #include <climits>
 #include <cstring>
 #include <new>
+#include <type_traits>
 
 #include "ep_header.cuh"
 #include "ep_launch.cuh"
 #include "ep_linear_grad.cuh"
+#include "ep_pieces.cuh"
 #include "ep_qlinear.cuh"
 #include "ep_quant.cuh"
 
@@ -26,19 +28,28 @@ struct QGradParams {
   int vec;                   // rows of dy and z are whole 16-byte pieces
 };
 
-template <typename T>
-__device__ __forceinline__ void load_some(const T* at, int left, bool vec, float (&v)[8]) {
-  if (vec && left >= 8) {
-    load_columns<8, T>(at, v);
-  } else {
+// Eight neighbouring columns, of which `left` exist, zeros for the others: whole 16-byte
+// pieces (VEC: all eight exist, or none), or one by one.
+template <bool VEC, typename T>
+struct Columns {
+  Raw8<T> raw;
+  __device__ __forceinline__ void load(const T* at, int left) {
+    zero8(raw);
+    if (VEC) {
+      if (left >= 8) load8<T>(at, 0, raw);
+    } else {
+      T* to = reinterpret_cast<T*>(&raw);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = i < left ? (float)at[i] : 0.0f;
+      for (int i = 0; i < 8; ++i)
+        if (i < left) to[i] = at[i];
+    }
   }
-}
+};
 
-__device__ __forceinline__ void store_some(__nv_bfloat16* at, int left, bool vec, const float (&v)[8]) {
-  if (vec && left >= 8) {
-    store_dz<8>(at, v);
+template <bool VEC>
+__device__ __forceinline__ void store_columns(__nv_bfloat16* at, int left, const float (&v)[8]) {
+  if (VEC) {
+    if (left >= 8) store8<__nv_bfloat16>(at, 0, v);
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i)
@@ -46,7 +57,7 @@ __device__ __forceinline__ void store_some(__nv_bfloat16* at, int left, bool vec
   }
 }
 
-template <int ACT, typename T>
+template <int ACT, typename T, bool VEC>
 __global__ void __launch_bounds__(kGradThreads) quant_grad_kernel(QGradParams a) {
   begin_overlapped();
   const GradParams& q = a.g;
@@ -54,6 +65,7 @@ __global__ void __launch_bounds__(kGradThreads) quant_grad_kernel(QGradParams a)
   __shared__ BlockPlace at;
   __shared__ float sums[2][kGradThreads * 8];
   constexpr bool kGated = ACT == EP_ACT_SWIGLU;
+  constexpr int kAhead = 2;                               // rows on their way
   const int64_t block = blockIdx.x;
   find_block(p.s, block, q.row_blocks, at);
   __syncthreads();
@@ -62,60 +74,76 @@ __global__ void __launch_bounds__(kGradThreads) quant_grad_kernel(QGradParams a)
   const int wide = kGradThreads / 16 / q.lanes;           // half-warps beside each other in a row
   const int lane_row = half / wide, cb = blockIdx.y * wide + half % wide;
   const int c = cb * 128 + sub * 8;
-  const bool block_in = cb < a.Nb, vec = a.vec;
+  const bool block_in = cb < a.Nb;
   const int left = block_in ? p.N - c : 0;                // columns that exist, from this lane's on
   float s0[8], s1[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) s0[i] = s1[i] = 0.0f;
-  const int steps = (int)((at.row1 - at.row0 + q.lanes - 1) / q.lanes);
-#pragma unroll 2
-  for (int step = 0; step < steps; ++step) {
-    const int64_t r = at.row0 + lane_row + (int64_t)step * q.lanes;
-    const bool row_in = r < at.row1;
-    const int here = row_in ? left : 0;
-    const int64_t row = at.begin + r;
-    float d0[8], d1[8];
-    load_some(static_cast<const T*>(p.dy) + row * p.N + c, here, vec, d0);
-    const __nv_bfloat16* z = p.z + row * p.Nw + c;
-    if (kGated) {
-      float zg[8], zu[8];
-      load_some(z, here, vec, zg);
-      load_some(z + p.N, here, vec, zu);
+  const int rows = (int)(at.row1 - at.row0);
+  const int64_t row0 = at.begin + at.row0;
+  struct Step {
+    Columns<VEC, T> dy;
+    Columns<VEC, __nv_bfloat16> z, up;
+  };
+  Step next[kAhead];
+  const auto fetch = [&](int r, Step& t) {
+    const int here = r < rows ? left : 0;
+    t.dy.load(static_cast<const T*>(p.dy) + (row0 + r) * p.N + c, here);
+    if (ACT != EP_ACT_NONE) t.z.load(p.z + (row0 + r) * p.Nw + c, here);
+    if (kGated) t.up.load(p.z + (row0 + r) * p.Nw + p.N + c, here);
+  };
+#pragma unroll
+  for (int i = 0; i < kAhead; ++i) fetch(lane_row + i * q.lanes, next[i]);
+  // every half-warp goes through the same number of steps: the shuffles are the warp's
+  for (int step = 0; step < rows; step += kAhead * q.lanes) {
+#pragma unroll
+    for (int n = 0; n < kAhead; ++n) {
+      const int r = step + n * q.lanes + lane_row;
+      float d0[8], d1[8];
+      floats8(next[n].dy.raw, d0);
+      if (kGated) {
+        float zg[8], zu[8];
+        floats8(next[n].z.raw, zg);
+        floats8(next[n].up.raw, zu);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          // silu'(g) = s (1 + g (1 - s)), silu(g) = g s
+          const float s = sigmoid_of(zg[i]);
+          d1[i] = d0[i] * (zg[i] * s);
+          d0[i] *= zu[i] * (s * (1.0f + zg[i] * (1.0f - s)));
+        }
+      } else if (ACT != EP_ACT_NONE) {
+        float zv[8];
+        floats8(next[n].z.raw, zv);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) d0[i] *= slope_of(ACT, zv[i]);
+      }
+      fetch(r + kAhead * q.lanes, next[n]);
+      // columns and rows that do not exist are zeros: zero times a finite slope
+      const bool row_in = r < rows;
+      const int here = row_in ? left : 0;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        // silu'(g) = s (1 + g (1 - s)), silu(g) = g s
-        const float s = sigmoid_of(zg[i]);
-        d1[i] = d0[i] * (zg[i] * s);
-        d0[i] *= zu[i] * (s * (1.0f + zg[i] * (1.0f - s)));
+        s0[i] += d0[i];
+        if (kGated) s1[i] += d1[i];
       }
-    } else if (ACT != EP_ACT_NONE) {
-      float zv[8];
-      load_some(z, here, vec, zv);
+      const int64_t row = row0 + r;
+      if (q.dz) {
+        __nv_bfloat16* out = q.dz + row * p.ldz + c;
+        store_columns<VEC>(out, here, d0);
+        if (kGated) store_columns<VEC>(out + p.N, here, d1);
+      }
+      if (a.codes) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) d0[i] *= slope_of(ACT, zv[i]);
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      s0[i] += i < here ? d0[i] : 0.0f;
-      if (kGated) s1[i] += i < here ? d1[i] : 0.0f;
-    }
-    if (q.dz) {
-      __nv_bfloat16* out = q.dz + row * p.ldz + c;
-      store_some(out, here, vec, d0);
-      if (kGated) store_some(out + p.N, here, vec, d1);
-    }
-    if (a.codes) {
-#pragma unroll
-      for (int h = 0; h < (kGated ? 2 : 1); ++h) {
-        float v[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = i < here ? (h ? d1[i] : d0[i]) : 0.0f;
-        const float amax = max16(amax8(v));
-        const float scale = scale_of(amax);
-        const uint2 code = e4m3x8(v, block_scale(amax, scale));
-        if (row_in && block_in) {
-          *reinterpret_cast<uint2*>(a.codes + row * a.ld + (int64_t)h * a.Nb * 128 + c) = code;
-          if (sub == 0) a.scales[row * a.Sw + h * a.Nb + cb] = scale;
+        for (int h = 0; h < (kGated ? 2 : 1); ++h) {
+          const float (&v)[8] = h ? d1 : d0;
+          const float amax = max16(amax8(v));
+          const float scale = scale_of(amax);
+          const uint2 code = e4m3x8(v, block_scale(amax, scale));
+          if (row_in && block_in) {
+            *reinterpret_cast<uint2*>(a.codes + row * a.ld + (int64_t)h * a.Nb * 128 + c) = code;
+            if (sub == 0) a.scales[row * a.Sw + h * a.Nb + cb] = scale;
+          }
         }
       }
     }
@@ -152,13 +180,17 @@ cudaError_t launch_quant_grad(QGradParams a, cudaStream_t st) {
   while (a.g.lanes < halves && a.Nb * a.g.lanes * 2 <= halves) a.g.lanes *= 2;
   const int wide = halves / a.g.lanes;
   const dim3 grid((unsigned)a.g.row_blocks, (unsigned)((a.Nb + wide - 1) / wide));
-  auto kernel = quant_grad_kernel<EP_ACT_NONE, T>;
-  switch (a.g.p.act) {
-    case EP_ACT_RELU: kernel = quant_grad_kernel<EP_ACT_RELU, T>; break;
-    case EP_ACT_SILU: kernel = quant_grad_kernel<EP_ACT_SILU, T>; break;
-    case EP_ACT_GELU: kernel = quant_grad_kernel<EP_ACT_GELU, T>; break;
-    case EP_ACT_SWIGLU: kernel = quant_grad_kernel<EP_ACT_SWIGLU, T>; break;
-  }
+  const auto of = [&](auto vec) {
+    constexpr bool VEC = decltype(vec)::value;
+    switch (a.g.p.act) {
+      case EP_ACT_RELU: return quant_grad_kernel<EP_ACT_RELU, T, VEC>;
+      case EP_ACT_SILU: return quant_grad_kernel<EP_ACT_SILU, T, VEC>;
+      case EP_ACT_GELU: return quant_grad_kernel<EP_ACT_GELU, T, VEC>;
+      case EP_ACT_SWIGLU: return quant_grad_kernel<EP_ACT_SWIGLU, T, VEC>;
+      default: return quant_grad_kernel<EP_ACT_NONE, T, VEC>;
+    }
+  };
+  const auto kernel = a.vec ? of(std::true_type()) : of(std::false_type());
   return launch_overlapped(kernel, grid, kGradThreads, 0, st, a);
 }
 
