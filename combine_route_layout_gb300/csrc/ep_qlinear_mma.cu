@@ -276,23 +276,6 @@ __device__ __forceinline__ void add_row(const float* at, float (&v)[32]) {
   }
 }
 
-// 32 columns' biases, the same for all lanes: 16 bytes a load where they allow it.
-__device__ __forceinline__ void add_bias(const float* at, float (&v)[32]) {
-  if ((uintptr_t)at % 16 == 0) {
-#pragma unroll
-    for (int c = 0; c < 32; c += 4) {
-      const float4 b = *reinterpret_cast<const float4*>(at + c);
-      v[c] += b.x;
-      v[c + 1] += b.y;
-      v[c + 2] += b.z;
-      v[c + 3] += b.w;
-    }
-  } else {
-#pragma unroll
-    for (int c = 0; c < 32; ++c) v[c] += at[c];
-  }
-}
-
 // The epilogue of 32 columns of a warp's rows: `z` (and `up`, with SwiGLU) is a lane's
 // row, T the output's type. Whole aligned pieces go out as they are; others are turned
 // round, kTurnRows rows at a time, so that a warp stores 32 neighbours of a row.
@@ -308,8 +291,11 @@ __device__ __forceinline__ void finish(const MmaParams& q, float* room, int g, i
   if (q.vec && col + 32 <= q.outs) {
     if (lane >= rows) return;
     if (bias) {
-      add_bias(bias, z);
-      if (kGated) add_bias(bias + p.N, up);
+#pragma unroll
+      for (int c = 0; c < 32; ++c) {
+        z[c] += bias[c];
+        if (kGated) up[c] += bias[p.N + c];
+      }
     }
     if (zp) {
       store_row(zp + (int64_t)lane * p.Nw, z);
