@@ -82,6 +82,7 @@ struct Barriers {
   uint64_t tile_full[kSlots], tile_empty[kSlots];
   uint64_t joined;            // the epilogue's warps meet
   Tile tiles[kSlots];
+  uint32_t failed;            // a wait for a sum gave up
   uint32_t tmem;
   uint32_t last;              // this CTA's part of a tile was the last
 };
@@ -378,11 +379,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     mbar_init(&bar->acc_full[threadIdx.x - kMaxStages], 1);
   }
   if (threadIdx.x >= 32 && threadIdx.x < 32 + kSlots) {
-    // producer, MMA, the epilogue's warps
+    // producer, MMA, sums, the epilogue's warps
     mbar_init(&bar->tile_full[threadIdx.x - 32], 1);
-    mbar_init(&bar->tile_empty[threadIdx.x - 32], 2 + kEpilogueWarps);
+    mbar_init(&bar->tile_empty[threadIdx.x - 32], 3 + kEpilogueWarps);
   } else if (threadIdx.x == 32 + kSlots) {
     mbar_init(&bar->joined, kEpilogueWarps);
+    bar->failed = 0;
   }
   if (threadIdx.x < 64) mbar_init_fence();
   if (threadIdx.x == 64) {
@@ -522,6 +524,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
       for (int last = n_acc < 2 ? 0 : n_acc - 2; last < n_acc; ++last) named_sync(1 + (last & 1), kHandover);
       if (!ok && lane == 0) atomicOr(timeout, kErrLinearTimeout);
+    } else if (warp == 2) {
+      // ---------------------------------------------- sums: looks for each and tells the epilogue.
+      // After a wait that gave up it tells it of all sums, as the others meet as often as ever.
+      int n_acc = 0;
+      bool ok = true;
+      for (int i = 0; i < mine; ++i) {
+        Tile w;
+        if (ok) ok = warp_take_tile(bar, i, w, lane);
+        if (!ok) w = qtile_at<kGated>(q, plan, first, begins, counts, sizes, pair + i * pairs);
+        if (share_of(q, w, cta).rows <= 0) continue;
+        for (int kb = w.kb0; kb < w.kb1; ++kb, ++n_acc) {
+          if (ok) {
+            ok = warp_wait(&bar->acc_full[n_acc & 1], (n_acc >> 1) & 1);
+            if (!ok && lane == 0) bar->failed = 1;
+          }
+          tc_fence_after();
+          tc_fence_before();
+          __syncwarp();
+          named_arrive(3 + (n_acc & 1), kHandover);
+        }
+      }
+      if (!ok && lane == 0) atomicOr(timeout, kErrLinearTimeout);
     } else if (warp == 3 && elect_one()) {
       // ---------------------------------------------- works out the tiles, ahead of all roles
       bool ok = true;
@@ -544,11 +568,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const int quad = warp & 3, turn = (warp - 4) >> 2;
     const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
     const int sub = plan.width / 128;                     // half as many blocks
-    const uint32_t sum0 = smem_addr(&bar->acc_full[0]);
     float* room = rooms + (warp - 4) * kTurnWords;
     int n_acc = 0;
     uint32_t meeting = 0;
-    bool ok = true, seen = false;                         // seen: the next sum was there already
+    bool ok = true;
     for (int i = 0; i < mine; ++i) {
       const int u = pair + i * pairs;
       Tile w;
@@ -592,7 +615,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           left = kScaleGroup;
           fetch(kb + kScaleGroup);
         }
-        if (ok && !__all_sync(kFull, seen)) ok = warp_wait(&bar->acc_full[n_acc & 1], (n_acc >> 1) & 1);
+        __syncwarp();
+        named_sync(3 + (n_acc & 1), kHandover);
         tc_fence_after();
         const float scale = by[0], scale_up = by_up[0];
 #pragma unroll
@@ -626,8 +650,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         tc_fence_before();
         __syncwarp();
         named_arrive(1 + (n_acc & 1), kHandover);
-        seen = mbar_test(sum0 + ((n_acc + 1) & 1) * 8, ((n_acc + 1) >> 1) & 1);
       }
+      if (*const_cast<volatile uint32_t*>(&bar->failed)) ok = false;
       if (!ok) continue;
       // the values of this part: the tile's result, or sums for the part that finishes
       // last, which then adds all of them in their order
