@@ -345,3 +345,53 @@ def test_layer_of_fp8_dispatch_products_combine_and_norms(layer, tokens):
     assert near(s2, want, 2.0 ** -8) and near(nxt, want * rms(want) * w_out.double(), 2.0 ** -8)
     for op in (norm, ex, wq, wq2, up, down, mid):
         op.sync()
+
+
+def test_the_most_groups(layer):
+    """1024 experts with 0 to 3 rows each, tight segments."""
+    torch.backends.cuda.matmul.allow_tf32 = False
+    G, k, n = 1024, 256, 144
+    counts = [(7 * g) % 4 for g in range(G)]
+    begins, pool = segments(counts, pad=0)
+    at = dict(row_begin=int32s(begins), row_count=int32s(counts))
+    w, ws = codes(3, G, n, k), powers(4, G, blocks(n), blocks(k))
+    x = torch.randint(-2, 3, (pool, k), generator=gen(5), device=DEV).float()
+    x[:, ::128] = 7.0                                  # scales of 1/64
+    quant = layer.EpQuantOp(layer.EpQuantConfig(G, k, pool, dtype=F32))
+    q, s = quant.quantize(x, **at)
+    assert torch.equal(values(q, s), x)
+    op = layer.EpQuantLinearOp(layer.EpLinearConfig(G, k, n, pool, out_dtype=F32, weight_grad_dtype=F32), backward=True)
+    y = op.forward(q, s, w, ws, **at)
+    wv = weight_values(w, ws, n)
+    of = torch.repeat_interleave(torch.arange(G, device=DEV), int32s(counts).long())
+    want = torch.bmm(wv[of], x[:, :, None])[..., 0]
+    assert torch.equal(y, want)
+    dy = torch.randint(-2, 3, (pool, n), generator=gen(6), device=DEV).float()
+    dy[:, ::64] = 7.0
+    dx, dw, db = op.backward(dy, q, s, w, ws, want_dbias=True, **at)
+    assert torch.equal(dx, torch.bmm(dy[:, None], wv[of])[:, 0].bfloat16())
+    assert torch.equal(dw, torch.zeros((G, n, k), device=DEV).index_add_(0, of, dy[:, :, None] * x[:, None]))
+    assert torch.equal(db, torch.zeros((G, n), device=DEV).index_add_(0, of, dy))
+    op.sync()
+    quant.sync()
+
+
+def test_part_of_the_rows_and_residual_in_place(layer):
+    """num_rows leaves the rows behind it alone; y may be the residual."""
+    torch.backends.cuda.matmul.allow_tf32 = False
+    for rows, m, n in ((300, 211, 160), (300, 211, 333), (20, 7, 160), (64, 40, 128)):
+        k = 4096 if rows == 64 else 512
+        x, xs = codes(1, rows, k), powers(2, rows, blocks(k))
+        w, ws = codes(3, 1, n, k), powers(4, 1, blocks(n), blocks(k))
+        op = layer.EpQuantLinearOp(layer.EpLinearConfig(1, k, n, rows, out_dtype=F32))
+        r = torch.randint(-9, 10, (rows, n), generator=gen(7), device=DEV).float()
+        want = r.clone()
+        want[:m] += (values(x, xs) @ weight_values(w, ws, n)[0].t())[:m]
+        assert op.forward(x, xs, w, ws, residual=r, out=r, num_rows=m) is r
+        assert torch.equal(r, want)
+        quant = layer.EpQuantOp(layer.EpQuantConfig(1, n, rows, dtype=F32)) if n % 16 == 0 else None
+        if quant:
+            q, s = torch.full((rows, n), 3, dtype=torch.uint8, device=DEV).view(E4M3), torch.full((rows, blocks(n)), -1.0, device=DEV)
+            quant.quantize(want, num_rows=m, codes=q, scales=s)
+            assert (q[m:].view(torch.uint8) == 3).all() and (s[m:] == -1).all() and (s[:m] > 0).all()
+        op.sync()
