@@ -1,6 +1,7 @@
 // Tiles of 256 features by up to 256 rows that a pair of CTAs shares, for the products
-// of bf16 operands and of block-quantised ones: which tiles there are, the parts that
-// their contractions are cut into, and what becomes of a tile's sums. A kernel's
+// of bf16 operands: which tiles there are, the parts that their contractions are cut
+// into, and what becomes of a tile's sums. The products of block-quantised operands, whose
+// tiles and sums are others, share the parts, the tiles' table, tickets and maps. A kernel's
 // parameters Q hold its LinearParams or QLinearParams `p`, the output (`out`,
 // `features` long, `f_tiles` tiles of them), the tiles' `cap` and a dense product's
 // `plan`, and the contraction's `terms`, Q::kDepth of them a stage. Its barriers B

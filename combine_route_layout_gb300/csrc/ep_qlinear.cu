@@ -16,9 +16,10 @@ namespace ep {
 namespace {
 
 // dz = dy act'(z), quantised by 128 of a row for dx, rounded to bf16 for dW, and the
-// sums of its columns over each block of rows: one pass, bound by HBM. A half-warp
-// takes 128 columns, eight a lane, of every `lanes`th row of a CTA's kGradRows; codes
-// and scales are of the unrounded dz.
+// sums of its columns over each block of rows: one pass. A half-warp takes 128 columns,
+// eight a lane, of every `lanes`th row of a CTA's kGradRows; codes and scales are of the
+// unrounded dz. Two rows are on their way ahead of the arithmetic: the sums alone of 128
+// experts x 973 rows x 2 x 2048 (1.5 GB) take 305 us, 5 TB/s, 673 with one row at a time.
 struct QGradParams {
   GradParams g;
   uint8_t* codes;            // [pool][ld], or NULL

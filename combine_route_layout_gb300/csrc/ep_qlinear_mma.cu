@@ -19,14 +19,21 @@
 // products, and its epilogue hands an accumulator back by a hardware barrier. A pair of
 // CTAs still shares a tile of 256 rows: each loads half of its weights for both. Groups
 // of at most 128 rows have tiles of twice the features instead, half of them each
-// CTA's, so that experts with a handful of rows keep all SMs reading weights.
+// CTA's, so that experts with a handful of rows keep all SMs reading weights (256 experts
+// x 32 rows, above: 306 us when it came in, 502 with such rows in one CTA of a pair).
 // SwiGLU: half of the tile's columns are gates, half the same features' up values; a
 // thread has both. W is read as it is for dx too: MN-major, a box of 128 terms x 128
 // features.
 //
-// Roles by warp: 0 TMA, 1 MMA, 3 works out the tiles (one thread each, but for MMA,
-// whose warp waits as one), 4-11 epilogue: TMEM lanes go by warp % 4, columns by halves.
-// 128 sums a thread: the other warps give registers up for them.
+// Roles by warp: 0 TMA, 1 MMA, 2 looks for complete sums and tells the epilogue by
+// another hardware barrier (8192^3: 515 us, 533 with every epilogue warp looking), 3 works
+// out the tiles (one thread each, but for 1 and 2, which wait as warps), 4-11 epilogue:
+// TMEM lanes go by warp % 4, columns by halves. 128 sums a thread: the other warps give
+// registers up for them (16 warps with 64 sums each: 870 us).
+//
+// Bound by that loop and by power: 8192^3 515 us, 2.14 PFLOP/s; 128 experts x 973 rows,
+// 4096 to 2 x 2048 with SwiGLU, bias and pre-activations, 2.47 ms, 1.7 PFLOP/s, 1350 W at
+// full clocks; 256 experts x 32 rows, 7168 to 2 x 512, 300 us, 95 % of the copy's bandwidth.
 #include <atomic>
 #include <climits>
 #include <cstring>
@@ -47,7 +54,8 @@ constexpr int kTurnRows = 8, kTurnPitch = 33;    // words: rows that are stored 
 constexpr int kTurnWords = 2 * kTurnRows * kTurnPitch;   // of a warp: gates and up
 constexpr int kTurnBytes = kEpilogueWarps * kTurnWords * 4;
 constexpr int kHandover = 32 * (1 + kEpilogueWarps);     // threads of the hardware barriers
-// Registers of a thread at the start, of the first four warps and of the epilogue's.
+// Registers of a thread at the start, of the first four warps and of the epilogue's:
+// 8192^3 took 535 us so, 614 to 687 with 216 for the epilogue, 580 with 232.
 constexpr int kRegisters = 168, kRegistersLess = 56, kRegistersMore = 224;
 static_assert(kThreads * kRegisters >= 128 * kRegistersLess + kEpilogueWarps * 32 * kRegistersMore,
               "registers for the epilogue");
@@ -358,7 +366,7 @@ template <int MODE, int ACT, typename T>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     product8_kernel(const __grid_constant__ Maps maps, MmaParams q) {
   constexpr bool kGated = MODE == kForward && ACT == EP_ACT_SWIGLU;
-  constexpr int kScaleGroup = kGated ? 4 : 2;   // stages whose scales are fetched at once
+  constexpr int kScaleGroup = kGated ? 4 : 2;   // stages whose scales are fetched at once: registers allow no more
   extern __shared__ uint8_t raw[];
   uint8_t* ring = reinterpret_cast<uint8_t*>(((uintptr_t)raw + 1023) & ~(uintptr_t)1023);
   float* rooms = reinterpret_cast<float*>(ring + kRingBytes);    // [epilogue warp][kTurnWords]

@@ -3,7 +3,8 @@
 //
 // A warp takes 16 weight rows (gated: 8 gate rows and their up rows) and all rows of x,
 // and lets the warp-wide 16 x 8 x 32 product of E4M3 do the arithmetic: with a
-// conversion and a multiply-add for each code a single row of 4096 x 32768 takes 39 us.
+// conversion and a multiply-add for each code a single row of 4096 x 32768 takes 39 us,
+// so 28.7 (4.7 TB/s); of 4096 x 4096 6.1 us, most of it one trip to HBM and the launch.
 // Which term a place of a fragment stands for is free, as long as both operands agree: a
 // lane loads 16 neighbouring codes of weight rows t / 4 and t / 4 + 8 and of row t / 4 of
 // x, and these are the two steps' fragments of 64 terms as they come. The four products of
@@ -19,6 +20,7 @@ namespace {
 constexpr int kWarps = 8;
 constexpr int kTile = 16;      // weight rows of a warp
 constexpr int kGroup = 4;      // neighbouring blocks of 128 terms that a warp asks for at once
+                               // (28.7 us; with 2 37, with 8 39; with four warps a CTA 33)
 
 __device__ __forceinline__ void mma_16x8x32(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                             uint32_t b0, uint32_t b1) {

@@ -2,12 +2,14 @@
 // each 128 x 128), and back: value = code scale, code = E4M3(x / scale), scale =
 // amax / 448.
 //
-// One pass each, bound by HBM. Rows: a half-warp takes a block of 128, eight
-// elements a lane, so that its amax is four shuffles and its codes one 8-byte store
-// a lane; a CTA takes pieces of the segments in turn (kElements of them: enough that
-// finding the piece's segment costs nothing, few enough that small batches fill the
-// GPU) and has kUnroll blocks of each half-warp on their way at once. Matrices: a
-// CTA keeps a whole 128 x 128 in registers between its amax and its codes.
+// One pass each. Rows: a half-warp takes a block of 128, eight elements a lane, so
+// that its amax is four shuffles and its codes one 8-byte store a lane; a CTA takes
+// pieces of the segments in turn (kElements of them: enough that finding the piece's
+// segment costs nothing, few enough that small batches fill the GPU) and has kUnroll
+// blocks of each half-warp on their way at once. 124518 x 2048 bf16: 135 us, 5.7 TB/s
+// (two blocks on their way: 158 to 166), with two thirds of the issue slots busy.
+// Matrices: a CTA keeps a whole 128 x 128 in registers between its amax and its codes.
+// 32 of 4096 x 4096 bf16: 271 us, 5.9 TB/s, bound by HBM.
 #include <climits>
 #include <cstring>
 #include <new>
