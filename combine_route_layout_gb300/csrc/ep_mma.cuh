@@ -256,18 +256,10 @@ __device__ __forceinline__ void mma8_stage(uint32_t d, uint32_t a, uint32_t a_hi
       : "memory");
 }
 
-// Arrive once this CTA's own products issued so far are complete: on this CTA's
-// barrier, and on this barrier of both CTAs of the cluster.
+// Arrive on this CTA's barrier once its own products issued so far are complete.
 __device__ __forceinline__ void mma8_commit(uint32_t bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
                : "memory");
-}
-__device__ __forceinline__ void mma8_commit_both(uint32_t bar) {
-  asm volatile(
-      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
-          bar),
-      "h"((uint16_t)3)
-      : "memory");
 }
 
 __device__ __forceinline__ void tmem_alloc_own(uint32_t* dst, uint32_t columns) {
@@ -282,8 +274,7 @@ __device__ __forceinline__ void tmem_free_own(uint32_t addr, uint32_t columns) {
   asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(columns));
 }
 
-// Tiled TMA loads: into this CTA's shared memory, and to the same place of both CTAs of
-// the cluster, where the bytes complete on each one's own barrier at `bar`.
+// Tiled TMA loads into this CTA's shared memory, whose bytes complete on its barrier.
 __device__ __forceinline__ void tma_own_2d(uint32_t dst, const void* map, int c0, int c1, uint32_t bar) {
   asm volatile(
       "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
@@ -298,15 +289,6 @@ __device__ __forceinline__ void tma_own_4d(uint32_t dst, const void* map, int c0
       "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
       " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
       "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(bar)
-      : "memory");
-}
-
-__device__ __forceinline__ void tma_both_4d(uint32_t dst, const void* map, int c0, int c1, int c2,
-                                            int c3, uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      ".multicast::cluster [%0], [%1, {%2, %3, %4, %5}], [%6], %7;" ::"r"(dst),
-      "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(bar), "h"((uint16_t)3)
       : "memory");
 }
 

@@ -16,8 +16,10 @@
 //
 // A sum changes hands twice a stage (512 cycles of the tensor core), and every look at a
 // shared-memory barrier takes 200 to 250 cycles then. So each CTA makes its own
-// products, and its epilogue hands an accumulator back by a hardware barrier. A pair of
-// CTAs still shares a tile of 256 rows: each loads half of its weights for both. Groups
+// products, and its epilogue hands an accumulator back by a hardware barrier. CTAs work
+// by themselves: neighbours take the halves of a tile of 256 rows, and each loads all of
+// its weights, which the second has from L2 (each loading half for both of a cluster
+// took 515 us for 8192^3 instead of 501: they waited for each other). Groups
 // of at most 128 rows have tiles of twice the features instead, half of them each
 // CTA's, so that experts with a handful of rows keep all SMs reading weights (256 experts
 // x 32 rows, above: 306 us when it came in, 502 with such rows in one CTA of a pair).
@@ -26,14 +28,13 @@
 // features.
 //
 // Roles by warp: 0 TMA, 1 MMA, 2 looks for complete sums and tells the epilogue by
-// another hardware barrier (8192^3: 515 us, 533 with every epilogue warp looking), 3 works
+// another hardware barrier (18 us of 8192^3's 533 with every epilogue warp looking), 3 works
 // out the tiles (one thread each, but for 1 and 2, which wait as warps), 4-11 epilogue:
 // TMEM lanes go by warp % 4, columns by halves. 128 sums a thread: the other warps give
 // registers up for them (16 warps with 64 sums each: 870 us).
 //
-// Bound by that loop and by power: 8192^3 515 us, 2.14 PFLOP/s; 128 experts x 973 rows,
-// 4096 to 2 x 2048 with SwiGLU, bias and pre-activations, 2.47 ms, 1.7 PFLOP/s, 1350 W at
-// full clocks; 256 experts x 32 rows, 7168 to 2 x 512, 300 us, 95 % of the copy's bandwidth.
+// Bound by that loop and by power: 8192^3 501 us, 2.19 PFLOP/s; 128 experts x 973 rows,
+// 4096 to 2 x 2048 with SwiGLU, bias and pre-activations, 2.5 ms, 1.65 PFLOP/s; 256 experts x 32 rows, 7168 to 2 x 512, 300 us, 95 % of the copy's bandwidth.
 #include <atomic>
 #include <climits>
 #include <cstring>
@@ -45,7 +46,7 @@ namespace ep {
 namespace {
 
 constexpr int kDepth = 128;                      // terms per stage: 128 bytes
-constexpr int kTileRows = 256;                   // of the pair
+constexpr int kTileRows = 256;                   // of both neighbours
 constexpr int kStageA = 128 * kDepth;            // bytes of a CTA's rows
 constexpr int kRingBytes = 4 * (kStageA + 256 * kDepth);
 constexpr int kMaxStages = 6;                    // of 128 features
@@ -85,7 +86,7 @@ struct MmaParams {
 
 struct Barriers {
   uint64_t full[kMaxStages];  // a stage's operands have landed
-  uint64_t empty[kMaxStages]; // both CTAs' products have read this stage
+  uint64_t empty[kMaxStages]; // the products have read this stage
   uint64_t acc_full[2];       // a stage's sum is complete
   uint64_t tile_full[kSlots], tile_empty[kSlots];
   uint64_t joined;            // the epilogue's warps meet
@@ -363,7 +364,7 @@ struct Maps {
 };
 
 template <int MODE, int ACT, typename T>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kThreads, 1)
     product8_kernel(const __grid_constant__ Maps maps, MmaParams q) {
   constexpr bool kGated = MODE == kForward && ACT == EP_ACT_SWIGLU;
   constexpr int kScaleGroup = kGated ? 4 : 2;   // stages whose scales are fetched at once: registers allow no more
@@ -376,13 +377,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   int* counts = begins + q.p.s.G;
   int* sizes = counts + q.p.s.G;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int cta = (int)cluster_rank();
+  const int cta = blockIdx.x & 1;
   int32_t* timeout = q.p.s.err;
 
   // one thread a barrier
   if (threadIdx.x < kMaxStages) {
     mbar_init(&bar->full[threadIdx.x], 1);
-    mbar_init(&bar->empty[threadIdx.x], 2);      // each CTA's products
+    mbar_init(&bar->empty[threadIdx.x], 1);
   } else if (threadIdx.x < kMaxStages + 2) {
     mbar_init(&bar->acc_full[threadIdx.x - kMaxStages], 1);
   }
@@ -399,8 +400,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     tma_prefetch_map(&maps.rows[0]);
     tma_prefetch_map(&maps.w[0]);
   }
-  __syncthreads();
-  cluster_arrive();                      // the barriers are ready; the wait is below
+  __syncthreads();                       // the barriers are ready
   if (warp == 1) tmem_alloc_own(&bar->tmem, kTmemColumns);
   begin_overlapped();
   const QPlan plan = plan_qtiles<kGated>(q, first, begins, counts, sizes);
@@ -411,7 +411,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();                       // the TMEM address is there
   tc_fence_after();
-  cluster_wait();
   const uint32_t tmem = bar->tmem;
   const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
   const int mine = pair < units ? (units - 1 - pair) / pairs + 1 : 0;   // this pair's units
@@ -429,10 +428,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         ok = take_tile(bar, i, w);
         if (!ok) break;
         const Share mine_of = share_of(q, w, cta);
-        const bool some = mine_of.rows > 0, few = w.terms > 0;
+        if (mine_of.rows <= 0) continue;
         const int row = (int)mine_of.row0, f = mine_of.f0;
         const int box = w.n > 64 ? 0 : w.n > 32 ? 1 : 2;
-        const uint32_t bytes = (some ? kStageA >> box : 0) + (some || !few ? 2 * half_bytes : 0);
+        const uint32_t bytes = (kStageA >> box) + 2 * half_bytes;
         const bool wide = plan.width == 256;
         const CUtensorMap* map_w = &maps.w[wide ? 0 : 1];
         for (int kb = w.kb0; kb < w.kb1; ++kb) {
@@ -457,16 +456,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             }
           };
           int c[3];
-          if (!few) {
-            half_at(cta, c);
-            tma_both_4d(b + cta * half_bytes, map_w, c[0], c[1], c[2], w.g, on);
-          } else if (some) {
-            half_at(0, c);
-            tma_own_4d(b, map_w, c[0], c[1], c[2], w.g, on);
-            half_at(1, c);
-            tma_own_4d(b + half_bytes, map_w, c[0], c[1], c[2], w.g, on);
-          }
-          if (some) tma_own_2d(a, &maps.rows[box], d, row, on);
+          half_at(0, c);
+          tma_own_4d(b, map_w, c[0], c[1], c[2], w.g, on);
+          half_at(1, c);
+          tma_own_4d(b + half_bytes, map_w, c[0], c[1], c[2], w.g, on);
+          tma_own_2d(a, &maps.rows[box], d, row, on);
           ++it;
           if (++s == stages) {
             s = 0;
@@ -474,7 +468,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           }
         }
       }
-      // both CTAs' arrivals here, before this one may leave
+      // the products' arrivals, before this CTA may leave
       for (int i = 0; i < stages && i < it && ok; ++i) {
         s = s == 0 ? stages - 1 : s - 1;
         ok = mbar_wait_soon(&bar->empty[s], ((it - 1 - i) / stages) & 1);
@@ -506,19 +500,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         Tile w;
         if (ok) ok = warp_take_tile(bar, i, w, lane);
         if (!ok) w = qtile_at<kGated>(q, plan, first, begins, counts, sizes, pair + i * pairs);
-        const bool some = share_of(q, w, cta).rows > 0;
-        for (int kb = w.kb0; kb < w.kb1; ++kb) {
+        if (share_of(q, w, cta).rows <= 0) continue;
+        for (int kb = w.kb0; kb < w.kb1; ++kb, ++n_acc) {
           if (ok && !__all_sync(kFull, ready)) ok = warp_wait(&bar->full[s], phase);
-          if (some && n_acc >= 2) named_sync(1 + (n_acc & 1), kHandover);
+          if (n_acc >= 2) named_sync(1 + (n_acc & 1), kHandover);
           if (ok) {
             tc_fence_after();
             if (lane == 0) {
-              if (some) {
-                mma8_stage<kStepA, kStepB>(tmem + (n_acc & 1) * 256, a0 + s * stage_units, a_high,
-                                           b0 + s * stage_units, b_high, form);
-                mma8_commit(sum0 + (n_acc & 1) * 8);
-              }
-              mma8_commit_both(empty0 + s * 8);
+              mma8_stage<kStepA, kStepB>(tmem + (n_acc & 1) * 256, a0 + s * stage_units, a_high,
+                                         b0 + s * stage_units, b_high, form);
+              mma8_commit(sum0 + (n_acc & 1) * 8);
+              mma8_commit(empty0 + s * 8);
             }
             __syncwarp();
             if (++s == (uint32_t)stages) {
@@ -527,7 +519,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             }
             ready = mbar_test(full0 + s * 8, phase);       // its answer comes under the MMAs
           }
-          n_acc += some;
         }
       }
       for (int last = n_acc < 2 ? 0 : n_acc - 2; last < n_acc; ++last) named_sync(1 + (last & 1), kHandover);
@@ -709,8 +700,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   }
   __syncwarp();
   __syncthreads();
-  cluster_arrive();   // the other CTA may still arrive on this one's barriers
-  cluster_wait();
   if (warp == 1) tmem_free_own(tmem, kTmemColumns);
 }
 
