@@ -17,8 +17,8 @@ def roles():
     lines = code()
     at = [next(i for i, line in enumerate(lines) if mark in line)
           for mark in ("} else if (warp == 1) {", "} else if (warp == 2) {", "} else if (warp == 3 &&",
-                       "registers_more<", "cluster_arrive();")]
-    end = max(i for i, line in enumerate(lines) if "cluster_arrive();" in line)
+                       "registers_more<")]
+    end = next(i for i, line in enumerate(lines) if "tmem_free_own(" in line)
     return lines[at[0]:at[1]], lines[at[1]:at[2]], lines[at[3]:end]
 
 
