@@ -34,7 +34,8 @@
 // registers up for them (16 warps with 64 sums each: 870 us).
 //
 // Bound by that loop and by power: 8192^3 501 us, 2.19 PFLOP/s; 128 experts x 973 rows,
-// 4096 to 2 x 2048 with SwiGLU, bias and pre-activations, 2.54 ms, 1.65 PFLOP/s; 256 experts x 32 rows, 7168 to 2 x 512, 298 us, 96 % of the copy's bandwidth.
+// 4096 to 2 x 2048 with SwiGLU, bias and pre-activations, 2.54 ms, 1.65 PFLOP/s; 256
+// experts x 32 rows, 7168 to 2 x 512, 298 us, 96 % of the copy's bandwidth.
 #include <atomic>
 #include <climits>
 #include <cstring>
