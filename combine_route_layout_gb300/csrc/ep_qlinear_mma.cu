@@ -92,10 +92,22 @@ struct Barriers {
   uint64_t tile_full[kSlots], tile_empty[kSlots];
   uint64_t joined;            // the epilogue's warps meet
   Tile tiles[kSlots];
-  uint32_t failed;            // a wait for a sum gave up
+  uint32_t failed;            // a sum's warp gave up: sums are not to be had
+  uint32_t met;               // sums for which the MMA warp has the accumulator back
   uint32_t tmem;
   uint32_t last;              // this CTA's part of a tile was the last
 };
+
+// Wait until the MMA warp has the accumulator of sum n back, for whoever is not told by
+// the sum itself. That warp's waits and the epilogue's give up after a second each, at
+// most five one after another; this one's limit is beyond them.
+constexpr uint64_t kMetNs = 16 * kMbarWaitNs;
+__device__ __forceinline__ void wait_met(const Barriers* bar, int n) {
+  const volatile uint32_t* met = &bar->met;
+  const uint64_t t0 = globaltimer_ns();
+  while (*met <= (uint32_t)n && globaltimer_ns() - t0 < kMetNs) __nanosleep(200);
+  __syncwarp();
+}
 
 // Results of a row that a CTA's tile has.
 __host__ __device__ __forceinline__ int results_in(int width, bool gated) { return gated ? width / 2 : width; }
@@ -394,7 +406,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&bar->tile_empty[threadIdx.x - 32], 3 + kEpilogueWarps);
   } else if (threadIdx.x == 32 + kSlots) {
     mbar_init(&bar->joined, kEpilogueWarps);
-    bar->failed = 0;
+    bar->failed = bar->met = 0;
   }
   if (threadIdx.x < 64) mbar_init_fence();
   if (threadIdx.x == 64) {
@@ -484,6 +496,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ---------------------------------------------- MMA: one lane issues, the warp waits.
       // After a wait that gave up it issues nothing, but meets the epilogue as often
       // as ever, and so do the epilogue's warps: the hardware barriers have no limit.
+      // `met` says how far it has come, sums or none.
       constexpr bool kMnB = MODE == kInputGrad;
       constexpr uint32_t kStepA = 32 >> 4, kStepB = (kMnB ? 4096 : 32) >> 4;
       const uint32_t stage_units = (uint32_t)stage_bytes >> 4;
@@ -494,7 +507,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t empty0 = smem_addr(&bar->empty[0]), sum0 = smem_addr(&bar->acc_full[0]);
       const uint32_t full0 = smem_addr(&bar->full[0]);
       const uint32_t form = mma8_form(plan.width, kMnB);
-      int n_acc = 0;
+      int n_acc = 0, issued = 0;             // sums met for, sums that are made
       uint32_t s = 0, phase = 0;             // the ring's place
       bool ok = true, ready = false;         // ready: that place was seen to be full
       for (int i = 0; i < mine; ++i) {
@@ -514,19 +527,26 @@ __global__ void __launch_bounds__(kThreads, 1)
               mma8_commit(empty0 + s * 8);
             }
             __syncwarp();
+            issued = n_acc + 1;
             if (++s == (uint32_t)stages) {
               s = 0;
               phase ^= 1;
             }
             ready = mbar_test(full0 + s * 8, phase);       // its answer comes under the MMAs
           }
+          if (lane == 0) *const_cast<volatile uint32_t*>(&bar->met) = n_acc + 1;
         }
       }
       for (int last = n_acc < 2 ? 0 : n_acc - 2; last < n_acc; ++last) named_sync(1 + (last & 1), kHandover);
+      // no sum may be on its way when the CTA gives its tensor memory back: the epilogue,
+      // if told of sums that nobody had seen, is no witness
+      if (issued > 0) ok = warp_wait(&bar->acc_full[(issued - 1) & 1], ((issued - 1) >> 1) & 1) && ok;
       if (!ok && lane == 0) atomicOr(timeout, kErrLinearTimeout);
     } else if (warp == 2) {
       // ---------------------------------------------- sums: looks for each and tells the epilogue.
-      // After a wait that gave up it tells it of all sums, as the others meet as often as ever.
+      // After a wait that gave up it tells it of all sums, as the others meet as often as
+      // ever, but of none before the MMA warp has come to it: told of the next but one too
+      // early, a warp would count twice in a meeting that another has not come to yet.
       int n_acc = 0;
       bool ok = true;
       for (int i = 0; i < mine; ++i) {
@@ -535,9 +555,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) w = qtile_at<kGated>(q, plan, first, begins, counts, sizes, pair + i * pairs);
         if (share_of(q, w, cta).rows <= 0) continue;
         for (int kb = w.kb0; kb < w.kb1; ++kb, ++n_acc) {
-          if (ok) {
-            ok = warp_wait(&bar->acc_full[n_acc & 1], (n_acc >> 1) & 1);
-            if (!ok && lane == 0) bar->failed = 1;
+          if (ok) ok = warp_wait(&bar->acc_full[n_acc & 1], (n_acc >> 1) & 1);
+          if (!ok) {
+            if (lane == 0) bar->failed = 1;
+            wait_met(bar, n_acc);
           }
           tc_fence_after();
           tc_fence_before();
