@@ -17,13 +17,20 @@ struct Piece {
 // Ints of shared memory for G groups: first piece and first row of each, one end.
 constexpr int kSegmentInts = 3;
 
+// Pieces of `per` rows of a segment. `count` goes up to INT32_MAX - 1024, so that with
+// `per` rows more it passes an int.
+__host__ __device__ inline int64_t pieces_of(int64_t count, int per) { return (count + per - 1) / per; }
+
+// Pieces of all segments, at most: what a CTA's next one, a grid of them on, still fits.
+constexpr int64_t kMostPieces = INT32_MAX - (1 << 20);
+
 inline size_t segment_bytes(int G) { return (size_t)(kSegmentInts * G + 1) * sizeof(int); }
 
 #ifdef __CUDACC__
 
 // table: [G + 1] first pieces, then [G] first rows, then [G] counts. All threads of the
 // CTA (at most 1024, whole warps); returns the number of pieces of `per` rows: none,
-// with an error, where overlapping segments have more than an int holds.
+// with an error, where overlapping segments have more than kMostPieces.
 __device__ __forceinline__ int segment_table(const LinearSegs& s, int per, int* table) {
   __shared__ int64_t sums[32];
   int* begins = table + s.G + 1;
@@ -37,7 +44,7 @@ __device__ __forceinline__ int segment_table(const LinearSegs& s, int per, int* 
     segment_of(s, g, b, c);
     begins[g] = (int)b;
     counts[g] = (int)c;
-    mine += (c + per - 1) / per;
+    mine += pieces_of(c, per);
   }
   int64_t incl = mine;
 #pragma unroll
@@ -51,11 +58,11 @@ __device__ __forceinline__ int segment_table(const LinearSegs& s, int per, int* 
   for (int w = 0; w < warp; ++w) before += sums[w];
   for (int g = g0; g < g1; ++g) {
     table[g] = (int)before;
-    before += (counts[g] + per - 1) / per;
+    before += pieces_of(counts[g], per);
   }
   int64_t total = 0;
   for (int w = 0; w < threads / 32; ++w) total += sums[w];
-  if (total > INT32_MAX) {
+  if (total > kMostPieces) {
     total = 0;
     if (threadIdx.x == 0) atomicOr(s.err, kErrSegment);
   }
