@@ -62,11 +62,13 @@ struct NormParams {
 
 // The sum over the CTA, the same in every thread: warps by shuffles, then their sums
 // in their order. `room` is written anew by every call: two calls in a row take two.
-__device__ __forceinline__ float cta_sum(float v, float* room) {
+// `flag`, if given, is read behind the meeting, beside the sums.
+__device__ __forceinline__ float cta_sum(float v, float* room, const int* flag = nullptr, int* set = nullptr) {
 #pragma unroll
   for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
   if ((threadIdx.x & 31) == 0) room[threadIdx.x >> 5] = v;
   __syncthreads();
+  if (flag) *set = *flag;
   const int warps = blockDim.x >> 5;
   v = 0.0f;
   for (int w = 0; w < warps; ++w) v += room[w];
@@ -213,11 +215,15 @@ __global__ void __launch_bounds__(VECS == 1 ? kGradThreadsMost : 512) norm_grad_
   extern __shared__ __align__(16) uint8_t ring[];
   __shared__ float room[4][32];
   __shared__ uint64_t landed[kRingRows];
+  __shared__ int gave_up;                              // a thread's wait for a row did
   const int T = blockDim.x;
   const bool has_block = p.block != nullptr;
   const RowPlace place = row_place<S, B>(p.H, p.d_stream != nullptr, has_block);
   if (threadIdx.x < kRingRows) mbar_init(&landed[threadIdx.x], 1);
-  if (threadIdx.x == 0) mbar_init_fence();
+  if (threadIdx.x == 0) {
+    mbar_init_fence();
+    gave_up = 0;
+  }
   __syncthreads();
   begin_overlapped();
   const auto fetch = [&](int64_t row, int slot) {      // one thread
@@ -254,7 +260,7 @@ __global__ void __launch_bounds__(VECS == 1 ? kGradThreadsMost : 512) norm_grad_
     const uint8_t* here = ring + (size_t)slot * place.bytes;
     const float by = next.x, by_block = next.y, times = next_times;
     numbers(row + gridDim.x);
-    if (!mbar_wait(&landed[slot], phase) && threadIdx.x == 0) atomicOr(p.err, kErrNormTimeout);
+    if (!mbar_wait(&landed[slot], phase)) gave_up = 1;
     float sum = 0.0f;
 #pragma unroll
     for (int i = 0; i < VECS; ++i) {
@@ -271,7 +277,22 @@ __global__ void __launch_bounds__(VECS == 1 ? kGradThreadsMost : 512) norm_grad_
         sum = fmaf(d[j] * w[j], n, sum);
       }
     }
-    const float by_mean = -by * by * (cta_sum(sum, room[0]) * p.inv);
+    int leaves;            // the same for all: not written again before the row's last meeting
+    const float by_mean = -by * by * (cta_sum(sum, room[0], &gave_up, &leaves) * p.inv);
+    if (leaves) {          // nothing more is asked for, and what was lands before the CTA leaves
+      if (threadIdx.x == 0) {
+        atomicOr(p.err, kErrNormTimeout);
+#pragma unroll 1
+        for (int i = 0; i < p.ring_rows && row + (int64_t)i * gridDim.x < p.rows; ++i) {
+          (void)mbar_wait(&landed[slot], phase);
+          if (++slot == p.ring_rows) {
+            slot = 0;
+            phase ^= 1;
+          }
+        }
+      }
+      return;
+    }
     float dot_gate = 0.0f, dot_post = 0.0f;
     float t[VECS][8];
 #pragma unroll
