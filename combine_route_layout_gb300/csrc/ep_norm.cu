@@ -219,8 +219,8 @@ __global__ void __launch_bounds__(VECS == 1 ? kGradThreadsMost : 512) norm_grad_
   const int T = blockDim.x;
   const bool has_block = p.block != nullptr;
   const RowPlace place = row_place<S, B>(p.H, p.d_stream != nullptr, has_block);
-  if (threadIdx.x < kRingRows) mbar_init(&landed[threadIdx.x], 1);
-  if (threadIdx.x == 0) {
+  if (threadIdx.x == 0) {      // the fence is for this thread's barriers alone
+    for (int i = 0; i < kRingRows; ++i) mbar_init(&landed[i], 1);
     mbar_init_fence();
     gave_up = 0;
   }

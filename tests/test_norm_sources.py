@@ -58,3 +58,11 @@ def test_nothing_is_asked_for_behind_it_and_what_was_lands():
     text = "\n".join(lines[leave:end])
     assert end < last and lines[end - 1] == "return;" and "atomicOr(p.err, kErrNormTimeout);" in text
     assert "i < p.ring_rows && row + (int64_t)i * gridDim.x < p.rows" in text and "mbar_wait(&landed[slot], phase)" in text
+
+
+def test_the_thread_that_makes_the_barriers_fences_them():
+    """The fence that shows barriers to bulk copies is for those its own thread has made."""
+    lines = kernel()
+    at = one(lines, r"mbar_init\(")
+    assert re.search(r"^for \(int i = 0; i < kRingRows; \+\+i\) mbar_init\(&landed\[i\], 1\);", lines[at])
+    assert lines[at - 1] == "if (threadIdx.x == 0) {" and lines[at + 1] == "mbar_init_fence();"
