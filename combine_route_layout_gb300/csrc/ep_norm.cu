@@ -278,7 +278,8 @@ __global__ void __launch_bounds__(VECS == 1 ? kGradThreadsMost : 512) norm_grad_
       }
     }
     int leaves;            // the same for all: not written again before the row's last meeting
-    const float by_mean = -by * by * (cta_sum(sum, room[0], &gave_up, &leaves) * p.inv);
+    // (by itself goes up to 1e22 with eps 1e-45, its square beyond f32)
+    const float by_mean = -by * (by * (cta_sum(sum, room[0], &gave_up, &leaves) * p.inv));
     if (leaves) {          // nothing more is asked for, and what was lands before the CTA leaves
       if (threadIdx.x == 0) {
         atomicOr(p.err, kErrNormTimeout);
@@ -338,7 +339,7 @@ __global__ void __launch_bounds__(VECS == 1 ? kGradThreadsMost : 512) norm_grad_
       if (p.gate == EP_GATE_TOKEN && threadIdx.x == 0) p.d_gate[row] = p.alpha * dot_gate;
     }
     if (has_block && POST) {
-      const float by_post = -by_block * by_block * (dot_post * p.inv);
+      const float by_post = -by_block * (by_block * (dot_post * p.inv));
 #pragma unroll
       for (int i = 0; i < VECS; ++i) {
         const int at = (threadIdx.x + i * T) * 8;
