@@ -46,4 +46,25 @@ cudaError_t launch_qlinear_few_rows(const QLinearParams& p, int sms, cudaStream_
 cudaError_t launch_dequantize(const LinearSegs& s, const uint8_t* codes, const float* scales, int K,
                               __nv_bfloat16* out, int sms, cudaStream_t st);
 
+#ifdef __CUDACC__
+
+// A block's sum is multiplied by the product of its two scales. Where that product is no
+// normal f32 and neither scale is zero, the result may be one all the same: the sum, 2^-18 to
+// 2^25, is then multiplied by one scale and by the other, in the order that leaves the
+// range only where the result does. Below the range the larger scale comes first, above
+// it the smaller one.
+__device__ __forceinline__ bool scales_apart(float a, float b, float by) {
+  return !(fabsf(by) >= 0x1p-126f && fabsf(by) < INFINITY) && a != 0.0f && b != 0.0f;
+}
+__device__ __forceinline__ void order_scales(float a, float b, float& first, float& second) {
+  const float by = a * b;
+  first = 1.0f;
+  second = by;
+  if (!scales_apart(a, b, by)) return;
+  const bool a_first = (fabsf(a) > fabsf(b)) == (fabsf(by) < 1.0f);
+  first = a_first ? a : b;
+  second = a_first ? b : a;
+}
+
+#endif
 }  // namespace ep

@@ -39,6 +39,7 @@
 #include <atomic>
 #include <climits>
 #include <cstring>
+#include <type_traits>
 
 #include "ep_linear_tiles.cuh"
 #include "ep_qlinear.cuh"
@@ -61,6 +62,13 @@ constexpr int kHandover = 32 * (1 + kEpilogueWarps);     // threads of the hardw
 constexpr int kRegisters = 168, kRegistersLess = 56, kRegistersMore = 224;
 static_assert(kThreads * kRegisters >= 128 * kRegistersLess + kEpilogueWarps * 32 * kRegistersMore,
               "registers for the epilogue");
+
+// How far an f32's exponent is from `least` on, zeros and negative distances beyond any: with
+// exponents below `most` alone if less than key_range(least, most).
+__device__ __forceinline__ uint32_t scale_key(float v, uint32_t least) {
+  return 2u * __float_as_uint(v) - 2u * (least << 23);
+}
+constexpr uint32_t key_range(uint32_t least, uint32_t most) { return 2u * ((most - least) << 23); }
 
 struct QPlan {
   int tiles, splits;
@@ -619,6 +627,17 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       };
+      // Scales whose product is no normal number stay apart: order_scales. Whether a group of
+      // stages may have such is a look at the products, or, with gates, which have twice
+      // as many, at scales beyond 2^-63 to 2^63: the rows' each time, the weights' here.
+      uint32_t key_w = 0;
+      constexpr uint32_t kLow = kGated ? 64 : 1, kHigh = kGated ? 190 : 255;
+      if (kGated) {
+        for (int kb = w.kb0 + lane; kb < w.kb1; kb += 32) {
+          const float* of_w = w_scales + (int64_t)kb * q.block_ld;
+          key_w = max(key_w, max(scale_key(of_w[0], kLow), scale_key(of_w[q.up], kLow)));
+        }
+      }
       fetch(w.kb0);
       float sum[4][32];
 #pragma unroll
@@ -626,13 +645,19 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int c = 0; c < 32; ++c) sum[h][c] = 0.0f;
       int left = 0;                                       // scales that are there
+      bool outside = false;                               // some of a group's may be such
+      int known = 0;                                      // where they may: 1 none has, 2 some have
       for (int kb = w.kb0; kb < w.kb1; ++kb, ++n_acc, --left) {
         if (left == 0) {
+          uint32_t key = key_w;
 #pragma unroll
           for (int j = 0; j < kScaleGroup; ++j) {
             by[j] = next[j] * next_w[j];
             by_up[j] = next[j] * next_up[j];
+            key = max(key, scale_key(kGated ? next[j] : by[j], kLow));
           }
+          outside = __any_sync(kFull, key >= key_range(kLow, kHigh));
+          known = 0;
           left = kScaleGroup;
           fetch(kb + kScaleGroup);
         }
@@ -654,18 +679,46 @@ __global__ void __launch_bounds__(kThreads, 1)
           const auto column_of = [&](int c) {             // of piece c of 16 columns
             return kGated ? (c >> 1 & 1) * (plan.width / 2) + (c >> 2) * 32 + (c & 1) * 16 : c * 16;
           };
-          tmem_begin16(at, r[0]);
-          tmem_wait16(r[0]);
+          bool apart = false;
+          if (__builtin_expect(outside, 0)) {
+            if (known == 0) {                             // zeros, or products that are normal all the same
+              bool any = false;
+              for (int j = 0; j < left && kb + j < w.kb1; ++j) {
+                const float row = row_scales[kb + j], *of_w = w_scales + (int64_t)(kb + j) * q.block_ld;
+                any |= scales_apart(row, of_w[0], row * of_w[0]);
+                if (kGated) any |= scales_apart(row, of_w[q.up], row * of_w[q.up]);
+              }
+              known = __any_sync(kFull, any) ? 2 : 1;
+            }
+            apart = known == 2;
+          }
+          const auto add = [&](auto which, float first, float first_up, float second, float second_up) {
+            constexpr bool APART = decltype(which)::value;
+            tmem_begin16(at, r[0]);
+            tmem_wait16(r[0]);
 #pragma unroll
-          for (int c = 0; c < 8; ++c) {
-            if (c >= 4 && sub == 1) continue;
-            const bool more = c != 7 && (c != 3 || sub == 2);
-            if (more) tmem_begin16(at + column_of(c + 1), r[(c + 1) & 1]);
-            const float by_c = kGated && (c >> 1 & 1) ? scale_up : scale;
+            for (int c = 0; c < 8; ++c) {
+              if (c >= 4 && sub == 1) continue;
+              const bool more = c != 7 && (c != 3 || sub == 2);
+              if (more) tmem_begin16(at + column_of(c + 1), r[(c + 1) & 1]);
+              const bool is_up = kGated && (c >> 1 & 1);
+              const float by_c = is_up ? second_up : second;
 #pragma unroll
-            for (int k = 0; k < 16; ++k)
-              sum[c / 2][(c & 1) * 16 + k] = fmaf(r[c & 1][k], by_c, sum[c / 2][(c & 1) * 16 + k]);
-            if (more) tmem_wait16(r[(c + 1) & 1]);
+              for (int k = 0; k < 16; ++k) {
+                const float v = APART ? r[c & 1][k] * (is_up ? first_up : first) : r[c & 1][k];
+                sum[c / 2][(c & 1) * 16 + k] = fmaf(v, by_c, sum[c / 2][(c & 1) * 16 + k]);
+              }
+              if (more) tmem_wait16(r[(c + 1) & 1]);
+            }
+          };
+          if (__builtin_expect(!apart, 1)) {
+            add(std::false_type(), 1.0f, 1.0f, scale, scale_up);
+          } else {
+            const float row = row_scales[kb], *of_w = w_scales + (int64_t)kb * q.block_ld;
+            float first, second, first_up = 1.0f, second_up = 0.0f;
+            order_scales(row, of_w[0], first, second);
+            if (kGated) order_scales(row, of_w[q.up], first_up, second_up);
+            add(std::true_type(), first, first_up, second, second_up);
           }
         }
         tc_fence_before();

@@ -83,10 +83,17 @@ __global__ void __launch_bounds__(kWarps * 32) few_rows8_kernel(QLinearParams p,
         mma_16x8x32(d, a0[i][h].x, a1[i][h].x, a0[i][h].y, a1[i][h].y, b.x, b.y);
         mma_16x8x32(d, a0[i][h].z, a1[i][h].z, a0[i][h].w, a1[i][h].w, b.z, b.w);
       }
-      acc[0] = fmaf(d[0], v0[i] * x0, acc[0]);
-      acc[1] = fmaf(d[1], v0[i] * x1, acc[1]);
-      acc[2] = fmaf(d[2], v1[i] * x0, acc[2]);
-      acc[3] = fmaf(d[3], v1[i] * x1, acc[3]);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float a = j < 2 ? v0[i] : v1[i], b = j & 1 ? x1 : x0, by = a * b;
+        if (scales_apart(a, b, by)) {
+          float first, second;
+          order_scales(a, b, first, second);
+          acc[j] = fmaf(d[j] * first, second, acc[j]);
+        } else {
+          acc[j] = fmaf(d[j], by, acc[j]);
+        }
+      }
     }
   }
   if (split > 1) {   // the first warp of each share adds the others' sums, in their order

@@ -745,7 +745,7 @@ ep_status ep_quantize(ep_quant_handle* h, const void* x, const int32_t* row_begi
                       const int32_t* row_count, const int32_t* row_base, int64_t num_rows,
                       void* codes, float* scales, void* stream);
 
-/* x of codes and scales: code scale, rounded once to dtype. */
+/* x of codes and scales: code scale in f32, then rounded to dtype. */
 ep_status ep_dequantize(ep_quant_handle* h, const void* codes, const float* scales,
                         const int32_t* row_begin, const int32_t* row_count,
                         const int32_t* row_base, int64_t num_rows, void* x, void* stream);
@@ -768,7 +768,10 @@ ep_status ep_quant_sync(ep_quant_handle* h, void* stream);
  * x's values rounded to bf16, which is what its tensor-core operands hold.
  *
  * The tensor core adds up a block's 128 terms; scales and the sum over blocks are
- * f32. in_features is a multiple of 16. A handle is made from an ep_linear_config.
+ * f32. The product of a block's two scales may leave f32's range where the block's
+ * part of the result does not: the sum then meets one scale after the other. In dW,
+ * codes times their scales are f32 before they are rounded to bf16.
+ * in_features is a multiple of 16. A handle is made from an ep_linear_config.
  * ---------------------------------------------------------------------------
  */
 typedef struct ep_qlinear_handle ep_qlinear_handle;
