@@ -377,6 +377,7 @@ extern "C" ep_status ep_linear_sync(ep_linear_handle* h, void* stream) {
   }
   if (bits & kErrSegment)
     return lfail(EP_ERR_INVALID_INDEX,
-                 "a segment reached outside the row pool and was cut, or a backward pass's overlapped");
+                 "a segment reached outside the row pool and was cut, or segments overlapped in a backward "
+                 "pass, or so much that the call did nothing");
   return EP_OK;
 }

@@ -99,6 +99,10 @@ __device__ __forceinline__ int tiles_in(int count, int cap) {
   return quotient(count + size - 1, size);
 }
 
+// Tiles are numbered in int32: segments that overlap may have more, and are refused then.
+constexpr int kMostTiles = (1 << 30) - 1;
+__device__ __forceinline__ int add_tiles(int a, int b) { return min(a + b, kMostTiles); }
+
 // Unit u of the plan: part u % splits of tile u / splits.
 template <int MODE, typename Q>
 __device__ __forceinline__ Tile tile_at(const Q& q, const Plan& plan, const int* first,
@@ -194,19 +198,19 @@ __device__ Plan plan_tiles(const Q& q, int* first, int* begins, int* counts, int
     if constexpr (MODE == kWeightGrad) {
       n0 = max(n0, (int)c);
     } else {
-      n0 += tiles_in((int)c, base_cap) * q.f_tiles;
-      n1 += tiles_in((int)c, base_cap / 2) * q.f_tiles;
-      n2 += tiles_in((int)c, base_cap / 4) * q.f_tiles;
+      n0 = add_tiles(n0, tiles_in((int)c, base_cap) * q.f_tiles);
+      n1 = add_tiles(n1, tiles_in((int)c, base_cap / 2) * q.f_tiles);
+      n2 = add_tiles(n2, tiles_in((int)c, base_cap / 4) * q.f_tiles);
     }
   }
   int s0 = n0, s1 = n1, s2 = n2;
 #pragma unroll
   for (int o = 16; o; o >>= 1) {
     const int x = __shfl_xor_sync(kFull, s0, o);
-    s0 = MODE == kWeightGrad ? max(s0, x) : s0 + x;
+    s0 = MODE == kWeightGrad ? max(s0, x) : add_tiles(s0, x);
     if (MODE != kWeightGrad) {
-      s1 += __shfl_xor_sync(kFull, s1, o);
-      s2 += __shfl_xor_sync(kFull, s2, o);
+      s1 = add_tiles(s1, __shfl_xor_sync(kFull, s1, o));
+      s2 = add_tiles(s2, __shfl_xor_sync(kFull, s2, o));
     }
   }
   if (lane == 0) {
@@ -227,9 +231,9 @@ __device__ Plan plan_tiles(const Q& q, int* first, int* begins, int* counts, int
   s0 = s1 = s2 = 0;
 #pragma unroll
   for (int w = 0; w < kThreads / 32; ++w) {
-    s0 += sums[0][w];
-    s1 += sums[1][w];
-    s2 += sums[2][w];
+    s0 = add_tiles(s0, sums[0][w]);
+    s1 = add_tiles(s1, sums[1][w]);
+    s2 = add_tiles(s2, sums[2][w]);
   }
   int level = 0, mine = n0;
   plan.tiles = s0;
@@ -259,6 +263,10 @@ __device__ Plan plan_tiles(const Q& q, int* first, int* begins, int* counts, int
     first[g] = before;
     sizes[g] = tile_rows(counts[g], plan.cap, quotient);
     before += quotient(counts[g] + sizes[g] - 1, sizes[g]) * q.f_tiles;
+  }
+  if (plan.tiles >= kMostTiles) {
+    plan.tiles = 0;
+    if (threadIdx.x == 0) atomicOr(q.p.s.err, kErrSegment);
   }
   __syncthreads();
   return plan;

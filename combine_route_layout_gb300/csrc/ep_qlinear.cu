@@ -465,6 +465,7 @@ extern "C" ep_status ep_qlinear_sync(ep_qlinear_handle* h, void* stream) {
   }
   if (bits & kErrSegment)
     return qlfail(EP_ERR_INVALID_INDEX,
-                  "a segment reached outside the row pool and was cut, or a backward pass's overlapped");
+                  "a segment reached outside the row pool and was cut, or segments overlapped in a backward "
+                  "pass, or so much that the call did nothing");
   return EP_OK;
 }

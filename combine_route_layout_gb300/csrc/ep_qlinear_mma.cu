@@ -155,16 +155,16 @@ __device__ QPlan plan_qtiles(const MmaParams& q, int* first, int* begins, int* c
     begins[g] = (int)b;
     counts[g] = (int)c;
     const int above = tiles_in((int)c, kTileRows);
-    n0 += above * tiles_beside(q.outs, 256, GATED, (int)c, quotient);
-    n1 += above * tiles_beside(q.outs, 128, GATED, (int)c, quotient);
+    n0 = add_tiles(n0, above * tiles_beside(q.outs, 256, GATED, (int)c, quotient));
+    n1 = add_tiles(n1, above * tiles_beside(q.outs, 128, GATED, (int)c, quotient));
   }
   int i0 = n0, i1 = n1;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const int v0 = __shfl_up_sync(kFull, i0, o), v1 = __shfl_up_sync(kFull, i1, o);
     if (lane >= o) {
-      i0 += v0;
-      i1 += v1;
+      i0 = add_tiles(i0, v0);
+      i1 = add_tiles(i1, v1);
     }
   }
   if (lane == 31) {
@@ -175,8 +175,8 @@ __device__ QPlan plan_qtiles(const MmaParams& q, int* first, int* begins, int* c
   int all0 = 0, all1 = 0;
 #pragma unroll
   for (int w = 0; w < kThreads / 32; ++w) {
-    all0 += sums[0][w];
-    all1 += sums[1][w];
+    all0 = add_tiles(all0, sums[0][w]);
+    all1 = add_tiles(all1, sums[1][w]);
   }
   QPlan plan;
   const int narrow = 2 * all0 <= pairs;
@@ -191,6 +191,10 @@ __device__ QPlan plan_qtiles(const MmaParams& q, int* first, int* begins, int* c
     first[g] = before;
     sizes[g] = tile_rows(counts[g], kTileRows, quotient);
     before += quotient(counts[g] + sizes[g] - 1, sizes[g]) * tiles_beside(q.outs, plan.width, GATED, counts[g], quotient);
+  }
+  if (plan.tiles >= kMostTiles) {
+    plan.tiles = 0;
+    if (threadIdx.x == 0) atomicOr(q.p.s.err, kErrSegment);
   }
   __syncthreads();
   return plan;

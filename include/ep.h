@@ -678,7 +678,9 @@ ep_status ep_linear_forward(ep_linear_handle* h, const void* x, const void* weig
                             void* y, void* preact, void* stream);
 
 /*
- * Segments must not overlap here (forward's may).
+ * Segments must not overlap here (forward's may, up to 2^30 tiles of 128 rows by 128
+ * features in all; where they have more tiles than the kernel can number it does
+ * nothing and raises EP_ERR_INVALID_INDEX at the sync).
  *   dy       device [max_rows][N] out_dtype
  *   preact   device [max_rows][Nw] bf16 as forward wrote it (may be NULL
  *            without an activation)
