@@ -1,11 +1,11 @@
 // Tiles of 256 features by up to 256 rows that a pair of CTAs shares, for the products
 // of bf16 operands: which tiles there are, the parts that their contractions are cut
-// into, and what becomes of a tile's sums. The products of block-quantised operands, whose
-// tiles and sums are others, share the parts, the tiles' table, tickets and maps. A kernel's
-// parameters Q hold its LinearParams or QLinearParams `p`, the output (`out`,
-// `features` long, `f_tiles` tiles of them), the tiles' `cap` and a dense product's
-// `plan`, and the contraction's `terms`, Q::kDepth of them a stage. Its barriers B
-// have tile_full, tile_empty, tiles and joined.
+// into, and what becomes of a tile's sums. The kernel's parameters Q hold its LinearParams
+// `p`, the output (`out`, `features` long, `f_tiles` tiles of them), the tiles' `cap` and
+// a dense product's `plan`, and the contraction's `terms`, Q::kDepth of them a stage.
+// The products of block-quantised operands have tiles and sums of their own; they share
+// what comes with parts (splits_for, tickets, add_parts), the tiles' table (take_tile, of
+// barriers B with tile_full, tile_empty and tiles), the epilogue's meeting and the maps.
 #pragma once
 
 #include <cuda.h>

@@ -4,15 +4,20 @@
 // Forward: a CTA takes a row, which stays in registers, VECS pieces of 8 elements a
 // thread, between the one or two sums over it and its results: every tensor is read
 // and written once. 32768 x 7168 bf16 335 us, 5.6 TB/s, with post norm and a gate of
-// features, whose weights come from L1 for each row, 270 without; with few rows bound by
-// latency, so that a row then takes as many threads as it has pieces (up to 1024).
+// features, whose weights come from L1 for each row, 270 without; with f32 rows the two
+// pieces a thread spill up to 64 bytes to keep three CTAs an SM (339 us of f32 blocks, to
+// codes). With few rows bound by latency, so that a row then takes as many threads as it
+// has pieces (up to 1024).
 //
 // Backward: a CTA walks rows, thread t always at the same columns, whose sums over
 // rows stay in registers; the CTAs' sums are added in their order by
 // norm_sums_kernel. Rows come by bulk copies into a ring of shared memory, the next
 // ones under the arithmetic of this one, which has two meetings of the CTA a row and is
-// bound by them: 16384 x 4096 with post norm and a gate of tokens 165 us, 4.9 TB/s (211
-// with loads of the row itself).
+// bound by them: 16384 x 4096 with post norm and a gate of tokens 174 us, 4.6 TB/s (211
+// with loads of the row itself when they came in); 32768 x 7168 with a gate of features
+// 675. Above 8192 features a thread has four pieces, and with post norm and a gate of
+// features more sums than registers (300 bytes of a thread spill): 4096 x 16384 bf16 278
+// us, 2.9 TB/s; f32, of which the ring holds one row, 444, 3.3 TB/s.
 #include <climits>
 #include <cstring>
 #include <new>
@@ -434,7 +439,7 @@ cudaError_t launch_grad_rows(NormParams& p, int sms, cudaStream_t st) {
 
 template <typename S, typename B, bool POST, bool FEATURE>
 cudaError_t launch_grad_vecs(NormParams& p, int sms, cudaStream_t st) {
-  // one piece a thread would take more warps to each meeting: 32768 x 7168 768 us for 667
+  // one piece a thread would take more warps to each meeting: 32768 x 7168 768 us for 667 when it was chosen
   if (p.pieces <= kGradOnePiece) return launch_grad_rows<S, B, 1, POST, FEATURE>(p, sms, st);
   if (p.pieces <= 1024) return launch_grad_rows<S, B, 2, POST, FEATURE>(p, sms, st);
   return launch_grad_rows<S, B, 4, POST, FEATURE>(p, sms, st);

@@ -18,8 +18,9 @@
 // shared-memory barrier takes 200 to 250 cycles then. So each CTA makes its own
 // products, and its epilogue hands an accumulator back by a hardware barrier. CTAs work
 // by themselves: neighbours take the halves of a tile of 256 rows, and each loads all of
-// its weights, which the second has from L2 (each loading half for both of a cluster
-// took 515 us for 8192^3 instead of 501: they waited for each other). Groups
+// its weights, which the second has from L2. (Each loading half for both of a cluster
+// takes 2 % less for the 128 experts below, but needs loads into another CTA's
+// shared memory, which no kernel here has.) Groups
 // of at most 128 rows have tiles of twice the features instead, half of them each
 // CTA's, so that experts with a handful of rows keep all SMs reading weights (256 experts
 // x 32 rows, above: 306 us when it came in, 502 with such rows in one CTA of a pair).
@@ -28,14 +29,15 @@
 // features.
 //
 // Roles by warp: 0 TMA, 1 MMA, 2 looks for complete sums and tells the epilogue by
-// another hardware barrier (18 us of 8192^3's 533 with every epilogue warp looking), 3 works
+// another hardware barrier (18 us of 8192^3 when it came in, 533 then), 3 works
 // out the tiles (one thread each, but for 1 and 2, which wait as warps), 4-11 epilogue:
 // TMEM lanes go by warp % 4, columns by halves. 128 sums a thread: the other warps give
 // registers up for them (16 warps with 64 sums each: 870 us).
 //
-// Bound by that loop and by power: 8192^3 501 us, 2.19 PFLOP/s; 128 experts x 973 rows,
-// 4096 to 2 x 2048 with SwiGLU, bias and pre-activations, 2.54 ms, 1.65 PFLOP/s; 256
-// experts x 32 rows, 7168 to 2 x 512, 298 us, 96 % of the copy's bandwidth.
+// Bound by that loop, at the full clock: 128 experts x 973 rows, 4096 to 2 x 2048 with
+// SwiGLU, bias and pre-activations, 2.59 ms, 1.61 PFLOP/s, 1000 to 1100 cycles a stage; 256
+// experts x 32 rows, 7168 to 2 x 512, 295 to 301 us, 96 % of the copy's bandwidth; 256
+// experts x 1024 rows, 7168 to 2 x 2048, 7.4 ms, 2.07 PFLOP/s; 8192^3 535 us, 2.05.
 #include <atomic>
 #include <climits>
 #include <cstring>
@@ -57,8 +59,9 @@ constexpr int kTurnRows = 8, kTurnPitch = 33;    // words: rows that are stored 
 constexpr int kTurnWords = 2 * kTurnRows * kTurnPitch;   // of a warp: gates and up
 constexpr int kTurnBytes = kEpilogueWarps * kTurnWords * 4;
 constexpr int kHandover = 32 * (1 + kEpilogueWarps);     // threads of the hardware barriers
-// Registers of a thread at the start, of the first four warps and of the epilogue's:
-// 8192^3 took 535 us so, 614 to 687 with 216 for the epilogue, 580 with 232.
+// Registers of a thread at the start, of the first four warps and of the epilogue's
+// (at an earlier step 8192^3 took 535 us so, 614 to 687 with 216 for the epilogue, 580
+// with 232).
 constexpr int kRegisters = 168, kRegistersLess = 56, kRegistersMore = 224;
 static_assert(kThreads * kRegisters >= 128 * kRegistersLess + kEpilogueWarps * 32 * kRegistersMore,
               "registers for the epilogue");

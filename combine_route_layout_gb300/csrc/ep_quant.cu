@@ -6,10 +6,11 @@
 // that its amax is four shuffles and its codes one 8-byte store a lane; a CTA takes
 // pieces of the segments in turn (kElements of them: enough that finding the piece's
 // segment costs nothing, few enough that small batches fill the GPU) and has kUnroll
-// blocks of each half-warp on their way at once. 124518 x 2048 bf16: 135 us, 5.7 TB/s
-// (two blocks on their way: 158 to 166), with two thirds of the issue slots busy.
+// blocks of each half-warp on their way at once. 124518 x 2048 bf16: 139 us, 5.5 TB/s
+// (two blocks on their way: 158 to 166), with two thirds of the issue slots busy; f32 201,
+// 6.3 TB/s. Back: 125 us to bf16, 239 to f32. 8192 x 512 and 128 x 7168: 6 to 7 us, the call.
 // Matrices: a CTA keeps a whole 128 x 128 in registers between its amax and its codes.
-// 32 of 4096 x 4096 bf16: 271 us, 5.9 TB/s, bound by HBM.
+// 32 of 4096 x 4096 bf16: 271 us, 5.9 TB/s, f32 403, 6.7; bound by HBM.
 #include <climits>
 #include <cstring>
 #include <new>
@@ -403,6 +404,7 @@ extern "C" ep_status ep_quant_sync(ep_quant_handle* h, void* stream) {
   const cudaError_t e = header_report(&h->header, static_cast<cudaStream_t>(stream), &bits);
   if (e != cudaSuccess) return qcuda(e);
   if (bits & kErrSegment)
-    return qfail(EP_ERR_INVALID_INDEX, "a segment reached outside the row pool and was cut");
+    return qfail(EP_ERR_INVALID_INDEX, "a segment reached outside the row pool and was cut, or segments overlapped so much that the "
+                 "call did nothing");
   return EP_OK;
 }

@@ -741,7 +741,9 @@ void ep_quant_destroy(ep_quant_handle* h);
  *   codes   device out, shaped as x, 16-byte aligned
  *   scales  device f32 out [max_rows][ceil(K/128)], or (block_rows 128)
  *           [G][ceil(max_rows/128)][ceil(K/128)]
- * Rows outside the segments are neither read nor written.
+ * Rows outside the segments are neither read nor written. Segments may overlap, up to
+ * what an int32 numbers in pieces of 2^15 elements or a row; beyond that a call does
+ * nothing and raises EP_ERR_INVALID_INDEX at the sync.
  */
 ep_status ep_quantize(ep_quant_handle* h, const void* x, const int32_t* row_begin,
                       const int32_t* row_count, const int32_t* row_base, int64_t num_rows,
