@@ -283,7 +283,7 @@ __global__ void __launch_bounds__(VECS == 1 ? kGradThreadsMost : 512) norm_grad_
       }
     }
     int leaves;            // the same for all: not written again before the row's last meeting
-    // (by itself goes up to 1e22 with eps 1e-45, its square beyond f32)
+    // `by` goes up to 1e22 (eps 1e-45), and its square would pass f32
     const float by_mean = -by * (by * (cta_sum(sum, room[0], &gave_up, &leaves) * p.inv));
     if (leaves) {          // nothing more is asked for, and what was lands before the CTA leaves
       if (threadIdx.x == 0) {
